@@ -243,6 +243,123 @@ poetx_status poetx_quantize_w0(const void* W0, int8_t* W0_q, float* scales, int 
 poetx_status poetx_dequantize_w0(const int8_t* W0_q, const float* scales, void* W0, int d_in,
                                  int d_out, poetx_dtype dtype, poetx_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Around the projections.  The paper has no counterpart for the calls of
+ * this section: they are what a decoder block holds next to its projections.
+ *
+ * Matrix product with bias, activation and residual in its epilogue, for
+ * weights that carry no block-diagonal factors (frozen, or merged by
+ * poetx_merge), from one token to many:
+ *   z_t = W x_t + bias,   y_t = act(z_t) + residual_t
+ *   x [tokens][d_in], W [d_out][d_in], residual, y, z_saved [tokens][d_out]:
+ *   dtype; bias [d_out] float32.  bias, residual: NULL = absent.  z_saved:
+ *   the rounded z, which the backward needs unless act is NONE (NULL = not
+ *   kept).  y may be residual (added in place); no other overlap.
+ * Accumulation, bias, activation and residual in fp32, rounded once into y.
+ * Backward (W gets no gradient; the residual's is dy itself):
+ *   dz_t = dy_t act'(z_t),   dx_t = W^T dz_t,   dbias = sum_t dz_t
+ *   BF16 rounds dz to bf16, the type the tensor cores take; dbias sums the
+ *   unrounded dz in fp32.  z_saved is not read (may be NULL) when act is
+ *   NONE.  dx or dbias may be NULL.  RELU'(0) = 0.
+ * GELU is z Phi(z); GELU_TANH its tanh approximation
+ *   z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).
+ * 1 <= d_in, d_out <= 2^20, any values (rows of BF16 features that are not a
+ * multiple of 8 take a slower path).
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  POETX_ACT_NONE = 0,
+  POETX_ACT_RELU = 1,
+  POETX_ACT_SILU = 2,
+  POETX_ACT_GELU = 3,
+  POETX_ACT_GELU_TANH = 4
+} poetx_activation;
+
+size_t poetx_linear_forward_workspace_size(int d_in, int d_out, int64_t tokens,
+                                           poetx_dtype dtype);
+poetx_status poetx_linear_forward(const void* x, const void* W, const float* bias,
+                                  const void* residual, void* y, void* z_saved, int d_in,
+                                  int d_out, int64_t tokens, poetx_activation act,
+                                  poetx_dtype dtype, void* workspace, size_t workspace_bytes,
+                                  poetx_stream stream);
+size_t poetx_linear_backward_workspace_size(int d_in, int d_out, int64_t tokens,
+                                            poetx_activation act, poetx_dtype dtype,
+                                            int with_dbias);
+poetx_status poetx_linear_backward(const void* dy, const void* z_saved, const void* W, void* dx,
+                                   float* dbias, int d_in, int d_out, int64_t tokens,
+                                   poetx_activation act, poetx_dtype dtype, void* workspace,
+                                   size_t workspace_bytes, poetx_stream stream);
+
+/* RMS norm of every query and key head and the rotary embedding, one pass.
+ * Row of a head, x[0..head_dim), at token t with (c, s) = tables[p][pair], p
+ * = positions[t] (NULL: p = t):
+ *   n_i = gamma_i x_i / sqrt(mean(x^2) + eps)      (gamma NULL: ones)
+ *   y_a = n_a c - n_b s, y_b = n_b c + n_a s       for pairs (a, b) of the
+ *   first rot_dim features, (i, i + rot_dim/2) or, interleaved, (2i, 2i+1);
+ *   the other features are n.
+ *   q: row t at q + t * ld_q elements, n_q_heads heads of head_dim
+ *   contiguous elements; likewise k and every other tensor, so slices of a
+ *   fused projection need no copy.  Any element alignment and any ld_* that
+ *   keeps rows apart (rows and slices aligned to 16 bytes are fastest).
+ *   gamma_q, gamma_k [head_dim], cos_table, sin_table [table_rows]
+ *   [rot_dim/2]: float32; positions [tokens] int32.  n_k_heads may be 0
+ *   (then the k pointers are not used); rot_dim = 0: the norm alone.
+ *   Outputs may be the inputs (with the same ld).
+ * A position outside 0..table_rows-1 is not followed: the token's outputs
+ * (backward: dq, dk) are 0, it adds nothing to dgamma, and
+ * POETX_ERR_INVALID_ARG is recorded in the status word.
+ * Backward, from the gradients of the outputs and the inputs: dq, dk, and
+ * the sums dgamma_q, dgamma_k [head_dim] (overwritten; NULL = not wanted).
+ * Arithmetic in fp32.  head_dim <= 512 (UNSUPPORTED beyond), rot_dim even
+ * and <= head_dim, eps > 0. */
+poetx_status poetx_qk_norm_rope_forward(const void* q, const void* k, const float* gamma_q,
+                                        const float* gamma_k, const float* cos_table,
+                                        const float* sin_table, const int32_t* positions,
+                                        void* q_out, void* k_out, int64_t ld_q, int64_t ld_k,
+                                        int64_t ld_q_out, int64_t ld_k_out, int n_q_heads,
+                                        int n_k_heads, int head_dim, int rot_dim,
+                                        int64_t table_rows, int interleaved, float eps,
+                                        int64_t tokens, poetx_dtype dtype, poetx_stream stream);
+size_t poetx_qk_norm_rope_backward_workspace_size(int n_q_heads, int n_k_heads, int head_dim,
+                                                  int64_t tokens, poetx_dtype dtype);
+poetx_status poetx_qk_norm_rope_backward(
+    const void* dq_out, const void* dk_out, const void* q, const void* k, const float* gamma_q,
+    const float* gamma_k, const float* cos_table, const float* sin_table, const int32_t* positions,
+    void* dq, void* dk, float* dgamma_q, float* dgamma_k, int64_t ld_dq_out, int64_t ld_dk_out,
+    int64_t ld_q, int64_t ld_k, int64_t ld_dq, int64_t ld_dk, int n_q_heads, int n_k_heads,
+    int head_dim, int rot_dim, int64_t table_rows, int interleaved, float eps, int64_t tokens,
+    poetx_dtype dtype, void* workspace, size_t workspace_bytes, poetx_stream stream);
+
+/* Global gradient norm over a list of tensors, the clipped gradients, and
+ * Adam over a list of packed vectors with the clip applied as it reads them:
+ *   norm  = sqrt(sum over all tensors of g^2)
+ *   scale = min(1, max_norm / (norm + 1e-6))     (max_norm >= 0)
+ *   poetx_clip_grads: out = scale g (outs may be grads: in place)
+ *   poetx_adam_update_many: poetx_adam_update's step on scale g;
+ *     max_norm < 0: no clip (norm and the workspace are not used).
+ *   grads, outs, theta, m, v: HOST arrays of n_tensors device pointers, read
+ *   during the call; counts: host array of element counts (0 allowed);
+ *   dtypes: host array of poetx_dtype per gradient, NULL = all float32
+ *   (theta, m, v and Adam's gradients are float32).  Any element alignment.
+ *   norm: one device float, written.
+ * Any finite gradients have a finite norm as long as it is below 3.4e38
+ * (squares that leave fp32's range are summed in 64 bits); a NaN or infinite
+ * gradient makes the norm, and then every output, NaN or infinite or 0 as
+ * the formulas say.  No atomics: results do not change from run to run. */
+size_t poetx_grad_norm_workspace_size(int n_tensors);
+poetx_status poetx_grad_norm(int n_tensors, const void* const* grads, const int64_t* counts,
+                             const int32_t* dtypes, float* norm, void* workspace,
+                             size_t workspace_bytes, poetx_stream stream);
+poetx_status poetx_clip_grads(int n_tensors, const void* const* grads, void* const* outs,
+                              const int64_t* counts, const int32_t* dtypes, float max_norm,
+                              float* norm, void* workspace, size_t workspace_bytes,
+                              poetx_stream stream);
+poetx_status poetx_adam_update_many(int n_tensors, float* const* theta, const float* const* grads,
+                                    float* const* m, float* const* v, const int64_t* counts,
+                                    int step, float lr, float beta1, float beta2, float eps,
+                                    float weight_decay, float max_norm, float* norm,
+                                    void* workspace, size_t workspace_bytes,
+                                    poetx_stream stream);
+
 /* The W0 GEMM fused with the block-diagonal factors (technical summary,
  * section 2, input-centric bullet; the fusion itself is this library's):
  * with fusion on, poetx_forward computes y = R v in the epilogue of the

@@ -21,6 +21,13 @@ __all__ = [
     "poetx_transform_workspace_size", "poetx_transform_forward", "poetx_transform_backward",
     "poetx_permute_features", "poetx_fold_permutations", "poetx_merge_workspace_size",
     "poetx_merge", "poetx_adam_update", "poetx_quantize_w0", "poetx_dequantize_w0",
+    "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH",
+    "poetx_linear_forward_workspace_size", "poetx_linear_forward",
+    "poetx_linear_backward_workspace_size", "poetx_linear_backward",
+    "poetx_qk_norm_rope_forward", "poetx_qk_norm_rope_backward_workspace_size",
+    "poetx_qk_norm_rope_backward",
+    "poetx_grad_norm_workspace_size", "poetx_grad_norm", "poetx_clip_grads",
+    "poetx_adam_update_many",
     "poetx_set_block_epilogue_fusion",
     "poetx_set_w0_split_tail",
     "poetx_set_w0_pair_mma",
@@ -31,12 +38,19 @@ __all__ = [
 F32 = 0
 BF16 = 1
 
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_SILU = 2
+ACT_GELU = 3
+ACT_GELU_TANH = 4
+
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpoetx.so")
 
 _c_size = ctypes.c_size_t
 _c_int = ctypes.c_int
 _c_i64 = ctypes.c_int64
 _c_ptr = ctypes.c_void_p
+_c_f = ctypes.c_float
 
 # name -> (restype, argtypes); mirrors include/poetx.h
 _SIGNATURES = {
@@ -72,6 +86,26 @@ _SIGNATURES = {
                                    ctypes.c_float, _c_ptr]),
     "poetx_quantize_w0": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_int, _c_int, _c_int, _c_ptr]),
     "poetx_dequantize_w0": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_int, _c_int, _c_int, _c_ptr]),
+    "poetx_linear_forward_workspace_size": (_c_size, [_c_int, _c_int, _c_i64, _c_int]),
+    "poetx_linear_forward": (_c_int, [_c_ptr] * 6 + [_c_int, _c_int, _c_i64, _c_int, _c_int,
+                                                     _c_ptr, _c_size, _c_ptr]),
+    "poetx_linear_backward_workspace_size": (_c_size, [_c_int, _c_int, _c_i64, _c_int, _c_int,
+                                                       _c_int]),
+    "poetx_linear_backward": (_c_int, [_c_ptr] * 5 + [_c_int, _c_int, _c_i64, _c_int, _c_int,
+                                                      _c_ptr, _c_size, _c_ptr]),
+    "poetx_qk_norm_rope_forward": (_c_int, [_c_ptr] * 9 + [_c_i64] * 4 + [_c_int] * 4 +
+                                   [_c_i64, _c_int, _c_f, _c_i64, _c_int, _c_ptr]),
+    "poetx_qk_norm_rope_backward_workspace_size": (_c_size, [_c_int, _c_int, _c_int, _c_i64,
+                                                             _c_int]),
+    "poetx_qk_norm_rope_backward": (_c_int, [_c_ptr] * 13 + [_c_i64] * 6 + [_c_int] * 4 +
+                                    [_c_i64, _c_int, _c_f, _c_i64, _c_int, _c_ptr, _c_size,
+                                     _c_ptr]),
+    "poetx_grad_norm_workspace_size": (_c_size, [_c_int]),
+    "poetx_grad_norm": (_c_int, [_c_int] + [_c_ptr] * 5 + [_c_size, _c_ptr]),
+    "poetx_clip_grads": (_c_int, [_c_int] + [_c_ptr] * 4 + [_c_f, _c_ptr, _c_ptr, _c_size,
+                                                            _c_ptr]),
+    "poetx_adam_update_many": (_c_int, [_c_int] + [_c_ptr] * 5 + [_c_int] + [_c_f] * 6 +
+                               [_c_ptr, _c_ptr, _c_size, _c_ptr]),
     "poetx_set_block_epilogue_fusion": (_c_int, [_c_int]),
     "poetx_set_w0_split_tail": (_c_int, [_c_int]),
     "poetx_set_w0_pair_mma": (_c_int, [_c_int]),
@@ -241,6 +275,106 @@ def poetx_quantize_w0(W0, W0_q, scales, d_in, d_out, dtype, stream=None):
 def poetx_dequantize_w0(W0_q, scales, W0, d_in, d_out, dtype, stream=None):
     _check("poetx_dequantize_w0", load_library().poetx_dequantize_w0(
         _ptr(W0_q), _ptr(scales), _ptr(W0), d_in, d_out, dtype, _stream(stream)))
+
+
+def poetx_linear_forward_workspace_size(d_in, d_out, tokens, dtype) -> int:
+    return load_library().poetx_linear_forward_workspace_size(d_in, d_out, tokens, dtype)
+
+
+def poetx_linear_forward(x, W, bias, residual, y, z_saved, d_in, d_out, tokens, act, dtype,
+                         workspace, stream=None):
+    _check("poetx_linear_forward", load_library().poetx_linear_forward(
+        _ptr(x), _ptr(W), _ptr(bias), _ptr(residual), _ptr(y), _ptr(z_saved), d_in, d_out, tokens,
+        act, dtype, _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def poetx_linear_backward_workspace_size(d_in, d_out, tokens, act, dtype, with_dbias=True) -> int:
+    return load_library().poetx_linear_backward_workspace_size(d_in, d_out, tokens, act, dtype,
+                                                               int(bool(with_dbias)))
+
+
+def poetx_linear_backward(dy, z_saved, W, dx, dbias, d_in, d_out, tokens, act, dtype, workspace,
+                          stream=None):
+    _check("poetx_linear_backward", load_library().poetx_linear_backward(
+        _ptr(dy), _ptr(z_saved), _ptr(W), _ptr(dx), _ptr(dbias), d_in, d_out, tokens, act, dtype,
+        _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def poetx_qk_norm_rope_forward(q, k, gamma_q, gamma_k, cos_table, sin_table, positions, q_out,
+                               k_out, ld_q, ld_k, ld_q_out, ld_k_out, n_q_heads, n_k_heads,
+                               head_dim, rot_dim, table_rows, interleaved, eps, tokens, dtype,
+                               stream=None):
+    _check("poetx_qk_norm_rope_forward", load_library().poetx_qk_norm_rope_forward(
+        _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(cos_table), _ptr(sin_table),
+        _ptr(positions), _ptr(q_out), _ptr(k_out), ld_q, ld_k, ld_q_out, ld_k_out, n_q_heads,
+        n_k_heads, head_dim, rot_dim, table_rows, int(bool(interleaved)), eps, tokens, dtype,
+        _stream(stream)))
+
+
+def poetx_qk_norm_rope_backward_workspace_size(n_q_heads, n_k_heads, head_dim, tokens,
+                                               dtype) -> int:
+    return load_library().poetx_qk_norm_rope_backward_workspace_size(n_q_heads, n_k_heads,
+                                                                     head_dim, tokens, dtype)
+
+
+def poetx_qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q, gamma_k, cos_table, sin_table,
+                                positions, dq, dk, dgamma_q, dgamma_k, ld_dq_out, ld_dk_out, ld_q,
+                                ld_k, ld_dq, ld_dk, n_q_heads, n_k_heads, head_dim, rot_dim,
+                                table_rows, interleaved, eps, tokens, dtype, workspace,
+                                stream=None):
+    _check("poetx_qk_norm_rope_backward", load_library().poetx_qk_norm_rope_backward(
+        _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
+        _ptr(cos_table), _ptr(sin_table), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dgamma_q),
+        _ptr(dgamma_k), ld_dq_out, ld_dk_out, ld_q, ld_k, ld_dq, ld_dk, n_q_heads, n_k_heads,
+        head_dim, rot_dim, table_rows, int(bool(interleaved)), eps, tokens, dtype,
+        _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def poetx_grad_norm_workspace_size(n_tensors) -> int:
+    return load_library().poetx_grad_norm_workspace_size(n_tensors)
+
+
+def _ptrs(tensors):
+    """Host array of the tensors' device pointers."""
+    return (_c_ptr * len(tensors))(*[_ptr(t) for t in tensors])
+
+
+def _counts(tensors):
+    return (_c_i64 * len(tensors))(*[t.numel() for t in tensors])
+
+
+def _dtypes(tensors):
+    """Host array of poetx_dtype per tensor, or None if all are float32."""
+    import torch
+    if all(t.dtype is torch.float32 for t in tensors):
+        return None
+    return (ctypes.c_int32 * len(tensors))(
+        *[{torch.float32: F32, torch.bfloat16: BF16}[t.dtype] for t in tensors])
+
+
+def poetx_grad_norm(grads, norm, workspace, stream=None):
+    """grads: list of contiguous float32 or bfloat16 tensors; norm: one float."""
+    _check("poetx_grad_norm", load_library().poetx_grad_norm(
+        len(grads), _ptrs(grads), _counts(grads), _dtypes(grads), _ptr(norm), _ptr(workspace),
+        _nbytes(workspace), _stream(stream)))
+
+
+def poetx_clip_grads(grads, outs, max_norm, norm, workspace, stream=None):
+    """outs (None: in place) <- the clipped gradients, norm <- their norm before."""
+    _check("poetx_clip_grads", load_library().poetx_clip_grads(
+        len(grads), _ptrs(grads), _ptrs(grads if outs is None else outs), _counts(grads),
+        _dtypes(grads), max_norm, _ptr(norm), _ptr(workspace), _nbytes(workspace),
+        _stream(stream)))
+
+
+def poetx_adam_update_many(theta, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
+                           weight_decay=0.0, max_norm=-1.0, norm=None, workspace=None,
+                           stream=None):
+    """Lists of contiguous float32 tensors; max_norm < 0: no clip."""
+    _check("poetx_adam_update_many", load_library().poetx_adam_update_many(
+        len(theta), _ptrs(theta), _ptrs(grads), _ptrs(m), _ptrs(v), _counts(theta), step, lr,
+        beta1, beta2, eps, weight_decay, max_norm, _ptr(norm), _ptr(workspace),
+        _nbytes(workspace), _stream(stream)))
 
 
 def poetx_set_block_epilogue_fusion(enable: bool) -> bool:

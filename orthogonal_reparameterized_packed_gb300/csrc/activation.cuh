@@ -1,0 +1,51 @@
+// The activations of poetx_linear_* and their derivatives in fp32.
+// FAST (bf16 results): exp and the quotient by the approximate intrinsics,
+// about 2^-21 relative, far below bf16's 2^-8; otherwise full fp32 accuracy.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "poetx.h"
+
+namespace poetx {
+
+template <bool FAST>
+__device__ __forceinline__ float sigmoid_f(float z) {
+  return FAST ? __fdividef(1.f, 1.f + __expf(-z)) : 1.f / (1.f + expf(-z));
+}
+
+// u of gelu_tanh: tanh(u) = 2 sigmoid(2u) - 1
+__device__ __forceinline__ float gelu_u(float z) {
+  return 0.7978845608028654f * fmaf(0.044715f * z * z, z, z);
+}
+
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act_f(float z) {
+  if (ACT == POETX_ACT_RELU) return z <= 0.f ? 0.f : z;  // NaN stays NaN
+  if (ACT == POETX_ACT_SILU) return z * sigmoid_f<FAST>(z);
+  if (ACT == POETX_ACT_GELU) return 0.5f * z * erfcf(-0.7071067811865476f * z);
+  if (ACT == POETX_ACT_GELU_TANH) return z * sigmoid_f<FAST>(2.f * gelu_u(z));
+  return z;
+}
+
+// d act / dz; relu: 0 at z = 0
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act_df(float z) {
+  if (ACT == POETX_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if (ACT == POETX_ACT_SILU) {
+    const float s = sigmoid_f<FAST>(z);
+    return s * (1.f + z * (1.f - s));
+  }
+  if (ACT == POETX_ACT_GELU) {
+    const float e = -0.5f * z * z;
+    return fmaf(z * 0.3989422804014327f, FAST ? __expf(e) : expf(e),
+                0.5f * erfcf(-0.7071067811865476f * z));
+  }
+  if (ACT == POETX_ACT_GELU_TANH) {
+    const float s = sigmoid_f<FAST>(2.f * gelu_u(z));
+    return s + 2.f * z * s * (1.f - s) * 0.7978845608028654f * fmaf(0.134145f * z, z, 1.f);
+  }
+  return 1.f;
+}
+
+}  // namespace poetx

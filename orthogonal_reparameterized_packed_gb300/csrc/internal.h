@@ -291,6 +291,68 @@ cudaError_t launch_adam(float* theta, const float* grad, float* m, float* v, lon
 cudaError_t launch_f32_to_bf16(const float* in, long long count, __nv_bfloat16* out,
                                cudaStream_t s);
 
+// ------------------------------------------- around the projections
+// z = x W^T + bias, y = act(z) + residual and its gradients (linear.cu); act
+// is a poetx_activation.  x [T][d_in], W [d_out][d_in], y / residual / z
+// [T][d_out] in the working type (is_bf16), bias [d_out] fp32; bias, residual
+// and z may be null.  `scratch` holds linear_forward_scratch bytes.
+size_t linear_forward_scratch(int d_in, int d_out, long long T, bool is_bf16);
+cudaError_t linear_forward(const void* x, const void* W, const float* bias, const void* residual,
+                           void* y, void* z, int d_in, int d_out, long long T, int act,
+                           bool is_bf16, void* scratch, cudaStream_t s);
+// dz = dy act'(z); dx = dz W, dbias = sum_t dz (either may be null).
+size_t linear_backward_scratch(int d_in, int d_out, long long T, int act, bool is_bf16,
+                               bool with_dbias);
+cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* dx, float* dbias,
+                            int d_in, int d_out, long long T, int act, bool is_bf16,
+                            void* scratch, cudaStream_t s);
+
+// RMS norm of every head of q and k and the rotary embedding (qk_norm_rope.cu).
+// Tensors: row t at ptr + t * ld, heads of D contiguous elements.
+struct QkNormRopeArgs {
+  const void* q = nullptr;
+  const void* k = nullptr;
+  long long ld_q = 0, ld_k = 0;
+  const float* gamma_q = nullptr;  // [D], null: ones
+  const float* gamma_k = nullptr;
+  const float* cos_table = nullptr;  // [table_rows][rot / 2]
+  const float* sin_table = nullptr;
+  const int* positions = nullptr;  // [T], null: t
+  long long table_rows = 0, T = 0;
+  int hq = 0, hk = 0, D = 0, rot = 0, interleaved = 0;
+  float eps = 0.f;
+  // forward: outputs; backward: the gradients of the outputs
+  const void* gq = nullptr;
+  const void* gk = nullptr;
+  long long ld_gq = 0, ld_gk = 0;
+  void* out_q = nullptr;  // forward: y; backward: dx
+  void* out_k = nullptr;
+  long long ld_out_q = 0, ld_out_k = 0;
+  float* dgamma_q = nullptr;  // backward, may be null
+  float* dgamma_k = nullptr;
+  float* part = nullptr;  // backward: partial sums of dgamma
+  int* status = nullptr;
+};
+cudaError_t qk_norm_rope_forward(const QkNormRopeArgs& a, bool is_bf16, cudaStream_t s);
+size_t qk_norm_rope_scratch(int hq, int hk, int D, long long T);
+cudaError_t qk_norm_rope_backward(const QkNormRopeArgs& a, bool is_bf16, cudaStream_t s);
+
+// Global gradient norm, clip and Adam over lists of tensors (optim.cu).
+// Host arrays of n device pointers; dtypes null: all fp32.
+size_t grad_norm_scratch(int n);
+cudaError_t grad_norm(int n, const void* const* grads, const int64_t* counts, const int* dtypes,
+                      float* norm, void* scratch, cudaStream_t s);
+cudaError_t clip_grads(int n, const void* const* grads, void* const* outs, const int64_t* counts,
+                       const int* dtypes, float max_norm, float* norm, void* scratch,
+                       cudaStream_t s);
+struct AdamHyper {
+  float lr, beta1, beta2, eps, wd, bc1, bc2;
+};
+cudaError_t adam_update_many(int n, float* const* theta, const float* const* grads,
+                             float* const* m, float* const* v, const int64_t* counts,
+                             const AdamHyper& h, float max_norm, float* norm, void* scratch,
+                             cudaStream_t s);
+
 // ------------------------------------------------------------ bookkeeping
 int* device_status_ptr();            // per-device status word (device memory)
 int read_and_clear_device_status();  // synchronous

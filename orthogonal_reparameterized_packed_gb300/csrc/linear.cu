@@ -1,0 +1,261 @@
+// The matrix product with bias, activation and residual, and its gradients:
+//   z = x W^T + bias,  y = act(z) + residual
+//   dz = dy act'(z),   dx = dz W,   dbias = sum_t dz
+#include <algorithm>
+#include <cstdint>
+
+#include "activation.cuh"
+#include "internal.h"
+#include "poetx.h"
+#include "ptx.cuh"
+
+namespace poetx {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float& o, float x) { o = x; }
+__device__ __forceinline__ void from_f(bf16& o, float x) { o = __float2bfloat16_rn(x); }
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T x[V];
+};
+
+// y = act(acc + bias) + residual for an fp32 product acc [T][N], element by element.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kThreads)
+    linear_epilogue_kernel(const float* __restrict__ acc, const float* __restrict__ bias,
+                           const T* residual, T* y, T* z, long long n, int N) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr bool FAST = sizeof(T) == 2;
+  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
+  for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < n;
+       i += stride) {
+    float v = acc[i];
+    if (bias != nullptr) v += bias[i % N];
+    if (z != nullptr) from_f(z[i], v);
+    v = act_f<ACT, FAST>(v);
+    if (residual != nullptr) v += to_f(residual[i]);
+    from_f(y[i], v);
+  }
+}
+
+// dz = dy act'(z) (stored where dz is not null) and, where part is not null,
+// its column sums over this CTA's rows: part[blockIdx.y][N].  32 column
+// threads of V columns each, 8 row threads; kRows rows per CTA.
+constexpr int kDzRows = 128;
+
+template <typename T, int ACT, int V>
+__global__ void __launch_bounds__(kThreads)
+    linear_dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, T* __restrict__ dz,
+                     float* __restrict__ part, long long T_rows, int N) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr bool FAST = sizeof(T) == 2;
+  __shared__ float sums[8][32 * V];
+  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+  const long long col = (static_cast<long long>(blockIdx.x) * 32 + tx) * V;
+  const long long r0 = static_cast<long long>(blockIdx.y) * kDzRows;
+  const long long r1 = min(r0 + kDzRows, T_rows);
+  float sum[V] = {};
+  if (col < N) {
+#pragma unroll 4
+    for (long long r = r0 + ty; r < r1; r += 8) {
+      const long long at = r * N + col;
+      Pack<T, V> g = *reinterpret_cast<const Pack<T, V>*>(dy + at);
+      Pack<T, V> zz = g;
+      if (ACT != POETX_ACT_NONE) zz = *reinterpret_cast<const Pack<T, V>*>(z + at);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float d = to_f(g.x[j]) * act_df<ACT, FAST>(to_f(zz.x[j]));
+        sum[j] += d;
+        from_f(g.x[j], d);
+      }
+      if (dz != nullptr) *reinterpret_cast<Pack<T, V>*>(dz + at) = g;
+    }
+  }
+  if (part == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < V; ++j) sums[ty][tx * V + j] = sum[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * V; i += kThreads) {
+    const long long c = static_cast<long long>(blockIdx.x) * 32 * V + i;
+    if (c >= N) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += sums[w][i];
+    part[static_cast<long long>(blockIdx.y) * N + c] = v;
+  }
+}
+
+// dbias[c] = sum over the row blocks' partial sums, in order.
+__global__ void __launch_bounds__(kThreads)
+    linear_dbias_kernel(const float* __restrict__ part, int blocks, int N,
+                        float* __restrict__ dbias) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ double sums[8][32];
+  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+  const int c = blockIdx.x * 32 + tx;
+  double v = 0.0;
+  if (c < N)
+    for (int b = ty; b < blocks; b += 8) v += part[static_cast<long long>(b) * N + c];
+  sums[ty][tx] = v;
+  __syncthreads();
+  if (ty == 0 && c < N) {
+    v = sums[0][tx];
+    for (int w = 1; w < 8; ++w) v += sums[w][tx];
+    dbias[c] = static_cast<float>(v);
+  }
+}
+
+// The kernel of a function template over the activation, by its runtime value.
+#define LINEAR_BY_ACT(act, call)        \
+  switch (act) {                        \
+    case POETX_ACT_RELU: call(1); break; \
+    case POETX_ACT_SILU: call(2); break; \
+    case POETX_ACT_GELU: call(3); break; \
+    case POETX_ACT_GELU_TANH: call(4); break; \
+    default: call(0);                   \
+  }
+
+// C[M][N] = A[M][K] B, fp32, on the CUDA cores (at most 65535 row tiles per launch).
+cudaError_t simt_product(const void* A, const void* B, long long b_k, long long b_n, float* C,
+                         long long M, int N, int K, bool is_bf16, const char* tag,
+                         cudaStream_t s) {
+  constexpr long long kRows = 1 << 21;
+  for (long long m = 0; m < M; m += kRows) {
+    SimtGemm g;
+    g.M = static_cast<int>(std::min(kRows, M - m));
+    g.N = N;
+    g.K = K;
+    g.bf16_inputs = is_bf16;
+    g.A = static_cast<const char*>(A) + m * K * (is_bf16 ? 2 : 4);
+    g.a_m = K;
+    g.a_k = 1;
+    g.B = B;
+    g.b_k = b_k;
+    g.b_n = b_n;
+    g.epi.out_f32 = C + m * N;
+    g.epi.ld = N;
+    g.tag = tag;
+    const cudaError_t e = simt_gemm_run(g, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <typename T>
+cudaError_t run_epilogue(const float* acc, const float* bias, const void* residual, void* y,
+                         void* z, long long n, int N, int act, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  const int grid = static_cast<int>(
+      std::min<long long>((n + kThreads - 1) / kThreads, 16ll * sm_count()));
+  prof_begin("linear_epilogue", s);
+#define RUN(A)                                                                              \
+  e = launch_pdl(linear_epilogue_kernel<T, A>, dim3(grid), dim3(kThreads), 0, s, acc, bias, \
+                 static_cast<const T*>(residual), static_cast<T*>(y), static_cast<T*>(z), n, N)
+  LINEAR_BY_ACT(act, RUN)
+#undef RUN
+  prof_end("linear_epilogue", s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t run_dz(const void* dy, const void* z, void* dz, float* part, long long T_rows, int N,
+                   int act, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  const dim3 grid(static_cast<unsigned>((N + 32 * V - 1) / (32 * V)),
+                  static_cast<unsigned>((T_rows + kDzRows - 1) / kDzRows));
+  prof_begin("linear_dz", s);
+#define RUN(A)                                                                       \
+  e = launch_pdl(linear_dz_kernel<T, A, V>, grid, dim3(kThreads), 0, s,              \
+                 static_cast<const T*>(dy), static_cast<const T*>(z), static_cast<T*>(dz), part, \
+                 T_rows, N)
+  LINEAR_BY_ACT(act, RUN)
+#undef RUN
+  prof_end("linear_dz", s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace
+
+size_t linear_forward_scratch(int d_in, int d_out, long long T, bool is_bf16) {
+  (void)d_in;
+  (void)is_bf16;
+  return round256(static_cast<size_t>(T) * d_out * 4);
+}
+
+cudaError_t linear_forward(const void* x, const void* W, const float* bias, const void* residual,
+                           void* y, void* z, int d_in, int d_out, long long T, int act,
+                           bool is_bf16, void* scratch, cudaStream_t s) {
+  float* acc = static_cast<float*>(scratch);
+  cudaError_t e = simt_product(x, W, 1, d_in, acc, T, d_out, d_in, is_bf16, "linear", s);
+  if (e != cudaSuccess) return e;
+  const long long n = T * d_out;
+  return is_bf16 ? run_epilogue<bf16>(acc, bias, residual, y, z, n, d_out, act, s)
+                 : run_epilogue<float>(acc, bias, residual, y, z, n, d_out, act, s);
+}
+
+size_t linear_backward_scratch(int d_in, int d_out, long long T, int act, bool is_bf16,
+                               bool with_dbias) {
+  size_t n = 0;
+  if (act != POETX_ACT_NONE) n += round256(static_cast<size_t>(T) * d_out * (is_bf16 ? 2 : 4));
+  if (with_dbias) n += round256(static_cast<size_t>((T + kDzRows - 1) / kDzRows) * d_out * 4);
+  return n + round256(static_cast<size_t>(T) * d_in * 4);
+}
+
+cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* dx, float* dbias,
+                            int d_in, int d_out, long long T, int act, bool is_bf16,
+                            void* scratch, cudaStream_t s) {
+  char* at = static_cast<char*>(scratch);
+  const size_t es = is_bf16 ? 2 : 4;
+  const void* dz = dy;
+  void* dz_out = nullptr;
+  if (act != POETX_ACT_NONE) {
+    dz_out = at;
+    dz = dz_out;
+    at += round256(static_cast<size_t>(T) * d_out * es);
+  }
+  float* part = nullptr;
+  const int blocks = static_cast<int>((T + kDzRows - 1) / kDzRows);
+  if (dbias != nullptr) {
+    part = reinterpret_cast<float*>(at);
+    at += round256(static_cast<size_t>(blocks) * d_out * 4);
+  }
+  cudaError_t e;
+  if (dz_out != nullptr || part != nullptr) {
+    void* keep = dx != nullptr ? dz_out : nullptr;
+    if (is_bf16)
+      e = d_out % 8 == 0 ? run_dz<bf16, 8>(dy, z, keep, part, T, d_out, act, s)
+                         : run_dz<bf16, 1>(dy, z, keep, part, T, d_out, act, s);
+    else
+      e = d_out % 4 == 0 ? run_dz<float, 4>(dy, z, keep, part, T, d_out, act, s)
+                         : run_dz<float, 1>(dy, z, keep, part, T, d_out, act, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (dbias != nullptr) {
+    prof_begin("linear_dbias", s);
+    e = launch_pdl(linear_dbias_kernel, dim3((d_out + 31) / 32), dim3(kThreads), 0, s,
+                   static_cast<const float*>(part), blocks, d_out, dbias);
+    prof_end("linear_dbias", s);
+    if (e != cudaSuccess) return e;
+  }
+  if (dx == nullptr) return cudaGetLastError();
+  float* acc = reinterpret_cast<float*>(at);
+  e = simt_product(dz, W, d_in, 1, acc, T, d_in, d_out, is_bf16, "linear_dgrad", s);
+  if (e != cudaSuccess) return e;
+  const long long n = T * d_in;
+  return is_bf16 ? run_epilogue<bf16>(acc, nullptr, nullptr, dx, nullptr, n, d_in, 0, s)
+                 : run_epilogue<float>(acc, nullptr, nullptr, dx, nullptr, n, d_in, 0, s);
+}
+
+}  // namespace poetx

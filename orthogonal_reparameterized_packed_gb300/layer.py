@@ -8,9 +8,10 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (BF16, F32, poetx_adam_update, poetx_backward, poetx_backward_workspace_size,
+from . import (BF16, F32, poetx_adam_update, poetx_adam_update_many, poetx_backward, poetx_backward_workspace_size,
                poetx_build_blocks, poetx_build_workspace_size, poetx_dequantize_w0,
                poetx_fold_permutations, poetx_forward, poetx_forward_workspace_size,
+               poetx_grad_norm_workspace_size,
                poetx_merge, poetx_merge_workspace_size, poetx_packed_size,
                poetx_permute_features, poetx_quantize_w0)
 
@@ -159,13 +160,17 @@ def quantize(W0, code, stream=None):
 
 class PoetxAdam:
     """Adam on packed parameter vectors (float32 device tensors), one fused
-    launch per vector per step."""
+    launch per vector per step.  With max_norm the gradients' global norm is
+    clipped to it as they are read (self.norm: the norm before the clip), and
+    a step is two launches for all vectors together (max_norm = inf: no
+    clip); results then agree with the launch per vector to rounding."""
 
     def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0):
         self.params = list(params)
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.m = [torch.zeros_like(p) for p in self.params]
         self.v = [torch.zeros_like(p) for p in self.params]
+        self.norm = self._workspace = None
         self.t = 0
 
     def reset(self):
@@ -175,11 +180,31 @@ class PoetxAdam:
             v.zero_()
         self.t = 0
 
-    def step(self, grads, stream=None):
+    def step(self, grads, stream=None, max_norm=None):
+        if max_norm is not None and not max_norm >= 0:
+            raise ValueError(f"max_norm must be at least 0, got {max_norm}")
+        todo = list(zip(self.params, grads, self.m, self.v))
+        for p, g, _, _ in todo:
+            if isinstance(g, torch.Tensor) and (g.numel() < p.numel() or
+                                                g.dtype is not torch.float32 or
+                                                not g.is_contiguous()):
+                raise ValueError(f"a contiguous float32 gradient of {p.numel()} elements is "
+                                 f"needed, got {tuple(g.shape)}, {g.dtype}")
         self.t += 1
-        for p, g, m, v in zip(self.params, grads, self.m, self.v):
-            poetx_adam_update(p, g, m, v, p.numel(), self.t, self.lr, self.betas[0],
-                              self.betas[1], self.eps, self.weight_decay, stream)
+        if max_norm is None:
+            for p, g, m, v in todo:
+                poetx_adam_update(p, g, m, v, p.numel(), self.t, self.lr, self.betas[0],
+                                  self.betas[1], self.eps, self.weight_decay, stream)
+            return
+        if self.norm is None:
+            dev = self.params[0].device
+            self.norm = torch.zeros((), dtype=torch.float32, device=dev)
+            self._workspace = torch.empty((poetx_grad_norm_workspace_size(len(self.params)),),
+                                          dtype=torch.uint8, device=dev)
+        poetx_adam_update_many([p for p, _, _, _ in todo], [g for _, g, _, _ in todo],
+                               [m for _, _, m, _ in todo], [v for _, _, _, v in todo], self.t,
+                               self.lr, self.betas[0], self.betas[1], self.eps,
+                               self.weight_decay, max_norm, self.norm, self._workspace, stream)
 
 
 def to_device(inp, device="cuda"):
