@@ -6,6 +6,7 @@
 
 #include "activation.cuh"
 #include "internal.h"
+#include "linear.h"
 #include "poetx.h"
 #include "ptx.cuh"
 
@@ -15,6 +16,9 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 256;
+
+// Elements between rows of `cols` bf16 features once they are TMA operands.
+long long pitch8(int cols) { return (static_cast<long long>(cols) + 7) / 8 * 8; }
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
@@ -54,7 +58,7 @@ constexpr int kDzRows = 128;
 template <typename T, int ACT, int V>
 __global__ void __launch_bounds__(kThreads)
     linear_dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, T* __restrict__ dz,
-                     float* __restrict__ part, long long T_rows, int N) {
+                     long long ld_dz, float* __restrict__ part, long long T_rows, int N) {
   pdl_wait();
   pdl_trigger();
   constexpr bool FAST = sizeof(T) == 2;
@@ -77,7 +81,7 @@ __global__ void __launch_bounds__(kThreads)
         sum[j] += d;
         from_f(g.x[j], d);
       }
-      if (dz != nullptr) *reinterpret_cast<Pack<T, V>*>(dz + at) = g;
+      if (dz != nullptr) *reinterpret_cast<Pack<T, V>*>(dz + r * ld_dz + col) = g;
     }
   }
   if (part == nullptr) return;
@@ -127,16 +131,14 @@ __global__ void __launch_bounds__(kThreads)
 
 // C[M][N] = A[M][K] B, fp32, on the CUDA cores (at most 65535 row tiles per launch).
 cudaError_t simt_product(const void* A, const void* B, long long b_k, long long b_n, float* C,
-                         long long M, int N, int K, bool is_bf16, const char* tag,
-                         cudaStream_t s) {
+                         long long M, int N, int K, const char* tag, cudaStream_t s) {
   constexpr long long kRows = 1 << 21;
   for (long long m = 0; m < M; m += kRows) {
     SimtGemm g;
     g.M = static_cast<int>(std::min(kRows, M - m));
     g.N = N;
     g.K = K;
-    g.bf16_inputs = is_bf16;
-    g.A = static_cast<const char*>(A) + m * K * (is_bf16 ? 2 : 4);
+    g.A = static_cast<const float*>(A) + m * K;
     g.a_m = K;
     g.a_k = 1;
     g.B = B;
@@ -149,6 +151,47 @@ cudaError_t simt_product(const void* A, const void* B, long long b_k, long long 
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+// out[r][0..cols) = in[r][0..cols), rows in_ld and out_ld apart: rows of an odd
+// number of bf16 features onto a 16-byte pitch, which TMA needs.  One warp
+// per row piece of 256 columns.
+__global__ void __launch_bounds__(kThreads)
+    pad_rows_kernel(const bf16* __restrict__ in, long long in_ld, bf16* __restrict__ out,
+                    long long out_ld, long long rows, int cols) {
+  pdl_wait();
+  pdl_trigger();
+  const int pieces = (cols + 255) / 256;
+  const long long items = rows * pieces;
+  const int lane = threadIdx.x % 32;
+  for (long long it = blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
+       it < items; it += static_cast<long long>(gridDim.x) * (kThreads / 32)) {
+    const long long r = it / pieces;
+    const int c0 = static_cast<int>(it - r * pieces) * 256;
+    bf16 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + lane + 32 * j;
+      if (c < cols) v[j] = in[r * in_ld + c];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + lane + 32 * j;
+      if (c < cols) out[r * out_ld + c] = v[j];
+    }
+  }
+}
+
+cudaError_t pad_rows(const void* in, void* out, long long rows, int cols, cudaStream_t s) {
+  const long long items = rows * ((cols + 255) / 256);
+  const int grid = static_cast<int>(
+      std::min<long long>((items + kThreads / 32 - 1) / (kThreads / 32), 16ll * sm_count()));
+  prof_begin("linear_pad", s);
+  const cudaError_t e =
+      launch_pdl(pad_rows_kernel, dim3(grid), dim3(kThreads), 0, s, static_cast<const bf16*>(in),
+                 static_cast<long long>(cols), static_cast<bf16*>(out), pitch8(cols), rows, cols);
+  prof_end("linear_pad", s);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T>
@@ -168,16 +211,16 @@ cudaError_t run_epilogue(const float* acc, const float* bias, const void* residu
 }
 
 template <typename T, int V>
-cudaError_t run_dz(const void* dy, const void* z, void* dz, float* part, long long T_rows, int N,
-                   int act, cudaStream_t s) {
+cudaError_t run_dz(const void* dy, const void* z, void* dz, long long ld_dz, float* part,
+                   long long T_rows, int N, int act, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   const dim3 grid(static_cast<unsigned>((N + 32 * V - 1) / (32 * V)),
                   static_cast<unsigned>((T_rows + kDzRows - 1) / kDzRows));
   prof_begin("linear_dz", s);
 #define RUN(A)                                                                       \
   e = launch_pdl(linear_dz_kernel<T, A, V>, grid, dim3(kThreads), 0, s,              \
-                 static_cast<const T*>(dy), static_cast<const T*>(z), static_cast<T*>(dz), part, \
-                 T_rows, N)
+                 static_cast<const T*>(dy), static_cast<const T*>(z), static_cast<T*>(dz), \
+                 ld_dz, part, T_rows, N)
   LINEAR_BY_ACT(act, RUN)
 #undef RUN
   prof_end("linear_dz", s);
@@ -186,76 +229,133 @@ cudaError_t run_dz(const void* dy, const void* z, void* dz, float* part, long lo
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
+// Bytes of a padded copy of [rows][cols] bf16, 0 where the rows are aligned already.
+size_t pad_bytes(long long rows, int cols) {
+  return cols % 8 == 0 ? 0 : round256(static_cast<size_t>(rows) * pitch8(cols) * 2);
+}
+
 }  // namespace
 
+// bf16: padded copies of x and W where d_in is no multiple of 8; fp32: the product.
 size_t linear_forward_scratch(int d_in, int d_out, long long T, bool is_bf16) {
-  (void)d_in;
-  (void)is_bf16;
+  if (is_bf16) return pad_bytes(T, d_in) + pad_bytes(d_out, d_in);
   return round256(static_cast<size_t>(T) * d_out * 4);
 }
 
 cudaError_t linear_forward(const void* x, const void* W, const float* bias, const void* residual,
                            void* y, void* z, int d_in, int d_out, long long T, int act,
                            bool is_bf16, void* scratch, cudaStream_t s) {
-  float* acc = static_cast<float*>(scratch);
-  cudaError_t e = simt_product(x, W, 1, d_in, acc, T, d_out, d_in, is_bf16, "linear", s);
-  if (e != cudaSuccess) return e;
-  const long long n = T * d_out;
-  return is_bf16 ? run_epilogue<bf16>(acc, bias, residual, y, z, n, d_out, act, s)
-                 : run_epilogue<float>(acc, bias, residual, y, z, n, d_out, act, s);
+  cudaError_t e;
+  if (!is_bf16) {
+    float* acc = static_cast<float*>(scratch);
+    e = simt_product(x, W, 1, d_in, acc, T, d_out, d_in, "linear", s);
+    if (e != cudaSuccess) return e;
+    return run_epilogue<float>(acc, bias, residual, y, z, T * d_out, d_out, act, s);
+  }
+  LinearProduct g;
+  g.A = x;
+  g.B = W;
+  g.lda = g.ldb = pitch8(d_in);
+  if (d_in % 8 != 0) {
+    char* xp = static_cast<char*>(scratch);
+    char* wp = xp + pad_bytes(T, d_in);
+    if ((e = pad_rows(x, xp, T, d_in, s)) != cudaSuccess) return e;
+    if ((e = pad_rows(W, wp, d_out, d_in, s)) != cudaSuccess) return e;
+    g.A = xp;
+    g.B = wp;
+  }
+  g.ld = d_out;
+  g.bias = bias;
+  g.residual = residual;
+  g.y = y;
+  g.z = z;
+  g.M = T;
+  g.N = d_out;
+  g.K = d_in;
+  g.act = act;
+  return linear_pair(g, s);
 }
+
+// Scratch of the backward: dz (unless it is dy itself, aligned), the row
+// blocks' sums of dbias, and bf16: the padded W; fp32: the product.
+namespace {
+
+struct BackwardPlan {
+  size_t dz = 0, part = 0, w = 0, acc = 0;
+  int blocks;
+  BackwardPlan(int d_in, int d_out, long long T, int act, bool is_bf16, bool with_dbias) {
+    blocks = static_cast<int>((T + kDzRows - 1) / kDzRows);
+    if (is_bf16) {
+      if (act != POETX_ACT_NONE || d_out % 8 != 0)
+        dz = round256(static_cast<size_t>(T) * pitch8(d_out) * 2);
+      w = pad_bytes(d_out, d_in);
+    } else {
+      if (act != POETX_ACT_NONE) dz = round256(static_cast<size_t>(T) * d_out * 4);
+      acc = round256(static_cast<size_t>(T) * d_in * 4);
+    }
+    if (with_dbias) part = round256(static_cast<size_t>(blocks) * d_out * 4);
+  }
+  size_t bytes() const { return dz + part + w + acc; }
+};
+
+}  // namespace
 
 size_t linear_backward_scratch(int d_in, int d_out, long long T, int act, bool is_bf16,
                                bool with_dbias) {
-  size_t n = 0;
-  if (act != POETX_ACT_NONE) n += round256(static_cast<size_t>(T) * d_out * (is_bf16 ? 2 : 4));
-  if (with_dbias) n += round256(static_cast<size_t>((T + kDzRows - 1) / kDzRows) * d_out * 4);
-  return n + round256(static_cast<size_t>(T) * d_in * 4);
+  return BackwardPlan(d_in, d_out, T, act, is_bf16, with_dbias).bytes();
 }
 
 cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* dx, float* dbias,
                             int d_in, int d_out, long long T, int act, bool is_bf16,
                             void* scratch, cudaStream_t s) {
+  const BackwardPlan plan(d_in, d_out, T, act, is_bf16, dbias != nullptr);
   char* at = static_cast<char*>(scratch);
-  const size_t es = is_bf16 ? 2 : 4;
-  const void* dz = dy;
-  void* dz_out = nullptr;
-  if (act != POETX_ACT_NONE) {
-    dz_out = at;
-    dz = dz_out;
-    at += round256(static_cast<size_t>(T) * d_out * es);
-  }
-  float* part = nullptr;
-  const int blocks = static_cast<int>((T + kDzRows - 1) / kDzRows);
-  if (dbias != nullptr) {
-    part = reinterpret_cast<float*>(at);
-    at += round256(static_cast<size_t>(blocks) * d_out * 4);
-  }
+  void* dz = plan.dz > 0 && dx != nullptr ? at : nullptr;  // null: not stored
+  float* part = plan.part > 0 ? reinterpret_cast<float*>(at + plan.dz) : nullptr;
+  void* wp = at + plan.dz + plan.part;
+  float* acc = reinterpret_cast<float*>(at + plan.dz + plan.part + plan.w);
+  const long long ld_dz = is_bf16 ? pitch8(d_out) : d_out;
   cudaError_t e;
-  if (dz_out != nullptr || part != nullptr) {
-    void* keep = dx != nullptr ? dz_out : nullptr;
+  if (dz != nullptr || part != nullptr) {
     if (is_bf16)
-      e = d_out % 8 == 0 ? run_dz<bf16, 8>(dy, z, keep, part, T, d_out, act, s)
-                         : run_dz<bf16, 1>(dy, z, keep, part, T, d_out, act, s);
+      e = d_out % 8 == 0 ? run_dz<bf16, 8>(dy, z, dz, ld_dz, part, T, d_out, act, s)
+                         : run_dz<bf16, 1>(dy, z, dz, ld_dz, part, T, d_out, act, s);
     else
-      e = d_out % 4 == 0 ? run_dz<float, 4>(dy, z, keep, part, T, d_out, act, s)
-                         : run_dz<float, 1>(dy, z, keep, part, T, d_out, act, s);
+      e = d_out % 4 == 0 ? run_dz<float, 4>(dy, z, dz, ld_dz, part, T, d_out, act, s)
+                         : run_dz<float, 1>(dy, z, dz, ld_dz, part, T, d_out, act, s);
     if (e != cudaSuccess) return e;
   }
-  if (dbias != nullptr) {
+  if (part != nullptr) {
     prof_begin("linear_dbias", s);
     e = launch_pdl(linear_dbias_kernel, dim3((d_out + 31) / 32), dim3(kThreads), 0, s,
-                   static_cast<const float*>(part), blocks, d_out, dbias);
+                   static_cast<const float*>(part), plan.blocks, d_out, dbias);
     prof_end("linear_dbias", s);
     if (e != cudaSuccess) return e;
   }
-  if (dx == nullptr) return cudaGetLastError();
-  float* acc = reinterpret_cast<float*>(at);
-  e = simt_product(dz, W, d_in, 1, acc, T, d_in, d_out, is_bf16, "linear_dgrad", s);
-  if (e != cudaSuccess) return e;
-  const long long n = T * d_in;
-  return is_bf16 ? run_epilogue<bf16>(acc, nullptr, nullptr, dx, nullptr, n, d_in, 0, s)
-                 : run_epilogue<float>(acc, nullptr, nullptr, dx, nullptr, n, d_in, 0, s);
+  if (dx == nullptr) return cudaSuccess;
+  const void* grad = dz != nullptr ? dz : dy;
+  if (!is_bf16) {
+    e = simt_product(grad, W, d_in, 1, acc, T, d_in, d_out, "linear_dgrad", s);
+    if (e != cudaSuccess) return e;
+    return run_epilogue<float>(acc, nullptr, nullptr, dx, nullptr, T * d_in, d_in, 0, s);
+  }
+  LinearProduct g;
+  g.A = grad;
+  g.lda = ld_dz;
+  g.B = W;
+  g.ldb = pitch8(d_in);
+  g.b_mn = true;
+  if (plan.w > 0) {
+    if ((e = pad_rows(W, wp, d_out, d_in, s)) != cudaSuccess) return e;
+    g.B = wp;
+  }
+  g.ld = d_in;
+  g.y = dx;
+  g.M = T;
+  g.N = d_in;
+  g.K = d_out;
+  g.tag = "linear_dgrad";
+  return linear_pair(g, s);
 }
 
 }  // namespace poetx

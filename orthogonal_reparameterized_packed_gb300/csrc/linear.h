@@ -1,0 +1,30 @@
+// One matrix product of poetx_linear_* on the tensor cores, bf16 in and out:
+//   z = A B^T + bias,  y = act(z) + residual
+// A [M][K], rows lda apart; B [N][K], or [K][N] when b_mn, rows ldb apart
+// (lda, ldb multiples of 8; pointers 16-byte aligned); y, z, residual [M][N],
+// rows ld apart (any ld).  bias fp32; bias, z and residual may be null.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace poetx {
+
+struct LinearProduct {
+  const void* A = nullptr;
+  const void* B = nullptr;
+  long long lda = 0, ldb = 0, ld = 0;
+  bool b_mn = false;
+  const float* bias = nullptr;
+  const void* residual = nullptr;
+  void* y = nullptr;
+  void* z = nullptr;
+  long long M = 0;
+  int N = 0, K = 0;
+  int act = 0;
+  const char* tag = "linear";
+};
+
+// On CTA pairs, 256 x 256 tiles (linear_pair.cu).
+cudaError_t linear_pair(const LinearProduct& g, cudaStream_t s);
+
+}  // namespace poetx
