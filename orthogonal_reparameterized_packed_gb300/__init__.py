@@ -9,6 +9,7 @@ PyTorch is used for device memory and streams only.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -163,7 +164,9 @@ def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    # the current device's current stream as torch.cuda.current_stream().cuda_stream gives it,
+    # without making a Stream object (0.5 instead of 3 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(fn, status):
@@ -334,36 +337,46 @@ def poetx_grad_norm_workspace_size(n_tensors) -> int:
     return load_library().poetx_grad_norm_workspace_size(n_tensors)
 
 
+def _host(code, values):
+    """(array kept alive, its address) of host values."""
+    a = array.array(code, values)
+    return a, a.buffer_info()[0]
+
+
 def _ptrs(tensors):
     """Host array of the tensors' device pointers."""
-    return (_c_ptr * len(tensors))(*[_ptr(t) for t in tensors])
+    import torch
+    return _host("Q", map(torch.Tensor.data_ptr, tensors))
 
 
 def _counts(tensors):
-    return (_c_i64 * len(tensors))(*[t.numel() for t in tensors])
+    import torch
+    return _host("q", map(torch.Tensor.numel, tensors))
 
 
 def _dtypes(tensors):
-    """Host array of poetx_dtype per tensor, or None if all are float32."""
+    """Host array of poetx_dtype per tensor, or no array if all are float32."""
     import torch
-    if all(t.dtype is torch.float32 for t in tensors):
-        return None
-    return (ctypes.c_int32 * len(tensors))(
-        *[{torch.float32: F32, torch.bfloat16: BF16}[t.dtype] for t in tensors])
+    kinds = {t.dtype for t in tensors}
+    if kinds <= {torch.float32}:
+        return None, None
+    code = {torch.float32: F32, torch.bfloat16: BF16}
+    return _host("i", [code[t.dtype] for t in tensors])
 
 
 def poetx_grad_norm(grads, norm, workspace, stream=None):
     """grads: list of contiguous float32 or bfloat16 tensors; norm: one float."""
+    (p, pa), (c, ca), (d, da) = _ptrs(grads), _counts(grads), _dtypes(grads)
     _check("poetx_grad_norm", load_library().poetx_grad_norm(
-        len(grads), _ptrs(grads), _counts(grads), _dtypes(grads), _ptr(norm), _ptr(workspace),
-        _nbytes(workspace), _stream(stream)))
+        len(c), pa, ca, da, _ptr(norm), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def poetx_clip_grads(grads, outs, max_norm, norm, workspace, stream=None):
     """outs (None: in place) <- the clipped gradients, norm <- their norm before."""
+    (p, pa), (c, ca), (d, da) = _ptrs(grads), _counts(grads), _dtypes(grads)
+    o, oa = (p, pa) if outs is None else _ptrs(outs)
     _check("poetx_clip_grads", load_library().poetx_clip_grads(
-        len(grads), _ptrs(grads), _ptrs(grads if outs is None else outs), _counts(grads),
-        _dtypes(grads), max_norm, _ptr(norm), _ptr(workspace), _nbytes(workspace),
+        len(c), pa, oa, ca, da, max_norm, _ptr(norm), _ptr(workspace), _nbytes(workspace),
         _stream(stream)))
 
 
@@ -371,10 +384,11 @@ def poetx_adam_update_many(theta, grads, m, v, step, lr, beta1=0.9, beta2=0.999,
                            weight_decay=0.0, max_norm=-1.0, norm=None, workspace=None,
                            stream=None):
     """Lists of contiguous float32 tensors; max_norm < 0: no clip."""
+    kept = [_ptrs(t) for t in (theta, grads, m, v)]
+    c, ca = _counts(theta)
     _check("poetx_adam_update_many", load_library().poetx_adam_update_many(
-        len(theta), _ptrs(theta), _ptrs(grads), _ptrs(m), _ptrs(v), _counts(theta), step, lr,
-        beta1, beta2, eps, weight_decay, max_norm, _ptr(norm), _ptr(workspace),
-        _nbytes(workspace), _stream(stream)))
+        len(c), *[a for _, a in kept], ca, step, lr, beta1, beta2, eps, weight_decay, max_norm,
+        _ptr(norm), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def poetx_set_block_epilogue_fusion(enable: bool) -> bool:

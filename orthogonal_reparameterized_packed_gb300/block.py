@@ -21,7 +21,7 @@ ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT
 
 def _need(t, shape, dtype, name):
     """t is a contiguous CUDA tensor of this shape and type, or a ValueError."""
-    if tuple(t.shape) != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: a contiguous CUDA tensor of shape {shape} and type {dtype} is "
                          f"needed, got {tuple(t.shape)}, {t.dtype}")
 
@@ -127,13 +127,13 @@ class PoetxQKNormRope:
 
     def _ld(self, x, heads, t, name):
         """The row stride of one q / k tensor."""
-        if x.dtype is not self.dtype or not x.is_cuda or x.shape[0] != t or \
-                x[:1].numel() != min(t, 1) * heads * self.D or x.stride(-1) != 1 or \
-                (x.dim() == 3 and x.stride(1) != self.D):
-            raise ValueError(f"{name}: rows of {heads * self.D} contiguous {self.dtype} elements "
-                             f"for {t} tokens are needed, got {tuple(x.shape)}, {x.dtype}, "
-                             f"strides {x.stride()}")
-        return x.stride(0)
+        st = x.stride()
+        if x.dtype is self.dtype and x.is_cuda and (
+                (x.shape == (t, heads * self.D) and st[1] == 1) or
+                (x.shape == (t, heads, self.D) and st[2] == 1 and st[1] == self.D)):
+            return st[0]
+        raise ValueError(f"{name}: rows of {heads * self.D} contiguous {self.dtype} elements for "
+                         f"{t} tokens are needed, got {tuple(x.shape)}, {x.dtype}, strides {st}")
 
     def _check(self, gamma_q, gamma_k, cos, sin, positions, t):
         if t > self.tokens:
@@ -182,43 +182,45 @@ class PoetxQKNormRope:
 
 
 def _need_list(tensors, others, dtypes, name):
-    for t in tensors:
-        if t.dtype not in dtypes or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"{name}: contiguous CUDA tensors of {dtypes} are needed, got "
-                             f"{tuple(t.shape)}, {t.dtype}")
-    if others is not None and [(t.numel(), t.dtype) for t in tensors] != \
-            [(t.numel(), t.dtype) for t in others]:
-        raise ValueError(f"{name}: the lists differ in sizes or types")
+    """Contiguous CUDA tensors of the types; `others` (or None) of the same sizes and types."""
+    if not ({t.dtype for t in tensors} <= dtypes and
+            all(map(torch.Tensor.is_contiguous, tensors)) and all(t.is_cuda for t in tensors)):
+        raise ValueError(f"{name}: contiguous CUDA tensors of {sorted(map(str, dtypes))} are needed")
+    if others is not None:
+        _need_list(others, None, dtypes, "out")
+        if [(t.numel(), t.dtype) for t in tensors] != [(t.numel(), t.dtype) for t in others]:
+            raise ValueError(f"{name}: the lists differ in sizes or types")
 
 
 class PoetxGradClip:
     """The global norm of a list of gradients (contiguous float32 or bfloat16
     tensors), and the clip to a largest norm.  self.norm is the norm of the
-    last call (a 0-dim float32 tensor, overwritten by the next)."""
+    last call (a 0-dim float32 tensor, overwritten by the next; undefined before the first)."""
 
-    _TYPES = (torch.float32, torch.bfloat16)
+    _TYPES = {torch.float32, torch.bfloat16}
 
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
-        self.norm = torch.zeros((), dtype=torch.float32, device=self.device)
-        self.workspace = torch.empty((0,), dtype=torch.uint8, device=self.device)
+        self.norm = torch.empty((), dtype=torch.float32, device=self.device)
+        self._spaces = []
 
     def _room(self, n):
+        """A workspace for n tensors.  Smaller ones are kept: a call on another
+        stream may still be using them."""
         need = poetx_grad_norm_workspace_size(n)
-        if self.workspace.numel() < need:
-            self.workspace = torch.empty((need,), dtype=torch.uint8, device=self.device)
+        if not self._spaces or self._spaces[-1].numel() < need:
+            self._spaces.append(torch.empty((need,), dtype=torch.uint8, device=self.device))
+        return self._spaces[-1]
 
     def total(self, grads, stream=None):
         """norm = sqrt(sum of squares over all tensors)."""
         _need_list(grads, None, self._TYPES, "grads")
-        self._room(len(grads))
-        poetx_grad_norm(grads, self.norm, self.workspace, stream)
+        poetx_grad_norm(grads, self.norm, self._room(len(grads)), stream)
         return self.norm
 
     def clip(self, grads, max_norm, out=None, stream=None):
         """out (None: the gradients themselves) = grads * min(1, max_norm /
         (norm + 1e-6)); returns the norm before the clip."""
         _need_list(grads, out, self._TYPES, "grads")
-        self._room(len(grads))
-        poetx_clip_grads(grads, out, max_norm, self.norm, self.workspace, stream)
+        poetx_clip_grads(grads, out, max_norm, self.norm, self._room(len(grads)), stream)
         return self.norm

@@ -27,4 +27,7 @@ struct LinearProduct {
 // On CTA pairs, 256 x 256 tiles (linear_pair.cu).
 cudaError_t linear_pair(const LinearProduct& g, cudaStream_t s);
 
+// For few tokens: the weight streamed once, K split over a cluster (linear_stream.cu).
+cudaError_t linear_stream(const LinearProduct& g, cudaStream_t s);
+
 }  // namespace poetx

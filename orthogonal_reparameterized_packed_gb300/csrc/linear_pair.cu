@@ -1,13 +1,17 @@
 // The matrix products of poetx_linear_* for many tokens, bf16, on CTA pairs:
 //   C[M][N] = act(A B^T + bias) + residual   (A [M][K]; B [N][K] or, MN-major, [K][N])
-// Each cluster of two CTAs computes 256 x 256 tiles with
-// tcgen05.mma.cta_group::2 over 64-wide K steps (a six-stage TMA ring of
-// 32 KiB per CTA); two TMEM accumulators let a tile's epilogue run under the
+// Each cluster of two CTAs computes 256 x 256 (or 256 x 128) tiles with
+// tcgen05.mma.cta_group::2 over 64-wide K steps (a TMA ring of six 32 KiB or
+// eight 24 KiB stages per CTA); two TMEM accumulators let a tile's epilogue run under the
 // next tile's main loop.
 //
 // Roles, per CTA (320 threads):
-//   warp 0      TMA producer (one lane)
-//   warp 1      TMEM allocation; in the leader CTA one lane issues the MMAs
+//   warp 0      TMA producer
+//   warp 1      TMEM allocation; in the leader CTA the MMAs
+//               (in both the whole warp runs the loop and one elected lane
+//               issues, which keeps addresses and descriptors in uniform
+//               registers: with the loop inside `lane == 0` a K step took 570
+//               cycles of issue, more than the 512 its MMAs take)
 //   warps 2..9  epilogue: two warps per 32-row quarter of the accumulator,
 //               128 columns each, in chunks of 64: bias, (z,) activation and
 //               residual in fp32 on the accumulator's values, one rounding,
@@ -40,18 +44,23 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kBN = 256;
-constexpr int kA = BM * BK * 2;          // this CTA's 128 rows, one K step
-constexpr int kB = (kBN / 2) * BK * 2;   // this CTA's half of B, one K step
-constexpr int kStage = kA + kB;
-constexpr int kStages = 6;
-constexpr int kRing = kStages * kStage;
-constexpr int kSlot = 32 * 128;          // 32 rows x 64 bf16
+constexpr int kA = BM * BK * 2;      // this CTA's 128 rows, one K step
+constexpr int kSlot = 32 * 128;      // 32 rows x 64 bf16
 constexpr int kStaging = kEpiWarps * kSlot;
 constexpr int kBiasBytes = kEpiWarps * 64 * 4;
-constexpr int kSmem = kRing + kStaging + kBiasBytes + 256;
-static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-constexpr uint32_t kTmemCols = 2 * kBN;
+
+template <int BN>
+struct Shape {
+  static constexpr int B = (BN / 2) * BK * 2;  // this CTA's half of B, one K step
+  static constexpr int STAGE = kA + B;
+  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int SMEM = RING + kStaging + kBiasBytes + 256;
+  static constexpr uint32_t TMEM_COLS = 2 * BN;
+  static constexpr int PER_SIDE = BN / 128;  // 64-column chunks of one epilogue warp
+  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+
 constexpr int kGroupM = 8;
 
 struct PairArgs {
@@ -89,22 +98,6 @@ __device__ __forceinline__ void apply_act(int act, float (&v)[16]) {
   }
 }
 
-// 16 consecutive accumulator columns of this thread's lane.
-__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-  tmem_load_wait();
-#pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-}
-
 // 16 values of this thread's row -> 16-byte pieces 2 part, 2 part + 1 of its staging row
 __device__ __forceinline__ void stage_part(uint8_t* row, int lane, int part, const float (&v)[16]) {
 #pragma unroll
@@ -121,19 +114,21 @@ __device__ __forceinline__ bf16* staged(uint8_t* slot, int row, int col) {
   return reinterpret_cast<bf16*>(slot + row * 128 + (((col >> 3) ^ (row & 7)) << 4)) + (col & 7);
 }
 
-template <bool B_MN>
+template <int BN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmY,
                        const __grid_constant__ CUtensorMap tmZ,
                        const __grid_constant__ CUtensorMap tmR, const PairArgs p) {
+  using S = Shape<BN>;
+  constexpr int kStages = S::STAGES, kStage = S::STAGE, kRing = S::RING, kBN = BN;
   extern __shared__ __align__(1024) uint8_t base[];  // 128B-swizzled tiles start on 1024 bytes
   if ((smem_u32(base) & 1023u) != 0) {  // the declared alignment, which the tiles rely on
     if (threadIdx.x == 0) atomicCAS(p.status, 0, static_cast<int>(POETX_ERR_CUDA));
     return;
   }
-  uint8_t* ring = base;  // stage s: A (16 KiB), then B half (16 KiB)
+  uint8_t* ring = base;  // stage s: A (16 KiB), then this CTA's half of B
   uint8_t* staging = base + kRing;
   float* bias_s = reinterpret_cast<float*>(staging + kStaging);
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(staging + kStaging + kBiasBytes);  // leader
@@ -172,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -187,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tempty0 = map_peer(smem_u32(tempty_bar), 0);
 
   if (warp == 0) {
-    if (lane == 0) {
+    {
       // ---------------------------------------------------------- producer
       int stage = 0;
       uint32_t phase = 0;
@@ -199,22 +194,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int a_row = mp * 2 * BM + static_cast<int>(rank) * BM;
         const int b_n = nt * kBN + static_cast<int>(rank) * (kBN / 2);
         for (int ks = 0; ks < p.k_steps; ++ks) {
-          if (!mbar_wait_cluster(&empty_bar[stage], phase ^ 1, abort_flag)) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) {
             record_timeout(p.status, abort_flag);
             ok = false;
             break;
           }
-          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStage);
-          uint8_t* a_dst = ring + stage * kStage;
-          uint8_t* b_dst = a_dst + kA;
-          const uint32_t bar = full0 + static_cast<uint32_t>(stage * 8);
-          tma_load_2d_pair(a_dst, &tmA, bar, ks * BK, a_row);
-          if (!B_MN) {
-            tma_load_2d_pair(b_dst, &tmB, bar, ks * BK, b_n);
-          } else {
-            tma_load_2d_pair(b_dst, &tmB, bar, b_n, ks * BK);
-            tma_load_2d_pair(b_dst + 8192, &tmB, bar, b_n + 64, ks * BK);
+          if (elect_one()) {
+            if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStage);
+            uint8_t* a_dst = ring + stage * kStage;
+            uint8_t* b_dst = a_dst + kA;
+            const uint32_t bar = full0 + static_cast<uint32_t>(stage * 8);
+            tma_load_2d_pair(a_dst, &tmA, bar, ks * BK, a_row);
+            if (!B_MN) {
+              tma_load_2d_pair(b_dst, &tmB, bar, ks * BK, b_n);
+            } else {
+              tma_load_2d_pair(b_dst, &tmB, bar, b_n, ks * BK);
+              if (BN == 256) tma_load_2d_pair(b_dst + 8192, &tmB, bar, b_n + 64, ks * BK);
+            }
           }
+          __syncwarp();
           ++issued;
           if (++stage == kStages) {
             stage = 0;
@@ -238,13 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // -------------------------------------------------- MMA issuer (pair)
       constexpr uint32_t IDESC = instr_desc_bf16(2 * BM, kBN, false, B_MN);
       const uint32_t empty_own = smem_u32(empty_bar);
-      const uint32_t empty_peer = map_peer(empty_own, 1);
       const uint32_t tfull_own = smem_u32(tfull_bar);
-      const uint32_t tfull_peer = map_peer(tfull_own, 1);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -260,39 +256,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kBN);
         for (int ks = 0; ks < p.k_steps; ++ks) {
-          if (!mbar_wait_cluster(&full_bar[stage], phase, abort_flag)) {
+          if (!mbar_wait(&full_bar[stage], phase, abort_flag)) {
             record_timeout(p.status, abort_flag);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_base = smem_u32(ring + stage * kStage);
+          const uint32_t a_base = smem_u32(ring) + stage * kStage;
           const uint32_t b_base = a_base + kA;
+          // 16 of K: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
+          const uint64_t adesc0 = smem_desc_sw128(a_base, 16, 1024);
+          const uint64_t bdesc0 = smem_desc_sw128(b_base, B_MN ? 8192 : 16, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < BK / 16; ++j) {
-            const uint64_t adesc = smem_desc_sw128(a_base + j * 32, 16, 1024);
-            const uint64_t bdesc = B_MN ? smem_desc_sw128(b_base + j * 2048, 8192, 1024)
-                                        : smem_desc_sw128(b_base + j * 32, 16, 1024);
-            umma_bf16_pair(d_tmem, adesc, bdesc, IDESC, (ks > 0 || j > 0) ? 1u : 0u);
+            for (int j = 0; j < BK / 16; ++j)
+              umma_bf16_pair(d_tmem, adesc0 + j * 2, bdesc0 + j * (B_MN ? 128 : 2), IDESC,
+                             (ks > 0 || j > 0) ? 1u : 0u);
+            // the slot is free in both CTAs once the MMAs have read it
+            umma_commit_both(empty_own + static_cast<uint32_t>(stage * 8));
           }
+          __syncwarp();
           any_mma = true;
-          // the slot is free in both CTAs once the MMAs have read it
-          umma_commit_pair(empty_own + static_cast<uint32_t>(stage * 8));
-          umma_commit_pair(empty_peer + static_cast<uint32_t>(stage * 8));
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        umma_commit_pair(tfull_own + static_cast<uint32_t>(acc * 8));
-        umma_commit_pair(tfull_peer + static_cast<uint32_t>(acc * 8));
+        if (elect_one()) umma_commit_both(tfull_own + static_cast<uint32_t>(acc * 8));
+        __syncwarp();
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }
       if (!ok && any_mma) {
         // the MMAs in flight finish before TMEM is released
-        umma_commit_pair(smem_u32(drain_bar));
+        if (elect_one()) umma_commit_pair(smem_u32(drain_bar));
+        __syncwarp();
         const unsigned long long t0 = global_timer_ns();
         while (!mbar_try_wait(drain_bar, 0) && global_timer_ns() - t0 < 10000000ull) {
         }
@@ -350,7 +349,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // 16 columns of z: the accumulator plus the chunk's bias
     auto load_z = [&](float (&v)[16], uint32_t taddr, int part) {
-      tmem_load_16cols(taddr + part * 16, v);
+      uint32_t r[16];
+      tmem_load_16(taddr + part * 16, r);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
       if (p.bias != nullptr) {
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int mp, nt;
       unit_tile(u, p, mp, nt);
       const long long row0 = static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32;
-      const int tile_col = nt * kBN + side * 128;
+      const int tile_col = nt * kBN + side * S::PER_SIDE * 64;
       const bool live = row0 < p.M;  // the same for the whole warp
       if (p.residual != nullptr && live && tile_col < p.N) {
         staging_free();
@@ -381,13 +383,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const uint32_t t_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                              static_cast<uint32_t>(acc * kBN + side * 128);
+                              static_cast<uint32_t>(acc * kBN + side * S::PER_SIDE * 64);
       bool timed_out = false;
 #pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < S::PER_SIDE; ++c) {
         const int col = tile_col + c * 64;
         if (!live || col >= p.N) break;
-        if (c == 1 && p.residual != nullptr) {
+        if (c > 0 && p.residual != nullptr) {
           staging_free();
           fetch_residual(row0, col);
         }
@@ -479,13 +481,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, kTmemCols);
+    tmem_dealloc_pair(tmem_base, S::TMEM_COLS);
   }
 }
 
-template <bool B_MN>
+template <int BN, bool B_MN>
 cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
-  auto* kernel = linear_pair_kernel<B_MN>;
+  using S = Shape<BN>;
+  constexpr int kSmem = S::SMEM, kBN = BN;
+  auto* kernel = linear_pair_kernel<BN, B_MN>;
   static bool ready[64] = {false};
   static int max_clusters[64] = {0};
   static std::mutex mu;
@@ -563,7 +567,17 @@ cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
 
 cudaError_t linear_pair(const LinearProduct& g, cudaStream_t s) {
   if (g.M <= 0 || g.N <= 0 || g.K <= 0) return cudaSuccess;
-  return g.b_mn ? launch<true>(g, s) : launch<false>(g, s);
+  // 128-wide tiles, where they fill idle clusters: a 64-wide K step of one takes
+  // 0.19 us (24 KiB of operands per CTA, bound by their loads), of a 256-wide
+  // tile 0.28 us (bound by the MMAs), so they win while the rounds of tiles over
+  // the clusters are fewer than 3/2 of the wide tiles'.  4096 -> 4096 features:
+  // T = 512 (32 wide tiles) 17.4 against 23.2 us, T = 1024 (64) 29.4 against 24.4.
+  const long long m_pairs = (g.M + 2 * BM - 1) / (2 * BM);
+  const long long clusters = std::max(1, sm_count() / 2);
+  const long long wide = (m_pairs * ((g.N + 255) / 256) + clusters - 1) / clusters;
+  const long long narrow = (m_pairs * ((g.N + 127) / 128) + clusters - 1) / clusters;
+  if (2 * narrow < 3 * wide) return g.b_mn ? launch<128, true>(g, s) : launch<128, false>(g, s);
+  return g.b_mn ? launch<256, true>(g, s) : launch<256, false>(g, s);
 }
 
 }  // namespace poetx

@@ -183,28 +183,29 @@ class PoetxAdam:
     def step(self, grads, stream=None, max_norm=None):
         if max_norm is not None and not max_norm >= 0:
             raise ValueError(f"max_norm must be at least 0, got {max_norm}")
-        todo = list(zip(self.params, grads, self.m, self.v))
-        for p, g, _, _ in todo:
-            if isinstance(g, torch.Tensor) and (g.numel() < p.numel() or
-                                                g.dtype is not torch.float32 or
-                                                not g.is_contiguous()):
-                raise ValueError(f"a contiguous float32 gradient of {p.numel()} elements is "
-                                 f"needed, got {tuple(g.shape)}, {g.dtype}")
-        self.t += 1
         if max_norm is None:
-            for p, g, m, v in todo:
+            self.t += 1
+            for p, g, m, v in zip(self.params, grads, self.m, self.v):
                 poetx_adam_update(p, g, m, v, p.numel(), self.t, self.lr, self.betas[0],
                                   self.betas[1], self.eps, self.weight_decay, stream)
             return
+        grads = list(grads)
+        sizes = list(map(torch.Tensor.numel, self.params))
+        if list(map(torch.Tensor.numel, grads)) != sizes or \
+                {g.dtype for g in grads} - {torch.float32} or \
+                not all(map(torch.Tensor.is_contiguous, grads)):
+            raise ValueError("contiguous float32 gradients of the parameters' sizes are needed")
+        self.t += 1
+        if not grads:
+            return
         if self.norm is None:
             dev = self.params[0].device
-            self.norm = torch.zeros((), dtype=torch.float32, device=dev)
+            self.norm = torch.empty((), dtype=torch.float32, device=dev)
             self._workspace = torch.empty((poetx_grad_norm_workspace_size(len(self.params)),),
                                           dtype=torch.uint8, device=dev)
-        poetx_adam_update_many([p for p, _, _, _ in todo], [g for _, g, _, _ in todo],
-                               [m for _, _, m, _ in todo], [v for _, _, _, v in todo], self.t,
-                               self.lr, self.betas[0], self.betas[1], self.eps,
-                               self.weight_decay, max_norm, self.norm, self._workspace, stream)
+        poetx_adam_update_many(self.params, grads, self.m, self.v, self.t, self.lr,
+                               self.betas[0], self.betas[1], self.eps, self.weight_decay,
+                               max_norm, self.norm, self._workspace, stream)
 
 
 def to_device(inp, device="cuda"):

@@ -226,10 +226,9 @@ def test_lists_are_checked(px):
     with pytest.raises(px.PoetxError):
         clip.clip([a], float("nan"))
     opt = PoetxAdam([a], lr=1e-3)
-    with pytest.raises(ValueError):
-        opt.step([a.bfloat16()])
-    with pytest.raises(ValueError):
-        opt.step([a[:4]])
+    for grads in ([a.bfloat16()], [a[:4]], [a, a], [torch.ones(16, device="cuda")[::2]]):
+        with pytest.raises(ValueError):
+            opt.step(grads, max_norm=1.0)
     with pytest.raises(ValueError):
         opt.step([a], max_norm=-2.0)
     assert opt.t == 0 and torch.all(a == 1)
