@@ -14,6 +14,22 @@ __device__ __forceinline__ float sigmoid_f(float z) {
   return FAST ? __fdividef(1.f, 1.f + __expf(-z)) : 1.f / (1.f + expf(-z));
 }
 
+// Phi(z), the standard normal distribution, with `e` = exp(-z^2 / 2).  FAST:
+// erfc by the rational approximation 7.1.26 of Abramowitz and Stegun, Handbook
+// of Mathematical Functions, whose error is at most 1.5e-7 (erfcf's branches
+// made the epilogue of a 2048 x 5632 x 2048 product take 47 us instead of 34).
+template <bool FAST>
+__device__ __forceinline__ float normal_cdf(float z, float e) {
+  if (!FAST) return 0.5f * erfcf(-0.7071067811865476f * z);
+  const float t = __fdividef(1.f, fmaf(0.3275911f * 0.7071067811865476f, fabsf(z), 1.f));
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  q *= 0.5f * t * e;
+  return z > 0.f ? 1.f - q : q;
+}
+
 // u of gelu_tanh: tanh(u) = 2 sigmoid(2u) - 1
 __device__ __forceinline__ float gelu_u(float z) {
   return 0.7978845608028654f * fmaf(0.044715f * z * z, z, z);
@@ -23,7 +39,7 @@ template <int ACT, bool FAST>
 __device__ __forceinline__ float act_f(float z) {
   if (ACT == POETX_ACT_RELU) return z <= 0.f ? 0.f : z;  // NaN stays NaN
   if (ACT == POETX_ACT_SILU) return z * sigmoid_f<FAST>(z);
-  if (ACT == POETX_ACT_GELU) return 0.5f * z * erfcf(-0.7071067811865476f * z);
+  if (ACT == POETX_ACT_GELU) return z * normal_cdf<FAST>(z, FAST ? __expf(-0.5f * z * z) : 0.f);
   if (ACT == POETX_ACT_GELU_TANH) return z * sigmoid_f<FAST>(2.f * gelu_u(z));
   return z;
 }
@@ -37,9 +53,8 @@ __device__ __forceinline__ float act_df(float z) {
     return s * (1.f + z * (1.f - s));
   }
   if (ACT == POETX_ACT_GELU) {
-    const float e = -0.5f * z * z;
-    return fmaf(z * 0.3989422804014327f, FAST ? __expf(e) : expf(e),
-                0.5f * erfcf(-0.7071067811865476f * z));
+    const float e = FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z);
+    return fmaf(z * 0.3989422804014327f, e, normal_cdf<FAST>(z, e));
   }
   if (ACT == POETX_ACT_GELU_TANH) {
     const float s = sigmoid_f<FAST>(2.f * gelu_u(z));
