@@ -14,6 +14,13 @@
 // needs the norm adds the partials itself, in every CTA and in the same order
 // (no atomics, no counter to reset, the same bits in every CTA), so a clip
 // is two launches.  All of it is bound by memory traffic.
+//
+// Squares are added in fp32, at most kChunk / kThreads + 2 at a time; those
+// sums, and everything after them, as pairs of fp32 (hi + lo, two-sum), about
+// 2^-45 of the total.  (In fp64, which this GPU runs at 1/64 of the rate, the
+// closing sums alone took several microseconds per launch.)  Where a sum of
+// squares is too large or too small for that it is taken again in fp64 and
+// kept apart, so that every finite gradient has a finite and accurate norm.
 #include <algorithm>
 #include <cstdint>
 
@@ -27,32 +34,46 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 8192;       // elements: 8 16-byte loads in flight per thread (fp32)
 constexpr int kMaxTensors = 512;   // per launch: the table is at most 24 KB of parameters
-constexpr int kMaxCtas = 1024;     // partial sums per launch
+constexpr int kFewTensors = 32;
+constexpr int kPerSm = 8;          // CTAs: every warp an SM can hold
+constexpr int kMaxCtas = 2048;     // partial sums per launch
 constexpr float kClipEps = 1e-6f;  // guards the division when the norm is 0
 
+// CAP tensors of one launch.  The parameters of a launch cost time by their
+// size, so short lists take a small table.
+template <int CAP>
 struct TensorTable {
   int n;
   unsigned chunks;
-  const void* grad[kMaxTensors];
-  long long count[kMaxTensors];
-  unsigned first[kMaxTensors];  // the tensor's first chunk
-  unsigned char bf16[kMaxTensors];
+  const void* grad[CAP];
+  long long count[CAP];
+  unsigned first[CAP];  // the tensor's first chunk
+  unsigned char bf16[CAP];
 };
 
+template <int CAP>
 struct ClipTable {
-  TensorTable t;
-  void* out[kMaxTensors];
+  TensorTable<CAP> t;
+  void* out[CAP];
 };
 
+template <int CAP>
 struct AdamTable {
-  TensorTable t;
-  float* theta[kMaxTensors];
-  float* m[kMaxTensors];
-  float* v[kMaxTensors];
+  TensorTable<CAP> t;
+  float* theta[CAP];
+  float* m[CAP];
+  float* v[CAP];
+};
+
+// A sum of squares: hi + lo, and what had to be added in fp64.
+struct Sum {
+  float hi, lo;
+  double wide;
 };
 
 // The last tensor whose first chunk is <= c (empty tensors own no chunk).
-__device__ __forceinline__ int find_tensor(const TensorTable& t, unsigned c) {
+template <int CAP>
+__device__ __forceinline__ int find_tensor(const TensorTable<CAP>& t, unsigned c) {
   int lo = 0, hi = t.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -82,13 +103,16 @@ __device__ __forceinline__ int head_elements(const T* p, int n) {
   return off == 0 ? 0 : min(n, static_cast<int>((16 - off) / sizeof(T)));
 }
 
-// Sum of squares of this thread's share of p[0..n).  The squares are added in
-// fp32 (at most kChunk / kThreads + 2 of them, so the sum keeps about 2^-22
-// of its value); sums that overflowed fp32, or are so small that squares may
-// have been lost below its range, are taken again in 64 bits, so every finite
-// gradient has a finite and accurate norm.
+// hi + lo += x, the rounding error of hi + x kept in lo (two-sum).
+__device__ __forceinline__ void add_to(float& hi, float& lo, float x) {
+  const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+  hi = s;
+}
+
+// acc += the sum of squares of this thread's share of p[0..n).
 template <typename T>
-__device__ __forceinline__ double chunk_sumsq(const T* p, int n) {
+__device__ __forceinline__ void chunk_sumsq(const T* p, int n, Sum& acc) {
   const int head = head_elements(p, n);
   const int nv = (n - head) / Vec<T>::N;
   const int tail = head + nv * Vec<T>::N;
@@ -109,67 +133,98 @@ __device__ __forceinline__ double chunk_sumsq(const T* p, int n) {
   const int i0 = threadIdx.x;  // at most 7 elements on either side
   if (i0 < head) add(p[i0]);
   if (tail + i0 < n) add(p[tail + i0]);
-  if (s >= 1e-24f && s <= 3e38f) return static_cast<double>(s);
-  if ((any & 0x7fffffffu) == 0) return 0.0;
+  // 2^42 elements are 2^29 chunks: sums of up to 1e28 each stay inside fp32, and
+  // squares that fp32 loses (below 1e-38) are nothing beside 1e-24
+  if (s >= 1e-24f && s <= 1e28f) {
+    add_to(acc.hi, acc.lo, s);
+    return;
+  }
+  if ((any & 0x7fffffffu) == 0) return;
   double d = 0.0;
+  auto add_wide = [&](T x) {
+    const double f = static_cast<double>(to_f(x));
+    d += f * f;
+  };
   for (int i = threadIdx.x; i < nv; i += kThreads)
-    for (int j = 0; j < Vec<T>::N; ++j) {
-      const double f = static_cast<double>(to_f(p[head + i * Vec<T>::N + j]));
-      d += f * f;
-    }
-  if (i0 < head) d += static_cast<double>(to_f(p[i0])) * static_cast<double>(to_f(p[i0]));
-  if (tail + i0 < n)
-    d += static_cast<double>(to_f(p[tail + i0])) * static_cast<double>(to_f(p[tail + i0]));
-  return d;
+    for (int j = 0; j < Vec<T>::N; ++j) add_wide(p[head + i * Vec<T>::N + j]);
+  if (i0 < head) add_wide(p[i0]);
+  if (tail + i0 < n) add_wide(p[tail + i0]);
+  acc.wide += d;
 }
 
-// Sum over the CTA, the same value in every thread, in a fixed order.
-__device__ __forceinline__ double block_sum(double v) {
-  __shared__ double warp_sum[kThreads / 32];
+// The CTA's total, the same bits in every thread (it goes by the warps' first
+// lanes), in a fixed order.
+__device__ __forceinline__ Sum block_sum(Sum v) {
+  __shared__ Sum warp_sum[kThreads / 32];
+  const bool wide = __syncthreads_or(v.wide != 0.0);  // NaN counts
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    const float hi = __shfl_xor_sync(0xffffffffu, v.hi, o);
+    const float lo = __shfl_xor_sync(0xffffffffu, v.lo, o);
+    add_to(v.hi, v.lo, hi);
+    v.lo = __fadd_rn(v.lo, lo);
+    if (wide) v.wide += __shfl_xor_sync(0xffffffffu, v.wide, o);
+  }
   if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = v;
   __syncthreads();
   v = warp_sum[0];
 #pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) v += warp_sum[w];
+  for (int w = 1; w < kThreads / 32; ++w) {
+    add_to(v.hi, v.lo, warp_sum[w].hi);
+    v.lo = __fadd_rn(v.lo, warp_sum[w].lo);
+    if (wide) v.wide += warp_sum[w].wide;
+  }
   return v;
 }
 
+template <int CAP>
 __global__ void __launch_bounds__(kThreads)
-    sumsq_kernel(const __grid_constant__ TensorTable t, double* part) {
+    sumsq_kernel(const __grid_constant__ TensorTable<CAP> t, Sum* part) {
   pdl_wait();
   pdl_trigger();
-  double acc = 0.0;
+  Sum acc = {0.f, 0.f, 0.0};
   for (unsigned c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const int i = find_tensor(t, c);
     const long long at = static_cast<long long>(c - t.first[i]) * kChunk;
     const int n = static_cast<int>(min(static_cast<long long>(kChunk), t.count[i] - at));
-    acc += t.bf16[i] ? chunk_sumsq(static_cast<const __nv_bfloat16*>(t.grad[i]) + at, n)
-                     : chunk_sumsq(static_cast<const float*>(t.grad[i]) + at, n);
+    if (t.bf16[i])
+      chunk_sumsq(static_cast<const __nv_bfloat16*>(t.grad[i]) + at, n, acc);
+    else
+      chunk_sumsq(static_cast<const float*>(t.grad[i]) + at, n, acc);
   }
   acc = block_sum(acc);
   if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }
 
-// The norm from the partial sums, the same bits in every CTA.
-__device__ __forceinline__ double norm_of(const double* part, int parts) {
-  double v = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kThreads) v += part[i];
-  return sqrt(block_sum(v));
+// The norm from the partial sums and min(1, max_norm / (norm + eps)), the same
+// bits in every thread of every CTA.  The scale is NaN where the norm is (or
+// where both are infinite).
+__device__ __forceinline__ float2 norm_and_scale(const Sum* part, int parts, float max_norm) {
+  Sum v = {0.f, 0.f, 0.0};
+  for (int i = threadIdx.x; i < parts; i += kThreads) {
+    const Sum p = part[i];
+    add_to(v.hi, v.lo, p.hi);
+    v.lo = __fadd_rn(v.lo, p.lo);
+    if (p.wide != 0.0) v.wide += p.wide;
+  }
+  v = block_sum(v);
+  float norm, scale;
+  if (v.wide != 0.0) {
+    const double d = sqrt(v.wide + static_cast<double>(v.hi) + static_cast<double>(v.lo));
+    norm = static_cast<float>(d);
+    scale = static_cast<float>(static_cast<double>(max_norm) / (d + static_cast<double>(kClipEps)));
+  } else {
+    norm = sqrtf(v.hi + v.lo);
+    scale = max_norm / (norm + kClipEps);
+  }
+  return make_float2(norm, scale > 1.f ? 1.f : scale);
 }
 
-// min(1, max_norm / (norm + eps)); NaN where the norm is NaN (or inf over inf).
-__device__ __forceinline__ float clip_scale(double norm, float max_norm) {
-  const double s = static_cast<double>(max_norm) / (norm + static_cast<double>(kClipEps));
-  return s > 1.0 ? 1.f : static_cast<float>(s);
-}
-
-__global__ void __launch_bounds__(kThreads) norm_kernel(const double* part, int parts, float* norm) {
+__global__ void __launch_bounds__(kThreads) norm_kernel(const Sum* part, int parts, float* norm) {
   pdl_wait();
   pdl_trigger();
-  const double v = norm_of(part, parts);
-  if (threadIdx.x == 0) *norm = static_cast<float>(v);
+  const float2 v = norm_and_scale(part, parts, 0.f);
+  if (threadIdx.x == 0) *norm = v.x;
 }
 
 template <typename T>
@@ -199,15 +254,16 @@ __device__ __forceinline__ void scale_chunk(const T* p, T* o, int n, float scale
 
 // Chunks in descending order: the ones that pass one read last are still in
 // the 129 MB L2 and are read from there before they are evicted.
+template <int CAP>
 __global__ void __launch_bounds__(kThreads)
-    clip_kernel(const __grid_constant__ ClipTable a, const double* part, int parts, float max_norm,
-                float* norm) {
+    clip_kernel(const __grid_constant__ ClipTable<CAP> a, const Sum* part, int parts,
+                float max_norm, float* norm) {
   pdl_wait();
   pdl_trigger();
-  const double nv = norm_of(part, parts);
-  const float scale = clip_scale(nv, max_norm);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(nv);
-  const TensorTable& t = a.t;
+  const float2 ns = norm_and_scale(part, parts, max_norm);
+  const float scale = ns.y;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = ns.x;
+  const TensorTable<CAP>& t = a.t;
   for (unsigned c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const unsigned r = t.chunks - 1 - c;
     const int i = find_tensor(t, r);
@@ -234,19 +290,23 @@ __device__ __forceinline__ void adam_one(float& th, float g, float& m, float& v,
   th = fmaf(-h.lr, fmaf(h.wd, th, step), th);
 }
 
-// parts = 0: no clip.
+// parts = 0: no clip.  One vector of each array in flight per thread and 64 warps
+// per SM: 336 vectors of 261,120 take 375 us, 6.55 TB/s of their 28 bytes per
+// parameter (two in flight at 48 warps 429, four at 32 warps 371 but the passes
+// over the gradients alone then lose more).
+template <int CAP>
 __global__ void __launch_bounds__(kThreads)
-    adam_many_kernel(const __grid_constant__ AdamTable a, const AdamHyper h, const double* part,
+    adam_many_kernel(const __grid_constant__ AdamTable<CAP> a, const AdamHyper h, const Sum* part,
                      int parts, float max_norm, float* norm) {
   pdl_wait();
   pdl_trigger();
   float scale = 1.f;
   if (parts > 0) {
-    const double nv = norm_of(part, parts);
-    scale = clip_scale(nv, max_norm);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(nv);
+    const float2 ns = norm_and_scale(part, parts, max_norm);
+    scale = ns.y;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = ns.x;
   }
-  const TensorTable& t = a.t;
+  const TensorTable<CAP>& t = a.t;
   for (unsigned c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const unsigned r = t.chunks - 1 - c;  // as in clip_kernel
     const int i = find_tensor(t, r);
@@ -263,7 +323,6 @@ __global__ void __launch_bounds__(kThreads)
                              15u) == 0;
     const int head = same_phase ? head_elements(g, n) : n;
     const int n4 = (n - head) / 4;
-#pragma unroll 2
     for (int j = threadIdx.x; j < n4; j += kThreads) {
       const float4 gj = reinterpret_cast<const float4*>(g + head)[j];
       float4 tj = reinterpret_cast<float4*>(th + head)[j];
@@ -283,14 +342,15 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Fills the table from tensors [at, at + kMaxTensors) of the list, empty ones
-// left out (`index` gives their places); returns where the next launch begins.
-// The caller has checked that all counts add up to at most 2^42 (2^29 chunks).
-int fill_table(TensorTable& t, int* index, int at, int n, const void* const* grads,
+// Fills the table from the list's tensors from `at` on, empty ones left out
+// (`index` gives their places); returns where the next launch begins.  The
+// caller has checked that all counts add up to at most 2^42 (2^29 chunks).
+template <int CAP>
+int fill_table(TensorTable<CAP>& t, int* index, int at, int n, const void* const* grads,
                const int64_t* counts, const int* dtypes) {
   t.n = 0;
   unsigned long long chunks = 0;
-  for (; at < n && t.n < kMaxTensors; ++at) {
+  for (; at < n && t.n < CAP; ++at) {
     if (counts[at] == 0) continue;
     t.grad[t.n] = grads[at];
     t.count[t.n] = counts[at];
@@ -303,26 +363,87 @@ int fill_table(TensorTable& t, int* index, int at, int n, const void* const* gra
   return at;
 }
 
-int grid_for(unsigned chunks, int per_sm) {
-  const int most = std::min(kMaxCtas, per_sm * sm_count());
+int grid_for(unsigned chunks) {
+  const int most = std::min(kMaxCtas, kPerSm * sm_count());
   return static_cast<int>(std::min<unsigned>(chunks, static_cast<unsigned>(most)));
 }
 
 // Pass one over the whole list; returns the number of partial sums.
+template <int CAP>
 cudaError_t sumsq_pass(int n, const void* const* grads, const int64_t* counts, const int* dtypes,
-                       double* part, int* parts, cudaStream_t s) {
-  TensorTable t;
-  int index[kMaxTensors];
+                       Sum* part, int* parts, cudaStream_t s) {
+  TensorTable<CAP> t;
+  int index[CAP];
   *parts = 0;
   for (int at = 0; at < n;) {
     at = fill_table(t, index, at, n, grads, counts, dtypes);
     if (t.n == 0) continue;
-    const int grid = grid_for(t.chunks, 6);
+    const int grid = grid_for(t.chunks);
     prof_begin("grad_sumsq", s);
-    cudaError_t e = launch_pdl(sumsq_kernel, dim3(grid), dim3(kThreads), 0, s, t, part + *parts);
+    cudaError_t e =
+        launch_pdl(sumsq_kernel<CAP>, dim3(grid), dim3(kThreads), 0, s, t, part + *parts);
     prof_end("grad_sumsq", s);
     if (e != cudaSuccess) return e;
     *parts += grid;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t norm_pass(const Sum* part, int parts, float* norm, cudaStream_t s) {
+  prof_begin("grad_norm", s);
+  const cudaError_t e = launch_pdl(norm_kernel, dim3(1), dim3(kThreads), 0, s, part, parts, norm);
+  prof_end("grad_norm", s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int CAP>
+cudaError_t clip_pass(int n, const void* const* grads, void* const* outs, const int64_t* counts,
+                      const int* dtypes, float max_norm, float* norm, Sum* part, cudaStream_t s) {
+  int parts = 0;
+  cudaError_t e = sumsq_pass<CAP>(n, grads, counts, dtypes, part, &parts, s);
+  if (e != cudaSuccess) return e;
+  if (parts == 0) return norm_pass(part, 0, norm, s);  // nothing to clip: norm = 0
+  ClipTable<CAP> a;
+  int index[CAP];
+  for (int at = 0; at < n;) {
+    at = fill_table(a.t, index, at, n, grads, counts, dtypes);
+    if (a.t.n == 0) continue;
+    for (int i = 0; i < a.t.n; ++i) a.out[i] = outs[index[i]];
+    prof_begin("grad_clip", s);
+    e = launch_pdl(clip_kernel<CAP>, dim3(grid_for(a.t.chunks)), dim3(kThreads), 0, s, a,
+                   static_cast<const Sum*>(part), parts, max_norm, norm);
+    prof_end("grad_clip", s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <int CAP>
+cudaError_t adam_pass(int n, float* const* theta, const void* const* grads, float* const* m,
+                      float* const* v, const int64_t* counts, const AdamHyper& h, float max_norm,
+                      float* norm, Sum* part, cudaStream_t s) {
+  int parts = 0;
+  cudaError_t e;
+  if (max_norm >= 0.f) {
+    e = sumsq_pass<CAP>(n, grads, counts, nullptr, part, &parts, s);
+    if (e != cudaSuccess) return e;
+    if (parts == 0) return norm_pass(part, 0, norm, s);
+  }
+  AdamTable<CAP> a;
+  int index[CAP];
+  for (int at = 0; at < n;) {
+    at = fill_table(a.t, index, at, n, grads, counts, nullptr);
+    if (a.t.n == 0) continue;
+    for (int i = 0; i < a.t.n; ++i) {
+      a.theta[i] = theta[index[i]];
+      a.m[i] = m[index[i]];
+      a.v[i] = v[index[i]];
+    }
+    prof_begin("adam_many", s);
+    e = launch_pdl(adam_many_kernel<CAP>, dim3(grid_for(a.t.chunks)), dim3(kThreads), 0, s, a, h,
+                   static_cast<const Sum*>(part), parts, max_norm, norm);
+    prof_end("adam_many", s);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
@@ -331,43 +452,26 @@ cudaError_t sumsq_pass(int n, const void* const* grads, const int64_t* counts, c
 
 size_t grad_norm_scratch(int n) {
   const long long launches = (static_cast<long long>(n) + kMaxTensors - 1) / kMaxTensors;
-  return static_cast<size_t>(launches > 0 ? launches : 1) * kMaxCtas * sizeof(double);
+  return static_cast<size_t>(launches > 0 ? launches : 1) * kMaxCtas * sizeof(Sum);
 }
 
 cudaError_t grad_norm(int n, const void* const* grads, const int64_t* counts, const int* dtypes,
                       float* norm, void* scratch, cudaStream_t s) {
-  double* part = static_cast<double*>(scratch);
+  Sum* part = static_cast<Sum*>(scratch);
   int parts = 0;
-  cudaError_t e = sumsq_pass(n, grads, counts, dtypes, part, &parts, s);
-  if (e != cudaSuccess) return e;
-  prof_begin("grad_norm", s);
-  e = launch_pdl(norm_kernel, dim3(1), dim3(kThreads), 0, s, static_cast<const double*>(part),
-                 parts, norm);
-  prof_end("grad_norm", s);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const cudaError_t e =
+      n <= kFewTensors ? sumsq_pass<kFewTensors>(n, grads, counts, dtypes, part, &parts, s)
+                       : sumsq_pass<kMaxTensors>(n, grads, counts, dtypes, part, &parts, s);
+  return e != cudaSuccess ? e : norm_pass(part, parts, norm, s);
 }
 
 cudaError_t clip_grads(int n, const void* const* grads, void* const* outs, const int64_t* counts,
                        const int* dtypes, float max_norm, float* norm, void* scratch,
                        cudaStream_t s) {
-  double* part = static_cast<double*>(scratch);
-  int parts = 0;
-  cudaError_t e = sumsq_pass(n, grads, counts, dtypes, part, &parts, s);
-  if (e != cudaSuccess) return e;
-  if (parts == 0) return grad_norm(0, grads, counts, dtypes, norm, scratch, s);  // norm = 0
-  ClipTable a;
-  int index[kMaxTensors];
-  for (int at = 0; at < n;) {
-    at = fill_table(a.t, index, at, n, grads, counts, dtypes);
-    if (a.t.n == 0) continue;
-    for (int i = 0; i < a.t.n; ++i) a.out[i] = outs[index[i]];
-    prof_begin("grad_clip", s);
-    e = launch_pdl(clip_kernel, dim3(grid_for(a.t.chunks, 6)), dim3(kThreads), 0, s, a,
-                   static_cast<const double*>(part), parts, max_norm, norm);
-    prof_end("grad_clip", s);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  Sum* part = static_cast<Sum*>(scratch);
+  return n <= kFewTensors
+             ? clip_pass<kFewTensors>(n, grads, outs, counts, dtypes, max_norm, norm, part, s)
+             : clip_pass<kMaxTensors>(n, grads, outs, counts, dtypes, max_norm, norm, part, s);
 }
 
 cudaError_t adam_update_many(int n, float* const* theta, const float* const* grads,
@@ -375,31 +479,10 @@ cudaError_t adam_update_many(int n, float* const* theta, const float* const* gra
                              const AdamHyper& h, float max_norm, float* norm, void* scratch,
                              cudaStream_t s) {
   const void* const* gr = reinterpret_cast<const void* const*>(grads);
-  double* part = static_cast<double*>(scratch);
-  int parts = 0;
-  cudaError_t e;
-  if (max_norm >= 0.f) {
-    e = sumsq_pass(n, gr, counts, nullptr, part, &parts, s);
-    if (e != cudaSuccess) return e;
-    if (parts == 0) return grad_norm(0, gr, counts, nullptr, norm, scratch, s);
-  }
-  AdamTable a;
-  int index[kMaxTensors];
-  for (int at = 0; at < n;) {
-    at = fill_table(a.t, index, at, n, gr, counts, nullptr);
-    if (a.t.n == 0) continue;
-    for (int i = 0; i < a.t.n; ++i) {
-      a.theta[i] = theta[index[i]];
-      a.m[i] = m[index[i]];
-      a.v[i] = v[index[i]];
-    }
-    prof_begin("adam_many", s);
-    e = launch_pdl(adam_many_kernel, dim3(grid_for(a.t.chunks, 6)), dim3(kThreads), 0, s, a, h,
-                   static_cast<const double*>(part), parts, max_norm, norm);
-    prof_end("adam_many", s);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  Sum* part = static_cast<Sum*>(scratch);
+  return n <= kFewTensors
+             ? adam_pass<kFewTensors>(n, theta, gr, m, v, counts, h, max_norm, norm, part, s)
+             : adam_pass<kMaxTensors>(n, theta, gr, m, v, counts, h, max_norm, norm, part, s);
 }
 
 }  // namespace poetx

@@ -668,7 +668,7 @@ struct BackwardGrid {
 // round of items is a small part of the whole.  T * items fits 32 bits.
 int chunks_for(long long T, int groups, long long warps) {
   return static_cast<int>(std::min<long long>(
-      groups, std::max<long long>(1, 8 * warps / std::max<long long>(T, 1))));
+      groups, std::max<long long>(1, 2 * warps / std::max<long long>(T, 1))));
 }
 
 // Lets a kernel use more shared memory than the default limit of 48 KiB for
