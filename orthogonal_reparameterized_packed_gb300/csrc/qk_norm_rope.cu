@@ -451,10 +451,11 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kForwardPerSm : 1)
 // As the forward, but a CTA stays with one side (the first ctas_q CTAs with q)
 // and keeps its lanes' sums of dgamma in registers over all its items; they go
 // to part[CTA][D], added up by qk_dgamma_kernel in a fixed order.  A token's
-// heads are cut into `chunks` items.
+// heads are cut into `chunks` items of `chunk` groups.
 template <typename T, int V, int G, int NS, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
-    qk_backward_kernel(const QkNormRopeArgs a, int ctas_q, int chunks_q, int chunks_k) {
+    qk_backward_kernel(const QkNormRopeArgs a, int ctas_q, int chunk_q, int chunks_q, int chunk_k,
+                       int chunks_k) {
   pdl_wait();
   pdl_trigger();
   using P = Pairs<V, INTER>;
@@ -469,8 +470,7 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
   const int cta = static_cast<int>(blockIdx.x) - (is_k ? ctas_q : 0);
   const int ctas = is_k ? static_cast<int>(gridDim.x) - ctas_q : ctas_q;
   const int groups = (sd.heads + R - 1) / R;
-  const int chunks = is_k ? chunks_k : chunks_q;
-  const int chunk = (groups + chunks - 1) / chunks;
+  const int chunk = is_k ? chunk_k : chunk_q, chunks = is_k ? chunks_k : chunks_q;
   const float inv_d = 1.f / static_cast<float>(a.D);
   Slot w[NS];
   float m[NS][2][V];
@@ -664,12 +664,18 @@ struct BackwardGrid {
   }
 };
 
-// Items per token: as many as give every warp about eight, so that the last
-// round of items is a small part of the whole.  T * items fits 32 bits.
-int chunks_for(long long T, int groups, long long warps) {
-  return static_cast<int>(std::min<long long>(
-      groups, std::max<long long>(1, 2 * warps / std::max<long long>(T, 1))));
-}
+// A token's groups cut into `count` items of `size` (the last may have fewer,
+// none is empty): as many as give every warp about eight, so that the last
+// round of items is a small part of the whole.  T * count fits 32 bits.
+struct Chunks {
+  int size, count;
+  Chunks(long long T, int groups, long long warps) {
+    const long long wanted = std::max<long long>(1, 8 * warps / std::max<long long>(T, 1));
+    const int most = static_cast<int>(std::min<long long>(std::max(groups, 1), wanted));
+    size = (std::max(groups, 1) + most - 1) / most;
+    count = (std::max(groups, 1) + size - 1) / size;
+  }
+};
 
 // Lets a kernel use more shared memory than the default limit of 48 KiB for
 // all of it; `done`: the kernel's own flags, one per device.
@@ -689,10 +695,8 @@ cudaError_t forward(const QkNormRopeArgs& a, cudaStream_t s) {
   constexpr int R = 32 / G;
   const int groups = (a.hq + R - 1) / R + (a.hk + R - 1) / R;
   const long long warps = static_cast<long long>(kForwardPerSm) * kWarps * sm_count();
-  const int wanted = chunks_for(a.T, groups, warps);
-  const int chunk = (groups + wanted - 1) / wanted;
-  const int chunks = (groups + chunk - 1) / chunk;
-  const long long items = a.T * chunks;
+  const Chunks cut(a.T, groups, warps);
+  const long long items = a.T * cut.count;
   const int grid = static_cast<int>(
       std::min<long long>((items + kWarps - 1) / kWarps, warps / kWarps));
   auto* kernel = qk_forward_kernel<T, V, G, NS, INTER, FULL>;
@@ -700,20 +704,21 @@ cudaError_t forward(const QkNormRopeArgs& a, cudaStream_t s) {
   static std::atomic<bool> done[64];
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, a, chunk, chunks);
+  return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, a, cut.size, cut.count);
 }
 
 template <typename T, int V, int G, int NS, bool INTER, bool FULL>
 cudaError_t backward(const QkNormRopeArgs& a, const BackwardGrid& n, cudaStream_t s) {
   constexpr int R = 32 / G;
-  const int cq = chunks_for(a.T, (a.hq + R - 1) / R, static_cast<long long>(kWarps) * n.q);
-  const int ck = chunks_for(a.T, (a.hk + R - 1) / R, static_cast<long long>(kWarps) * n.k);
+  const Chunks cq(a.T, (a.hq + R - 1) / R, static_cast<long long>(kWarps) * n.q);
+  const Chunks ck(a.T, (a.hk + R - 1) / R, static_cast<long long>(kWarps) * n.k);
   auto* kernel = qk_backward_kernel<T, V, G, NS, INTER, FULL>;
   constexpr int smem = Rows<T, V, 4 * NS>::SMEM;
   static std::atomic<bool> done[64];
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(n.q + n.k), dim3(kThreads), smem, s, a, n.q, cq, std::max(1, ck));
+  return launch_pdl(kernel, dim3(n.q + n.k), dim3(kThreads), smem, s, a, n.q, cq.size,
+                    cq.count, ck.size, ck.count);
 }
 
 // The widest vectors (at most 16 bytes) that the sizes, pointers and strides

@@ -29,7 +29,9 @@ CASES = [(1, 32, 8, 128, 128, False), (1, 1, 1, 1, 0, False), (3, 2, 1, 2, 2, Tr
          (64, 2, 2, 96, 96, False), (11, 6, 2, 72, 36, False), (11, 6, 2, 72, 72, True),
          (130, 8, 8, 128, 128, True), (100, 9, 5, 128, 64, False), (10, 3, 3, 192, 192, False),
          (7, 3, 1, 256, 256, True), (6, 2, 2, 512, 512, False), (5, 1, 1, 511, 510, False),
-         (300, 40, 10, 16, 16, False), (257, 3, 2, 48, 24, False), (1500, 4, 2, 128, 128, False)]
+         (300, 40, 10, 16, 16, False), (257, 3, 2, 48, 24, False), (1500, 4, 2, 128, 128, False),
+         # tokens' heads cut into pieces that do not divide them
+         (480, 48, 12, 128, 128, False), (1500, 48, 12, 128, 128, False), (112, 32, 8, 96, 48, False), (2300, 20, 28, 64, 64, True)]
 
 
 @pytest.fixture(scope="module")
