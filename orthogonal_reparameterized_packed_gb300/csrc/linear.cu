@@ -30,26 +30,6 @@ struct alignas(sizeof(T) * V) Pack {
   T x[V];
 };
 
-// y = act(acc + bias) + residual for an fp32 product acc [T][N], element by element.
-template <typename T, int ACT>
-__global__ void __launch_bounds__(kThreads)
-    linear_epilogue_kernel(const float* __restrict__ acc, const float* __restrict__ bias,
-                           const T* residual, T* y, T* z, long long n, int N) {
-  pdl_wait();
-  pdl_trigger();
-  constexpr bool FAST = sizeof(T) == 2;
-  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < n;
-       i += stride) {
-    float v = acc[i];
-    if (bias != nullptr) v += bias[i % N];
-    if (z != nullptr) from_f(z[i], v);
-    v = act_f<ACT, FAST>(v);
-    if (residual != nullptr) v += to_f(residual[i]);
-    from_f(y[i], v);
-  }
-}
-
 // dz = dy act'(z) (stored where dz is not null) and, where part is not null,
 // its column sums over this CTA's rows: part[blockIdx.y][N].  32 column
 // threads of V columns each, 8 row threads, kDzRows rows per CTA.  Bound by its
@@ -135,30 +115,6 @@ __global__ void __launch_bounds__(kThreads)
     default: call(0);                   \
   }
 
-// C[M][N] = A[M][K] B, fp32, on the CUDA cores (at most 65535 row tiles per launch).
-cudaError_t simt_product(const void* A, const void* B, long long b_k, long long b_n, float* C,
-                         long long M, int N, int K, const char* tag, cudaStream_t s) {
-  constexpr long long kRows = 1 << 21;
-  for (long long m = 0; m < M; m += kRows) {
-    SimtGemm g;
-    g.M = static_cast<int>(std::min(kRows, M - m));
-    g.N = N;
-    g.K = K;
-    g.A = static_cast<const float*>(A) + m * K;
-    g.a_m = K;
-    g.a_k = 1;
-    g.B = B;
-    g.b_k = b_k;
-    g.b_n = b_n;
-    g.epi.out_f32 = C + m * N;
-    g.epi.ld = N;
-    g.tag = tag;
-    const cudaError_t e = simt_gemm_run(g, s);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
-}
-
 // out[r][0..cols) = in[r][0..cols), rows in_ld and out_ld apart: rows of an odd
 // number of bf16 features onto a 16-byte pitch, which TMA needs.  One warp
 // per row piece of 256 columns.
@@ -197,22 +153,6 @@ cudaError_t pad_rows(const void* in, void* out, long long rows, int cols, cudaSt
       launch_pdl(pad_rows_kernel, dim3(grid), dim3(kThreads), 0, s, static_cast<const bf16*>(in),
                  static_cast<long long>(cols), static_cast<bf16*>(out), pitch8(cols), rows, cols);
   prof_end("linear_pad", s);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t run_epilogue(const float* acc, const float* bias, const void* residual, void* y,
-                         void* z, long long n, int N, int act, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
-  const int grid = static_cast<int>(
-      std::min<long long>((n + kThreads - 1) / kThreads, 16ll * sm_count()));
-  prof_begin("linear_epilogue", s);
-#define RUN(A)                                                                              \
-  e = launch_pdl(linear_epilogue_kernel<T, A>, dim3(grid), dim3(kThreads), 0, s, acc, bias, \
-                 static_cast<const T*>(residual), static_cast<T*>(y), static_cast<T*>(z), n, N)
-  LINEAR_BY_ACT(act, RUN)
-#undef RUN
-  prof_end("linear_epilogue", s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -255,27 +195,20 @@ cudaError_t run_product(const LinearProduct& g, cudaStream_t s) {
 
 }  // namespace
 
-// bf16: padded copies of x and W where d_in is no multiple of 8; fp32: the product.
+// bf16: padded copies of x and W where d_in is no multiple of 8.
 size_t linear_forward_scratch(int d_in, int d_out, long long T, bool is_bf16) {
-  if (is_bf16) return pad_bytes(T, d_in) + pad_bytes(d_out, d_in);
-  return round256(static_cast<size_t>(T) * d_out * 4);
+  return is_bf16 ? pad_bytes(T, d_in) + pad_bytes(d_out, d_in) : 0;
 }
 
 cudaError_t linear_forward(const void* x, const void* W, const float* bias, const void* residual,
                            void* y, void* z, int d_in, int d_out, long long T, int act,
                            bool is_bf16, void* scratch, cudaStream_t s) {
   cudaError_t e;
-  if (!is_bf16) {
-    float* acc = static_cast<float*>(scratch);
-    e = simt_product(x, W, 1, d_in, acc, T, d_out, d_in, "linear", s);
-    if (e != cudaSuccess) return e;
-    return run_epilogue<float>(acc, bias, residual, y, z, T * d_out, d_out, act, s);
-  }
   LinearProduct g;
   g.A = x;
   g.B = W;
   g.lda = g.ldb = pitch8(d_in);
-  if (d_in % 8 != 0) {
+  if (is_bf16 && d_in % 8 != 0) {
     char* xp = static_cast<char*>(scratch);
     char* wp = xp + pad_bytes(T, d_in);
     if ((e = pad_rows(x, xp, T, d_in, s)) != cudaSuccess) return e;
@@ -292,15 +225,15 @@ cudaError_t linear_forward(const void* x, const void* W, const float* bias, cons
   g.N = d_out;
   g.K = d_in;
   g.act = act;
-  return run_product(g, s);
+  return is_bf16 ? run_product(g, s) : linear_simt(g, s);
 }
 
 // Scratch of the backward: dz (unless it is dy itself, aligned), the row
-// blocks' sums of dbias, and bf16: the padded W; fp32: the product.
+// blocks' sums of dbias, and in bf16 the padded W.
 namespace {
 
 struct BackwardPlan {
-  size_t dz = 0, part = 0, w = 0, acc = 0;
+  size_t dz = 0, part = 0, w = 0;
   int blocks;
   BackwardPlan(int d_in, int d_out, long long T, int act, bool is_bf16, bool with_dbias) {
     blocks = static_cast<int>((T + kDzRows - 1) / kDzRows);
@@ -308,13 +241,12 @@ struct BackwardPlan {
       if (act != POETX_ACT_NONE || d_out % 8 != 0)
         dz = round256(static_cast<size_t>(T) * pitch8(d_out) * 2);
       w = pad_bytes(d_out, d_in);
-    } else {
-      if (act != POETX_ACT_NONE) dz = round256(static_cast<size_t>(T) * d_out * 4);
-      acc = round256(static_cast<size_t>(T) * d_in * 4);
+    } else if (act != POETX_ACT_NONE) {
+      dz = round256(static_cast<size_t>(T) * d_out * 4);
     }
     if (with_dbias) part = round256(static_cast<size_t>(blocks) * d_out * 4);
   }
-  size_t bytes() const { return dz + part + w + acc; }
+  size_t bytes() const { return dz + part + w; }
 };
 
 }  // namespace
@@ -332,7 +264,6 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
   void* dz = plan.dz > 0 && dx != nullptr ? at : nullptr;  // null: not stored
   float* part = plan.part > 0 ? reinterpret_cast<float*>(at + plan.dz) : nullptr;
   void* wp = at + plan.dz + plan.part;
-  float* acc = reinterpret_cast<float*>(at + plan.dz + plan.part + plan.w);
   const long long ld_dz = is_bf16 ? pitch8(d_out) : d_out;
   cudaError_t e;
   if (dz != nullptr || part != nullptr) {
@@ -353,11 +284,6 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
   }
   if (dx == nullptr) return cudaSuccess;
   const void* grad = dz != nullptr ? dz : dy;
-  if (!is_bf16) {
-    e = simt_product(grad, W, d_in, 1, acc, T, d_in, d_out, "linear_dgrad", s);
-    if (e != cudaSuccess) return e;
-    return run_epilogue<float>(acc, nullptr, nullptr, dx, nullptr, T * d_in, d_in, 0, s);
-  }
   LinearProduct g;
   g.A = grad;
   g.lda = ld_dz;
@@ -374,7 +300,7 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
   g.N = d_in;
   g.K = d_out;
   g.tag = "linear_dgrad";
-  return run_product(g, s);
+  return is_bf16 ? run_product(g, s) : linear_simt(g, s);
 }
 
 }  // namespace poetx

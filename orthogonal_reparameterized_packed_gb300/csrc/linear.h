@@ -30,4 +30,8 @@ cudaError_t linear_pair(const LinearProduct& g, cudaStream_t s);
 // For few tokens: the weight streamed once, K split over a cluster (linear_stream.cu).
 cudaError_t linear_stream(const LinearProduct& g, cudaStream_t s);
 
+// In fp32 on the CUDA cores (linear_simt.cu): A, y, z, residual contiguous, B
+// [N][K] or, b_mn, [K][N] contiguous; lda, ldb and ld are not used.
+cudaError_t linear_simt(const LinearProduct& g, cudaStream_t s);
+
 }  // namespace poetx

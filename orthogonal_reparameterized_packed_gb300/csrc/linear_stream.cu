@@ -30,7 +30,6 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxSplits = 8;
 
 template <int BT>
 struct Shape {
