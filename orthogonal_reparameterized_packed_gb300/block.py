@@ -8,22 +8,29 @@ from __future__ import annotations
 
 import torch
 
-from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, poetx_clip_grads,
-               poetx_grad_norm, poetx_grad_norm_workspace_size, poetx_linear_backward,
-               poetx_linear_backward_workspace_size, poetx_linear_forward,
-               poetx_linear_forward_workspace_size, poetx_qk_norm_rope_backward,
-               poetx_qk_norm_rope_backward_workspace_size, poetx_qk_norm_rope_forward)
+from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, _check, _stream,
+               load_library, poetx_clip_grads, poetx_grad_norm, poetx_grad_norm_workspace_size,
+               poetx_linear_backward_workspace_size, poetx_linear_forward_workspace_size,
+               poetx_qk_norm_rope_backward_workspace_size)
 from .layer import _TORCH_DTYPE, dtype_code
+
+# These classes call the library directly: a call for one token costs the host
+# about as long as the GPU.
 
 ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU,
                "gelu_tanh": ACT_GELU_TANH}
 
 
 def _need(t, shape, dtype, name):
-    """t is a contiguous CUDA tensor of this shape and type, or a ValueError."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: a contiguous CUDA tensor of shape {shape} and type {dtype} is "
-                         f"needed, got {tuple(t.shape)}, {t.dtype}")
+    """The address of t, a contiguous CUDA tensor of this shape and type."""
+    if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
+    raise ValueError(f"{name}: a contiguous CUDA tensor of shape {tuple(shape)} and type {dtype} "
+                     f"is needed, got {tuple(t.shape)}, {t.dtype}, {t.device}")
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 class PoetxLinear:
@@ -49,24 +56,25 @@ class PoetxLinear:
             ws = max(ws, poetx_linear_backward_workspace_size(d_in, d_out, tokens, self.act,
                                                               self.code, True))
         self.workspace = torch.empty((max(ws, 16),), dtype=torch.uint8, device=dev)
+        lib = load_library()
+        self._fwd, self._bwd = lib.poetx_linear_forward, lib.poetx_linear_backward
 
-    def _rows(self, t):
-        if t > self.tokens:
-            raise ValueError(f"{t} tokens: the layer holds buffers for {self.tokens}")
-        return t
+    def _too_many(self, t):
+        raise ValueError(f"{t} tokens: the layer holds buffers for {self.tokens}")
 
     def forward(self, x, W, bias=None, residual=None, stream=None):
         """y for x's tokens (a view of the layer's buffer; so is z, kept in
         self.z's first rows)."""
-        t = self._rows(x.shape[0])
-        _need(x, (t, self.d_in), self.dtype, "x")
-        _need(W, (self.d_out, self.d_in), self.dtype, "W")
-        if bias is not None:
-            _need(bias, (self.d_out,), torch.float32, "bias")
-        if residual is not None:
-            _need(residual, (t, self.d_out), self.dtype, "residual")
-        poetx_linear_forward(x, W, bias, residual, self.y, self.z, self.d_in, self.d_out, t,
-                             self.act, self.code, self.workspace, stream)
+        t = x.shape[0]
+        if t > self.tokens:
+            self._too_many(t)
+        _check("poetx_linear_forward", self._fwd(
+            _need(x, (t, self.d_in), self.dtype, "x"),
+            _need(W, (self.d_out, self.d_in), self.dtype, "W"),
+            None if bias is None else _need(bias, (self.d_out,), torch.float32, "bias"),
+            None if residual is None else _need(residual, (t, self.d_out), self.dtype, "residual"),
+            self.y.data_ptr(), _address(self.z), self.d_in, self.d_out, t, self.act, self.code,
+            self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)))
         return self.y if t == self.tokens else self.y[:t]
 
     def backward(self, dy, W, z=None, stream=None):
@@ -74,16 +82,20 @@ class PoetxLinear:
         the residual's gradient is dy."""
         if self.dx is None:
             raise RuntimeError("PoetxLinear was made without backward=True")
-        t = self._rows(dy.shape[0])
+        t = dy.shape[0]
+        if t > self.tokens:
+            self._too_many(t)
         z = self.z if z is None else z
-        _need(dy, (t, self.d_out), self.dtype, "dy")
-        _need(W, (self.d_out, self.d_in), self.dtype, "W")
+        z_at = None
         if self.act != ACT_NONE:
             if z is None:
                 raise ValueError("the backward of an activation needs z (save_z=True)")
-            _need(z[:t] if z.shape[0] != t else z, (t, self.d_out), self.dtype, "z")
-        poetx_linear_backward(dy, z, W, self.dx, self.dbias, self.d_in, self.d_out, t, self.act,
-                              self.code, self.workspace, stream)
+            z_at = _need(z if z.shape[0] == t else z[:t], (t, self.d_out), self.dtype, "z")
+        _check("poetx_linear_backward", self._bwd(
+            _need(dy, (t, self.d_out), self.dtype, "dy"), z_at,
+            _need(W, (self.d_out, self.d_in), self.dtype, "W"), self.dx.data_ptr(),
+            self.dbias.data_ptr(), self.d_in, self.d_out, t, self.act, self.code,
+            self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)))
         return (self.dx if t == self.tokens else self.dx[:t]), self.dbias
 
 
@@ -107,7 +119,7 @@ class PoetxQKNormRope:
                  interleaved=False, dtype="bf16", device="cuda", backward=False):
         self.hq, self.hk, self.D, self.tokens = n_q_heads, n_k_heads, head_dim, tokens
         self.rot = head_dim if rot_dim is None else rot_dim
-        self.eps, self.interleaved = eps, interleaved
+        self.eps, self.interleaved = eps, int(bool(interleaved))
         self.code = dtype_code(dtype)
         self.dtype = _TORCH_DTYPE[self.code]
         dev = torch.device(device)
@@ -124,42 +136,46 @@ class PoetxQKNormRope:
             ws = poetx_qk_norm_rope_backward_workspace_size(n_q_heads, n_k_heads, head_dim,
                                                             tokens, self.code)
             self.workspace = torch.empty((max(ws, 16),), dtype=torch.uint8, device=dev)
+        lib = load_library()
+        self._fwd = lib.poetx_qk_norm_rope_forward
+        self._bwd = lib.poetx_qk_norm_rope_backward
+        self._wq, self._wk = n_q_heads * head_dim, n_k_heads * head_dim
 
-    def _ld(self, x, heads, t, name):
-        """The row stride of one q / k tensor."""
+    def _rows(self, x, heads, t, name):
+        """(address, row stride) of one q / k tensor."""
         st = x.stride()
         if x.dtype is self.dtype and x.is_cuda and (
                 (x.shape == (t, heads * self.D) and st[1] == 1) or
                 (x.shape == (t, heads, self.D) and st[2] == 1 and st[1] == self.D)):
-            return st[0]
+            return x.data_ptr(), st[0]
         raise ValueError(f"{name}: rows of {heads * self.D} contiguous {self.dtype} elements for "
                          f"{t} tokens are needed, got {tuple(x.shape)}, {x.dtype}, strides {st}")
 
-    def _check(self, gamma_q, gamma_k, cos, sin, positions, t):
+    def _small(self, gamma_q, gamma_k, cos, sin, positions, t):
+        """Addresses of the weights, tables and positions, and the tables' rows."""
         if t > self.tokens:
             raise ValueError(f"{t} tokens: the step holds buffers for {self.tokens}")
-        for g, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
-            if g is not None:
-                _need(g, (self.D,), torch.float32, name)
-        if self.rot:
-            _need(cos, (cos.shape[0], self.rot // 2), torch.float32, "cos")
-            _need(sin, (cos.shape[0], self.rot // 2), torch.float32, "sin")
-        if positions is not None:
-            _need(positions, (t,), torch.int32, "positions")
-        return cos.shape[0] if self.rot else 0
+        rows = cos.shape[0] if self.rot else 0
+        trig = (rows, self.rot // 2)
+        return (None if gamma_q is None else _need(gamma_q, (self.D,), torch.float32, "gamma_q"),
+                None if gamma_k is None else _need(gamma_k, (self.D,), torch.float32, "gamma_k"),
+                _need(cos, trig, torch.float32, "cos") if self.rot else None,
+                _need(sin, trig, torch.float32, "sin") if self.rot else None,
+                None if positions is None else _need(positions, (t,), torch.int32, "positions"),
+                rows)
 
     def _cut(self, buf, t):
         return buf if t == self.tokens else buf[:t]
 
     def forward(self, q, k, gamma_q, gamma_k, cos, sin, positions=None, stream=None):
         t = q.shape[0]
-        rows = self._check(gamma_q, gamma_k, cos, sin, positions, t)
-        ld_q = self._ld(q, self.hq, t, "q")
-        ld_k = self._ld(k, self.hk, t, "k") if self.hk else 0
-        poetx_qk_norm_rope_forward(q, k, gamma_q, gamma_k, cos, sin, positions, self.q_out,
-                                   self.k_out, ld_q, ld_k, self.hq * self.D, self.hk * self.D,
-                                   self.hq, self.hk, self.D, self.rot, rows, self.interleaved,
-                                   self.eps, t, self.code, stream)
+        gq, gk, c, s, pos, rows = self._small(gamma_q, gamma_k, cos, sin, positions, t)
+        q_at, ld_q = self._rows(q, self.hq, t, "q")
+        k_at, ld_k = self._rows(k, self.hk, t, "k") if self.hk else (None, 0)
+        _check("poetx_qk_norm_rope_forward", self._fwd(
+            q_at, k_at, gq, gk, c, s, pos, self.q_out.data_ptr(), self.k_out.data_ptr(), ld_q,
+            ld_k, self._wq, self._wk, self.hq, self.hk, self.D, self.rot, rows, self.interleaved, self.eps, t,
+            self.code, _stream(stream)))
         return self._cut(self.q_out, t), self._cut(self.k_out, t)
 
     def backward(self, dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, positions=None,
@@ -169,15 +185,20 @@ class PoetxQKNormRope:
         if self.dq is None:
             raise RuntimeError("PoetxQKNormRope was made without backward=True")
         t = q.shape[0]
-        rows = self._check(gamma_q, gamma_k, cos, sin, positions, t)
-        ld = [self._ld(dq_out, self.hq, t, "dq_out"),
-              self._ld(dk_out, self.hk, t, "dk_out") if self.hk else 0,
-              self._ld(q, self.hq, t, "q"), self._ld(k, self.hk, t, "k") if self.hk else 0]
-        poetx_qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, positions,
-                                    self.dq, self.dk, self.dgamma_q, self.dgamma_k, *ld,
-                                    self.hq * self.D, self.hk * self.D, self.hq, self.hk, self.D,
-                                    self.rot, rows, self.interleaved, self.eps, t, self.code,
-                                    self.workspace, stream)
+        gq, gk, c, s, pos, rows = self._small(gamma_q, gamma_k, cos, sin, positions, t)
+        dq_at, ld_dq = self._rows(dq_out, self.hq, t, "dq_out")
+        q_at, ld_q = self._rows(q, self.hq, t, "q")
+        dk_at = k_at = None
+        ld_dk = ld_k = 0
+        if self.hk:
+            dk_at, ld_dk = self._rows(dk_out, self.hk, t, "dk_out")
+            k_at, ld_k = self._rows(k, self.hk, t, "k")
+        _check("poetx_qk_norm_rope_backward", self._bwd(
+            dq_at, dk_at, q_at, k_at, gq, gk, c, s, pos, self.dq.data_ptr(), self.dk.data_ptr(),
+            self.dgamma_q.data_ptr(), self.dgamma_k.data_ptr(), ld_dq, ld_dk, ld_q, ld_k,
+            self._wq, self._wk, self.hq, self.hk, self.D, self.rot, rows, self.interleaved,
+            self.eps, t, self.code, self.workspace.data_ptr(), self.workspace.numel(),
+            _stream(stream)))
         return self._cut(self.dq, t), self._cut(self.dk, t), self.dgamma_q, self.dgamma_k
 
 
