@@ -195,9 +195,30 @@ cudaError_t run_product(const LinearProduct& g, cudaStream_t s) {
 
 }  // namespace
 
-// bf16: padded copies of x and W where d_in is no multiple of 8.
+namespace {
+
+// fp32: the scratch and the run of a product [M][K] x [K][N] (b_mn as in LinearProduct).
+size_t fp32_scratch(long long M, int N, int K, bool b_mn) {
+  if (!linear_split_pays(M, N, K)) return 0;
+  LinearProduct g;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.b_mn = b_mn;
+  return linear_split_scratch(g);
+}
+
+cudaError_t run_fp32(const LinearProduct& g, void* scratch, cudaStream_t s) {
+  return linear_split_pays(g.M, g.N, g.K) ? linear_split(g, scratch, s) : linear_simt(g, s);
+}
+
+}  // namespace
+
+// bf16: padded copies of x and W where d_in is no multiple of 8; fp32: the
+// planes of x and W where the product runs on the tensor cores.
 size_t linear_forward_scratch(int d_in, int d_out, long long T, bool is_bf16) {
-  return is_bf16 ? pad_bytes(T, d_in) + pad_bytes(d_out, d_in) : 0;
+  return is_bf16 ? pad_bytes(T, d_in) + pad_bytes(d_out, d_in)
+                 : fp32_scratch(T, d_out, d_in, false);
 }
 
 cudaError_t linear_forward(const void* x, const void* W, const float* bias, const void* residual,
@@ -225,11 +246,11 @@ cudaError_t linear_forward(const void* x, const void* W, const float* bias, cons
   g.N = d_out;
   g.K = d_in;
   g.act = act;
-  return is_bf16 ? run_product(g, s) : linear_simt(g, s);
+  return is_bf16 ? run_product(g, s) : run_fp32(g, scratch, s);
 }
 
 // Scratch of the backward: dz (unless it is dy itself, aligned), the row
-// blocks' sums of dbias, and in bf16 the padded W.
+// blocks' sums of dbias, and in bf16 the padded W, in fp32 the planes.
 namespace {
 
 struct BackwardPlan {
@@ -241,8 +262,9 @@ struct BackwardPlan {
       if (act != POETX_ACT_NONE || d_out % 8 != 0)
         dz = round256(static_cast<size_t>(T) * pitch8(d_out) * 2);
       w = pad_bytes(d_out, d_in);
-    } else if (act != POETX_ACT_NONE) {
-      dz = round256(static_cast<size_t>(T) * d_out * 4);
+    } else {
+      if (act != POETX_ACT_NONE) dz = round256(static_cast<size_t>(T) * d_out * 4);
+      w = fp32_scratch(T, d_in, d_out, true);
     }
     if (with_dbias) part = round256(static_cast<size_t>(blocks) * d_out * 4);
   }
@@ -290,7 +312,7 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
   g.B = W;
   g.ldb = pitch8(d_in);
   g.b_mn = true;
-  if (plan.w > 0) {
+  if (is_bf16 && plan.w > 0) {
     if ((e = pad_rows(W, wp, d_out, d_in, s)) != cudaSuccess) return e;
     g.B = wp;
   }
@@ -300,7 +322,7 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
   g.N = d_in;
   g.K = d_out;
   g.tag = "linear_dgrad";
-  return is_bf16 ? run_product(g, s) : linear_simt(g, s);
+  return is_bf16 ? run_product(g, s) : run_fp32(g, wp, s);
 }
 
 }  // namespace poetx

@@ -21,6 +21,8 @@ struct LinearProduct {
   long long M = 0;
   int N = 0, K = 0;
   int act = 0;
+  // linear_simt: where flags[0] is 0, only rows with flags[1 + row] != 0 are computed
+  const int* flags = nullptr;
   const char* tag = "linear";
 };
 
@@ -33,5 +35,11 @@ cudaError_t linear_stream(const LinearProduct& g, cudaStream_t s);
 // In fp32 on the CUDA cores (linear_simt.cu): A, y, z, residual contiguous, B
 // [N][K] or, b_mn, [K][N] contiguous; lda, ldb and ld are not used.
 cudaError_t linear_simt(const LinearProduct& g, cudaStream_t s);
+
+// In fp32 on the tensor cores, as six bf16 products (linear_split.cu); layouts
+// as for linear_simt, scratch of linear_split_scratch(g) bytes.
+bool linear_split_pays(long long M, int N, int K);
+size_t linear_split_scratch(const LinearProduct& g);
+cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s);
 
 }  // namespace poetx

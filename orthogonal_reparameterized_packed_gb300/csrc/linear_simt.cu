@@ -41,6 +41,8 @@ struct SimtArgs {
   float* z;
   long long M;
   int N, K, splits, k_slice, act;
+  const int* all_rows;   // null: every row; otherwise every row where it is not 0,
+  const int* row_flags;  // and else the rows flagged here
   bool vec_a, vec_b, vec_n;  // 16-byte rows: of A, of B, of the outputs
 };
 
@@ -114,6 +116,7 @@ __device__ __forceinline__ float apply(int act, float v) {
 // The epilogue of outputs (m, n .. n + 3).
 __device__ __forceinline__ void finish4(const SimtArgs& p, long long m, int n, float4 acc) {
   if (m >= p.M || n >= p.N) return;
+  if (p.all_rows != nullptr && *p.all_rows == 0 && p.row_flags[m] == 0) return;
   float v[4] = {acc.x, acc.y, acc.z, acc.w};
   const int live = min(4, p.N - n);
   const long long at = m * p.N + n;
@@ -152,6 +155,11 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
   extern __shared__ __align__(16) float smem[];
   pdl_wait();
   pdl_trigger();
+  if (p.all_rows != nullptr && *p.all_rows == 0) {
+    // the same for all CTAs of a cluster: they have the same rows
+    const long long m = static_cast<long long>(blockIdx.y) * S::TM + threadIdx.x;
+    if (!__syncthreads_or(threadIdx.x < S::TM && m < p.M && p.row_flags[m] != 0)) return;
+  }
   const int slice = static_cast<int>(blockIdx.x) % p.splits;
   const int n0 = static_cast<int>(blockIdx.x) / p.splits * kTN;
   const long long m0 = static_cast<long long>(blockIdx.y) * TM;
@@ -364,6 +372,8 @@ cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, cu
   p.N = g.N;
   p.K = g.K;
   p.act = g.act;
+  p.all_rows = g.flags;
+  p.row_flags = g.flags != nullptr ? g.flags + 1 + m_first : nullptr;
   p.vec_a = g.K % 4 == 0;
   p.vec_b = (B_KN ? g.N : g.K) % 4 == 0;
   p.vec_n = g.N % 4 == 0;

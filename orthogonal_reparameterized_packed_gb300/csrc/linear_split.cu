@@ -1,0 +1,562 @@
+// The matrix products of poetx_linear_* in fp32 on the tensor cores.
+//
+// Every fp32 value is the sum of three bf16 numbers, x = x1 + x2 + x3, each the
+// rounding of what the ones before leave (24 bits in all), so
+//   x w = x1 w1 + (x1 w2 + x2 w1) + (x1 w3 + x2 w2 + x3 w1) + O(2^-24 |x w|)
+// and an fp32 product is six bf16 products with fp32 accumulation.  The tensor
+// core's accumulation truncates (a sum of 1 and 64 terms of 0.75 ulp is 1), which
+// would bias long sums; so the six products of every 128 of K, the small ones
+// first, are accumulated on their own, and those partial sums are added up in
+// registers with round-to-nearest: 2e-7 to 4e-7 of the result, as a plain fp32
+// product has (cuBLAS: 4e-7 to 1e-6 on the same inputs).
+//
+// x and W are split into three bf16 planes each in the workspace first.  Where
+// a value is not finite (or its rounding to bf16 is not) the planes cannot
+// express it: the split sets the flag of its token (of all, where it is W's),
+// this kernel leaves those rows alone and linear_simt, enqueued behind it,
+// computes them; its tiles without such rows return at once.
+//
+// The kernel is linear_pair's with another epilogue: CTA pairs, 256 x 256
+// tiles, 64-wide K steps in a ring of six 32 KiB stages, one step per pair of
+// planes; 16 epilogue warps (64 columns each) drain one of two TMEM
+// accumulators into registers while the next 128 of K go into the other.
+#include <algorithm>
+#include <mutex>
+
+#include "activation.cuh"
+#include "internal.h"
+#include "linear.h"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+
+namespace poetx {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kBN = 256;
+constexpr int kA = BM * BK * 2;         // this CTA's 128 rows, one K step
+constexpr int kB = (kBN / 2) * BK * 2;  // this CTA's half of B, one K step
+constexpr int kStage = kA + kB;
+constexpr int kStages = 6;
+constexpr int kRing = kStages * kStage;
+constexpr int kBiasBytes = kEpiWarps * 64 * 4;
+constexpr int kSmem = kRing + kBiasBytes + 256;
+static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+constexpr uint32_t kTmemCols = 2 * kBN;
+constexpr int kGroupM = 8;
+constexpr int kPlanes = 3;
+constexpr int kProducts = 6;
+constexpr int kChunkSteps = 2;  // K steps accumulated by the tensor core in one go
+
+// Product p = 0 .. 5, the smallest first: planes (2,0) (0,2) (1,1) (1,0) (0,1)
+// (0,0) of A and B, four bits each.
+__device__ __forceinline__ int plane_a(int p) { return (0x001102 >> (4 * p)) & 3; }
+__device__ __forceinline__ int plane_b(int p) { return (0x010120 >> (4 * p)) & 3; }
+
+struct SplitArgs {
+  int m_pairs, n_tiles, k_steps, N;
+  int plane_rows_a, plane_rows_b;  // rows between planes of A, of B
+  long long M;
+  int act;
+  bool vec;  // 16-byte output rows
+  const float* bias;
+  const float* residual;
+  float* y;
+  float* z;
+  const int* flags;  // [0]: of W, [1 + row]: of A's rows; not 0: left to linear_simt
+  int* status;
+};
+
+__device__ __forceinline__ void unit_tile(int u, const SplitArgs& p, int& mp, int& nt) {
+  const int per_group = kGroupM * p.n_tiles;
+  const int g = u / per_group, r = u - g * per_group;
+  const int rows = min(kGroupM, p.m_pairs - g * kGroupM);
+  mp = g * kGroupM + r % rows;
+  nt = r / rows;
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_all(float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = act_f<ACT, false>(v[j]);
+}
+
+__device__ __forceinline__ void apply_act(int act, float (&v)[16]) {
+  switch (act) {  // uniform over the grid
+    case POETX_ACT_RELU: act_all<POETX_ACT_RELU>(v); break;
+    case POETX_ACT_SILU: act_all<POETX_ACT_SILU>(v); break;
+    case POETX_ACT_GELU: act_all<POETX_ACT_GELU>(v); break;
+    case POETX_ACT_GELU_TANH: act_all<POETX_ACT_GELU_TANH>(v); break;
+    default: break;
+  }
+}
+
+// 16 values of a row at `at`, `live` of them inside.
+__device__ __forceinline__ void store16(float* out, long long at, const float (&v)[16], int live,
+                                        bool vec) {
+  if (vec && live >= 16) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 4)
+      *reinterpret_cast<float4*>(out + at + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < live) out[at + j] = v[j];
+  }
+}
+
+template <bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_split_kernel(const __grid_constant__ CUtensorMap tmA,
+                        const __grid_constant__ CUtensorMap tmB, const SplitArgs p) {
+  extern __shared__ __align__(1024) uint8_t base[];  // 128B-swizzled tiles start on 1024 bytes
+  if ((smem_u32(base) & 1023u) != 0) {  // the declared alignment, which the tiles rely on
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, static_cast<int>(POETX_ERR_CUDA));
+    return;
+  }
+  uint8_t* ring = base;  // stage s: A (16 KiB), then this CTA's half of B
+  float* bias_s = reinterpret_cast<float*>(base + kRing);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(base + kRing + kBiasBytes);  // leader
+  uint64_t* empty_bar = full_bar + kStages;   // each CTA: its slot is free
+  uint64_t* tfull_bar = empty_bar + kStages;  // [2] each CTA: accumulator ready
+  uint64_t* tempty_bar = tfull_bar + 2;       // [2] leader: accumulator drained
+  uint64_t* drain_bar = tempty_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int first = static_cast<int>(cluster_id_x());
+  const int step = static_cast<int>(cluster_count_x());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull_bar[a], 1);
+      mbar_init(&tempty_bar[a], 2 * kEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before either signals the other
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  const int units = p.flags[0] != 0 ? 0 : p.m_pairs * p.n_tiles;
+
+  const uint32_t full0 = map_peer(smem_u32(full_bar), 0);
+  const uint32_t tempty0 = map_peer(smem_u32(tempty_bar), 0);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    // (here and in the MMA warp one elected lane issues, as in linear_pair)
+    int stage = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool ok = true;
+    for (int u = first; u < units && ok; u += step) {
+      int mp, nt;
+      unit_tile(u, p, mp, nt);
+      const int a_row = mp * 2 * BM + static_cast<int>(rank) * BM;
+      const int b_n = nt * kBN + static_cast<int>(rank) * (kBN / 2);
+      for (int k0 = 0; k0 < p.k_steps && ok; k0 += kChunkSteps) {
+        const int k1 = min(p.k_steps, k0 + kChunkSteps);
+        for (int pr = 0; pr < kProducts && ok; ++pr) {
+          const int ra = plane_a(pr) * p.plane_rows_a + a_row;
+          const int rb = plane_b(pr) * p.plane_rows_b;
+          for (int ks = k0; ks < k1; ++ks) {
+            if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) {
+              record_timeout(p.status, abort_flag);
+              ok = false;
+              break;
+            }
+            if (elect_one()) {
+              if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStage);
+              uint8_t* a_dst = ring + stage * kStage;
+              uint8_t* b_dst = a_dst + kA;
+              const uint32_t bar = full0 + static_cast<uint32_t>(stage * 8);
+              tma_load_2d_pair(a_dst, &tmA, bar, ks * BK, ra);
+              if (!B_MN) {
+                tma_load_2d_pair(b_dst, &tmB, bar, ks * BK, rb + b_n);
+              } else {
+                tma_load_2d_pair(b_dst, &tmB, bar, b_n, rb + ks * BK);
+                tma_load_2d_pair(b_dst + 8192, &tmB, bar, b_n + 64, rb + ks * BK);
+              }
+            }
+            __syncwarp();
+            ++issued;
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+        }
+      }
+    }
+    // every slot this CTA filled is released again before it leaves
+    const int outstanding = issued < kStages ? static_cast<int>(issued) : kStages;
+    int st = stage;
+    uint32_t ph = phase;
+    for (int n = 0; n < outstanding; ++n) {
+      if (--st < 0) {
+        st = kStages - 1;
+        ph ^= 1;
+      }
+      const unsigned long long t0 = global_timer_ns();
+      while (!mbar_try_wait_cluster(&empty_bar[st], ph) &&
+             global_timer_ns() - t0 < (ok ? kWaitLimitNs : 10000000ull)) {
+      }
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      // -------------------------------------------------- MMA issuer (pair)
+      constexpr uint32_t IDESC = instr_desc_bf16(2 * BM, kBN, false, B_MN);
+      const uint32_t empty_own = smem_u32(empty_bar);
+      const uint32_t tfull_own = smem_u32(tfull_bar);
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      bool any_mma = false;
+      for (int u = first; u < units && ok; u += step) {
+        for (int k0 = 0; k0 < p.k_steps && ok; k0 += kChunkSteps) {
+          const int steps = (min(p.k_steps, k0 + kChunkSteps) - k0) * kProducts;
+          if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1, abort_flag)) {
+            record_timeout(p.status, abort_flag);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kBN);
+          for (int i = 0; i < steps; ++i) {
+            if (!mbar_wait(&full_bar[stage], phase, abort_flag)) {
+              record_timeout(p.status, abort_flag);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_base = smem_u32(ring) + stage * kStage;
+            const uint64_t adesc0 = smem_desc_sw128(a_base, 16, 1024);
+            const uint64_t bdesc0 = smem_desc_sw128(a_base + kA, B_MN ? 8192 : 16, 1024);
+            if (elect_one()) {
+#pragma unroll
+              for (int j = 0; j < BK / 16; ++j)
+                umma_bf16_pair(d_tmem, adesc0 + j * 2, bdesc0 + j * (B_MN ? 128 : 2), IDESC,
+                               (i > 0 || j > 0) ? 1u : 0u);
+              umma_commit_both(empty_own + static_cast<uint32_t>(stage * 8));
+            }
+            __syncwarp();
+            any_mma = true;
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+          if (!ok) break;
+          if (elect_one()) umma_commit_both(tfull_own + static_cast<uint32_t>(acc * 8));
+          __syncwarp();
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+        }
+      }
+      if (!ok && any_mma) {
+        // the MMAs in flight finish before TMEM is released
+        if (elect_one()) umma_commit_pair(smem_u32(drain_bar));
+        __syncwarp();
+        const unsigned long long t0 = global_timer_ns();
+        while (!mbar_try_wait(drain_bar, 0) && global_timer_ns() - t0 < 10000000ull) {
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int ew = warp - 2;
+    const int quarter = warp & 3;  // the TMEM lanes this warp may read
+    const int side = ew >> 2;      // its quarter of the tile's columns
+    float* bias_w = bias_s + ew * 64;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int u = first; u < units && ok; u += step) {
+      int mp, nt;
+      unit_tile(u, p, mp, nt);
+      const long long row =
+          static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32 + lane;
+      const int col0 = nt * kBN + side * 64;
+      float sum[4][16] = {};
+      for (int k0 = 0; k0 < p.k_steps; k0 += kChunkSteps) {
+        const bool got = mbar_wait_cluster(&tfull_bar[acc], acc_phase, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
+          record_timeout(p.status, abort_flag);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t t_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                static_cast<uint32_t>(acc * kBN + side * 64);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t r[16];
+          tmem_load_16(t_base + q * 16, r);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[q][j] += __uint_as_float(r[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        // the accumulator is free again once both CTAs' epilogue warps have read it
+        if (lane == 0) mbar_arrive_remote(tempty0 + static_cast<uint32_t>(acc * 8));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+      if (!ok) break;
+      if (p.bias != nullptr) {
+        __syncwarp();
+        bias_w[lane] = col0 + lane < p.N ? __ldg(p.bias + col0 + lane) : 0.f;
+        bias_w[lane + 32] = col0 + lane + 32 < p.N ? __ldg(p.bias + col0 + lane + 32) : 0.f;
+        __syncwarp();
+      }
+      if (row >= p.M || p.flags[1 + row] != 0) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int live = p.N - (col0 + q * 16);
+        if (live <= 0) break;
+        const long long at = row * p.N + col0 + q * 16;
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          v[j] = sum[q][j] + (p.bias != nullptr ? bias_w[q * 16 + j] : 0.f);
+        if (p.z != nullptr) store16(p.z, at, v, live, p.vec);
+        apply_act(p.act, v);
+        if (p.residual != nullptr) {
+          if (p.vec && live >= 16) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 r = *reinterpret_cast<const float4*>(p.residual + at + j);
+              v[j] += r.x, v[j + 1] += r.y, v[j + 2] += r.z, v[j + 3] += r.w;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j < live) v[j] += p.residual[at + j];
+          }
+        }
+        store16(p.y, at, v, live, p.vec);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still signal or read it
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// in [rows][cols] fp32 -> planes [3][plane_rows][pitch] bf16, rows from `rows` to
+// plane_rows zero (columns past cols are not read by any tile).  Where a value's
+// planes are not finite, sets flag[r] (by_row) or flag[0].
+constexpr int kSplitThreads = 256;
+
+__global__ void __launch_bounds__(kSplitThreads)
+    split_planes_kernel(const float* __restrict__ in, long long rows, int cols,
+                        bf16* __restrict__ planes, long long plane_rows, long long pitch,
+                        int* flag, bool by_row) {
+  pdl_wait();
+  pdl_trigger();
+  const int quads = (cols + 3) / 4;
+  const bool vec = cols % 4 == 0;
+  // a warp per piece of 32 quads of a row
+  const int pieces = (quads + 31) / 32, lane = threadIdx.x % 32;
+  const long long items = plane_rows * pieces;
+  for (long long it = blockIdx.x * static_cast<long long>(kSplitThreads / 32) + threadIdx.x / 32;
+       it < items; it += static_cast<long long>(gridDim.x) * (kSplitThreads / 32)) {
+    const long long r = it / pieces;
+    const int c = (static_cast<int>(it - r * pieces) * 32 + lane) * 4;
+    if (c >= cols) continue;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r < rows) {
+      if (vec) {
+        const float4 q = *reinterpret_cast<const float4*>(in + r * cols + c);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j < cols) v[j] = in[r * cols + c + j];
+      }
+    }
+    bool bad = false;
+    uint32_t w[kPlanes][2];
+#pragma unroll
+    for (int s = 0; s < kPlanes; ++s) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * h], v[2 * h + 1]);
+        const float2 f = __bfloat1622float2(b);
+        if (s == 0) bad |= !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
+        v[2 * h] -= f.x;  // exact: the rounding error of a bf16 rounding
+        v[2 * h + 1] -= f.y;
+        w[s][h] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      // rows are a multiple of 8 elements apart: 8 bytes fit, padding included
+      *reinterpret_cast<uint2*>(planes + (s * plane_rows + r) * pitch + c) =
+          make_uint2(w[s][0], w[s][1]);
+    }
+    if (bad) flag[by_row ? r : 0] = 1;  // whoever writes it writes 1
+  }
+}
+
+cudaError_t split_planes(const void* in, long long rows, int cols, void* planes,
+                         long long plane_rows, int* flag, bool by_row, cudaStream_t s) {
+  const long long items = plane_rows * (((cols + 3) / 4 + 31) / 32);
+  const int grid = static_cast<int>(std::min<long long>((items + 7) / 8, 16ll * sm_count()));
+  prof_begin("linear_split_planes", s);
+  const cudaError_t e = launch_pdl(split_planes_kernel, dim3(grid), dim3(kSplitThreads), 0, s,
+                                   static_cast<const float*>(in), rows, cols,
+                                   static_cast<bf16*>(planes), plane_rows,
+                                   static_cast<long long>((cols + 7) / 8 * 8), flag, by_row);
+  prof_end("linear_split_planes", s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+long long b_plane_rows(const LinearProduct& g) {
+  // [K][N]: rows to a whole K step, so that no tile meets the next plane's rows
+  return g.b_mn ? (g.K + BK - 1) / BK * BK : g.N;
+}
+
+int b_cols(const LinearProduct& g) { return g.b_mn ? g.N : g.K; }
+
+size_t planes_bytes(long long plane_rows, int cols) {
+  return round256(static_cast<size_t>(kPlanes) * plane_rows * ((cols + 7) / 8 * 8) * 2);
+}
+
+template <bool B_MN>
+cudaError_t launch(const LinearProduct& g, const void* a_planes, const void* b_planes,
+                   const int* flags, cudaStream_t stream) {
+  auto* kernel = linear_split_kernel<B_MN>;
+  static bool ready[64] = {false};
+  static int max_clusters[64] = {0};
+  static std::mutex mu;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  int cmax;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+      cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      if (e != cudaSuccess) return e;
+      cfg.gridDim = dim3(2 * sm_count());
+      cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorLaunchOutOfResources;
+      max_clusters[dev] = n;
+      ready[dev] = true;
+    }
+    cmax = max_clusters[dev];
+  }
+  SplitArgs p;
+  p.plane_rows_a = static_cast<int>(g.M);
+  p.plane_rows_b = static_cast<int>(b_plane_rows(g));
+  CUtensorMap tmA, tmB;
+  if (!make_map(&tmA, a_planes, kPlanes * g.M, g.K, (g.K + 7) / 8 * 8, 2, 64, BM))
+    return cudaErrorInvalidValue;
+  if (!make_map(&tmB, b_planes, kPlanes * b_plane_rows(g), b_cols(g), (b_cols(g) + 7) / 8 * 8, 2,
+                64, B_MN ? 64 : kBN / 2))
+    return cudaErrorInvalidValue;
+  p.m_pairs = static_cast<int>((g.M + 2 * BM - 1) / (2 * BM));
+  p.n_tiles = (g.N + kBN - 1) / kBN;
+  p.k_steps = (g.K + BK - 1) / BK;
+  p.N = g.N;
+  p.M = g.M;
+  p.act = g.act;
+  p.vec = g.N % 4 == 0;
+  p.bias = g.bias;
+  p.residual = static_cast<const float*>(g.residual);
+  p.y = static_cast<float*>(g.y);
+  p.z = static_cast<float*>(g.z);
+  p.flags = flags;
+  p.status = device_status_ptr();
+  const int clusters = static_cast<int>(
+      std::min<long long>(static_cast<long long>(p.m_pairs) * p.n_tiles, cmax));
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.numAttrs = 2;
+  prof_begin(g.tag, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, p);
+  prof_end(g.tag, stream);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+bool linear_split_pays(long long M, int N, int K) {
+  if (M > (1ll << 24)) return false;
+  const long long units = ((M + 255) / 256) * ((N + 255) / 256);
+  const long long clusters = std::max(1, sm_count() / 2);
+  const double split = 16.0 + 1.75 * ((K + 63) / 64) * ((units + clusters - 1) / clusters) +
+                       10e-6 * K * (static_cast<double>(M) + N) / 6.0;
+  const double simt = 8.0 + 2e-6 * M * N * K / 45.0;
+  return split < simt;
+}
+
+size_t linear_split_scratch(const LinearProduct& g) {
+  return round256(static_cast<size_t>(1 + g.M) * sizeof(int)) + planes_bytes(g.M, g.K) +
+         planes_bytes(b_plane_rows(g), b_cols(g));
+}
+
+cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) {
+  int* flags = static_cast<int*>(scratch);
+  const size_t flag_bytes = static_cast<size_t>(1 + g.M) * sizeof(int);
+  char* a = static_cast<char*>(scratch) + round256(flag_bytes);
+  char* b = a + planes_bytes(g.M, g.K);
+  cudaError_t e = cudaMemsetAsync(flags, 0, flag_bytes, s);
+  if (e != cudaSuccess) return e;
+  if ((e = split_planes(g.A, g.M, g.K, a, g.M, flags + 1, true, s)) != cudaSuccess) return e;
+  e = split_planes(g.B, g.b_mn ? g.K : g.N, b_cols(g), b, b_plane_rows(g), flags, false, s);
+  if (e != cudaSuccess) return e;
+  e = g.b_mn ? launch<true>(g, a, b, flags, s) : launch<false>(g, a, b, flags, s);
+  if (e != cudaSuccess) return e;
+  LinearProduct again = g;
+  again.flags = flags;
+  return linear_simt(again, s);
+}
+
+}  // namespace poetx

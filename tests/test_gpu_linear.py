@@ -30,7 +30,9 @@ ACT_ERR = {"bf16": 2.0 ** -18, "f32": 2.0 ** -21}
 SHAPES = [(1, 1, 1), (1, 64, 128), (1, 4096, 512), (2, 72, 40), (5, 3, 7), (7, 8, 8),
           (16, 256, 136), (17, 1000, 777), (24, 512, 1416), (33, 264, 1000), (64, 2048, 256),
           (65, 128, 520), (127, 192, 264), (128, 64, 128), (129, 320, 1288), (200, 576, 96),
-          (256, 256, 256), (300, 136, 304), (513, 512, 640), (700, 1024, 2056), (1025, 2048, 513)]
+          (256, 256, 256), (300, 136, 304), (513, 512, 640), (700, 1024, 2056), (1025, 2048, 513),
+          # fp32: large enough for the tensor cores, either way
+          (1301, 517, 1303), (900, 1536, 1200), (2100, 1000, 130), (700, 2056, 1024)]
 
 
 @pytest.fixture(scope="module")
@@ -172,7 +174,7 @@ def test_dx_is_the_difference_of_the_forward(px):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("T,a,b", [(20, 64, 128), (300, 256, 512)])
+@pytest.mark.parametrize("T,a,b", [(20, 64, 128), (300, 256, 512), (1301, 517, 1303)])
 def test_nan_and_inf_stay_in_their_token(px, T, a, b, dtype):
     (x, _), (W, _), (bias, _), (res, _) = inputs(T, a, b, dtype, 150)
     from orthogonal_reparameterized_packed_gb300.block import PoetxLinear
@@ -188,6 +190,39 @@ def test_nan_and_inf_stay_in_their_token(px, T, a, b, dtype):
     assert torch.equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("T,a,b", [(700, 4096, 1024), (1301, 517, 1303), (900, 1536, 1200)])
+def test_fp32_keeps_its_accuracy_on_the_tensor_cores(px, T, a, b):
+    # Sums over 128 of K truncate at eight steps, each by at most 2^-23 and half of it on
+    # average, so the whole by 8 * 2^-24 = 4.8e-7 on average; the fp32 additions of the partial
+    # sums round to nearest (2^-24 each, of either sign).  Twice the average: 1e-6.
+    (x, x64), (W, W64), _, _ = inputs(T, a, b, "f32", 180)
+    from orthogonal_reparameterized_packed_gb300.block import PoetxLinear
+    layer = PoetxLinear(a, b, T, dtype="f32", backward=True)
+    want = x64 @ W64.T
+    assert np.linalg.norm(host(layer.forward(x, W)) - want) <= 1e-6 * np.linalg.norm(want)
+    dy, dy64 = rounded(np.random.default_rng(181).standard_normal((T, b)), "f32")
+    want = dy64 @ W64
+    dx, _ = layer.backward(dy, W)
+    status_ok(px)
+    assert np.linalg.norm(host(dx) - want) <= 1e-6 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-18, 1e15, 1e38])
+def test_fp32_over_its_whole_range(px, scale):
+    # values whose bf16 planes under- or overflow: large x with small W and the other way round
+    T, a, b = 1301, 517, 1303
+    rng = np.random.default_rng(190)
+    x, x64 = rounded(rng.uniform(1, 3.3, (T, a)) * scale, "f32")
+    W, W64 = rounded(rng.standard_normal((b, a)) / scale * 1e-2, "f32")
+    from orthogonal_reparameterized_packed_gb300.block import PoetxLinear
+    y = host(PoetxLinear(a, b, T, dtype="f32").forward(x, W))
+    status_ok(px)
+    S = np.abs(x64) @ np.abs(W64).T
+    # subnormal parts (below 2^-126) may be lost whole: 517 of them times the largest factor
+    lost = 517 * 2.0 ** -126 * max(np.abs(x64).max(), np.abs(W64).max())
+    within(y, x64 @ W64.T, (a + 4) * 2.0 ** -23 * S + lost)
+
+
 def test_zero_tokens(px):
     W = torch.zeros((64, 32), dtype=torch.bfloat16, device="cuda")
     db = torch.full((64,), 7.0, device="cuda")
@@ -198,7 +233,8 @@ def test_zero_tokens(px):
 
 
 @pytest.mark.parametrize("dtype,T,a,b", [("bf16", 1, 512, 512), ("bf16", 40, 1024, 264),
-                                         ("bf16", 900, 512, 768), ("f32", 200, 136, 264)])
+                                         ("bf16", 900, 512, 768), ("f32", 200, 136, 264),
+                                         ("f32", 1301, 517, 1303)])
 def test_same_bits_on_another_stream_and_in_a_graph(px, dtype, T, a, b):
     (x, _), (W, _), (bias, _), (res, _) = inputs(T, a, b, dtype, 160)
     dy, _ = rounded(np.random.default_rng(161).standard_normal((T, b)), dtype)
