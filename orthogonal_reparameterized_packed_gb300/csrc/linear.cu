@@ -17,8 +17,11 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 256;
 
-// Elements between rows of `cols` bf16 features once they are TMA operands.
-long long pitch8(int cols) { return (static_cast<long long>(cols) + 7) / 8 * 8; }
+// Elements between rows of `cols` bf16 features as TMA operands: as they are
+// where that is a multiple of 16 bytes, else copied onto whole 128-byte lines.
+long long tma_pitch(int cols) {
+  return cols % 8 == 0 ? cols : (static_cast<long long>(cols) + 63) / 64 * 64;
+}
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
@@ -151,7 +154,7 @@ cudaError_t pad_rows(const void* in, void* out, long long rows, int cols, cudaSt
   prof_begin("linear_pad", s);
   const cudaError_t e =
       launch_pdl(pad_rows_kernel, dim3(grid), dim3(kThreads), 0, s, static_cast<const bf16*>(in),
-                 static_cast<long long>(cols), static_cast<bf16*>(out), pitch8(cols), rows, cols);
+                 static_cast<long long>(cols), static_cast<bf16*>(out), tma_pitch(cols), rows, cols);
   prof_end("linear_pad", s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -177,7 +180,7 @@ size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // Bytes of a padded copy of [rows][cols] bf16, 0 where the rows are aligned already.
 size_t pad_bytes(long long rows, int cols) {
-  return cols % 8 == 0 ? 0 : round256(static_cast<size_t>(rows) * pitch8(cols) * 2);
+  return cols % 8 == 0 ? 0 : round256(static_cast<size_t>(rows) * tma_pitch(cols) * 2);
 }
 
 }  // namespace
@@ -228,7 +231,7 @@ cudaError_t linear_forward(const void* x, const void* W, const float* bias, cons
   LinearProduct g;
   g.A = x;
   g.B = W;
-  g.lda = g.ldb = pitch8(d_in);
+  g.lda = g.ldb = tma_pitch(d_in);
   if (is_bf16 && d_in % 8 != 0) {
     char* xp = static_cast<char*>(scratch);
     char* wp = xp + pad_bytes(T, d_in);
@@ -260,7 +263,7 @@ struct BackwardPlan {
     blocks = static_cast<int>((T + kDzRows - 1) / kDzRows);
     if (is_bf16) {
       if (act != POETX_ACT_NONE || d_out % 8 != 0)
-        dz = round256(static_cast<size_t>(T) * pitch8(d_out) * 2);
+        dz = round256(static_cast<size_t>(T) * tma_pitch(d_out) * 2);
       w = pad_bytes(d_out, d_in);
     } else {
       if (act != POETX_ACT_NONE) dz = round256(static_cast<size_t>(T) * d_out * 4);
@@ -286,7 +289,7 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
   void* dz = plan.dz > 0 && dx != nullptr ? at : nullptr;  // null: not stored
   float* part = plan.part > 0 ? reinterpret_cast<float*>(at + plan.dz) : nullptr;
   void* wp = at + plan.dz + plan.part;
-  const long long ld_dz = is_bf16 ? pitch8(d_out) : d_out;
+  const long long ld_dz = is_bf16 ? tma_pitch(d_out) : d_out;
   cudaError_t e;
   if (dz != nullptr || part != nullptr) {
     if (is_bf16)
@@ -310,7 +313,7 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
   g.A = grad;
   g.lda = ld_dz;
   g.B = W;
-  g.ldb = pitch8(d_in);
+  g.ldb = tma_pitch(d_in);
   g.b_mn = true;
   if (is_bf16 && plan.w > 0) {
     if ((e = pad_rows(W, wp, d_out, d_in, s)) != cudaSuccess) return e;

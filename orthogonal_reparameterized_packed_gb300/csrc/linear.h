@@ -21,8 +21,10 @@ struct LinearProduct {
   long long M = 0;
   int N = 0, K = 0;
   int act = 0;
-  // linear_simt: where flags[0] is 0, only rows with flags[1 + row] != 0 are computed
+  // linear_simt: where flags[0] is 0, only rows with one of flags[1 + row * segs ..
+  // + segs) not 0 are computed
   const int* flags = nullptr;
+  int segs = 0;
   const char* tag = "linear";
 };
 

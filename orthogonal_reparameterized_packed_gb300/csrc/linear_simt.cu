@@ -19,9 +19,9 @@
 #include <algorithm>
 #include <atomic>
 
-#include "activation.cuh"
 #include "internal.h"
 #include "linear.h"
+#include "linear_fp32.cuh"
 #include "ptx.cuh"
 
 namespace poetx {
@@ -35,15 +35,13 @@ constexpr int kMaxSplits = 8;
 struct SimtArgs {
   const float* A;
   const float* B;
-  const float* bias;
-  const float* residual;
-  float* y;
-  float* z;
+  Fp32Epilogue epi;
   long long M;
-  int N, K, splits, k_slice, act;
+  int N, K, splits, k_slice;
   const int* all_rows;   // null: every row; otherwise every row where it is not 0,
-  const int* row_flags;  // and else the rows flagged here
-  bool vec_a, vec_b, vec_n;  // 16-byte rows: of A, of B, of the outputs
+  const int* row_flags;  // and else the rows with one of their `segs` flags set
+  int segs;
+  bool vec_a, vec_b;  // 16-byte rows of A, of B
 };
 
 template <int RM, bool FLAT>
@@ -103,46 +101,16 @@ __device__ __forceinline__ void piece(int e, int& row, int& quad) {
   row = rest / (KQ / 2) * RL + low;
 }
 
-__device__ __forceinline__ float apply(int act, float v) {
-  switch (act) {  // uniform over the grid
-    case POETX_ACT_RELU: return act_f<POETX_ACT_RELU, false>(v);
-    case POETX_ACT_SILU: return act_f<POETX_ACT_SILU, false>(v);
-    case POETX_ACT_GELU: return act_f<POETX_ACT_GELU, false>(v);
-    case POETX_ACT_GELU_TANH: return act_f<POETX_ACT_GELU_TANH, false>(v);
-    default: return v;
-  }
+__device__ __forceinline__ bool flagged(const SimtArgs& p, long long m) {
+  int bad = 0;
+  for (int i = 0; i < p.segs; ++i) bad |= p.row_flags[m * p.segs + i];
+  return bad != 0;
 }
 
-// The epilogue of outputs (m, n .. n + 3).
-__device__ __forceinline__ void finish4(const SimtArgs& p, long long m, int n, float4 acc) {
+__device__ __forceinline__ void finish(const SimtArgs& p, long long m, int n, float4 acc) {
   if (m >= p.M || n >= p.N) return;
-  if (p.all_rows != nullptr && *p.all_rows == 0 && p.row_flags[m] == 0) return;
-  float v[4] = {acc.x, acc.y, acc.z, acc.w};
-  const int live = min(4, p.N - n);
-  const long long at = m * p.N + n;
-  float r[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.bias != nullptr)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < live) v[j] += __ldg(p.bias + n + j);
-  if (p.vec_n) {  // then live is 4
-    if (p.residual != nullptr) {
-      const float4 q = *reinterpret_cast<const float4*>(p.residual + at);
-      r[0] = q.x, r[1] = q.y, r[2] = q.z, r[3] = q.w;
-    }
-    if (p.z != nullptr) *reinterpret_cast<float4*>(p.z + at) = make_float4(v[0], v[1], v[2], v[3]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = apply(p.act, v[j]) + r[j];
-    *reinterpret_cast<float4*>(p.y + at) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j >= live) continue;
-      if (p.residual != nullptr) r[j] = p.residual[at + j];
-      if (p.z != nullptr) p.z[at + j] = v[j];
-      p.y[at + j] = apply(p.act, v[j]) + r[j];
-    }
-  }
+  if (p.all_rows != nullptr && *p.all_rows == 0 && !flagged(p, m)) return;
+  finish4(p.epi, m, n, acc);
 }
 
 // Grid: x = N tile * splits + slice (a cluster along x), y = row tile.
@@ -158,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
   if (p.all_rows != nullptr && *p.all_rows == 0) {
     // the same for all CTAs of a cluster: they have the same rows
     const long long m = static_cast<long long>(blockIdx.y) * S::TM + threadIdx.x;
-    if (!__syncthreads_or(threadIdx.x < S::TM && m < p.M && p.row_flags[m] != 0)) return;
+    if (!__syncthreads_or(threadIdx.x < S::TM && m < p.M && flagged(p, m))) return;
   }
   const int slice = static_cast<int>(blockIdx.x) % p.splits;
   const int n0 = static_cast<int>(blockIdx.x) / p.splits * kTN;
@@ -293,15 +261,10 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
       const float4 q = mine[w * TM * kLdb / 4];
       v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
     }
-    if (p.splits == 1) {
-      finish4(p, m0 + warp, n0 + lane * 4, v);
-      return;
-    }
     mine[0] = v;  // row `warp` of the first tile: read by this thread only
   } else {
     auto row_of = [&](int i) { return i / VEC * 64 + ty * VEC + i % VEC; };
-    // to the outputs, or to the partial tile over the stages (the last step
-    // ended with a barrier)
+    // to the tile over the stages (the last step ended with a barrier)
 #pragma unroll
     for (int i = 0; i < RM; ++i)
 #pragma unroll
@@ -309,15 +272,22 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
         float4 v;
         split_pair(acc[i][2 * h], v.x, v.y);
         split_pair(acc[i][2 * h + 1], v.z, v.w);
-        if (p.splits == 1)
-          finish4(p, m0 + row_of(i), n0 + h * 64 + tx * 4, v);
-        else
-          *reinterpret_cast<float4*>(smem + row_of(i) * kLdb + h * 64 + tx * 4) = v;
+        *reinterpret_cast<float4*>(smem + row_of(i) * kLdb + h * 64 + tx * 4) = v;
       }
-    if (p.splits == 1) return;
+  }
+  // the epilogue goes through the tile in a loop: whole rows per warp, and one
+  // copy of its code
+  if (p.splits == 1) {
+    __syncthreads();
+#pragma unroll 1
+    for (int e = threadIdx.x; e < TM * 32; e += kThreads)
+      finish(p, m0 + e / 32, n0 + e % 32 * 4,
+             *reinterpret_cast<const float4*>(smem + e / 32 * kLdb + e % 32 * 4));
+    return;
   }
   cluster_sync();  // every slice's partial tile is written
   const int share = TM / p.splits;  // splits divides TM (8 at least)
+#pragma unroll 1
   for (int e = threadIdx.x; e < share * 32; e += kThreads) {
     const int r = slice * share + e / 32, c = e % 32 * 4;
     const uint32_t at = smem_u32(smem + r * kLdb + c);
@@ -339,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
 #pragma unroll
     for (int s = 1; s < kMaxSplits; ++s)
       if (s < p.splits) v.x += q[s].x, v.y += q[s].y, v.z += q[s].z, v.w += q[s].w;
-    finish4(p, m0 + r, n0 + c, v);
+    finish(p, m0 + r, n0 + c, v);
   }
   cluster_sync();  // no CTA leaves while a peer still reads its tile
 }
@@ -359,24 +329,17 @@ cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, cu
     ready[dev].store(true, std::memory_order_relaxed);
   }
   SimtArgs p;
-  auto at = [&](const void* base, long long ld) {
-    return static_cast<const float*>(base) + (base != nullptr ? m_first * ld : 0);
-  };
-  p.A = at(g.A, g.K);
+  p.A = static_cast<const float*>(g.A) + m_first * g.K;
   p.B = static_cast<const float*>(g.B);
-  p.bias = g.bias;
-  p.residual = at(g.residual, g.N);
-  p.y = const_cast<float*>(at(g.y, g.N));
-  p.z = const_cast<float*>(at(g.z, g.N));
+  p.epi = fp32_epilogue(g, m_first);
   p.M = rows;
   p.N = g.N;
   p.K = g.K;
-  p.act = g.act;
   p.all_rows = g.flags;
-  p.row_flags = g.flags != nullptr ? g.flags + 1 + m_first : nullptr;
+  p.row_flags = g.flags != nullptr ? g.flags + 1 + m_first * g.segs : nullptr;
+  p.segs = g.segs;
   p.vec_a = g.K % 4 == 0;
   p.vec_b = (B_KN ? g.N : g.K) % 4 == 0;
-  p.vec_n = g.N % 4 == 0;
   const int n_tiles = (g.N + kTN - 1) / kTN;
   const long long m_tiles = (rows + S::TM - 1) / S::TM;
   // slices of at least 64 of K while the grid still fits the CTAs that

@@ -23,9 +23,9 @@
 #include <algorithm>
 #include <mutex>
 
-#include "activation.cuh"
 #include "internal.h"
 #include "linear.h"
+#include "linear_fp32.cuh"
 #include "ptx.cuh"
 #include "tc_common.cuh"
 
@@ -42,8 +42,9 @@ constexpr int kB = (kBN / 2) * BK * 2;  // this CTA's half of B, one K step
 constexpr int kStage = kA + kB;
 constexpr int kStages = 6;
 constexpr int kRing = kStages * kStage;
-constexpr int kBiasBytes = kEpiWarps * 64 * 4;
-constexpr int kSmem = kRing + kBiasBytes + 256;
+constexpr int kSlot = 32 * 16 * 4;  // an epilogue warp's 32 rows x 16 columns
+constexpr int kStaging = kEpiWarps * kSlot;
+constexpr int kSmem = kRing + kStaging + 256;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 constexpr uint32_t kTmemCols = 2 * kBN;
 constexpr int kGroupM = 8;
@@ -60,13 +61,11 @@ struct SplitArgs {
   int m_pairs, n_tiles, k_steps, N;
   int plane_rows_a, plane_rows_b;  // rows between planes of A, of B
   long long M;
-  int act;
-  bool vec;  // 16-byte output rows
-  const float* bias;
-  const float* residual;
-  float* y;
-  float* z;
-  const int* flags;  // [0]: of W, [1 + row]: of A's rows; not 0: left to linear_simt
+  Fp32Epilogue epi;
+  int segs;           // flags per row of A
+  long long b_flags;  // flags of B
+  int* flags;  // [0]: set here, whether any of B's; from 1: A's, then B's.  Rows
+               // with one that is not 0 are left to linear_simt
   int* status;
 };
 
@@ -76,36 +75,6 @@ __device__ __forceinline__ void unit_tile(int u, const SplitArgs& p, int& mp, in
   const int rows = min(kGroupM, p.m_pairs - g * kGroupM);
   mp = g * kGroupM + r % rows;
   nt = r / rows;
-}
-
-template <int ACT>
-__device__ __forceinline__ void act_all(float (&v)[16]) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = act_f<ACT, false>(v[j]);
-}
-
-__device__ __forceinline__ void apply_act(int act, float (&v)[16]) {
-  switch (act) {  // uniform over the grid
-    case POETX_ACT_RELU: act_all<POETX_ACT_RELU>(v); break;
-    case POETX_ACT_SILU: act_all<POETX_ACT_SILU>(v); break;
-    case POETX_ACT_GELU: act_all<POETX_ACT_GELU>(v); break;
-    case POETX_ACT_GELU_TANH: act_all<POETX_ACT_GELU_TANH>(v); break;
-    default: break;
-  }
-}
-
-// 16 values of a row at `at`, `live` of them inside.
-__device__ __forceinline__ void store16(float* out, long long at, const float (&v)[16], int live,
-                                        bool vec) {
-  if (vec && live >= 16) {
-#pragma unroll
-    for (int j = 0; j < 16; j += 4)
-      *reinterpret_cast<float4*>(out + at + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (j < live) out[at + j] = v[j];
-  }
 }
 
 template <bool B_MN>
@@ -118,8 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   uint8_t* ring = base;  // stage s: A (16 KiB), then this CTA's half of B
-  float* bias_s = reinterpret_cast<float*>(base + kRing);
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(base + kRing + kBiasBytes);  // leader
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(base + kRing + kStaging);  // leader
   uint64_t* empty_bar = full_bar + kStages;   // each CTA: its slot is free
   uint64_t* tfull_bar = empty_bar + kStages;  // [2] each CTA: accumulator ready
   uint64_t* tempty_bar = tfull_bar + 2;       // [2] leader: accumulator drained
@@ -160,7 +128,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
   pdl_trigger();
-  const int units = p.flags[0] != 0 ? 0 : p.m_pairs * p.n_tiles;
+  int bad = 0;
+  for (long long i = threadIdx.x; i < p.b_flags; i += kThreads)
+    bad |= p.flags[1 + p.M * p.segs + i];
+  bad = __syncthreads_or(bad);
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.flags[0] = bad;
+  const int units = bad != 0 ? 0 : p.m_pairs * p.n_tiles;
 
   const uint32_t full0 = map_peer(smem_u32(full_bar), 0);
   const uint32_t tempty0 = map_peer(smem_u32(tempty_bar), 0);
@@ -292,15 +265,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ew = warp - 2;
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
     const int side = ew >> 2;      // its quarter of the tile's columns
-    float* bias_w = bias_s + ew * 64;
+    float* slot = reinterpret_cast<float*>(base + kRing + ew * kSlot);
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int u = first; u < units && ok; u += step) {
       int mp, nt;
       unit_tile(u, p, mp, nt);
-      const long long row =
-          static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32 + lane;
+      const long long row0 = static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32;
       const int col0 = nt * kBN + side * 64;
       float sum[4][16] = {};
       for (int k0 = 0; k0 < p.k_steps; k0 += kChunkSteps) {
@@ -328,38 +300,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (acc == 0) acc_phase ^= 1;
       }
       if (!ok) break;
-      if (p.bias != nullptr) {
+      // this lane's row: outside, or left to linear_simt
+      int skip = row0 + lane >= p.M;
+      if (!skip)
+        for (int i = 0; i < p.segs; ++i) skip |= p.flags[1 + (row0 + lane) * p.segs + i];
+      // 16 columns at a time through the warp's staging tile, so that four lanes
+      // write 64 bytes of a row (pieces of 16 bytes xor-swizzled by the row)
+      // (one copy of the epilogue's code: sixteen unrolled ones, with every
+      // activation in each, cost 10 us of instruction fetches)
+#pragma unroll 1
+      for (int q = 0; q < 4 && col0 + q * 16 < p.N; ++q) {
         __syncwarp();
-        bias_w[lane] = col0 + lane < p.N ? __ldg(p.bias + col0 + lane) : 0.f;
-        bias_w[lane + 32] = col0 + lane + 32 < p.N ? __ldg(p.bias + col0 + lane + 32) : 0.f;
-        __syncwarp();
-      }
-      if (row >= p.M || p.flags[1 + row] != 0) continue;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int live = p.N - (col0 + q * 16);
-        if (live <= 0) break;
-        const long long at = row * p.N + col0 + q * 16;
-        float v[16];
+        for (int s = 0; s < 4; ++s)
+          if (s == q) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          v[j] = sum[q][j] + (p.bias != nullptr ? bias_w[q * 16 + j] : 0.f);
-        if (p.z != nullptr) store16(p.z, at, v, live, p.vec);
-        apply_act(p.act, v);
-        if (p.residual != nullptr) {
-          if (p.vec && live >= 16) {
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 r = *reinterpret_cast<const float4*>(p.residual + at + j);
-              v[j] += r.x, v[j + 1] += r.y, v[j + 2] += r.z, v[j + 3] += r.w;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (j < live) v[j] += p.residual[at + j];
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float4*>(slot + lane * 16 + ((j ^ (lane >> 1)) & 3) * 4) =
+                  make_float4(sum[s][4 * j], sum[s][4 * j + 1], sum[s][4 * j + 2],
+                              sum[s][4 * j + 3]);
           }
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + lane / 4, n = col0 + q * 16 + lane % 4 * 4;
+          const float4 v =
+              *reinterpret_cast<const float4*>(slot + r * 16 + ((lane % 4 ^ (r >> 1)) & 3) * 4);
+          const int no = __shfl_sync(0xffffffffu, skip, r);
+          if (no == 0 && n < p.N) finish4(p.epi, row0 + r, n, v);
         }
-        store16(p.y, at, v, live, p.vec);
       }
     }
   }
@@ -374,70 +343,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// in [rows][cols] fp32 -> planes [3][plane_rows][pitch] bf16, rows from `rows` to
-// plane_rows zero (columns past cols are not read by any tile).  Where a value's
-// planes are not finite, sets flag[r] (by_row) or flag[0].
+// One operand: in [rows][cols] fp32 -> planes [3][plane_rows][pitch] bf16, rows
+// from `rows` to plane_rows zero (columns past cols are not read by any tile);
+// flag[r][segs]: whether a value of the row's segment of kSegment columns has
+// planes that are not finite.
+constexpr int kSegment = 1024;
+
+struct SplitOperand {
+  const float* in;
+  bf16* planes;
+  int* flag;
+  long long rows, plane_rows, pitch;
+  int cols, segs;
+};
+
 constexpr int kSplitThreads = 256;
 
+// Both operands, a warp per segment of a row.
 __global__ void __launch_bounds__(kSplitThreads)
-    split_planes_kernel(const float* __restrict__ in, long long rows, int cols,
-                        bf16* __restrict__ planes, long long plane_rows, long long pitch,
-                        int* flag, bool by_row) {
+    split_planes_kernel(const SplitOperand a, const SplitOperand b) {
   pdl_wait();
   pdl_trigger();
-  const int quads = (cols + 3) / 4;
-  const bool vec = cols % 4 == 0;
-  // a warp per piece of 32 quads of a row
-  const int pieces = (quads + 31) / 32, lane = threadIdx.x % 32;
-  const long long items = plane_rows * pieces;
+  const int lane = threadIdx.x % 32;
+  const long long items_a = a.plane_rows * a.segs, items = items_a + b.plane_rows * b.segs;
   for (long long it = blockIdx.x * static_cast<long long>(kSplitThreads / 32) + threadIdx.x / 32;
        it < items; it += static_cast<long long>(gridDim.x) * (kSplitThreads / 32)) {
-    const long long r = it / pieces;
-    const int c = (static_cast<int>(it - r * pieces) * 32 + lane) * 4;
-    if (c >= cols) continue;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r < rows) {
-      if (vec) {
-        const float4 q = *reinterpret_cast<const float4*>(in + r * cols + c);
-        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c + j < cols) v[j] = in[r * cols + c + j];
-      }
-    }
+    const bool first = it < items_a;
+    const SplitOperand& o = first ? a : b;
+    const long long at = first ? it : it - items_a;
+    const long long r = at / o.segs;
+    const int c0 = static_cast<int>(at - r * o.segs) * kSegment;
+    const int c1 = min(o.cols, c0 + kSegment);
+    const float* in = o.in + r * o.cols;
+    const bool vec = o.cols % 4 == 0;
     bool bad = false;
-    uint32_t w[kPlanes][2];
+#pragma unroll 4
+    for (int c = c0 + lane * 4; c < c1; c += 128) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (r < o.rows) {
+        if (vec) {
+          const float4 q = *reinterpret_cast<const float4*>(in + c);
+          v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        } else {
 #pragma unroll
-    for (int s = 0; s < kPlanes; ++s) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * h], v[2 * h + 1]);
-        const float2 f = __bfloat1622float2(b);
-        if (s == 0) bad |= !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
-        v[2 * h] -= f.x;  // exact: the rounding error of a bf16 rounding
-        v[2 * h + 1] -= f.y;
-        w[s][h] = *reinterpret_cast<const uint32_t*>(&b);
+          for (int j = 0; j < 4; ++j)
+            if (c + j < o.cols) v[j] = in[c + j];
+        }
       }
-      // rows are a multiple of 8 elements apart: 8 bytes fit, padding included
-      *reinterpret_cast<uint2*>(planes + (s * plane_rows + r) * pitch + c) =
-          make_uint2(w[s][0], w[s][1]);
+#pragma unroll
+      for (int s = 0; s < kPlanes; ++s) {
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * h], v[2 * h + 1]);
+          const float2 f = __bfloat1622float2(q);
+          if (s == 0) bad |= !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
+          v[2 * h] -= f.x;  // exact: the rounding error of a bf16 rounding
+          v[2 * h + 1] -= f.y;
+          w[h] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+        // rows are a multiple of 64 elements apart: 8 bytes fit, padding included
+        *reinterpret_cast<uint2*>(o.planes + (s * o.plane_rows + r) * o.pitch + c) =
+            make_uint2(w[0], w[1]);
+      }
     }
-    if (bad) flag[by_row ? r : 0] = 1;  // whoever writes it writes 1
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) o.flag[at] = bad;
   }
-}
-
-cudaError_t split_planes(const void* in, long long rows, int cols, void* planes,
-                         long long plane_rows, int* flag, bool by_row, cudaStream_t s) {
-  const long long items = plane_rows * (((cols + 3) / 4 + 31) / 32);
-  const int grid = static_cast<int>(std::min<long long>((items + 7) / 8, 16ll * sm_count()));
-  prof_begin("linear_split_planes", s);
-  const cudaError_t e = launch_pdl(split_planes_kernel, dim3(grid), dim3(kSplitThreads), 0, s,
-                                   static_cast<const float*>(in), rows, cols,
-                                   static_cast<bf16*>(planes), plane_rows,
-                                   static_cast<long long>((cols + 7) / 8 * 8), flag, by_row);
-  prof_end("linear_split_planes", s);
-  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -449,13 +421,19 @@ long long b_plane_rows(const LinearProduct& g) {
 
 int b_cols(const LinearProduct& g) { return g.b_mn ? g.N : g.K; }
 
+// Rows of planes start on 128 bytes: rows of 2000 bytes made the loads a third
+// slower than the products (1000^3: 750 cycles a step instead of 512).
+long long pitch64(int cols) { return (static_cast<long long>(cols) + 63) / 64 * 64; }
+
+int segments(int cols) { return (cols + kSegment - 1) / kSegment; }
+
 size_t planes_bytes(long long plane_rows, int cols) {
-  return round256(static_cast<size_t>(kPlanes) * plane_rows * ((cols + 7) / 8 * 8) * 2);
+  return round256(static_cast<size_t>(kPlanes) * plane_rows * pitch64(cols) * 2);
 }
 
 template <bool B_MN>
 cudaError_t launch(const LinearProduct& g, const void* a_planes, const void* b_planes,
-                   const int* flags, cudaStream_t stream) {
+                   int* flags, cudaStream_t stream) {
   auto* kernel = linear_split_kernel<B_MN>;
   static bool ready[64] = {false};
   static int max_clusters[64] = {0};
@@ -497,23 +475,20 @@ cudaError_t launch(const LinearProduct& g, const void* a_planes, const void* b_p
   p.plane_rows_a = static_cast<int>(g.M);
   p.plane_rows_b = static_cast<int>(b_plane_rows(g));
   CUtensorMap tmA, tmB;
-  if (!make_map(&tmA, a_planes, kPlanes * g.M, g.K, (g.K + 7) / 8 * 8, 2, 64, BM))
+  if (!make_map(&tmA, a_planes, kPlanes * g.M, g.K, pitch64(g.K), 2, 64, BM))
     return cudaErrorInvalidValue;
-  if (!make_map(&tmB, b_planes, kPlanes * b_plane_rows(g), b_cols(g), (b_cols(g) + 7) / 8 * 8, 2,
-                64, B_MN ? 64 : kBN / 2))
+  if (!make_map(&tmB, b_planes, kPlanes * b_plane_rows(g), b_cols(g), pitch64(b_cols(g)), 2, 64,
+                B_MN ? 64 : kBN / 2))
     return cudaErrorInvalidValue;
   p.m_pairs = static_cast<int>((g.M + 2 * BM - 1) / (2 * BM));
   p.n_tiles = (g.N + kBN - 1) / kBN;
   p.k_steps = (g.K + BK - 1) / BK;
   p.N = g.N;
   p.M = g.M;
-  p.act = g.act;
-  p.vec = g.N % 4 == 0;
-  p.bias = g.bias;
-  p.residual = static_cast<const float*>(g.residual);
-  p.y = static_cast<float*>(g.y);
-  p.z = static_cast<float*>(g.z);
+  p.epi = fp32_epilogue(g, 0);
   p.flags = flags;
+  p.segs = segments(g.K);
+  p.b_flags = b_plane_rows(g) * segments(b_cols(g));
   p.status = device_status_ptr();
   const int clusters = static_cast<int>(
       std::min<long long>(static_cast<long long>(p.m_pairs) * p.n_tiles, cmax));
@@ -537,25 +512,52 @@ bool linear_split_pays(long long M, int N, int K) {
   return split < simt;
 }
 
+namespace {
+
+size_t flag_bytes(const LinearProduct& g) {
+  return round256(
+      static_cast<size_t>(1 + g.M * segments(g.K) + b_plane_rows(g) * segments(b_cols(g))) *
+      sizeof(int));
+}
+
+}  // namespace
+
 size_t linear_split_scratch(const LinearProduct& g) {
-  return round256(static_cast<size_t>(1 + g.M) * sizeof(int)) + planes_bytes(g.M, g.K) +
-         planes_bytes(b_plane_rows(g), b_cols(g));
+  return flag_bytes(g) + planes_bytes(g.M, g.K) + planes_bytes(b_plane_rows(g), b_cols(g));
 }
 
 cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) {
+  SplitOperand a, b;
   int* flags = static_cast<int*>(scratch);
-  const size_t flag_bytes = static_cast<size_t>(1 + g.M) * sizeof(int);
-  char* a = static_cast<char*>(scratch) + round256(flag_bytes);
-  char* b = a + planes_bytes(g.M, g.K);
-  cudaError_t e = cudaMemsetAsync(flags, 0, flag_bytes, s);
+  char* at = static_cast<char*>(scratch) + flag_bytes(g);
+  a.in = static_cast<const float*>(g.A);
+  a.planes = reinterpret_cast<bf16*>(at);
+  a.flag = flags + 1;
+  a.rows = a.plane_rows = g.M;
+  a.cols = g.K;
+  a.segs = segments(a.cols);
+  a.pitch = pitch64(a.cols);
+  b.in = static_cast<const float*>(g.B);
+  b.planes = reinterpret_cast<bf16*>(at + planes_bytes(g.M, g.K));
+  b.flag = flags + 1 + g.M * segments(g.K);
+  b.rows = g.b_mn ? g.K : g.N;
+  b.plane_rows = b_plane_rows(g);
+  b.cols = b_cols(g);
+  b.segs = segments(b.cols);
+  b.pitch = pitch64(b.cols);
+  const int grid = static_cast<int>(
+      std::min<long long>((a.plane_rows * a.segs + b.plane_rows * b.segs + 7) / 8, 8ll * sm_count()));
+  prof_begin("linear_split_planes", s);
+  cudaError_t e = launch_pdl(split_planes_kernel, dim3(grid), dim3(kSplitThreads), 0, s, a, b);
+  prof_end("linear_split_planes", s);
   if (e != cudaSuccess) return e;
-  if ((e = split_planes(g.A, g.M, g.K, a, g.M, flags + 1, true, s)) != cudaSuccess) return e;
-  e = split_planes(g.B, g.b_mn ? g.K : g.N, b_cols(g), b, b_plane_rows(g), flags, false, s);
-  if (e != cudaSuccess) return e;
-  e = g.b_mn ? launch<true>(g, a, b, flags, s) : launch<false>(g, a, b, flags, s);
+  e = g.b_mn ? launch<true>(g, a.planes, b.planes, flags, s)
+             : launch<false>(g, a.planes, b.planes, flags, s);
   if (e != cudaSuccess) return e;
   LinearProduct again = g;
   again.flags = flags;
+  again.segs = a.segs;
+  again.tag = "linear_rows";
   return linear_simt(again, s);
 }
 
