@@ -16,9 +16,9 @@
 // this kernel leaves those rows alone and linear_simt, enqueued behind it,
 // computes them; its tiles without such rows return at once.
 //
-// The kernel is linear_pair's with another epilogue: CTA pairs, 256 x 256
-// tiles, 64-wide K steps in a ring of six 32 KiB stages, one step per pair of
-// planes; 16 epilogue warps (64 columns each) drain one of two TMEM
+// The kernel is linear_pair's with another epilogue: CTA pairs, 256 x 256 or
+// 256 x 128 tiles, 64-wide K steps in a TMA ring, one step per pair of planes;
+// 16 epilogue warps (a quarter of the columns each) drain one of two TMEM
 // accumulators into registers while the next 128 of K go into the other.
 #include <algorithm>
 #include <mutex>
@@ -36,17 +36,22 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kBN = 256;
-constexpr int kA = BM * BK * 2;         // this CTA's 128 rows, one K step
-constexpr int kB = (kBN / 2) * BK * 2;  // this CTA's half of B, one K step
-constexpr int kStage = kA + kB;
-constexpr int kStages = 6;
-constexpr int kRing = kStages * kStage;
+constexpr int kA = BM * BK * 2;     // this CTA's 128 rows, one K step
 constexpr int kSlot = 32 * 16 * 4;  // an epilogue warp's 32 rows x 16 columns
 constexpr int kStaging = kEpiWarps * kSlot;
-constexpr int kSmem = kRing + kStaging + 256;
-static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-constexpr uint32_t kTmemCols = 2 * kBN;
+
+template <int BN>
+struct Shape {
+  static constexpr int B = (BN / 2) * BK * 2;  // this CTA's half of B, one K step
+  static constexpr int STAGE = kA + B;
+  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int SMEM = RING + kStaging + 256;
+  static constexpr uint32_t TMEM_COLS = 2 * BN;
+  static constexpr int COLS = BN / 4;  // columns of an epilogue warp
+  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+
 constexpr int kGroupM = 8;
 constexpr int kPlanes = 3;
 constexpr int kProducts = 6;
@@ -77,10 +82,12 @@ __device__ __forceinline__ void unit_tile(int u, const SplitArgs& p, int& mp, in
   nt = r / rows;
 }
 
-template <bool B_MN>
+template <int BN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB, const SplitArgs p) {
+  using S = Shape<BN>;
+  constexpr int kStages = S::STAGES, kStage = S::STAGE, kRing = S::RING, kBN = BN;
   extern __shared__ __align__(1024) uint8_t base[];  // 128B-swizzled tiles start on 1024 bytes
   if ((smem_u32(base) & 1023u) != 0) {  // the declared alignment, which the tiles rely on
     if (threadIdx.x == 0) atomicCAS(p.status, 0, static_cast<int>(POETX_ERR_CUDA));
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -171,7 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_2d_pair(b_dst, &tmB, bar, ks * BK, rb + b_n);
               } else {
                 tma_load_2d_pair(b_dst, &tmB, bar, b_n, rb + ks * BK);
-                tma_load_2d_pair(b_dst + 8192, &tmB, bar, b_n + 64, rb + ks * BK);
+                if (BN == 256)
+                  tma_load_2d_pair(b_dst + 8192, &tmB, bar, b_n + 64, rb + ks * BK);
               }
             }
             __syncwarp();
@@ -273,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int mp, nt;
       unit_tile(u, p, mp, nt);
       const long long row0 = static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32;
-      const int col0 = nt * kBN + side * 64;
-      float sum[4][16] = {};
+      const int col0 = nt * kBN + side * S::COLS;
+      float sum[S::COLS / 16][16] = {};
       for (int k0 = 0; k0 < p.k_steps; k0 += kChunkSteps) {
         const bool got = mbar_wait_cluster(&tfull_bar[acc], acc_phase, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
@@ -284,9 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t t_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                static_cast<uint32_t>(acc * kBN + side * 64);
+                                static_cast<uint32_t>(acc * kBN + side * S::COLS);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < S::COLS / 16; ++q) {
           uint32_t r[16];
           tmem_load_16(t_base + q * 16, r);
 #pragma unroll
@@ -309,10 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (one copy of the epilogue's code: sixteen unrolled ones, with every
       // activation in each, cost 10 us of instruction fetches)
 #pragma unroll 1
-      for (int q = 0; q < 4 && col0 + q * 16 < p.N; ++q) {
+      for (int q = 0; q < S::COLS / 16 && col0 + q * 16 < p.N; ++q) {
         __syncwarp();
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < S::COLS / 16; ++s)
           if (s == q) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, kTmemCols);
+    tmem_dealloc_pair(tmem_base, S::TMEM_COLS);
   }
 }
 
@@ -431,10 +439,11 @@ size_t planes_bytes(long long plane_rows, int cols) {
   return round256(static_cast<size_t>(kPlanes) * plane_rows * pitch64(cols) * 2);
 }
 
-template <bool B_MN>
+template <int BN, bool B_MN>
 cudaError_t launch(const LinearProduct& g, const void* a_planes, const void* b_planes,
                    int* flags, cudaStream_t stream) {
-  auto* kernel = linear_split_kernel<B_MN>;
+  constexpr int kSmem = Shape<BN>::SMEM, kBN = BN;
+  auto* kernel = linear_split_kernel<BN, B_MN>;
   static bool ready[64] = {false};
   static int max_clusters[64] = {0};
   static std::mutex mu;
@@ -502,14 +511,29 @@ cudaError_t launch(const LinearProduct& g, const void* a_planes, const void* b_p
 
 }  // namespace
 
+namespace {
+
+// Microseconds of the products' main loops: a 64-wide step of the six products
+// takes 1.71 us in a 256-wide tile, 1.12 in a 128-wide one (see linear_pair),
+// which pays where it fills idle clusters.
+double loop_us(long long M, int N, int K, bool* narrow) {
+  const long long m_pairs = (M + 2 * BM - 1) / (2 * BM), clusters = std::max(1, sm_count() / 2);
+  const long long wide = (m_pairs * ((N + 255) / 256) + clusters - 1) / clusters;
+  const long long thin = (m_pairs * ((N + 127) / 128) + clusters - 1) / clusters;
+  *narrow = 1.12 * thin < 1.71 * wide;
+  return (*narrow ? 1.12 * thin : 1.71 * wide) * ((K + BK - 1) / BK);
+}
+
+}  // namespace
+
+// By the measured costs of both: here the loops above, 18 us for three launches
+// and the pipeline's ends, and 10 bytes per element of the operands for their
+// planes; linear_simt 8 us and 45 TFLOP/s.  They cross near 1000^3.
 bool linear_split_pays(long long M, int N, int K) {
-  if (M > (1ll << 24)) return false;
-  const long long units = ((M + 255) / 256) * ((N + 255) / 256);
-  const long long clusters = std::max(1, sm_count() / 2);
-  const double split = 16.0 + 1.75 * ((K + 63) / 64) * ((units + clusters - 1) / clusters) +
-                       10e-6 * K * (static_cast<double>(M) + N) / 6.0;
-  const double simt = 8.0 + 2e-6 * M * N * K / 45.0;
-  return split < simt;
+  bool narrow;
+  const double split =
+      18.0 + loop_us(M, N, K, &narrow) + 10e-6 * K * (static_cast<double>(M) + N) / 6.0;
+  return split < 8.0 + 2e-6 * M * N * K / 45.0;
 }
 
 namespace {
@@ -551,8 +575,12 @@ cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) 
   cudaError_t e = launch_pdl(split_planes_kernel, dim3(grid), dim3(kSplitThreads), 0, s, a, b);
   prof_end("linear_split_planes", s);
   if (e != cudaSuccess) return e;
-  e = g.b_mn ? launch<true>(g, a.planes, b.planes, flags, s)
-             : launch<false>(g, a.planes, b.planes, flags, s);
+  bool narrow;
+  loop_us(g.M, g.N, g.K, &narrow);
+  e = narrow ? g.b_mn ? launch<128, true>(g, a.planes, b.planes, flags, s)
+                      : launch<128, false>(g, a.planes, b.planes, flags, s)
+      : g.b_mn ? launch<256, true>(g, a.planes, b.planes, flags, s)
+               : launch<256, false>(g, a.planes, b.planes, flags, s);
   if (e != cudaSuccess) return e;
   LinearProduct again = g;
   again.flags = flags;
