@@ -263,8 +263,11 @@ poetx_status poetx_dequantize_w0(const int8_t* W0_q, const float* scales, void* 
  *   NONE.  dx or dbias may be NULL.  RELU'(0) = 0.
  * GELU is z Phi(z); GELU_TANH its tanh approximation
  *   z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).
- * 1 <= d_in, d_out <= 2^20, any values (rows of BF16 features that are not a
- * multiple of 8 take a slower path).
+ * 1 <= d_in, d_out <= 2^20, any values (BF16 rows that are not a multiple of
+ * 8 features are copied to aligned rows first).
+ * F32 accumulates in fp32; large products run on the tensor cores, each
+ * operand as three bf16 parts (24 bits), tokens or weights with values that
+ * are not finite on the CUDA cores.
  * ------------------------------------------------------------------------ */
 typedef enum {
   POETX_ACT_NONE = 0,
