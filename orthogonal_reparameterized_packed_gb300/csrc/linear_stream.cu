@@ -303,17 +303,30 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
   }
 }
 
-// Slices of K: as many as keep every cluster resident at one time, each with
-// at least four K steps.  Clusters of eight do not fill the GPU's processing
-// clusters, so CTAs alone do not tell (2048 -> 2048 features, T = 256: 8 slices
-// ran in two waves, 19.2 us; 4 take 10.0).  Slices of 16 steps and more hide a
-// few clusters too many (14336 -> 4096, T = 1: 8 slices 20.4, 4 slices 21.6 us).
-int split_count(long long tiles, int k_steps, const int (&most)[4]) {
-  int i = 0;
-  while (i < 3 && k_steps >= 8 << i &&
-         (tiles <= most[i + 1] || (4 * tiles <= 5 * most[i + 1] && k_steps >= 32 << i)))
-    ++i;
-  return 1 << i;
+// Slices of K.  Two CTAs share an SM where BT <= 128: up to 7/4 CTAs per SM
+// (4096 -> 14336 features, one token: 112 / 224 / 448 CTAs take 21.5 / 20.8 / 22.8
+// us; 14336 -> 4096: 128 / 256 CTAs 21.4 / 20.4; 2048 -> 5632: 88 / 176 / 352
+// CTAs 7.2 / 6.8 / 10.2).  The closing sum costs by BT: a slice has at least
+// four K steps, eight for BT = 128 (2048 -> 2048: 9.1 with four, 7.7 with eight),
+// and beyond one CTA per SM eight, sixteen for BT >= 64 (4096 -> 4096, T = 128:
+// 13.5 with eight, 12.1 in half as many slices).  One CTA per SM (BT = 256): as
+// long as every cluster is resident at one time; clusters of eight do not fill
+// the GPU's processing clusters (2048 -> 2048, T = 256: 8 slices ran in two waves,
+// 19.2 us; 4 take 10.0).
+int split_count(long long tiles, int k_steps, int bt, const int (&most)[4]) {
+  int s = 1;
+  for (int i = 1; i < 4; ++i) {
+    const int next = 2 * s, per_slice = k_steps / next;
+    const long long ctas = tiles * next;
+    if (bt > 128) {
+      if (per_slice < 4 || tiles > most[i]) break;
+    } else {
+      if (per_slice < (bt >= 128 ? 8 : 4) || 4 * ctas > 7ll * sm_count()) break;
+      if (ctas > sm_count() && per_slice < (bt >= 64 ? 16 : 8)) break;
+    }
+    s = next;
+  }
+  return s;
 }
 
 template <int BT, bool A_MN>
@@ -372,7 +385,7 @@ cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
   p.status = device_status_ptr();
   const int n_tiles = (g.N + BM - 1) / BM;
   const long long t_tiles = (g.M + BT - 1) / BT;
-  p.splits = split_count(n_tiles * t_tiles, p.k_steps, most[dev]);
+  p.splits = split_count(n_tiles * t_tiles, p.k_steps, BT, most[dev]);
   cfg.gridDim = dim3(static_cast<unsigned>(n_tiles * p.splits), static_cast<unsigned>(t_tiles));
   attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
   cfg.numAttrs = 2;
