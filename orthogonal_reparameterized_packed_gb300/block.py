@@ -174,8 +174,8 @@ class PoetxQKNormRope:
         k_at, ld_k = self._rows(k, self.hk, t, "k") if self.hk else (None, 0)
         _check("poetx_qk_norm_rope_forward", self._fwd(
             q_at, k_at, gq, gk, c, s, pos, self.q_out.data_ptr(), self.k_out.data_ptr(), ld_q,
-            ld_k, self._wq, self._wk, self.hq, self.hk, self.D, self.rot, rows, self.interleaved, self.eps, t,
-            self.code, _stream(stream)))
+            ld_k, self._wq, self._wk, self.hq, self.hk, self.D, self.rot, rows,
+            self.interleaved, self.eps, t, self.code, _stream(stream)))
         return self._cut(self.q_out, t), self._cut(self.k_out, t)
 
     def backward(self, dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, positions=None,
@@ -206,7 +206,8 @@ def _need_list(tensors, others, dtypes, name):
     """Contiguous CUDA tensors of the types; `others` (or None) of the same sizes and types."""
     if not ({t.dtype for t in tensors} <= dtypes and
             all(map(torch.Tensor.is_contiguous, tensors)) and all(t.is_cuda for t in tensors)):
-        raise ValueError(f"{name}: contiguous CUDA tensors of {sorted(map(str, dtypes))} are needed")
+        raise ValueError(
+            f"{name}: contiguous CUDA tensors of {sorted(map(str, dtypes))} are needed")
     if others is not None:
         _need_list(others, None, dtypes, "out")
         if [(t.numel(), t.dtype) for t in tensors] != [(t.numel(), t.dtype) for t in others]:

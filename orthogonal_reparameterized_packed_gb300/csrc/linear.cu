@@ -154,7 +154,8 @@ cudaError_t pad_rows(const void* in, void* out, long long rows, int cols, cudaSt
   prof_begin("linear_pad", s);
   const cudaError_t e =
       launch_pdl(pad_rows_kernel, dim3(grid), dim3(kThreads), 0, s, static_cast<const bf16*>(in),
-                 static_cast<long long>(cols), static_cast<bf16*>(out), tma_pitch(cols), rows, cols);
+                 static_cast<long long>(cols), static_cast<bf16*>(out), tma_pitch(cols), rows,
+                 cols);
   prof_end("linear_pad", s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

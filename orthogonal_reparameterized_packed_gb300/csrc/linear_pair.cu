@@ -512,7 +512,8 @@ cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
       cfg.gridDim = dim3(2 * sm_count());
       cfg.numAttrs = 1;

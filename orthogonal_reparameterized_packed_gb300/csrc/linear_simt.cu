@@ -54,20 +54,6 @@ struct Shape {
   static constexpr int SMEM = 2 * STAGE > PART ? 2 * STAGE : PART;
 };
 
-typedef unsigned long long f32x2;
-
-__device__ __forceinline__ f32x2 pair_of(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void split_pair(f32x2 p, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
-}
-__device__ __forceinline__ void fma_pair(f32x2& acc, f32x2 a, f32x2 b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
-}
-
 // Four consecutive floats at row r, from column c, of a [rows][cols] array;
 // zeros outside.
 __device__ __forceinline__ float4 load4(const float* p, long long r, long long rows, int c,
@@ -223,9 +209,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
       }
 #pragma unroll
       for (int i = 0; i < RM; ++i) {
-        const f32x2 aa = pair_of(a[i], a[i]);
+        const f32x2 aa = f32x2_of(a[i], a[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) fma_pair(acc[i][j], aa, b[j]);
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x2_fma(aa, b[j], acc[i][j]);
       }
     }
     buf ^= 1;
@@ -241,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[4];
-        split_pair(acc[i][2 * h], v[0], v[1]);
-        split_pair(acc[i][2 * h + 1], v[2], v[3]);
+        f32x2_split(acc[i][2 * h], v[0], v[1]);
+        f32x2_split(acc[i][2 * h + 1], v[2], v[3]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           v[j] += __shfl_xor_sync(0xffffffffu, v[j], 8);
@@ -270,8 +256,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float4 v;
-        split_pair(acc[i][2 * h], v.x, v.y);
-        split_pair(acc[i][2 * h + 1], v.z, v.w);
+        f32x2_split(acc[i][2 * h], v.x, v.y);
+        f32x2_split(acc[i][2 * h + 1], v.z, v.w);
         *reinterpret_cast<float4*>(smem + row_of(i) * kLdb + h * 64 + tx * 4) = v;
       }
   }

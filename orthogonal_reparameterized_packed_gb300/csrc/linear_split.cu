@@ -570,7 +570,8 @@ cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) 
   b.segs = segments(b.cols);
   b.pitch = pitch64(b.cols);
   const int grid = static_cast<int>(
-      std::min<long long>((a.plane_rows * a.segs + b.plane_rows * b.segs + 7) / 8, 8ll * sm_count()));
+      std::min<long long>((a.plane_rows * a.segs + b.plane_rows * b.segs + 7) / 8,
+                          8ll * sm_count()));
   prof_begin("linear_split_planes", s);
   cudaError_t e = launch_pdl(split_planes_kernel, dim3(grid), dim3(kSplitThreads), 0, s, a, b);
   prof_end("linear_split_planes", s);

@@ -12,14 +12,15 @@
 //
 // A row is cut into slots of two V-element vectors that hold whole pairs, so
 // no lane needs another's elements to rotate; the G lanes of a row share only
-// the sums, and a warp works on 32 / G heads of a token at once.  A warp goes
-// through the heads of its token with the table row and gamma in registers
-// (few tokens: through a part of them, so that every SM has work).  What
-// bounds it is memory traffic: 2 (forward) or 3 (backward) passes over q and k.
+// the sums, and a warp works on 32 / G heads of a token at once: a group.  What
+// bounds it is memory traffic, 2 (forward) or 3 (backward) passes over q and k:
+// 16384 tokens of 40 heads of 128, bf16, take 55.5 us forward (6.0 TB/s) and 88
+// backward (5.7), in fp32 half as many tokens 54 and 85.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "poetx.h"
@@ -79,10 +80,11 @@ __device__ __forceinline__ Pack<T, V> pack(const float (&v)[V]) {
   return q;
 }
 
-// Slot s of a row: the vectors at o0 and o1; `turns`: its pairs are rotated,
-// with the trigonometric entries [s V, s V + V).
+// Slot s of a row: the vectors at o0 and o1, apart by half of the rotated part,
+// so that the lanes' vectors are next to each other; `turns`: its pairs are
+// rotated, with V table entries from e0 and e1, a half of them each.
 struct Slot {
-  int o0, o1;
+  int o0, o1, e0, e1;
   bool turns, has0, has1;
 };
 
@@ -93,30 +95,85 @@ __device__ __forceinline__ Slot slot_of(int s, int D, int rot) {
   const int nrot = rot / 2 / V;
   w.turns = FULL || s < nrot;
   if (w.turns) {
-    w.o0 = INTER ? 2 * s * V : s * V;
-    w.o1 = INTER ? w.o0 + V : rot / 2 + s * V;
+    const bool pair = INTER && V == 1;
+    w.o0 = pair ? 2 * s : s * V;
+    w.o1 = pair ? 2 * s + 1 : rot / 2 + s * V;
+    w.e0 = INTER ? w.o0 / 2 : w.o0;
+    w.e1 = INTER ? w.o1 / 2 : w.o0 + V / 2;
   } else {
     w.o0 = rot + (s - nrot) * 2 * V;
     w.o1 = w.o0 + V;
+    w.e0 = w.e1 = 0;
   }
   w.has0 = FULL || w.o0 < D;
   w.has1 = FULL || w.o1 < D;
   return w;
 }
 
-// Where value j of the slot's first (b = 0) or second vector finds its pair:
-// half by half, value j of the other vector; interleaved vectors hold whole
-// pairs, (2i, 2i + 1), the first vector's with table entries [0, V/2) and the
-// second's with [V/2, V).
-template <int V, bool INTER>
-struct Pairs {
-  static constexpr bool ADJACENT = INTER && V > 1;  // V = 1: a slot is one pair either way
-  // table entry of pair i = 0 .. V - 1, and its two members' (vector, value)
-  static constexpr int vec_a(int i) { return ADJACENT ? (i >= V / 2) : 0; }
-  static constexpr int vec_b(int i) { return ADJACENT ? (i >= V / 2) : 1; }
-  static constexpr int at_a(int i) { return ADJACENT ? 2 * (i % (V / 2 > 0 ? V / 2 : 1)) : i; }
-  static constexpr int at_b(int i) { return ADJACENT ? at_a(i) + 1 : i; }
+// A slot's values as the arithmetic holds them: V pairs, members a and b apart,
+// two pairs to a register pair (fma.rn.f32x2; singly for V = 1).  Half by half, a
+// is the slot's first vector and b its second; interleaved, the vectors hold
+// whole pairs (a0 b0 a1 b1 ..).
+template <int V>
+struct Vals {
+  using E = std::conditional_t<(V > 1), f32x2, float>;
+  static constexpr int N = V > 1 ? V / 2 : 1;
+  E a[N], b[N];
 };
+
+__device__ __forceinline__ void join(f32x2& o, float lo, float hi) { o = f32x2_of(lo, hi); }
+__device__ __forceinline__ void join(float& o, float lo, float) { o = lo; }
+__device__ __forceinline__ void part(f32x2 v, float& lo, float& hi) { f32x2_split(v, lo, hi); }
+__device__ __forceinline__ void part(float v, float& lo, float&) { lo = v; }
+__device__ __forceinline__ f32x2 mul(f32x2 a, f32x2 b) { return f32x2_mul(a, b); }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ f32x2 mad(f32x2 a, f32x2 b, f32x2 c) { return f32x2_fma(a, b, c); }
+__device__ __forceinline__ float mad(float a, float b, float c) { return fmaf(a, b, c); }
+template <typename E>
+__device__ __forceinline__ E both(float x) {
+  E o;
+  join(o, x, x);
+  return o;
+}
+__device__ __forceinline__ float total(f32x2 v) {
+  float lo, hi;
+  f32x2_split(v, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ float total(float v) { return v; }
+
+// The two vectors of a slot as values, and back.
+template <int V, bool INTER>
+__device__ __forceinline__ Vals<V> values(const float (&x)[2][V]) {
+  Vals<V> o;
+  auto at = [&](int i) { return i < V ? x[0][i] : x[1][i - V]; };  // of both, end to end
+#pragma unroll
+  for (int j = 0; j < Vals<V>::N; ++j) {
+    if (INTER) {
+      join(o.a[j], at(4 * j), V > 1 ? at(4 * j + 2) : 0.f);
+      join(o.b[j], at(4 * j + 1), V > 1 ? at(4 * j + 3) : 0.f);
+    } else {
+      join(o.a[j], at(2 * j), V > 1 ? at(2 * j + 1) : 0.f);
+      join(o.b[j], at(V + 2 * j), V > 1 ? at(V + 2 * j + 1) : 0.f);
+    }
+  }
+  return o;
+}
+template <int V, bool INTER>
+__device__ __forceinline__ void vectors(float (&x)[2][V], const Vals<V>& o) {
+  auto at = [&](int i) -> float& { return i < V ? x[0][i] : x[1][i - V]; };
+  float unused;
+#pragma unroll
+  for (int j = 0; j < Vals<V>::N; ++j) {
+    if (INTER) {
+      part(o.a[j], at(4 * j), V > 1 ? at(4 * j + 2) : unused);
+      part(o.b[j], at(4 * j + 1), V > 1 ? at(4 * j + 3) : unused);
+    } else {
+      part(o.a[j], at(2 * j), V > 1 ? at(2 * j + 1) : unused);
+      part(o.b[j], at(V + 2 * j), V > 1 ? at(V + 2 * j + 1) : unused);
+    }
+  }
+}
 
 // V floats; V >= 4: from a 16-byte aligned address.
 template <int V>
@@ -135,15 +192,16 @@ __device__ __forceinline__ void load_f32(float (&o)[V], const float* p) {
 
 // The next rows of a warp on their way to shared memory while it works on the
 // current ones: STAGES groups of N vectors per lane.  Every lane copies and
-// reads only its own vectors, so the ring needs no barrier.  (It is the bytes
-// in flight that bound these kernels: with the next group in registers
-// instead, 126 of them left 16 warps per SM and the backward pass at 3.9 TB/s.)
-// Vectors of two bytes cannot be copied this way and are read when needed.
+// reads only its own vectors, so the ring needs no barrier.  Two groups of 16
+// warps keep the memory busy; four are slower (16384 x 40 heads of 128: forward
+// 62 against 55.5 us, backward 97.6 against 88), as are the next group in
+// registers and 24 warps of 80 registers (forward 83).  Vectors of two bytes
+// cannot be copied this way and are read when needed.
 template <typename T, int V, int N>
 struct Rows {
   static constexpr int BYTES = sizeof(T) * V;
   static constexpr bool ASYNC = BYTES >= 4;
-  static constexpr int STAGES = !ASYNC ? 1 : N * BYTES <= 64 ? 4 : 2;
+  static constexpr int STAGES = ASYNC ? 2 : 1;
   static constexpr int SMEM = ASYNC ? kWarps * STAGES * N * 32 * BYTES : 0;  // of a CTA
 
   uint32_t base;         // this lane's first vector
@@ -174,11 +232,11 @@ struct Rows {
     }
   }
   __device__ __forceinline__ static void commit() {
-    if constexpr (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
   // The oldest of the STAGES groups has arrived.
   __device__ __forceinline__ static void wait() {
-    if constexpr (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
   }
   __device__ __forceinline__ void read(int stage, int n, float (&o)[V]) const {
     Pack<T, V> q;
@@ -206,24 +264,49 @@ struct Rows {
 };
 
 // gamma's values of a slot (ones where there is no gamma).
-template <int V>
-__device__ __forceinline__ void load_gamma(float (&m)[2][V], const float* gamma, const Slot& w) {
+template <int V, bool INTER>
+__device__ __forceinline__ Vals<V> load_gamma(const float* gamma, const Slot& w) {
+  float m[2][V];
 #pragma unroll
   for (int i = 0; i < V; ++i) m[0][i] = m[1][i] = 1.f;
-  if (gamma == nullptr) return;
-  if (w.has0) load_f32<V>(m[0], gamma + w.o0);
-  if (w.has1) load_f32<V>(m[1], gamma + w.o1);
+  if (gamma != nullptr) {
+    if (w.has0) load_f32<V>(m[0], gamma + w.o0);
+    if (w.has1) load_f32<V>(m[1], gamma + w.o1);
+  }
+  return values<V, INTER>(m);
 }
 
-// The slot's table entries of row tr (1 and 0 where nothing turns).
+// A slot's table entries (1 and 0 where nothing turns).
 template <int V>
-__device__ __forceinline__ void load_trig(float (&c)[V], float (&s)[V], const QkNormRopeArgs& a,
-                                          long long tr, int slot, const Slot& w) {
+struct Trig {
+  using E = typename Vals<V>::E;
+  static constexpr int N = Vals<V>::N;
+  E c[N], s[N];
+};
+
+// cos, sin: the token's rows in shared memory.
+template <int V>
+__device__ __forceinline__ Trig<V> load_trig(const float* cos, const float* sin, const Slot& w) {
+  constexpr int H = V > 1 ? V / 2 : 1;
+  float c[V], s[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) c[i] = 1.f, s[i] = 0.f;
-  if (!w.turns) return;
-  load_f32<V>(c, a.cos_table + tr * (a.rot / 2) + slot * V);
-  load_f32<V>(s, a.sin_table + tr * (a.rot / 2) + slot * V);
+  if (w.turns) {
+#pragma unroll
+    for (int i = 0; i < V; i += H) {
+      const int e = i == 0 ? w.e0 : w.e1;
+      memcpy(c + i, __builtin_assume_aligned(cos + e, 4 * H), 4 * H);
+      memcpy(s + i, __builtin_assume_aligned(sin + e, 4 * H), 4 * H);
+    }
+  }
+  Trig<V> t;
+#pragma unroll
+  for (int j = 0; j < Trig<V>::N; ++j) {
+    constexpr int H = V > 1 ? 1 : 0;  // the second of two pairs
+    join(t.c[j], c[2 * j], c[2 * j + H]);
+    join(t.s[j], s[2 * j], s[2 * j + H]);
+  }
+  return t;
 }
 
 template <int G>
@@ -231,13 +314,6 @@ __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
-}
-
-// The table row of token t, or -1 where its position is outside the table.
-__device__ __forceinline__ long long table_row(const QkNormRopeArgs& a, long long t) {
-  if (a.rot == 0) return 0;
-  const long long p = a.positions != nullptr ? a.positions[t] : t;
-  return p >= 0 && p < a.table_rows ? p : -1;
 }
 
 // One side (q or k) as the kernels see it.
@@ -265,63 +341,119 @@ __device__ __forceinline__ Side<T> side_of(const QkNormRopeArgs& a, bool is_k) {
   return s;
 }
 
-// A warp's way through its items, `chunk` of the groups of one token each, q's
-// groups (iq of them) before k's; stepped without divisions.
+enum class New { nothing, side, token };
+
+// A warp's way through its share of all groups (T tokens' `groups` each, the
+// first iq of them q's, the rest k's): consecutive ones, so that the shares
+// differ by one group at most and a token's table row serves all its heads.
+// (Whole tokens in turn: backward 97 us for 16384 tokens, 16.8 for 1024; in
+// shares 88 and 14.4.)
 struct Walk {
-  int items, step, step_t, step_c, chunk, chunks, iq, groups;
-  int it, t, c;       // the item: token t, its c-th chunk
-  int g, end, after;  // group g of [.., end) of a side; k's groups that follow
+  int left, iq, groups;
+  int t, g, end;  // token t's group g of [0, end) of a side
   bool is_k;
 
-  __device__ __forceinline__ Walk(int first, int step_, int items_, int chunk_, int chunks_,
-                                  int iq_, int groups_)
-      : items(items_), step(step_), chunk(chunk_), chunks(chunks_), iq(iq_), groups(groups_) {
-    step_t = step / chunks;
-    step_c = step - step_t * chunks;
-    it = first;
-    t = first / chunks;
-    c = first - t * chunks;
-    enter();
+  __device__ __forceinline__ Walk(int warp, int warps, long long T, int iq_, int groups_)
+      : iq(iq_), groups(groups_) {
+    const long long total = T * groups, first = total * warp / warps;
+    left = static_cast<int>(total * (warp + 1) / warps - first);
+    t = static_cast<int>(first / groups);
+    g = static_cast<int>(first - static_cast<long long>(t) * groups);
+    is_k = g >= iq;
+    end = is_k ? groups - iq : iq;
+    if (is_k) g -= iq;
   }
-  __device__ __forceinline__ void enter() {
-    const int first = c * chunk, last = min(groups, first + chunk);
-    is_k = first >= iq;
-    g = is_k ? first - iq : first;
-    end = is_k ? last - iq : min(last, iq);
-    after = is_k ? 0 : last - iq;
-  }
-  __device__ __forceinline__ bool live() const { return it < items; }
-  // To the next group; true where it is of another token or side.
-  __device__ __forceinline__ bool next() {
-    if (++g < end) return false;
-    if (after > 0) {
+  __device__ __forceinline__ bool live() const { return left > 0; }
+  // To the next group; what is new there.
+  __device__ __forceinline__ New next() {
+    --left;
+    if (++g < end) return New::nothing;
+    g = 0;
+    if (!is_k && groups > iq) {
       is_k = true;
-      g = 0;
-      end = after;
-      after = 0;
-      return true;
+      end = groups - iq;
+      return New::side;
     }
-    it += step;
-    t += step_t;
-    c += step_c;
-    if (c >= chunks) {
-      c -= chunks;
-      ++t;
-    }
-    enter();
-    return true;
+    is_k = false;
+    end = iq;
+    ++t;
+    return New::token;
   }
 };
 
-// Items of groups of 32 / G heads of one token (q's groups, then k's), NS slots
-// per lane.  gamma and the table row are multiplied once per token and side,
+// The table rows of a warp's tokens on their way to shared memory, with the
+// groups that they turn: SLOTS tokens (one is started per group at most, and a
+// row is read before the group STAGES later is fetched).  Positions are read 32
+// tokens at a time.  (With loads at the token's first group
+// instead, a warp stood still twice per token for a trip to memory: backward 98
+// us instead of 88, heads of 64 65 instead of 52.)
+template <int V, int SLOTS>
+struct Tables {
+  static constexpr int bytes(int half) {
+    return kWarps * SLOTS * 2 * ((half + 3) & ~3) * 4;
+  }
+
+  const QkNormRopeArgs& a;
+  float* rows;  // this warp's slots: a row of each table
+  int half, pitch, count, slot, ahead_slot;
+  int position;  // of the lane's token among 32; -1: outside the table
+  uint32_t valid;
+
+  __device__ __forceinline__ Tables(const QkNormRopeArgs& a_, uint8_t* smem)
+      : a(a_), half(a_.rot / 2), pitch((a_.rot / 2 + 3) & ~3), count(0), slot(SLOTS - 1),
+        ahead_slot(SLOTS - 1), position(-1), valid(0) {
+    rows = reinterpret_cast<float*>(smem) + (threadIdx.x / 32) * SLOTS * 2 * pitch;
+  }
+  __device__ __forceinline__ void positions(const Walk& w) {
+    const long long t = w.t + static_cast<long long>(threadIdx.x % 32);
+    position = -1;
+    if (t < a.T) {
+      const int p = a.rot == 0 ? 0 : a.positions != nullptr ? a.positions[t] : static_cast<int>(t);
+      if (a.rot == 0 || (p >= 0 && p < a.table_rows)) position = p;
+    }
+  }
+  // The rows of the token that w enters.
+  __device__ __forceinline__ void fetch(const Walk& w) {
+    if (count == 32) {
+      positions(w);
+      count = 0;
+    }
+    const int p = __shfl_sync(0xffffffffu, position, count);  // and every lane has read the slot
+    ++count;
+    ahead_slot = ahead_slot + 1 == SLOTS ? 0 : ahead_slot + 1;
+    valid = p >= 0 ? valid | 1u << ahead_slot : valid & ~(1u << ahead_slot);
+    if (p < 0) return;
+    float* to = rows + ahead_slot * 2 * pitch;
+    const float* cos = a.cos_table + static_cast<long long>(p) * half;
+    const float* sin = a.sin_table + static_cast<long long>(p) * half;
+    constexpr int W = V % 4 == 0 ? 4 : 1;  // floats per copy (vector_width: 16-byte rows)
+    for (int i = (threadIdx.x % 32) * W; i < 2 * half; i += 32 * W) {
+      const float* from = i < half ? cos + i : sin + (i - half);
+      const uint32_t dst = smem_u32(to + (i < half ? i : i - half + pitch));
+      if constexpr (W == 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(from) : "memory");
+    }
+  }
+  // To the rows of the next token; whether its position is in the table.
+  __device__ __forceinline__ bool enter() {
+    slot = slot + 1 == SLOTS ? 0 : slot + 1;
+    return (valid >> slot & 1u) != 0;
+  }
+  __device__ __forceinline__ const float* cos() const { return rows + slot * 2 * pitch; }
+  __device__ __forceinline__ const float* sin() const { return cos() + pitch; }
+};
+
+// Groups of 32 / G heads of one token (q's, then k's), NS slots per lane.  gamma and the table row are multiplied once per token and side,
 // so that a value costs three operations: y_a = r (x_a (g_a c) - x_b (g_b s)).
 template <typename T, int V, int G, int NS, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kThreads, NS == 1 ? kForwardPerSm : 1)
-    qk_forward_kernel(const QkNormRopeArgs a, int chunk, int chunks) {
+    qk_forward_kernel(const QkNormRopeArgs a) {
   pdl_wait();
   pdl_trigger();
-  using P = Pairs<V, INTER>;
+  using W = Vals<V>;
+  using E = typename W::E;
   using Ring = Rows<T, V, 2 * NS>;
   constexpr int R = 32 / G;  // rows per warp
   extern __shared__ __align__(16) uint8_t smem[];
@@ -333,15 +465,16 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kForwardPerSm : 1)
 #pragma unroll
   for (int j = 0; j < NS; ++j) w[j] = slot_of<V, INTER, FULL>(li + G * j, a.D, a.rot);
   Walk now(static_cast<int>(blockIdx.x) * kWarps + threadIdx.x / 32,
-           static_cast<int>(gridDim.x) * kWarps, static_cast<int>(a.T) * chunks, chunk, chunks, iq,
-           groups);
+           static_cast<int>(gridDim.x) * kWarps, a.T, iq, groups);
   Walk ahead = now;
-  bool fresh = true;  // the group ahead begins another token or side
+  Tables<V, Ring::STAGES> tables(a, smem + Ring::SMEM);
+  tables.positions(now);
+  New fresh = New::token;  // at the group ahead
   const T* x = nullptr;
   int x_head = 0;
   auto fetch = [&](int stage) {
     if (ahead.live()) {
-      if (fresh) {
+      if (fresh != New::nothing) {
         x_head = ahead.g * R + row;
         x = static_cast<const T*>(ahead.is_k ? a.k : a.q) +
             ahead.t * (ahead.is_k ? a.ld_k : a.ld_q) + x_head * a.D;
@@ -352,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kForwardPerSm : 1)
         ring.fetch(stage, 2 * j, x + w[j].o0, live && (FULL || w[j].has0));
         ring.fetch(stage, 2 * j + 1, x + w[j].o1, live && (FULL || w[j].has1));
       }
+      if (fresh == New::token) tables.fetch(ahead);
       x_head += R;
       x += R * a.D;
       fresh = ahead.next();
@@ -360,56 +494,62 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kForwardPerSm : 1)
   };
   if (Ring::ASYNC)
     for (int s = 0; s < Ring::STAGES; ++s) fetch(s);
-  // own[v][i] x[v][i] is the value's own part, cross[v][i] x[v][i] its partner's
-  float own[NS][2][V], cross[NS][2][V];
-  long long tr = -1;
-  bool turned = true;  // another token or side than the last group's
+  // a value's output is r (own x + cross (its partner's x)); cross is indexed by
+  // the value that it multiplies
+  W own[NS], cross[NS];
+  const E minus = both<E>(-1.f);
+  bool valid = false;
+  New turned = New::token;
   T* out = nullptr;
   int head = 0;
   for (int stage = 0; now.live(); stage = stage + 1 == Ring::STAGES ? 0 : stage + 1) {
-    if (turned) {
+    if (!Ring::ASYNC) fetch(stage);
+    Ring::wait();
+    if (turned != New::nothing) {
       head = now.g * R + row;
       out = static_cast<T*>(now.is_k ? a.out_k : a.out_q) +
             now.t * (now.is_k ? a.ld_out_k : a.ld_out_q) + head * a.D;
-      tr = table_row(a, now.t);
-      if (tr >= 0) {
+      if (turned == New::token) {
+        valid = tables.enter();
+        __syncwarp();  // the other lanes' copies of the rows
+      }
+      if (valid) {
         const float* gamma = now.is_k ? a.gamma_k : a.gamma_q;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-          float cs[V], sn[V], m[2][V];
-          load_trig<V>(cs, sn, a, tr, li + G * j, w[j]);
-          load_gamma<V>(m, gamma, w[j]);
+          const Trig<V> t = load_trig<V>(tables.cos(), tables.sin(), w[j]);
+          const W m = load_gamma<V, INTER>(gamma, w[j]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            own[j][P::vec_a(i)][P::at_a(i)] = m[P::vec_a(i)][P::at_a(i)] * cs[i];
-            own[j][P::vec_b(i)][P::at_b(i)] = m[P::vec_b(i)][P::at_b(i)] * cs[i];
-            cross[j][P::vec_a(i)][P::at_a(i)] = m[P::vec_a(i)][P::at_a(i)] * sn[i];
-            cross[j][P::vec_b(i)][P::at_b(i)] = -m[P::vec_b(i)][P::at_b(i)] * sn[i];
+          for (int i = 0; i < W::N; ++i) {
+            own[j].a[i] = mul(m.a[i], t.c[i]);
+            own[j].b[i] = mul(m.b[i], t.c[i]);
+            cross[j].a[i] = mul(m.a[i], t.s[i]);
+            cross[j].b[i] = mul(m.b[i], mul(minus, t.s[i]));
           }
         }
       } else if (lane == 0) {
         atomicCAS(a.status, 0, static_cast<int>(POETX_ERR_INVALID_ARG));
       }
     }
-    if (!Ring::ASYNC) fetch(stage);
-    Ring::wait();
-    float v[NS][2][V];
+    W v[NS];
+    E sq_a = both<E>(0.f), sq_b = sq_a;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-      ring.read(stage, 2 * j, v[j][0]);
-      ring.read(stage, 2 * j + 1, v[j][1]);
+      float x2[2][V];
+      ring.read(stage, 2 * j, x2[0]);
+      ring.read(stage, 2 * j + 1, x2[1]);
+      v[j] = values<V, INTER>(x2);
+#pragma unroll
+      for (int i = 0; i < W::N; ++i) {
+        sq_a = mad(v[j].a[i], v[j].a[i], sq_a);
+        sq_b = mad(v[j].b[i], v[j].b[i], sq_b);
+      }
     }
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < NS; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        ss = fmaf(v[j][0][i], v[j][0][i], fmaf(v[j][1][i], v[j][1][i], ss));
     if (Ring::ASYNC) fetch(stage);
     const bool live = head < (now.is_k ? a.hk : a.hq);
-    ss = group_sum<G>(ss);
+    const float ss = group_sum<G>(total(sq_a) + total(sq_b));
     const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
-    if (tr < 0) {  // outside the table: zeros
+    if (!valid) {  // outside the table: zeros
       const float zero[V] = {};
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
@@ -419,23 +559,24 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kForwardPerSm : 1)
     } else {
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
-        float y[2][V];
+        const E rr = both<E>(r);
+        W o;
         if (FULL || w[j].turns) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float xa = v[j][P::vec_a(i)][P::at_a(i)];
-            const float xb = v[j][P::vec_b(i)][P::at_b(i)];
-            y[P::vec_a(i)][P::at_a(i)] = r * fmaf(xa, own[j][P::vec_a(i)][P::at_a(i)],
-                                                  xb * cross[j][P::vec_b(i)][P::at_b(i)]);
-            y[P::vec_b(i)][P::at_b(i)] = r * fmaf(xb, own[j][P::vec_b(i)][P::at_b(i)],
-                                                  xa * cross[j][P::vec_a(i)][P::at_a(i)]);
+          for (int i = 0; i < W::N; ++i) {
+            const E xa = v[j].a[i], xb = v[j].b[i];
+            o.a[i] = mul(rr, mad(xa, own[j].a[i], mul(xb, cross[j].b[i])));
+            o.b[i] = mul(rr, mad(xb, own[j].b[i], mul(xa, cross[j].a[i])));
           }
         } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < V; ++i) y[h][i] = r * (v[j][h][i] * own[j][h][i]);
+          for (int i = 0; i < W::N; ++i) {
+            o.a[i] = mul(rr, mul(v[j].a[i], own[j].a[i]));
+            o.b[i] = mul(rr, mul(v[j].b[i], own[j].b[i]));
+          }
         }
+        float y[2][V];
+        vectors<V, INTER>(y, o);
         if (live && (FULL || w[j].has0))
           *reinterpret_cast<Pack<T, V>*>(out + w[j].o0) = pack<T, V>(y[0]);
         if (live && (FULL || w[j].has1))
@@ -449,16 +590,16 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kForwardPerSm : 1)
 }
 
 // As the forward, but a CTA stays with one side (the first ctas_q CTAs with q)
-// and keeps its lanes' sums of dgamma in registers over all its items; they go
-// to part[CTA][D], added up by qk_dgamma_kernel in a fixed order.  A token's
-// heads are cut into `chunks` items of `chunk` groups.
+// and keeps its lanes' sums of dgamma in registers over all its groups; they go
+// to part[CTA][D], added up by qk_dgamma_kernel in a fixed order.  The table
+// entries are read from shared memory for every group: in registers they spill.
 template <typename T, int V, int G, int NS, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
-    qk_backward_kernel(const QkNormRopeArgs a, int ctas_q, int chunk_q, int chunks_q, int chunk_k,
-                       int chunks_k) {
+    qk_backward_kernel(const QkNormRopeArgs a, int ctas_q) {
   pdl_wait();
   pdl_trigger();
-  using P = Pairs<V, INTER>;
+  using W = Vals<V>;
+  using E = typename W::E;
   using Ring = Rows<T, V, 4 * NS>;
   constexpr int R = 32 / G;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -470,25 +611,25 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
   const int cta = static_cast<int>(blockIdx.x) - (is_k ? ctas_q : 0);
   const int ctas = is_k ? static_cast<int>(gridDim.x) - ctas_q : ctas_q;
   const int groups = (sd.heads + R - 1) / R;
-  const int chunk = is_k ? chunk_k : chunk_q, chunks = is_k ? chunks_k : chunks_q;
   const float inv_d = 1.f / static_cast<float>(a.D);
   Slot w[NS];
-  float m[NS][2][V];
+  W m[NS];
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
     w[j] = slot_of<V, INTER, FULL>(li + G * j, a.D, a.rot);
-    load_gamma<V>(m[j], sd.gamma, w[j]);
+    m[j] = load_gamma<V, INTER>(sd.gamma, w[j]);
   }
-  Walk now(cta * kWarps + threadIdx.x / 32, ctas * kWarps, static_cast<int>(a.T) * chunks, chunk,
-           chunks, groups, groups);
+  Walk now(cta * kWarps + threadIdx.x / 32, ctas * kWarps, a.T, groups, groups);
   Walk ahead = now;
-  bool fresh = true;  // the group ahead begins another token
+  Tables<V, Ring::STAGES> tables(a, smem + Ring::SMEM);
+  tables.positions(now);
+  New fresh = New::token;  // at the group ahead
   const T* x = nullptr;
   const T* dy = nullptr;
   int x_head = 0;
   auto fetch = [&](int stage) {
     if (ahead.live()) {
-      if (fresh) {
+      if (fresh != New::nothing) {
         x_head = ahead.g * R + row;
         x = sd.x + ahead.t * sd.ld_x + x_head * a.D;
         dy = sd.g + ahead.t * sd.ld_g + x_head * a.D;
@@ -501,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
         ring.fetch(stage, 4 * j + 2, dy + w[j].o0, live && (FULL || w[j].has0));
         ring.fetch(stage, 4 * j + 3, dy + w[j].o1, live && (FULL || w[j].has1));
       }
+      if (fresh == New::token) tables.fetch(ahead);
       x_head += R;
       x += R * a.D;
       dy += R * a.D;
@@ -510,61 +652,60 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
   };
   if (Ring::ASYNC)
     for (int s = 0; s < Ring::STAGES; ++s) fetch(s);
-  float dg[NS][2][V] = {};
-  float cs[NS][V], sn[NS][V];
-  long long tr = -1;
-  bool turned = true;  // another token than the last group's
+  W dg[NS];
+#pragma unroll
+  for (int j = 0; j < NS; ++j)
+#pragma unroll
+    for (int i = 0; i < W::N; ++i) dg[j].a[i] = dg[j].b[i] = both<E>(0.f);
+  const E minus = both<E>(-1.f);
+  bool valid = false;
+  New turned = New::token;
   T* out = nullptr;
   int head = 0;
   for (int stage = 0; now.live(); stage = stage + 1 == Ring::STAGES ? 0 : stage + 1) {
-    if (turned) {
-      head = now.g * R + row;
-      out = sd.out + now.t * sd.ld_out + head * a.D;
-      tr = table_row(a, now.t);
-      if (tr >= 0) {
-#pragma unroll
-        for (int j = 0; j < NS; ++j) load_trig<V>(cs[j], sn[j], a, tr, li + G * j, w[j]);
-      } else if (lane == 0) {
-        atomicCAS(a.status, 0, static_cast<int>(POETX_ERR_INVALID_ARG));
-      }
-    }
     if (!Ring::ASYNC) fetch(stage);
     Ring::wait();
-    float v[NS][2][V], dn[NS][2][V];
-    float ss = 0.f, gx = 0.f;
+    if (turned != New::nothing) {
+      head = now.g * R + row;
+      out = sd.out + now.t * sd.ld_out + head * a.D;
+      valid = tables.enter();
+      __syncwarp();  // the other lanes' copies of the rows
+      if (!valid && lane == 0) atomicCAS(a.status, 0, static_cast<int>(POETX_ERR_INVALID_ARG));
+    }
+    W v[NS], dn[NS];
+    E sq_a = both<E>(0.f), sq_b = sq_a, gx_a = sq_a, gx_b = sq_a;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-      float d[2][V];
-      ring.read(stage, 4 * j, v[j][0]);
-      ring.read(stage, 4 * j + 1, v[j][1]);
-      ring.read(stage, 4 * j + 2, d[0]);
-      ring.read(stage, 4 * j + 3, d[1]);
-      if (FULL || w[j].turns) {  // the rotation transposed
+      float x2[2][V], d2[2][V];
+      ring.read(stage, 4 * j, x2[0]);
+      ring.read(stage, 4 * j + 1, x2[1]);
+      ring.read(stage, 4 * j + 2, d2[0]);
+      ring.read(stage, 4 * j + 3, d2[1]);
+      v[j] = values<V, INTER>(x2);
+      const W d = values<V, INTER>(d2);
+      if (valid && (FULL || w[j].turns)) {  // the rotation transposed
+        const Trig<V> t = load_trig<V>(tables.cos(), tables.sin(), w[j]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float da = d[P::vec_a(i)][P::at_a(i)], db = d[P::vec_b(i)][P::at_b(i)];
-          dn[j][P::vec_a(i)][P::at_a(i)] = fmaf(da, cs[j][i], db * sn[j][i]);
-          dn[j][P::vec_b(i)][P::at_b(i)] = fmaf(db, cs[j][i], -da * sn[j][i]);
+        for (int i = 0; i < W::N; ++i) {
+          dn[j].a[i] = mad(d.a[i], t.c[i], mul(d.b[i], t.s[i]));
+          dn[j].b[i] = mad(minus, mul(d.a[i], t.s[i]), mul(d.b[i], t.c[i]));
         }
       } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < V; ++i) dn[j][h][i] = d[h][i];
+        dn[j] = d;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          ss = fmaf(v[j][h][i], v[j][h][i], ss);
-          gx = fmaf(dn[j][h][i] * m[j][h][i], v[j][h][i], gx);
-        }
+      for (int i = 0; i < W::N; ++i) {
+        sq_a = mad(v[j].a[i], v[j].a[i], sq_a);
+        sq_b = mad(v[j].b[i], v[j].b[i], sq_b);
+        gx_a = mad(mul(dn[j].a[i], m[j].a[i]), v[j].a[i], gx_a);
+        gx_b = mad(mul(dn[j].b[i], m[j].b[i]), v[j].b[i], gx_b);
+      }
     }
     if (Ring::ASYNC) fetch(stage);
     const bool live = head < sd.heads;
-    ss = group_sum<G>(ss);
-    gx = group_sum<G>(gx);
-    if (tr < 0) {  // outside the table: no gradient
+    const float ss = group_sum<G>(total(sq_a) + total(sq_b));
+    const float gx = group_sum<G>(total(gx_a) + total(gx_b));
+    if (!valid) {  // outside the table: no gradient
       const float zero[V] = {};
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
@@ -573,21 +714,24 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
       }
     } else {
       const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
-      const float k = r * (r * r * gx * inv_d);
+      const E rr = both<E>(r), k = both<E>(-(r * (r * r * gx * inv_d)));
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
+        W o;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float rd = r * dn[j][h][i];
-            dg[j][h][i] = fmaf(rd, v[j][h][i], dg[j][h][i]);
-            dn[j][h][i] = fmaf(rd, m[j][h][i], -v[j][h][i] * k);
-          }
+        for (int i = 0; i < W::N; ++i) {
+          const E ra = mul(rr, dn[j].a[i]), rb = mul(rr, dn[j].b[i]);
+          dg[j].a[i] = mad(ra, v[j].a[i], dg[j].a[i]);
+          dg[j].b[i] = mad(rb, v[j].b[i], dg[j].b[i]);
+          o.a[i] = mad(ra, m[j].a[i], mul(v[j].a[i], k));
+          o.b[i] = mad(rb, m[j].b[i], mul(v[j].b[i], k));
+        }
+        float y[2][V];
+        vectors<V, INTER>(y, o);
         if (live && (FULL || w[j].has0))
-          *reinterpret_cast<Pack<T, V>*>(out + w[j].o0) = pack<T, V>(dn[j][0]);
+          *reinterpret_cast<Pack<T, V>*>(out + w[j].o0) = pack<T, V>(y[0]);
         if (live && (FULL || w[j].has1))
-          *reinterpret_cast<Pack<T, V>*>(out + w[j].o1) = pack<T, V>(dn[j][1]);
+          *reinterpret_cast<Pack<T, V>*>(out + w[j].o1) = pack<T, V>(y[1]);
       }
     }
     head += R;
@@ -595,23 +739,26 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
     turned = now.next();
   }
   // the CTA's sum, warp by warp in order (rows of a warp by shuffles)
+  float sums[NS][2][V];
 #pragma unroll
-  for (int j = 0; j < NS; ++j)
+  for (int j = 0; j < NS; ++j) {
+    vectors<V, INTER>(sums[j], dg[j]);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int o = 16; o >= G; o >>= 1)
-          dg[j][h][i] += __shfl_xor_sync(0xffffffffu, dg[j][h][i], o);
+          sums[j][h][i] += __shfl_xor_sync(0xffffffffu, sums[j][h][i], o);
+  }
   for (int wp = 0; wp < kWarps; ++wp) {
     if (threadIdx.x / 32 == wp && row == 0) {
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if (w[j].has0) acc[w[j].o0 + i] = (wp == 0 ? 0.f : acc[w[j].o0 + i]) + dg[j][0][i];
-          if (w[j].has1) acc[w[j].o1 + i] = (wp == 0 ? 0.f : acc[w[j].o1 + i]) + dg[j][1][i];
+          if (w[j].has0) acc[w[j].o0 + i] = (wp == 0 ? 0.f : acc[w[j].o0 + i]) + sums[j][0][i];
+          if (w[j].has1) acc[w[j].o1 + i] = (wp == 0 ? 0.f : acc[w[j].o1 + i]) + sums[j][1][i];
         }
       }
     }
@@ -664,19 +811,6 @@ struct BackwardGrid {
   }
 };
 
-// A token's groups cut into `count` items of `size` (the last may have fewer,
-// none is empty): as many as give every warp about eight, so that the last
-// round of items is a small part of the whole.  T * count fits 32 bits.
-struct Chunks {
-  int size, count;
-  Chunks(long long T, int groups, long long warps) {
-    const long long wanted = std::max<long long>(1, 8 * warps / std::max<long long>(T, 1));
-    const int most = static_cast<int>(std::min<long long>(std::max(groups, 1), wanted));
-    size = (std::max(groups, 1) + most - 1) / most;
-    count = (std::max(groups, 1) + size - 1) / size;
-  }
-};
-
 // Lets a kernel use more shared memory than the default limit of 48 KiB for
 // all of it; `done`: the kernel's own flags, one per device.
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<bool> (&done)[64]) {
@@ -695,30 +829,30 @@ cudaError_t forward(const QkNormRopeArgs& a, cudaStream_t s) {
   constexpr int R = 32 / G;
   const int groups = (a.hq + R - 1) / R + (a.hk + R - 1) / R;
   const long long warps = static_cast<long long>(kForwardPerSm) * kWarps * sm_count();
-  const Chunks cut(a.T, groups, warps);
-  const long long items = a.T * cut.count;
   const int grid = static_cast<int>(
-      std::min<long long>((items + kWarps - 1) / kWarps, warps / kWarps));
+      std::min<long long>((a.T * groups + kWarps - 1) / kWarps, warps / kWarps));
   auto* kernel = qk_forward_kernel<T, V, G, NS, INTER, FULL>;
-  constexpr int smem = Rows<T, V, 2 * NS>::SMEM;
+  using Ring = Rows<T, V, 2 * NS>;
+  using Rot = Tables<V, Ring::STAGES>;
+  const int smem = Ring::SMEM + Rot::bytes(a.rot / 2);
   static std::atomic<bool> done[64];
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel),
+                                   Ring::SMEM + Rot::bytes(kMaxD / 2), done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, a, cut.size, cut.count);
+  return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, a);
 }
 
 template <typename T, int V, int G, int NS, bool INTER, bool FULL>
 cudaError_t backward(const QkNormRopeArgs& a, const BackwardGrid& n, cudaStream_t s) {
-  constexpr int R = 32 / G;
-  const Chunks cq(a.T, (a.hq + R - 1) / R, static_cast<long long>(kWarps) * n.q);
-  const Chunks ck(a.T, (a.hk + R - 1) / R, static_cast<long long>(kWarps) * n.k);
   auto* kernel = qk_backward_kernel<T, V, G, NS, INTER, FULL>;
-  constexpr int smem = Rows<T, V, 4 * NS>::SMEM;
+  using Ring = Rows<T, V, 4 * NS>;
+  using Rot = Tables<V, Ring::STAGES>;
+  const int smem = Ring::SMEM + Rot::bytes(a.rot / 2);
   static std::atomic<bool> done[64];
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel),
+                                   Ring::SMEM + Rot::bytes(kMaxD / 2), done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(n.q + n.k), dim3(kThreads), smem, s, a, n.q, cq.size,
-                    cq.count, ck.size, ck.count);
+  return launch_pdl(kernel, dim3(n.q + n.k), dim3(kThreads), smem, s, a, n.q);
 }
 
 // The widest vectors (at most 16 bytes) that the sizes, pointers and strides
@@ -746,7 +880,9 @@ int vector_width(const QkNormRopeArgs& a) {
 }
 
 // Slots of a row: whole pairs of vectors of the rotated part, then of the rest.
-int slots_of(const QkNormRopeArgs& a, int v) { return a.rot / 2 / v + (a.D - a.rot + 2 * v - 1) / (2 * v); }
+int slots_of(const QkNormRopeArgs& a, int v) {
+  return a.rot / 2 / v + (a.D - a.rot + 2 * v - 1) / (2 * v);
+}
 
 // call(V, G, NS) for the row's slots: G lanes, a power of two, of NS slots each.
 #define QK_BY_SLOTS(slots, call)                                             \
