@@ -1,23 +1,25 @@
 // The matrix products of poetx_linear_* for many tokens, bf16, on CTA pairs:
 //   C[M][N] = act(A B^T + bias) + residual   (A [M][K]; B [N][K] or, MN-major, [K][N])
-// Each cluster of two CTAs computes 256 x 256 (or 256 x 128) tiles with
-// tcgen05.mma.cta_group::2 over 64-wide K steps (a TMA ring of six 32 KiB or
-// eight 24 KiB stages per CTA); two TMEM accumulators let a tile's epilogue run under the
-// next tile's main loop.
+// Each cluster of two CTAs computes tiles of 256 x 256, 224, 192 or 128 with
+// tcgen05.mma.cta_group::2 over 64-wide K steps (a TMA ring of six to eight
+// stages per CTA; five instead of six cost 3 us in 79 at 4096^3); two TMEM
+// accumulators let a tile's epilogue run under the next tile's main loop.
 //
-// Roles, per CTA (320 threads):
+// Roles, per CTA (576 threads, fewer with narrower tiles):
 //   warp 0      TMA producer
 //   warp 1      TMEM allocation; in the leader CTA the MMAs
 //               (in both the whole warp runs the loop and one elected lane
 //               issues, which keeps addresses and descriptors in uniform
 //               registers: with the loop inside `lane == 0` a K step took 570
 //               cycles of issue, more than the 512 its MMAs take)
-//   warps 2..9  epilogue: two warps per 32-row quarter of the accumulator,
-//               128 columns each, in chunks of 64: bias, (z,) activation and
-//               residual in fp32 on the accumulator's values, one rounding,
-//               through a 4 KiB staging tile per warp.  The residual comes
-//               into the same staging tile by TMA; a tile's first chunk is
-//               asked for while its main loop still runs.
+//   the others  epilogue: a warp for 64 columns of each 32-row quarter of the
+//               accumulator, 32 at a time: bias, (z,) activation and residual
+//               in fp32 on the accumulator's values, one rounding, through a
+//               2 KiB staging tile per warp.  The residual comes into the same
+//               staging tile by TMA; a tile's first chunk is asked for while
+//               its main loop still runs.  (Half as many warps with twice the
+//               columns: 2048 -> 2048, T = 8192 with gelu 49.8 us instead of
+//               47.3; staging tiles of 4 KiB leave five stages.)
 // Rows that are not a multiple of 16 bytes apart (an odd number of output
 // features) cannot be TMA tiles: there the staging tile is filled and emptied
 // with plain loads and stores, a row at a time so that they coalesce.
@@ -42,23 +44,25 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kA = BM * BK * 2;      // this CTA's 128 rows, one K step
-constexpr int kSlot = 32 * 128;      // 32 rows x 64 bf16
-constexpr int kStaging = kEpiWarps * kSlot;
-constexpr int kBiasBytes = kEpiWarps * 64 * 4;
+constexpr int kChunk = 32;           // columns that a warp stages at a time
+constexpr int kSlot = 32 * kChunk * 2;
 
-template <int BN>
+template <int BN, bool B_MN>
 struct Shape {
-  static constexpr int B = (BN / 2) * BK * 2;  // this CTA's half of B, one K step
+  // this CTA's half of B, one K step (MN-major: whole 64-column boxes)
+  static constexpr int B = B_MN ? (BN / 2 + 63) / 64 * 64 * BK * 2 : (BN / 2) * BK * 2;
   static constexpr int STAGE = kA + B;
-  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int SIDES = (BN + 63) / 64;  // of 64 columns, four warps each
+  static constexpr int EPI_WARPS = 4 * SIDES;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int STAGING = EPI_WARPS * kSlot;
+  static constexpr int BIAS = EPI_WARPS * kChunk * 4;
+  static constexpr int STAGES = (227 * 1024 - STAGING - BIAS - 512) / STAGE;
   static constexpr int RING = STAGES * STAGE;
-  static constexpr int SMEM = RING + kStaging + kBiasBytes + 256;
-  static constexpr uint32_t TMEM_COLS = 2 * BN;
-  static constexpr int PER_SIDE = BN / 128;  // 64-column chunks of one epilogue warp
-  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+  static constexpr int SMEM = RING + STAGING + BIAS + 512;
+  static constexpr uint32_t ACC = BN > 128 ? 256 : 128;  // TMEM columns of an accumulator
+  static_assert(BN % 32 == 0 && (STAGE & 1023) == 0, "tiles on 1024 bytes");
 };
 
 constexpr int kGroupM = 8;
@@ -98,31 +102,41 @@ __device__ __forceinline__ void apply_act(int act, float (&v)[16]) {
   }
 }
 
-// 16 values of this thread's row -> 16-byte pieces 2 part, 2 part + 1 of its staging row
-__device__ __forceinline__ void stage_part(uint8_t* row, int lane, int part, const float (&v)[16]) {
+// A warp's staging tile: 32 rows of 64 bytes as TMA's 64-byte swizzle lays them out.
+struct Staged {
+  uint8_t* base;
+
+  __device__ __forceinline__ uint4* piece(int row, int q) const {  // 16 bytes
+    return reinterpret_cast<uint4*>(base + row * 64 + ((q ^ (row >> 1 & 3)) << 4));
+  }
+  __device__ __forceinline__ bf16* value(int row, int col) const {
+    return reinterpret_cast<bf16*>(piece(row, col >> 3)) + (col & 7);
+  }
+};
+
+// 16 values of this thread's row -> pieces 2 part, 2 part + 1 of its staging row
+__device__ __forceinline__ void stage_part(const Staged& slot, int lane, int part,
+                                           const float (&v)[16]) {
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     uint32_t w[4];
 #pragma unroll
     for (int h = 0; h < 4; ++h)
       w[h] = pack_bf16x2(__float_as_uint(v[8 * q + 2 * h]), __float_as_uint(v[8 * q + 2 * h + 1]));
-    st_shared_v4(row + (((2 * part + q) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+    st_shared_v4(slot.piece(lane, 2 * part + q), w[0], w[1], w[2], w[3]);
   }
 }
 
-__device__ __forceinline__ bf16* staged(uint8_t* slot, int row, int col) {
-  return reinterpret_cast<bf16*>(slot + row * 128 + (((col >> 3) ^ (row & 7)) << 4)) + (col & 7);
-}
-
 template <int BN, bool B_MN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<BN, B_MN>::THREADS, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmY,
                        const __grid_constant__ CUtensorMap tmZ,
                        const __grid_constant__ CUtensorMap tmR, const PairArgs p) {
-  using S = Shape<BN>;
+  using S = Shape<BN, B_MN>;
   constexpr int kStages = S::STAGES, kStage = S::STAGE, kRing = S::RING, kBN = BN;
+  constexpr int kEpiWarps = S::EPI_WARPS;
   extern __shared__ __align__(1024) uint8_t base[];  // 128B-swizzled tiles start on 1024 bytes
   if ((smem_u32(base) & 1023u) != 0) {  // the declared alignment, which the tiles rely on
     if (threadIdx.x == 0) atomicCAS(p.status, 0, static_cast<int>(POETX_ERR_CUDA));
@@ -130,8 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   uint8_t* ring = base;  // stage s: A (16 KiB), then this CTA's half of B
   uint8_t* staging = base + kRing;
-  float* bias_s = reinterpret_cast<float*>(staging + kStaging);
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(staging + kStaging + kBiasBytes);  // leader
+  float* bias_s = reinterpret_cast<float*>(staging + S::STAGING);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(staging + S::STAGING + S::BIAS);  // leader
   uint64_t* empty_bar = full_bar + kStages;  // each CTA: its slot is free
   uint64_t* tfull_bar = empty_bar + kStages;  // [2] each CTA: accumulator ready
   uint64_t* tempty_bar = tfull_bar + 2;       // [2] leader: accumulator drained
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
+    tmem_alloc_pair(tmem_slot, 2 * S::ACC);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -209,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d_pair(b_dst, &tmB, bar, ks * BK, b_n);
             } else {
               tma_load_2d_pair(b_dst, &tmB, bar, b_n, ks * BK);
-              if (BN == 256) tma_load_2d_pair(b_dst + 8192, &tmB, bar, b_n + 64, ks * BK);
+              if (BN > 128) tma_load_2d_pair(b_dst + 8192, &tmB, bar, b_n + 64, ks * BK);
             }
           }
           __syncwarp();
@@ -254,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kBN);
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc) * S::ACC;
         for (int ks = 0; ks < p.k_steps; ++ks) {
           if (!mbar_wait(&full_bar[stage], phase, abort_flag)) {
             record_timeout(p.status, abort_flag);
@@ -301,10 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int ew = warp - 2;
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
-    const int side = ew >> 2;      // its half of the tile's columns
-    uint8_t* slot = staging + ew * kSlot;
-    uint8_t* my_row = slot + lane * 128;
-    float* bias_w = bias_s + ew * 64;
+    const int side = ew >> 2;      // its 64 (at the end of a 224-wide tile 32) columns
+    const Staged slot{staging + ew * kSlot};
     int acc = 0;
     uint32_t acc_phase = 0;
     uint32_t res_phase = 0;
@@ -316,14 +328,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.tma_rows) {
         if (lane == 0) {
           mbar_arrive_expect_tx(&res_bar[ew], kSlot);
-          tma_load_2d(slot, &tmR, &res_bar[ew], col, static_cast<int>(row0));
+          tma_load_2d(slot.base, &tmR, &res_bar[ew], col, static_cast<int>(row0));
         }
         res_pending = true;
       } else {
         for (int r = 0; r < 32 && row0 + r < p.M; ++r)
-#pragma unroll
-          for (int c = lane; c < 64; c += 32)
-            if (col + c < p.N) *staged(slot, r, c) = p.residual[(row0 + r) * p.ld + col + c];
+          if (col + lane < p.N)
+            *slot.value(r, lane) = p.residual[(row0 + r) * p.ld + col + lane];
         __syncwarp();
       }
     };
@@ -334,21 +345,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(map, slot, col, static_cast<int>(row0));
+          tma_store_2d(map, slot.base, col, static_cast<int>(row0));
           bulk_commit();
         }
         stores_pending = true;
       } else {
         __syncwarp();
         for (int r = 0; r < 32 && row0 + r < p.M; ++r)
-#pragma unroll
-          for (int c = lane; c < 64; c += 32)
-            if (col + c < p.N) out[(row0 + r) * p.ld + col + c] = *staged(slot, r, c);
+          if (col + lane < p.N) out[(row0 + r) * p.ld + col + lane] = *slot.value(r, lane);
         __syncwarp();
       }
     };
     // 16 columns of z: the accumulator plus the chunk's bias
-    auto load_z = [&](float (&v)[16], uint32_t taddr, int part) {
+    auto load_z = [&](float (&v)[16], uint32_t taddr, const float* bias_w, int part) {
       uint32_t r[16];
       tmem_load_16(taddr + part * 16, r);
 #pragma unroll
@@ -370,11 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int mp, nt;
       unit_tile(u, p, mp, nt);
       const long long row0 = static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32;
-      const int tile_col = nt * kBN + side * S::PER_SIDE * 64;
-      const bool live = row0 < p.M;  // the same for the whole warp
-      if (p.residual != nullptr && live && tile_col < p.N) {
+      const int side_col = nt * kBN + side * 64;
+      const bool live = row0 < p.M && side_col < p.N;  // the same for the whole warp
+      if (p.residual != nullptr && live) {
         staging_free();
-        fetch_residual(row0, tile_col);
+        fetch_residual(row0, side_col);
       }
       const bool got = mbar_wait_cluster(&tfull_bar[acc], acc_phase, abort_flag);
       if (!__all_sync(0xffffffffu, got)) {
@@ -382,21 +391,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t t_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                              static_cast<uint32_t>(acc * kBN + side * S::PER_SIDE * 64);
       bool timed_out = false;
 #pragma unroll 1
-      for (int c = 0; c < S::PER_SIDE; ++c) {
-        const int col = tile_col + c * 64;
-        if (!live || col >= p.N) break;
+      for (int c = 0; c < 64 && live; c += kChunk) {
+        const int col = side_col + c;
+        if (side * 64 + c >= BN || col >= p.N) break;
+        const uint32_t t_chunk = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                 static_cast<uint32_t>(acc) * S::ACC +
+                                 static_cast<uint32_t>(side * 64 + c);
         if (c > 0 && p.residual != nullptr) {
           staging_free();
           fetch_residual(row0, col);
         }
+        float* bias_w = bias_s + ew * kChunk;
         if (p.bias != nullptr) {
           __syncwarp();
           bias_w[lane] = col + lane < p.N ? __ldg(p.bias + col + lane) : 0.f;
-          bias_w[lane + 32] = col + lane + 32 < p.N ? __ldg(p.bias + col + lane + 32) : 0.f;
           __syncwarp();
         }
         if (p.residual == nullptr) staging_free();
@@ -409,39 +419,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           res_phase ^= 1;
           res_pending = false;
         }
-        uint4 res[8];
+        uint4 res[kChunk / 8];
         if (p.residual != nullptr && p.z != nullptr) {  // z takes the staging tile first
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            res[q] = *reinterpret_cast<const uint4*>(my_row + ((q ^ (lane & 7)) << 4));
+          for (int q = 0; q < kChunk / 8; ++q) res[q] = *slot.piece(lane, q);
           __syncwarp();
         }
         if (p.z != nullptr) {
 #pragma unroll 1
-          for (int part = 0; part < 4; ++part) {
+          for (int part = 0; part < kChunk / 16; ++part) {
             float v[16];
-            load_z(v, t_base + c * 64, part);
-            stage_part(my_row, lane, part, v);
+            load_z(v, t_chunk, bias_w, part);
+            stage_part(slot, lane, part, v);
           }
           store_chunk(&tmZ, p.z, row0, col);
           staging_free();
           if (p.residual != nullptr) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              st_shared_v4(my_row + ((q ^ (lane & 7)) << 4), res[q].x, res[q].y, res[q].z,
-                           res[q].w);
+            for (int q = 0; q < kChunk / 8; ++q)
+              st_shared_v4(slot.piece(lane, q), res[q].x, res[q].y, res[q].z, res[q].w);
           }
         }
 #pragma unroll 1
-        for (int part = 0; part < 4; ++part) {
+        for (int part = 0; part < kChunk / 16; ++part) {
           float v[16];
-          load_z(v, t_base + c * 64, part);
+          load_z(v, t_chunk, bias_w, part);
           apply_act(p.act, v);
           if (p.residual != nullptr) {  // this thread's own row: read, added, written over
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const uint4 r =
-                  *reinterpret_cast<const uint4*>(my_row + (((2 * part + q) ^ (lane & 7)) << 4));
+              const uint4 r = *slot.piece(lane, 2 * part + q);
               const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -452,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          stage_part(my_row, lane, part, v);
+          stage_part(slot, lane, part, v);
         }
         store_chunk(&tmY, p.y, row0, col);
       }
@@ -481,13 +488,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, S::TMEM_COLS);
+    tmem_dealloc_pair(tmem_base, 2 * S::ACC);
   }
 }
 
 template <int BN, bool B_MN>
 cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
-  using S = Shape<BN>;
+  using S = Shape<BN, B_MN>;
   constexpr int kSmem = S::SMEM, kBN = BN;
   auto* kernel = linear_pair_kernel<BN, B_MN>;
   static bool ready[64] = {false};
@@ -497,7 +504,7 @@ cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(S::THREADS);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -536,10 +543,10 @@ cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   tmY = tmZ = tmR = tmA;  // stand-ins where a tensor is absent: never used
   if (p.tma_rows) {
-    if (!make_map(&tmY, g.y, g.M, g.N, g.ld, 2, 64, 32)) return cudaErrorInvalidValue;
-    if (g.z != nullptr && !make_map(&tmZ, g.z, g.M, g.N, g.ld, 2, 64, 32))
-      return cudaErrorInvalidValue;
-    if (g.residual != nullptr && !make_map(&tmR, g.residual, g.M, g.N, g.ld, 2, 64, 32))
+    const auto map = [&](CUtensorMap* m, const void* at) {
+      return at == nullptr || make_map(m, at, g.M, g.N, g.ld, 2, kChunk, 32, 64);
+    };
+    if (!map(&tmY, g.y) || !map(&tmZ, g.z) || !map(&tmR, g.residual))
       return cudaErrorInvalidValue;
   }
   p.m_pairs = static_cast<int>((g.M + 2 * BM - 1) / (2 * BM));
@@ -566,19 +573,35 @@ cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
 
 }  // namespace
 
+namespace {
+
+template <int BN>
+cudaError_t by_layout(const LinearProduct& g, cudaStream_t s) {
+  return g.b_mn ? launch<BN, true>(g, s) : launch<BN, false>(g, s);
+}
+
+}  // namespace
+
+// The width of the tiles: the one whose rounds over the clusters take the least
+// time, at 0.28 us for a 64-wide K step of a 256-wide tile (bound by the MMAs),
+// 0.25 for 224, 0.23 for 192 and 0.17 for 128 (bound by the operands' loads).
+// Bare products, us, of 256 / 224 / 192 / 128: 4096^3 78.7 / 73.4 / 76.1 / 85.0
+// (4, 4, 5 and 7 rounds); 2048 -> 5632, T = 2048 32.5 / 30.1 / 32.1 / 33.4;
+// 2048 -> 2048, T = 8192 44.8 / 49.5 / 43.8 / 47.8.
 cudaError_t linear_pair(const LinearProduct& g, cudaStream_t s) {
   if (g.M <= 0 || g.N <= 0 || g.K <= 0) return cudaSuccess;
-  // 128-wide tiles, where they fill idle clusters: a 64-wide K step of one takes
-  // 0.19 us (24 KiB of operands per CTA, bound by their loads), of a 256-wide
-  // tile 0.28 us (bound by the MMAs), so they win while the rounds of tiles over
-  // the clusters are fewer than 3/2 of the wide tiles'.  4096 -> 4096 features:
-  // T = 512 (32 wide tiles) 17.4 against 23.2 us, T = 1024 (64) 29.4 against 24.4.
   const long long m_pairs = (g.M + 2 * BM - 1) / (2 * BM);
   const long long clusters = std::max(1, sm_count() / 2);
-  const long long wide = (m_pairs * ((g.N + 255) / 256) + clusters - 1) / clusters;
-  const long long narrow = (m_pairs * ((g.N + 127) / 128) + clusters - 1) / clusters;
-  if (2 * narrow < 3 * wide) return g.b_mn ? launch<128, true>(g, s) : launch<128, false>(g, s);
-  return g.b_mn ? launch<256, true>(g, s) : launch<256, false>(g, s);
+  const auto cost = [&](int width, int step) {
+    return (m_pairs * ((g.N + width - 1) / width) + clusters - 1) / clusters * step;
+  };
+  const long long c256 = cost(256, 28), c224 = cost(224, 25), c192 = cost(192, 23),
+                  c128 = cost(128, 17);
+  const long long best = std::min(std::min(c256, c224), std::min(c192, c128));
+  if (c256 == best) return by_layout<256>(g, s);
+  if (c224 == best) return by_layout<224>(g, s);
+  if (c192 == best) return by_layout<192>(g, s);
+  return by_layout<128>(g, s);
 }
 
 }  // namespace poetx

@@ -139,9 +139,9 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 2-D map over a row-major array, box = box_cols x box_rows, 128B swizzle.
+// 2-D map over a row-major array, box = box_cols x box_rows, swizzle 128 or 64 bytes.
 bool make_map(CUtensorMap* map, const void* ptr, long long rows, long long cols, long long pitch,
-              int elem_bytes, int box_cols, int box_rows) {
+              int elem_bytes, int box_cols, int box_rows, int swizzle = 128) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
@@ -151,7 +151,8 @@ bool make_map(CUtensorMap* map, const void* ptr, long long rows, long long cols,
   const CUtensorMapDataType dt =
       elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   CUresult r = fn(map, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
