@@ -188,13 +188,22 @@ size_t pad_bytes(long long rows, int cols) {
 
 namespace {
 
-// Few tokens: linear_stream.  Up to 64 it is always ahead (4096 -> 4096, T = 1:
-// 8.5 against 14.8 us); up to 256 where K is long enough to be split and no
-// shorter than the weight is wide (14336 -> 4096, T = 256: 31 against 42 us;
-// the other way round, 4096 -> 14336, 36 against 28).
+// Where linear_stream is ahead of linear_pair: up to 64 tokens always (4096 ->
+// 4096, one token: 8.5 against 14.8 us), and where its tiles are too few to give
+// every cluster of the pairs one while K is long enough to be split.  Up to 128
+// tokens: 64 tiles, K / 64 of them (8192 -> 8192, 64 tiles: 28.2 against 30.6 us;
+// 2048 -> 4096, 32: 8.7 against 10.3; 2048 -> 5632, 44: 11.4 against 10.7).
+// Beyond, with one CTA per SM: 32 tiles, K / 128 of them (256 tokens, 4096 ->
+// 4096, 32 tiles: 14.5 against 15.8; 6144 -> 6144, 48: 25.8 against 22.2; 2048 ->
+// 4096, 32: 11.3 against 10.4; 1024 tokens, 8192 -> 1024, 32: 18.6 against 25.9).
+bool stream_form(long long M, int N, int K) {
+  if (M <= 64) return true;
+  const long long tiles = (N + 127) / 128 * ((M + 255) / 256);
+  return K >= 2048 && tiles <= (M <= 128 ? std::min(64, K / 64) : std::min(32, K / 128));
+}
+
 cudaError_t run_product(const LinearProduct& g, cudaStream_t s) {
-  const bool stream = g.M <= 64 || (g.M <= 256 && g.K >= g.N && g.K >= 2048);
-  return stream ? linear_stream(g, s) : linear_pair(g, s);
+  return stream_form(g.M, g.N, g.K) ? linear_stream(g, s) : linear_pair(g, s);
 }
 
 }  // namespace

@@ -28,7 +28,7 @@ struct LinearProduct {
   const char* tag = "linear";
 };
 
-// On CTA pairs, 256 x 256 tiles (linear_pair.cu).
+// On CTA pairs, tiles of 256 x 128 to 256 (linear_pair.cu).
 cudaError_t linear_pair(const LinearProduct& g, cudaStream_t s);
 
 // For few tokens: the weight streamed once, K split over a cluster (linear_stream.cu).

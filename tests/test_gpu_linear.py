@@ -96,6 +96,19 @@ def test_forward_matches_oracle(px, i, dtype):
     run_forward(px, *SHAPES[i], dtype, ACTS[i % 5], i % 2 == 0, i % 3 != 1, i % 4 < 2, 10 + i)
 
 
+# Sizes that take each tile width, with whole and cut tiles and rows off 16 bytes,
+# and the weight-streaming form with several tiles of tokens.
+WIDTHS = [(1024, 72, 4096), (1000, 64, 4093), (1024, 72, 3648), (1001, 136, 3645),
+          (2304, 64, 1536), (1000, 72, 1500), (260, 2048, 130), (600, 4096, 264)]
+
+
+@pytest.mark.parametrize("i", range(len(WIDTHS)))
+def test_every_tile_width(px, i):
+    T, a, b = WIDTHS[i]
+    run_forward(px, T, a, b, "bf16", ACTS[i % 5], i % 3 != 2, i % 2 == 0, i % 4 < 2, 110 + i)
+    run_backward(px, T, b, a, "bf16", ACTS[(i + 1) % 5], True, i % 2 == 1, 130 + i)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("T,a,b", [(3, 128, 264), (150, 256, 384), (600, 512, 512)])
