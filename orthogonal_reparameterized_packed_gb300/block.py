@@ -6,12 +6,13 @@ enqueues its calls on a stream (the current one by default)."""
 
 from __future__ import annotations
 
+import array
+
 import torch
 
-from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, _check, _stream,
-               load_library, poetx_clip_grads, poetx_grad_norm, poetx_grad_norm_workspace_size,
-               poetx_linear_backward_workspace_size, poetx_linear_forward_workspace_size,
-               poetx_qk_norm_rope_backward_workspace_size)
+from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, BF16, F32, _check, _stream,
+               load_library, poetx_grad_norm_workspace_size, poetx_linear_backward_workspace_size,
+               poetx_linear_forward_workspace_size, poetx_qk_norm_rope_backward_workspace_size)
 from .layer import _TORCH_DTYPE, dtype_code
 
 # These classes call the library directly: a call for one token costs the host
@@ -202,16 +203,18 @@ class PoetxQKNormRope:
         return self._cut(self.dq, t), self._cut(self.dk, t), self.dgamma_q, self.dgamma_k
 
 
-def _need_list(tensors, others, dtypes, name):
-    """Contiguous CUDA tensors of the types; `others` (or None) of the same sizes and types."""
-    if not ({t.dtype for t in tensors} <= dtypes and
-            all(map(torch.Tensor.is_contiguous, tensors)) and all(t.is_cuda for t in tensors)):
+def _described(tensors, dtypes, name):
+    """(counts, types) of contiguous CUDA tensors of `dtypes`."""
+    kinds = [t.dtype for t in tensors]
+    if not (set(kinds) <= dtypes and all(map(torch.Tensor.is_contiguous, tensors)) and
+            all([t.is_cuda for t in tensors])):
         raise ValueError(
             f"{name}: contiguous CUDA tensors of {sorted(map(str, dtypes))} are needed")
-    if others is not None:
-        _need_list(others, None, dtypes, "out")
-        if [(t.numel(), t.dtype) for t in tensors] != [(t.numel(), t.dtype) for t in others]:
-            raise ValueError(f"{name}: the lists differ in sizes or types")
+    return array.array("q", map(torch.Tensor.numel, tensors)), kinds
+
+
+def _pointers(tensors):
+    return array.array("Q", map(torch.Tensor.data_ptr, tensors))
 
 
 class PoetxGradClip:
@@ -225,6 +228,8 @@ class PoetxGradClip:
         self.device = torch.device(device)
         self.norm = torch.empty((), dtype=torch.float32, device=self.device)
         self._spaces = []
+        lib = load_library()
+        self._total, self._clip = lib.poetx_grad_norm, lib.poetx_clip_grads
 
     def _room(self, n):
         """A workspace for n tensors.  Smaller ones are kept: a call on another
@@ -234,15 +239,33 @@ class PoetxGradClip:
             self._spaces.append(torch.empty((need,), dtype=torch.uint8, device=self.device))
         return self._spaces[-1]
 
+    def _codes(self, kinds):
+        """The list's poetx_dtype array; empty where all are float32."""
+        return array.array("i", () if torch.bfloat16 not in kinds else
+                           [BF16 if k is torch.bfloat16 else F32 for k in kinds])
+
     def total(self, grads, stream=None):
         """norm = sqrt(sum of squares over all tensors)."""
-        _need_list(grads, None, self._TYPES, "grads")
-        poetx_grad_norm(grads, self.norm, self._room(len(grads)), stream)
+        counts, kinds = _described(grads, self._TYPES, "grads")
+        at, codes, room = _pointers(grads), self._codes(kinds), self._room(len(kinds))
+        _check("poetx_grad_norm", self._total(
+            len(kinds), at.buffer_info()[0], counts.buffer_info()[0],
+            codes.buffer_info()[0] if codes else None, self.norm.data_ptr(), room.data_ptr(),
+            room.numel(), _stream(stream)))
         return self.norm
 
     def clip(self, grads, max_norm, out=None, stream=None):
         """out (None: the gradients themselves) = grads * min(1, max_norm /
         (norm + 1e-6)); returns the norm before the clip."""
-        _need_list(grads, out, self._TYPES, "grads")
-        poetx_clip_grads(grads, out, max_norm, self.norm, self._room(len(grads)), stream)
+        counts, kinds = _described(grads, self._TYPES, "grads")
+        at = to = _pointers(grads)
+        if out is not None:
+            if _described(out, self._TYPES, "out") != (counts, kinds):
+                raise ValueError("grads: the lists differ in sizes or types")
+            to = _pointers(out)
+        codes, room = self._codes(kinds), self._room(len(kinds))
+        _check("poetx_clip_grads", self._clip(
+            len(kinds), at.buffer_info()[0], to.buffer_info()[0], counts.buffer_info()[0],
+            codes.buffer_info()[0] if codes else None, max_norm, self.norm.data_ptr(),
+            room.data_ptr(), room.numel(), _stream(stream)))
         return self.norm

@@ -23,6 +23,7 @@
 // kept apart, so that every finite gradient has a finite and accurate norm.
 #include <algorithm>
 #include <cstdint>
+#include <cstring>
 
 #include "internal.h"
 #include "poetx.h"
@@ -32,10 +33,15 @@ namespace poetx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 8192;       // elements: 8 16-byte loads in flight per thread (fp32)
+constexpr int kChunk = 8192;       // elements
+constexpr int kFlight = kChunk / 4 / kThreads;  // a thread's 16-byte vectors of one (fp32)
 constexpr int kMaxTensors = 512;   // per launch: the table is at most 24 KB of parameters
 constexpr int kFewTensors = 32;
-constexpr int kPerSm = 8;          // CTAs: every warp an SM can hold
+// CTAs per SM.  The norm and the clip have a whole chunk in registers, all its
+// loads in flight (336 gradients of 261,120: norm 53.6 us, 6.55 TB/s; 8 CTAs of 32
+// registers 60.2; clip 164 against 176); Adam has one vector of each array, and
+// every warp that an SM can hold.
+constexpr int kSumPerSm = 4, kClipPerSm = 3, kAdamPerSm = 8;
 constexpr int kMaxCtas = 2048;     // partial sums per launch
 constexpr float kClipEps = 1e-6f;  // guards the division when the norm is 0
 
@@ -124,12 +130,20 @@ __device__ __forceinline__ void chunk_sumsq(const T* p, int n, Sum& acc) {
     s = fmaf(f, f, s);
     any |= __float_as_uint(f);
   };
-#pragma unroll 8
-  for (int i = threadIdx.x; i < nv; i += kThreads) {
-    const Vec<T> q = pv[i];
+  constexpr int FLIGHT = kChunk / Vec<T>::N / kThreads;
+  Vec<T> q[FLIGHT];
 #pragma unroll
-    for (int j = 0; j < Vec<T>::N; ++j) add(q.x[j]);
+  for (int k = 0; k < FLIGHT; ++k) {
+    const int i = threadIdx.x + k * kThreads;
+    if (i < nv)
+      q[k] = pv[i];
+    else
+      memset(&q[k], 0, sizeof(q[k]));
   }
+#pragma unroll
+  for (int k = 0; k < FLIGHT; ++k)
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N; ++j) add(q[k].x[j]);
   const int i0 = threadIdx.x;  // at most 7 elements on either side
   if (i0 < head) add(p[i0]);
   if (tail + i0 < n) add(p[tail + i0]);
@@ -178,7 +192,7 @@ __device__ __forceinline__ Sum block_sum(Sum v) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kSumPerSm)
     sumsq_kernel(const __grid_constant__ TensorTable<CAP> t, Sum* part) {
   pdl_wait();
   pdl_trigger();
@@ -227,55 +241,85 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const Sum* part, int par
   if (threadIdx.x == 0) *norm = v.x;
 }
 
-template <typename T>
-__device__ __forceinline__ void scale_chunk(const T* p, T* o, int n, float scale) {
-  auto one = [&](T x) {
-    T r;
-    from_f(r, to_f(x) * scale);
-    return r;
-  };
-  const bool same_phase =
-      ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15u) == 0;
-  const int head = same_phase ? head_elements(p, n) : n;
-  const int nv = (n - head) / Vec<T>::N;
-  const int tail = head + nv * Vec<T>::N;
-  const Vec<T>* pv = reinterpret_cast<const Vec<T>*>(p + head);
-  Vec<T>* ov = reinterpret_cast<Vec<T>*>(o + head);
-#pragma unroll 4
-  for (int i = threadIdx.x; i < nv; i += kThreads) {
-    Vec<T> q = pv[i];
-#pragma unroll
-    for (int j = 0; j < Vec<T>::N; ++j) q.x[j] = one(q.x[j]);
-    ov[i] = q;
-  }
-  for (int i = threadIdx.x; i < head; i += kThreads) o[i] = one(p[i]);
-  for (int i = tail + threadIdx.x; i < n; i += kThreads) o[i] = one(p[i]);
-}
+// Chunk r of a clip: where it is, and each thread's vectors of it.
+struct ClipChunk {
+  const void* p;
+  void* o;
+  int n, head, nv;  // head elements before the first of nv vectors; no vector: head = n
+  bool bf16;
+  uint4 vec[kFlight];
 
-// Chunks in descending order: the ones that pass one read last are still in
-// the 129 MB L2 and are read from there before they are evicted.
-template <int CAP>
-__global__ void __launch_bounds__(kThreads)
-    clip_kernel(const __grid_constant__ ClipTable<CAP> a, const Sum* part, int parts,
-                float max_norm, float* norm) {
-  pdl_wait();
-  pdl_trigger();
-  const float2 ns = norm_and_scale(part, parts, max_norm);
-  const float scale = ns.y;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = ns.x;
-  const TensorTable<CAP>& t = a.t;
-  for (unsigned c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const unsigned r = t.chunks - 1 - c;
+  template <int CAP>
+  __device__ __forceinline__ ClipChunk(const ClipTable<CAP>& a, unsigned r) {
+    const TensorTable<CAP>& t = a.t;
     const int i = find_tensor(t, r);
     const long long at = static_cast<long long>(r - t.first[i]) * kChunk;
-    const int n = static_cast<int>(min(static_cast<long long>(kChunk), t.count[i] - at));
-    if (scale == 1.f && t.grad[i] == a.out[i]) continue;  // times one, in place
-    if (t.bf16[i])
-      scale_chunk(static_cast<const __nv_bfloat16*>(t.grad[i]) + at,
-                  static_cast<__nv_bfloat16*>(a.out[i]) + at, n, scale);
+    n = static_cast<int>(min(static_cast<long long>(kChunk), t.count[i] - at));
+    bf16 = t.bf16[i];
+    const int size = bf16 ? 2 : 4, per = 16 / size;
+    p = static_cast<const char*>(t.grad[i]) + at * size;
+    o = static_cast<char*>(a.out[i]) + at * size;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(p), oa = reinterpret_cast<uintptr_t>(o);
+    const int off = static_cast<int>(pa & 15u);
+    head = ((pa ^ oa) & 15u) != 0 ? n : off == 0 ? 0 : min(n, (16 - off) / size);
+    nv = (n - head) / per;
+    const uint4* pv = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + head * size);
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int v = threadIdx.x + k * kThreads;
+      if (v < nv) vec[k] = pv[v];
+    }
+  }
+
+  template <typename T>
+  __device__ __forceinline__ void scaled(float scale) const {
+    const T* g = static_cast<const T*>(p);
+    T* out = static_cast<T*>(o);
+    auto one = [&](T x) {
+      T r;
+      from_f(r, to_f(x) * scale);
+      return r;
+    };
+    Vec<T>* ov = reinterpret_cast<Vec<T>*>(out + head);
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int v = threadIdx.x + k * kThreads;
+      if (v >= nv) break;
+      Vec<T> q;
+      memcpy(&q, &vec[k], 16);
+#pragma unroll
+      for (int j = 0; j < Vec<T>::N; ++j) q.x[j] = one(q.x[j]);
+      ov[v] = q;
+    }
+    for (int i = threadIdx.x; i < head; i += kThreads) out[i] = one(g[i]);
+    for (int i = head + nv * Vec<T>::N + threadIdx.x; i < n; i += kThreads) out[i] = one(g[i]);
+  }
+};
+
+// Chunks in descending order: the ones that pass one read last are still in
+// the 129 MB L2 and are read from there before they are evicted.  The first one's
+// loads do not wait for pass one, which only reads the gradients: this launch
+// begins when that one's CTAs have begun, and by then all before it is done.
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kClipPerSm)
+    clip_kernel(const __grid_constant__ ClipTable<CAP> a, const Sum* part, int parts,
+                float max_norm, float* norm) {
+  const unsigned chunks = a.t.chunks;
+  float scale = 1.f;
+  for (unsigned c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const ClipChunk k(a, chunks - 1 - c);
+    if (c == blockIdx.x) {
+      pdl_wait();
+      pdl_trigger();
+      const float2 ns = norm_and_scale(part, parts, max_norm);
+      scale = ns.y;
+      if (c == 0 && threadIdx.x == 0) *norm = ns.x;
+    }
+    if (scale == 1.f && k.p == k.o) continue;  // times one, in place
+    if (k.bf16)
+      k.template scaled<__nv_bfloat16>(scale);
     else
-      scale_chunk(static_cast<const float*>(t.grad[i]) + at, static_cast<float*>(a.out[i]) + at, n,
-                  scale);
+      k.template scaled<float>(scale);
   }
 }
 
@@ -363,8 +407,8 @@ int fill_table(TensorTable<CAP>& t, int* index, int at, int n, const void* const
   return at;
 }
 
-int grid_for(unsigned chunks) {
-  const int most = std::min(kMaxCtas, kPerSm * sm_count());
+int grid_for(unsigned chunks, int per_sm) {
+  const int most = std::min(kMaxCtas, per_sm * sm_count());
   return static_cast<int>(std::min<unsigned>(chunks, static_cast<unsigned>(most)));
 }
 
@@ -378,7 +422,7 @@ cudaError_t sumsq_pass(int n, const void* const* grads, const int64_t* counts, c
   for (int at = 0; at < n;) {
     at = fill_table(t, index, at, n, grads, counts, dtypes);
     if (t.n == 0) continue;
-    const int grid = grid_for(t.chunks);
+    const int grid = grid_for(t.chunks, kSumPerSm);
     prof_begin("grad_sumsq", s);
     cudaError_t e =
         launch_pdl(sumsq_kernel<CAP>, dim3(grid), dim3(kThreads), 0, s, t, part + *parts);
@@ -410,8 +454,8 @@ cudaError_t clip_pass(int n, const void* const* grads, void* const* outs, const 
     if (a.t.n == 0) continue;
     for (int i = 0; i < a.t.n; ++i) a.out[i] = outs[index[i]];
     prof_begin("grad_clip", s);
-    e = launch_pdl(clip_kernel<CAP>, dim3(grid_for(a.t.chunks)), dim3(kThreads), 0, s, a,
-                   static_cast<const Sum*>(part), parts, max_norm, norm);
+    e = launch_pdl(clip_kernel<CAP>, dim3(grid_for(a.t.chunks, kClipPerSm)), dim3(kThreads), 0, s,
+                   a, static_cast<const Sum*>(part), parts, max_norm, norm);
     prof_end("grad_clip", s);
     if (e != cudaSuccess) return e;
   }
@@ -440,8 +484,8 @@ cudaError_t adam_pass(int n, float* const* theta, const void* const* grads, floa
       a.v[i] = v[index[i]];
     }
     prof_begin("adam_many", s);
-    e = launch_pdl(adam_many_kernel<CAP>, dim3(grid_for(a.t.chunks)), dim3(kThreads), 0, s, a, h,
-                   static_cast<const Sum*>(part), parts, max_norm, norm);
+    e = launch_pdl(adam_many_kernel<CAP>, dim3(grid_for(a.t.chunks, kAdamPerSm)), dim3(kThreads), 0,
+                   s, a, h, static_cast<const Sum*>(part), parts, max_norm, norm);
     prof_end("adam_many", s);
     if (e != cudaSuccess) return e;
   }
