@@ -87,25 +87,55 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
 }
 
-// dbias[c] = sum over the row blocks' partial sums, in order.
+// hi + lo += x, the rounding error of hi + x kept in lo (two-sum).
+__device__ __forceinline__ void add_to(float& hi, float& lo, float x) {
+  const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+  hi = s;
+}
+
+// dbias[c] = sum over the row blocks' partial sums, in order, as pairs of fp32
+// (fp64 runs at 1/64 of the rate); kDbiasFlight loads in flight per thread.
+// Enqueued behind the product, it runs on the SMs that the product's last round
+// leaves idle: it starts without waiting, since every kernel of the product
+// triggers its successor only after its own wait, when the sums are there, and
+// waits at its end, so that what follows it follows the product too.  It lets
+// its successor begin only then: CTAs that wait beside the product slow it down.
+// The backward of 2048 -> 5632, T = 8192, in a row: 161 us with this kernel before
+// the product, 157 behind it, 152 without the early trigger (166 in fp64).
+constexpr int kDbiasFlight = 8;
+
 __global__ void __launch_bounds__(kThreads)
     linear_dbias_kernel(const float* __restrict__ part, int blocks, int N,
-                        float* __restrict__ dbias) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ double sums[8][32];
+                        float* __restrict__ dbias, bool beside) {
+  if (!beside) pdl_wait();
+  __shared__ float2 sums[8][32];
   const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + tx;
-  double v = 0.0;
+  float hi = 0.f, lo = 0.f;
   if (c < N)
-    for (int b = ty; b < blocks; b += 8) v += part[static_cast<long long>(b) * N + c];
-  sums[ty][tx] = v;
+    for (int b0 = ty; b0 < blocks; b0 += 8 * kDbiasFlight) {
+      float p[kDbiasFlight];
+#pragma unroll
+      for (int i = 0; i < kDbiasFlight; ++i) {
+        const int b = b0 + 8 * i;
+        p[i] = b < blocks ? part[static_cast<long long>(b) * N + c] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kDbiasFlight; ++i) add_to(hi, lo, p[i]);
+    }
+  sums[ty][tx] = make_float2(hi, lo);
   __syncthreads();
   if (ty == 0 && c < N) {
-    v = sums[0][tx];
-    for (int w = 1; w < 8; ++w) v += sums[w][tx];
-    dbias[c] = static_cast<float>(v);
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      add_to(hi, lo, sums[w][tx].x);
+      lo = __fadd_rn(lo, sums[w][tx].y);
+    }
+    // an infinite hi has a lo that is NaN
+    dbias[c] = fabsf(hi) < INFINITY ? hi + lo : hi;
   }
+  if (beside) pdl_wait();
 }
 
 // The kernel of a function template over the activation, by its runtime value.
@@ -310,14 +340,15 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
                          : run_dz<float, 1>(dy, z, dz, ld_dz, part, T, d_out, act, s);
     if (e != cudaSuccess) return e;
   }
-  if (part != nullptr) {
+  const auto sum_dbias = [&]() {
+    if (part == nullptr) return cudaSuccess;
     prof_begin("linear_dbias", s);
     e = launch_pdl(linear_dbias_kernel, dim3((d_out + 31) / 32), dim3(kThreads), 0, s,
-                   static_cast<const float*>(part), plan.blocks, d_out, dbias);
+                   static_cast<const float*>(part), plan.blocks, d_out, dbias, dx != nullptr);
     prof_end("linear_dbias", s);
-    if (e != cudaSuccess) return e;
-  }
-  if (dx == nullptr) return cudaSuccess;
+    return e != cudaSuccess ? e : cudaGetLastError();
+  };
+  if (dx == nullptr) return sum_dbias();
   const void* grad = dz != nullptr ? dz : dy;
   LinearProduct g;
   g.A = grad;
@@ -335,7 +366,8 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
   g.N = d_in;
   g.K = d_out;
   g.tag = "linear_dgrad";
-  return is_bf16 ? run_product(g, s) : run_fp32(g, wp, s);
+  e = is_bf16 ? run_product(g, s) : run_fp32(g, wp, s);
+  return e != cudaSuccess ? e : sum_dbias();
 }
 
 }  // namespace poetx
