@@ -13,7 +13,8 @@
 // share of the weight is then read from shared memory once and not 16 times,
 // which bounded the other form (4096 x 4096, one token: 62 us).
 //
-// Few tiles: K is split over a cluster of up to 8 CTAs whose partial tiles are
+// Few tiles: K is split over a cluster of up to 8 CTAs (any number; powers of two
+// in the FLAT form) whose partial tiles are
 // added through distributed shared memory, in rank order, rank r finishing
 // the r-th share of the rows.
 #include <algorithm>
@@ -272,10 +273,13 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
     return;
   }
   cluster_sync();  // every slice's partial tile is written
-  const int share = TM / p.splits;  // splits divides TM (8 at least)
+  // FLAT: the slices divide its eight rows (any number of them costs registers
+  // that the main loop needs: 4096 x 4096, one token 25.8 us instead of 24)
+  const int share = FLAT ? TM / p.splits : (TM + p.splits - 1) / p.splits;
 #pragma unroll 1
   for (int e = threadIdx.x; e < share * 32; e += kThreads) {
     const int r = slice * share + e / 32, c = e % 32 * 4;
+    if (!FLAT && r >= TM) break;
     const uint32_t at = smem_u32(smem + r * kLdb + c);
     float4 q[kMaxSplits];
 #pragma unroll
@@ -300,8 +304,41 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
   cluster_sync();  // no CTA leaves while a peer still reads its tile
 }
 
+// How K is cut for a grid of some tiles.
+struct Slices {
+  int count, length;
+  double us;  // of the main loop
+};
+
+// Slices of whole K steps (`step`), so that the SM with the most CTAs has the
+// least to do: per_k us per k for one CTA, 1.9 times that for two, and 0.1 us per
+// slice for adding them up.  Clusters of up to six CTAs get an SM per CTA up to
+// 128 of 152 CTAs (64 tiles in two slices, 32 in four, 20 in six; 35 tiles in four
+// ran two to an SM while others stayed empty), clusters of seven or eight up to 64
+// (8 tiles in eight slices, not 12).  powers: powers of two only.
+Slices slices_for(long long tiles, int K, int step, double per_k, bool powers) {
+  Slices best = {};
+  for (int n = 1; n <= kMaxSplits; ++n) {
+    const int length = ((K + n - 1) / n + step - 1) / step * step;
+    const long long ctas = tiles * n, sms = sm_count();
+    if (n > 1 && ctas > 2 * sms) break;
+    if (powers && (n & (n - 1)) != 0) continue;
+    if (n > 1 && static_cast<long long>(length) * (n - 1) >= K) continue;  // an empty slice
+    const long long apart = n == 1 ? sms : n <= 6 ? sms * 128 / 152 : sms * 64 / 152;
+    const long long rounds = (ctas + 2 * sms - 1) / (2 * sms);
+    const double us =
+        per_k * length * (ctas <= apart ? 1.0 : 1.9 * static_cast<double>(rounds)) + 0.1 * n;
+    if (n == 1 || us < 0.97 * best.us) best = {n, length, us};
+  }
+  return best;
+}
+
+// us per k of a CTA's tile, measured (1024 of K in one slice).
+constexpr double kPerK8 = 0.105, kPerK4 = 0.067, kPerK2 = 0.052, kPerKFlat = 0.03;
+
 template <int RM, bool B_KN, bool FLAT>
-cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, cudaStream_t stream) {
+cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, double per_k,
+                   cudaStream_t stream) {
   using S = Shape<RM, FLAT>;
   auto* kernel = linear_simt_kernel<RM, B_KN, FLAT>;
   static std::atomic<bool> ready[64];
@@ -328,14 +365,10 @@ cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, cu
   p.vec_b = (B_KN ? g.N : g.K) % 4 == 0;
   const int n_tiles = (g.N + kTN - 1) / kTN;
   const long long m_tiles = (rows + S::TM - 1) / S::TM;
-  // slices of at least 64 of K while the grid still fits the CTAs that
-  // are resident at one time
-  int splits = 1;
-  while (splits < kMaxSplits && n_tiles * m_tiles * splits * 2 <= 2ll * sm_count() &&
-         g.K >= 128 * splits)
-    splits *= 2;
+  const Slices cut = slices_for(n_tiles * m_tiles, g.K, S::TK, per_k, FLAT);
+  const int splits = cut.count;
   p.splits = splits;
-  p.k_slice = ((g.K + splits - 1) / splits + S::TK - 1) / S::TK * S::TK;
+  p.k_slice = cut.length;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_tiles * splits), static_cast<unsigned>(m_tiles));
   cfg.blockDim = dim3(kThreads);
@@ -357,9 +390,10 @@ cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, cu
 }
 
 template <int RM, bool FLAT = false>
-cudaError_t by_major(const LinearProduct& g, long long m, long long rows, cudaStream_t s) {
-  return g.b_mn ? launch<RM, true, FLAT>(g, m, rows, s)
-               : launch<RM, false, FLAT>(g, m, rows, s);
+cudaError_t by_major(const LinearProduct& g, long long m, long long rows, double per_k,
+                     cudaStream_t s) {
+  return g.b_mn ? launch<RM, true, FLAT>(g, m, rows, per_k, s)
+               : launch<RM, false, FLAT>(g, m, rows, per_k, s);
 }
 
 }  // namespace
@@ -370,17 +404,22 @@ cudaError_t linear_simt(const LinearProduct& g, cudaStream_t s) {
   for (long long m = 0; m < g.M; m += kRows) {
     const long long rows = std::min(kRows, g.M - m);
     const long long tiles = (g.N + kTN - 1) / kTN;
+    const auto us = [&](int tm, int step, double per_k) {
+      return slices_for(tiles * ((rows + tm - 1) / tm), g.K, step, per_k, false).us;
+    };
     cudaError_t e;
-    // the fewest rows that hold the tokens; 64 and not 128 where tiles of 128,
-    // cut into eight K slices, would leave SMs without work
+    // the fewest rows that hold the tokens; beyond 64, tiles of 128 rows unless
+    // the main loop of 64 is clearly shorter (300 x 4096 -> 512: 51 against 71 us)
+    const bool half = rows <= 64 || us(64, Shape<4, false>::TK, kPerK4) <
+                                        0.93 * us(128, Shape<8, false>::TK, kPerK8);
     if (rows <= 16)
-      e = by_major<8, true>(g, m, rows, s);
+      e = by_major<8, true>(g, m, rows, kPerKFlat, s);
     else if (rows <= 32)
-      e = by_major<2>(g, m, rows, s);
-    else if (rows <= 64 || 8 * tiles * ((rows + 127) / 128) < sm_count())
-      e = by_major<4>(g, m, rows, s);
+      e = by_major<2>(g, m, rows, kPerK2, s);
+    else if (half)
+      e = by_major<4>(g, m, rows, kPerK4, s);
     else
-      e = by_major<8>(g, m, rows, s);
+      e = by_major<8>(g, m, rows, kPerK8, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
