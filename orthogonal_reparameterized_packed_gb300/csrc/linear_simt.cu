@@ -14,9 +14,8 @@
 // which bounded the other form (4096 x 4096, one token: 62 us).
 //
 // Few tiles: K is split over a cluster of up to 8 CTAs (any number; powers of two
-// in the FLAT form) whose partial tiles are
-// added through distributed shared memory, in rank order, rank r finishing
-// the r-th share of the rows.
+// in the FLAT form) whose partial tiles are added through distributed shared
+// memory, in rank order, rank r finishing the r-th share of the rows.
 #include <algorithm>
 #include <atomic>
 
