@@ -14,8 +14,9 @@
 // no lane needs another's elements to rotate; the G lanes of a row share only
 // the sums, and a warp works on 32 / G heads of a token at once: a group.  What
 // bounds it is memory traffic, 2 (forward) or 3 (backward) passes over q and k:
-// 16384 tokens of 40 heads of 128, bf16, take 55.5 us forward (6.0 TB/s) and 88
-// backward (5.7), in fp32 half as many tokens 54 and 85.
+// 16384 tokens of 40 heads of 128, bf16, take 55.7 us forward (6.0 TB/s) and 83.5
+// backward (6.0), in fp32 half as many tokens 54 and 82.6.  (Alternatives below
+// were measured before the sums of dgamma took their present form, 4 us less.)
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
   constexpr int R = 32 / G;
   extern __shared__ __align__(16) uint8_t smem[];
   Ring ring(smem);
-  __shared__ float acc[kMaxD];
+  __shared__ float acc[kWarps][kMaxD];
   const int lane = threadIdx.x % 32, li = lane % G, row = lane / G;
   const bool is_k = static_cast<int>(blockIdx.x) >= ctas_q;
   const Side<T> sd = side_of<T>(a, is_k);
@@ -751,33 +752,40 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
         for (int o = 16; o >= G; o >>= 1)
           sums[j][h][i] += __shfl_xor_sync(0xffffffffu, sums[j][h][i], o);
   }
-  for (int wp = 0; wp < kWarps; ++wp) {
-    if (threadIdx.x / 32 == wp && row == 0) {
+  if (row == 0) {
 #pragma unroll
-      for (int j = 0; j < NS; ++j) {
+    for (int j = 0; j < NS; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (w[j].has0) acc[w[j].o0 + i] = (wp == 0 ? 0.f : acc[w[j].o0 + i]) + sums[j][0][i];
-          if (w[j].has1) acc[w[j].o1 + i] = (wp == 0 ? 0.f : acc[w[j].o1 + i]) + sums[j][1][i];
-        }
+      for (int i = 0; i < V; ++i) {
+        if (w[j].has0) acc[threadIdx.x / 32][w[j].o0 + i] = sums[j][0][i];
+        if (w[j].has1) acc[threadIdx.x / 32][w[j].o1 + i] = sums[j][1][i];
       }
-    }
-    __syncthreads();
   }
+  __syncthreads();
   float* part = a.part + static_cast<long long>(blockIdx.x) * a.D;
-  for (int i = threadIdx.x; i < a.D; i += kThreads) part[i] = acc[i];
+  for (int i = threadIdx.x; i < a.D; i += kThreads) {
+    float v = acc[0][i];
+#pragma unroll
+    for (int wp = 1; wp < kWarps; ++wp) v += acc[wp][i];
+    part[i] = v;
+  }
 }
 
 // dgamma[i] = sum over the CTAs' partial sums in a fixed order: 32 features a
-// CTA, its eight warps take every eighth partial sum each.  In fp32: the few
-// hundred additions lose less than the partial sums did (in fp64, which this
-// GPU runs at 1/64 of the rate, the launch took 14 us instead of 2).
-__global__ void __launch_bounds__(kThreads)
+// CTA, its 32 warps take every 32nd partial sum each, all their loads in flight
+// (8 warps: backward of 1024 tokens 14.4 us, 32: 12.8; with the CTA's own sums in
+// one round instead of warp after warp 10.4).  In fp32: the few hundred additions lose less than the partial
+// sums did (in fp64, which this GPU runs at 1/64 of the rate, the launch took 14 us
+// instead of 2).
+constexpr int kGammaWarps = 32;
+constexpr int kGammaFlight = 10;
+
+__global__ void __launch_bounds__(32 * kGammaWarps)
     qk_dgamma_kernel(const float* part, int ctas_q, int ctas_k, int D, float* dgamma_q,
                      float* dgamma_k) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float sums[kWarps][32];
+  __shared__ float sums[kGammaWarps][32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int i = blockIdx.x * 32 + lane;
   const bool is_k = blockIdx.y != 0;
@@ -787,13 +795,21 @@ __global__ void __launch_bounds__(kThreads)
   const int ctas = is_k ? ctas_k : ctas_q;
   float v = 0.f;
   if (i < D)
-#pragma unroll 8
-    for (int c = warp; c < ctas; c += kWarps) v += p[static_cast<long long>(c) * D];
+    for (int c0 = warp; c0 < ctas; c0 += kGammaWarps * kGammaFlight) {
+      float x[kGammaFlight];
+#pragma unroll
+      for (int n = 0; n < kGammaFlight; ++n) {
+        const int c = c0 + n * kGammaWarps;
+        x[n] = c < ctas ? p[static_cast<long long>(c) * D] : 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < kGammaFlight; ++n) v += x[n];
+    }
   sums[warp][lane] = v;
   __syncthreads();
   if (warp != 0 || i >= D) return;
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) v += sums[w][lane];
+  for (int w = 1; w < kGammaWarps; ++w) v += sums[w][lane];
   out[i] = v;
 }
 
@@ -957,7 +973,7 @@ cudaError_t qk_norm_rope_backward(const QkNormRopeArgs& a, bool is_bf16, cudaStr
   if (a.dgamma_q == nullptr && a.dgamma_k == nullptr) return cudaGetLastError();
   prof_begin("qk_dgamma", s);
   e = launch_pdl(qk_dgamma_kernel, dim3((a.D + 31) / 32, a.hk > 0 ? 2 : 1),
-                 dim3(kThreads), 0, s, static_cast<const float*>(a.part), n.q, n.k, a.D,
+                 dim3(32 * kGammaWarps), 0, s, static_cast<const float*>(a.part), n.q, n.k, a.D,
                  a.dgamma_q, a.dgamma_k);
   prof_end("qk_dgamma", s);
   return e != cudaSuccess ? e : cudaGetLastError();
