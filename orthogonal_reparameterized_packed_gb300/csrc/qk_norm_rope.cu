@@ -446,8 +446,8 @@ struct Tables {
   __device__ __forceinline__ const float* sin() const { return cos() + pitch; }
 };
 
-// Groups of 32 / G heads of one token (q's, then k's), NS slots per lane.  gamma and the table row are multiplied once per token and side,
-// so that a value costs three operations: y_a = r (x_a (g_a c) - x_b (g_b s)).
+// Groups of 32 / G heads of one token (q's, then k's), NS slots per lane.  gamma
+// and the table row are multiplied once per token and side, so that a value costs three operations: y_a = r (x_a (g_a c) - x_b (g_b s)).
 template <typename T, int V, int G, int NS, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kThreads, NS == 1 ? kForwardPerSm : 1)
     qk_forward_kernel(const QkNormRopeArgs a) {
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
     out += R * a.D;
     turned = now.next();
   }
-  // the CTA's sum, warp by warp in order (rows of a warp by shuffles)
+  // the CTA's sum over its warps in order (rows of a warp by shuffles)
   float sums[NS][2][V];
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
@@ -774,9 +774,9 @@ __global__ void __launch_bounds__(kThreads, NS == 1 ? kBackwardPerSm : 1)
 // dgamma[i] = sum over the CTAs' partial sums in a fixed order: 32 features a
 // CTA, its 32 warps take every 32nd partial sum each, all their loads in flight
 // (8 warps: backward of 1024 tokens 14.4 us, 32: 12.8; with the CTA's own sums in
-// one round instead of warp after warp 10.4).  In fp32: the few hundred additions lose less than the partial
-// sums did (in fp64, which this GPU runs at 1/64 of the rate, the launch took 14 us
-// instead of 2).
+// one round instead of warp after warp 10.4).  In fp32: the few hundred additions
+// lose less than the partial sums did (in fp64, which this GPU runs at 1/64 of the
+// rate, the launch took 14 us instead of 2).
 constexpr int kGammaWarps = 32;
 constexpr int kGammaFlight = 10;
 
