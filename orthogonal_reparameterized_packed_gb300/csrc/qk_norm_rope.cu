@@ -447,7 +447,8 @@ struct Tables {
 };
 
 // Groups of 32 / G heads of one token (q's, then k's), NS slots per lane.  gamma
-// and the table row are multiplied once per token and side, so that a value costs three operations: y_a = r (x_a (g_a c) - x_b (g_b s)).
+// and the table row are multiplied once per token and side, so that a value costs
+// three operations: y_a = r (x_a (g_a c) - x_b (g_b s)).
 template <typename T, int V, int G, int NS, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kThreads, NS == 1 ? kForwardPerSm : 1)
     qk_forward_kernel(const QkNormRopeArgs a) {
