@@ -96,19 +96,17 @@ __device__ __forceinline__ void add_to(float& hi, float& lo, float x) {
 
 // dbias[c] = sum over the row blocks' partial sums, in order, as pairs of fp32
 // (fp64 runs at 1/64 of the rate); kDbiasFlight loads in flight per thread.
-// Enqueued behind the product, it runs on the SMs that the product's last round
-// leaves idle: it starts without waiting, since every kernel of the product
-// triggers its successor only after its own wait, when the sums are there, and
-// waits at its end, so that what follows it follows the product too.  It lets
-// its successor begin only then: CTAs that wait beside the product slow it down.
-// The backward of 2048 -> 5632, T = 8192, in a row: 161 us with this kernel before
-// the product, 157 behind it, 152 without the early trigger (166 in fp64).
+// It waits like every kernel, though the sums were complete before the product
+// began: what a grid two launches back wrote is visible only after the wait.  Its
+// CTAs get there while the product's last round runs; what follows begins behind
+// them.  The backward of 2048 -> 5632, T = 8192, in a graph: 157.5 us with this
+// kernel behind the product, 158.5 if it triggers early, 162 before the product.
 constexpr int kDbiasFlight = 8;
 
 __global__ void __launch_bounds__(kThreads)
     linear_dbias_kernel(const float* __restrict__ part, int blocks, int N,
-                        float* __restrict__ dbias, bool beside) {
-  if (!beside) pdl_wait();
+                        float* __restrict__ dbias) {
+  pdl_wait();
   __shared__ float2 sums[8][32];
   const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + tx;
@@ -135,7 +133,6 @@ __global__ void __launch_bounds__(kThreads)
     // an infinite hi has a lo that is NaN
     dbias[c] = fabsf(hi) < INFINITY ? hi + lo : hi;
   }
-  if (beside) pdl_wait();
 }
 
 // The kernel of a function template over the activation, by its runtime value.
@@ -344,7 +341,7 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
     if (part == nullptr) return cudaSuccess;
     prof_begin("linear_dbias", s);
     e = launch_pdl(linear_dbias_kernel, dim3((d_out + 31) / 32), dim3(kThreads), 0, s,
-                   static_cast<const float*>(part), plan.blocks, d_out, dbias, dx != nullptr);
+                   static_cast<const float*>(part), plan.blocks, d_out, dbias);
     prof_end("linear_dbias", s);
     return e != cudaSuccess ? e : cudaGetLastError();
   };
