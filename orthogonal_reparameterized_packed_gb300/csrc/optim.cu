@@ -298,19 +298,18 @@ struct ClipChunk {
 
 // Chunks in descending order: the ones that pass one read last are still in
 // the 129 MB L2 and are read from there before they are evicted.  The first one's
-// loads do not wait for pass one, which only reads the gradients: this launch
-// begins when that one's CTAs have begun, and by then all before it is done.
+// loads are on their way while the partial sums are added up.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, kClipPerSm)
     clip_kernel(const __grid_constant__ ClipTable<CAP> a, const Sum* part, int parts,
                 float max_norm, float* norm) {
+  pdl_wait();
+  pdl_trigger();
   const unsigned chunks = a.t.chunks;
   float scale = 1.f;
   for (unsigned c = blockIdx.x; c < chunks; c += gridDim.x) {
     const ClipChunk k(a, chunks - 1 - c);
     if (c == blockIdx.x) {
-      pdl_wait();
-      pdl_trigger();
       const float2 ns = norm_and_scale(part, parts, max_norm);
       scale = ns.y;
       if (c == 0 && threadIdx.x == 0) *norm = ns.x;

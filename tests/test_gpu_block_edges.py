@@ -50,3 +50,29 @@ def test_dbias_of_gradients_written_just_before(px, T, a, b, dtype):
     for i in range(n):
         assert all(torch.equal(p, q) for p, q in zip(got[i], want[i])), i
     assert len({float(w[1].double().sum()) for w in want}) == n
+
+
+@pytest.mark.parametrize("counts", [[5000, 3, 700], [8192] * 30, [20000] * 90])
+def test_clip_of_gradients_written_just_before(px, counts):
+    # 100 clips in a row, lists from fewer chunks than SMs on, each of values that a kernel
+    # writes right before it: the bits of the same clips one by one
+    from orthogonal_reparameterized_packed_gb300.block import PoetxGradClip
+    n, clip = 100, PoetxGradClip()
+    base = normal(sum(counts), seed=410)
+    now, out = torch.empty_like(base), torch.empty_like(base)
+    grads, outs = now.split(counts), out.split(counts)
+
+    def one(i):
+        torch.mul(base, 1.0 + i, out=now)
+        norm = clip.clip(grads, 0.5, out=outs)
+        return out.clone(), norm.clone()
+
+    want = []
+    for i in range(n):
+        want.append(one(i))
+        torch.cuda.synchronize()
+    got = [one(i) for i in range(n)]
+    status_ok(px)
+    for i in range(n):
+        assert all(torch.equal(p, q) for p, q in zip(got[i], want[i])), i
+    assert len({float(w[1]) for w in want}) == n
