@@ -419,7 +419,8 @@ struct Tables {
       positions(w);
       count = 0;
     }
-    const int p = __shfl_sync(0xffffffffu, position, count);  // and every lane has read the slot
+    const int p = __shfl_sync(0xffffffffu, position, count);
+    __syncwarp();  // every lane has read the slot (a shuffle orders no memory)
     ++count;
     ahead_slot = ahead_slot + 1 == SLOTS ? 0 : ahead_slot + 1;
     valid = p >= 0 ? valid | 1u << ahead_slot : valid & ~(1u << ahead_slot);

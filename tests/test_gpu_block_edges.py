@@ -76,3 +76,26 @@ def test_clip_of_gradients_written_just_before(px, counts):
     for i in range(n):
         assert all(torch.equal(p, q) for p, q in zip(got[i], want[i])), i
     assert len({float(w[1]) for w in want}) == n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,D", [(1, 128), (1, 96), (2, 64)])
+def test_every_group_of_heads_begins_a_token(px, heads, D, dtype):
+    # one group of heads per token: every step of a warp takes the table's next row into the
+    # ring and reads the one before; the bits of the same tokens in one call of their own
+    from orthogonal_reparameterized_packed_gb300.block import PoetxQKNormRope, rope_tables
+    T = 9001
+    cos, sin = rope_tables(T, D)
+    q, dq = (normal(T, heads * D, seed=420 + i) for i in range(2))
+    q, dq = (t.to(torch.bfloat16) if dtype == "bf16" else t for t in (q, dq))
+    none = q[:, :0]
+    step = PoetxQKNormRope(heads, 0, D, T, dtype=dtype, backward=True)
+    y = step.forward(q, none, None, None, cos, sin)[0].clone()
+    dx = step.backward(dq, none, q, none, None, None, cos, sin)[0].clone()
+    at = torch.arange(T, dtype=torch.int32, device="cuda")
+    for t0 in range(0, T, 700):
+        s = slice(t0, min(T, t0 + 700))
+        assert torch.equal(step.forward(q[s], none, None, None, cos, sin, at[s])[0], y[s])
+        assert torch.equal(step.backward(dq[s], none, q[s], none, None, None, cos, sin,
+                                         at[s])[0], dx[s])
+    status_ok(px)
