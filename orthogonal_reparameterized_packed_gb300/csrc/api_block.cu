@@ -81,7 +81,7 @@ extern "C" {
 size_t poetx_linear_forward_workspace_size(int d_in, int d_out, int64_t tokens,
                                            poetx_dtype dtype) {
   if (!linear_dims_ok(d_in, d_out, tokens, dtype) || tokens == 0) return 0;
-  return linear_forward_scratch(d_in, d_out, tokens, dtype == POETX_BF16);
+  return linear_forward_scratch(d_in, d_out, tokens, dtype == POETX_BF16, true);
 }
 
 poetx_status poetx_linear_forward(const void* x, const void* W, const float* bias,
@@ -97,8 +97,9 @@ poetx_status poetx_linear_forward(const void* x, const void* W, const float* bia
                         static_cast<const void*>(y), static_cast<const void*>(z_saved)})
     if (!aligned(p, 16)) return POETX_ERR_INVALID_ARG;
   const bool is_bf16 = dtype == POETX_BF16;
-  const poetx_status st = check_workspace(linear_forward_scratch(d_in, d_out, tokens, is_bf16),
-                                          workspace, workspace_bytes);
+  const poetx_status st =
+      check_workspace(linear_forward_scratch(d_in, d_out, tokens, is_bf16, false), workspace,
+                      workspace_bytes);
   if (st != POETX_OK) return st;
   return to_status(linear_forward(x, W, bias, residual, y, z_saved, d_in, d_out, tokens, act,
                                   is_bf16, workspace, static_cast<cudaStream_t>(stream)));
@@ -108,7 +109,8 @@ size_t poetx_linear_backward_workspace_size(int d_in, int d_out, int64_t tokens,
                                             poetx_activation act, poetx_dtype dtype,
                                             int with_dbias) {
   if (!linear_dims_ok(d_in, d_out, tokens, dtype) || !act_ok(act) || tokens == 0) return 0;
-  return linear_backward_scratch(d_in, d_out, tokens, act, dtype == POETX_BF16, with_dbias != 0);
+  return linear_backward_scratch(d_in, d_out, tokens, act, dtype == POETX_BF16, with_dbias != 0,
+                                 true);
 }
 
 poetx_status poetx_linear_backward(const void* dy, const void* z_saved, const void* W, void* dx,
@@ -129,8 +131,8 @@ poetx_status poetx_linear_backward(const void* dy, const void* z_saved, const vo
     if (!aligned(p, 16)) return POETX_ERR_INVALID_ARG;
   const bool is_bf16 = dtype == POETX_BF16;
   const poetx_status st = check_workspace(
-      linear_backward_scratch(d_in, d_out, tokens, act, is_bf16, dbias != nullptr), workspace,
-      workspace_bytes);
+      linear_backward_scratch(d_in, d_out, tokens, act, is_bf16, dbias != nullptr, false),
+      workspace, workspace_bytes);
   if (st != POETX_OK) return st;
   return to_status(linear_backward(dy, z_saved, W, dx, dbias, d_in, d_out, tokens, act, is_bf16,
                                    workspace, s));

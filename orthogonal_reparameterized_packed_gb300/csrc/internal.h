@@ -295,14 +295,15 @@ cudaError_t launch_f32_to_bf16(const float* in, long long count, __nv_bfloat16* 
 // z = x W^T + bias, y = act(z) + residual and its gradients (linear.cu); act
 // is a poetx_activation.  x [T][d_in], W [d_out][d_in], y / residual / z
 // [T][d_out] in the working type (is_bf16), bias [d_out] fp32; bias, residual
-// and z may be null.  `scratch` holds linear_forward_scratch bytes.
-size_t linear_forward_scratch(int d_in, int d_out, long long T, bool is_bf16);
+// and z may be null.  `scratch` holds linear_forward_scratch bytes; with `fewer`
+// these are enough for every call of at most T tokens, without it for calls of T.
+size_t linear_forward_scratch(int d_in, int d_out, long long T, bool is_bf16, bool fewer);
 cudaError_t linear_forward(const void* x, const void* W, const float* bias, const void* residual,
                            void* y, void* z, int d_in, int d_out, long long T, int act,
                            bool is_bf16, void* scratch, cudaStream_t s);
 // dz = dy act'(z); dx = dz W, dbias = sum_t dz (either may be null).
 size_t linear_backward_scratch(int d_in, int d_out, long long T, int act, bool is_bf16,
-                               bool with_dbias);
+                               bool with_dbias, bool fewer);
 cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* dx, float* dbias,
                             int d_in, int d_out, long long T, int act, bool is_bf16,
                             void* scratch, cudaStream_t s);

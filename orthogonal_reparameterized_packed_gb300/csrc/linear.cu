@@ -237,15 +237,16 @@ cudaError_t run_product(const LinearProduct& g, cudaStream_t s) {
 
 namespace {
 
-// fp32: the scratch and the run of a product [M][K] x [K][N] (b_mn as in LinearProduct).
-size_t fp32_scratch(long long M, int N, int K, bool b_mn) {
-  if (!linear_split_pays(M, N, K)) return 0;
+// fp32: the scratch and the run of a product [M][K] x [K][N] (b_mn as in
+// LinearProduct); fewer: the scratch that every product of up to M rows fits.
+size_t fp32_scratch(long long M, int N, int K, bool b_mn, bool fewer) {
   LinearProduct g;
   g.M = M;
   g.N = N;
   g.K = K;
   g.b_mn = b_mn;
-  return linear_split_scratch(g);
+  if (fewer) return linear_split_scratch_up_to(g);
+  return linear_split_pays(M, N, K) ? linear_split_scratch(g) : 0;
 }
 
 cudaError_t run_fp32(const LinearProduct& g, void* scratch, cudaStream_t s) {
@@ -256,9 +257,9 @@ cudaError_t run_fp32(const LinearProduct& g, void* scratch, cudaStream_t s) {
 
 // bf16: padded copies of x and W where d_in is no multiple of 8; fp32: the
 // planes of x and W where the product runs on the tensor cores.
-size_t linear_forward_scratch(int d_in, int d_out, long long T, bool is_bf16) {
+size_t linear_forward_scratch(int d_in, int d_out, long long T, bool is_bf16, bool fewer) {
   return is_bf16 ? pad_bytes(T, d_in) + pad_bytes(d_out, d_in)
-                 : fp32_scratch(T, d_out, d_in, false);
+                 : fp32_scratch(T, d_out, d_in, false, fewer);
 }
 
 cudaError_t linear_forward(const void* x, const void* W, const float* bias, const void* residual,
@@ -296,7 +297,8 @@ namespace {
 struct BackwardPlan {
   size_t dz = 0, part = 0, w = 0;
   int blocks;
-  BackwardPlan(int d_in, int d_out, long long T, int act, bool is_bf16, bool with_dbias) {
+  BackwardPlan(int d_in, int d_out, long long T, int act, bool is_bf16, bool with_dbias,
+               bool fewer) {
     blocks = static_cast<int>((T + kDzRows - 1) / kDzRows);
     if (is_bf16) {
       if (act != POETX_ACT_NONE || d_out % 8 != 0)
@@ -304,7 +306,7 @@ struct BackwardPlan {
       w = pad_bytes(d_out, d_in);
     } else {
       if (act != POETX_ACT_NONE) dz = round256(static_cast<size_t>(T) * d_out * 4);
-      w = fp32_scratch(T, d_in, d_out, true);
+      w = fp32_scratch(T, d_in, d_out, true, fewer);
     }
     if (with_dbias) part = round256(static_cast<size_t>(blocks) * d_out * 4);
   }
@@ -314,14 +316,14 @@ struct BackwardPlan {
 }  // namespace
 
 size_t linear_backward_scratch(int d_in, int d_out, long long T, int act, bool is_bf16,
-                               bool with_dbias) {
-  return BackwardPlan(d_in, d_out, T, act, is_bf16, with_dbias).bytes();
+                               bool with_dbias, bool fewer) {
+  return BackwardPlan(d_in, d_out, T, act, is_bf16, with_dbias, fewer).bytes();
 }
 
 cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* dx, float* dbias,
                             int d_in, int d_out, long long T, int act, bool is_bf16,
                             void* scratch, cudaStream_t s) {
-  const BackwardPlan plan(d_in, d_out, T, act, is_bf16, dbias != nullptr);
+  const BackwardPlan plan(d_in, d_out, T, act, is_bf16, dbias != nullptr, false);
   char* at = static_cast<char*>(scratch);
   void* dz = plan.dz > 0 && dx != nullptr ? at : nullptr;  // null: not stored
   float* part = plan.part > 0 ? reinterpret_cast<float*>(at + plan.dz) : nullptr;

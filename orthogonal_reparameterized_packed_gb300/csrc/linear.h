@@ -42,6 +42,7 @@ cudaError_t linear_simt(const LinearProduct& g, cudaStream_t s);
 // as for linear_simt, scratch of linear_split_scratch(g) bytes.
 bool linear_split_pays(long long M, int N, int K);
 size_t linear_split_scratch(const LinearProduct& g);
+size_t linear_split_scratch_up_to(const LinearProduct& g);  // of any product of at most g.M rows
 cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s);
 
 }  // namespace poetx

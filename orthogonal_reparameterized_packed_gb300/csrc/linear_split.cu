@@ -550,6 +550,21 @@ size_t linear_split_scratch(const LinearProduct& g) {
   return flag_bytes(g) + planes_bytes(g.M, g.K) + planes_bytes(b_plane_rows(g), b_cols(g));
 }
 
+// Whether this form is taken does not grow with the rows: a new pair of row tiles
+// can add a round over the clusters, and linear_simt wins.  But within a pair both
+// costs are linear in the rows, so its first and its last row decide; the scratch
+// grows with the rows, so the last pair that has any bounds it.
+size_t linear_split_scratch_up_to(const LinearProduct& g) {
+  LinearProduct at = g;
+  while (at.M > 0) {
+    const long long first = (at.M - 1) / (2 * BM) * (2 * BM) + 1;
+    if (linear_split_pays(at.M, g.N, g.K) || linear_split_pays(first, g.N, g.K))
+      return linear_split_scratch(at);
+    at.M = first - 1;
+  }
+  return 0;
+}
+
 cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) {
   SplitOperand a, b;
   int* flags = static_cast<int*>(scratch);

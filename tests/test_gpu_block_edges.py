@@ -99,3 +99,36 @@ def test_every_group_of_heads_begins_a_token(px, heads, D, dtype):
         assert torch.equal(step.backward(dq[s], none, q[s], none, None, None, cos, sin,
                                          at[s])[0], dx[s])
     status_ok(px)
+
+
+# (tokens, d_in, d_out) for which a product of these tokens takes more scratch than one of
+# tokens + 1 (tensor cores with 256 tokens, CUDA cores with 257)
+STEPS = [(256, 256, 6400), (256, 256, 6144), (512, 256, 6400), (300, 1000, 2000)]
+
+
+@pytest.mark.parametrize("T,a,b", STEPS)
+def test_fp32_layer_takes_fewer_tokens_than_it_holds(px, T, a, b):
+    # results are those of a layer made for the tokens, both ways, at every capacity
+    from orthogonal_reparameterized_packed_gb300.block import PoetxLinear
+    x, W = normal(T, a, seed=430), normal(b, a, seed=431, scale=a ** -0.5)
+    dy, V = normal(T, a, seed=432), normal(a, b, seed=433, scale=b ** -0.5)
+    want = PoetxLinear(a, b, T, dtype="f32").forward(x, W)
+    back = [t.clone() for t in PoetxLinear(b, a, T, dtype="f32", backward=True).backward(dy, V)]
+    for more in (1, 2, 40, 1000):
+        layer = PoetxLinear(a, b, T + more, dtype="f32")
+        assert torch.equal(layer.forward(x, W), want)
+        layer = PoetxLinear(b, a, T + more, dtype="f32", backward=True)
+        assert all(torch.equal(p, q) for p, q in zip(layer.backward(dy, V), back))
+    status_ok(px)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("a,b", [(256, 6400), (6400, 256), (5120, 320), (78, 3050), (147, 1098),
+                                 (1000, 999), (4096, 4096), (33, 7)])
+def test_workspace_of_more_tokens_serves_fewer(px, a, b, dtype):
+    code = px.BF16 if dtype == "bf16" else px.F32
+    for size in (lambda t: px.poetx_linear_forward_workspace_size(a, b, t, code),
+                 lambda t: px.poetx_linear_backward_workspace_size(a, b, t, 2, code),
+                 lambda t: px.poetx_linear_backward_workspace_size(a, b, t, 0, code, False)):
+        sizes = [size(t) for t in [*range(1, 1100), 5000, 5001, 1 << 20, 1 << 22]]
+        assert all(p <= q for p, q in zip(sizes, sizes[1:]))
