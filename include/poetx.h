@@ -260,7 +260,8 @@ poetx_status poetx_dequantize_w0(const int8_t* W0_q, const float* scales, void* 
  *   dz_t = dy_t act'(z_t),   dx_t = W^T dz_t,   dbias = sum_t dz_t
  *   BF16 rounds dz to bf16, the type the tensor cores take; dbias sums the
  *   unrounded dz in fp32.  z_saved is not read (may be NULL) when act is
- *   NONE.  dx or dbias may be NULL.  RELU'(0) = 0.
+ *   NONE.  dx or dbias may be NULL.  RELU: dz is 0 wherever z is not above 0,
+ *   whatever dy is there.
  * GELU is z Phi(z); GELU_TANH its tanh approximation
  *   z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).
  * 1 <= d_in, d_out <= 2^20, any values (BF16 rows that are not a multiple of

@@ -44,10 +44,9 @@ __device__ __forceinline__ float act_f(float z) {
   return z;
 }
 
-// d act / dz; relu: 0 at z = 0
+// d act / dz, but for relu (act_grad)
 template <int ACT, bool FAST>
 __device__ __forceinline__ float act_df(float z) {
-  if (ACT == POETX_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   if (ACT == POETX_ACT_SILU) {
     const float s = sigmoid_f<FAST>(z);
     return s * (1.f + z * (1.f - s));
@@ -61,6 +60,15 @@ __device__ __forceinline__ float act_df(float z) {
     return s + 2.f * z * s * (1.f - s) * 0.7978845608028654f * fmaf(0.134145f * z, z, 1.f);
   }
   return 1.f;
+}
+
+// dy act'(z).  relu selects: where z is not above 0 (0 and NaN among them) the
+// gradient is 0, an infinite or NaN dy too, which a product with 0 would keep.
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act_grad(float dy, float z) {
+  if (ACT == POETX_ACT_NONE) return dy;
+  if (ACT == POETX_ACT_RELU) return z > 0.f ? dy : 0.f;
+  return dy * act_df<ACT, FAST>(z);
 }
 
 }  // namespace poetx

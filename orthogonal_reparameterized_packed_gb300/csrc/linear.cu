@@ -64,8 +64,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       if (ACT != POETX_ACT_NONE) zz = *reinterpret_cast<const Pack<T, V>*>(zp + at);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        float d = to_f(g.x[j]);
-        if (ACT != POETX_ACT_NONE) d *= act_df<ACT, FAST>(to_f(zz.x[j]));
+        const float d = act_grad<ACT, FAST>(to_f(g.x[j]), to_f(zz.x[j]));
         sum[j] += d;
         from_f(g.x[j], d);
       }

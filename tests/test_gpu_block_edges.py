@@ -132,3 +132,30 @@ def test_workspace_of_more_tokens_serves_fewer(px, a, b, dtype):
                  lambda t: px.poetx_linear_backward_workspace_size(a, b, t, 0, code, False)):
         sizes = [size(t) for t in [*range(1, 1100), 5000, 5001, 1 << 20, 1 << 22]]
         assert all(p <= q for p, q in zip(sizes, sizes[1:]))
+
+
+def through_identity(px, dtype, act, z, dy, sums=True):
+    """(dx, dbias) of a layer with the unit weight: dz itself, rounded, and its sums."""
+    from orthogonal_reparameterized_packed_gb300.block import PoetxLinear
+    T, n = z.shape
+    layer = PoetxLinear(n, n, T, act=act, dtype=dtype, backward=True)
+    dx, dbias = layer.backward(dy, torch.eye(n, device="cuda", dtype=layer.dtype), z=z)
+    status_ok(px)
+    return dx, dbias
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,n", [(5, 64), (70, 72), (1000, 520)])
+def test_relu_passes_no_gradient_where_it_is_zero(px, T, n, dtype):
+    # infinite and NaN gradients at z <= 0 and at NaN: dz = 0 there, as the definition selects
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    z, dy = normal(T, n, seed=440).to(tdt), normal(T, n, seed=441).to(tdt)
+    z[0, 1], z[1, 2], z[T - 1, n - 1] = 0.0, float("-inf"), float("nan")
+    off = ~(z > 0)
+    want = torch.where(off, torch.zeros_like(dy), dy)
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        spoilt = torch.where(off, torch.full_like(dy, bad), dy)
+        dx, dbias = through_identity(px, dtype, "relu", z, spoilt)
+        assert torch.equal(dx, want)
+        clean = through_identity(px, dtype, "relu", z, want)[1]
+        assert torch.equal(dbias, clean)
