@@ -159,3 +159,17 @@ def test_relu_passes_no_gradient_where_it_is_zero(px, T, n, dtype):
         assert torch.equal(dx, want)
         clean = through_identity(px, dtype, "relu", z, want)[1]
         assert torch.equal(dbias, clean)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_gradient_of_large_finite_values(px, act, dtype):
+    # far from zero every activation's slope is 1 or 0, whatever leaves the range on the way
+    # (silu's and gelu's slope is 1 + z e^-z .. there: within 1e-40 of 1 from z = 100 on)
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    top = float(torch.finfo(tdt).max)
+    z = torch.tensor([1e2, 1e4, 1e10, 1e18, 1.9e19, 1e20, 1e30, top], device="cuda").repeat(5, 8)
+    for sign, slope in ((1, 1.0), (-1, 0.0)):
+        dx, dbias = through_identity(px, dtype, act, (sign * z).to(tdt),
+                                     torch.ones_like(z).to(tdt))
+        assert torch.all(dx == slope) and torch.all(dbias == 5 * slope)
