@@ -56,9 +56,9 @@ __device__ __forceinline__ float act_df(float z) {
     return fmaf(z * 0.3989422804014327f, e, normal_cdf<FAST>(z, e));
   }
   if (ACT == POETX_ACT_GELU_TANH) {
-    // s (1 - s) is 0 from |z| = 11 on; z^2, which may leave the range, must not undo it
+    // s (1 - s) is 0 from |z| = 11 on and comes first; z^2 must not leave the range
     const float s = sigmoid_f<FAST>(2.f * gelu_u(z)), zz = fminf(z * z, 1e30f);
-    return s + 2.f * z * s * (1.f - s) * 0.7978845608028654f * fmaf(0.134145f, zz, 1.f);
+    return s + s * (1.f - s) * z * (2.f * 0.7978845608028654f * fmaf(0.134145f, zz, 1.f));
   }
   return 1.f;
 }
