@@ -173,3 +173,22 @@ def test_gradient_of_large_finite_values(px, act, dtype):
         dx, dbias = through_identity(px, dtype, act, (sign * z).to(tdt),
                                      torch.ones_like(z).to(tdt))
         assert torch.all(dx == slope) and torch.all(dbias == 5 * slope)
+
+
+def test_gelu_is_relatively_accurate_in_its_tail(px):
+    # bf16: z Phi(z) from -0.5 down to where it leaves bf16's normal range, through the unit
+    # weight.  Phi's approximation is within 2^-13 relative, its exponential within
+    # |z^2 / 2| 2^-23 of argument and quotient errors (2^-16 at z = -12.5), the result is
+    # rounded once (2^-8); z + 0 is exact.
+    from math import erfc
+    from orthogonal_reparameterized_packed_gb300.block import PoetxLinear
+    n = 64
+    for T in (16, 1000):
+        x = torch.linspace(-12.5, -0.5, T * n, device="cuda").view(T, n).bfloat16()
+        layer = PoetxLinear(n, n, T, act="gelu")
+        y = layer.forward(x, torch.eye(n, device="cuda", dtype=torch.bfloat16))
+        status_ok(px)
+        x64 = x.double().cpu().numpy()
+        want = x64 * 0.5 * np.vectorize(erfc)(-x64 / np.sqrt(2))
+        off = np.abs(y.double().cpu().numpy() / want - 1)
+        assert off.max() <= 2.0 ** -8 + 2.0 ** -12, (off.max(), x64.flat[off.argmax()])
