@@ -268,7 +268,7 @@ poetx_status poetx_dequantize_w0(const int8_t* W0_q, const float* scales, void* 
  * 8 features are copied to aligned rows first).
  * F32 accumulates in fp32; large products run on the tensor cores, each
  * operand as three bf16 parts (24 bits), tokens or weights with values that
- * are not finite on the CUDA cores.
+ * are not finite, above 2^60 or (but for 0) below 2^-109 on the CUDA cores.
  * The workspace of `tokens` tokens is large enough for any fewer.
  * ------------------------------------------------------------------------ */
 typedef enum {

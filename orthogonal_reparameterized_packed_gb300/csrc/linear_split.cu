@@ -10,11 +10,15 @@
 // registers with round-to-nearest: 2e-7 to 4e-7 of the result, as a plain fp32
 // product has (cuBLAS: 4e-7 to 1e-6 on the same inputs).
 //
-// x and W are split into three bf16 planes each in the workspace first.  Where
-// a value is not finite (or its rounding to bf16 is not) the planes cannot
-// express it: the split sets the flag of its token (of all, where it is W's),
-// this kernel leaves those rows alone and linear_simt, enqueued behind it,
-// computes them; its tiles without such rows return at once.
+// x and W are split into three bf16 planes each in the workspace first, which
+// takes 0 and magnitudes from 2^-109 to 2^60.  Below, the third plane's bits fall
+// under bf16's smallest number, 2^-133; up to 2^60, 128 products of two stay
+// under 2^128, so that no partial sum meets an infinite one of the other sign (beyond,
+// a product of small parts can leave the range before the main one does, and the
+// infinity had the wrong sign).  Where a value is outside, or not finite, the
+// split sets the flag of its token (of all, where it is W's), this kernel leaves
+// those rows alone and linear_simt, enqueued behind it, computes them; its tiles
+// without such rows return at once.
 //
 // The kernel is linear_pair's with another epilogue: CTA pairs, 256 x 256 or
 // 256 x 128 tiles, 64-wide K steps in a TMA ring, one step per pair of planes;
@@ -353,9 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // One operand: in [rows][cols] fp32 -> planes [3][plane_rows][pitch] bf16, rows
 // from `rows` to plane_rows zero (columns past cols are not read by any tile);
-// flag[r][segs]: whether a value of the row's segment of kSegment columns has
-// planes that are not finite.
+// flag[r][segs]: whether a value of the row's segment of kSegment columns is
+// neither 0 nor of a magnitude that the planes take.
 constexpr int kSegment = 1024;
+constexpr unsigned kLeastBits = (127u - 109u) << 23, kMostBits = (127u + 60u) << 23;
 
 struct SplitOperand {
   const float* in;
@@ -399,13 +404,17 @@ __global__ void __launch_bounds__(kSplitThreads)
         }
       }
 #pragma unroll
+      for (int j = 0; j < 4; ++j) {  // infinities and NaN have larger bits than 2^60
+        const unsigned u = __float_as_uint(v[j]) & 0x7fffffffu;
+        bad |= u != 0 && u - kLeastBits > kMostBits - kLeastBits;
+      }
+#pragma unroll
       for (int s = 0; s < kPlanes; ++s) {
         uint32_t w[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * h], v[2 * h + 1]);
           const float2 f = __bfloat1622float2(q);
-          if (s == 0) bad |= !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
           v[2 * h] -= f.x;  // exact: the rounding error of a bf16 rounding
           v[2 * h + 1] -= f.y;
           w[h] = *reinterpret_cast<const uint32_t*>(&q);

@@ -192,3 +192,69 @@ def test_gelu_is_relatively_accurate_in_its_tail(px):
         want = x64 * 0.5 * np.vectorize(erfc)(-x64 / np.sqrt(2))
         off = np.abs(y.double().cpu().numpy() / want - 1)
         assert off.max() <= 2.0 ** -8 + 2.0 ** -12, (off.max(), x64.flat[off.argmax()])
+
+
+def fp32_product(px, x, W, residual=None, inplace=False):
+    """x W^T (+ residual) and the magnitudes' sums, in 64 bits too."""
+    from orthogonal_reparameterized_packed_gb300.block import PoetxLinear
+    layer = PoetxLinear(x.shape[1], W.shape[0], x.shape[0], dtype="f32")
+    y = layer.forward(x, W, residual=residual)
+    status_ok(px)
+    x64, W64 = x.double().cpu().numpy(), W.double().cpu().numpy()
+    return y.double().cpu().numpy(), x64 @ W64.T, np.abs(x64) @ np.abs(W64).T
+
+
+# fp32 sizes of the tensor cores, [N][K] weights
+LARGE = [(1301, 517, 1303), (700, 2056, 1024)]
+
+
+@pytest.mark.parametrize("T,a,b", LARGE)
+@pytest.mark.parametrize("exponent", [-126, -120, -114, -110, -109, -108, -100, -60, 59, 61, 80])
+def test_fp32_rows_of_any_size_keep_24_bits(px, T, a, b, exponent):
+    # a few tokens of this size among others of size 1, weights of the opposite size, so that
+    # no product leaves the normal range; K 2^-23 of the magnitudes' sum, as every fp32 sum
+    x, W = normal(T, a, seed=450), normal(b, a, seed=451, scale=a ** -0.5)
+    far = [0, 3, T // 2, T - 1]
+    x[far] = torch.rand((len(far), a), device="cuda") * 2.0 ** exponent + 2.0 ** exponent
+    if abs(exponent) > 100:
+        W *= 2.0 ** 40
+    y, want, S = fp32_product(px, x, W)
+    assert np.all(np.abs(y - want) <= (a + 4) * 2.0 ** -23 * S)
+    # far fewer bits would be lost than the bound allows: also on the average of a row
+    for t in far:
+        assert np.linalg.norm(y[t] - want[t]) <= 1e-6 * np.linalg.norm(want[t])
+
+
+@pytest.mark.parametrize("T,a,b", LARGE)
+def test_fp32_weights_of_any_size_keep_24_bits(px, T, a, b):
+    x, W = normal(T, a, seed=452), normal(b, a, seed=453)
+    for small in (1.5e-38, 3e-34, 5e19):
+        V = W.clone()
+        V[7] *= small
+        y, want, S = fp32_product(px, x, V)
+        assert np.all(np.abs(y - want) <= (a + 4) * 2.0 ** -23 * S + a * 2.0 ** -149)
+
+
+@pytest.mark.parametrize("T,a,b", LARGE)
+def test_fp32_products_beyond_the_range_are_infinite(px, T, a, b):
+    # one product each of a sign, far beyond fp32, in values just under a bf16 number (whose
+    # second parts have the other sign); the rest of the row is small
+    x, W = normal(T, a, seed=454), normal(b, a, seed=455)
+    x[5, 9] = 3e38 * (1 - 2.0 ** -12)
+    W[:, 9] = W[:, 9].sign() * 1e6 * (1 - 2.0 ** -12)
+    x[:, 9].mul_((torch.arange(T, device="cuda") == 5).float())
+    y, want, _ = fp32_product(px, x, W)
+    assert np.array_equal(y[5], np.sign(W[:, 9].double().cpu().numpy()) * np.inf)
+    keep = [t for t in range(T) if t != 5]
+    assert np.isfinite(y[keep]).all()
+
+
+@pytest.mark.parametrize("T,a,b", LARGE)
+def test_fp32_products_near_the_bottom_of_the_range(px, T, a, b):
+    # both operands inside what the tensor cores take, products of 2^-120: each of the six sums
+    # of a product's parts is rounded to a multiple of 2^-149, and truncated up to once more
+    x, W = normal(T, a, seed=456) * 2.0 ** -70, normal(b, a, seed=457) * 2.0 ** -50
+    y, want, S = fp32_product(px, x, W)
+    bottom = 12 * a * 2.0 ** -149
+    assert np.all(np.abs(y - want) <= (a + 4) * 2.0 ** -23 * S + bottom)
+    assert np.linalg.norm(y - want) <= 1e-6 * np.linalg.norm(want) + bottom * want.size ** 0.5
