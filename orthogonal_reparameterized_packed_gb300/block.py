@@ -133,7 +133,9 @@ class PoetxQKNormRope:
         if backward:
             self.dq, self.dk = rows(n_q_heads), rows(n_k_heads)
             self.dgamma_q = torch.empty((head_dim,), dtype=torch.float32, device=dev)
-            self.dgamma_k = torch.empty((head_dim,), dtype=torch.float32, device=dev)
+            # without key heads no call writes it: the sum over no rows
+            self.dgamma_k = (torch.empty if n_k_heads else torch.zeros)(
+                (head_dim,), dtype=torch.float32, device=dev)
             ws = poetx_qk_norm_rope_backward_workspace_size(n_q_heads, n_k_heads, head_dim,
                                                             tokens, self.code)
             self.workspace = torch.empty((max(ws, 16),), dtype=torch.uint8, device=dev)

@@ -258,3 +258,18 @@ def test_fp32_products_near_the_bottom_of_the_range(px, T, a, b):
     bottom = 12 * a * 2.0 ** -149
     assert np.all(np.abs(y - want) <= (a + 4) * 2.0 ** -23 * S + bottom)
     assert np.linalg.norm(y - want) <= 1e-6 * np.linalg.norm(want) + bottom * want.size ** 0.5
+
+
+def test_no_key_heads_have_no_gradient(px):
+    # dgamma_k of a step without key heads: the sum over no rows, not what the memory held
+    from orthogonal_reparameterized_packed_gb300.block import PoetxQKNormRope, rope_tables
+    D, T = 64, 20
+    stale = [torch.full((D,), 7.0, device="cuda") for _ in range(8)]
+    del stale
+    step = PoetxQKNormRope(2, 0, D, T, dtype="f32", backward=True)
+    q, dq = normal(T, 2 * D, seed=460), normal(T, 2 * D, seed=461)
+    dk, dgamma_k = step.backward(dq, dq[:, :0], q, q[:, :0], None, None,
+                                 *rope_tables(T, D))[1::2]
+    status_ok(px)
+    assert dk.shape == (T, 0) and dgamma_k.shape == (D,)
+    assert torch.count_nonzero(dgamma_k) == 0
