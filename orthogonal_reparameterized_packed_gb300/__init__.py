@@ -349,45 +349,71 @@ def _ptrs(tensors):
     return _host("Q", map(torch.Tensor.data_ptr, tensors))
 
 
-def _counts(tensors):
+def _described(tensors, name, bf16=False):
+    """(tensors, counts, types) of any iterable of contiguous CUDA tensors, float32 or, with
+    bf16, bfloat16 too: the tensors as a list and the host array of their sizes.  The C calls
+    read all their lists up to one count, so no list reaches them that was not looked over."""
     import torch
-    return _host("q", map(torch.Tensor.numel, tensors))
+    tensors = list(tensors)
+    kinds = [t.dtype for t in tensors]
+    allowed = {torch.float32, torch.bfloat16} if bf16 else {torch.float32}
+    if not (set(kinds) <= allowed and all(map(torch.Tensor.is_contiguous, tensors)) and
+            all([t.is_cuda for t in tensors])):
+        raise ValueError(f"{name}: contiguous CUDA tensors of {sorted(map(str, allowed))} are "
+                         "needed")
+    return tensors, array.array("q", map(torch.Tensor.numel, tensors)), kinds
 
 
-def _dtypes(tensors):
+def _same(name, got, want):
+    """got, want: (counts, types) of two lists that go together."""
+    if got != want:
+        raise ValueError(f"{name}: the lists differ in sizes or types")
+
+
+def _dtypes(kinds):
     """Host array of poetx_dtype per tensor, or no array if all are float32."""
     import torch
-    kinds = {t.dtype for t in tensors}
-    if kinds <= {torch.float32}:
+    if torch.bfloat16 not in kinds:
         return None, None
-    code = {torch.float32: F32, torch.bfloat16: BF16}
-    return _host("i", [code[t.dtype] for t in tensors])
+    return _host("i", [BF16 if k is torch.bfloat16 else F32 for k in kinds])
 
 
 def poetx_grad_norm(grads, norm, workspace, stream=None):
     """grads: list of contiguous float32 or bfloat16 tensors; norm: one float."""
-    (p, pa), (c, ca), (d, da) = _ptrs(grads), _counts(grads), _dtypes(grads)
+    grads, c, kinds = _described(grads, "grads", bf16=True)
+    (p, pa), (d, da) = _ptrs(grads), _dtypes(kinds)
     _check("poetx_grad_norm", load_library().poetx_grad_norm(
-        len(c), pa, ca, da, _ptr(norm), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+        len(c), pa, c.buffer_info()[0], da, _ptr(norm), _ptr(workspace), _nbytes(workspace),
+        _stream(stream)))
 
 
 def poetx_clip_grads(grads, outs, max_norm, norm, workspace, stream=None):
     """outs (None: in place) <- the clipped gradients, norm <- their norm before."""
-    (p, pa), (c, ca), (d, da) = _ptrs(grads), _counts(grads), _dtypes(grads)
-    o, oa = (p, pa) if outs is None else _ptrs(outs)
+    grads, c, kinds = _described(grads, "grads", bf16=True)
+    (p, pa), (d, da) = _ptrs(grads), _dtypes(kinds)
+    o, oa = p, pa
+    if outs is not None:
+        outs, *like = _described(outs, "outs", bf16=True)
+        _same("outs", like, [c, kinds])
+        o, oa = _ptrs(outs)
     _check("poetx_clip_grads", load_library().poetx_clip_grads(
-        len(c), pa, oa, ca, da, max_norm, _ptr(norm), _ptr(workspace), _nbytes(workspace),
-        _stream(stream)))
+        len(c), pa, oa, c.buffer_info()[0], da, max_norm, _ptr(norm), _ptr(workspace),
+        _nbytes(workspace), _stream(stream)))
 
 
 def poetx_adam_update_many(theta, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
                            weight_decay=0.0, max_norm=-1.0, norm=None, workspace=None,
                            stream=None):
-    """Lists of contiguous float32 tensors; max_norm < 0: no clip."""
-    kept = [_ptrs(t) for t in (theta, grads, m, v)]
-    c, ca = _counts(theta)
+    """Lists of contiguous float32 tensors of the same sizes; max_norm < 0: no clip."""
+    theta, c, _ = _described(theta, "theta")
+    lists = [theta]
+    for name, tensors in (("grads", grads), ("m", m), ("v", v)):
+        tensors, like, _ = _described(tensors, name)
+        _same(name, like, c)
+        lists.append(tensors)
+    kept = [_ptrs(t) for t in lists]
     _check("poetx_adam_update_many", load_library().poetx_adam_update_many(
-        len(c), *[a for _, a in kept], ca, step, lr, beta1, beta2, eps, weight_decay, max_norm,
+        len(c), *[a for _, a in kept], c.buffer_info()[0], step, lr, beta1, beta2, eps, weight_decay, max_norm,
         _ptr(norm), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 

@@ -2,6 +2,7 @@
 what the calls and classes refuse before anything is enqueued."""
 
 import pytest
+import torch
 
 import orthogonal_reparameterized_packed_gb300 as poetx
 from orthogonal_reparameterized_packed_gb300.build import build_library
@@ -26,3 +27,71 @@ def test_linear_forward_needs_its_workspace(L):
                                       work, n, None)
 
     assert fwd(n=need - 1) == 3 and fwd(work=None) == 3 and fwd(work=FAKE + 8) == 3
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it is on the GPU, for checks that come before any use."""
+
+    is_cuda = True
+
+
+def on_gpu(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
+
+
+class Recorder:
+    """In the library's place: what reached it; every call returns POETX_OK."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if name.endswith("_workspace_size"):
+            return lambda *a: 64
+
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    # on these host tensors nothing may be launched: the calls end here
+    fake = Recorder()
+    monkeypatch.setattr(poetx, "load_library", lambda: fake)
+    monkeypatch.setattr(poetx, "_stream", lambda stream: 0)
+    return fake
+
+
+def test_lists_of_the_calls_go_together(lib):
+    a, b, h = on_gpu(8), on_gpu(6), on_gpu(8, dtype=torch.bfloat16)
+    norm, ws = on_gpu(1), on_gpu(16)
+    host, strided, double = torch.zeros(8), on_gpu(8, 2)[:, 0], on_gpu(8, dtype=torch.float64)
+    for grads in ([host], [strided], [double], [a, host]):
+        with pytest.raises(ValueError):
+            poetx.poetx_grad_norm(grads, norm, ws)
+        with pytest.raises(ValueError):
+            poetx.poetx_clip_grads(grads, None, 1.0, norm, ws)
+    for outs in ([], [a], [a, a], [b, a], [a, b, a], [h, b], [host, b], [strided, b]):
+        with pytest.raises(ValueError):
+            poetx.poetx_clip_grads([a, b], outs, 1.0, norm, ws)
+    good = [a, b]
+    for bad in ([], [a], [a, a], [b, a], [a, b, b], [h, b], [host, b], [strided, b]):
+        for i in range(4):
+            lists = [good] * 4
+            lists[i] = bad
+            with pytest.raises(ValueError):
+                poetx.poetx_adam_update_many(*lists, 1, 1e-3)
+    assert lib.calls == []
+    poetx.poetx_clip_grads([a, h], [a, h], 1.0, norm, ws)
+    poetx.poetx_adam_update_many(good, good, good, good, 1, 1e-3)
+    assert [n for n, _ in lib.calls] == ["poetx_clip_grads", "poetx_adam_update_many"]
+
+
+def test_lists_may_be_any_iterable(lib):
+    a, b, norm, ws = on_gpu(8), on_gpu(6), on_gpu(1), on_gpu(16)
+    poetx.poetx_grad_norm((t for t in (a, b)), norm, ws)
+    poetx.poetx_clip_grads((t for t in (a, b)), iter([a, b]), 1.0, norm, ws)
+    poetx.poetx_adam_update_many(*[(t for t in (a, b)) for _ in range(4)], 1, 1e-3)
+    assert [args[0] for _, args in lib.calls] == [2, 2, 2]
