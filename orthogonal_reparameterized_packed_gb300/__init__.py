@@ -411,10 +411,18 @@ def poetx_adam_update_many(theta, grads, m, v, step, lr, beta1=0.9, beta2=0.999,
         tensors, like, _ = _described(tensors, name)
         _same(name, like, c)
         lists.append(tensors)
+    _adam_update_many(lists, c, step, lr, beta1, beta2, eps, weight_decay, max_norm, norm,
+                      workspace, stream)
+
+
+def _adam_update_many(lists, c, step, lr, beta1, beta2, eps, weight_decay, max_norm, norm,
+                      workspace, stream):
+    """The call on lists (theta, grads, m, v) of the sizes c, looked over before."""
     kept = [_ptrs(t) for t in lists]
     _check("poetx_adam_update_many", load_library().poetx_adam_update_many(
-        len(c), *[a for _, a in kept], c.buffer_info()[0], step, lr, beta1, beta2, eps, weight_decay, max_norm,
-        _ptr(norm), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+        len(c), *[a for _, a in kept], c.buffer_info()[0], step, lr, beta1, beta2, eps,
+        weight_decay, max_norm, _ptr(norm), _ptr(workspace), _nbytes(workspace),
+        _stream(stream)))
 
 
 def poetx_set_block_epilogue_fusion(enable: bool) -> bool:

@@ -5,10 +5,14 @@ tensors, one shared workspace, and the four calls of a training step
 
 from __future__ import annotations
 
+import array
+import operator
+
 import numpy as np
 import torch
 
-from . import (BF16, F32, poetx_adam_update, poetx_adam_update_many, poetx_backward, poetx_backward_workspace_size,
+from . import (BF16, F32, _adam_update_many, _described, _same, poetx_adam_update,
+               poetx_backward, poetx_backward_workspace_size,
                poetx_build_blocks, poetx_build_workspace_size, poetx_dequantize_w0,
                poetx_fold_permutations, poetx_forward, poetx_forward_workspace_size,
                poetx_grad_norm_workspace_size,
@@ -163,7 +167,9 @@ class PoetxAdam:
     launch per vector per step.  With max_norm the gradients' global norm is
     clipped to it as they are read (self.norm: the norm before the clip), and
     a step is two launches for all vectors together (max_norm = inf: no
-    clip); results then agree with the launch per vector to rounding."""
+    clip); results then agree with the launch per vector to rounding.
+    params, m and v: contiguous float32 CUDA tensors, m and v of the
+    parameters' sizes; so are the gradients (ValueError otherwise)."""
 
     def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0):
         self.params = list(params)
@@ -172,6 +178,23 @@ class PoetxAdam:
         self.v = [torch.zeros_like(p) for p in self.params]
         self.norm = self._workspace = None
         self.t = 0
+        self._look_over()
+
+    def _look_over(self):
+        """Refuses parameters and moments that the calls would read or write wrongly."""
+        _, counts, _ = _described(self.params, "params")
+        for name, tensors in (("m", self.m), ("v", self.v)):
+            _same(name, _described(tensors, name)[1], counts)
+        self._looked_over, self._sizes = [*self.params, *self.m, *self.v], counts
+
+    def _state_sizes(self):
+        """The parameters' sizes; what was replaced since the last step is looked over."""
+        state = [*self.params, *self.m, *self.v]
+        if len(state) != len(self._looked_over) or \
+                not all(map(operator.is_, state, self._looked_over)) or \
+                array.array("q", map(torch.Tensor.numel, self.params)) != self._sizes:
+            self._look_over()
+        return self._sizes
 
     def reset(self):
         """Zero the moments (after a merge restarts the factors)."""
@@ -183,18 +206,16 @@ class PoetxAdam:
     def step(self, grads, stream=None, max_norm=None):
         if max_norm is not None and not max_norm >= 0:
             raise ValueError(f"max_norm must be at least 0, got {max_norm}")
+        sizes = self._state_sizes()
+        grads, counts, _ = _described(grads, "grads")
         if max_norm is None:
+            _same("grads", counts[:len(sizes)], sizes[:len(counts)])
             self.t += 1
             for p, g, m, v in zip(self.params, grads, self.m, self.v):
                 poetx_adam_update(p, g, m, v, p.numel(), self.t, self.lr, self.betas[0],
                                   self.betas[1], self.eps, self.weight_decay, stream)
             return
-        grads = list(grads)
-        sizes = list(map(torch.Tensor.numel, self.params))
-        if list(map(torch.Tensor.numel, grads)) != sizes or \
-                {g.dtype for g in grads} - {torch.float32} or \
-                not all(map(torch.Tensor.is_contiguous, grads)):
-            raise ValueError("contiguous float32 gradients of the parameters' sizes are needed")
+        _same("grads", counts, sizes)
         self.t += 1
         if not grads:
             return
@@ -203,9 +224,9 @@ class PoetxAdam:
             self.norm = torch.empty((), dtype=torch.float32, device=dev)
             self._workspace = torch.empty((poetx_grad_norm_workspace_size(len(self.params)),),
                                           dtype=torch.uint8, device=dev)
-        poetx_adam_update_many(self.params, grads, self.m, self.v, self.t, self.lr,
-                               self.betas[0], self.betas[1], self.eps, self.weight_decay,
-                               max_norm, self.norm, self._workspace, stream)
+        _adam_update_many([self.params, grads, self.m, self.v], sizes, self.t, self.lr,
+                          self.betas[0], self.betas[1], self.eps, self.weight_decay, max_norm,
+                          self.norm, self._workspace, stream)
 
 
 def to_device(inp, device="cuda"):

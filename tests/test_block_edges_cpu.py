@@ -95,3 +95,43 @@ def test_lists_may_be_any_iterable(lib):
     poetx.poetx_clip_grads((t for t in (a, b)), iter([a, b]), 1.0, norm, ws)
     poetx.poetx_adam_update_many(*[(t for t in (a, b)) for _ in range(4)], 1, 1e-3)
     assert [args[0] for _, args in lib.calls] == [2, 2, 2]
+
+
+BAD = [torch.zeros(8),                                 # on the host
+       on_gpu(8, 2)[:, 0],                             # every other element
+       on_gpu(4, 2).t(),                               # dense, in another order
+       on_gpu(8, dtype=torch.bfloat16), on_gpu(8, dtype=torch.float64)]
+
+
+def test_adam_refuses_parameters_that_it_would_read_wrongly(lib):
+    from orthogonal_reparameterized_packed_gb300.layer import PoetxAdam
+    for bad in BAD:
+        with pytest.raises(ValueError):
+            PoetxAdam([on_gpu(3), bad], lr=1e-3)
+    assert lib.calls == []
+
+
+@pytest.mark.parametrize("max_norm", [None, 1.0])
+def test_adam_refuses_gradients_and_moments_that_do_not_fit(lib, monkeypatch, max_norm):
+    from orthogonal_reparameterized_packed_gb300 import layer
+    monkeypatch.setattr(layer, "poetx_grad_norm_workspace_size", lambda n: 64)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: on_gpu(64))
+    opt = layer.PoetxAdam([on_gpu(8), on_gpu(6)], lr=1e-3)
+    good = [on_gpu(8), on_gpu(6)]
+    for bad in [*([b, good[1]] for b in BAD), [on_gpu(7), good[1]], [good[1], good[0]]]:
+        with pytest.raises(ValueError):
+            opt.step(bad, max_norm=max_norm)
+    for name in ("params", "m", "v"):
+        for bad in [*([b, good[1]] for b in BAD), good[:1], [*good, good[0]], [good[1], good[0]]]:
+            kept = getattr(opt, name)
+            setattr(opt, name, bad)
+            with pytest.raises(ValueError):
+                opt.step(good, max_norm=max_norm)
+            setattr(opt, name, kept)
+    opt.m[1] = on_gpu(5)  # in place too
+    with pytest.raises(ValueError):
+        opt.step(good, max_norm=max_norm)
+    opt.m[1] = on_gpu(6)
+    assert lib.calls == [] and opt.t == 0
+    opt.step((g for g in good), max_norm=max_norm)
+    assert opt.t == 1 and len(lib.calls) == (2 if max_norm is None else 1)
