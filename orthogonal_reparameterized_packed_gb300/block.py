@@ -6,13 +6,12 @@ enqueues its calls on a stream (the current one by default)."""
 
 from __future__ import annotations
 
-import array
-
 import torch
 
-from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, BF16, F32, _check, _stream,
-               load_library, poetx_grad_norm_workspace_size, poetx_linear_backward_workspace_size,
-               poetx_linear_forward_workspace_size, poetx_qk_norm_rope_backward_workspace_size)
+from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, _check, _described, _dtypes,
+               _ptrs, _same, _stream, load_library, poetx_grad_norm_workspace_size,
+               poetx_linear_backward_workspace_size, poetx_linear_forward_workspace_size,
+               poetx_qk_norm_rope_backward_workspace_size)
 from .layer import _TORCH_DTYPE, dtype_code
 
 # These classes call the library directly: a call for one token costs the host
@@ -205,26 +204,10 @@ class PoetxQKNormRope:
         return self._cut(self.dq, t), self._cut(self.dk, t), self.dgamma_q, self.dgamma_k
 
 
-def _described(tensors, dtypes, name):
-    """(counts, types) of contiguous CUDA tensors of `dtypes`."""
-    kinds = [t.dtype for t in tensors]
-    if not (set(kinds) <= dtypes and all(map(torch.Tensor.is_contiguous, tensors)) and
-            all([t.is_cuda for t in tensors])):
-        raise ValueError(
-            f"{name}: contiguous CUDA tensors of {sorted(map(str, dtypes))} are needed")
-    return array.array("q", map(torch.Tensor.numel, tensors)), kinds
-
-
-def _pointers(tensors):
-    return array.array("Q", map(torch.Tensor.data_ptr, tensors))
-
-
 class PoetxGradClip:
-    """The global norm of a list of gradients (contiguous float32 or bfloat16
-    tensors), and the clip to a largest norm.  self.norm is the norm of the
-    last call (a 0-dim float32 tensor, overwritten by the next; undefined before the first)."""
-
-    _TYPES = {torch.float32, torch.bfloat16}
+    """The global norm of a list (any iterable) of gradients, contiguous float32
+    or bfloat16 tensors, and the clip to a largest norm.  self.norm is the norm of the last
+    call (a 0-dim float32 tensor, overwritten by the next; undefined before the first)."""
 
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
@@ -241,33 +224,26 @@ class PoetxGradClip:
             self._spaces.append(torch.empty((need,), dtype=torch.uint8, device=self.device))
         return self._spaces[-1]
 
-    def _codes(self, kinds):
-        """The list's poetx_dtype array; empty where all are float32."""
-        return array.array("i", () if torch.bfloat16 not in kinds else
-                           [BF16 if k is torch.bfloat16 else F32 for k in kinds])
-
     def total(self, grads, stream=None):
         """norm = sqrt(sum of squares over all tensors)."""
-        counts, kinds = _described(grads, self._TYPES, "grads")
-        at, codes, room = _pointers(grads), self._codes(kinds), self._room(len(kinds))
+        grads, counts, kinds = _described(grads, "grads", bf16=True)
+        (at, at_p), (codes, codes_p), room = _ptrs(grads), _dtypes(kinds), self._room(len(kinds))
         _check("poetx_grad_norm", self._total(
-            len(kinds), at.buffer_info()[0], counts.buffer_info()[0],
-            codes.buffer_info()[0] if codes else None, self.norm.data_ptr(), room.data_ptr(),
-            room.numel(), _stream(stream)))
+            len(counts), at_p, counts.buffer_info()[0], codes_p, self.norm.data_ptr(),
+            room.data_ptr(), room.numel(), _stream(stream)))
         return self.norm
 
     def clip(self, grads, max_norm, out=None, stream=None):
         """out (None: the gradients themselves) = grads * min(1, max_norm /
         (norm + 1e-6)); returns the norm before the clip."""
-        counts, kinds = _described(grads, self._TYPES, "grads")
-        at = to = _pointers(grads)
+        grads, counts, kinds = _described(grads, "grads", bf16=True)
+        (at, at_p), (codes, codes_p), room = _ptrs(grads), _dtypes(kinds), self._room(len(kinds))
+        to, to_p = at, at_p
         if out is not None:
-            if _described(out, self._TYPES, "out") != (counts, kinds):
-                raise ValueError("grads: the lists differ in sizes or types")
-            to = _pointers(out)
-        codes, room = self._codes(kinds), self._room(len(kinds))
+            out, *like = _described(out, "out", bf16=True)
+            _same("out", like, [counts, kinds])
+            to, to_p = _ptrs(out)
         _check("poetx_clip_grads", self._clip(
-            len(kinds), at.buffer_info()[0], to.buffer_info()[0], counts.buffer_info()[0],
-            codes.buffer_info()[0] if codes else None, max_norm, self.norm.data_ptr(),
-            room.data_ptr(), room.numel(), _stream(stream)))
+            len(counts), at_p, to_p, counts.buffer_info()[0], codes_p, max_norm,
+            self.norm.data_ptr(), room.data_ptr(), room.numel(), _stream(stream)))
         return self.norm

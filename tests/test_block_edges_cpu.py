@@ -1,6 +1,8 @@
 """Host-side edges of the operators around the projections (no GPU needed):
 what the calls and classes refuse before anything is enqueued."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -135,3 +137,36 @@ def test_adam_refuses_gradients_and_moments_that_do_not_fit(lib, monkeypatch, ma
     assert lib.calls == [] and opt.t == 0
     opt.step((g for g in good), max_norm=max_norm)
     assert opt.t == 1 and len(lib.calls) == (2 if max_norm is None else 1)
+
+
+@pytest.fixture
+def host_clip(monkeypatch):
+    """A PoetxGradClip on the host whose calls are recorded: (counts or None, norm, workspace,
+    stream)."""
+    from orthogonal_reparameterized_packed_gb300 import block
+    calls = []
+
+    def counts(n, at):
+        return list((ctypes.c_int64 * n).from_address(at)) if at or not n else None
+
+    class Library:
+        def poetx_grad_norm(self, n, grads, c, types, norm, room, size, stream):
+            calls.append((counts(n, c), norm, room, stream))
+            return 0
+
+        def poetx_clip_grads(self, n, grads, outs, c, types, most, norm, room, size, stream):
+            calls.append((counts(n, c), norm, room, stream))
+            return 0
+
+    monkeypatch.setattr(block, "load_library", Library)
+    clip = block.PoetxGradClip(device="cpu")
+    clip.calls = calls
+    return clip
+
+
+def test_clip_takes_any_iterable_whole(host_clip):
+    a, b = on_gpu(8), on_gpu(6)
+    host_clip.total((t for t in (a, b)), stream=7)
+    host_clip.clip((t for t in (a, b)), 1.0, stream=7)
+    host_clip.clip(iter([a, b]), 1.0, out=(t for t in (a, b)), stream=7)
+    assert [c[0] for c in host_clip.calls] == [[8, 6]] * 3
