@@ -169,6 +169,18 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _allocating_on(stream, device):
+    """Within it, CUDA memory is taken from the stream that a call is enqueued on: what is
+    allocated on another stream may still be in use by work queued there."""
+    import contextlib
+    import torch
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
 def _check(fn, status):
     if status != 0:
         raise PoetxError(fn, status)

@@ -2,16 +2,17 @@
 with bias, activation and residual (for frozen or merged weights), the norm of
 queries and keys with the rotary embedding, and the clip of the gradients.
 Each class holds the output buffers and the workspace of one such step and
-enqueues its calls on a stream (the current one by default)."""
+enqueues its calls on a stream (the current one by default); calls of one object
+on several streams have to be ordered by the caller (but for PoetxGradClip)."""
 
 from __future__ import annotations
 
 import torch
 
-from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, _check, _described, _dtypes,
-               _ptrs, _same, _stream, load_library, poetx_grad_norm_workspace_size,
-               poetx_linear_backward_workspace_size, poetx_linear_forward_workspace_size,
-               poetx_qk_norm_rope_backward_workspace_size)
+from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, _allocating_on, _check,
+               _described, _dtypes, _ptrs, _same, _stream, load_library,
+               poetx_grad_norm_workspace_size, poetx_linear_backward_workspace_size,
+               poetx_linear_forward_workspace_size, poetx_qk_norm_rope_backward_workspace_size)
 from .layer import _TORCH_DTYPE, dtype_code
 
 # These classes call the library directly: a call for one token costs the host
@@ -207,37 +208,48 @@ class PoetxQKNormRope:
 class PoetxGradClip:
     """The global norm of a list (any iterable) of gradients, contiguous float32
     or bfloat16 tensors, and the clip to a largest norm.  self.norm is the norm of the last
-    call (a 0-dim float32 tensor, overwritten by the next; undefined before the first)."""
+    call (a 0-dim float32 tensor; undefined before the first).
+
+    Every stream has a norm, overwritten by the next call on it, and a workspace of its
+    own, so that calls of one object on several streams may run at one time.  A captured
+    graph holds those of the stream that it was captured on: graphs captured on one
+    stream with one object are not to be replayed at one time."""
 
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
         self.norm = torch.empty((), dtype=torch.float32, device=self.device)
-        self._spaces = []
+        self._of_stream = {}  # handle -> (norm, workspaces)
         lib = load_library()
         self._total, self._clip = lib.poetx_grad_norm, lib.poetx_clip_grads
 
-    def _room(self, n):
-        """A workspace for n tensors.  Smaller ones are kept: a call on another
-        stream may still be using them."""
-        need = poetx_grad_norm_workspace_size(n)
-        if not self._spaces or self._spaces[-1].numel() < need:
-            self._spaces.append(torch.empty((need,), dtype=torch.uint8, device=self.device))
-        return self._spaces[-1]
+    def _buffers(self, n, stream):
+        """(norm's address, address and bytes of a workspace for n tensors, handle) of the
+        stream.  Smaller workspaces are kept: a captured graph may hold them."""
+        handle, need = _stream(stream), poetx_grad_norm_workspace_size(n)
+        norm, rooms = self._of_stream.get(handle, (None, []))
+        if not rooms or rooms[-1].numel() < need:
+            with _allocating_on(stream, self.device):
+                rooms.append(torch.empty((need,), dtype=torch.uint8, device=self.device))
+                if norm is None:
+                    norm = torch.empty((), dtype=torch.float32, device=self.device)
+            self._of_stream[handle] = norm, rooms
+        self.norm = norm
+        return norm.data_ptr(), rooms[-1].data_ptr(), rooms[-1].numel(), handle
 
     def total(self, grads, stream=None):
         """norm = sqrt(sum of squares over all tensors)."""
         grads, counts, kinds = _described(grads, "grads", bf16=True)
-        (at, at_p), (codes, codes_p), room = _ptrs(grads), _dtypes(kinds), self._room(len(kinds))
+        (at, at_p), (codes, codes_p) = _ptrs(grads), _dtypes(kinds)
         _check("poetx_grad_norm", self._total(
-            len(counts), at_p, counts.buffer_info()[0], codes_p, self.norm.data_ptr(),
-            room.data_ptr(), room.numel(), _stream(stream)))
+            len(counts), at_p, counts.buffer_info()[0], codes_p,
+            *self._buffers(len(counts), stream)))
         return self.norm
 
     def clip(self, grads, max_norm, out=None, stream=None):
         """out (None: the gradients themselves) = grads * min(1, max_norm /
         (norm + 1e-6)); returns the norm before the clip."""
         grads, counts, kinds = _described(grads, "grads", bf16=True)
-        (at, at_p), (codes, codes_p), room = _ptrs(grads), _dtypes(kinds), self._room(len(kinds))
+        (at, at_p), (codes, codes_p) = _ptrs(grads), _dtypes(kinds)
         to, to_p = at, at_p
         if out is not None:
             out, *like = _described(out, "out", bf16=True)
@@ -245,5 +257,5 @@ class PoetxGradClip:
             to, to_p = _ptrs(out)
         _check("poetx_clip_grads", self._clip(
             len(counts), at_p, to_p, counts.buffer_info()[0], codes_p, max_norm,
-            self.norm.data_ptr(), room.data_ptr(), room.numel(), _stream(stream)))
+            *self._buffers(len(counts), stream)))
         return self.norm

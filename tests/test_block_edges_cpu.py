@@ -170,3 +170,40 @@ def test_clip_takes_any_iterable_whole(host_clip):
     host_clip.clip((t for t in (a, b)), 1.0, stream=7)
     host_clip.clip(iter([a, b]), 1.0, out=(t for t in (a, b)), stream=7)
     assert [c[0] for c in host_clip.calls] == [[8, 6]] * 3
+
+
+def test_clip_has_buffers_of_its_own_on_every_stream(host_clip):
+    few, many = [on_gpu(4)], [on_gpu(4)] * 1500
+    norms = [host_clip.total(few, stream=5), host_clip.clip(few, 1.0, stream=6),
+             host_clip.total(many, stream=6), host_clip.clip(many, 1.0, stream=5),
+             host_clip.clip(few, 1.0, stream=5)]
+    _, norm, room, stream = zip(*host_clip.calls)
+    assert stream == (5, 6, 6, 5, 5)
+    assert norm[0] == norm[3] == norm[4] != norm[1] == norm[2]
+    assert list(norm) == [t.data_ptr() for t in norms] and host_clip.norm is norms[-1]
+    assert len({room[i] for i in (0, 1, 2, 3)}) == 4  # no two streams, no two sizes share one
+    assert room[4] == room[3]
+
+
+def test_what_a_call_needs_comes_from_its_stream(monkeypatch):
+    # the stream that is current while memory is taken is the call's
+    seen = []
+
+    class Current:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            seen.append(self.stream)
+
+        def __exit__(self, *a):
+            pass
+
+    monkeypatch.setattr(torch.cuda, "stream", Current)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
+    cuda = torch.device("cuda")
+    with poetx._allocating_on(77, cuda), poetx._allocating_on("a stream", cuda):
+        pass
+    with poetx._allocating_on(None, cuda), poetx._allocating_on(3, torch.device("cpu")):
+        pass
+    assert seen == [77, "a stream"]

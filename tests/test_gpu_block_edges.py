@@ -273,3 +273,25 @@ def test_no_key_heads_have_no_gradient(px):
     status_ok(px)
     assert dk.shape == (T, 0) and dgamma_k.shape == (D,)
     assert torch.count_nonzero(dgamma_k) == 0
+
+
+def test_one_clip_on_two_streams_at_one_time(px):
+    # long and short lists on two streams, many times with nothing between: every norm and
+    # every output has the bits of a call on its own
+    from orthogonal_reparameterized_packed_gb300.block import PoetxGradClip
+    counts = ([60000] * 40, [500, 7])
+    sides, clip = [torch.cuda.Stream() for _ in counts], PoetxGradClip()
+    grads = [[normal(n, seed=470 + 50 * i + j) for j, n in enumerate(c)]
+             for i, c in enumerate(counts)]
+    outs = [[torch.empty_like(g) for g in gs] for gs in grads]
+    want = []
+    for g, o in zip(grads, outs):
+        norm = clip.clip(g, 0.5, out=o)
+        torch.cuda.synchronize()
+        want.append((norm.clone(), [t.clone() for t in o]))
+    torch.cuda.synchronize()
+    for _ in range(50):
+        norms = [clip.clip(g, 0.5, out=o, stream=s) for g, o, s in zip(grads, outs, sides)]
+    status_ok(px)
+    for (norm, values), got, o in zip(want, norms, outs):
+        assert torch.equal(got, norm) and all(torch.equal(p, q) for p, q in zip(o, values))
