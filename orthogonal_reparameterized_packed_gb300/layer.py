@@ -11,8 +11,8 @@ import operator
 import numpy as np
 import torch
 
-from . import (BF16, F32, _adam_update_many, _described, _same, poetx_adam_update,
-               poetx_backward, poetx_backward_workspace_size,
+from . import (BF16, F32, _adam_update_many, _allocating_on, _described, _same,
+               poetx_adam_update, poetx_backward, poetx_backward_workspace_size,
                poetx_build_blocks, poetx_build_workspace_size, poetx_dequantize_w0,
                poetx_fold_permutations, poetx_forward, poetx_forward_workspace_size,
                poetx_grad_norm_workspace_size,
@@ -220,10 +220,10 @@ class PoetxAdam:
         if not grads:
             return
         if self.norm is None:
-            dev = self.params[0].device
-            self.norm = torch.empty((), dtype=torch.float32, device=dev)
-            self._workspace = torch.empty((poetx_grad_norm_workspace_size(len(self.params)),),
-                                          dtype=torch.uint8, device=dev)
+            dev, need = self.params[0].device, poetx_grad_norm_workspace_size(len(self.params))
+            with _allocating_on(stream, dev):
+                self.norm = torch.empty((), dtype=torch.float32, device=dev)
+                self._workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
         _adam_update_many([self.params, grads, self.m, self.v], sizes, self.t, self.lr,
                           self.betas[0], self.betas[1], self.eps, self.weight_decay, max_norm,
                           self.norm, self._workspace, stream)

@@ -207,3 +207,24 @@ def test_what_a_call_needs_comes_from_its_stream(monkeypatch):
     with poetx._allocating_on(None, cuda), poetx._allocating_on(3, torch.device("cpu")):
         pass
     assert seen == [77, "a stream"]
+
+
+def test_adam_takes_its_workspace_from_the_call_s_stream(lib, monkeypatch):
+    from orthogonal_reparameterized_packed_gb300 import layer
+    inside, taken = [], []
+
+    class Marked:
+        def __init__(self, stream, device):
+            self.stream = stream
+
+        def __enter__(self):
+            inside.append(self.stream)
+
+        def __exit__(self, *a):
+            inside.pop()
+
+    monkeypatch.setattr(layer, "_allocating_on", Marked, raising=False)
+    monkeypatch.setattr(layer, "poetx_grad_norm_workspace_size", lambda n: 64)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (taken.append(list(inside)), on_gpu(64))[1])
+    layer.PoetxAdam([on_gpu(8)], lr=1e-3).step([on_gpu(8)], stream=11, max_norm=1.0)
+    assert taken == [[11], [11]]
