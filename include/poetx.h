@@ -308,7 +308,7 @@ poetx_status poetx_linear_backward(const void* dy, const void* z_saved, const vo
  *   gamma_q, gamma_k [head_dim], cos_table, sin_table [table_rows]
  *   [rot_dim/2]: float32; positions [tokens] int32.  n_k_heads may be 0
  *   (then the k pointers are not used); rot_dim = 0: the norm alone.
- *   Outputs may be the inputs (with the same ld).
+ *   Outputs may be the inputs of their side (q's or k's, with the same ld).
  * A position outside 0..table_rows-1 is not followed: the token's outputs
  * (backward: dq, dk) are 0, it adds nothing to dgamma, and
  * POETX_ERR_INVALID_ARG is recorded in the status word.

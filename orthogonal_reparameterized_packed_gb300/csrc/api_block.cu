@@ -49,6 +49,13 @@ poetx_status check_qk(int hq, int hk, int D, int rot, int64_t table_rows, float 
   return D > 512 ? POETX_ERR_UNSUPPORTED : POETX_OK;
 }
 
+// An output may be an input of its own side with the same rows, never the other
+// side's: warps read and write the heads of both at their own pace.
+bool in_place_ok(const void* in, int64_t ld_in, const void* other_in, const void* out,
+                 int64_t ld_out, int64_t tokens) {
+  return out != other_in && (out != in || ld_in == ld_out || tokens <= 1);
+}
+
 // Counts, pointers and types of a tensor list.
 poetx_status check_list(int n, const int64_t* counts, const int32_t* dtypes) {
   if (n < 0 || (n > 0 && counts == nullptr)) return POETX_ERR_INVALID_ARG;
@@ -91,7 +98,8 @@ poetx_status poetx_linear_forward(const void* x, const void* W, const float* bia
                                   poetx_stream stream) {
   if (!linear_dims_ok(d_in, d_out, tokens, dtype) || !act_ok(act)) return POETX_ERR_INVALID_ARG;
   if (tokens == 0) return POETX_OK;
-  if (x == nullptr || W == nullptr || y == nullptr || y == x || z_saved == x || z_saved == y)
+  if (x == nullptr || W == nullptr || y == nullptr || y == x || z_saved == x || z_saved == y ||
+      (z_saved != nullptr && z_saved == residual))
     return POETX_ERR_INVALID_ARG;
   for (const void* p : {x, W, static_cast<const void*>(bias), residual,
                         static_cast<const void*>(y), static_cast<const void*>(z_saved)})
@@ -162,6 +170,9 @@ poetx_status poetx_qk_norm_rope_forward(const void* q, const void* k, const floa
       (rot_dim > 0 && (cos_table == nullptr || sin_table == nullptr || !aligned(cos_table, 4) ||
                        !aligned(sin_table, 4))))
     return POETX_ERR_INVALID_ARG;
+  if (!in_place_ok(q, ld_q, n_k_heads > 0 ? k : nullptr, q_out, ld_q_out, tokens) ||
+      (n_k_heads > 0 && !in_place_ok(k, ld_k, q, k_out, ld_k_out, tokens)))
+    return POETX_ERR_INVALID_ARG;
   QkNormRopeArgs a;
   a.q = q, a.k = k, a.ld_q = ld_q, a.ld_k = ld_k;
   a.gamma_q = gamma_q, a.gamma_k = gamma_k;
@@ -209,6 +220,14 @@ poetx_status poetx_qk_norm_rope_backward(
   st = check_workspace(qk_norm_rope_scratch(n_q_heads, n_k_heads, head_dim, tokens), workspace,
                        workspace_bytes);
   if (st != POETX_OK) return st;
+  if (tokens > 0) {
+    const bool has_k = n_k_heads > 0;
+    if (!in_place_ok(q, ld_q, has_k ? k : nullptr, dq, ld_dq, tokens) ||
+        !in_place_ok(dq_out, ld_dq_out, has_k ? dk_out : nullptr, dq, ld_dq, tokens) ||
+        (has_k && (!in_place_ok(k, ld_k, q, dk, ld_dk, tokens) ||
+                   !in_place_ok(dk_out, ld_dk_out, dq_out, dk, ld_dk, tokens))))
+      return POETX_ERR_INVALID_ARG;
+  }
   QkNormRopeArgs a;
   a.q = q, a.k = k, a.ld_q = ld_q, a.ld_k = ld_k;
   a.gamma_q = gamma_q, a.gamma_k = gamma_k;

@@ -228,3 +228,26 @@ def test_adam_takes_its_workspace_from_the_call_s_stream(lib, monkeypatch):
     monkeypatch.setattr(torch, "empty", lambda *a, **k: (taken.append(list(inside)), on_gpu(64))[1])
     layer.PoetxAdam([on_gpu(8)], lr=1e-3).step([on_gpu(8)], stream=11, max_norm=1.0)
     assert taken == [[11], [11]]
+
+
+def test_outputs_over_other_inputs_are_refused(L):
+    # z over the residual; q's outputs over k's inputs and the other way round; rows in place
+    # at another distance.  What is allowed would be launched, and is run on a GPU elsewhere.
+    f, A = ctypes.c_float, [FAKE + 65536 * i for i in range(8)]
+    assert L.poetx_linear_forward(A[0], A[1], None, A[2], A[3], A[2], 64, 64, 8, 0, B, None, 0,
+                                  None) == 1
+
+    def fwd(q=A[0], k=A[1], oq=A[2], ok=A[3], loq=512):
+        return L.poetx_qk_norm_rope_forward(q, k, None, None, None, None, None, oq, ok, 512, 128,
+                                            loq, 128, 4, 1, 128, 0, 0, 0, f(1e-6), 3, B, None)
+
+    def bwd(gq=A[0], gk=A[1], q=A[2], k=A[3], dq=A[4], dk=A[5], ldq=512):
+        return L.poetx_qk_norm_rope_backward(gq, gk, q, k, None, None, None, None, None, dq, dk,
+                                             None, None, 512, 128, 512, 128, ldq, 128, 4, 1, 128,
+                                             0, 0, 0, f(1e-6), 3, B, A[7], 1 << 40, None)
+
+    for kw in (dict(oq=A[1]), dict(ok=A[0]), dict(oq=A[0], loq=520)):
+        assert fwd(**kw) == 1, kw
+    for kw in (dict(dq=A[1]), dict(dq=A[3]), dict(dk=A[0]), dict(dk=A[2]),
+               dict(dq=A[0], ldq=520), dict(dq=A[2], ldq=520)):
+        assert bwd(**kw) == 1, kw
