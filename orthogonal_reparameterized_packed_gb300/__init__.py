@@ -9,7 +9,6 @@ PyTorch is used for device memory and streams only.
 
 from __future__ import annotations
 
-import array
 import ctypes
 import os
 
@@ -349,51 +348,11 @@ def poetx_grad_norm_workspace_size(n_tensors) -> int:
     return load_library().poetx_grad_norm_workspace_size(n_tensors)
 
 
-def _host(code, values):
-    """(array kept alive, its address) of host values."""
-    a = array.array(code, values)
-    return a, a.buffer_info()[0]
-
-
-def _ptrs(tensors):
-    """Host array of the tensors' device pointers."""
-    import torch
-    return _host("Q", map(torch.Tensor.data_ptr, tensors))
-
-
-def _described(tensors, name, bf16=False):
-    """(tensors, counts, types) of any iterable of contiguous CUDA tensors, float32 or, with
-    bf16, bfloat16 too: the tensors as a list and the host array of their sizes.  The C calls
-    read all their lists up to one count, so no list reaches them that was not looked over."""
-    import torch
-    tensors = list(tensors)
-    kinds = [t.dtype for t in tensors]
-    allowed = {torch.float32, torch.bfloat16} if bf16 else {torch.float32}
-    if not (set(kinds) <= allowed and all(map(torch.Tensor.is_contiguous, tensors)) and
-            all([t.is_cuda for t in tensors])):
-        raise ValueError(f"{name}: contiguous CUDA tensors of {sorted(map(str, allowed))} are "
-                         "needed")
-    return tensors, array.array("q", map(torch.Tensor.numel, tensors)), kinds
-
-
-def _same(name, got, want):
-    """got, want: (counts, types) of two lists that go together."""
-    if got != want:
-        raise ValueError(f"{name}: the lists differ in sizes or types")
-
-
-def _dtypes(kinds):
-    """Host array of poetx_dtype per tensor, or no array if all are float32."""
-    import torch
-    if torch.bfloat16 not in kinds:
-        return None, None
-    return _host("i", [BF16 if k is torch.bfloat16 else F32 for k in kinds])
-
-
 def poetx_grad_norm(grads, norm, workspace, stream=None):
     """grads: list of contiguous float32 or bfloat16 tensors; norm: one float."""
-    grads, c, kinds = _described(grads, "grads", bf16=True)
-    (p, pa), (d, da) = _ptrs(grads), _dtypes(kinds)
+    from . import lists
+    grads, c, kinds = lists.described(grads, "grads", bf16=True)
+    (p, pa), (d, da) = lists.pointers(grads), lists.codes(kinds)
     _check("poetx_grad_norm", load_library().poetx_grad_norm(
         len(c), pa, c.buffer_info()[0], da, _ptr(norm), _ptr(workspace), _nbytes(workspace),
         _stream(stream)))
@@ -401,13 +360,14 @@ def poetx_grad_norm(grads, norm, workspace, stream=None):
 
 def poetx_clip_grads(grads, outs, max_norm, norm, workspace, stream=None):
     """outs (None: in place) <- the clipped gradients, norm <- their norm before."""
-    grads, c, kinds = _described(grads, "grads", bf16=True)
-    (p, pa), (d, da) = _ptrs(grads), _dtypes(kinds)
+    from . import lists
+    grads, c, kinds = lists.described(grads, "grads", bf16=True)
+    (p, pa), (d, da) = lists.pointers(grads), lists.codes(kinds)
     o, oa = p, pa
     if outs is not None:
-        outs, *like = _described(outs, "outs", bf16=True)
-        _same("outs", like, [c, kinds])
-        o, oa = _ptrs(outs)
+        outs, *like = lists.described(outs, "outs", bf16=True)
+        lists.same("outs", like, [c, kinds])
+        o, oa = lists.pointers(outs)
     _check("poetx_clip_grads", load_library().poetx_clip_grads(
         len(c), pa, oa, c.buffer_info()[0], da, max_norm, _ptr(norm), _ptr(workspace),
         _nbytes(workspace), _stream(stream)))
@@ -417,20 +377,20 @@ def poetx_adam_update_many(theta, grads, m, v, step, lr, beta1=0.9, beta2=0.999,
                            weight_decay=0.0, max_norm=-1.0, norm=None, workspace=None,
                            stream=None):
     """Lists of contiguous float32 tensors of the same sizes; max_norm < 0: no clip."""
-    theta, c, _ = _described(theta, "theta")
-    lists = [theta]
+    from . import lists
+    theta, c, _ = lists.described(theta, "theta")
+    kept = [lists.pointers(theta)]
     for name, tensors in (("grads", grads), ("m", m), ("v", v)):
-        tensors, like, _ = _described(tensors, name)
-        _same(name, like, c)
-        lists.append(tensors)
-    _adam_update_many(lists, c, step, lr, beta1, beta2, eps, weight_decay, max_norm, norm,
+        tensors, like, _ = lists.described(tensors, name)
+        lists.same(name, like, c)
+        kept.append(lists.pointers(tensors))
+    _adam_update_many(kept, c, step, lr, beta1, beta2, eps, weight_decay, max_norm, norm,
                       workspace, stream)
 
 
-def _adam_update_many(lists, c, step, lr, beta1, beta2, eps, weight_decay, max_norm, norm,
+def _adam_update_many(kept, c, step, lr, beta1, beta2, eps, weight_decay, max_norm, norm,
                       workspace, stream):
-    """The call on lists (theta, grads, m, v) of the sizes c, looked over before."""
-    kept = [_ptrs(t) for t in lists]
+    """The call on the (array, address) of theta, grads, m and v and on their sizes c."""
     _check("poetx_adam_update_many", load_library().poetx_adam_update_many(
         len(c), *[a for _, a in kept], c.buffer_info()[0], step, lr, beta1, beta2, eps,
         weight_decay, max_norm, _ptr(norm), _ptr(workspace), _nbytes(workspace),

@@ -10,10 +10,11 @@ from __future__ import annotations
 import torch
 
 from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, _allocating_on, _check,
-               _described, _dtypes, _ptrs, _same, _stream, load_library,
-               poetx_grad_norm_workspace_size, poetx_linear_backward_workspace_size,
-               poetx_linear_forward_workspace_size, poetx_qk_norm_rope_backward_workspace_size)
+               _stream, load_library, poetx_grad_norm_workspace_size,
+               poetx_linear_backward_workspace_size, poetx_linear_forward_workspace_size,
+               poetx_qk_norm_rope_backward_workspace_size)
 from .layer import _TORCH_DTYPE, dtype_code
+from .lists import codes, described, pointers, same
 
 # These classes call the library directly: a call for one token costs the host
 # about as long as the GPU.
@@ -238,24 +239,24 @@ class PoetxGradClip:
 
     def total(self, grads, stream=None):
         """norm = sqrt(sum of squares over all tensors)."""
-        grads, counts, kinds = _described(grads, "grads", bf16=True)
-        (at, at_p), (codes, codes_p) = _ptrs(grads), _dtypes(kinds)
+        grads, counts, kinds = described(grads, "grads", bf16=True)
+        (at, at_p), (types, types_p) = pointers(grads), codes(kinds)
         _check("poetx_grad_norm", self._total(
-            len(counts), at_p, counts.buffer_info()[0], codes_p,
+            len(counts), at_p, counts.buffer_info()[0], types_p,
             *self._buffers(len(counts), stream)))
         return self.norm
 
     def clip(self, grads, max_norm, out=None, stream=None):
         """out (None: the gradients themselves) = grads * min(1, max_norm /
         (norm + 1e-6)); returns the norm before the clip."""
-        grads, counts, kinds = _described(grads, "grads", bf16=True)
-        (at, at_p), (codes, codes_p) = _ptrs(grads), _dtypes(kinds)
+        grads, counts, kinds = described(grads, "grads", bf16=True)
+        (at, at_p), (types, types_p) = pointers(grads), codes(kinds)
         to, to_p = at, at_p
         if out is not None:
-            out, *like = _described(out, "out", bf16=True)
-            _same("out", like, [counts, kinds])
-            to, to_p = _ptrs(out)
+            out, *like = described(out, "out", bf16=True)
+            same("out", like, [counts, kinds])
+            to, to_p = pointers(out)
         _check("poetx_clip_grads", self._clip(
-            len(counts), at_p, to_p, counts.buffer_info()[0], codes_p, max_norm,
+            len(counts), at_p, to_p, counts.buffer_info()[0], types_p, max_norm,
             *self._buffers(len(counts), stream)))
         return self.norm

@@ -11,13 +11,14 @@ import operator
 import numpy as np
 import torch
 
-from . import (BF16, F32, _adam_update_many, _allocating_on, _described, _same,
-               poetx_adam_update, poetx_backward, poetx_backward_workspace_size,
+from . import (BF16, F32, _adam_update_many, _allocating_on, poetx_adam_update, poetx_backward,
+               poetx_backward_workspace_size,
                poetx_build_blocks, poetx_build_workspace_size, poetx_dequantize_w0,
                poetx_fold_permutations, poetx_forward, poetx_forward_workspace_size,
                poetx_grad_norm_workspace_size,
                poetx_merge, poetx_merge_workspace_size, poetx_packed_size,
                poetx_permute_features, poetx_quantize_w0)
+from .lists import described, pointers, same
 
 _TORCH_DTYPE = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -182,9 +183,9 @@ class PoetxAdam:
 
     def _look_over(self):
         """Refuses parameters and moments that the calls would read or write wrongly."""
-        _, counts, _ = _described(self.params, "params")
+        _, counts, _ = described(self.params, "params")
         for name, tensors in (("m", self.m), ("v", self.v)):
-            _same(name, _described(tensors, name)[1], counts)
+            same(name, described(tensors, name)[1], counts)
         self._looked_over, self._sizes = [*self.params, *self.m, *self.v], counts
 
     def _state_sizes(self):
@@ -207,15 +208,15 @@ class PoetxAdam:
         if max_norm is not None and not max_norm >= 0:
             raise ValueError(f"max_norm must be at least 0, got {max_norm}")
         sizes = self._state_sizes()
-        grads, counts, _ = _described(grads, "grads")
+        grads, counts, _ = described(grads, "grads")
         if max_norm is None:
-            _same("grads", counts[:len(sizes)], sizes[:len(counts)])
+            same("grads", counts[:len(sizes)], sizes[:len(counts)])
             self.t += 1
             for p, g, m, v in zip(self.params, grads, self.m, self.v):
                 poetx_adam_update(p, g, m, v, p.numel(), self.t, self.lr, self.betas[0],
                                   self.betas[1], self.eps, self.weight_decay, stream)
             return
-        _same("grads", counts, sizes)
+        same("grads", counts, sizes)
         self.t += 1
         if not grads:
             return
@@ -224,9 +225,9 @@ class PoetxAdam:
             with _allocating_on(stream, dev):
                 self.norm = torch.empty((), dtype=torch.float32, device=dev)
                 self._workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        _adam_update_many([self.params, grads, self.m, self.v], sizes, self.t, self.lr,
-                          self.betas[0], self.betas[1], self.eps, self.weight_decay, max_norm,
-                          self.norm, self._workspace, stream)
+        kept = [pointers(t) for t in (self.params, grads, self.m, self.v)]
+        _adam_update_many(kept, sizes, self.t, self.lr, self.betas[0], self.betas[1], self.eps,
+                          self.weight_decay, max_norm, self.norm, self._workspace, stream)
 
 
 def to_device(inp, device="cuda"):
