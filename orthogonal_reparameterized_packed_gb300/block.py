@@ -219,21 +219,23 @@ class PoetxGradClip:
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
         self.norm = torch.empty((), dtype=torch.float32, device=self.device)
-        self._of_stream = {}  # handle -> (norm, workspaces)
+        self._of_stream = {}  # handle -> (norm, workspaces, tensors that the last one takes)
         lib = load_library()
         self._total, self._clip = lib.poetx_grad_norm, lib.poetx_clip_grads
 
     def _buffers(self, n, stream):
         """(norm's address, address and bytes of a workspace for n tensors, handle) of the
         stream.  Smaller workspaces are kept: a captured graph may hold them."""
-        handle, need = _stream(stream), poetx_grad_norm_workspace_size(n)
-        norm, rooms = self._of_stream.get(handle, (None, []))
-        if not rooms or rooms[-1].numel() < need:
+        handle = _stream(stream)
+        norm, rooms, most = self._of_stream.get(handle, (None, [], -1))
+        if n > most:
+            need = poetx_grad_norm_workspace_size(n)
             with _allocating_on(stream, self.device):
-                rooms.append(torch.empty((need,), dtype=torch.uint8, device=self.device))
+                if not rooms or rooms[-1].numel() < need:
+                    rooms.append(torch.empty((need,), dtype=torch.uint8, device=self.device))
                 if norm is None:
                     norm = torch.empty((), dtype=torch.float32, device=self.device)
-            self._of_stream[handle] = norm, rooms
+            self._of_stream[handle] = norm, rooms, n
         self.norm = norm
         return norm.data_ptr(), rooms[-1].data_ptr(), rooms[-1].numel(), handle
 
