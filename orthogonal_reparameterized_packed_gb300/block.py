@@ -115,7 +115,9 @@ class PoetxQKNormRope:
 
     q, k: [tokens][heads * head_dim] (or [tokens][heads][head_dim]) tensors
     whose last dimensions are contiguous; rows may be strided (slices of a
-    fused projection).  cos, sin: [rows][rot_dim / 2] float32 (rope_tables)."""
+    fused projection).  cos, sin: [rows][rot_dim / 2] float32 (rope_tables);
+    a token whose position is outside their rows gets zeros, no gradient, and sets the
+    status word (poetx_device_status)."""
 
     def __init__(self, n_q_heads, n_k_heads, head_dim, tokens, rot_dim=None, eps=1e-6,
                  interleaved=False, dtype="bf16", device="cuda", backward=False):

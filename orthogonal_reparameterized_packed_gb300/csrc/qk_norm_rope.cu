@@ -14,8 +14,8 @@
 // no lane needs another's elements to rotate; the G lanes of a row share only
 // the sums, and a warp works on 32 / G heads of a token at once: a group.  What
 // bounds it is memory traffic, 2 (forward) or 3 (backward) passes over q and k:
-// 16384 tokens of 40 heads of 128, bf16, take 55.7 us forward (6.0 TB/s) and 83.5
-// backward (6.0), in fp32 half as many tokens 54 and 82.6.  (Alternatives below
+// 16384 tokens of 40 heads of 128, bf16, take 55.8 us forward (6.0 TB/s) and 84.2
+// backward (6.0), in fp32 half as many tokens 54 and 82.7.  (Alternatives below
 // were measured before the sums of dgamma took their present form, 4 us less.)
 #include <algorithm>
 #include <atomic>
