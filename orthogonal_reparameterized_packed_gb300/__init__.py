@@ -281,6 +281,15 @@ def poetx_adam_update(theta, grad, m, v, n, step, lr, beta1=0.9, beta2=0.999, ep
         _stream(stream)))
 
 
+def _adam_update_each(vectors, step, lr, beta1, beta2, eps, weight_decay, stream):
+    """poetx_adam_update on every (theta, grad, m, v, n), tensors looked over before."""
+    call, stream = load_library().poetx_adam_update, _stream(stream)
+    for theta, grad, m, v, n in vectors:
+        _check("poetx_adam_update", call(
+            theta.data_ptr(), grad.data_ptr(), m.data_ptr(), v.data_ptr(), n, step, lr, beta1,
+            beta2, eps, weight_decay, stream))
+
+
 def poetx_quantize_w0(W0, W0_q, scales, d_in, d_out, dtype, stream=None):
     _check("poetx_quantize_w0", load_library().poetx_quantize_w0(
         _ptr(W0), _ptr(W0_q), _ptr(scales), d_in, d_out, dtype, _stream(stream)))

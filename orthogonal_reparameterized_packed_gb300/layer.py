@@ -6,12 +6,13 @@ tensors, one shared workspace, and the four calls of a training step
 from __future__ import annotations
 
 import array
+import itertools
 import operator
 
 import numpy as np
 import torch
 
-from . import (BF16, F32, _adam_update_many, _allocating_on, poetx_adam_update, poetx_backward,
+from . import (BF16, F32, _adam_update_each, _adam_update_many, _allocating_on, poetx_backward,
                poetx_backward_workspace_size,
                poetx_build_blocks, poetx_build_workspace_size, poetx_dequantize_w0,
                poetx_fold_permutations, poetx_forward, poetx_forward_workspace_size,
@@ -186,14 +187,14 @@ class PoetxAdam:
         _, counts, _ = described(self.params, "params")
         for name, tensors in (("m", self.m), ("v", self.v)):
             same(name, described(tensors, name)[1], counts)
-        self._looked_over, self._sizes = [*self.params, *self.m, *self.v], counts
+        self._looked_over, self._sizes = (*self.params, *self.m, *self.v), counts
 
     def _state_sizes(self):
         """The parameters' sizes; what was replaced since the last step is looked over."""
-        state = [*self.params, *self.m, *self.v]
-        if len(state) != len(self._looked_over) or \
-                not all(map(operator.is_, state, self._looked_over)) or \
-                array.array("q", map(torch.Tensor.numel, self.params)) != self._sizes:
+        p, m, v, looked_over = self.params, self.m, self.v, self._looked_over
+        if len(p) + len(m) + len(v) != len(looked_over) or \
+                not all(map(operator.is_, itertools.chain(p, m, v), looked_over)) or \
+                array.array("q", map(torch.Tensor.numel, p)) != self._sizes:
             self._look_over()
         return self._sizes
 
@@ -210,11 +211,11 @@ class PoetxAdam:
         sizes = self._state_sizes()
         grads, counts, _ = described(grads, "grads")
         if max_norm is None:
-            same("grads", counts[:len(sizes)], sizes[:len(counts)])
+            if counts != sizes:  # the vectors that have a gradient, as zip pairs them
+                same("grads", counts[:len(sizes)], sizes[:len(counts)])
             self.t += 1
-            for p, g, m, v in zip(self.params, grads, self.m, self.v):
-                poetx_adam_update(p, g, m, v, p.numel(), self.t, self.lr, self.betas[0],
-                                  self.betas[1], self.eps, self.weight_decay, stream)
+            _adam_update_each(zip(self.params, grads, self.m, self.v, sizes), self.t, self.lr,
+                              self.betas[0], self.betas[1], self.eps, self.weight_decay, stream)
             return
         same("grads", counts, sizes)
         self.t += 1

@@ -10,19 +10,20 @@ import torch
 
 from . import BF16, F32
 
-_FLOAT32, _EITHER = {torch.float32}, {torch.float32, torch.bfloat16}
+_EITHER = {torch.float32, torch.bfloat16}
 
 
 def described(tensors, name, bf16=False):
     """(tensors, counts, types) of any iterable of contiguous CUDA tensors, float32 or,
-    with bf16, bfloat16 too: the tensors as a list and the host array of their sizes."""
-    tensors = list(tensors)
+    with bf16, bfloat16 too: the tensors as a list (a list itself) and the host array of
+    their sizes."""
+    if type(tensors) is not list:
+        tensors = list(tensors)
     kinds = [t.dtype for t in tensors]
-    allowed = _EITHER if bf16 else _FLOAT32
-    if not (set(kinds) <= allowed and all(map(torch.Tensor.is_contiguous, tensors)) and
-            all([t.is_cuda for t in tensors])):
-        raise ValueError(f"{name}: contiguous CUDA tensors of {sorted(map(str, allowed))} are "
-                         "needed")
+    if not ((kinds.count(torch.float32) == len(kinds) or bf16 and set(kinds) <= _EITHER) and
+            all(map(torch.Tensor.is_contiguous, tensors)) and all([t.is_cuda for t in tensors])):
+        raise ValueError(f"{name}: contiguous CUDA tensors of type float32"
+                         f"{' or bfloat16' if bf16 else ''} are needed")
     return tensors, array.array("q", map(torch.Tensor.numel, tensors)), kinds
 
 
