@@ -365,6 +365,56 @@ poetx_status poetx_adam_update_many(int n_tensors, float* const* theta, const fl
                                     void* workspace, size_t workspace_bytes,
                                     poetx_stream stream);
 
+/* ------------------------------------------------------------------------
+ * The losses at the output head, from the last hidden states x and the head's
+ * weight W, without keeping the logits.  The paper has no counterpart: a
+ * training step ends in one of them.
+ *   u_tv = x_t . W_v / tau,  lse_t = log sum_v exp(u_tv)
+ *   cross entropy (tau = 1):  loss_t = lse_t - u_t,target
+ *   distillation from a teacher's top logits s_tk at the indices i_tk,
+ *   temperature tau:  p_tk = softmax over k of s_tk / tau,
+ *                     loss_t = tau^2 sum_k p_tk (log p_tk - u_t,i_tk + lse_t)
+ *   total = sum_t w_t loss_t,   dx, dW: the gradients of total
+ *   x, dx [tokens][d], W, dW [vocab][d] dtype; loss [tokens], total one
+ *   float32; weights w [tokens] float32, NULL: 1 / (tokens that count).
+ *   targets [tokens], top_indices [tokens][top]: signed integers of
+ *   index_bytes (4 or 8); top_logits [tokens][top] of logits_dtype.
+ *   dx, dW: NULL = not wanted (a head that is frozen has no dW).
+ * A negative index is no entry, whatever its logit is, nor is one whose logit
+ * is -infinity; an index from vocab on is not followed either and records
+ * POETX_ERR_INVALID_ARG in the status word.  The same index may come twice: its
+ * weights add up.  A token without an entry does not count: loss and dx are 0,
+ * and neither its x nor its weight is used (they may be NaN).  If no token
+ * counts, total and dW are 0.
+ * Logits, softmax, losses and sums are fp32.  BF16 rounds the softmax's terms to
+ * bf16 for the gradients' products, and dx and dW once more.  A logit that is
+ * not finite makes its token's loss and gradients what the formulas say (inf
+ * or NaN).
+ * The tokens that count are taken block_tokens at a time (0: as many as keep the
+ * workspace's largest part at 2 GiB); the workspace holds one block's terms, in
+ * BF16 with dW and more than one block also dW in fp32.  That of `tokens`
+ * tokens is enough for any fewer with the same block_tokens; gradients: what is
+ * wanted (POETX_GRAD_X | POETX_GRAD_W).
+ * 1 <= d, vocab <= 2^20, 1 <= top <= 1024, 1/64 <= temperature <= 64.
+ * Results do not change from run to run.  Outputs and inputs may not overlap. */
+enum { POETX_GRAD_X = 1, POETX_GRAD_W = 2 };
+
+size_t poetx_cross_entropy_workspace_size(int d, int vocab, int64_t tokens, poetx_dtype dtype,
+                                          int gradients, int64_t block_tokens);
+poetx_status poetx_cross_entropy(const void* x, const void* W, const void* targets,
+                                 int index_bytes, const float* weights, float* loss, float* total,
+                                 void* dx, void* dW, int d, int vocab, int64_t tokens,
+                                 poetx_dtype dtype, int64_t block_tokens, void* workspace,
+                                 size_t workspace_bytes, poetx_stream stream);
+size_t poetx_distill_workspace_size(int d, int vocab, int64_t tokens, int top, poetx_dtype dtype,
+                                    int gradients, int64_t block_tokens);
+poetx_status poetx_distill(const void* x, const void* W, const void* top_indices, int index_bytes,
+                           const void* top_logits, poetx_dtype logits_dtype, const float* weights,
+                           float* loss, float* total, void* dx, void* dW, int d, int vocab,
+                           int64_t tokens, int top, float temperature, poetx_dtype dtype,
+                           int64_t block_tokens, void* workspace, size_t workspace_bytes,
+                           poetx_stream stream);
+
 /* The W0 GEMM fused with the block-diagonal factors (technical summary,
  * section 2, input-centric bullet; the fusion itself is this library's):
  * with fusion on, poetx_forward computes y = R v in the epilogue of the

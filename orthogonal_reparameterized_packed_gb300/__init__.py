@@ -28,6 +28,9 @@ __all__ = [
     "poetx_qk_norm_rope_backward",
     "poetx_grad_norm_workspace_size", "poetx_grad_norm", "poetx_clip_grads",
     "poetx_adam_update_many",
+    "GRAD_X", "GRAD_W",
+    "poetx_cross_entropy_workspace_size", "poetx_cross_entropy",
+    "poetx_distill_workspace_size", "poetx_distill",
     "poetx_set_block_epilogue_fusion",
     "poetx_set_w0_split_tail",
     "poetx_set_w0_pair_mma",
@@ -43,6 +46,9 @@ ACT_RELU = 1
 ACT_SILU = 2
 ACT_GELU = 3
 ACT_GELU_TANH = 4
+
+GRAD_X = 1
+GRAD_W = 2
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpoetx.so")
 
@@ -106,6 +112,15 @@ _SIGNATURES = {
                                                             _c_ptr]),
     "poetx_adam_update_many": (_c_int, [_c_int] + [_c_ptr] * 5 + [_c_int] + [_c_f] * 6 +
                                [_c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "poetx_cross_entropy_workspace_size": (_c_size, [_c_int, _c_int, _c_i64, _c_int, _c_int,
+                                                     _c_i64]),
+    "poetx_cross_entropy": (_c_int, [_c_ptr] * 3 + [_c_int] + [_c_ptr] * 5 +
+                            [_c_int, _c_int, _c_i64, _c_int, _c_i64, _c_ptr, _c_size, _c_ptr]),
+    "poetx_distill_workspace_size": (_c_size, [_c_int, _c_int, _c_i64, _c_int, _c_int, _c_int,
+                                               _c_i64]),
+    "poetx_distill": (_c_int, [_c_ptr] * 3 + [_c_int, _c_ptr, _c_int] + [_c_ptr] * 5 +
+                      [_c_int, _c_int, _c_i64, _c_int, _c_f, _c_int, _c_i64, _c_ptr, _c_size,
+                       _c_ptr]),
     "poetx_set_block_epilogue_fusion": (_c_int, [_c_int]),
     "poetx_set_w0_split_tail": (_c_int, [_c_int]),
     "poetx_set_w0_pair_mma": (_c_int, [_c_int]),
@@ -404,6 +419,34 @@ def _adam_update_many(kept, c, step, lr, beta1, beta2, eps, weight_decay, max_no
         len(c), *[a for _, a in kept], c.buffer_info()[0], step, lr, beta1, beta2, eps,
         weight_decay, max_norm, _ptr(norm), _ptr(workspace), _nbytes(workspace),
         _stream(stream)))
+
+
+def poetx_cross_entropy_workspace_size(d, vocab, tokens, dtype, gradients,
+                                       block_tokens=0) -> int:
+    return load_library().poetx_cross_entropy_workspace_size(d, vocab, tokens, dtype, gradients,
+                                                             block_tokens)
+
+
+def poetx_cross_entropy(x, W, targets, index_bytes, weights, loss, total, dx, dW, d, vocab,
+                        tokens, dtype, block_tokens, workspace, stream=None):
+    _check("poetx_cross_entropy", load_library().poetx_cross_entropy(
+        _ptr(x), _ptr(W), _ptr(targets), index_bytes, _ptr(weights), _ptr(loss), _ptr(total),
+        _ptr(dx), _ptr(dW), d, vocab, tokens, dtype, block_tokens, _ptr(workspace),
+        _nbytes(workspace), _stream(stream)))
+
+
+def poetx_distill_workspace_size(d, vocab, tokens, top, dtype, gradients, block_tokens=0) -> int:
+    return load_library().poetx_distill_workspace_size(d, vocab, tokens, top, dtype, gradients,
+                                                       block_tokens)
+
+
+def poetx_distill(x, W, top_indices, index_bytes, top_logits, logits_dtype, weights, loss, total,
+                  dx, dW, d, vocab, tokens, top, temperature, dtype, block_tokens, workspace,
+                  stream=None):
+    _check("poetx_distill", load_library().poetx_distill(
+        _ptr(x), _ptr(W), _ptr(top_indices), index_bytes, _ptr(top_logits), logits_dtype,
+        _ptr(weights), _ptr(loss), _ptr(total), _ptr(dx), _ptr(dW), d, vocab, tokens, top,
+        temperature, dtype, block_tokens, _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def poetx_set_block_epilogue_fusion(enable: bool) -> bool:
