@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libpoetx.so")
 SOURCES = ["api.cu", "gemm_tc.cu", "gemm_pair.cu", "chain_tc.cu", "cnp_pair.cu",
            "transform_sum_tc.cu", "kernels_simt.cu", "selftest.cu", "api_block.cu", "linear.cu",
            "linear_pair.cu", "linear_stream.cu", "linear_simt.cu", "linear_split.cu",
-           "qk_norm_rope.cu", "optim.cu", "api_loss.cu", "loss.cu"]
+           "qk_norm_rope.cu", "optim.cu", "api_loss.cu", "loss.cu",
+           "loss_pair.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

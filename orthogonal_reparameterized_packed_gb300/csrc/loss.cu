@@ -12,6 +12,7 @@
 // So the tokens that count are gathered first, in order, and everything runs on
 // the gathered rows; they are taken in blocks whose logits fit the workspace.
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include "internal.h"
@@ -47,77 +48,118 @@ __device__ __forceinline__ long long index_at(const void* p, int bytes, long lon
   return bytes == 8 ? static_cast<const long long*>(p)[i] : static_cast<const int*>(p)[i];
 }
 
-// What the kernels share in the workspace.
-struct Lists {
-  int* count;   // [0]: tokens that count
-  int* pos;     // [T]: a token's gathered row, -1 where it does not count
-  int* rows;    // [T]: a gathered row's token
-  int* index;   // [T][top] of the token, -1: no entry
-  float* p;     // [T][top]
-  float* ent;   // [T]: sum_k p log p
-};
+// Entries (index, p) of a warp in ascending order of the index; n a power of two,
+// entries from `top` on are INT_MAX.
+__device__ __forceinline__ void sort_entries(int* key, float* val, int n, int lane) {
+  for (int size = 2; size <= n; size *= 2)
+    for (int stride = size / 2; stride > 0; stride /= 2) {
+      for (int i = lane; i < n / 2; i += 32) {
+        const int a = 2 * i - (i & (stride - 1)), b = a + stride;
+        const bool up = (a & size) == 0;
+        const int ka = key[a], kb = key[b];
+        if (up ? ka > kb : ka < kb) {
+          const float va = val[a], vb = val[b];
+          key[a] = kb, key[b] = ka;
+          val[a] = vb, val[b] = va;
+        }
+      }
+      __syncwarp();
+    }
+}
+
+constexpr int kEntryWarps = 4;
+constexpr int kMostEntries = 1024;
 
 // The entries of a token, a warp each: p = softmax of the teacher's logits at tau
-// over the entries that are there (for the cross entropy 1).  Differences are
-// divided by tau, not the logits: the type's lowest value stays finite.
-__global__ void __launch_bounds__(kThreads)
+// over the entries that are there (for the cross entropy 1), sorted by their
+// indices.  Differences are divided by tau, not the logits: the type's lowest value
+// stays finite.
+__global__ void __launch_bounds__(32 * kEntryWarps)
     loss_entries_kernel(const void* indices, int index_bytes, const void* logits, bool logits_bf16,
-                        long long T, int top, int V, float inv_tau, Lists l, int* status) {
+                        long long T, int top, int V, float inv_tau, LossRows l, int* status) {
+  __shared__ int keys[kEntryWarps][kMostEntries];
+  __shared__ float vals[kEntryWarps][kMostEntries];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x % 32;
-  const long long t = blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const long long t = blockIdx.x * static_cast<long long>(kEntryWarps) + warp;
   if (t >= T) return;
   const long long base = t * top;
+  int* key = keys[warp];
+  float* val = vals[warp];
+  int padded = 1;
+  while (padded < top) padded *= 2;
   bool outside = false, any = false;
   float m = -INFINITY;
-  const auto logit = [&](int k) {
-    if (logits == nullptr) return 0.f;
-    return logits_bf16 ? to_f(static_cast<const bf16*>(logits)[base + k])
-                       : static_cast<const float*>(logits)[base + k];
-  };
-  for (int k = lane; k < top; k += 32) {
-    const long long i = index_at(indices, index_bytes, base + k);
-    outside |= i >= V;
-    const bool there = i >= 0 && i < V && !(logit(k) == -INFINITY);
-    l.index[base + k] = there ? static_cast<int>(i) : -1;
-    if (there) m = fmaxf(m, logit(k));
-    any |= there;
+  for (int k = lane; k < padded; k += 32) {
+    int at = INT_MAX;
+    float v = 0.f;
+    if (k < top) {
+      const long long i = index_at(indices, index_bytes, base + k);
+      if (logits != nullptr)
+        v = logits_bf16 ? to_f(static_cast<const bf16*>(logits)[base + k])
+                        : static_cast<const float*>(logits)[base + k];
+      outside |= i >= V;
+      const bool there = i >= 0 && i < V && !(v == -INFINITY);
+      at = there ? static_cast<int>(i) : -1;
+      any |= there;
+      if (there) m = fmaxf(m, v);
+    }
+    key[k] = at;
+    val[k] = v;
   }
   m = warp_max(m);
   any = __any_sync(0xffffffffu, any);
   outside = __any_sync(0xffffffffu, outside);
   float sum = 0.f;
   for (int k = lane; k < top; k += 32)
-    if (l.index[base + k] >= 0) sum += expf((logit(k) - m) * inv_tau);
+    if (key[k] >= 0) sum += expf((val[k] - m) * inv_tau);
   const float log_sum = logf(warp_sum(sum));
-  float ent = 0.f;
+  float ent = 0.f, best = -1.f;
+  int lead = INT_MAX;
   for (int k = lane; k < top; k += 32) {
     float p = 0.f;
-    if (l.index[base + k] >= 0) {
-      const float log_p = (logit(k) - m) * inv_tau - log_sum;
+    if (key[k] >= 0) {
+      const float log_p = (val[k] - m) * inv_tau - log_sum;
       p = expf(log_p);
-      if (p > 0.f) ent += p * log_p;
-      if (isnan(log_p)) ent = log_p;
+      if (!(p == 0.f)) ent += p * log_p;
+      if (!(p <= best)) best = p, lead = key[k];
     }
-    l.p[base + k] = p;
+    val[k] = p;
   }
   ent = warp_sum(ent);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {  // the largest p, of equal ones the lowest index
+    const float other = __shfl_xor_sync(0xffffffffu, best, o);
+    const int at = __shfl_xor_sync(0xffffffffu, lead, o);
+    if (other > best || (other == best && at < lead)) best = other, lead = at;
+  }
+  __syncwarp();
+  sort_entries(key, val, padded, lane);
+  for (int k = lane; k < top; k += 32) {
+    l.index[base + k] = key[k];
+    l.p[base + k] = val[k];
+  }
   if (lane == 0) {
     l.pos[t] = any ? 0 : -1;
     l.ent[t] = ent;
+    l.lead[t] = lead < V ? lead : 0;
     if (outside) atomicCAS(status, 0, static_cast<int>(POETX_ERR_INVALID_ARG));
   }
 }
 
-// pos[t] (0 or -1) -> the number of tokens before t that count, or -1; rows its
-// inverse.  One CTA, kOrderThreads tokens at a time.
-__global__ void __launch_bounds__(kOrderThreads) loss_order_kernel(Lists l, long long T) {
+// pos[t] (0 or -1) -> the number of tokens before t that count, or -1; token its
+// inverse; the largest weight; the blocks' flags cleared.  One CTA, kOrderThreads
+// tokens at a time.
+__global__ void __launch_bounds__(kOrderThreads)
+    loss_order_kernel(LossRows l, long long T, const float* __restrict__ weights, int blocks) {
   __shared__ int sums[32];
+  __shared__ float largest[32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   int before = 0;
+  float most = 0.f;
   for (long long t0 = 0; t0 < T; t0 += kOrderThreads) {
     const long long t = t0 + threadIdx.x;
     const bool on = t < T && l.pos[t] >= 0;
@@ -132,36 +174,66 @@ __global__ void __launch_bounds__(kOrderThreads) loss_order_kernel(Lists l, long
     mine += __popc(mask & ((1u << lane) - 1));
     if (on) {
       l.pos[t] = mine;
-      l.rows[mine] = static_cast<int>(t);
+      l.token[mine] = static_cast<int>(t);
+      if (weights != nullptr) most = fmaxf(most, fabsf(weights[t]));
     }
     before += all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) l.count[0] = before;
+  for (int b = threadIdx.x; b < blocks; b += kOrderThreads) l.again[b] = 0;
+  most = warp_max(most);
+  if (lane == 0) largest[warp] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < 32; ++w) most = fmaxf(most, largest[w]);
+    *l.count = before;
+    *l.most = weights == nullptr ? 1.f / static_cast<float>(max(1, before)) : most > 0.f ? most : 1.f;
+  }
 }
 
-// A warp per token: the rows that count to their places, zeros to dx and loss of
-// the others; warps from T on: zeros to the gathered rows behind the last.
+// How far above its lead entry's exponent a row's reference lies, and the largest
+// logit's exponent that may lie above the reference (below it: never by more than
+// kAbove but for rounding), in powers of 2.  The terms are then between 2^-126 and
+// 2^44: no sum or product of V of them leaves fp32's or bf16's range, and the
+// largest is at least 2^-28.  A token whose loss is above (28 + 44) log 2 = 50 does
+// not fit; its block is taken again with the largest logit as the reference.
+constexpr float kAbove = 28.f, kFits = 44.f;
+
+// A warp per token: the tokens that count to their rows, zeros to dx and loss of
+// the others; warps from T on: zeros to the rows behind the last, to all of them or
+// up to a multiple of 64.  unit: log2(e) / tau where references are wanted, else 0.
 template <typename TX>
 __global__ void __launch_bounds__(kThreads)
-    loss_gather_kernel(const TX* __restrict__ x, Lists l, long long T, int d, TX* __restrict__ xg,
-                       float* __restrict__ loss, TX* __restrict__ dx) {
+    loss_gather_kernel(const TX* __restrict__ x, const TX* __restrict__ W, LossRows l, long long T,
+                       int d, long long ldw, TX* __restrict__ xg, long long ldx, bool zero_all,
+                       float unit, float* __restrict__ loss, TX* __restrict__ dx) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % 32;
   const long long t = blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
-  if (t >= 2 * T) return;
   TX zero;
   from_f(zero, 0.f);
   if (t >= T) {
     const long long r = t - T;
-    if (r >= *l.count)
-      for (int c = lane; c < d; c += 32) xg[r * d + c] = zero;
+    const long long n = *l.count;
+    if (r >= n && r < (zero_all ? T : (n + 63) / 64 * 64))
+      for (int c = lane; c < d; c += 32) xg[r * ldx + c] = zero;
     return;
   }
   const int at = l.pos[t];
   if (at >= 0) {
-    for (int c = lane; c < d; c += 32) xg[static_cast<long long>(at) * d + c] = x[t * d + c];
+    const TX* lead = W + static_cast<long long>(l.lead[t]) * ldw;
+    TX* to = xg + at * ldx;
+    float dot = 0.f;
+    for (int c = lane; c < d; c += 32) {
+      const TX v = x[t * d + c];
+      to[c] = v;
+      if (unit > 0.f) dot = fmaf(to_f(v), to_f(lead[c]), dot);
+    }
+    if (unit > 0.f) {
+      dot = warp_sum(dot);
+      if (lane == 0) l.ref[at] = fmaf(dot, unit, kAbove);
+    }
     return;
   }
   if (lane == 0) loss[t] = 0.f;
@@ -169,10 +241,117 @@ __global__ void __launch_bounds__(kThreads)
     for (int c = lane; c < d; c += 32) dx[t * d + c] = zero;
 }
 
+// What becomes of a block's statistics.
+struct FinishArgs {
+  LossRows rows;
+  const float2* part;
+  long long ldp, first, block;
+  int parts, top, d;
+  float unit, tau;
+  const float* weights;
+  float* loss;
+  bf16* E;  // null: no gradients
+  long long lde;
+  bf16* x;  // the block's rows; null: no dW
+  long long ldx;
+  bool second;
+};
+
+constexpr int kFinishRows = 8;
+
+// Eight rows per CTA.  The parts of their sums (all threads), then a warp per row:
+// its loss, its factor, and in E the entries' terms e - p sum.  A row whose reference
+// does not fit sets its block's flag.  The second pass does this again where the flag
+// is set, and scales the rows of x for dW.
+__global__ void __launch_bounds__(kThreads) loss_finish_kernel(const FinishArgs a) {
+  __shared__ float2 sums[kThreads / 32][kFinishRows];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int count = *a.rows.count;
+  const long long n = max(0ll, min(a.block, count - a.first));
+  const long long r0 = blockIdx.x * static_cast<long long>(kFinishRows);
+  if (r0 >= n) return;
+  int* again = a.rows.again + a.first / a.block;
+  const bool own = a.E == nullptr;  // every part has its own reference
+  const long long row = r0 + warp, r = a.first + row;
+  if (!a.second || *again != 0) {
+    const int j = threadIdx.x % kFinishRows;
+    float m = -INFINITY, s = 0.f;
+    const auto add = [&](float m2, float s2) {
+      if (own) {
+        const float top = fmaxf(m, m2);
+        // a largest of the row's that is -inf or equal has the factor 1
+        s = s * (m == top ? 1.f : exp2f((m - top) * a.unit)) +
+            s2 * (m2 == top ? 1.f : exp2f((m2 - top) * a.unit));
+        m = top;
+      } else {
+        m = fmaxf(m, m2);
+        s += s2;
+      }
+    };
+    if (r0 + j < n)
+      for (int i = threadIdx.x / kFinishRows; i < a.parts; i += kThreads / kFinishRows) {
+        const float2 v = a.part[i * a.ldp + r0 + j];
+        add(v.x, v.y);
+      }
+#pragma unroll
+    for (int o = kFinishRows; o < 32; o *= 2) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      add(m2, s2);
+    }
+    if (lane < kFinishRows) sums[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) add(sums[w][warp].x, sums[w][warp].y);
+    if (row < n) {
+      const float ref = own ? (m == -INFINITY ? 0.f : m * a.unit) : a.rows.ref[r];
+      // an infinite logit: the sum is infinite too
+      const float log_s = m == INFINITY ? 0.f : log2f(s);
+      const int t = a.rows.token[r];
+      const long long base = static_cast<long long>(t) * a.top;
+      float sum = 0.f;
+      for (int k = lane; k < a.top; k += 32) {
+        const int i = a.rows.index[base + k];
+        if (i < 0) continue;
+        const float over = fmaf(a.rows.z[base + k], a.unit, -ref), p = a.rows.p[base + k];
+        if (!(p == 0.f)) sum += p * (log_s - over);
+        if (!own && (k == 0 || a.rows.index[base + k - 1] != i)) {
+          float all = p;
+          for (int q = k + 1; q < a.top && a.rows.index[base + q] == i; ++q)
+            all += a.rows.p[base + q];
+          a.E[row * a.lde + i] = __float2bfloat16_rn(exp2f(over) - all * s);
+        }
+      }
+      sum = warp_sum(sum);
+      if (lane == 0) {
+        a.loss[t] = a.tau * a.tau * (a.rows.ent[t] + 0.69314718056f * sum);
+        if (!own) {
+          a.rows.scale[r] = make_float2(
+              a.tau / s, a.weights != nullptr ? a.weights[t] : 1.f / static_cast<float>(count));
+          const float above = m * a.unit - ref;
+          if (!a.second && (above > kFits || above < -2.f * kAbove)) {
+            a.rows.ref[r] = m * a.unit;
+            *again = 1;
+          }
+        }
+      }
+    }
+  }
+  if (a.second && a.x != nullptr && row < n) {
+    __syncwarp();
+    const float2 f = a.rows.scale[r];
+    const float by = f.x * (f.y / *a.rows.most);
+    bf16* x = a.x + row * a.ldx;
+    for (int c = lane; c < a.d; c += 32) x[c] = __float2bfloat16_rn(__bfloat162float(x[c]) * by);
+  }
+}
+
 // A CTA per gathered row of the block: its loss from the fp32 logits z, and in
 // place of them dz where the gradients are wanted (rows that do not count: 0).
 __global__ void __launch_bounds__(kThreads)
-    loss_rows_kernel(float* __restrict__ z, Lists l, long long first, int V, int top,
+    loss_rows_kernel(float* __restrict__ z, LossRows l, long long first, int V, int top,
                      float inv_tau, float tau, const float* __restrict__ weights, bool grad,
                      float* __restrict__ loss) {
   pdl_wait();
@@ -202,7 +381,7 @@ __global__ void __launch_bounds__(kThreads)
   s = 0.f;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) s += ss[w];
-  const long long t = l.rows[r], base = t * top;
+  const long long t = l.token[r], base = t * top;
   const float log_s = logf(s);
   if (warp == 0) {
     float sum = 0.f;
@@ -228,7 +407,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // total = sum over the tokens that count of w loss, in 64 bits, one CTA.
 __global__ void __launch_bounds__(kOrderThreads)
-    loss_total_kernel(const float* __restrict__ loss, const float* __restrict__ weights, Lists l,
+    loss_total_kernel(const float* __restrict__ loss, const float* __restrict__ weights, LossRows l,
                       long long T, float* __restrict__ total) {
   pdl_wait();
   pdl_trigger();
@@ -321,88 +500,163 @@ cudaError_t product(const Product& p, cudaStream_t s) {
 }
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+long long round64(long long n) { return (n + 63) / 64 * 64; }
 
-constexpr size_t kBlockBytes = size_t{1} << 31;  // of logits at a time
+constexpr size_t kBlockBytes = size_t{1} << 31;  // of a block's terms
 
+// Elements between rows of d features as TMA operands (16-byte multiples).
+long long pitch_of(int d, bool is_bf16) { return !is_bf16 || d % 8 == 0 ? d : round64(d); }
+
+// Where everything lies in the workspace.
 struct Plan {
-  long long block;
-  size_t count = 0, pos, rows, index, p, ent, xg, z, acc, total;
-  Plan(const LossArgs& a, bool want_dw) {
-    const size_t T = static_cast<size_t>(a.T);
-    block = a.block > 0 ? a.block
-                        : static_cast<long long>(kBlockBytes / (4 * static_cast<size_t>(a.V)));
-    block = std::max<long long>(1, std::min<long long>(block, a.T));
-    block = std::min<long long>(block, 64ll * 65535);
+  long long block;  // rows taken at a time, a multiple of 64
+  int blocks;
+  long long ldx, lde, ldp;
+  size_t meta = 0, again, pos, token, index, p, ent, lead, z, ref, scale, xg, wp, terms, part, acc,
+         total;
+  Plan(const LossArgs& a, bool want_dx, bool want_dw) {
+    const size_t T = static_cast<size_t>(a.T), es = a.is_bf16 ? 2 : 4;
+    const bool grad = want_dx || want_dw;
+    lde = a.is_bf16 ? round64(a.V) : a.V;
+    ldx = pitch_of(a.d, a.is_bf16);
+    block = a.block > 0 ? a.block : static_cast<long long>(kBlockBytes / es / lde / 64 * 64);
+    block = std::max(64ll, std::min(round64(block), round64(a.T)));
+    blocks = static_cast<int>((a.T + block - 1) / block);
+    ldp = block;
     size_t at = 256;
     const auto take = [&](size_t bytes) {
       const size_t here = at;
       at += round256(bytes);
       return here;
     };
+    again = take(4 * T);  // a block has at least 64 rows, but fewer tokens more blocks
     pos = take(4 * T);
-    rows = take(4 * T);
+    token = take(4 * T);
     index = take(4 * T * a.top);
     p = take(4 * T * a.top);
     ent = take(4 * T);
-    xg = take((a.is_bf16 ? 2 : 4) * T * a.d);
-    z = take(4 * static_cast<size_t>(block) * a.V);
-    acc = take(want_dw && a.is_bf16 ? 4 * static_cast<size_t>(a.V) * a.d : 0);
+    lead = take(4 * T);
+    z = take(4 * T * a.top);
+    ref = take(4 * T);
+    scale = take(8 * T);
+    xg = take(es * static_cast<size_t>(round64(a.T)) * ldx);
+    wp = take(ldx != a.d ? es * static_cast<size_t>(a.V) * ldx : 0);
+    terms = take(!a.is_bf16 || grad ? es * static_cast<size_t>(block) * lde : 0);
+    part = take(a.is_bf16 ? sizeof(float2) * static_cast<size_t>(loss_parts(a.V)) * ldp : 0);
+    acc = take(want_dw && a.is_bf16 && blocks > 1 ? 4 * static_cast<size_t>(a.V) * a.d : 0);
     total = at;
   }
 };
 
-template <typename T>
-cudaError_t run(const LossArgs& a, char* ws, cudaStream_t s) {
-  const Plan plan(a, a.dW != nullptr);
-  Lists l;
-  l.count = reinterpret_cast<int*>(ws + plan.count);
-  l.pos = reinterpret_cast<int*>(ws + plan.pos);
-  l.rows = reinterpret_cast<int*>(ws + plan.rows);
-  l.index = reinterpret_cast<int*>(ws + plan.index);
-  l.p = reinterpret_cast<float*>(ws + plan.p);
-  l.ent = reinterpret_cast<float*>(ws + plan.ent);
-  T* xg = reinterpret_cast<T*>(ws + plan.xg);
-  float* z = reinterpret_cast<float*>(ws + plan.z);
-  float* acc = a.is_bf16 ? reinterpret_cast<float*>(ws + plan.acc) : static_cast<float*>(a.dW);
-  const float inv_tau = 1.f / a.tau;
-  const unsigned warps = kThreads / 32;
-  cudaError_t e;
-  const auto launched = [&](const char* tag, auto&& call) {
-    prof_begin(tag, s);
-    cudaError_t err = call();
-    prof_end(tag, s);
-    return err != cudaSuccess ? err : cudaGetLastError();
-  };
-  e = launched("loss_entries", [&] {
-    return launch_pdl(loss_entries_kernel, dim3(static_cast<unsigned>((a.T + warps - 1) / warps)),
-                      dim3(kThreads), 0, s, a.indices, a.index_bytes, a.top_logits, a.top_bf16,
-                      a.T, a.top, a.V, inv_tau, l, device_status_ptr());
-  });
-  if (e != cudaSuccess) return e;
-  e = launched("loss_order", [&] {
-    return launch_pdl(loss_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, l, a.T);
-  });
-  if (e != cudaSuccess) return e;
-  e = launched("loss_gather", [&] {
-    return launch_pdl(loss_gather_kernel<T>,
-                      dim3(static_cast<unsigned>((2 * a.T + warps - 1) / warps)), dim3(kThreads),
-                      0, s, static_cast<const T*>(a.x), l, a.T, a.d, xg, a.loss,
-                      static_cast<T*>(a.dx));
-  });
-  if (e != cudaSuccess) return e;
+template <typename F>
+cudaError_t launched(const char* tag, cudaStream_t s, F&& call) {
+  prof_begin(tag, s);
+  const cudaError_t e = call();
+  prof_end(tag, s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+unsigned warps_grid(long long warps) {
+  return static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32));
+}
+
+// rows of d features onto rows of ld: 16-byte multiples, which TMA needs.
+__global__ void __launch_bounds__(kThreads)
+    loss_pad_kernel(const bf16* __restrict__ in, int d, bf16* __restrict__ out, long long ld,
+                    long long rows) {
+  pdl_wait();
+  pdl_trigger();
+  const long long r = blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
+  if (r >= rows) return;
+  for (int c = threadIdx.x % 32; c < d; c += 32) out[r * ld + c] = in[r * d + c];
+}
+
+cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, char* ws,
+                     cudaStream_t s) {
   const bool grad = a.dx != nullptr || a.dW != nullptr;
+  bf16* xg = reinterpret_cast<bf16*>(ws + plan.xg);
+  bf16* E = grad ? reinterpret_cast<bf16*>(ws + plan.terms) : nullptr;
+  cudaError_t e;
+  LossProducts g;
+  g.W = a.W;
+  g.ldw = g.ldx = plan.ldx;
+  if (plan.ldx != a.d) {
+    bf16* wp = reinterpret_cast<bf16*>(ws + plan.wp);
+    g.W = wp;
+    e = launched("loss_pad", s, [&] {
+      return launch_pdl(loss_pad_kernel, dim3(warps_grid(a.V)), dim3(kThreads), 0, s,
+                        static_cast<const bf16*>(a.W), a.d, wp, plan.ldx,
+                        static_cast<long long>(a.V));
+    });
+    if (e != cudaSuccess) return e;
+  }
+  g.E = E;
+  g.lde = plan.lde;
+  g.part = reinterpret_cast<float2*>(ws + plan.part);
+  g.ldp = plan.ldp;
+  g.unit = 1.44269504089f / a.tau;
+  g.block = plan.block;
+  g.d = a.d;
+  g.V = a.V;
+  g.top = a.top;
+  g.dx = a.dx;
+  g.dW = a.dW;
+  g.acc = plan.blocks > 1 ? reinterpret_cast<float*>(ws + plan.acc) : nullptr;
+  g.rows = l;
+  FinishArgs f = {};
+  f.rows = l;
+  f.part = g.part;
+  f.ldp = g.ldp;
+  f.block = plan.block;
+  f.parts = loss_parts(a.V);
+  f.top = a.top;
+  f.d = a.d;
+  f.unit = g.unit;
+  f.tau = a.tau;
+  f.weights = a.weights;
+  f.loss = a.loss;
+  f.E = E;
+  f.lde = g.lde;
+  f.ldx = g.ldx;
+  const dim3 finish_grid(static_cast<unsigned>((plan.block + kFinishRows - 1) / kFinishRows));
+  for (int b = 0; b < plan.blocks; ++b) {
+    bf16* xb = xg + b * plan.block * plan.ldx;
+    g.first = f.first = b * plan.block;
+    g.x = xb;
+    g.x_rows = std::min(plan.block, round64(a.T) - g.first);
+    for (int pass = 0; pass < (grad ? 2 : 1); ++pass) {
+      if ((e = loss_logits(g, pass > 0, s)) != cudaSuccess) return e;
+      f.second = pass > 0;
+      f.x = a.dW != nullptr ? xb : nullptr;
+      e = launched("loss_finish", s, [&] {
+        return launch_pdl(loss_finish_kernel, finish_grid, dim3(kThreads), 0, s, f);
+      });
+      if (e != cudaSuccess) return e;
+    }
+    if (a.dx != nullptr && (e = loss_dx(g, s)) != cudaSuccess) return e;
+    if (a.dW != nullptr && (e = loss_dw(g, s)) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char* ws,
+                    cudaStream_t s) {
+  float* xg = reinterpret_cast<float*>(ws + plan.xg);
+  float* z = reinterpret_cast<float*>(ws + plan.terms);
+  const bool grad = a.dx != nullptr || a.dW != nullptr;
+  cudaError_t e;
   for (long long first = 0; first < a.T; first += plan.block) {
     const long long rows = std::min(plan.block, a.T - first);
-    const T* xb = xg + first * a.d;
+    const float* xb = xg + first * a.d;
     Product p = {};
     p.A = xb, p.am = a.d, p.ak = 1;
     p.B = a.W, p.bk = 1, p.bn = a.d;
     p.M = rows, p.N = a.V, p.K = a.d;
     p.out32 = z;
-    if ((e = product<T, T, T>(p, s)) != cudaSuccess) return e;
-    e = launched("loss_rows", [&] {
+    if ((e = product<float, float, float>(p, s)) != cudaSuccess) return e;
+    e = launched("loss_rows", s, [&] {
       return launch_pdl(loss_rows_kernel, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, s,
-                        z, l, first, a.V, a.top, inv_tau, a.tau, a.weights, grad, a.loss);
+                        z, l, first, a.V, a.top, 1.f / a.tau, a.tau, a.weights, grad, a.loss);
     });
     if (e != cudaSuccess) return e;
     if (a.dx != nullptr) {
@@ -410,35 +664,77 @@ cudaError_t run(const LossArgs& a, char* ws, cudaStream_t s) {
       q.A = z, q.am = a.V, q.ak = 1;
       q.B = a.W, q.bk = a.d, q.bn = 1;
       q.M = rows, q.N = a.d, q.K = a.V;
-      q.out = a.dx, q.rows = l.rows, q.limit = l.count, q.first = first;
-      if ((e = product<float, T, T>(q, s)) != cudaSuccess) return e;
+      q.out = a.dx, q.rows = l.token, q.limit = l.count, q.first = first;
+      if ((e = product<float, float, float>(q, s)) != cudaSuccess) return e;
     }
     if (a.dW != nullptr) {
       Product q = {};
       q.A = z, q.am = 1, q.ak = a.V;
       q.B = xb, q.bk = a.d, q.bn = 1;
       q.M = a.V, q.N = a.d, q.K = rows;
-      q.out32 = acc, q.add = first > 0;
-      q.out = a.is_bf16 && first + plan.block >= a.T ? a.dW : nullptr;
-      if ((e = product<float, T, T>(q, s)) != cudaSuccess) return e;
+      q.out32 = static_cast<float*>(a.dW), q.add = first > 0;
+      if ((e = product<float, float, float>(q, s)) != cudaSuccess) return e;
     }
   }
-  return launched("loss_total", [&] {
-    return launch_pdl(loss_total_kernel, dim3(1), dim3(kOrderThreads), 0, s,
-                      static_cast<const float*>(a.loss), a.weights, l, a.T, a.total);
+  return cudaSuccess;
+}
+
+template <typename TX>
+cudaError_t run_gather(const LossArgs& a, const Plan& plan, const LossRows& l, char* ws,
+                       cudaStream_t s) {
+  const bool grad = a.dx != nullptr || a.dW != nullptr;
+  return launched("loss_gather", s, [&] {
+    return launch_pdl(loss_gather_kernel<TX>, dim3(warps_grid(a.T + round64(a.T))),
+                      dim3(kThreads), 0, s, static_cast<const TX*>(a.x),
+                      static_cast<const TX*>(a.W), l, a.T, a.d, static_cast<long long>(a.d),
+                      reinterpret_cast<TX*>(ws + plan.xg), plan.ldx, !a.is_bf16,
+                      a.is_bf16 && grad ? 1.44269504089f / a.tau : 0.f, a.loss,
+                      static_cast<TX*>(a.dx));
   });
 }
 
 }  // namespace
 
 size_t head_loss_scratch(const LossArgs& a, bool want_dx, bool want_dw) {
-  (void)want_dx;
-  return Plan(a, want_dw).total;
+  return Plan(a, want_dx, want_dw).total;
 }
 
 cudaError_t head_loss(const LossArgs& a, void* scratch, cudaStream_t s) {
   char* ws = static_cast<char*>(scratch);
-  return a.is_bf16 ? run<bf16>(a, ws, s) : run<float>(a, ws, s);
+  const Plan plan(a, a.dx != nullptr, a.dW != nullptr);
+  LossRows l;
+  l.count = reinterpret_cast<int*>(ws + plan.meta);
+  l.most = reinterpret_cast<float*>(ws + plan.meta + 4);
+  l.again = reinterpret_cast<int*>(ws + plan.again);
+  l.pos = reinterpret_cast<int*>(ws + plan.pos);
+  l.token = reinterpret_cast<int*>(ws + plan.token);
+  l.index = reinterpret_cast<int*>(ws + plan.index);
+  l.p = reinterpret_cast<float*>(ws + plan.p);
+  l.ent = reinterpret_cast<float*>(ws + plan.ent);
+  l.lead = reinterpret_cast<int*>(ws + plan.lead);
+  l.z = reinterpret_cast<float*>(ws + plan.z);
+  l.ref = reinterpret_cast<float*>(ws + plan.ref);
+  l.scale = reinterpret_cast<float2*>(ws + plan.scale);
+  cudaError_t e = launched("loss_entries", s, [&] {
+    return launch_pdl(loss_entries_kernel,
+                      dim3(static_cast<unsigned>((a.T + kEntryWarps - 1) / kEntryWarps)),
+                      dim3(32 * kEntryWarps), 0, s, a.indices, a.index_bytes, a.top_logits,
+                      a.top_bf16, a.T, a.top, a.V, 1.f / a.tau, l, device_status_ptr());
+  });
+  if (e != cudaSuccess) return e;
+  e = launched("loss_order", s, [&] {
+    return launch_pdl(loss_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, l, a.T, a.weights,
+                      plan.blocks);
+  });
+  if (e != cudaSuccess) return e;
+  e = a.is_bf16 ? run_gather<bf16>(a, plan, l, ws, s) : run_gather<float>(a, plan, l, ws, s);
+  if (e != cudaSuccess) return e;
+  e = a.is_bf16 ? run_bf16(a, plan, l, ws, s) : run_f32(a, plan, l, ws, s);
+  if (e != cudaSuccess) return e;
+  return launched("loss_total", s, [&] {
+    return launch_pdl(loss_total_kernel, dim3(1), dim3(kOrderThreads), 0, s,
+                      static_cast<const float*>(a.loss), a.weights, l, a.T, a.total);
+  });
 }
 
 }  // namespace poetx

@@ -1,0 +1,653 @@
+// The products of the head's losses in bf16, on CTA pairs (loss.h):
+//   logits  z = x W^T with the softmax's statistics in the epilogue
+//   dx      dx = E W, each row times its factor, stored to its token's row
+//   dw      dW = E^T x
+// The kernel is linear_pair's with other epilogues: clusters of two CTAs compute
+// tiles of 256 x 256 with tcgen05.mma.cta_group::2 over 64-wide K steps from a TMA
+// ring, two TMEM accumulators, 16 epilogue warps (64 columns of a 32-row quarter
+// each).  dw's A is E as it lies, [rows][V]: an MN-major operand.  The rows are
+// counted on the GPU: tiles behind the last row are not computed.
+//
+// The logits are never stored.  A tile's epilogue takes each z once: its
+// exponential relative to the row's reference, the sum and the largest of 64
+// columns; the entries' logits (a token's entries are sorted, so that a warp finds
+// those of its 64 columns by bisection) are read from TMEM a column at a time.
+//
+// Every wait is bounded as in gemm_pair.cu.
+#include <algorithm>
+#include <climits>
+#include <mutex>
+
+#include "internal.h"
+#include "loss.h"
+#include "poetx.h"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+
+namespace poetx {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+enum Kind { kLogits, kDx, kDw };
+
+constexpr int BN = 256;
+constexpr int kA = BM * BK * 2;        // this CTA's 128 rows, one K step
+constexpr int kB = (BN / 2) * BK * 2;  // this CTA's half of B, one K step
+constexpr int kStage = kA + kB;
+constexpr int kStages = 6;
+constexpr int kRing = kStages * kStage;
+constexpr int kSides = BN / 64;  // of 64 columns, four warps each
+constexpr int kEpiWarps = 4 * kSides;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kChunk = 32;  // columns that a warp stages at a time
+constexpr int kSlot = 32 * kChunk * 2;
+constexpr int kSmem = kRing + kEpiWarps * kSlot + 256;
+constexpr int kGroupM = 8;
+constexpr uint32_t kAcc = 256;  // TMEM columns of an accumulator
+static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+
+struct PairArgs {
+  int n_tiles, N, K, V, top;
+  long long M;           // kDw: the output's rows
+  long long first, block;
+  long long ld, ldp;
+  const int* only;       // null, or nothing is done while it is 0
+  float unit;
+  bool store, vec;       // kLogits: E is wanted; output rows are 16-byte aligned
+  float2* part;
+  bf16* out;             // dx or dW
+  float* acc;
+  LossRows rows;
+  int* status;
+};
+
+__device__ __forceinline__ void unit_tile(int u, int m_pairs, int n_tiles, int& mp, int& nt) {
+  const int per_group = kGroupM * n_tiles;
+  const int g = u / per_group, r = u - g * per_group;
+  const int rows = min(kGroupM, m_pairs - g * kGroupM);
+  mp = g * kGroupM + r % rows;
+  nt = r / rows;
+}
+
+// A warp's staging tile: 32 rows of 64 bytes as TMA's 64-byte swizzle lays them out.
+struct Staged {
+  uint8_t* base;
+
+  __device__ __forceinline__ uint4* piece(int row, int q) const {  // 16 bytes
+    return reinterpret_cast<uint4*>(base + row * 64 + ((q ^ (row >> 1 & 3)) << 4));
+  }
+  __device__ __forceinline__ bf16* value(int row, int col) const {
+    return reinterpret_cast<bf16*>(piece(row, col >> 3)) + (col & 7);
+  }
+};
+
+// 16 values of this thread's row -> pieces 2 part, 2 part + 1 of its staging row
+__device__ __forceinline__ void stage_part(const Staged& slot, int lane, int part,
+                                           const float (&v)[16]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      w[h] = pack_bf16x2(__float_as_uint(v[8 * q + 2 * h]), __float_as_uint(v[8 * q + 2 * h + 1]));
+    st_shared_v4(slot.piece(lane, 2 * part + q), w[0], w[1], w[2], w[3]);
+  }
+}
+
+// One accumulator column of this thread's lane.
+__device__ __forceinline__ float tmem_load_1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr)
+               : "memory");
+  tmem_load_wait();
+  return __uint_as_float(r);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 logits of a row: their exponentials, sum and largest; `live` of them are in
+// the vocabulary, the others become 0.
+__device__ __forceinline__ void exp_part(float (&v)[16], float unit, float ref, int live,
+                                         float& sum, float& most) {
+  if (live >= 16) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      most = fmaxf(most, v[j]);
+      v[j] = exp2_fast(fmaf(v[j], unit, -ref));
+      sum += v[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (j < live) {
+        most = fmaxf(most, v[j]);
+        v[j] = exp2_fast(fmaf(v[j], unit, -ref));
+        sum += v[j];
+      } else {
+        v[j] = 0.f;
+      }
+    }
+  }
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kThreads, 1)
+    loss_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmOut, const PairArgs p) {
+  constexpr bool A_MN = KIND == kDw, B_MN = KIND != kLogits;
+  extern __shared__ __align__(1024) uint8_t base[];  // 128B-swizzled tiles start on 1024 bytes
+  if ((smem_u32(base) & 1023u) != 0) {  // the declared alignment, which the tiles rely on
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, static_cast<int>(POETX_ERR_CUDA));
+    return;
+  }
+  uint8_t* ring = base;  // stage s: A (16 KiB), then this CTA's half of B
+  uint8_t* staging = base + kRing;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kSlot);  // leader
+  uint64_t* empty_bar = full_bar + kStages;   // each CTA: its slot is free
+  uint64_t* tfull_bar = empty_bar + kStages;  // [2] each CTA: accumulator ready
+  uint64_t* tempty_bar = tfull_bar + 2;       // [2] leader: accumulator drained
+  uint64_t* drain_bar = tempty_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int first_unit = static_cast<int>(cluster_id_x());
+  const int step = static_cast<int>(cluster_count_x());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull_bar[a], 1);
+      mbar_init(&tempty_bar[a], 2 * kEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 2 * kAcc);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before either signals the other
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  // the same for every thread of the grid
+  const long long counted = *p.rows.count;
+  const long long n = max(0ll, min(p.block, counted - p.first));  // rows of this block
+  const long long M = KIND == kDw ? p.M : n;
+  const int m_pairs = static_cast<int>((M + 2 * BM - 1) / (2 * BM));
+  const int k_steps = static_cast<int>(((KIND == kDw ? n : p.K) + BK - 1) / BK);
+  int units = m_pairs * p.n_tiles;
+  if (p.only != nullptr && *p.only == 0) units = 0;
+  if (KIND == kDw && n == 0 && p.first > 0) units = 0;  // the block before was the last
+  const int mma_units = k_steps > 0 ? units : 0;  // dW without a row is 0
+
+  const uint32_t full0 = map_peer(smem_u32(full_bar), 0);
+  const uint32_t tempty0 = map_peer(smem_u32(tempty_bar), 0);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    int stage = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool ok = true;
+    for (int u = first_unit; u < mma_units && ok; u += step) {
+      int mp, nt;
+      unit_tile(u, m_pairs, p.n_tiles, mp, nt);
+      const int a_row = mp * 2 * BM + static_cast<int>(rank) * BM;
+      const int b_n = nt * BN + static_cast<int>(rank) * (BN / 2);
+      for (int ks = 0; ks < k_steps; ++ks) {
+        if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) {
+          record_timeout(p.status, abort_flag);
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStage);
+          uint8_t* a_dst = ring + stage * kStage;
+          uint8_t* b_dst = a_dst + kA;
+          const uint32_t bar = full0 + static_cast<uint32_t>(stage * 8);
+          if (!A_MN) {
+            tma_load_2d_pair(a_dst, &tmA, bar, ks * BK, a_row);
+          } else {
+            tma_load_2d_pair(a_dst, &tmA, bar, a_row, ks * BK);
+            tma_load_2d_pair(a_dst + 8192, &tmA, bar, a_row + 64, ks * BK);
+          }
+          if (!B_MN) {
+            tma_load_2d_pair(b_dst, &tmB, bar, ks * BK, b_n);
+          } else {
+            tma_load_2d_pair(b_dst, &tmB, bar, b_n, ks * BK);
+            tma_load_2d_pair(b_dst + 8192, &tmB, bar, b_n + 64, ks * BK);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // every slot this CTA filled is released again before it leaves
+    const int outstanding = issued < kStages ? static_cast<int>(issued) : kStages;
+    int st = stage;
+    uint32_t ph = phase;
+    for (int i = 0; i < outstanding; ++i) {
+      if (--st < 0) {
+        st = kStages - 1;
+        ph ^= 1;
+      }
+      const unsigned long long t0 = global_timer_ns();
+      while (!mbar_try_wait_cluster(&empty_bar[st], ph) &&
+             global_timer_ns() - t0 < (ok ? kWaitLimitNs : 10000000ull)) {
+      }
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      // -------------------------------------------------- MMA issuer (pair)
+      constexpr uint32_t IDESC = instr_desc_bf16(2 * BM, BN, A_MN, B_MN);
+      const uint32_t empty_own = smem_u32(empty_bar);
+      const uint32_t tfull_own = smem_u32(tfull_bar);
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      bool any_mma = false;
+      for (int u = first_unit; u < mma_units && ok; u += step) {
+        if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1, abort_flag)) {
+          record_timeout(p.status, abort_flag);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc) * kAcc;
+        for (int ks = 0; ks < k_steps; ++ks) {
+          if (!mbar_wait(&full_bar[stage], phase, abort_flag)) {
+            record_timeout(p.status, abort_flag);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(ring) + stage * kStage;
+          const uint32_t b_base = a_base + kA;
+          // 16 of K: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
+          const uint64_t adesc0 = smem_desc_sw128(a_base, A_MN ? 8192 : 16, 1024);
+          const uint64_t bdesc0 = smem_desc_sw128(b_base, B_MN ? 8192 : 16, 1024);
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < BK / 16; ++j)
+              umma_bf16_pair(d_tmem, adesc0 + j * (A_MN ? 128 : 2), bdesc0 + j * (B_MN ? 128 : 2),
+                             IDESC, (ks > 0 || j > 0) ? 1u : 0u);
+            // the slot is free in both CTAs once the MMAs have read it
+            umma_commit_both(empty_own + static_cast<uint32_t>(stage * 8));
+          }
+          __syncwarp();
+          any_mma = true;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit_both(tfull_own + static_cast<uint32_t>(acc * 8));
+        __syncwarp();
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+      if (!ok && any_mma) {
+        // the MMAs in flight finish before TMEM is released
+        if (elect_one()) umma_commit_pair(smem_u32(drain_bar));
+        __syncwarp();
+        const unsigned long long t0 = global_timer_ns();
+        while (!mbar_try_wait(drain_bar, 0) && global_timer_ns() - t0 < 10000000ull) {
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int ew = warp - 2;
+    const int quarter = warp & 3;  // the TMEM lanes this warp may read
+    const int side = ew >> 2;      // its 64 columns
+    const Staged slot{staging + ew * kSlot};
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool stores_pending = false;
+    const float most = KIND == kDw ? *p.rows.most : 0.f;
+    const bool last = KIND != kDw || p.acc == nullptr || p.first + p.block >= counted;
+
+    const auto staging_free = [&]() {
+      if (stores_pending && lane == 0) bulk_wait_read_all();
+      __syncwarp();
+    };
+    // The staged chunk by TMA; the staging tile may be written again after
+    // staging_free().
+    const auto store_tma = [&](long long row0, int col) {
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(&tmOut, slot.base, col, static_cast<int>(row0));
+        bulk_commit();
+      }
+      stores_pending = true;
+    };
+    // The staged chunk with plain stores, row r to output row `to` of lane r (-1:
+    // none); rows of 16-byte pieces, or an odd length value by value.
+    const auto store_rows = [&](int to, int col) {
+      __syncwarp();
+      if (p.vec) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + lane / 4, q = lane % 4;
+          const int row = __shfl_sync(0xffffffffu, to, r);
+          if (row >= 0 && col + q * 8 < p.N)
+            *reinterpret_cast<uint4*>(p.out + static_cast<long long>(row) * p.ld + col + q * 8) =
+                *slot.piece(r, q);
+        }
+      } else {
+        for (int r = 0; r < 32; ++r) {
+          const int row = __shfl_sync(0xffffffffu, to, r);
+          if (row >= 0 && col + lane < p.N)
+            p.out[static_cast<long long>(row) * p.ld + col + lane] = *slot.value(r, lane);
+        }
+      }
+      __syncwarp();
+    };
+
+    for (int u = first_unit; u < units; u += step) {
+      int mp, nt;
+      unit_tile(u, m_pairs, p.n_tiles, mp, nt);
+      const long long row0 = static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32;
+      const int side_col = nt * BN + side * 64;
+      const long long row = row0 + lane;
+      // E's rows behind the last are written up to a whole K step of dW
+      const long long rows_end = KIND == kLogits ? (n + BK - 1) / BK * BK : M;
+      const bool live = row0 < rows_end && side_col < p.N;  // the same for the whole warp
+      const bool on = row < M;
+      // what the row needs besides the accumulator, under the main loop
+      int token = -1;
+      float ref = 0.f;
+      float2 scale = make_float2(0.f, 0.f);
+      if (KIND != kDw && live && on) {
+        token = p.rows.token[p.first + row];
+        if (KIND == kLogits && p.store) ref = p.rows.ref[p.first + row];
+        if (KIND == kDx) scale = p.rows.scale[p.first + row];
+      }
+      int k = p.top, next = INT_MAX;  // the row's next entry from this warp's columns on
+      if (KIND == kLogits && live && on) {
+        const int* idx = p.rows.index + static_cast<long long>(token) * p.top;
+        int lo = 0, hi = p.top;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (idx[mid] < side_col)
+            lo = mid + 1;
+          else
+            hi = mid;
+        }
+        k = lo;
+        if (k < p.top) next = idx[k];
+      }
+      if (mma_units > 0) {
+        const bool got = mbar_wait_cluster(&tfull_bar[acc], acc_phase, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
+          record_timeout(p.status, abort_flag);
+          break;
+        }
+        tc_fence_after();
+      }
+      const uint32_t t_side = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                              static_cast<uint32_t>(acc) * kAcc + static_cast<uint32_t>(side * 64);
+      float sum = 0.f, top_z = -INFINITY;
+      if (KIND == kLogits && !p.store && live) {
+        // the reference is the largest of the 64 columns
+#pragma unroll 1
+        for (int c = 0; c < 64 && side_col + c < p.N; c += 16) {
+          uint32_t r[16];
+          tmem_load_16(t_side + c, r);
+          const int in = p.N - side_col - c;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j < in) top_z = fmaxf(top_z, __uint_as_float(r[j]));
+        }
+        ref = top_z == -INFINITY ? 0.f : top_z * p.unit;
+      }
+#pragma unroll 1
+      for (int c = 0; c < 64 && live; c += kChunk) {
+        const int col = side_col + c;
+        if (col >= p.N) break;
+        if (stores_pending) staging_free();
+        float* acc_row = nullptr;
+        if (KIND == kDw && p.acc != nullptr)
+          acc_row = p.acc + row * p.N + col;
+#pragma unroll 1
+        for (int part = 0; part < kChunk / 16; ++part) {
+          float v[16];
+          if (mma_units > 0) {
+            uint32_t r[16];
+            tmem_load_16(t_side + c + part * 16, r);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0.f;
+          }
+          const int in = p.N - col - part * 16;
+          if (KIND == kLogits) {
+            exp_part(v, p.unit, ref, in, sum, top_z);
+            if (!on) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = 0.f;
+            }
+          } else if (KIND == kDx) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = v[j] * scale.x * scale.y;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] *= most;
+            if (acc_row != nullptr && on) {
+              float* at = acc_row + part * 16;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (j < in) {
+                  if (p.first > 0) v[j] += at[j];
+                  if (!last) at[j] = v[j];
+                }
+            }
+          }
+          if (KIND != kLogits || p.store) stage_part(slot, lane, part, v);
+        }
+        if (KIND == kLogits) {
+          if (p.store) store_tma(row0, col);
+        } else if (KIND == kDx) {
+          store_rows(token, col);
+        } else if (last) {
+          if (p.vec)
+            store_tma(row0, col);
+          else
+            store_rows(on ? static_cast<int>(row) : -1, col);
+        } else {
+          __syncwarp();
+        }
+      }
+      if (KIND == kLogits && live) {
+        if (on)
+          p.part[(static_cast<long long>(nt) * kSides + side) * p.ldp + row] =
+              make_float2(top_z, sum);
+        const int end = min(side_col + 64, p.N);
+        while (true) {  // a column that is an entry of some row, all rows that have it
+          const unsigned some = __ballot_sync(0xffffffffu, next < end);
+          if (some == 0) break;
+          const int col = __shfl_sync(0xffffffffu, next, __ffs(some) - 1);
+          const float z = tmem_load_1(t_side + static_cast<uint32_t>(col - side_col));
+          if (next == col) {
+            const long long at = static_cast<long long>(token) * p.top + k;
+            p.rows.z[at] = z;
+            next = ++k < p.top ? p.rows.index[at + 1] : INT_MAX;
+          }
+        }
+      }
+      if (mma_units > 0) {
+        tc_fence_before();
+        __syncwarp();
+        // the accumulator is free again once both CTAs' epilogue warps have read it
+        if (lane == 0) mbar_arrive_remote(tempty0 + static_cast<uint32_t>(acc * 8));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+    }
+    if (lane == 0 && stores_pending) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still signal or read it
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * kAcc);
+  }
+}
+
+template <int KIND>
+cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
+                   const PairArgs& p, long long most_units, const char* tag,
+                   cudaStream_t stream) {
+  auto* kernel = loss_pair_kernel<KIND>;
+  static bool ready[64] = {false};
+  static int max_clusters[64] = {0};
+  static std::mutex mu;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  int cmax;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+      cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      if (e != cudaSuccess) return e;
+      cfg.gridDim = dim3(2 * sm_count());
+      cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorLaunchOutOfResources;
+      max_clusters[dev] = n;
+      ready[dev] = true;
+    }
+    cmax = max_clusters[dev];
+  }
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(most_units, cmax)));
+  cfg.numAttrs = 2;
+  prof_begin(tag, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmOut, p);
+  prof_end(tag, stream);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+PairArgs common(const LossProducts& g) {
+  PairArgs p = {};
+  p.V = g.V;
+  p.top = g.top;
+  p.first = g.first;
+  p.block = g.block;
+  p.unit = g.unit;
+  p.rows = g.rows;
+  p.status = device_status_ptr();
+  return p;
+}
+
+long long pairs(long long rows) { return (rows + 2 * BM - 1) / (2 * BM); }
+
+}  // namespace
+
+int loss_parts(int V) { return (V + 63) / 64; }
+
+cudaError_t loss_logits(const LossProducts& g, bool only_again, cudaStream_t s) {
+  PairArgs p = common(g);
+  CUtensorMap tmA, tmB, tmE;
+  if (!make_map(&tmA, g.x, g.x_rows, g.d, g.ldx, 2, 64, BM) ||
+      !make_map(&tmB, g.W, g.V, g.d, g.ldw, 2, 64, BN / 2))
+    return cudaErrorInvalidValue;
+  tmE = tmA;  // a stand-in: not used
+  p.store = g.E != nullptr;
+  if (p.store && !make_map(&tmE, g.E, g.block, g.V, g.lde, 2, kChunk, 32, 64))
+    return cudaErrorInvalidValue;
+  p.n_tiles = (g.V + BN - 1) / BN;
+  p.N = g.V;
+  p.K = g.d;
+  p.part = g.part;
+  p.ldp = g.ldp;
+  if (only_again) p.only = g.rows.again + g.first / g.block;
+  return launch<kLogits>(tmA, tmB, tmE, p, pairs(g.block) * p.n_tiles,
+                         only_again ? "loss_logits_again" : "loss_logits", s);
+}
+
+cudaError_t loss_dx(const LossProducts& g, cudaStream_t s) {
+  PairArgs p = common(g);
+  CUtensorMap tmA, tmB;
+  if (!make_map(&tmA, g.E, g.block, g.V, g.lde, 2, 64, BM) ||
+      !make_map(&tmB, g.W, g.V, g.d, g.ldw, 2, 64, 64))
+    return cudaErrorInvalidValue;
+  p.n_tiles = (g.d + BN - 1) / BN;
+  p.N = g.d;
+  p.K = g.V;
+  p.out = static_cast<bf16*>(g.dx);
+  p.ld = g.d;
+  p.vec = g.d % 8 == 0;
+  return launch<kDx>(tmA, tmB, tmA, p, pairs(g.block) * p.n_tiles, "loss_dx", s);
+}
+
+cudaError_t loss_dw(const LossProducts& g, cudaStream_t s) {
+  PairArgs p = common(g);
+  CUtensorMap tmA, tmB, tmOut;
+  if (!make_map(&tmA, g.E, g.block, g.V, g.lde, 2, 64, 64) ||
+      !make_map(&tmB, g.x, g.x_rows, g.d, g.ldx, 2, 64, 64))
+    return cudaErrorInvalidValue;
+  tmOut = tmA;
+  p.vec = g.d % 8 == 0;
+  if (p.vec && !make_map(&tmOut, g.dW, g.V, g.d, g.d, 2, kChunk, 32, 64))
+    return cudaErrorInvalidValue;
+  p.n_tiles = (g.d + BN - 1) / BN;
+  p.N = g.d;
+  p.M = g.V;
+  p.out = static_cast<bf16*>(g.dW);
+  p.acc = g.acc;
+  p.ld = g.d;
+  return launch<kDw>(tmA, tmB, tmOut, p, pairs(g.V) * p.n_tiles, "loss_dw", s);
+}
+
+}  // namespace poetx
