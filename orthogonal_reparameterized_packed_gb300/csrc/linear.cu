@@ -251,11 +251,11 @@ size_t fp32_scratch(long long M, int N, int K, bool b_mn, bool fewer) {
   return linear_split_pays(M, N, K) ? linear_split_scratch(g) : 0;
 }
 
-cudaError_t run_fp32(const LinearProduct& g, void* scratch, cudaStream_t s) {
+}  // namespace
+
+cudaError_t linear_fp32(const LinearProduct& g, void* scratch, cudaStream_t s) {
   return linear_split_pays(g.M, g.N, g.K) ? linear_split(g, scratch, s) : linear_simt(g, s);
 }
-
-}  // namespace
 
 // bf16: padded copies of x and W where d_in is no multiple of 8; fp32: the
 // planes of x and W where the product runs on the tensor cores.
@@ -289,7 +289,7 @@ cudaError_t linear_forward(const void* x, const void* W, const float* bias, cons
   g.N = d_out;
   g.K = d_in;
   g.act = act;
-  return is_bf16 ? run_product(g, s) : run_fp32(g, scratch, s);
+  return is_bf16 ? run_product(g, s) : linear_fp32(g, scratch, s);
 }
 
 // Scratch of the backward: dz (unless it is dy itself, aligned), the row
@@ -367,7 +367,7 @@ cudaError_t linear_backward(const void* dy, const void* z, const void* W, void* 
   g.N = d_in;
   g.K = d_out;
   g.tag = "linear_dgrad";
-  e = is_bf16 ? run_product(g, s) : run_fp32(g, wp, s);
+  e = is_bf16 ? run_product(g, s) : linear_fp32(g, wp, s);
   return e != cudaSuccess ? e : sum_dbias();
 }
 

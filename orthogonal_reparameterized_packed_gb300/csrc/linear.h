@@ -45,4 +45,8 @@ size_t linear_split_scratch(const LinearProduct& g);
 size_t linear_split_scratch_up_to(const LinearProduct& g);  // of any product of at most g.M rows
 cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s);
 
+// In fp32 in the form that takes less time, with linear_split_scratch_up_to(g) bytes
+// of scratch or more (linear.cu).
+cudaError_t linear_fp32(const LinearProduct& g, void* scratch, cudaStream_t s);
+
 }  // namespace poetx

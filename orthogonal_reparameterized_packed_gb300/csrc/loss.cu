@@ -16,6 +16,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "linear.h"
 #include "loss.h"
 #include "poetx.h"
 #include "ptx.cuh"
@@ -395,8 +396,11 @@ __global__ void __launch_bounds__(kThreads)
   if (!grad) return;
   const float scale = (weights != nullptr ? weights[t] : 1.f / static_cast<float>(n)) * tau;
   __syncthreads();
-  for (int v = threadIdx.x; v < V; v += kThreads)
-    row[v] = scale * (expf((row[v] - m) * inv_tau) / s);
+  for (int v = threadIdx.x; v < V; v += kThreads) {
+    const float dz = scale * (expf((row[v] - m) * inv_tau) / s);
+    // below 2^-109 the products on the tensor cores do not take a value: 0
+    row[v] = fabsf(dz) < 1.5407439555e-33f ? 0.f : dz;
+  }
   __syncthreads();
   if (threadIdx.x == 0)
     for (int k = 0; k < top; ++k) {
@@ -427,76 +431,36 @@ __global__ void __launch_bounds__(kOrderThreads)
   }
 }
 
-// out[m][n] = sum_k A(m, k) B(k, n) in fp32, element strides; accumulated onto
-// out32 and / or rounded into out (row m at rows[m], only the first *limit).
-struct Product {
-  const void* A;
-  const void* B;
-  long long am, ak, bk, bn;
-  long long M;
-  int N;
-  long long K;
-  float* out32;
-  bool add;
-  void* out;
-  const int* rows;
-  const int* limit;
-  long long first;
-};
-
-template <typename TA, typename TB, typename TO>
-__global__ void __launch_bounds__(256) loss_product_kernel(const Product p) {
+// out[c][r] = in[r][c], in [rows][cols].
+__global__ void __launch_bounds__(kThreads)
+    loss_transpose_kernel(const float* __restrict__ in, float* __restrict__ out, int rows,
+                          int cols) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float as[16][65], bs[16][65];
-  const TA* A = static_cast<const TA*>(p.A);
-  const TB* B = static_cast<const TB*>(p.B);
-  const long long m0 = blockIdx.y * 64ll, n0 = blockIdx.x * 64ll;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (long long k0 = 0; k0 < p.K; k0 += 16) {
-    for (int e = threadIdx.x; e < 1024; e += 256) {
-      const int k = p.ak == 1 ? e % 16 : e / 64, m = p.ak == 1 ? e / 16 : e % 64;
-      as[k][m] = m0 + m < p.M && k0 + k < p.K ? to_f(A[(m0 + m) * p.am + (k0 + k) * p.ak]) : 0.f;
-      const int kb = p.bk == 1 ? e % 16 : e / 64, n = p.bk == 1 ? e / 16 : e % 64;
-      bs[kb][n] =
-          n0 + n < p.N && k0 + kb < p.K ? to_f(B[(n0 + n) * p.bn + (k0 + kb) * p.bk]) : 0.f;
-    }
-    __syncthreads();
+  __shared__ float tile[32][33];
+  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+  const int r0 = blockIdx.x * 32, c0 = blockIdx.y * 32;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      float a[4], b[4];
+  for (int i = ty; i < 32; i += kThreads / 32)
+    if (r0 + i < rows && c0 + tx < cols)
+      tile[i][tx] = in[static_cast<long long>(r0 + i) * cols + c0 + tx];
+  __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = as[k][ty * 4 + i], b[i] = bs[k][tx * 4 + i];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const long long m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m >= p.M || n >= p.N || (p.limit != nullptr && p.first + m >= *p.limit)) continue;
-      float v = acc[i][j];
-      if (p.add) v += p.out32[m * p.N + n];
-      if (p.out32 != nullptr) p.out32[m * p.N + n] = v;
-      if (p.out != nullptr) {
-        const long long row = p.rows != nullptr ? p.rows[p.first + m] : m;
-        from_f(static_cast<TO*>(p.out)[row * p.N + n], v);
-      }
-    }
+  for (int i = ty; i < 32; i += kThreads / 32)
+    if (c0 + i < cols && r0 + tx < rows)
+      out[static_cast<long long>(c0 + i) * rows + r0 + tx] = tile[tx][i];
 }
 
-template <typename TA, typename TB, typename TO>
-cudaError_t product(const Product& p, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.N + 63) / 64), static_cast<unsigned>((p.M + 63) / 64));
-  prof_begin("loss_product", s);
-  const cudaError_t e =
-      launch_pdl(loss_product_kernel<TA, TB, TO>, grid, dim3(256), 0, s, p);
-  prof_end("loss_product", s);
-  return e != cudaSuccess ? e : cudaGetLastError();
+// dx of the block's rows to their tokens, a warp per row.
+__global__ void __launch_bounds__(kThreads)
+    loss_scatter_kernel(const float* __restrict__ rows, LossRows l, long long first,
+                        long long block, int d, float* __restrict__ dx) {
+  pdl_wait();
+  pdl_trigger();
+  const long long r = blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
+  if (r >= block || first + r >= *l.count) return;
+  const long long t = l.token[first + r];
+  for (int c = threadIdx.x % 32; c < d; c += 32) dx[t * d + c] = rows[r * d + c];
 }
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -513,13 +477,13 @@ struct Plan {
   int blocks;
   long long ldx, lde, ldp;
   size_t meta = 0, again, pos, token, index, p, ent, lead, z, ref, scale, xg, wp, terms, part, acc,
-         total;
+         turned, scratch, total;
   Plan(const LossArgs& a, bool want_dx, bool want_dw) {
     const size_t T = static_cast<size_t>(a.T), es = a.is_bf16 ? 2 : 4;
     const bool grad = want_dx || want_dw;
     lde = a.is_bf16 ? round64(a.V) : a.V;
     ldx = pitch_of(a.d, a.is_bf16);
-    block = a.block > 0 ? a.block : static_cast<long long>(kBlockBytes / es / lde / 64 * 64);
+    block = a.block > 0 ? a.block : static_cast<long long>(kBlockBytes / es / static_cast<size_t>(lde) / 64 * 64);
     block = std::max(64ll, std::min(round64(block), round64(a.T)));
     blocks = static_cast<int>((a.T + block - 1) / block);
     ldp = block;
@@ -544,7 +508,25 @@ struct Plan {
     terms = take(!a.is_bf16 || grad ? es * static_cast<size_t>(block) * lde : 0);
     part = take(a.is_bf16 ? sizeof(float2) * static_cast<size_t>(loss_parts(a.V)) * ldp : 0);
     acc = take(want_dw && a.is_bf16 && blocks > 1 ? 4 * static_cast<size_t>(a.V) * a.d : 0);
+    turned = take(want_dw && !a.is_bf16 ? 4 * static_cast<size_t>(block) * a.V : 0);
+    scratch = take(a.is_bf16 ? 0 : fp32_scratch(a, want_dx, want_dw));
     total = at;
+  }
+
+  // The largest of the products' scratch, for blocks of any number of rows.
+  size_t fp32_scratch(const LossArgs& a, bool want_dx, bool want_dw) const {
+    LinearProduct g;
+    g.M = block, g.N = a.V, g.K = a.d;
+    size_t most = linear_split_scratch_up_to(g);
+    if (want_dx) {
+      g.N = a.d, g.K = a.V, g.b_mn = true;
+      most = std::max(most, linear_split_scratch_up_to(g));
+    }
+    if (want_dw) {  // K is the number of rows
+      g.M = a.V, g.N = a.d, g.K = static_cast<int>(block), g.b_mn = true;
+      most = std::max(most, linear_split_scratch(g));
+    }
+    return most;
   }
 };
 
@@ -639,41 +621,65 @@ cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, cha
   return cudaSuccess;
 }
 
+// fp32: the products of linear_fp32 on a block's logits, which become dz in place,
+// and on their transpose for dW.  Rows that do not count are 0.
 cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char* ws,
                     cudaStream_t s) {
   float* xg = reinterpret_cast<float*>(ws + plan.xg);
   float* z = reinterpret_cast<float*>(ws + plan.terms);
+  float* zt = reinterpret_cast<float*>(ws + plan.turned);
+  void* scratch = ws + plan.scratch;
   const bool grad = a.dx != nullptr || a.dW != nullptr;
   cudaError_t e;
   for (long long first = 0; first < a.T; first += plan.block) {
     const long long rows = std::min(plan.block, a.T - first);
-    const float* xb = xg + first * a.d;
-    Product p = {};
-    p.A = xb, p.am = a.d, p.ak = 1;
-    p.B = a.W, p.bk = 1, p.bn = a.d;
-    p.M = rows, p.N = a.V, p.K = a.d;
-    p.out32 = z;
-    if ((e = product<float, float, float>(p, s)) != cudaSuccess) return e;
+    float* xb = xg + first * a.d;
+    LinearProduct g;
+    g.A = xb;
+    g.B = a.W;
+    g.y = z;
+    g.M = rows, g.N = a.V, g.K = a.d;
+    g.tag = "loss_logits";
+    if ((e = linear_fp32(g, scratch, s)) != cudaSuccess) return e;
     e = launched("loss_rows", s, [&] {
       return launch_pdl(loss_rows_kernel, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, s,
                         z, l, first, a.V, a.top, 1.f / a.tau, a.tau, a.weights, grad, a.loss);
     });
     if (e != cudaSuccess) return e;
-    if (a.dx != nullptr) {
-      Product q = {};
-      q.A = z, q.am = a.V, q.ak = 1;
-      q.B = a.W, q.bk = a.d, q.bn = 1;
-      q.M = rows, q.N = a.d, q.K = a.V;
-      q.out = a.dx, q.rows = l.token, q.limit = l.count, q.first = first;
-      if ((e = product<float, float, float>(q, s)) != cudaSuccess) return e;
-    }
     if (a.dW != nullptr) {
-      Product q = {};
-      q.A = z, q.am = 1, q.ak = a.V;
-      q.B = xb, q.bk = a.d, q.bn = 1;
-      q.M = a.V, q.N = a.d, q.K = rows;
-      q.out32 = static_cast<float*>(a.dW), q.add = first > 0;
-      if ((e = product<float, float, float>(q, s)) != cudaSuccess) return e;
+      e = launched("loss_transpose", s, [&] {
+        return launch_pdl(loss_transpose_kernel,
+                          dim3(static_cast<unsigned>((rows + 31) / 32),
+                               static_cast<unsigned>((a.V + 31) / 32)),
+                          dim3(kThreads), 0, s, static_cast<const float*>(z), zt,
+                          static_cast<int>(rows), a.V);
+      });
+      if (e != cudaSuccess) return e;
+      LinearProduct q;
+      q.A = zt;
+      q.B = xb;
+      q.b_mn = true;
+      q.residual = first > 0 ? a.dW : nullptr;
+      q.y = a.dW;
+      q.M = a.V, q.N = a.d, q.K = static_cast<int>(rows);
+      q.tag = "loss_dw";
+      if ((e = linear_fp32(q, scratch, s)) != cudaSuccess) return e;
+    }
+    if (a.dx != nullptr) {  // over the block's rows of x, which are not needed any more
+      LinearProduct q;
+      q.A = z;
+      q.B = a.W;
+      q.b_mn = true;
+      q.y = xb;
+      q.M = rows, q.N = a.d, q.K = a.V;
+      q.tag = "loss_dx";
+      if ((e = linear_fp32(q, scratch, s)) != cudaSuccess) return e;
+      e = launched("loss_scatter", s, [&] {
+        return launch_pdl(loss_scatter_kernel, dim3(warps_grid(rows)), dim3(kThreads), 0, s,
+                          static_cast<const float*>(xb), l, first, rows, a.d,
+                          static_cast<float*>(a.dx));
+      });
+      if (e != cudaSuccess) return e;
     }
   }
   return cudaSuccess;
