@@ -477,7 +477,7 @@ struct Plan {
   int blocks;
   long long ldx, lde, ldp;
   size_t meta = 0, again, pos, token, index, p, ent, lead, z, ref, scale, xg, wp, terms, part, acc,
-         turned, scratch, total;
+         cut, turned, scratch, total;
   Plan(const LossArgs& a, bool want_dx, bool want_dw) {
     const size_t T = static_cast<size_t>(a.T), es = a.is_bf16 ? 2 : 4;
     const bool grad = want_dx || want_dw;
@@ -508,6 +508,9 @@ struct Plan {
     terms = take(!a.is_bf16 || grad ? es * static_cast<size_t>(block) * lde : 0);
     part = take(a.is_bf16 ? sizeof(float2) * static_cast<size_t>(loss_parts(a.V)) * ldp : 0);
     acc = take(want_dw && a.is_bf16 && blocks > 1 ? 4 * static_cast<size_t>(a.V) * a.d : 0);
+    cut = take(a.is_bf16 && ((want_dx && loss_cuts(a.V)) || (want_dw && loss_cuts(block)))
+                   ? loss_cut_bytes()
+                   : 0);
     turned = take(want_dw && !a.is_bf16 ? 4 * static_cast<size_t>(block) * a.V : 0);
     scratch = take(a.is_bf16 ? 0 : fp32_scratch(a, want_dx, want_dw));
     total = at;
@@ -584,6 +587,7 @@ cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, cha
   g.dx = a.dx;
   g.dW = a.dW;
   g.acc = plan.blocks > 1 ? reinterpret_cast<float*>(ws + plan.acc) : nullptr;
+  g.parts = reinterpret_cast<float*>(ws + plan.cut);
   g.rows = l;
   FinishArgs f = {};
   f.rows = l;

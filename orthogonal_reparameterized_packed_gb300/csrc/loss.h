@@ -71,10 +71,13 @@ struct LossProducts {
   void* dx;       // [T][d]
   void* dW;       // [V][d]
   float* acc;     // [V][d] fp32, or null: there is one block
+  float* parts;   // loss_cut_bytes, needed where loss_cuts(V) for dx, loss_cuts(block) for dw
   LossRows rows;
 };
 
 int loss_parts(int V);
+bool loss_cuts(long long K);
+size_t loss_cut_bytes();
 // only_again: does nothing unless the block's flag is set
 cudaError_t loss_logits(const LossProducts& g, bool only_again, cudaStream_t s);
 cudaError_t loss_dx(const LossProducts& g, cudaStream_t s);

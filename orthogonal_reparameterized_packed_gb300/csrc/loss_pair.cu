@@ -45,6 +45,10 @@ constexpr int kSlot = 32 * kChunk * 2;
 constexpr int kSmem = kRing + kEpiWarps * kSlot + 256;
 constexpr int kGroupM = 8;
 constexpr uint32_t kAcc = 256;  // TMEM columns of an accumulator
+constexpr int kLeastShare = 8;   // K steps of a slice
+constexpr int kMaxSlices = 16;
+constexpr int kSlots = 4;        // slices' tiles per cluster at most
+constexpr float kCutCost = 20.f;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
 struct PairArgs {
@@ -58,8 +62,62 @@ struct PairArgs {
   float2* part;
   bf16* out;             // dx or dW
   float* acc;
+  float* parts;          // of tiles cut along K; null: none is
   LossRows rows;
   int* status;
+};
+
+// The order of the work.  Whole rounds of tiles over the clusters come first; the
+// tiles of the last round (`rest`) are cut into `slices` of their K steps, all of one
+// slice before the next, so that what runs at one time still shares its operands
+// through L2 (parts of equal length at any K took 187 us where uncut tiles took 145:
+// 1638 rows, d = 2048, V = 32000).  A slice's tile is kept in fp32, [256][256], and
+// added up by loss_sum_kernel.
+struct Schedule {
+  int whole, rest = 0, slices = 1, share, k_steps, clusters;
+
+  // In units of a K step (0.28 us): the rounds of the rest and, when it is cut, 0.4
+  // for a slice's tile written and read and kCutCost for the launch.
+  __device__ Schedule(int tiles, int steps, int clusters_, bool may_cut)
+      : whole(tiles), share(steps), k_steps(steps), clusters(clusters_) {
+    const int left = tiles % clusters;
+    if (!may_cut || left == 0) return;
+    float best = static_cast<float>(steps);
+    for (int n = 2; n <= kMaxSlices && n * left <= kSlots * clusters; ++n) {
+      const int len = (steps + n - 1) / n;
+      if (len < kLeastShare) break;
+      const float cost = static_cast<float>((n * left + clusters - 1) / clusters * len) +
+                         0.4f * static_cast<float>(n * left) + kCutCost;
+      if (cost < best && len * (n - 1) < steps) {
+        best = cost;
+        slices = n;
+        share = len;
+      }
+    }
+    if (slices > 1) {
+      whole = tiles - left;
+      rest = left;
+    }
+  }
+  // Item i of cluster c: its tile, its K steps and where a slice goes (-1: whole).
+  __device__ __forceinline__ bool item(int i, int c, int& tile, int& k0, int& k1,
+                                       int& slot) const {
+    const long long u = static_cast<long long>(i) * clusters + c;
+    slot = -1;
+    k0 = 0;
+    k1 = k_steps;
+    if (u < whole) {
+      tile = static_cast<int>(u);
+      return true;
+    }
+    if (u - whole >= static_cast<long long>(rest) * slices) return false;
+    slot = static_cast<int>(u - whole);
+    const int slice = slot / rest;
+    tile = whole + slot - slice * rest;
+    k0 = slice * share;
+    k1 = min(k_steps, k0 + share);
+    return true;
+  }
 };
 
 __device__ __forceinline__ void unit_tile(int u, int m_pairs, int n_tiles, int& mp, int& nt) {
@@ -201,7 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int units = m_pairs * p.n_tiles;
   if (p.only != nullptr && *p.only == 0) units = 0;
   if (KIND == kDw && n == 0 && p.first > 0) units = 0;  // the block before was the last
-  const int mma_units = k_steps > 0 ? units : 0;  // dW without a row is 0
+  const bool products = k_steps > 0;  // dW without a row is 0
+  const Schedule todo(units, k_steps, step, KIND != kLogits && p.parts != nullptr);
 
   const uint32_t full0 = map_peer(smem_u32(full_bar), 0);
   const uint32_t tempty0 = map_peer(smem_u32(tempty_bar), 0);
@@ -212,12 +271,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     long long issued = 0;
     bool ok = true;
-    for (int u = first_unit; u < mma_units && ok; u += step) {
+    int tile, ks0, ks1, part_slot;
+    for (int i = 0; products && ok && todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
       int mp, nt;
-      unit_tile(u, m_pairs, p.n_tiles, mp, nt);
+      unit_tile(tile, m_pairs, p.n_tiles, mp, nt);
       const int a_row = mp * 2 * BM + static_cast<int>(rank) * BM;
       const int b_n = nt * BN + static_cast<int>(rank) * (BN / 2);
-      for (int ks = 0; ks < k_steps; ++ks) {
+      for (int ks = ks0; ks < ks1; ++ks) {
         if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) {
           record_timeout(p.status, abort_flag);
           ok = false;
@@ -275,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t acc_phase = 0;
       bool ok = true;
       bool any_mma = false;
-      for (int u = first_unit; u < mma_units && ok; u += step) {
+      int tile, ks0, ks1, part_slot;
+      for (int i = 0; products && ok && todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
         if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1, abort_flag)) {
           record_timeout(p.status, abort_flag);
           ok = false;
@@ -283,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc) * kAcc;
-        for (int ks = 0; ks < k_steps; ++ks) {
+        for (int ks = ks0; ks < ks1; ++ks) {
           if (!mbar_wait(&full_bar[stage], phase, abort_flag)) {
             record_timeout(p.status, abort_flag);
             ok = false;
@@ -299,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < BK / 16; ++j)
               umma_bf16_pair(d_tmem, adesc0 + j * (A_MN ? 128 : 2), bdesc0 + j * (B_MN ? 128 : 2),
-                             IDESC, (ks > 0 || j > 0) ? 1u : 0u);
+                             IDESC, (ks > ks0 || j > 0) ? 1u : 0u);
             // the slot is free in both CTAs once the MMAs have read it
             umma_commit_both(empty_own + static_cast<uint32_t>(stage * 8));
           }
@@ -375,9 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
 
-    for (int u = first_unit; u < units; u += step) {
+    int tile, ks0, ks1, part_slot;
+    for (int i = 0; todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
       int mp, nt;
-      unit_tile(u, m_pairs, p.n_tiles, mp, nt);
+      unit_tile(tile, m_pairs, p.n_tiles, mp, nt);
       const long long row0 = static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32;
       const int side_col = nt * BN + side * 64;
       const long long row = row0 + lane;
@@ -408,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         k = lo;
         if (k < p.top) next = idx[k];
       }
-      if (mma_units > 0) {
+      if (products) {
         const bool got = mbar_wait_cluster(&tfull_bar[acc], acc_phase, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
           record_timeout(p.status, abort_flag);
@@ -432,8 +494,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ref = top_z == -INFINITY ? 0.f : top_z * p.unit;
       }
+      if (KIND != kLogits && part_slot >= 0 && live) {
+        float* to = p.parts + static_cast<long long>(part_slot) * 2 * BM * BN +
+                    (rank * BM + quarter * 32 + lane) * BN + side * 64;
 #pragma unroll 1
-      for (int c = 0; c < 64 && live; c += kChunk) {
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t r[16];
+          tmem_load_16(t_side + c, r);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<uint4*>(to + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; c < 64 && live && part_slot < 0; c += kChunk) {
         const int col = side_col + c;
         if (col >= p.N) break;
         if (stores_pending) staging_free();
@@ -443,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int part = 0; part < kChunk / 16; ++part) {
           float v[16];
-          if (mma_units > 0) {
+          if (products) {
             uint32_t r[16];
             tmem_load_16(t_side + c + part * 16, r);
 #pragma unroll
@@ -507,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (mma_units > 0) {
+      if (products) {
         tc_fence_before();
         __syncwarp();
         // the accumulator is free again once both CTAs' epilogue warps have read it
@@ -526,6 +600,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 2 * kAcc);
+  }
+}
+
+// The tiles that were cut along K: their slices added up in order, then
+// what the epilogue does.  A CTA takes four rows of a tile, a thread four
+// columns.
+constexpr int kSumRows = 4;
+constexpr int kSumThreads = 256;
+
+template <int KIND>
+__global__ void __launch_bounds__(kSumThreads) loss_sum_kernel(const PairArgs p, int clusters) {
+  pdl_wait();
+  pdl_trigger();
+  const long long counted = *p.rows.count;
+  const long long n = max(0ll, min(p.block, counted - p.first));
+  const long long M = KIND == kDw ? p.M : n;
+  const int m_pairs = static_cast<int>((M + 2 * BM - 1) / (2 * BM));
+  const int k_steps = static_cast<int>(((KIND == kDw ? n : p.K) + BK - 1) / BK);
+  const Schedule todo(m_pairs * p.n_tiles, k_steps, clusters, true);
+  constexpr int kPieces = 2 * BM / kSumRows;
+  const int j = static_cast<int>(blockIdx.x) / kPieces, piece = blockIdx.x % kPieces;
+  if (j >= todo.rest) return;
+  int mp, nt;
+  unit_tile(todo.whole + j, m_pairs, p.n_tiles, mp, nt);
+  const bool last = KIND != kDw || p.acc == nullptr || p.first + p.block >= counted;
+  const int col = threadIdx.x % 64 * 4, to_col = nt * BN + col;
+  if (to_col >= p.N) return;
+  const int in = min(4, p.N - to_col);
+  const int r = piece * kSumRows + threadIdx.x / 64;
+  const long long row = static_cast<long long>(mp) * 2 * BM + r;
+  if (row >= M) return;
+  const float* part = p.parts + static_cast<long long>(j) * 2 * BM * BN + r * BN + col;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int i = 0; i < todo.slices; ++i) {
+    const float4 q =
+        *reinterpret_cast<const float4*>(part + static_cast<long long>(i) * todo.rest * 2 * BM * BN);
+    v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
+  }
+  long long to = row;
+  if (KIND == kDx) {
+    to = p.rows.token[p.first + row];
+    const float2 scale = p.rows.scale[p.first + row];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = v[i] * scale.x * scale.y;
+  } else {
+    const float most = *p.rows.most;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] *= most;
+      if (p.acc == nullptr || i >= in) continue;
+      float* sum = p.acc + row * p.N + to_col + i;
+      if (p.first > 0) v[i] += *sum;
+      if (!last) *sum = v[i];
+    }
+  }
+  if (!last) return;
+  bf16* out = p.out + to * p.ld + to_col;
+  if (p.vec) {
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_bf16x2(__float_as_uint(v[0]), __float_as_uint(v[1])),
+                   pack_bf16x2(__float_as_uint(v[2]), __float_as_uint(v[3])));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < in) out[i] = __float2bfloat16_rn(v[i]);
   }
 }
 
@@ -570,11 +710,21 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
     }
     cmax = max_clusters[dev];
   }
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(most_units, cmax)));
+  // tiles that may be cut keep every cluster busy
+  cfg.gridDim = dim3(
+      2 * static_cast<unsigned>(p.parts != nullptr ? cmax : std::min<long long>(most_units, cmax)));
   cfg.numAttrs = 2;
   prof_begin(tag, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmOut, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmOut, p);
   prof_end(tag, stream);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess || KIND == kLogits || p.parts == nullptr) return e;
+  const int clusters = static_cast<int>(cfg.gridDim.x / 2);
+  prof_begin("loss_sum", stream);
+  e = launch_pdl(loss_sum_kernel<KIND>,
+                 dim3(static_cast<unsigned>(clusters * (2 * BM / kSumRows))), dim3(kSumThreads), 0,
+                 stream, p, clusters);
+  prof_end("loss_sum", stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -593,6 +743,12 @@ PairArgs common(const LossProducts& g) {
 long long pairs(long long rows) { return (rows + 2 * BM - 1) / (2 * BM); }
 
 }  // namespace
+
+bool loss_cuts(long long K) { return (K + BK - 1) / BK > static_cast<long long>(kCutCost); }
+
+size_t loss_cut_bytes() {
+  return static_cast<size_t>(sm_count() / 2 + 1) * kSlots * 2 * BM * BN * sizeof(float);
+}
 
 int loss_parts(int V) { return (V + 63) / 64; }
 
@@ -625,6 +781,7 @@ cudaError_t loss_dx(const LossProducts& g, cudaStream_t s) {
   p.n_tiles = (g.d + BN - 1) / BN;
   p.N = g.d;
   p.K = g.V;
+  p.parts = loss_cuts(g.V) ? g.parts : nullptr;
   p.out = static_cast<bf16*>(g.dx);
   p.ld = g.d;
   p.vec = g.d % 8 == 0;
@@ -646,6 +803,7 @@ cudaError_t loss_dw(const LossProducts& g, cudaStream_t s) {
   p.M = g.V;
   p.out = static_cast<bf16*>(g.dW);
   p.acc = g.acc;
+  p.parts = loss_cuts(g.block) ? g.parts : nullptr;
   p.ld = g.d;
   return launch<kDw>(tmA, tmB, tmOut, p, pairs(g.V) * p.n_tiles, "loss_dw", s);
 }
