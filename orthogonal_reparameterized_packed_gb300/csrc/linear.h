@@ -9,6 +9,18 @@
 
 namespace poetx {
 
+// What linear_stream leaves instead of y and z for the head's losses (loss.h), 128
+// outputs (vocabulary entries) at a time: part[n / 128][token] = (their largest z,
+// the sum of 2^((z - largest) unit)), and the z at a token's `top` ascending indices.
+struct LossColumns {
+  float2* part = nullptr;
+  long long ldp = 0;
+  float unit = 0.f;
+  const int* index = nullptr;
+  float* z = nullptr;
+  int top = 0;
+};
+
 struct LinearProduct {
   const void* A = nullptr;
   const void* B = nullptr;
@@ -25,6 +37,7 @@ struct LinearProduct {
   // + segs) not 0 are computed
   const int* flags = nullptr;
   int segs = 0;
+  const LossColumns* loss = nullptr;  // linear_stream with B [N][K]
   const char* tag = "linear";
 };
 

@@ -54,6 +54,7 @@ struct StreamArgs {
   const bf16* residual;
   bf16* y;
   bf16* z;
+  LossColumns loss;
   int* status;
 };
 
@@ -93,10 +94,49 @@ __device__ __forceinline__ void store4(bf16* out, long long at, const float (&v)
   }
 }
 
+// The statistics of one token over the warp's 128 features, n .. n + 3 of this lane,
+// `live` of them inside.
+__device__ __forceinline__ void loss_columns(const LossColumns& p, const float (&v)[4], int n,
+                                             int live, long long token) {
+  const int lane = threadIdx.x % 32, n0 = n - 4 * lane;
+  float top = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < live) top = fmaxf(top, v[j]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top == -INFINITY ? 0.f : top * p.unit;
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < live) sum += exp2f(fmaf(v[j], p.unit, -ref));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) p.part[n0 / BM * p.ldp + token] = make_float2(top, sum);
+  // the token's entries among these features, the same for the whole warp
+  const int* index = p.index + token * p.top;
+  int lo = 0, hi = p.top;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (index[mid] < n0)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  for (; lo < p.top; ++lo) {
+    const int c = index[lo] - n0;
+    if (c >= BM) break;
+    if (c >> 2 == lane) {
+      const float z = (c & 2) ? ((c & 1) ? v[3] : v[2]) : ((c & 1) ? v[1] : v[0]);
+      p.z[token * p.top + lo] = z;
+    }
+  }
+}
+
 // Adds the slices' partial values of features n .. n + 3 for this CTA's tokens,
 // in rank order, and finishes them: one warp per token, U tokens at a time so
 // that U x SPLITS remote loads are in flight.
-template <int BT, int SPLITS, int U>
+template <int BT, int SPLITS, int U, bool LOSS>
 __device__ __forceinline__ void finish(const StreamArgs& p, const float* part, long long t0,
                                        int slice, int t_end, int n) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -120,11 +160,15 @@ __device__ __forceinline__ void finish(const StreamArgs& p, const float* part, l
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (t + u * kWarps >= t_end || live_n <= 0) continue;
+      if (t + u * kWarps >= t_end || (!LOSS && live_n <= 0)) continue;
       float v[4] = {q[u][0].x, q[u][0].y, q[u][0].z, q[u][0].w};
 #pragma unroll
       for (int r = 1; r < SPLITS; ++r)
         v[0] += q[u][r].x, v[1] += q[u][r].y, v[2] += q[u][r].z, v[3] += q[u][r].w;
+      if (LOSS) {
+        loss_columns(p.loss, v, n, live_n, t0 + t + u * kWarps);
+        continue;
+      }
       const long long o = (t0 + t + u * kWarps) * p.ld + n;
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] += b4[j];
@@ -148,7 +192,7 @@ __device__ __forceinline__ void finish(const StreamArgs& p, const float* part, l
 }
 
 // Grid: x = feature tile * splits + slice (a cluster along x), y = token tile.
-template <int BT, bool A_MN>
+template <int BT, bool A_MN, bool LOSS>
 __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
     linear_stream_kernel(const __grid_constant__ CUtensorMap tmW,
                          const __grid_constant__ CUtensorMap tmX, const StreamArgs p) {
@@ -290,10 +334,10 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
   // tokens [slice BT / splits, (slice + 1) BT / splits)
   const int t_end = min(live_t, (slice + 1) * (BT / p.splits));
   switch (p.splits) {
-    case 1: finish<BT, 1, 2>(p, part, t0, slice, t_end, n0 + 4 * lane); break;
-    case 2: finish<BT, 2, 2>(p, part, t0, slice, t_end, n0 + 4 * lane); break;
-    case 4: finish<BT, 4, 1>(p, part, t0, slice, t_end, n0 + 4 * lane); break;
-    default: finish<BT, 8, 1>(p, part, t0, slice, t_end, n0 + 4 * lane);
+    case 1: finish<BT, 1, 2, LOSS>(p, part, t0, slice, t_end, n0 + 4 * lane); break;
+    case 2: finish<BT, 2, 2, LOSS>(p, part, t0, slice, t_end, n0 + 4 * lane); break;
+    case 4: finish<BT, 4, 1, LOSS>(p, part, t0, slice, t_end, n0 + 4 * lane); break;
+    default: finish<BT, 8, 1, LOSS>(p, part, t0, slice, t_end, n0 + 4 * lane);
   }
   __syncthreads();
   if (p.splits > 1) cluster_sync();  // no CTA leaves while a peer still reads its tile
@@ -329,10 +373,10 @@ int split_count(long long tiles, int k_steps, int bt, const int (&most)[4]) {
   return s;
 }
 
-template <int BT, bool A_MN>
+template <int BT, bool A_MN, bool LOSS>
 cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
   using S = Shape<BT>;
-  auto* kernel = linear_stream_kernel<BT, A_MN>;
+  auto* kernel = linear_stream_kernel<BT, A_MN, LOSS>;
   static bool ready[64] = {false};
   static int most[64][4] = {};  // clusters of 1, 2, 4, 8 CTAs resident at one time
   static std::mutex mu;
@@ -382,6 +426,7 @@ cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
   p.residual = static_cast<const bf16*>(g.residual);
   p.y = static_cast<bf16*>(g.y);
   p.z = static_cast<bf16*>(g.z);
+  if (LOSS) p.loss = *g.loss;
   p.status = device_status_ptr();
   const int n_tiles = (g.N + BM - 1) / BM;
   const long long t_tiles = (g.M + BT - 1) / BT;
@@ -395,20 +440,21 @@ cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <bool A_MN>
+template <bool A_MN, bool LOSS>
 cudaError_t run(const LinearProduct& g, cudaStream_t s) {
-  if (g.M <= 16) return launch<16, A_MN>(g, s);
-  if (g.M <= 32) return launch<32, A_MN>(g, s);
-  if (g.M <= 64) return launch<64, A_MN>(g, s);
-  if (g.M <= 128) return launch<128, A_MN>(g, s);
-  return launch<256, A_MN>(g, s);
+  if (g.M <= 16) return launch<16, A_MN, LOSS>(g, s);
+  if (g.M <= 32) return launch<32, A_MN, LOSS>(g, s);
+  if (g.M <= 64) return launch<64, A_MN, LOSS>(g, s);
+  if (g.M <= 128) return launch<128, A_MN, LOSS>(g, s);
+  return launch<256, A_MN, LOSS>(g, s);
 }
 
 }  // namespace
 
 cudaError_t linear_stream(const LinearProduct& g, cudaStream_t s) {
   if (g.M <= 0 || g.N <= 0 || g.K <= 0) return cudaSuccess;
-  return g.b_mn ? run<true>(g, s) : run<false>(g, s);
+  if (g.loss != nullptr) return run<false, true>(g, s);
+  return g.b_mn ? run<true, false>(g, s) : run<false, false>(g, s);
 }
 
 }  // namespace poetx

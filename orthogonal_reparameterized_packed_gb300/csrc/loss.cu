@@ -72,8 +72,7 @@ constexpr int kEntryWarps = 4;
 constexpr int kMostEntries = 1024;
 
 // The entries of a token, a warp each: p = softmax of the teacher's logits at tau
-// over the entries that are there (for the cross entropy 1), sorted by their
-// indices.  Differences are divided by tau, not the logits: the type's lowest value
+// over the entries that are there, sorted by their indices.  Differences are divided by tau, not the logits: the type's lowest value
 // stays finite.
 __global__ void __launch_bounds__(32 * kEntryWarps)
     loss_entries_kernel(const void* indices, int index_bytes, const void* logits, bool logits_bf16,
@@ -97,9 +96,8 @@ __global__ void __launch_bounds__(32 * kEntryWarps)
     float v = 0.f;
     if (k < top) {
       const long long i = index_at(indices, index_bytes, base + k);
-      if (logits != nullptr)
-        v = logits_bf16 ? to_f(static_cast<const bf16*>(logits)[base + k])
-                        : static_cast<const float*>(logits)[base + k];
+      v = logits_bf16 ? to_f(static_cast<const bf16*>(logits)[base + k])
+                      : static_cast<const float*>(logits)[base + k];
       outside |= i >= V;
       const bool there = i >= 0 && i < V && !(v == -INFINITY);
       at = there ? static_cast<int>(i) : -1;
@@ -150,10 +148,12 @@ __global__ void __launch_bounds__(32 * kEntryWarps)
 }
 
 // pos[t] (0 or -1) -> the number of tokens before t that count, or -1; token its
-// inverse; the largest weight; the blocks' flags cleared.  One CTA, kOrderThreads
-// tokens at a time.
+// inverse; the largest weight; the blocks' flags and the counter of finished CTAs
+// cleared.  For the cross entropy also the entries: the targets.  One CTA,
+// kOrderThreads tokens at a time.
 __global__ void __launch_bounds__(kOrderThreads)
-    loss_order_kernel(LossRows l, long long T, const float* __restrict__ weights, int blocks) {
+    loss_order_kernel(LossRows l, long long T, const float* __restrict__ weights, int blocks,
+                      const void* targets, int index_bytes, int V, int* status) {
   __shared__ int sums[32];
   __shared__ float largest[32];
   pdl_wait();
@@ -161,20 +161,34 @@ __global__ void __launch_bounds__(kOrderThreads)
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   int before = 0;
   float most = 0.f;
+  bool outside = false;
   for (long long t0 = 0; t0 < T; t0 += kOrderThreads) {
     const long long t = t0 + threadIdx.x;
-    const bool on = t < T && l.pos[t] >= 0;
+    bool on = false;
+    if (t < T) {
+      if (targets != nullptr) {
+        const long long i = index_at(targets, index_bytes, t);
+        outside |= i >= V;
+        on = i >= 0 && i < V;
+        l.index[t] = l.lead[t] = on ? static_cast<int>(i) : -1;
+        l.p[t] = 1.f;
+        l.ent[t] = 0.f;
+      } else {
+        on = l.pos[t] >= 0;
+      }
+    }
     const unsigned mask = __ballot_sync(0xffffffffu, on);
     if (lane == 0) sums[warp] = __popc(mask);
     __syncthreads();
     int mine = before, all = 0;
+#pragma unroll
     for (int w = 0; w < 32; ++w) {
       if (w < warp) mine += sums[w];
       all += sums[w];
     }
     mine += __popc(mask & ((1u << lane) - 1));
+    if (t < T) l.pos[t] = on ? mine : -1;
     if (on) {
-      l.pos[t] = mine;
       l.token[mine] = static_cast<int>(t);
       if (weights != nullptr) most = fmaxf(most, fabsf(weights[t]));
     }
@@ -184,11 +198,13 @@ __global__ void __launch_bounds__(kOrderThreads)
   for (int b = threadIdx.x; b < blocks; b += kOrderThreads) l.again[b] = 0;
   most = warp_max(most);
   if (lane == 0) largest[warp] = most;
-  __syncthreads();
+  outside = __syncthreads_or(outside);
   if (threadIdx.x == 0) {
     for (int w = 0; w < 32; ++w) most = fmaxf(most, largest[w]);
     *l.count = before;
+    *l.done = 0;
     *l.most = weights == nullptr ? 1.f / static_cast<float>(max(1, before)) : most > 0.f ? most : 1.f;
+    if (outside) atomicCAS(status, 0, static_cast<int>(POETX_ERR_INVALID_ARG));
   }
 }
 
@@ -200,36 +216,52 @@ __global__ void __launch_bounds__(kOrderThreads)
 // not fit; its block is taken again with the largest logit as the reference.
 constexpr float kAbove = 28.f, kFits = 44.f;
 
+// V consecutive values.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T x[V];
+};
+
 // A warp per token: the tokens that count to their rows, zeros to dx and loss of
 // the others; warps from T on: zeros to the rows behind the last, to all of them or
 // up to a multiple of 64.  unit: log2(e) / tau where references are wanted, else 0.
-template <typename TX>
+// V values (16 bytes) at a time.
+template <typename TX, int V>
 __global__ void __launch_bounds__(kThreads)
     loss_gather_kernel(const TX* __restrict__ x, const TX* __restrict__ W, LossRows l, long long T,
-                       int d, long long ldw, TX* __restrict__ xg, long long ldx, bool zero_all,
-                       float unit, float* __restrict__ loss, TX* __restrict__ dx) {
+                       int d, TX* __restrict__ xg, long long ldx, bool zero_all, float unit,
+                       float* __restrict__ loss, TX* __restrict__ dx) {
+  using P = Pack<TX, V>;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % 32;
   const long long t = blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
-  TX zero;
-  from_f(zero, 0.f);
+  const auto at_row = [&](auto* base, long long row, long long ld, int c) {
+    return base + row * ld + c;
+  };
+  P zero;
+#pragma unroll
+  for (int j = 0; j < V; ++j) from_f(zero.x[j], 0.f);
   if (t >= T) {
     const long long r = t - T;
     const long long n = *l.count;
     if (r >= n && r < (zero_all ? T : (n + 63) / 64 * 64))
-      for (int c = lane; c < d; c += 32) xg[r * ldx + c] = zero;
+      for (int c = lane * V; c < d; c += 32 * V) *reinterpret_cast<P*>(at_row(xg, r, ldx, c)) = zero;
     return;
   }
   const int at = l.pos[t];
   if (at >= 0) {
-    const TX* lead = W + static_cast<long long>(l.lead[t]) * ldw;
-    TX* to = xg + at * ldx;
+    const long long lead = l.lead[t];
     float dot = 0.f;
-    for (int c = lane; c < d; c += 32) {
-      const TX v = x[t * d + c];
-      to[c] = v;
-      if (unit > 0.f) dot = fmaf(to_f(v), to_f(lead[c]), dot);
+#pragma unroll 4
+    for (int c = lane * V; c < d; c += 32 * V) {
+      const P v = *reinterpret_cast<const P*>(at_row(x, t, d, c));
+      *reinterpret_cast<P*>(at_row(xg, at, ldx, c)) = v;
+      if (unit > 0.f) {
+        const P w = *reinterpret_cast<const P*>(at_row(W, lead, d, c));
+#pragma unroll
+        for (int j = 0; j < V; ++j) dot = fmaf(to_f(v.x[j]), to_f(w.x[j]), dot);
+      }
     }
     if (unit > 0.f) {
       dot = warp_sum(dot);
@@ -239,7 +271,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (lane == 0) loss[t] = 0.f;
   if (dx != nullptr)
-    for (int c = lane; c < d; c += 32) dx[t * d + c] = zero;
+    for (int c = lane * V; c < d; c += 32 * V) *reinterpret_cast<P*>(at_row(dx, t, d, c)) = zero;
 }
 
 // What becomes of a block's statistics.
@@ -255,29 +287,64 @@ struct FinishArgs {
   long long lde;
   bf16* x;  // the block's rows; null: no dW
   long long ldx;
-  bool second;
+  bool second, last;  // last: of the call; total is taken behind it
+  bool direct;        // the rows are the tokens, also those that do not count
+  long long T;
+  float* total;
 };
 
-constexpr int kFinishRows = 8;
+// total = sum over the tokens that count of w loss, in 64 bits, by one CTA.
+__device__ void sum_losses(const LossRows& l, const float* loss, const float* weights, long long T,
+                           float* total) {
+  __shared__ double sums[kThreads / 32];
+  double sum = 0.0;
+#pragma unroll 4
+  for (long long t = threadIdx.x; t < T; t += kThreads)
+    if (l.pos[t] >= 0) sum += (weights != nullptr ? weights[t] : 1.0) * __ldcg(loss + t);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = 0.0;
+    for (int w = 0; w < kThreads / 32; ++w) sum += sums[w];
+    if (weights == nullptr) sum /= max(1, *l.count);
+    *total = static_cast<float>(sum);
+  }
+}
 
-// Eight rows per CTA.  The parts of their sums (all threads), then a warp per row:
+// Called by every CTA of the last kernel that writes losses: the one that comes last
+// sums them.
+__device__ void total_behind(const LossRows& l, const float* loss, const float* weights,
+                             long long T, float* total) {
+  __shared__ bool mine;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) mine = atomicAdd(l.done, 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (!mine) return;
+  __threadfence();
+  sum_losses(l, loss, weights, T, total);
+}
+
+// R rows per CTA, 8 or, for few rows, 1.  The parts of their sums (all threads), then a warp per row:
 // its loss, its factor, and in E the entries' terms e - p sum.  A row whose reference
 // does not fit sets its block's flag.  The second pass does this again where the flag
 // is set, and scales the rows of x for dW.
-__global__ void __launch_bounds__(kThreads) loss_finish_kernel(const FinishArgs a) {
-  __shared__ float2 sums[kThreads / 32][kFinishRows];
-  pdl_wait();
-  pdl_trigger();
+template <int R>
+__device__ __forceinline__ void finish_rows(const FinishArgs& a) {
+  __shared__ float2 sums[kThreads / 32][R];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int count = *a.rows.count;
-  const long long n = max(0ll, min(a.block, count - a.first));
-  const long long r0 = blockIdx.x * static_cast<long long>(kFinishRows);
+  const long long n = max(0ll, min(a.block, (a.direct ? a.T : count) - a.first));
+  const long long r0 = blockIdx.x * static_cast<long long>(R);
   if (r0 >= n) return;
   int* again = a.rows.again + a.first / a.block;
   const bool own = a.E == nullptr;  // every part has its own reference
-  const long long row = r0 + warp, r = a.first + row;
+  const long long row = r0 + warp, r = a.first + row;  // of the first R warps
+  const bool on = warp < R && row < n;
   if (!a.second || *again != 0) {
-    const int j = threadIdx.x % kFinishRows;
+    const int j = threadIdx.x % R;
     float m = -INFINITY, s = 0.f;
     const auto add = [&](float m2, float s2) {
       if (own) {
@@ -292,26 +359,28 @@ __global__ void __launch_bounds__(kThreads) loss_finish_kernel(const FinishArgs 
       }
     };
     if (r0 + j < n)
-      for (int i = threadIdx.x / kFinishRows; i < a.parts; i += kThreads / kFinishRows) {
+#pragma unroll 4
+      for (int i = threadIdx.x / R; i < a.parts; i += kThreads / R) {
         const float2 v = a.part[i * a.ldp + r0 + j];
         add(v.x, v.y);
       }
 #pragma unroll
-    for (int o = kFinishRows; o < 32; o *= 2) {
+    for (int o = R; o < 32; o *= 2) {
       const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
       add(m2, s2);
     }
-    if (lane < kFinishRows) sums[warp][lane] = make_float2(m, s);
+    if (lane < R) sums[warp][lane] = make_float2(m, s);
     __syncthreads();
     m = -INFINITY, s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) add(sums[w][warp].x, sums[w][warp].y);
-    if (row < n) {
+    for (int w = 0; w < kThreads / 32; ++w) add(sums[w][warp % R].x, sums[w][warp % R].y);
+    if (on) {
       const float ref = own ? (m == -INFINITY ? 0.f : m * a.unit) : a.rows.ref[r];
       // an infinite logit: the sum is infinite too
       const float log_s = m == INFINITY ? 0.f : log2f(s);
-      const int t = a.rows.token[r];
-      const long long base = static_cast<long long>(t) * a.top;
+      const long long t = a.direct ? r : a.rows.token[r];
+      const bool counts = !a.direct || a.rows.pos[t] >= 0;
+      const long long base = t * a.top;
       float sum = 0.f;
       for (int k = lane; k < a.top; k += 32) {
         const int i = a.rows.index[base + k];
@@ -327,7 +396,8 @@ __global__ void __launch_bounds__(kThreads) loss_finish_kernel(const FinishArgs 
       }
       sum = warp_sum(sum);
       if (lane == 0) {
-        a.loss[t] = a.tau * a.tau * (a.rows.ent[t] + 0.69314718056f * sum);
+        a.loss[t] =
+            counts ? a.tau * a.tau * (a.rows.ent[t] + 0.69314718056f * sum) : 0.f;
         if (!own) {
           a.rows.scale[r] = make_float2(
               a.tau / s, a.weights != nullptr ? a.weights[t] : 1.f / static_cast<float>(count));
@@ -340,23 +410,45 @@ __global__ void __launch_bounds__(kThreads) loss_finish_kernel(const FinishArgs 
       }
     }
   }
-  if (a.second && a.x != nullptr && row < n) {
-    __syncwarp();
-    const float2 f = a.rows.scale[r];
-    const float by = f.x * (f.y / *a.rows.most);
-    bf16* x = a.x + row * a.ldx;
-    for (int c = lane; c < a.d; c += 32) x[c] = __float2bfloat16_rn(__bfloat162float(x[c]) * by);
+  if (!a.second || a.x == nullptr) return;
+  __syncthreads();
+  // the rows of x, all threads
+  const bool vec = a.d % 8 == 0;
+  const int pieces = vec ? a.d / 8 : a.d;
+  const int rows = static_cast<int>(min(static_cast<long long>(R), n - r0));
+  const float most = *a.rows.most;
+  for (int i = 0; i < rows; ++i) {
+    const float2 f = a.rows.scale[a.first + r0 + i];
+    const float by = f.x * (f.y / most);
+    bf16* x = a.x + (r0 + i) * a.ldx;
+    for (int c = threadIdx.x; c < pieces; c += kThreads) {
+      if (vec) {
+        Pack<bf16, 8>* at = reinterpret_cast<Pack<bf16, 8>*>(x) + c;
+        Pack<bf16, 8> v = *at;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v.x[k] = __float2bfloat16_rn(__bfloat162float(v.x[k]) * by);
+        *at = v;
+      } else {
+        x[c] = __float2bfloat16_rn(__bfloat162float(x[c]) * by);
+      }
+    }
   }
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads) loss_finish_kernel(const FinishArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  finish_rows<R>(a);
+  if (a.last) total_behind(a.rows, a.loss, a.weights, a.T, a.total);
 }
 
 // A CTA per gathered row of the block: its loss from the fp32 logits z, and in
 // place of them dz where the gradients are wanted (rows that do not count: 0).
-__global__ void __launch_bounds__(kThreads)
-    loss_rows_kernel(float* __restrict__ z, LossRows l, long long first, int V, int top,
-                     float inv_tau, float tau, const float* __restrict__ weights, bool grad,
-                     float* __restrict__ loss) {
-  pdl_wait();
-  pdl_trigger();
+__device__ __forceinline__ void loss_row(float* __restrict__ z, const LossRows& l, long long first,
+                                         int V, int top, float inv_tau, float tau,
+                                         const float* __restrict__ weights, bool grad,
+                                         float* __restrict__ loss) {
   __shared__ float ms[kThreads / 32], ss[kThreads / 32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const long long r = first + blockIdx.x;
@@ -409,26 +501,14 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// total = sum over the tokens that count of w loss, in 64 bits, one CTA.
-__global__ void __launch_bounds__(kOrderThreads)
-    loss_total_kernel(const float* __restrict__ loss, const float* __restrict__ weights, LossRows l,
-                      long long T, float* __restrict__ total) {
+__global__ void __launch_bounds__(kThreads)
+    loss_rows_kernel(float* __restrict__ z, LossRows l, long long first, int V, int top,
+                     float inv_tau, float tau, const float* __restrict__ weights, bool grad,
+                     float* __restrict__ loss, bool last, long long T, float* __restrict__ total) {
   pdl_wait();
   pdl_trigger();
-  __shared__ double sums[32];
-  double sum = 0.0;
-  for (long long t = threadIdx.x; t < T; t += kOrderThreads)
-    if (l.pos[t] >= 0) sum += (weights != nullptr ? weights[t] : 1.0) * loss[t];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    sum = 0.0;
-    for (int w = 0; w < kOrderThreads / 32; ++w) sum += sums[w];
-    if (weights == nullptr) sum /= max(1, *l.count);
-    *total = static_cast<float>(sum);
-  }
+  loss_row(z, l, first, V, top, inv_tau, tau, weights, grad, loss);
+  if (last) total_behind(l, loss, weights, T, total);
 }
 
 // out[c][r] = in[r][c], in [rows][cols].
@@ -467,6 +547,7 @@ size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 long long round64(long long n) { return (n + 63) / 64 * 64; }
 
 constexpr size_t kBlockBytes = size_t{1} << 31;  // of a block's terms
+constexpr long long kFewTokens = 64;
 
 // Elements between rows of d features as TMA operands (16-byte multiples).
 long long pitch_of(int d, bool is_bf16) { return !is_bf16 || d % 8 == 0 ? d : round64(d); }
@@ -556,8 +637,33 @@ __global__ void __launch_bounds__(kThreads)
   for (int c = threadIdx.x % 32; c < d; c += 32) out[r * ld + c] = in[r * d + c];
 }
 
+// Losses alone of a few tokens: from x as it lies, the weight streamed once.  The
+// rows do not touch each other, so tokens that do not count may run along.
+bool few_form(const LossArgs& a) {
+  return a.is_bf16 && a.dx == nullptr && a.dW == nullptr && a.T <= kFewTokens && a.d % 8 == 0;
+}
+
+cudaError_t few_logits(const LossArgs& a, const LossProducts& p, cudaStream_t s) {
+  LossColumns c;
+  c.part = p.part;
+  c.ldp = p.ldp;
+  c.unit = p.unit;
+  c.index = p.rows.index;
+  c.z = p.rows.z;
+  c.top = a.top;
+  LinearProduct g;
+  g.A = a.x;
+  g.B = a.W;
+  g.lda = g.ldb = a.d;
+  g.M = a.T, g.N = a.V, g.K = a.d;
+  g.loss = &c;
+  g.tag = "loss_stream";
+  return linear_stream(g, s);
+}
+
 cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, char* ws,
                      cudaStream_t s) {
+  const bool direct = few_form(a);
   const bool grad = a.dx != nullptr || a.dW != nullptr;
   bf16* xg = reinterpret_cast<bf16*>(ws + plan.xg);
   bf16* E = grad ? reinterpret_cast<bf16*>(ws + plan.terms) : nullptr;
@@ -588,13 +694,15 @@ cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, cha
   g.dW = a.dW;
   g.acc = plan.blocks > 1 ? reinterpret_cast<float*>(ws + plan.acc) : nullptr;
   g.parts = reinterpret_cast<float*>(ws + plan.cut);
+  g.schedule = ws + plan.meta + 64;
   g.rows = l;
   FinishArgs f = {};
+  f.direct = direct;
   f.rows = l;
   f.part = g.part;
   f.ldp = g.ldp;
   f.block = plan.block;
-  f.parts = loss_parts(a.V);
+  f.parts = direct ? (a.V + 127) / 128 : loss_parts(a.V);
   f.top = a.top;
   f.d = a.d;
   f.unit = g.unit;
@@ -604,18 +712,27 @@ cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, cha
   f.E = E;
   f.lde = g.lde;
   f.ldx = g.ldx;
-  const dim3 finish_grid(static_cast<unsigned>((plan.block + kFinishRows - 1) / kFinishRows));
+  // a row of many parts is a CTA's work where there are few rows
+  const bool few = plan.block <= 2 * sm_count();
+  f.T = a.T;
+  f.total = a.total;
   for (int b = 0; b < plan.blocks; ++b) {
     bf16* xb = xg + b * plan.block * plan.ldx;
     g.first = f.first = b * plan.block;
     g.x = xb;
     g.x_rows = std::min(plan.block, round64(a.T) - g.first);
     for (int pass = 0; pass < (grad ? 2 : 1); ++pass) {
-      if ((e = loss_logits(g, pass > 0, s)) != cudaSuccess) return e;
+      e = direct ? few_logits(a, g, s) : loss_logits(g, pass > 0, s);
+      if (e != cudaSuccess) return e;
       f.second = pass > 0;
       f.x = a.dW != nullptr ? xb : nullptr;
+      f.last = b == plan.blocks - 1 && (!grad || pass == 1);
       e = launched("loss_finish", s, [&] {
-        return launch_pdl(loss_finish_kernel, finish_grid, dim3(kThreads), 0, s, f);
+        return few ? launch_pdl(loss_finish_kernel<1>, dim3(static_cast<unsigned>(plan.block)),
+                                dim3(kThreads), 0, s, f)
+                   : launch_pdl(loss_finish_kernel<8>,
+                                dim3(static_cast<unsigned>((plan.block + 7) / 8)), dim3(kThreads),
+                                0, s, f);
       });
       if (e != cudaSuccess) return e;
     }
@@ -647,7 +764,8 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
     if ((e = linear_fp32(g, scratch, s)) != cudaSuccess) return e;
     e = launched("loss_rows", s, [&] {
       return launch_pdl(loss_rows_kernel, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, s,
-                        z, l, first, a.V, a.top, 1.f / a.tau, a.tau, a.weights, grad, a.loss);
+                        z, l, first, a.V, a.top, 1.f / a.tau, a.tau, a.weights, grad, a.loss,
+                        first + rows >= a.T, a.T, a.total);
     });
     if (e != cudaSuccess) return e;
     if (a.dW != nullptr) {
@@ -689,14 +807,14 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
   return cudaSuccess;
 }
 
-template <typename TX>
+template <typename TX, int V>
 cudaError_t run_gather(const LossArgs& a, const Plan& plan, const LossRows& l, char* ws,
                        cudaStream_t s) {
   const bool grad = a.dx != nullptr || a.dW != nullptr;
   return launched("loss_gather", s, [&] {
-    return launch_pdl(loss_gather_kernel<TX>, dim3(warps_grid(a.T + round64(a.T))),
+    return launch_pdl(loss_gather_kernel<TX, V>, dim3(warps_grid(a.T + round64(a.T))),
                       dim3(kThreads), 0, s, static_cast<const TX*>(a.x),
-                      static_cast<const TX*>(a.W), l, a.T, a.d, static_cast<long long>(a.d),
+                      static_cast<const TX*>(a.W), l, a.T, a.d,
                       reinterpret_cast<TX*>(ws + plan.xg), plan.ldx, !a.is_bf16,
                       a.is_bf16 && grad ? 1.44269504089f / a.tau : 0.f, a.loss,
                       static_cast<TX*>(a.dx));
@@ -725,26 +843,33 @@ cudaError_t head_loss(const LossArgs& a, void* scratch, cudaStream_t s) {
   l.z = reinterpret_cast<float*>(ws + plan.z);
   l.ref = reinterpret_cast<float*>(ws + plan.ref);
   l.scale = reinterpret_cast<float2*>(ws + plan.scale);
-  cudaError_t e = launched("loss_entries", s, [&] {
-    return launch_pdl(loss_entries_kernel,
-                      dim3(static_cast<unsigned>((a.T + kEntryWarps - 1) / kEntryWarps)),
-                      dim3(32 * kEntryWarps), 0, s, a.indices, a.index_bytes, a.top_logits,
-                      a.top_bf16, a.T, a.top, a.V, 1.f / a.tau, l, device_status_ptr());
-  });
-  if (e != cudaSuccess) return e;
+  l.done = reinterpret_cast<int*>(ws + plan.meta + 8);
+  cudaError_t e;
+  const bool ce = a.top_logits == nullptr;
+  if (!ce) {
+    e = launched("loss_entries", s, [&] {
+      return launch_pdl(loss_entries_kernel,
+                        dim3(static_cast<unsigned>((a.T + kEntryWarps - 1) / kEntryWarps)),
+                        dim3(32 * kEntryWarps), 0, s, a.indices, a.index_bytes, a.top_logits,
+                        a.top_bf16, a.T, a.top, a.V, 1.f / a.tau, l, device_status_ptr());
+    });
+    if (e != cudaSuccess) return e;
+  }
   e = launched("loss_order", s, [&] {
     return launch_pdl(loss_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, l, a.T, a.weights,
-                      plan.blocks);
+                      plan.blocks, ce ? a.indices : nullptr, a.index_bytes, a.V,
+                      device_status_ptr());
   });
   if (e != cudaSuccess) return e;
-  e = a.is_bf16 ? run_gather<bf16>(a, plan, l, ws, s) : run_gather<float>(a, plan, l, ws, s);
+  if (few_form(a))
+    e = cudaSuccess;
+  else if (a.is_bf16)
+    e = a.d % 8 == 0 ? run_gather<bf16, 8>(a, plan, l, ws, s) : run_gather<bf16, 1>(a, plan, l, ws, s);
+  else
+    e = a.d % 4 == 0 ? run_gather<float, 4>(a, plan, l, ws, s)
+                     : run_gather<float, 1>(a, plan, l, ws, s);
   if (e != cudaSuccess) return e;
-  e = a.is_bf16 ? run_bf16(a, plan, l, ws, s) : run_f32(a, plan, l, ws, s);
-  if (e != cudaSuccess) return e;
-  return launched("loss_total", s, [&] {
-    return launch_pdl(loss_total_kernel, dim3(1), dim3(kOrderThreads), 0, s,
-                      static_cast<const float*>(a.loss), a.weights, l, a.T, a.total);
-  });
+  return a.is_bf16 ? run_bf16(a, plan, l, ws, s) : run_f32(a, plan, l, ws, s);
 }
 
 }  // namespace poetx

@@ -37,6 +37,7 @@ cudaError_t head_loss(const LossArgs& a, void* scratch, cudaStream_t s);
 struct LossRows {
   int* count;    // rows
   float* most;   // the largest |weight| of a row (1 if that is 0 or none is given)
+  int* done;     // CTAs of the last kernel that writes losses
   int* again;    // per block: a row's reference did not fit
   int* pos;      // [T]: a token's row, -1 where it does not count
   int* token;    // [T]: a row's token
@@ -72,6 +73,7 @@ struct LossProducts {
   void* dW;       // [V][d]
   float* acc;     // [V][d] fp32, or null: there is one block
   float* parts;   // loss_cut_bytes, needed where loss_cuts(V) for dx, loss_cuts(block) for dw
+  void* schedule;  // 64 bytes
   LossRows rows;
 };
 

@@ -51,22 +51,6 @@ constexpr int kSlots = 4;        // slices' tiles per cluster at most
 constexpr float kCutCost = 20.f;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
-struct PairArgs {
-  int n_tiles, N, K, V, top;
-  long long M;           // kDw: the output's rows
-  long long first, block;
-  long long ld, ldp;
-  const int* only;       // null, or nothing is done while it is 0
-  float unit;
-  bool store, vec;       // kLogits: E is wanted; output rows are 16-byte aligned
-  float2* part;
-  bf16* out;             // dx or dW
-  float* acc;
-  float* parts;          // of tiles cut along K; null: none is
-  LossRows rows;
-  int* status;
-};
-
 // The order of the work.  Whole rounds of tiles over the clusters come first; the
 // tiles of the last round (`rest`) are cut into `slices` of their K steps, all of one
 // slice before the next, so that what runs at one time still shares its operands
@@ -74,12 +58,16 @@ struct PairArgs {
 // 1638 rows, d = 2048, V = 32000).  A slice's tile is kept in fp32, [256][256], and
 // added up by loss_sum_kernel.
 struct Schedule {
-  int whole, rest = 0, slices = 1, share, k_steps, clusters;
+  int whole, rest, slices, share, k_steps, clusters;
 
   // In units of a K step (0.28 us): the rounds of the rest and, when it is cut, 0.4
   // for a slice's tile written and read and kCutCost for the launch.
-  __device__ Schedule(int tiles, int steps, int clusters_, bool may_cut)
-      : whole(tiles), share(steps), k_steps(steps), clusters(clusters_) {
+  __device__ void plan(int tiles, int steps, int clusters_, bool may_cut) {
+    whole = tiles;
+    rest = 0;
+    slices = 1;
+    share = k_steps = steps;
+    clusters = clusters_;
     const int left = tiles % clusters;
     if (!may_cut || left == 0) return;
     float best = static_cast<float>(steps);
@@ -118,6 +106,23 @@ struct Schedule {
     k1 = min(k_steps, k0 + share);
     return true;
   }
+};
+
+struct PairArgs {
+  int n_tiles, N, K, V, top;
+  long long M;           // kDw: the output's rows
+  long long first, block;
+  long long ld, ldp;
+  const int* only;       // null, or nothing is done while it is 0
+  float unit;
+  bool store, vec;       // kLogits: E is wanted; output rows are 16-byte aligned
+  float2* part;
+  bf16* out;             // dx or dW
+  float* acc;
+  float* parts;          // of tiles cut along K; null: none is
+  Schedule* schedule;    // what loss_sum_kernel goes by
+  LossRows rows;
+  int* status;
 };
 
 __device__ __forceinline__ void unit_tile(int u, int m_pairs, int n_tiles, int& mp, int& nt) {
@@ -213,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain_bar = tempty_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Schedule* schedule = reinterpret_cast<Schedule*>(tmem_slot + 2);
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
@@ -260,7 +266,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.only != nullptr && *p.only == 0) units = 0;
   if (KIND == kDw && n == 0 && p.first > 0) units = 0;  // the block before was the last
   const bool products = k_steps > 0;  // dW without a row is 0
-  const Schedule todo(units, k_steps, step, KIND != kLogits && p.parts != nullptr);
+  if (threadIdx.x == 0) {
+    schedule->plan(units, k_steps, step, KIND != kLogits && p.parts != nullptr);
+    if (blockIdx.x == 0 && p.parts != nullptr) *p.schedule = *schedule;
+  }
+  __syncthreads();
+  const Schedule todo = *schedule;
 
   const uint32_t full0 = map_peer(smem_u32(full_bar), 0);
   const uint32_t tempty0 = map_peer(smem_u32(tempty_bar), 0);
@@ -610,62 +621,60 @@ constexpr int kSumRows = 4;
 constexpr int kSumThreads = 256;
 
 template <int KIND>
-__global__ void __launch_bounds__(kSumThreads) loss_sum_kernel(const PairArgs p, int clusters) {
+__global__ void __launch_bounds__(kSumThreads) loss_sum_kernel(const PairArgs p) {
   pdl_wait();
   pdl_trigger();
+  const int rest = p.schedule->rest, slices = p.schedule->slices, whole = p.schedule->whole;
   const long long counted = *p.rows.count;
-  const long long n = max(0ll, min(p.block, counted - p.first));
-  const long long M = KIND == kDw ? p.M : n;
+  const long long M = KIND == kDw ? p.M : max(0ll, min(p.block, counted - p.first));
   const int m_pairs = static_cast<int>((M + 2 * BM - 1) / (2 * BM));
-  const int k_steps = static_cast<int>(((KIND == kDw ? n : p.K) + BK - 1) / BK);
-  const Schedule todo(m_pairs * p.n_tiles, k_steps, clusters, true);
-  constexpr int kPieces = 2 * BM / kSumRows;
-  const int j = static_cast<int>(blockIdx.x) / kPieces, piece = blockIdx.x % kPieces;
-  if (j >= todo.rest) return;
-  int mp, nt;
-  unit_tile(todo.whole + j, m_pairs, p.n_tiles, mp, nt);
   const bool last = KIND != kDw || p.acc == nullptr || p.first + p.block >= counted;
-  const int col = threadIdx.x % 64 * 4, to_col = nt * BN + col;
-  if (to_col >= p.N) return;
-  const int in = min(4, p.N - to_col);
-  const int r = piece * kSumRows + threadIdx.x / 64;
-  const long long row = static_cast<long long>(mp) * 2 * BM + r;
-  if (row >= M) return;
-  const float* part = p.parts + static_cast<long long>(j) * 2 * BM * BN + r * BN + col;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  constexpr int kPieces = 2 * BM / kSumRows;
+  for (int item = blockIdx.x; item < rest * kPieces; item += gridDim.x) {
+    const int j = item / kPieces;
+    int mp, nt;
+    unit_tile(whole + j, m_pairs, p.n_tiles, mp, nt);
+    const int col = threadIdx.x % 64 * 4, to_col = nt * BN + col;
+    const int in = min(4, p.N - to_col);
+    const int r = item % kPieces * kSumRows + threadIdx.x / 64;
+    const long long row = static_cast<long long>(mp) * 2 * BM + r;
+    if (row >= M || in <= 0) continue;
+    const float* part = p.parts + static_cast<long long>(j) * 2 * BM * BN + r * BN + col;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-  for (int i = 0; i < todo.slices; ++i) {
-    const float4 q =
-        *reinterpret_cast<const float4*>(part + static_cast<long long>(i) * todo.rest * 2 * BM * BN);
-    v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
-  }
-  long long to = row;
-  if (KIND == kDx) {
-    to = p.rows.token[p.first + row];
-    const float2 scale = p.rows.scale[p.first + row];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = v[i] * scale.x * scale.y;
-  } else {
-    const float most = *p.rows.most;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] *= most;
-      if (p.acc == nullptr || i >= in) continue;
-      float* sum = p.acc + row * p.N + to_col + i;
-      if (p.first > 0) v[i] += *sum;
-      if (!last) *sum = v[i];
+    for (int i = 0; i < slices; ++i) {
+      const float4 q =
+          *reinterpret_cast<const float4*>(part + static_cast<long long>(i) * rest * 2 * BM * BN);
+      v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
     }
-  }
-  if (!last) return;
-  bf16* out = p.out + to * p.ld + to_col;
-  if (p.vec) {
-    *reinterpret_cast<uint2*>(out) =
-        make_uint2(pack_bf16x2(__float_as_uint(v[0]), __float_as_uint(v[1])),
-                   pack_bf16x2(__float_as_uint(v[2]), __float_as_uint(v[3])));
-  } else {
+    long long to = row;
+    if (KIND == kDx) {
+      to = p.rows.token[p.first + row];
+      const float2 scale = p.rows.scale[p.first + row];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < in) out[i] = __float2bfloat16_rn(v[i]);
+      for (int i = 0; i < 4; ++i) v[i] = v[i] * scale.x * scale.y;
+    } else {
+      const float most = *p.rows.most;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] *= most;
+        if (p.acc == nullptr || i >= in) continue;
+        float* sum = p.acc + row * p.N + to_col + i;
+        if (p.first > 0) v[i] += *sum;
+        if (!last) *sum = v[i];
+      }
+    }
+    if (!last) continue;
+    bf16* out = p.out + to * p.ld + to_col;
+    if (p.vec) {
+      *reinterpret_cast<uint2*>(out) =
+          make_uint2(pack_bf16x2(__float_as_uint(v[0]), __float_as_uint(v[1])),
+                     pack_bf16x2(__float_as_uint(v[2]), __float_as_uint(v[3])));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < in) out[i] = __float2bfloat16_rn(v[i]);
+    }
   }
 }
 
@@ -719,11 +728,9 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
   prof_end(tag, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess || KIND == kLogits || p.parts == nullptr) return e;
-  const int clusters = static_cast<int>(cfg.gridDim.x / 2);
   prof_begin("loss_sum", stream);
-  e = launch_pdl(loss_sum_kernel<KIND>,
-                 dim3(static_cast<unsigned>(clusters * (2 * BM / kSumRows))), dim3(kSumThreads), 0,
-                 stream, p, clusters);
+  e = launch_pdl(loss_sum_kernel<KIND>, dim3(8 * static_cast<unsigned>(sm_count())),
+                 dim3(kSumThreads), 0, stream, p);
   prof_end("loss_sum", stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -782,6 +789,7 @@ cudaError_t loss_dx(const LossProducts& g, cudaStream_t s) {
   p.N = g.d;
   p.K = g.V;
   p.parts = loss_cuts(g.V) ? g.parts : nullptr;
+  p.schedule = static_cast<Schedule*>(g.schedule);
   p.out = static_cast<bf16*>(g.dx);
   p.ld = g.d;
   p.vec = g.d % 8 == 0;
@@ -804,6 +812,7 @@ cudaError_t loss_dw(const LossProducts& g, cudaStream_t s) {
   p.out = static_cast<bf16*>(g.dW);
   p.acc = g.acc;
   p.parts = loss_cuts(g.block) ? g.parts : nullptr;
+  p.schedule = static_cast<Schedule*>(g.schedule);
   p.ld = g.d;
   return launch<kDw>(tmA, tmB, tmOut, p, pairs(g.V) * p.n_tiles, "loss_dw", s);
 }
