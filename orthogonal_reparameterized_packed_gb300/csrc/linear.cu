@@ -254,7 +254,8 @@ size_t fp32_scratch(long long M, int N, int K, bool b_mn, bool fewer) {
 }  // namespace
 
 cudaError_t linear_fp32(const LinearProduct& g, void* scratch, cudaStream_t s) {
-  return linear_split_pays(g.M, g.N, g.K) ? linear_split(g, scratch, s) : linear_simt(g, s);
+  return g.slices > 1 || linear_split_pays(g.M, g.N, g.K) ? linear_split(g, scratch, s)
+                                                          : linear_simt(g, s);
 }
 
 // bf16: padded copies of x and W where d_in is no multiple of 8; fp32: the

@@ -33,10 +33,16 @@ struct LinearProduct {
   long long M = 0;
   int N = 0, K = 0;
   int act = 0;
-  // linear_simt: where flags[0] is 0, only rows with one of flags[1 + row * segs ..
+  // linear_simt: where *all_rows is 0, only rows with one of row_flags[row * segs ..
   // + segs) not 0 are computed
-  const int* flags = nullptr;
+  const int* all_rows = nullptr;
+  const int* row_flags = nullptr;
   int segs = 0;
+  // linear_fp32: K in `slices` pieces whose products are apart, piece i's in y + i M N
+  // (no bias, residual or activation); linear_fp32_slices says how many pay
+  int slices = 1;
+  // linear_split: the last product on this scratch had the same array B
+  bool b_ready = false;
   const LossColumns* loss = nullptr;  // linear_stream with B [N][K]
   const char* tag = "linear";
 };
@@ -53,13 +59,21 @@ cudaError_t linear_simt(const LinearProduct& g, cudaStream_t s);
 
 // In fp32 on the tensor cores, as six bf16 products (linear_split.cu); layouts
 // as for linear_simt, scratch of linear_split_scratch(g) bytes.
-bool linear_split_pays(long long M, int N, int K);
+bool linear_split_pays(long long M, int N, int K, int slices = 1);
 size_t linear_split_scratch(const LinearProduct& g);
 size_t linear_split_scratch_up_to(const LinearProduct& g);  // of any product of at most g.M rows
 cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s);
+// Whether linear_split left *scratch not 0: values of B are for the CUDA cores, which
+// computed everything (with slices, the first slice).
 
 // In fp32 in the form that takes less time, with linear_split_scratch_up_to(g) bytes
-// of scratch or more (linear.cu).
+// of scratch or more (linear.cu); in slices always linear_split.
 cudaError_t linear_fp32(const LinearProduct& g, void* scratch, cudaStream_t s);
+
+// Pieces of K, 2 to kMaxFp32Slices with outputs of at most most_bytes, where these
+// are faster than linear_fp32 on the whole of K: a product of few tiles and a long K.
+// Else 1.
+constexpr int kMaxFp32Slices = 8;
+int linear_split_slices(long long M, int N, int K, size_t most_bytes);
 
 }  // namespace poetx

@@ -357,8 +357,8 @@ cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, do
   p.M = rows;
   p.N = g.N;
   p.K = g.K;
-  p.all_rows = g.flags;
-  p.row_flags = g.flags != nullptr ? g.flags + 1 + m_first * g.segs : nullptr;
+  p.all_rows = g.all_rows;
+  p.row_flags = g.row_flags != nullptr ? g.row_flags + m_first * g.segs : nullptr;
   p.segs = g.segs;
   p.vec_a = g.K % 4 == 0;
   p.vec_b = (B_KN ? g.N : g.K) % 4 == 0;

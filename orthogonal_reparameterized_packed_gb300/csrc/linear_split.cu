@@ -68,17 +68,25 @@ __device__ __forceinline__ int plane_b(int p) { return (0x010120 >> (4 * p)) & 3
 
 struct SplitArgs {
   int m_pairs, n_tiles, k_steps, N;
+  int slices, slice_steps;  // of K; a slice's outputs are M N values behind the last's
   int plane_rows_a, plane_rows_b;  // rows between planes of A, of B
   long long M;
   Fp32Epilogue epi;
-  int segs;           // flags per row of A
-  long long b_flags;  // flags of B
-  int* flags;  // [0]: set here, whether any of B's; from 1: A's, then B's.  Rows
-               // with one that is not 0 are left to linear_simt
+  int segs;              // flags per row of A
+  const int* row_flags;  // A's: rows with one that is not 0 are left to linear_simt
+  int b_flags;           // flags of B, behind `all`: then all rows are
+  int* all;              // set here: whether any of B's is
   int* status;
 };
 
-__device__ __forceinline__ void unit_tile(int u, const SplitArgs& p, int& mp, int& nt) {
+// Unit u: its tile and K steps; all tiles of a slice before the next.
+__device__ __forceinline__ void unit_tile(int u, const SplitArgs& p, int& mp, int& nt, int& slice,
+                                          int& begin, int& end) {
+  const int tiles = p.m_pairs * p.n_tiles;
+  slice = u / tiles;
+  u -= slice * tiles;
+  begin = slice * p.slice_steps;
+  end = min(p.k_steps, begin + p.slice_steps);
   const int per_group = kGroupM * p.n_tiles;
   const int g = u / per_group, r = u - g * per_group;
   const int rows = min(kGroupM, p.m_pairs - g * kGroupM);
@@ -140,11 +148,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
   int bad = 0;
-  for (long long i = threadIdx.x; i < p.b_flags; i += kThreads)
-    bad |= p.flags[1 + p.M * p.segs + i];
+  for (int i = threadIdx.x; i < p.b_flags; i += kThreads) bad |= p.all[1 + i];
   bad = __syncthreads_or(bad);
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.flags[0] = bad;
-  const int units = bad != 0 ? 0 : p.m_pairs * p.n_tiles;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.all = bad;
+  const int units = bad != 0 ? 0 : p.m_pairs * p.n_tiles * p.slices;
 
   const uint32_t full0 = map_peer(smem_u32(full_bar), 0);
   const uint32_t tempty0 = map_peer(smem_u32(tempty_bar), 0);
@@ -157,12 +164,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long issued = 0;
     bool ok = true;
     for (int u = first; u < units && ok; u += step) {
-      int mp, nt;
-      unit_tile(u, p, mp, nt);
+      int mp, nt, slice, begin, end;
+      unit_tile(u, p, mp, nt, slice, begin, end);
       const int a_row = mp * 2 * BM + static_cast<int>(rank) * BM;
       const int b_n = nt * kBN + static_cast<int>(rank) * (kBN / 2);
-      for (int k0 = 0; k0 < p.k_steps && ok; k0 += kChunkSteps) {
-        const int k1 = min(p.k_steps, k0 + kChunkSteps);
+      for (int k0 = begin; k0 < end && ok; k0 += kChunkSteps) {
+        const int k1 = min(end, k0 + kChunkSteps);
         for (int pr = 0; pr < kProducts && ok; ++pr) {
           const int ra = plane_a(pr) * p.plane_rows_a + a_row;
           const int rb = plane_b(pr) * p.plane_rows_b;
@@ -223,8 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       bool any_mma = false;
       for (int u = first; u < units && ok; u += step) {
-        for (int k0 = 0; k0 < p.k_steps && ok; k0 += kChunkSteps) {
-          const int steps = (min(p.k_steps, k0 + kChunkSteps) - k0) * kProducts;
+        int mp, nt, slice, begin, end;
+        unit_tile(u, p, mp, nt, slice, begin, end);
+        for (int k0 = begin; k0 < end && ok; k0 += kChunkSteps) {
+          const int steps = (min(end, k0 + kChunkSteps) - k0) * kProducts;
           if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1, abort_flag)) {
             record_timeout(p.status, abort_flag);
             ok = false;
@@ -282,12 +291,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int u = first; u < units && ok; u += step) {
-      int mp, nt;
-      unit_tile(u, p, mp, nt);
+      int mp, nt, slice, begin, end;
+      unit_tile(u, p, mp, nt, slice, begin, end);
       const long long row0 = static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32;
       const int col0 = nt * kBN + side * S::COLS;
       float sum[S::COLS / 16][16] = {};
-      for (int k0 = 0; k0 < p.k_steps; k0 += kChunkSteps) {
+      for (int k0 = begin; k0 < end; k0 += kChunkSteps) {
         const bool got = mbar_wait_cluster(&tfull_bar[acc], acc_phase, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
           record_timeout(p.status, abort_flag);
@@ -315,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this lane's row: outside, or left to linear_simt
       int skip = row0 + lane >= p.M;
       if (!skip)
-        for (int i = 0; i < p.segs; ++i) skip |= p.flags[1 + (row0 + lane) * p.segs + i];
+        for (int i = 0; i < p.segs; ++i) skip |= p.row_flags[(row0 + lane) * p.segs + i];
       // 16 columns at a time through the warp's staging tile, so that four lanes
       // write 64 bytes of a row (pieces of 16 bytes xor-swizzled by the row)
       // (one copy of the epilogue's code: sixteen unrolled ones, with every
@@ -339,7 +348,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float4 v =
               *reinterpret_cast<const float4*>(slot + r * 16 + ((lane % 4 ^ (r >> 1)) & 3) * 4);
           const int no = __shfl_sync(0xffffffffu, skip, r);
-          if (no == 0 && n < p.N) finish4(p.epi, row0 + r, n, v);
+          if (p.slices == 1) {
+            if (no == 0 && n < p.N) finish4(p.epi, row0 + r, n, v);
+          } else if (row0 + r < p.M && n < p.N && (no == 0 || slice > 0)) {
+            // a row of linear_simt's is whole in the first slice, 0 in the others
+            const float4 part = no == 0 ? v : make_float4(0.f, 0.f, 0.f, 0.f);
+            finish4(p.epi, slice * p.M + row0 + r, n, part);
+          }
         }
       }
     }
@@ -358,7 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // One operand: in [rows][cols] fp32 -> planes [3][plane_rows][pitch] bf16, rows
 // from `rows` to plane_rows zero (columns past cols are not read by any tile);
 // flag[r][segs]: whether a value of the row's segment of kSegment columns is
-// neither 0 nor of a magnitude that the planes take.
+// neither 0 nor of a magnitude that the planes take.  Of B a flag per CTA, `flags` of
+// them, is enough: one for every row (30001) made each CTA of the product read them
+// for 20 us.
 constexpr int kSegment = 1024;
 constexpr unsigned kLeastBits = (127u - 109u) << 23, kMostBits = (127u + 60u) << 23;
 
@@ -374,9 +391,10 @@ constexpr int kSplitThreads = 256;
 
 // Both operands, a warp per segment of a row.
 __global__ void __launch_bounds__(kSplitThreads)
-    split_planes_kernel(const SplitOperand a, const SplitOperand b) {
+    split_planes_kernel(const SplitOperand a, const SplitOperand b, int flags) {
   pdl_wait();
   pdl_trigger();
+  bool bad_b = false;
   const int lane = threadIdx.x % 32;
   const long long items_a = a.plane_rows * a.segs, items = items_a + b.plane_rows * b.segs;
   for (long long it = blockIdx.x * static_cast<long long>(kSplitThreads / 32) + threadIdx.x / 32;
@@ -425,15 +443,24 @@ __global__ void __launch_bounds__(kSplitThreads)
       }
     }
     bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) o.flag[at] = bad;
+    if (!first)
+      bad_b |= bad;
+    else if (lane == 0)
+      o.flag[at] = bad;
   }
+  if (b.plane_rows == 0) return;  // B's were made before
+  bad_b = __syncthreads_or(bad_b);
+  if (blockIdx.x == 0)
+    for (int i = gridDim.x + threadIdx.x; i < flags; i += kSplitThreads) b.flag[i] = 0;
+  if (threadIdx.x == 0) b.flag[blockIdx.x] = bad_b;
 }
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 long long b_plane_rows(const LinearProduct& g) {
-  // [K][N]: rows to a whole K step, so that no tile meets the next plane's rows
-  return g.b_mn ? (g.K + BK - 1) / BK * BK : g.N;
+  // [K][N]: rows to a whole K step, so that no tile meets the next plane's rows; [N][K]
+  // the same, for a next product with the array the other way round (b_ready)
+  return ((g.b_mn ? g.K : g.N) + BK - 1ll) / BK * BK;
 }
 
 int b_cols(const LinearProduct& g) { return g.b_mn ? g.N : g.K; }
@@ -444,13 +471,15 @@ long long pitch64(int cols) { return (static_cast<long long>(cols) + 63) / 64 * 
 
 int segments(int cols) { return (cols + kSegment - 1) / kSegment; }
 
+int split_ctas() { return 8 * sm_count(); }
+
 size_t planes_bytes(long long plane_rows, int cols) {
   return round256(static_cast<size_t>(kPlanes) * plane_rows * pitch64(cols) * 2);
 }
 
 template <int BN, bool B_MN>
 cudaError_t launch(const LinearProduct& g, const void* a_planes, const void* b_planes,
-                   int* flags, cudaStream_t stream) {
+                   int* all, const int* row_flags, cudaStream_t stream) {
   constexpr int kSmem = Shape<BN>::SMEM, kBN = BN;
   auto* kernel = linear_split_kernel<BN, B_MN>;
   static bool ready[64] = {false};
@@ -501,15 +530,18 @@ cudaError_t launch(const LinearProduct& g, const void* a_planes, const void* b_p
   p.m_pairs = static_cast<int>((g.M + 2 * BM - 1) / (2 * BM));
   p.n_tiles = (g.N + kBN - 1) / kBN;
   p.k_steps = (g.K + BK - 1) / BK;
+  p.slices = g.slices;
+  p.slice_steps = (p.k_steps + g.slices - 1) / g.slices;
   p.N = g.N;
   p.M = g.M;
   p.epi = fp32_epilogue(g, 0);
-  p.flags = flags;
+  p.all = all;
+  p.row_flags = row_flags;
   p.segs = segments(g.K);
-  p.b_flags = b_plane_rows(g) * segments(b_cols(g));
+  p.b_flags = split_ctas();
   p.status = device_status_ptr();
   const int clusters = static_cast<int>(
-      std::min<long long>(static_cast<long long>(p.m_pairs) * p.n_tiles, cmax));
+      std::min<long long>(static_cast<long long>(p.m_pairs) * p.n_tiles * p.slices, cmax));
   cfg.gridDim = dim3(2 * clusters);
   cfg.numAttrs = 2;
   prof_begin(g.tag, stream);
@@ -525,12 +557,25 @@ namespace {
 // Microseconds of the products' main loops: a 64-wide step of the six products
 // takes 1.71 us in a 256-wide tile, 1.12 in a 128-wide one (see linear_pair),
 // which pays where it fills idle clusters.
-double loop_us(long long M, int N, int K, bool* narrow) {
+double loop_us(long long M, int N, int K, bool* narrow, int slices = 1) {
   const long long m_pairs = (M + 2 * BM - 1) / (2 * BM), clusters = std::max(1, sm_count() / 2);
-  const long long wide = (m_pairs * ((N + 255) / 256) + clusters - 1) / clusters;
-  const long long thin = (m_pairs * ((N + 127) / 128) + clusters - 1) / clusters;
+  const long long wide = (slices * m_pairs * ((N + 255) / 256) + clusters - 1) / clusters;
+  const long long thin = (slices * m_pairs * ((N + 127) / 128) + clusters - 1) / clusters;
+  const long long steps = (K + BK - 1) / BK;
   *narrow = 1.12 * thin < 1.71 * wide;
-  return (*narrow ? 1.12 * thin : 1.71 * wide) * ((K + BK - 1) / BK);
+  return (*narrow ? 1.12 * thin : 1.71 * wide) * ((steps + slices - 1) / slices);
+}
+
+}  // namespace
+
+namespace {
+
+// With 4 bytes written and read per output and slice.
+double split_us(long long M, int N, int K, int slices) {
+  bool narrow;
+  return 18.0 + loop_us(M, N, K, &narrow, slices) +
+         10e-6 * K * (static_cast<double>(M) + N) / 6.0 +
+         (slices > 1 ? 2e-6 * slices * M * N : 0.0);
 }
 
 }  // namespace
@@ -538,25 +583,42 @@ double loop_us(long long M, int N, int K, bool* narrow) {
 // By the measured costs of both: here the loops above, 18 us for three launches
 // and the pipeline's ends, and 10 bytes per element of the operands for their
 // planes; linear_simt 8 us and 45 TFLOP/s.  They cross near 1000^3.
-bool linear_split_pays(long long M, int N, int K) {
-  bool narrow;
-  const double split =
-      18.0 + loop_us(M, N, K, &narrow) + 10e-6 * K * (static_cast<double>(M) + N) / 6.0;
-  return split < 8.0 + 2e-6 * M * N * K / 45.0;
+bool linear_split_pays(long long M, int N, int K, int slices) {
+  return split_us(M, N, K, slices) < 8.0 + 2e-6 * M * N * K / 45.0;
+}
+
+// A slice has at least four K steps, none is empty.  333 x 30001 -> 768 (6 tiles of
+// 256, 12 of 128, 469 steps): on the CUDA cores 459 us, SLICED us in 6 slices.
+int linear_split_slices(long long M, int N, int K, size_t most_bytes) {
+  const int steps = (K + BK - 1) / BK;
+  int best = 1;
+  double least = split_us(M, N, K, 1);
+  for (int n = 2; n <= kMaxFp32Slices && steps / n >= 4; ++n) {
+    if (4ull * n * M * N > most_bytes) break;
+    if ((steps + n - 1) / n * (n - 1) >= steps) continue;
+    const double us = split_us(M, N, K, n);
+    if (us < least) {
+      least = us;
+      best = n;
+    }
+  }
+  return linear_split_pays(M, N, K, best) ? best : 1;
 }
 
 namespace {
 
-size_t flag_bytes(const LinearProduct& g) {
-  return round256(
-      static_cast<size_t>(1 + g.M * segments(g.K) + b_plane_rows(g) * segments(b_cols(g))) *
-      sizeof(int));
+size_t row_flag_bytes(const LinearProduct& g) {
+  return round256(static_cast<size_t>(g.M * segments(g.K)) * sizeof(int));
 }
+
+size_t all_flag_bytes() { return round256((1 + split_ctas()) * sizeof(int)); }
 
 }  // namespace
 
+// B's flags and planes come first: their place depends on B alone.
 size_t linear_split_scratch(const LinearProduct& g) {
-  return flag_bytes(g) + planes_bytes(g.M, g.K) + planes_bytes(b_plane_rows(g), b_cols(g));
+  return all_flag_bytes() + planes_bytes(b_plane_rows(g), b_cols(g)) + row_flag_bytes(g) +
+         planes_bytes(g.M, g.K);
 }
 
 // Whether this form is taken does not grow with the rows: a new pair of row tiles
@@ -576,39 +638,44 @@ size_t linear_split_scratch_up_to(const LinearProduct& g) {
 
 cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) {
   SplitOperand a, b;
-  int* flags = static_cast<int*>(scratch);
-  char* at = static_cast<char*>(scratch) + flag_bytes(g);
+  int* all = static_cast<int*>(scratch);
+  char* b_at = static_cast<char*>(scratch) + all_flag_bytes();
+  char* a_at = b_at + planes_bytes(b_plane_rows(g), b_cols(g));
+  int* row_flags = reinterpret_cast<int*>(a_at);
   a.in = static_cast<const float*>(g.A);
-  a.planes = reinterpret_cast<bf16*>(at);
-  a.flag = flags + 1;
+  a.planes = reinterpret_cast<bf16*>(a_at + row_flag_bytes(g));
+  a.flag = row_flags;
   a.rows = a.plane_rows = g.M;
   a.cols = g.K;
   a.segs = segments(a.cols);
   a.pitch = pitch64(a.cols);
   b.in = static_cast<const float*>(g.B);
-  b.planes = reinterpret_cast<bf16*>(at + planes_bytes(g.M, g.K));
-  b.flag = flags + 1 + g.M * segments(g.K);
+  b.planes = reinterpret_cast<bf16*>(b_at);
+  b.flag = all + 1;
   b.rows = g.b_mn ? g.K : g.N;
-  b.plane_rows = b_plane_rows(g);
+  b.plane_rows = g.b_ready ? 0 : b_plane_rows(g);
   b.cols = b_cols(g);
   b.segs = segments(b.cols);
   b.pitch = pitch64(b.cols);
   const int grid = static_cast<int>(
-      std::min<long long>((a.plane_rows * a.segs + b.plane_rows * b.segs + 7) / 8,
-                          8ll * sm_count()));
+      std::min<long long>((a.plane_rows * a.segs + b_plane_rows(g) * b.segs + 7) / 8,
+                          split_ctas()));
   prof_begin("linear_split_planes", s);
-  cudaError_t e = launch_pdl(split_planes_kernel, dim3(grid), dim3(kSplitThreads), 0, s, a, b);
+  cudaError_t e =
+      launch_pdl(split_planes_kernel, dim3(grid), dim3(kSplitThreads), 0, s, a, b, split_ctas());
   prof_end("linear_split_planes", s);
   if (e != cudaSuccess) return e;
   bool narrow;
-  loop_us(g.M, g.N, g.K, &narrow);
-  e = narrow ? g.b_mn ? launch<128, true>(g, a.planes, b.planes, flags, s)
-                      : launch<128, false>(g, a.planes, b.planes, flags, s)
-      : g.b_mn ? launch<256, true>(g, a.planes, b.planes, flags, s)
-               : launch<256, false>(g, a.planes, b.planes, flags, s);
+  loop_us(g.M, g.N, g.K, &narrow, g.slices);
+  e = narrow ? g.b_mn ? launch<128, true>(g, a.planes, b.planes, all, row_flags, s)
+                      : launch<128, false>(g, a.planes, b.planes, all, row_flags, s)
+      : g.b_mn ? launch<256, true>(g, a.planes, b.planes, all, row_flags, s)
+               : launch<256, false>(g, a.planes, b.planes, all, row_flags, s);
   if (e != cudaSuccess) return e;
   LinearProduct again = g;
-  again.flags = flags;
+  again.all_rows = all;
+  again.row_flags = row_flags;
+  again.slices = 1;
   again.segs = a.segs;
   again.tag = "linear_rows";
   return linear_simt(again, s);

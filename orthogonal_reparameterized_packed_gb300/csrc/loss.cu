@@ -294,12 +294,13 @@ struct FinishArgs {
 };
 
 // total = sum over the tokens that count of w loss, in 64 bits, by one CTA.
+template <int THREADS>
 __device__ void sum_losses(const LossRows& l, const float* loss, const float* weights, long long T,
                            float* total) {
-  __shared__ double sums[kThreads / 32];
+  __shared__ double sums[THREADS / 32];
   double sum = 0.0;
 #pragma unroll 4
-  for (long long t = threadIdx.x; t < T; t += kThreads)
+  for (long long t = threadIdx.x; t < T; t += THREADS)
     if (l.pos[t] >= 0) sum += (weights != nullptr ? weights[t] : 1.0) * __ldcg(loss + t);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -307,7 +308,7 @@ __device__ void sum_losses(const LossRows& l, const float* loss, const float* we
   __syncthreads();
   if (threadIdx.x == 0) {
     sum = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w) sum += sums[w];
+    for (int w = 0; w < THREADS / 32; ++w) sum += sums[w];
     if (weights == nullptr) sum /= max(1, *l.count);
     *total = static_cast<float>(sum);
   }
@@ -315,6 +316,7 @@ __device__ void sum_losses(const LossRows& l, const float* loss, const float* we
 
 // Called by every CTA of the last kernel that writes losses: the one that comes last
 // sums them.
+template <int THREADS>
 __device__ void total_behind(const LossRows& l, const float* loss, const float* weights,
                              long long T, float* total) {
   __shared__ bool mine;
@@ -324,7 +326,7 @@ __device__ void total_behind(const LossRows& l, const float* loss, const float* 
   __syncthreads();
   if (!mine) return;
   __threadfence();
-  sum_losses(l, loss, weights, T, total);
+  sum_losses<THREADS>(l, loss, weights, T, total);
 }
 
 // R rows per CTA, 8 or, for few rows, 1.  The parts of their sums (all threads), then a warp per row:
@@ -440,47 +442,63 @@ __global__ void __launch_bounds__(kThreads) loss_finish_kernel(const FinishArgs 
   pdl_wait();
   pdl_trigger();
   finish_rows<R>(a);
-  if (a.last) total_behind(a.rows, a.loss, a.weights, a.T, a.total);
+  if (a.last) total_behind<kThreads>(a.rows, a.loss, a.weights, a.T, a.total);
 }
 
-// A CTA per gathered row of the block: its loss from the fp32 logits z, and in
+// A CTA per row of the block: its loss from the fp32 logits z, and in
 // place of them dz where the gradients are wanted (rows that do not count: 0).
+template <int THREADS>
 __device__ __forceinline__ void loss_row(float* __restrict__ z, const LossRows& l, long long first,
                                          int V, int top, float inv_tau, float tau,
                                          const float* __restrict__ weights, bool grad,
                                          float* __restrict__ loss) {
-  __shared__ float ms[kThreads / 32], ss[kThreads / 32];
+  __shared__ float ms[THREADS / 32], ss[THREADS / 32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const long long r = first + blockIdx.x;
   float* row = z + static_cast<long long>(blockIdx.x) * V;
   const int n = *l.count;
   if (r >= n) {
     if (grad)
-      for (int v = threadIdx.x; v < V; v += kThreads) row[v] = 0.f;
+      for (int v = threadIdx.x; v < V; v += THREADS) row[v] = 0.f;
     return;
   }
-  float m = -INFINITY;
-  for (int v = threadIdx.x; v < V; v += kThreads) m = fmaxf(m, row[v]);
+  // largest and sum in one pass, eight values at a time
+  float m = -INFINITY, s = 0.f;
+  for (int v0 = threadIdx.x; v0 < V; v0 += 8 * THREADS) {
+    float x[8], top_x = m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = v0 + j * THREADS < V ? row[v0 + j * THREADS] : -INFINITY;
+      top_x = fmaxf(top_x, x[j]);
+    }
+    if (m < top_x) {
+      s *= expf((m - top_x) * inv_tau);
+      m = top_x;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += expf((x[j] - ref) * inv_tau);
+  }
+  const float mine = m;
   m = warp_max(m);
   if (lane == 0) ms[warp] = m;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, ms[w]);
-  float s = 0.f;
-  for (int v = threadIdx.x; v < V; v += kThreads) s += expf((row[v] - m) * inv_tau);
+  for (int w = 0; w < THREADS / 32; ++w) m = fmaxf(m, ms[w]);
+  if (mine < m) s *= expf((mine - m) * inv_tau);
   s = warp_sum(s);
   if (lane == 0) ss[warp] = s;
   __syncthreads();
   s = 0.f;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) s += ss[w];
+  for (int w = 0; w < THREADS / 32; ++w) s += ss[w];
   const long long t = l.token[r], base = t * top;
-  const float log_s = logf(s);
   if (warp == 0) {
+    // an infinite logit: the sum is infinite too
+    const float log_s = m == INFINITY ? 0.f : logf(s);
     float sum = 0.f;
     for (int k = lane; k < top; k += 32) {
       const int i = l.index[base + k];
-      if (i >= 0) sum += l.p[base + k] * (log_s - (row[i] - m) * inv_tau);
+      const float p = l.p[base + k];
+      if (i >= 0 && !(p == 0.f)) sum += p * (log_s - (row[i] - m) * inv_tau);
     }
     sum = warp_sum(sum);
     if (lane == 0) loss[t] = tau * tau * (l.ent[t] + sum);
@@ -488,27 +506,31 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, const LossRows& 
   if (!grad) return;
   const float scale = (weights != nullptr ? weights[t] : 1.f / static_cast<float>(n)) * tau;
   __syncthreads();
-  for (int v = threadIdx.x; v < V; v += kThreads) {
+#pragma unroll 8
+  for (int v = threadIdx.x; v < V; v += THREADS) {
     const float dz = scale * (expf((row[v] - m) * inv_tau) / s);
     // below 2^-109 the products on the tensor cores do not take a value: 0
     row[v] = fabsf(dz) < 1.5407439555e-33f ? 0.f : dz;
   }
   __syncthreads();
-  if (threadIdx.x == 0)
-    for (int k = 0; k < top; ++k) {
-      const int i = l.index[base + k];
-      if (i >= 0) row[i] -= scale * l.p[base + k];
-    }
+  for (int k = threadIdx.x; k < top; k += THREADS) {  // the first of every index
+    const int i = l.index[base + k];
+    if (i < 0 || (k > 0 && l.index[base + k - 1] == i)) continue;
+    float all = l.p[base + k];
+    for (int q = k + 1; q < top && l.index[base + q] == i; ++q) all += l.p[base + q];
+    row[i] -= scale * all;
+  }
 }
 
-__global__ void __launch_bounds__(kThreads)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
     loss_rows_kernel(float* __restrict__ z, LossRows l, long long first, int V, int top,
                      float inv_tau, float tau, const float* __restrict__ weights, bool grad,
                      float* __restrict__ loss, bool last, long long T, float* __restrict__ total) {
   pdl_wait();
   pdl_trigger();
-  loss_row(z, l, first, V, top, inv_tau, tau, weights, grad, loss);
-  if (last) total_behind(l, loss, weights, T, total);
+  loss_row<THREADS>(z, l, first, V, top, inv_tau, tau, weights, grad, loss);
+  if (last) total_behind<THREADS>(l, loss, weights, T, total);
 }
 
 // out[c][r] = in[r][c], in [rows][cols].
@@ -531,22 +553,31 @@ __global__ void __launch_bounds__(kThreads)
       out[static_cast<long long>(c0 + i) * rows + r0 + tx] = tile[tx][i];
 }
 
-// dx of the block's rows to their tokens, a warp per row.
+// dx of the block's rows, the sum of `slices` products (the first alone where the
+// product's flag `whole` says that the CUDA cores made it), to their tokens.
 __global__ void __launch_bounds__(kThreads)
-    loss_scatter_kernel(const float* __restrict__ rows, LossRows l, long long first,
-                        long long block, int d, float* __restrict__ dx) {
+    loss_scatter_kernel(const float* __restrict__ rows, int slices, const int* __restrict__ whole,
+                        LossRows l, long long first, long long block, int d,
+                        float* __restrict__ dx) {
   pdl_wait();
   pdl_trigger();
-  const long long r = blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
-  if (r >= block || first + r >= *l.count) return;
+  const long long r = blockIdx.x;
+  const int c = blockIdx.y * kThreads + threadIdx.x;
+  if (first + r >= *l.count || c >= d) return;
   const long long t = l.token[first + r];
-  for (int c = threadIdx.x % 32; c < d; c += 32) dx[t * d + c] = rows[r * d + c];
+  if (slices > 1 && *whole != 0) slices = 1;
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxFp32Slices; ++i)
+    if (i < slices) v += rows[(i * block + r) * d + c];
+  dx[t * d + c] = v;
 }
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 long long round64(long long n) { return (n + 63) / 64 * 64; }
 
 constexpr size_t kBlockBytes = size_t{1} << 31;  // of a block's terms
+constexpr size_t kCutBytes = size_t{64} << 20;  // of fp32 dx's slices
 constexpr long long kFewTokens = 64;
 
 // Elements between rows of d features as TMA operands (16-byte multiples).
@@ -591,6 +622,10 @@ struct Plan {
     acc = take(want_dw && a.is_bf16 && blocks > 1 ? 4 * static_cast<size_t>(a.V) * a.d : 0);
     cut = take(a.is_bf16 && ((want_dx && loss_cuts(a.V)) || (want_dw && loss_cuts(block)))
                    ? loss_cut_bytes()
+               : !a.is_bf16 && want_dx
+                   ? std::max(4 * static_cast<size_t>(block) * a.d,
+                              std::min(kCutBytes,
+                                       4 * kMaxFp32Slices * static_cast<size_t>(block) * a.d))
                    : 0);
     turned = take(want_dw && !a.is_bf16 ? 4 * static_cast<size_t>(block) * a.V : 0);
     scratch = take(a.is_bf16 ? 0 : fp32_scratch(a, want_dx, want_dw));
@@ -604,7 +639,7 @@ struct Plan {
     size_t most = linear_split_scratch_up_to(g);
     if (want_dx) {
       g.N = a.d, g.K = a.V, g.b_mn = true;
-      most = std::max(most, linear_split_scratch_up_to(g));
+      most = std::max(most, linear_split_scratch(g));
     }
     if (want_dw) {  // K is the number of rows
       g.M = a.V, g.N = a.d, g.K = static_cast<int>(block), g.b_mn = true;
@@ -750,8 +785,10 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
   float* z = reinterpret_cast<float*>(ws + plan.terms);
   float* zt = reinterpret_cast<float*>(ws + plan.turned);
   void* scratch = ws + plan.scratch;
+  float* out = reinterpret_cast<float*>(ws + plan.cut);
   const bool grad = a.dx != nullptr || a.dW != nullptr;
   cudaError_t e;
+  bool ready = false;  // W's planes are in the scratch
   for (long long first = 0; first < a.T; first += plan.block) {
     const long long rows = std::min(plan.block, a.T - first);
     float* xb = xg + first * a.d;
@@ -760,14 +797,42 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
     g.B = a.W;
     g.y = z;
     g.M = rows, g.N = a.V, g.K = a.d;
+    g.b_ready = ready;
     g.tag = "loss_logits";
     if ((e = linear_fp32(g, scratch, s)) != cudaSuccess) return e;
+    ready |= linear_split_pays(rows, a.V, a.d);
     e = launched("loss_rows", s, [&] {
-      return launch_pdl(loss_rows_kernel, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, s,
-                        z, l, first, a.V, a.top, 1.f / a.tau, a.tau, a.weights, grad, a.loss,
+      // long rows: 512 threads each (333 rows of 30001: ROWS_A -> ROWS_B us)
+      const bool wide = a.V > 8192;
+      return launch_pdl(wide ? loss_rows_kernel<512> : loss_rows_kernel<kThreads>,
+                        dim3(static_cast<unsigned>(rows)), dim3(wide ? 512 : kThreads), 0, s, z,
+                        l, first, a.V, a.top, 1.f / a.tau, a.tau, a.weights, grad, a.loss,
                         first + rows >= a.T, a.T, a.total);
     });
     if (e != cudaSuccess) return e;
+    if (a.dx != nullptr) {
+      LinearProduct q;
+      q.A = z;
+      q.B = a.W;
+      q.b_mn = true;
+      q.slices = linear_split_slices(rows, a.d, a.V, kCutBytes);
+      q.b_ready = ready;
+      q.y = out;
+      q.M = rows, q.N = a.d, q.K = a.V;
+      q.tag = "loss_dx";
+      if ((e = linear_fp32(q, scratch, s)) != cudaSuccess) return e;
+      ready |= q.slices > 1 || linear_split_pays(rows, a.d, a.V);
+      e = launched("loss_scatter", s, [&] {
+        return launch_pdl(loss_scatter_kernel,
+                          dim3(static_cast<unsigned>(rows),
+                               static_cast<unsigned>((a.d + kThreads - 1) / kThreads)),
+                          dim3(kThreads), 0, s,
+                          static_cast<const float*>(out), q.slices,
+                          static_cast<const int*>(scratch), l, first, rows, a.d,
+                          static_cast<float*>(a.dx));
+      });
+      if (e != cudaSuccess) return e;
+    }
     if (a.dW != nullptr) {
       e = launched("loss_transpose", s, [&] {
         return launch_pdl(loss_transpose_kernel,
@@ -786,22 +851,7 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
       q.M = a.V, q.N = a.d, q.K = static_cast<int>(rows);
       q.tag = "loss_dw";
       if ((e = linear_fp32(q, scratch, s)) != cudaSuccess) return e;
-    }
-    if (a.dx != nullptr) {  // over the block's rows of x, which are not needed any more
-      LinearProduct q;
-      q.A = z;
-      q.B = a.W;
-      q.b_mn = true;
-      q.y = xb;
-      q.M = rows, q.N = a.d, q.K = a.V;
-      q.tag = "loss_dx";
-      if ((e = linear_fp32(q, scratch, s)) != cudaSuccess) return e;
-      e = launched("loss_scatter", s, [&] {
-        return launch_pdl(loss_scatter_kernel, dim3(warps_grid(rows)), dim3(kThreads), 0, s,
-                          static_cast<const float*>(xb), l, first, rows, a.d,
-                          static_cast<float*>(a.dx));
-      });
-      if (e != cudaSuccess) return e;
+      ready &= !linear_split_pays(a.V, a.d, q.K);  // else x's planes took their place
     }
   }
   return cudaSuccess;
