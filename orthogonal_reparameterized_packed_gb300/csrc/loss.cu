@@ -28,6 +28,7 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 256;
 constexpr int kOrderThreads = 1024;
+constexpr int kOrderDeep = 8;  // tokens of a thread in flight
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
@@ -150,11 +151,11 @@ __global__ void __launch_bounds__(32 * kEntryWarps)
 // pos[t] (0 or -1) -> the number of tokens before t that count, or -1; token its
 // inverse; the largest weight; the blocks' flags and the counter of finished CTAs
 // cleared.  For the cross entropy also the entries: the targets.  One CTA,
-// kOrderThreads tokens at a time.
+// kOrderThreads * kOrderDeep tokens at a time.
 __global__ void __launch_bounds__(kOrderThreads)
     loss_order_kernel(LossRows l, long long T, const float* __restrict__ weights, int blocks,
                       const void* targets, int index_bytes, int V, int* status) {
-  __shared__ int sums[32];
+  __shared__ int sums[kOrderDeep][32];
   __shared__ float largest[32];
   pdl_wait();
   pdl_trigger();
@@ -162,37 +163,47 @@ __global__ void __launch_bounds__(kOrderThreads)
   int before = 0;
   float most = 0.f;
   bool outside = false;
-  for (long long t0 = 0; t0 < T; t0 += kOrderThreads) {
-    const long long t = t0 + threadIdx.x;
-    bool on = false;
-    if (t < T) {
-      if (targets != nullptr) {
-        const long long i = index_at(targets, index_bytes, t);
-        outside |= i >= V;
-        on = i >= 0 && i < V;
-        l.index[t] = l.lead[t] = on ? static_cast<int>(i) : -1;
-        l.p[t] = 1.f;
-        l.ent[t] = 0.f;
-      } else {
-        on = l.pos[t] >= 0;
-      }
-    }
-    const unsigned mask = __ballot_sync(0xffffffffu, on);
-    if (lane == 0) sums[warp] = __popc(mask);
-    __syncthreads();
-    int mine = before, all = 0;
+  for (long long t0 = 0; t0 < T; t0 += kOrderThreads * kOrderDeep) {
+    bool on[kOrderDeep];
+    unsigned mask[kOrderDeep];
+    long long at[kOrderDeep];
 #pragma unroll
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) mine += sums[w];
-      all += sums[w];
+    for (int i = 0; i < kOrderDeep; ++i) {
+      const long long t = t0 + i * kOrderThreads + threadIdx.x;
+      at[i] = t >= T ? -1 : targets != nullptr ? index_at(targets, index_bytes, t) : l.pos[t];
     }
-    mine += __popc(mask & ((1u << lane) - 1));
-    if (t < T) l.pos[t] = on ? mine : -1;
-    if (on) {
-      l.token[mine] = static_cast<int>(t);
-      if (weights != nullptr) most = fmaxf(most, fabsf(weights[t]));
+#pragma unroll
+    for (int i = 0; i < kOrderDeep; ++i) {
+      const long long t = t0 + i * kOrderThreads + threadIdx.x;
+      on[i] = at[i] >= 0;
+      if (targets != nullptr) {
+        outside |= at[i] >= V;
+        on[i] &= at[i] < V;
+        if (t < T) {
+          l.index[t] = l.lead[t] = on[i] ? static_cast<int>(at[i]) : -1;
+          l.p[t] = 1.f;
+          l.ent[t] = 0.f;
+        }
+      }
+      mask[i] = __ballot_sync(0xffffffffu, on[i]);
+      if (lane == 0) sums[i][warp] = __popc(mask[i]);
     }
-    before += all;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kOrderDeep; ++i) {
+      if (t0 + i * kOrderThreads >= T) break;
+      const long long t = t0 + i * kOrderThreads + threadIdx.x;
+      const int of_warp = sums[i][lane];
+      const int all = __reduce_add_sync(0xffffffffu, of_warp);
+      const int mine = before + __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0) +
+                       __popc(mask[i] & ((1u << lane) - 1));
+      if (t < T) l.pos[t] = on[i] ? mine : -1;
+      if (on[i]) {
+        l.token[mine] = static_cast<int>(t);
+        if (weights != nullptr) most = fmaxf(most, fabsf(weights[t]));
+      }
+      before += all;
+    }
     __syncthreads();
   }
   for (int b = threadIdx.x; b < blocks; b += kOrderThreads) l.again[b] = 0;
@@ -293,15 +304,13 @@ struct FinishArgs {
   float* total;
 };
 
-// total = sum over the tokens that count of w loss, in 64 bits, by one CTA.
+// total, from the parts (w loss of some rows, in 64 bits, in order), by one CTA.
 template <int THREADS>
-__device__ void sum_losses(const LossRows& l, const float* loss, const float* weights, long long T,
-                           float* total) {
+__device__ void sum_total(const LossRows& l, long long count, bool mean, float* total) {
   __shared__ double sums[THREADS / 32];
   double sum = 0.0;
 #pragma unroll 4
-  for (long long t = threadIdx.x; t < T; t += THREADS)
-    if (l.pos[t] >= 0) sum += (weights != nullptr ? weights[t] : 1.0) * __ldcg(loss + t);
+  for (long long i = threadIdx.x; i < count; i += THREADS) sum += __ldcg(l.totals + i);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = sum;
@@ -309,33 +318,34 @@ __device__ void sum_losses(const LossRows& l, const float* loss, const float* we
   if (threadIdx.x == 0) {
     sum = 0.0;
     for (int w = 0; w < THREADS / 32; ++w) sum += sums[w];
-    if (weights == nullptr) sum /= max(1, *l.count);
+    if (mean) sum /= max(1, *l.count);
     *total = static_cast<float>(sum);
   }
 }
 
-// Called by every CTA of the last kernel that writes losses: the one that comes last
-// sums them.
+// The same where this kernel wrote the parts, every CTA's by its thread 0: the CTA
+// that comes last adds them up.
 template <int THREADS>
-__device__ void total_behind(const LossRows& l, const float* loss, const float* weights,
-                             long long T, float* total) {
+__device__ void total_behind(const LossRows& l, long long count, bool mean, float* total) {
   __shared__ bool mine;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) mine = atomicAdd(l.done, 1) == static_cast<int>(gridDim.x) - 1;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    mine = atomicAdd(l.done, 1) == static_cast<int>(gridDim.x) - 1;
+  }
   __syncthreads();
   if (!mine) return;
   __threadfence();
-  sum_losses<THREADS>(l, loss, weights, T, total);
+  sum_total<THREADS>(l, count, mean, total);
 }
 
-// R rows per CTA, 8 or, for few rows, 1.  The parts of their sums (all threads), then a warp per row:
+// R rows per CTA, 4 or, for few rows, 1.  The parts of their sums (all threads), then a warp per row:
 // its loss, its factor, and in E the entries' terms e - p sum.  A row whose reference
 // does not fit sets its block's flag.  The second pass does this again where the flag
 // is set, and scales the rows of x for dW.
 template <int R>
 __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
   __shared__ float2 sums[kThreads / 32][R];
+  __shared__ double totals[R];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int count = *a.rows.count;
   const long long n = max(0ll, min(a.block, (a.direct ? a.T : count) - a.first));
@@ -346,6 +356,24 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
   const long long row = r0 + warp, r = a.first + row;  // of the first R warps
   const bool on = warp < R && row < n;
   if (!a.second || *again != 0) {
+    // what the row needs besides its statistics, first
+    long long t = 0, base = 0;
+    bool counts = false;
+    float weight = 0.f, ent = 0.f, ref = 0.f, p0 = 0.f, z0 = 0.f;
+    int i0 = -1;
+    if (on) {
+      t = a.direct ? r : a.rows.token[r];
+      base = t * a.top;
+      if (lane < a.top) {
+        i0 = a.rows.index[base + lane];
+        p0 = a.rows.p[base + lane];
+        z0 = i0 >= 0 ? a.rows.z[base + lane] : 0.f;
+      }
+      counts = !a.direct || a.rows.pos[t] >= 0;
+      ent = a.rows.ent[t];
+      if (counts) weight = a.weights != nullptr ? a.weights[t] : 1.f;
+      if (!own) ref = a.rows.ref[r];
+    }
     const int j = threadIdx.x % R;
     float m = -INFINITY, s = 0.f;
     const auto add = [&](float m2, float s2) {
@@ -377,17 +405,15 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) add(sums[w][warp % R].x, sums[w][warp % R].y);
     if (on) {
-      const float ref = own ? (m == -INFINITY ? 0.f : m * a.unit) : a.rows.ref[r];
+      if (own) ref = m == -INFINITY ? 0.f : m * a.unit;
       // an infinite logit: the sum is infinite too
       const float log_s = m == INFINITY ? 0.f : log2f(s);
-      const long long t = a.direct ? r : a.rows.token[r];
-      const bool counts = !a.direct || a.rows.pos[t] >= 0;
-      const long long base = t * a.top;
       float sum = 0.f;
       for (int k = lane; k < a.top; k += 32) {
-        const int i = a.rows.index[base + k];
+        const int i = k == lane ? i0 : a.rows.index[base + k];
         if (i < 0) continue;
-        const float over = fmaf(a.rows.z[base + k], a.unit, -ref), p = a.rows.p[base + k];
+        const float p = k == lane ? p0 : a.rows.p[base + k];
+        const float over = fmaf(k == lane ? z0 : a.rows.z[base + k], a.unit, -ref);
         if (!(p == 0.f)) sum += p * (log_s - over);
         if (!own && (k == 0 || a.rows.index[base + k - 1] != i)) {
           float all = p;
@@ -398,11 +424,12 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
       }
       sum = warp_sum(sum);
       if (lane == 0) {
-        a.loss[t] =
-            counts ? a.tau * a.tau * (a.rows.ent[t] + 0.69314718056f * sum) : 0.f;
+        const float loss = counts ? a.tau * a.tau * (ent + 0.69314718056f * sum) : 0.f;
+        a.loss[t] = loss;
+        totals[warp] = counts ? static_cast<double>(weight) * loss : 0.0;
         if (!own) {
           a.rows.scale[r] = make_float2(
-              a.tau / s, a.weights != nullptr ? a.weights[t] : 1.f / static_cast<float>(count));
+              a.tau / s, a.weights != nullptr ? weight : 1.f / static_cast<float>(count));
           const float above = m * a.unit - ref;
           if (!a.second && (above > kFits || above < -2.f * kAbove)) {
             a.rows.ref[r] = m * a.unit;
@@ -412,6 +439,14 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
       }
     }
   }
+  if (!a.second || *again != 0) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      double sum = 0.0;
+      for (int i = 0; i < min(static_cast<long long>(R), n - r0); ++i) sum += totals[i];
+      a.rows.totals[(a.first + r0) / R] = sum;
+    }
+  }
   if (!a.second || a.x == nullptr) return;
   __syncthreads();
   // the rows of x, all threads
@@ -419,30 +454,46 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
   const int pieces = vec ? a.d / 8 : a.d;
   const int rows = static_cast<int>(min(static_cast<long long>(R), n - r0));
   const float most = *a.rows.most;
-  for (int i = 0; i < rows; ++i) {
-    const float2 f = a.rows.scale[a.first + r0 + i];
-    const float by = f.x * (f.y / most);
-    bf16* x = a.x + (r0 + i) * a.ldx;
-    for (int c = threadIdx.x; c < pieces; c += kThreads) {
-      if (vec) {
-        Pack<bf16, 8>* at = reinterpret_cast<Pack<bf16, 8>*>(x) + c;
-        Pack<bf16, 8> v = *at;
+  float by[R];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v.x[k] = __float2bfloat16_rn(__bfloat162float(v.x[k]) * by);
-        *at = v;
-      } else {
-        x[c] = __float2bfloat16_rn(__bfloat162float(x[c]) * by);
+  for (int i = 0; i < R; ++i) {
+    const float2 f = i < rows ? a.rows.scale[a.first + r0 + i] : make_float2(0.f, 0.f);
+    by[i] = f.x * (f.y / most);
+  }
+  bf16* x = a.x + r0 * a.ldx;
+  for (int c = threadIdx.x; c < pieces; c += kThreads) {
+    if (vec) {
+      Pack<bf16, 8> v[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i < rows) v[i] = *reinterpret_cast<const Pack<bf16, 8>*>(x + i * a.ldx + 8 * c);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[i].x[k] = __float2bfloat16_rn(__bfloat162float(v[i].x[k]) * by[i]);
+        if (i < rows) *reinterpret_cast<Pack<bf16, 8>*>(x + i * a.ldx + 8 * c) = v[i];
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i < rows) x[i * a.ldx + c] = __float2bfloat16_rn(__bfloat162float(x[i * a.ldx + c]) * by[i]);
     }
   }
 }
 
 template <int R>
-__global__ void __launch_bounds__(kThreads) loss_finish_kernel(const FinishArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) loss_finish_kernel(const FinishArgs a) {
   pdl_wait();
   pdl_trigger();
   finish_rows<R>(a);
-  if (a.last) total_behind<kThreads>(a.rows, a.loss, a.weights, a.T, a.total);
+  if (!a.last) return;
+  const long long count = ((a.direct ? a.T : *a.rows.count) + R - 1) / R;
+  const bool mean = a.weights == nullptr;
+  if (!a.second || a.rows.again[a.first / a.block] != 0)
+    total_behind<kThreads>(a.rows, count, mean, a.total);
+  else if (blockIdx.x == gridDim.x - 1)  // the parts are the last kernel's
+    sum_total<kThreads>(a.rows, count, mean, a.total);
 }
 
 // A CTA per row of the block: its loss from the fp32 logits z, and in
@@ -501,7 +552,11 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, const LossRows& 
       if (i >= 0 && !(p == 0.f)) sum += p * (log_s - (row[i] - m) * inv_tau);
     }
     sum = warp_sum(sum);
-    if (lane == 0) loss[t] = tau * tau * (l.ent[t] + sum);
+    if (lane == 0) {  // thread 0
+      const float of_row = tau * tau * (l.ent[t] + sum);
+      loss[t] = of_row;
+      l.totals[r] = (weights != nullptr ? weights[t] : 1.0) * of_row;
+    }
   }
   if (!grad) return;
   const float scale = (weights != nullptr ? weights[t] : 1.f / static_cast<float>(n)) * tau;
@@ -526,11 +581,11 @@ template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
     loss_rows_kernel(float* __restrict__ z, LossRows l, long long first, int V, int top,
                      float inv_tau, float tau, const float* __restrict__ weights, bool grad,
-                     float* __restrict__ loss, bool last, long long T, float* __restrict__ total) {
+                     float* __restrict__ loss, bool last, float* __restrict__ total) {
   pdl_wait();
   pdl_trigger();
   loss_row<THREADS>(z, l, first, V, top, inv_tau, tau, weights, grad, loss);
-  if (last) total_behind<THREADS>(l, loss, weights, T, total);
+  if (last) total_behind<THREADS>(l, *l.count, weights == nullptr, total);
 }
 
 // out[c][r] = in[r][c], in [rows][cols].
@@ -588,7 +643,7 @@ struct Plan {
   long long block;  // rows taken at a time, a multiple of 64
   int blocks;
   long long ldx, lde, ldp;
-  size_t meta = 0, again, pos, token, index, p, ent, lead, z, ref, scale, xg, wp, terms, part, acc,
+  size_t meta = 0, again, pos, token, index, p, ent, lead, z, totals, ref, scale, xg, wp, terms, part, acc,
          cut, turned, scratch, total;
   Plan(const LossArgs& a, bool want_dx, bool want_dw) {
     const size_t T = static_cast<size_t>(a.T), es = a.is_bf16 ? 2 : 4;
@@ -613,6 +668,7 @@ struct Plan {
     ent = take(4 * T);
     lead = take(4 * T);
     z = take(4 * T * a.top);
+    totals = take(8 * T);
     ref = take(4 * T);
     scale = take(8 * T);
     xg = take(es * static_cast<size_t>(round64(a.T)) * ldx);
@@ -765,8 +821,8 @@ cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, cha
       e = launched("loss_finish", s, [&] {
         return few ? launch_pdl(loss_finish_kernel<1>, dim3(static_cast<unsigned>(plan.block)),
                                 dim3(kThreads), 0, s, f)
-                   : launch_pdl(loss_finish_kernel<8>,
-                                dim3(static_cast<unsigned>((plan.block + 7) / 8)), dim3(kThreads),
+                   : launch_pdl(loss_finish_kernel<4>,
+                                dim3(static_cast<unsigned>((plan.block + 3) / 4)), dim3(kThreads),
                                 0, s, f);
       });
       if (e != cudaSuccess) return e;
@@ -807,7 +863,7 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
       return launch_pdl(wide ? loss_rows_kernel<512> : loss_rows_kernel<kThreads>,
                         dim3(static_cast<unsigned>(rows)), dim3(wide ? 512 : kThreads), 0, s, z,
                         l, first, a.V, a.top, 1.f / a.tau, a.tau, a.weights, grad, a.loss,
-                        first + rows >= a.T, a.T, a.total);
+                        first + rows >= a.T, a.total);
     });
     if (e != cudaSuccess) return e;
     if (a.dx != nullptr) {
@@ -891,6 +947,7 @@ cudaError_t head_loss(const LossArgs& a, void* scratch, cudaStream_t s) {
   l.ent = reinterpret_cast<float*>(ws + plan.ent);
   l.lead = reinterpret_cast<int*>(ws + plan.lead);
   l.z = reinterpret_cast<float*>(ws + plan.z);
+  l.totals = reinterpret_cast<double*>(ws + plan.totals);
   l.ref = reinterpret_cast<float*>(ws + plan.ref);
   l.scale = reinterpret_cast<float2*>(ws + plan.scale);
   l.done = reinterpret_cast<int*>(ws + plan.meta + 8);

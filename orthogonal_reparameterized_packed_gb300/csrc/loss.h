@@ -45,6 +45,7 @@ struct LossRows {
   float* p;      // [T][top]
   float* ent;    // [T] by token: sum_k p log p
   int* lead;     // [T] by token: the index of its largest p
+  double* totals;  // [T]: w loss, summed over the rows of a CTA
   float* z;      // [T][top] by token: the entries' logits
   float* ref;    // [T] by row: reference of the exponentials, in units of log 2
   float2* scale;  // [T] by row: tau / (sum of its exponentials), weight

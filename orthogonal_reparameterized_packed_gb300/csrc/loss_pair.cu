@@ -227,6 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first_unit = static_cast<int>(cluster_id_x());
   const int step = static_cast<int>(cluster_count_x());
 
+  if (KIND == kLogits && p.only != nullptr) {  // the same for every CTA, before anything is set up
+    pdl_wait();
+    if (*p.only == 0) return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full_bar[s], 1);
@@ -263,7 +267,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int m_pairs = static_cast<int>((M + 2 * BM - 1) / (2 * BM));
   const int k_steps = static_cast<int>(((KIND == kDw ? n : p.K) + BK - 1) / BK);
   int units = m_pairs * p.n_tiles;
-  if (p.only != nullptr && *p.only == 0) units = 0;
   if (KIND == kDw && n == 0 && p.first > 0) units = 0;  // the block before was the last
   const bool products = k_steps > 0;  // dW without a row is 0
   if (threadIdx.x == 0) {
