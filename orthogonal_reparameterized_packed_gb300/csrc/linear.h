@@ -11,14 +11,18 @@ namespace poetx {
 
 // What linear_stream leaves instead of y and z for the head's losses (loss.h), 128
 // outputs (vocabulary entries) at a time: part[n / 128][token] = (their largest z,
-// the sum of 2^((z - largest) unit)), and the z at a token's `top` ascending indices.
+// the sum of 2^((z - largest) unit)), and the z at a token's `top` ascending indices
+// or, where targets are given, at its target.  *done = 0 for the kernel behind.
 struct LossColumns {
   float2* part = nullptr;
   long long ldp = 0;
   float unit = 0.f;
   const int* index = nullptr;
+  const void* targets = nullptr;  // target_bytes each
+  int target_bytes = 8;
   float* z = nullptr;
   int top = 0;
+  int* done = nullptr;
 };
 
 struct LinearProduct {

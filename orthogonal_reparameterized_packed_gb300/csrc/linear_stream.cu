@@ -113,7 +113,17 @@ __device__ __forceinline__ void loss_columns(const LossColumns& p, const float (
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) p.part[n0 / BM * p.ldp + token] = make_float2(top, sum);
+  const auto take = [&](int c, long long to) {
+    if (c >> 2 == lane) p.z[to] = (c & 2) ? ((c & 1) ? v[3] : v[2]) : ((c & 1) ? v[1] : v[0]);
+  };
   // the token's entries among these features, the same for the whole warp
+  if (p.targets != nullptr) {
+    const long long c = (p.target_bytes == 8 ? static_cast<const long long*>(p.targets)[token]
+                                             : static_cast<const int*>(p.targets)[token]) -
+                        n0;
+    if (c >= 0 && c < BM) take(static_cast<int>(c), token);
+    return;
+  }
   const int* index = p.index + token * p.top;
   int lo = 0, hi = p.top;
   while (lo < hi) {
@@ -126,10 +136,7 @@ __device__ __forceinline__ void loss_columns(const LossColumns& p, const float (
   for (; lo < p.top; ++lo) {
     const int c = index[lo] - n0;
     if (c >= BM) break;
-    if (c >> 2 == lane) {
-      const float z = (c & 2) ? ((c & 1) ? v[3] : v[2]) : ((c & 1) ? v[1] : v[0]);
-      p.z[token * p.top + lo] = z;
-    }
+    take(c, token * p.top + lo);
   }
 }
 
@@ -238,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_trigger();
+  if (LOSS && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) *p.loss.done = 0;
 
   // In both roles the whole warp runs the loop and one elected lane issues, so
   // that addresses and descriptors stay in uniform registers.

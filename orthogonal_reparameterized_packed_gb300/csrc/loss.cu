@@ -299,14 +299,18 @@ struct FinishArgs {
   bf16* x;  // the block's rows; null: no dW
   long long ldx;
   bool second, last;  // last: of the call; total is taken behind it
-  bool direct;        // the rows are the tokens, also those that do not count
+  bool direct;        // the rows are the tokens, also those that do not count,
+  const void* targets;  // and (not null) the entries are the targets, not looked over yet
+  int target_bytes, V;
+  int* status;
   long long T;
   float* total;
 };
 
-// total, from the parts (w loss of some rows, in 64 bits, in order), by one CTA.
+// total, from the parts (w loss of some rows, in 64 bits, in order) divided by `by`,
+// by one CTA.
 template <int THREADS>
-__device__ void sum_total(const LossRows& l, long long count, bool mean, float* total) {
+__device__ void sum_total(const LossRows& l, long long count, float by, float* total) {
   __shared__ double sums[THREADS / 32];
   double sum = 0.0;
 #pragma unroll 4
@@ -318,15 +322,14 @@ __device__ void sum_total(const LossRows& l, long long count, bool mean, float* 
   if (threadIdx.x == 0) {
     sum = 0.0;
     for (int w = 0; w < THREADS / 32; ++w) sum += sums[w];
-    if (mean) sum /= max(1, *l.count);
-    *total = static_cast<float>(sum);
+    *total = static_cast<float>(sum / by);
   }
 }
 
 // The same where this kernel wrote the parts, every CTA's by its thread 0: the CTA
 // that comes last adds them up.
 template <int THREADS>
-__device__ void total_behind(const LossRows& l, long long count, bool mean, float* total) {
+__device__ void total_behind(const LossRows& l, long long count, float by, float* total) {
   __shared__ bool mine;
   if (threadIdx.x == 0) {
     __threadfence();
@@ -335,7 +338,7 @@ __device__ void total_behind(const LossRows& l, long long count, bool mean, floa
   __syncthreads();
   if (!mine) return;
   __threadfence();
-  sum_total<THREADS>(l, count, mean, total);
+  sum_total<THREADS>(l, count, by, total);
 }
 
 // R rows per CTA, 4 or, for few rows, 1.  The parts of their sums (all threads), then a warp per row:
@@ -347,7 +350,7 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
   __shared__ float2 sums[kThreads / 32][R];
   __shared__ double totals[R];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int count = *a.rows.count;
+  const int count = a.targets != nullptr ? 0 : *a.rows.count;
   const long long n = max(0ll, min(a.block, (a.direct ? a.T : count) - a.first));
   const long long r0 = blockIdx.x * static_cast<long long>(R);
   if (r0 >= n) return;
@@ -364,13 +367,24 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
     if (on) {
       t = a.direct ? r : a.rows.token[r];
       base = t * a.top;
-      if (lane < a.top) {
-        i0 = a.rows.index[base + lane];
-        p0 = a.rows.p[base + lane];
-        z0 = i0 >= 0 ? a.rows.z[base + lane] : 0.f;
+      if (a.targets != nullptr) {
+        const long long i = index_at(a.targets, a.target_bytes, t);
+        counts = i >= 0 && i < a.V;
+        if (i >= a.V && lane == 0) atomicCAS(a.status, 0, static_cast<int>(POETX_ERR_INVALID_ARG));
+        if (lane == 0 && counts) {
+          i0 = static_cast<int>(i);
+          p0 = 1.f;
+          z0 = a.rows.z[t];
+        }
+      } else {
+        if (lane < a.top) {
+          i0 = a.rows.index[base + lane];
+          p0 = a.rows.p[base + lane];
+          z0 = i0 >= 0 ? a.rows.z[base + lane] : 0.f;
+        }
+        counts = !a.direct || a.rows.pos[t] >= 0;
+        ent = a.rows.ent[t];
       }
-      counts = !a.direct || a.rows.pos[t] >= 0;
-      ent = a.rows.ent[t];
       if (counts) weight = a.weights != nullptr ? a.weights[t] : 1.f;
       if (!own) ref = a.rows.ref[r];
     }
@@ -483,17 +497,25 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
 }
 
 template <int R>
-__global__ void __launch_bounds__(kThreads, 6) loss_finish_kernel(const FinishArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) loss_finish_kernel(const FinishArgs a) {
   pdl_wait();
   pdl_trigger();
   finish_rows<R>(a);
   if (!a.last) return;
-  const long long count = ((a.direct ? a.T : *a.rows.count) + R - 1) / R;
-  const bool mean = a.weights == nullptr;
+  long long tokens;  // that count
+  if (a.targets != nullptr) {  // T is kFewTokens at most
+    long long i = -1;
+    if (threadIdx.x < a.T) i = index_at(a.targets, a.target_bytes, threadIdx.x);
+    tokens = __syncthreads_count(i >= 0 && i < a.V);
+  } else {
+    tokens = *a.rows.count;
+  }
+  const long long count = ((a.direct ? a.T : tokens) + R - 1) / R;
+  const float by = a.weights == nullptr ? static_cast<float>(max(1ll, tokens)) : 1.f;
   if (!a.second || a.rows.again[a.first / a.block] != 0)
-    total_behind<kThreads>(a.rows, count, mean, a.total);
+    total_behind<kThreads>(a.rows, count, by, a.total);
   else if (blockIdx.x == gridDim.x - 1)  // the parts are the last kernel's
-    sum_total<kThreads>(a.rows, count, mean, a.total);
+    sum_total<kThreads>(a.rows, count, by, a.total);
 }
 
 // A CTA per row of the block: its loss from the fp32 logits z, and in
@@ -585,7 +607,9 @@ __global__ void __launch_bounds__(THREADS)
   pdl_wait();
   pdl_trigger();
   loss_row<THREADS>(z, l, first, V, top, inv_tau, tau, weights, grad, loss);
-  if (last) total_behind<THREADS>(l, *l.count, weights == nullptr, total);
+  if (last)
+    total_behind<THREADS>(l, *l.count,
+                          weights == nullptr ? static_cast<float>(max(1, *l.count)) : 1.f, total);
 }
 
 // out[c][r] = in[r][c], in [rows][cols].
@@ -740,8 +764,11 @@ cudaError_t few_logits(const LossArgs& a, const LossProducts& p, cudaStream_t s)
   c.ldp = p.ldp;
   c.unit = p.unit;
   c.index = p.rows.index;
+  c.targets = a.top_logits == nullptr ? a.indices : nullptr;
+  c.target_bytes = a.index_bytes;
   c.z = p.rows.z;
   c.top = a.top;
+  c.done = p.rows.done;
   LinearProduct g;
   g.A = a.x;
   g.B = a.W;
@@ -789,6 +816,10 @@ cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, cha
   g.rows = l;
   FinishArgs f = {};
   f.direct = direct;
+  f.targets = direct && a.top_logits == nullptr ? a.indices : nullptr;
+  f.target_bytes = a.index_bytes;
+  f.V = a.V;
+  f.status = device_status_ptr();
   f.rows = l;
   f.part = g.part;
   f.ldp = g.ldp;
@@ -951,7 +982,7 @@ cudaError_t head_loss(const LossArgs& a, void* scratch, cudaStream_t s) {
   l.ref = reinterpret_cast<float*>(ws + plan.ref);
   l.scale = reinterpret_cast<float2*>(ws + plan.scale);
   l.done = reinterpret_cast<int*>(ws + plan.meta + 8);
-  cudaError_t e;
+  cudaError_t e = cudaSuccess;
   const bool ce = a.top_logits == nullptr;
   if (!ce) {
     e = launched("loss_entries", s, [&] {
@@ -962,13 +993,16 @@ cudaError_t head_loss(const LossArgs& a, void* scratch, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
   }
-  e = launched("loss_order", s, [&] {
-    return launch_pdl(loss_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, l, a.T, a.weights,
-                      plan.blocks, ce ? a.indices : nullptr, a.index_bytes, a.V,
-                      device_status_ptr());
-  });
-  if (e != cudaSuccess) return e;
-  if (few_form(a))
+  const bool direct = few_form(a);
+  if (!direct || !ce) {  // else the two kernels of few_logits take the targets themselves
+    e = launched("loss_order", s, [&] {
+      return launch_pdl(loss_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, l, a.T, a.weights,
+                        plan.blocks, ce ? a.indices : nullptr, a.index_bytes, a.V,
+                        device_status_ptr());
+    });
+    if (e != cudaSuccess) return e;
+  }
+  if (direct)
     e = cudaSuccess;
   else if (a.is_bf16)
     e = a.d % 8 == 0 ? run_gather<bf16, 8>(a, plan, l, ws, s) : run_gather<bf16, 1>(a, plan, l, ws, s);
