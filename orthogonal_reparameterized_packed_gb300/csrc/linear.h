@@ -42,7 +42,10 @@ struct LinearProduct {
   const int* all_rows = nullptr;
   const int* row_flags = nullptr;
   int segs = 0;
-  // linear_fp32: K in `slices` pieces whose products are apart, piece i's in y + i M N
+  // fp32: elements between A's rows and between y's (z's, residual's), 0: K and N.  Up
+  // to three of y's elements behind a row's last are written.
+  long long pitch_a = 0, pitch_y = 0;
+  // linear_fp32: K in `slices` pieces whose products are apart, piece i's in y + i M pitch_y
   // (no bias, residual or activation); linear_fp32_slices says how many pay
   int slices = 1;
   // linear_split: the last product on this scratch had the same array B
@@ -57,8 +60,9 @@ cudaError_t linear_pair(const LinearProduct& g, cudaStream_t s);
 // For few tokens: the weight streamed once, K split over a cluster (linear_stream.cu).
 cudaError_t linear_stream(const LinearProduct& g, cudaStream_t s);
 
-// In fp32 on the CUDA cores (linear_simt.cu): A, y, z, residual contiguous, B
-// [N][K] or, b_mn, [K][N] contiguous; lda, ldb and ld are not used.
+// In fp32 on the CUDA cores (linear_simt.cu): A, y, z, residual contiguous unless
+// pitch_a, pitch_y say otherwise, B [N][K] or, b_mn, [K][N] contiguous; lda, ldb and
+// ld are not used.
 cudaError_t linear_simt(const LinearProduct& g, cudaStream_t s);
 
 // In fp32 on the tensor cores, as six bf16 products (linear_split.cu); layouts
@@ -77,7 +81,7 @@ cudaError_t linear_fp32(const LinearProduct& g, void* scratch, cudaStream_t s);
 // Pieces of K, 2 to kMaxFp32Slices with outputs of at most most_bytes, where these
 // are faster than linear_fp32 on the whole of K: a product of few tiles and a long K.
 // Else 1.
-constexpr int kMaxFp32Slices = 8;
+constexpr int kMaxFp32Slices = 16;
 int linear_split_slices(long long M, int N, int K, size_t most_bytes);
 
 }  // namespace poetx

@@ -12,23 +12,26 @@ struct Fp32Epilogue {
   const float* residual;
   float* y;
   float* z;
+  long long ld;  // between rows
   int N, act;
   bool vec_n;  // 16-byte rows
 };
 
 // Of the product's rows from m_first on.
 Fp32Epilogue fp32_epilogue(const LinearProduct& g, long long m_first) {
+  const long long ld = g.pitch_y > 0 ? g.pitch_y : g.N;
   auto at = [&](const void* base) {
-    return static_cast<const float*>(base) + (base != nullptr ? m_first * g.N : 0);
+    return static_cast<const float*>(base) + (base != nullptr ? m_first * ld : 0);
   };
   Fp32Epilogue e;
+  e.ld = ld;
   e.bias = g.bias;
   e.residual = at(g.residual);
   e.y = const_cast<float*>(at(g.y));
   e.z = const_cast<float*>(at(g.z));
   e.N = g.N;
   e.act = g.act;
-  e.vec_n = g.N % 4 == 0;
+  e.vec_n = ld % 4 == 0;
   return e;
 }
 
@@ -51,8 +54,8 @@ __device__ __forceinline__ void apply4(int act, float (&v)[4]) {
 // Outputs (m, n .. n + 3), n < N a multiple of 4.
 __device__ __forceinline__ void finish4(const Fp32Epilogue& p, long long m, int n, float4 acc) {
   float v[4] = {acc.x, acc.y, acc.z, acc.w};
-  const long long at = m * p.N + n;
-  if (p.vec_n) {  // all four are inside
+  const long long at = m * p.ld + n;
+  if (p.vec_n) {  // all four are inside the pitch (a bias only comes without one)
     if (p.bias != nullptr) {
       const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + n));
       v[0] += b.x, v[1] += b.y, v[2] += b.z, v[3] += b.w;

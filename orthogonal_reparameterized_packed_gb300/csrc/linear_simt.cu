@@ -36,7 +36,7 @@ struct SimtArgs {
   const float* A;
   const float* B;
   Fp32Epilogue epi;
-  long long M;
+  long long M, lda;
   int N, K, splits, k_slice;
   const int* all_rows;   // null: every row; otherwise every row where it is not 0,
   const int* row_flags;  // and else the rows with one of their `segs` flags set
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
       int row, quad;
       piece<TM, KQ>(e, row, quad);
       if (QA % kThreads == 0 || e < QA)
-        ra[q] = load4(p.A, m0 + row, p.M, k + quad * 4, k1, p.K, p.vec_a);
+        ra[q] = load4(p.A, m0 + row, p.M, k + quad * 4, k1, p.lda, p.vec_a);
     }
 #pragma unroll
     for (int q = 0; q < NB; ++q) {
@@ -351,7 +351,8 @@ cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, do
     ready[dev].store(true, std::memory_order_relaxed);
   }
   SimtArgs p;
-  p.A = static_cast<const float*>(g.A) + m_first * g.K;
+  p.lda = g.pitch_a > 0 ? g.pitch_a : g.K;
+  p.A = static_cast<const float*>(g.A) + m_first * p.lda;
   p.B = static_cast<const float*>(g.B);
   p.epi = fp32_epilogue(g, m_first);
   p.M = rows;
@@ -360,7 +361,7 @@ cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, do
   p.all_rows = g.all_rows;
   p.row_flags = g.row_flags != nullptr ? g.row_flags + m_first * g.segs : nullptr;
   p.segs = g.segs;
-  p.vec_a = g.K % 4 == 0;
+  p.vec_a = p.lda % 4 == 0;
   p.vec_b = (B_KN ? g.N : g.K) % 4 == 0;
   const int n_tiles = (g.N + kTN - 1) / kTN;
   const long long m_tiles = (rows + S::TM - 1) / S::TM;

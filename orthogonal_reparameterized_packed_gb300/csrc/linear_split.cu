@@ -383,7 +383,7 @@ struct SplitOperand {
   const float* in;
   bf16* planes;
   int* flag;
-  long long rows, plane_rows, pitch;
+  long long rows, ld, plane_rows, pitch;
   int cols, segs;
 };
 
@@ -405,8 +405,8 @@ __global__ void __launch_bounds__(kSplitThreads)
     const long long r = at / o.segs;
     const int c0 = static_cast<int>(at - r * o.segs) * kSegment;
     const int c1 = min(o.cols, c0 + kSegment);
-    const float* in = o.in + r * o.cols;
-    const bool vec = o.cols % 4 == 0;
+    const float* in = o.in + r * o.ld;
+    const bool vec = o.ld % 4 == 0;
     bool bad = false;
 #pragma unroll 4
     for (int c = c0 + lane * 4; c < c1; c += 128) {
@@ -415,6 +415,11 @@ __global__ void __launch_bounds__(kSplitThreads)
         if (vec) {
           const float4 q = *reinterpret_cast<const float4*>(in + c);
           v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+          if (c + 3 >= o.cols) {  // what lies between the rows is nothing
+#pragma unroll
+            for (int j = 1; j < 4; ++j)
+              if (c + j >= o.cols) v[j] = 0.f;
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -588,7 +593,7 @@ bool linear_split_pays(long long M, int N, int K, int slices) {
 }
 
 // A slice has at least four K steps, none is empty.  333 x 30001 -> 768 (6 tiles of
-// 256, 12 of 128, 469 steps): on the CUDA cores 459 us, SLICED us in 6 slices.
+// 256, 12 of 128, 469 steps): on the CUDA cores 459 us, in 8 slices 103, in 12 90.
 int linear_split_slices(long long M, int N, int K, size_t most_bytes) {
   const int steps = (K + BK - 1) / BK;
   int best = 1;
@@ -647,6 +652,7 @@ cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) 
   a.flag = row_flags;
   a.rows = a.plane_rows = g.M;
   a.cols = g.K;
+  a.ld = g.pitch_a > 0 ? g.pitch_a : g.K;
   a.segs = segments(a.cols);
   a.pitch = pitch64(a.cols);
   b.in = static_cast<const float*>(g.B);
@@ -655,6 +661,7 @@ cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) 
   b.rows = g.b_mn ? g.K : g.N;
   b.plane_rows = g.b_ready ? 0 : b_plane_rows(g);
   b.cols = b_cols(g);
+  b.ld = b.cols;
   b.segs = segments(b.cols);
   b.pitch = pitch64(b.cols);
   const int grid = static_cast<int>(

@@ -521,29 +521,44 @@ __global__ void __launch_bounds__(kThreads, 5) loss_finish_kernel(const FinishAr
 // A CTA per row of the block: its loss from the fp32 logits z, and in
 // place of them dz where the gradients are wanted (rows that do not count: 0).
 template <int THREADS>
-__device__ __forceinline__ void loss_row(float* __restrict__ z, const LossRows& l, long long first,
-                                         int V, int top, float inv_tau, float tau,
+__device__ __forceinline__ void loss_row(float* __restrict__ z, long long ld, const LossRows& l,
+                                         long long first, int V, int top, float inv_tau, float tau,
                                          const float* __restrict__ weights, bool grad,
                                          float* __restrict__ loss) {
   __shared__ float ms[THREADS / 32], ss[THREADS / 32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const long long r = first + blockIdx.x;
-  float* row = z + static_cast<long long>(blockIdx.x) * V;
+  float* row = z + static_cast<long long>(blockIdx.x) * ld;
   const int n = *l.count;
+  constexpr int kStep = 8 * THREADS;  // values at a time, two quads of a thread
   if (r >= n) {
     if (grad)
-      for (int v = threadIdx.x; v < V; v += THREADS) row[v] = 0.f;
+      for (int v = 4 * threadIdx.x; v < V; v += 4 * THREADS)
+        *reinterpret_cast<float4*>(row + v) = make_float4(0.f, 0.f, 0.f, 0.f);
     return;
   }
-  // largest and sum in one pass, eight values at a time
-  float m = -INFINITY, s = 0.f;
-  for (int v0 = threadIdx.x; v0 < V; v0 += 8 * THREADS) {
-    float x[8], top_x = m;
+  // this thread's eight values from v0 on; behind the row's end -inf
+  const auto load = [&](int v0, float (&x)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] = v0 + j * THREADS < V ? row[v0 + j * THREADS] : -INFINITY;
-      top_x = fmaxf(top_x, x[j]);
+    for (int h = 0; h < 2; ++h) {
+      const int v = v0 + 4 * (threadIdx.x + h * THREADS);
+      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (v < V) q = *reinterpret_cast<const float4*>(row + v);
+      x[4 * h] = q.x, x[4 * h + 1] = q.y, x[4 * h + 2] = q.z, x[4 * h + 3] = q.w;
+      if (v + 3 >= V) {
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+          if (v + j >= V) x[4 * h + j] = -INFINITY;
+      }
     }
+  };
+  // largest and sum in one pass
+  float m = -INFINITY, s = 0.f;
+  for (int v0 = 0; v0 < V; v0 += kStep) {
+    float x[8], top_x = m;
+    load(v0, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top_x = fmaxf(top_x, x[j]);
     if (m < top_x) {
       s *= expf((m - top_x) * inv_tau);
       m = top_x;
@@ -583,11 +598,23 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, const LossRows& 
   if (!grad) return;
   const float scale = (weights != nullptr ? weights[t] : 1.f / static_cast<float>(n)) * tau;
   __syncthreads();
-#pragma unroll 8
-  for (int v = threadIdx.x; v < V; v += THREADS) {
-    const float dz = scale * (expf((row[v] - m) * inv_tau) / s);
-    // below 2^-109 the products on the tensor cores do not take a value: 0
-    row[v] = fabsf(dz) < 1.5407439555e-33f ? 0.f : dz;
+  const float over = scale / s;
+  for (int v0 = 0; v0 < V; v0 += kStep) {
+    float x[8];
+    load(v0, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float dz = over * expf((x[j] - m) * inv_tau);
+      // below 2^-109 the products on the tensor cores do not take a value: 0
+      x[j] = fabsf(dz) < 1.5407439555e-33f ? 0.f : dz;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int v = v0 + 4 * (threadIdx.x + h * THREADS);
+      if (v < V)
+        *reinterpret_cast<float4*>(row + v) =
+            make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
+    }
   }
   __syncthreads();
   for (int k = threadIdx.x; k < top; k += THREADS) {  // the first of every index
@@ -601,21 +628,21 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, const LossRows& 
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
-    loss_rows_kernel(float* __restrict__ z, LossRows l, long long first, int V, int top,
+    loss_rows_kernel(float* __restrict__ z, long long ld, LossRows l, long long first, int V, int top,
                      float inv_tau, float tau, const float* __restrict__ weights, bool grad,
                      float* __restrict__ loss, bool last, float* __restrict__ total) {
   pdl_wait();
   pdl_trigger();
-  loss_row<THREADS>(z, l, first, V, top, inv_tau, tau, weights, grad, loss);
+  loss_row<THREADS>(z, ld, l, first, V, top, inv_tau, tau, weights, grad, loss);
   if (last)
     total_behind<THREADS>(l, *l.count,
                           weights == nullptr ? static_cast<float>(max(1, *l.count)) : 1.f, total);
 }
 
-// out[c][r] = in[r][c], in [rows][cols].
+// out[c][r] = in[r][c], in [rows][cols], its rows ld apart.
 __global__ void __launch_bounds__(kThreads)
-    loss_transpose_kernel(const float* __restrict__ in, float* __restrict__ out, int rows,
-                          int cols) {
+    loss_transpose_kernel(const float* __restrict__ in, long long ld, float* __restrict__ out,
+                          int rows, int cols) {
   pdl_wait();
   pdl_trigger();
   __shared__ float tile[32][33];
@@ -624,7 +651,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int i = ty; i < 32; i += kThreads / 32)
     if (r0 + i < rows && c0 + tx < cols)
-      tile[i][tx] = in[static_cast<long long>(r0 + i) * cols + c0 + tx];
+      tile[i][tx] = in[(r0 + i) * ld + c0 + tx];
   __syncthreads();
 #pragma unroll
   for (int i = ty; i < 32; i += kThreads / 32)
@@ -672,7 +699,7 @@ struct Plan {
   Plan(const LossArgs& a, bool want_dx, bool want_dw) {
     const size_t T = static_cast<size_t>(a.T), es = a.is_bf16 ? 2 : 4;
     const bool grad = want_dx || want_dw;
-    lde = a.is_bf16 ? round64(a.V) : a.V;
+    lde = a.is_bf16 ? round64(a.V) : (a.V + 3) / 4 * 4;  // 16-byte rows
     ldx = pitch_of(a.d, a.is_bf16);
     block = a.block > 0 ? a.block : static_cast<long long>(kBlockBytes / es / static_cast<size_t>(lde) / 64 * 64);
     block = std::max(64ll, std::min(round64(block), round64(a.T)));
@@ -883,23 +910,26 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
     g.A = xb;
     g.B = a.W;
     g.y = z;
+    g.pitch_y = plan.lde;
     g.M = rows, g.N = a.V, g.K = a.d;
     g.b_ready = ready;
     g.tag = "loss_logits";
     if ((e = linear_fp32(g, scratch, s)) != cudaSuccess) return e;
     ready |= linear_split_pays(rows, a.V, a.d);
     e = launched("loss_rows", s, [&] {
-      // long rows: 512 threads each (333 rows of 30001: ROWS_A -> ROWS_B us)
+      // long rows take 512 threads, four CTAs on an SM: 333 of 30001 28 us (with 1024
+      // a second wave), 515 of 10007 19; short ones 256
       const bool wide = a.V > 8192;
       return launch_pdl(wide ? loss_rows_kernel<512> : loss_rows_kernel<kThreads>,
                         dim3(static_cast<unsigned>(rows)), dim3(wide ? 512 : kThreads), 0, s, z,
-                        l, first, a.V, a.top, 1.f / a.tau, a.tau, a.weights, grad, a.loss,
+                        plan.lde, l, first, a.V, a.top, 1.f / a.tau, a.tau, a.weights, grad, a.loss,
                         first + rows >= a.T, a.total);
     });
     if (e != cudaSuccess) return e;
     if (a.dx != nullptr) {
       LinearProduct q;
       q.A = z;
+      q.pitch_a = plan.lde;
       q.B = a.W;
       q.b_mn = true;
       q.slices = linear_split_slices(rows, a.d, a.V, kCutBytes);
@@ -925,7 +955,7 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
         return launch_pdl(loss_transpose_kernel,
                           dim3(static_cast<unsigned>((rows + 31) / 32),
                                static_cast<unsigned>((a.V + 31) / 32)),
-                          dim3(kThreads), 0, s, static_cast<const float*>(z), zt,
+                          dim3(kThreads), 0, s, static_cast<const float*>(z), plan.lde, zt,
                           static_cast<int>(rows), a.V);
       });
       if (e != cudaSuccess) return e;
