@@ -42,6 +42,11 @@ struct Shape {
   static constexpr int PART = BT * BM * 4;  // the partial tile, over the ring when it is done
   static constexpr int SMEM = RING + 256;
   static constexpr uint32_t TMEM_COLS = BT < 32 ? 32 : BT;
+  // For the losses K's steps are shared out over several accumulators, which are
+  // added up with round-to-nearest: the tensor core's own accumulation truncates (24
+  // tokens, K = 2048: losses 2.9e-6 off with one, 2.8e-7 with eight).
+  static constexpr int ACCS = BT <= 32 ? 8 : BT <= 64 ? 4 : 1;
+  static constexpr uint32_t LOSS_COLS = ACCS * BT < 32 ? 32 : ACCS * BT;
   static_assert(PART <= RING, "the partial tile fits the ring");
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
 };
@@ -204,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
     linear_stream_kernel(const __grid_constant__ CUtensorMap tmW,
                          const __grid_constant__ CUtensorMap tmX, const StreamArgs p) {
   using S = Shape<BT>;
+  constexpr uint32_t kCols = LOSS ? S::LOSS_COLS : S::TMEM_COLS;
   extern __shared__ __align__(1024) uint8_t base[];
   if ((smem_u32(base) & 1023u) != 0) {  // the declared alignment, which the tiles rely on
     if (threadIdx.x == 0) atomicCAS(p.status, 0, static_cast<int>(POETX_ERR_CUDA));
@@ -223,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
   const int per = (p.k_steps + p.splits - 1) / p.splits;
   const int k_begin = slice * per;
   const int steps = max(0, min(p.k_steps, k_begin + per) - k_begin);
+  const int accs = LOSS ? min(S::ACCS, steps) : 1;  // accumulators that are used
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
     tma_prefetch_desc(&tmX);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, S::TMEM_COLS);
+    tmem_alloc(tmem_slot, kCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -300,11 +307,14 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
       // 16 of K: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
       const uint64_t adesc0 = smem_desc_sw128(a_base, A_MN ? 8192 : 16, 1024);
       const uint64_t bdesc0 = smem_desc_sw128(a_base + S::A, 16, 1024);
+      // step i belongs to accumulator i accs / steps
+      const int acc = LOSS ? i * accs / steps : 0;
+      const bool begins = LOSS ? i == 0 || (i - 1) * accs / steps != acc : i == 0;
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < BK / 16; ++j)
-          umma_bf16(tmem, adesc0 + j * (A_MN ? 128 : 2), bdesc0 + j * 2, IDESC,
-                    (i > 0 || j > 0) ? 1u : 0u);
+          umma_bf16(tmem + static_cast<uint32_t>(acc * BT), adesc0 + j * (A_MN ? 128 : 2),
+                    bdesc0 + j * 2, IDESC, (!begins || j > 0) ? 1u : 0u);
         umma_commit(&empty_bar[st]);
       }
       __syncwarp();
@@ -328,6 +338,15 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
     for (int c = (warp >> 2) * 16; c < live_t; c += 32) {
       uint32_t r[16];
       tmem_load_16(t_base + c, r);
+      if (LOSS) {
+        for (int a = 1; a < accs; ++a) {
+          uint32_t more[16];
+          tmem_load_16(t_base + static_cast<uint32_t>(a * BT) + c, more);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(more[j]));
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         if (c + j < live_t) col[(c + j) * BM] = steps > 0 ? __uint_as_float(r[j]) : 0.f;
@@ -351,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
   if (p.splits > 1) cluster_sync();  // no CTA leaves while a peer still reads its tile
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, S::TMEM_COLS);
+    tmem_dealloc(tmem, kCols);
   }
 }
 

@@ -422,7 +422,7 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
       if (own) ref = m == -INFINITY ? 0.f : m * a.unit;
       // an infinite logit: the sum is infinite too
       const float log_s = m == INFINITY ? 0.f : log2f(s);
-      float sum = 0.f;
+      float sum = 0.f, both = 0.f, square = 0.f;
       for (int k = lane; k < a.top; k += 32) {
         const int i = k == lane ? i0 : a.rows.index[base + k];
         if (i < 0) continue;
@@ -433,17 +433,27 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
           float all = p;
           for (int q = k + 1; q < a.top && a.rows.index[base + q] == i; ++q)
             all += a.rows.p[base + q];
-          a.E[row * a.lde + i] = __float2bfloat16_rn(exp2f(over) - all * s);
+          const float term = exp2f(over) / s - all;
+          const bf16 kept = __float2bfloat16_rn(term * s);
+          a.E[row * a.lde + i] = kept;
+          both = fmaf(term, term, both);
+          square = fmaf(__bfloat162float(kept) / s, term, square);
         }
       }
       sum = warp_sum(sum);
+      both = warp_sum(both);
+      square = warp_sum(square);
       if (lane == 0) {
         const float loss = counts ? a.tau * a.tau * (ent + 0.69314718056f * sum) : 0.f;
         a.loss[t] = loss;
         totals[warp] = counts ? static_cast<double>(weight) * loss : 0.0;
         if (!own) {
+          // The row's factor takes up what the rounding of its entries' terms has in
+          // common (least squares; for one entry all of it): these are most of the
+          // gradient, and their errors would be a whole row's of dx and dW.
+          const float fit = square > 0.f ? both / square : 1.f;
           a.rows.scale[r] = make_float2(
-              a.tau / s, a.weights != nullptr ? weight : 1.f / static_cast<float>(count));
+              a.tau / s * fit, a.weights != nullptr ? weight : 1.f / static_cast<float>(count));
           const float above = m * a.unit - ref;
           if (!a.second && (above > kFits || above < -2.f * kAbove)) {
             a.rows.ref[r] = m * a.unit;
@@ -497,7 +507,7 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
 }
 
 template <int R>
-__global__ void __launch_bounds__(kThreads, 5) loss_finish_kernel(const FinishArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) loss_finish_kernel(const FinishArgs a) {
   pdl_wait();
   pdl_trigger();
   finish_rows<R>(a);

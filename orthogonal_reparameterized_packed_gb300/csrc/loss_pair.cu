@@ -4,14 +4,14 @@
 //   dw      dW = E^T x
 // The kernel is linear_pair's with other epilogues: clusters of two CTAs compute
 // tiles of 256 x 256 with tcgen05.mma.cta_group::2 over 64-wide K steps from a TMA
-// ring, two TMEM accumulators, 16 epilogue warps (64 columns of a 32-row quarter
-// each).  dw's A is E as it lies, [rows][V]: an MN-major operand.  The rows are
+// ring, two TMEM accumulators; warp 0 loads, warp 1 issues the MMAs, and behind their
+// warpgroup 16 epilogue warps take 64 columns of a 32-row quarter each.  dw's A is E as it lies, [rows][V]: an MN-major operand.  The rows are
 // counted on the GPU: tiles behind the last row are not computed.
 //
 // The logits are never stored.  A tile's epilogue takes each z once: its
 // exponential relative to the row's reference, the sum and the largest of 64
-// columns; the entries' logits (a token's entries are sorted, so that a warp finds
-// those of its 64 columns by bisection) are read from TMEM a column at a time.
+// columns; a token's entries are sorted, so that a warp finds those of its 64 columns
+// by bisection.
 //
 // Every wait is bounded as in gemm_pair.cu.
 #include <algorithm>
@@ -29,7 +29,8 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-enum Kind { kLogits, kDx, kDw };
+// kLogits leaves the terms, kStats the statistics alone
+enum Kind { kLogits, kStats, kDx, kDw };
 
 constexpr int BN = 256;
 constexpr int kA = BM * BK * 2;        // this CTA's 128 rows, one K step
@@ -39,7 +40,7 @@ constexpr int kStages = 6;
 constexpr int kRing = kStages * kStage;
 constexpr int kSides = BN / 64;  // of 64 columns, four warps each
 constexpr int kEpiWarps = 4 * kSides;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 128 + 32 * kEpiWarps;  // warps 2 and 3 have no role
 constexpr int kChunk = 32;  // columns that a warp stages at a time
 constexpr int kSlot = 32 * kChunk * 2;
 constexpr int kSmem = kRing + kEpiWarps * kSlot + 256;
@@ -49,6 +50,13 @@ constexpr int kLeastShare = 8;   // K steps of a slice
 constexpr int kMaxSlices = 16;
 constexpr int kSlots = 4;        // slices' tiles per cluster at most
 constexpr float kCutCost = 20.f;
+// The tensor core's accumulation truncates: over 2048 of K a logit comes out 4e-6 of
+// itself too small, and the losses were 2.4e-6 off where a product rounded to nearest
+// leaves 8e-7.  So the logits take kDrain K steps at a time, and the epilogue adds
+// those up in registers.  Shorter pieces leave the epilogue of the tile before less
+// time, which the first two of them hide.  2049 tokens, 2048 -> 50001, forward: 8 / 12 /
+// 16 / 32 steps 206 / 199 / 199 / 200 us and 5e-7 / 7.5e-7 / 1.1e-6 / 2.3e-6 off.
+constexpr int kDrain = 12;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
 // The order of the work.  Whole rounds of tiles over the clusters come first; the
@@ -58,7 +66,7 @@ static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 // 1638 rows, d = 2048, V = 32000).  A slice's tile is kept in fp32, [256][256], and
 // added up by loss_sum_kernel.
 struct Schedule {
-  int whole, rest, slices, share, k_steps, clusters;
+  int whole, rest, slices, share, k_steps, clusters, rows;
 
   // In units of a K step (0.28 us): the rounds of the rest and, when it is cut, 0.4
   // for a slice's tile written and read and kCutCost for the launch.
@@ -115,7 +123,7 @@ struct PairArgs {
   long long ld, ldp;
   const int* only;       // null, or nothing is done while it is 0
   float unit;
-  bool store, vec;       // kLogits: E is wanted; output rows are 16-byte aligned
+  bool vec;              // output rows are 16-byte aligned
   float2* part;
   bf16* out;             // dx or dW
   float* acc;
@@ -158,44 +166,20 @@ __device__ __forceinline__ void stage_part(const Staged& slot, int lane, int par
   }
 }
 
-// One accumulator column of this thread's lane.
-__device__ __forceinline__ float tmem_load_1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr)
-               : "memory");
-  tmem_load_wait();
-  return __uint_as_float(r);
-}
-
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// 16 logits of a row: their exponentials, sum and largest; `live` of them are in
-// the vocabulary, the others become 0.
-__device__ __forceinline__ void exp_part(float (&v)[16], float unit, float ref, int live,
-                                         float& sum, float& most) {
-  if (live >= 16) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      most = fmaxf(most, v[j]);
-      v[j] = exp2_fast(fmaf(v[j], unit, -ref));
-      sum += v[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (j < live) {
-        most = fmaxf(most, v[j]);
-        v[j] = exp2_fast(fmaf(v[j], unit, -ref));
-        sum += v[j];
-      } else {
-        v[j] = 0.f;
-      }
-    }
-  }
+// A block of 640 threads has 96 registers each, 61440.  The logits' epilogue keeps 64
+// sums a thread and takes 112 (512 threads: 57344), the first warpgroup keeps 32
+// (4096).  With 96 the sums spilled, and took twice the time.
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+}
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
 }
 
 template <int KIND>
@@ -203,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     loss_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmOut, const PairArgs p) {
-  constexpr bool A_MN = KIND == kDw, B_MN = KIND != kLogits;
+  constexpr bool LOGITS = KIND == kLogits || KIND == kStats, STORE = KIND == kLogits;
+  constexpr bool A_MN = KIND == kDw, B_MN = !LOGITS;
   extern __shared__ __align__(1024) uint8_t base[];  // 128B-swizzled tiles start on 1024 bytes
   if ((smem_u32(base) & 1023u) != 0) {  // the declared alignment, which the tiles rely on
     if (threadIdx.x == 0) atomicCAS(p.status, 0, static_cast<int>(POETX_ERR_CUDA));
@@ -227,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first_unit = static_cast<int>(cluster_id_x());
   const int step = static_cast<int>(cluster_count_x());
 
-  if (KIND == kLogits && p.only != nullptr) {  // the same for every CTA, before anything is set up
+  if (STORE && p.only != nullptr) {  // the same for every CTA, before anything is set up
     pdl_wait();
     if (*p.only == 0) return;
   }
@@ -270,139 +255,151 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (KIND == kDw && n == 0 && p.first > 0) units = 0;  // the block before was the last
   const bool products = k_steps > 0;  // dW without a row is 0
   if (threadIdx.x == 0) {
-    schedule->plan(units, k_steps, step, KIND != kLogits && p.parts != nullptr);
+    schedule->rows = static_cast<int>(n);
+    schedule->plan(units, k_steps, step, !LOGITS && p.parts != nullptr);
     if (blockIdx.x == 0 && p.parts != nullptr) *p.schedule = *schedule;
   }
   __syncthreads();
-  const Schedule todo = *schedule;
+  const Schedule& todo = *schedule;
 
   const uint32_t full0 = map_peer(smem_u32(full_bar), 0);
   const uint32_t tempty0 = map_peer(smem_u32(tempty_bar), 0);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    int stage = 0;
-    uint32_t phase = 0;
-    long long issued = 0;
-    bool ok = true;
-    int tile, ks0, ks1, part_slot;
-    for (int i = 0; products && ok && todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
-      int mp, nt;
-      unit_tile(tile, m_pairs, p.n_tiles, mp, nt);
-      const int a_row = mp * 2 * BM + static_cast<int>(rank) * BM;
-      const int b_n = nt * BN + static_cast<int>(rank) * (BN / 2);
-      for (int ks = ks0; ks < ks1; ++ks) {
-        if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) {
-          record_timeout(p.status, abort_flag);
-          ok = false;
-          break;
-        }
-        if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStage);
-          uint8_t* a_dst = ring + stage * kStage;
-          uint8_t* b_dst = a_dst + kA;
-          const uint32_t bar = full0 + static_cast<uint32_t>(stage * 8);
-          if (!A_MN) {
-            tma_load_2d_pair(a_dst, &tmA, bar, ks * BK, a_row);
-          } else {
-            tma_load_2d_pair(a_dst, &tmA, bar, a_row, ks * BK);
-            tma_load_2d_pair(a_dst + 8192, &tmA, bar, a_row + 64, ks * BK);
-          }
-          if (!B_MN) {
-            tma_load_2d_pair(b_dst, &tmB, bar, ks * BK, b_n);
-          } else {
-            tma_load_2d_pair(b_dst, &tmB, bar, b_n, ks * BK);
-            tma_load_2d_pair(b_dst + 8192, &tmB, bar, b_n + 64, ks * BK);
-          }
-        }
-        __syncwarp();
-        ++issued;
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-    }
-    // every slot this CTA filled is released again before it leaves
-    const int outstanding = issued < kStages ? static_cast<int>(issued) : kStages;
-    int st = stage;
-    uint32_t ph = phase;
-    for (int i = 0; i < outstanding; ++i) {
-      if (--st < 0) {
-        st = kStages - 1;
-        ph ^= 1;
-      }
-      const unsigned long long t0 = global_timer_ns();
-      while (!mbar_try_wait_cluster(&empty_bar[st], ph) &&
-             global_timer_ns() - t0 < (ok ? kWaitLimitNs : 10000000ull)) {
-      }
-    }
-  } else if (warp == 1) {
-    if (leader) {
-      // -------------------------------------------------- MMA issuer (pair)
-      constexpr uint32_t IDESC = instr_desc_bf16(2 * BM, BN, A_MN, B_MN);
-      const uint32_t empty_own = smem_u32(empty_bar);
-      const uint32_t tfull_own = smem_u32(tfull_bar);
+  // Registers: 640 threads get 96 each at the launch, 61440; the epilogue of the logits
+  // takes 112 (57344), the first four warps keep 32 (4096).
+  if (warp < 4) {  // the same for each warpgroup, as setmaxnreg needs
+    if (LOGITS) registers_down();
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
       int stage = 0;
       uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
+      long long issued = 0;
       bool ok = true;
-      bool any_mma = false;
       int tile, ks0, ks1, part_slot;
       for (int i = 0; products && ok && todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
-        if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1, abort_flag)) {
-          record_timeout(p.status, abort_flag);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc) * kAcc;
+        int mp, nt;
+        unit_tile(tile, m_pairs, p.n_tiles, mp, nt);
+        const int a_row = mp * 2 * BM + static_cast<int>(rank) * BM;
+        const int b_n = nt * BN + static_cast<int>(rank) * (BN / 2);
         for (int ks = ks0; ks < ks1; ++ks) {
-          if (!mbar_wait(&full_bar[stage], phase, abort_flag)) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) {
             record_timeout(p.status, abort_flag);
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t a_base = smem_u32(ring) + stage * kStage;
-          const uint32_t b_base = a_base + kA;
-          // 16 of K: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
-          const uint64_t adesc0 = smem_desc_sw128(a_base, A_MN ? 8192 : 16, 1024);
-          const uint64_t bdesc0 = smem_desc_sw128(b_base, B_MN ? 8192 : 16, 1024);
           if (elect_one()) {
-#pragma unroll
-            for (int j = 0; j < BK / 16; ++j)
-              umma_bf16_pair(d_tmem, adesc0 + j * (A_MN ? 128 : 2), bdesc0 + j * (B_MN ? 128 : 2),
-                             IDESC, (ks > ks0 || j > 0) ? 1u : 0u);
-            // the slot is free in both CTAs once the MMAs have read it
-            umma_commit_both(empty_own + static_cast<uint32_t>(stage * 8));
+            if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStage);
+            uint8_t* a_dst = ring + stage * kStage;
+            uint8_t* b_dst = a_dst + kA;
+            const uint32_t bar = full0 + static_cast<uint32_t>(stage * 8);
+            if (!A_MN) {
+              tma_load_2d_pair(a_dst, &tmA, bar, ks * BK, a_row);
+            } else {
+              tma_load_2d_pair(a_dst, &tmA, bar, a_row, ks * BK);
+              tma_load_2d_pair(a_dst + 8192, &tmA, bar, a_row + 64, ks * BK);
+            }
+            if (!B_MN) {
+              tma_load_2d_pair(b_dst, &tmB, bar, ks * BK, b_n);
+            } else {
+              tma_load_2d_pair(b_dst, &tmB, bar, b_n, ks * BK);
+              tma_load_2d_pair(b_dst + 8192, &tmB, bar, b_n + 64, ks * BK);
+            }
           }
           __syncwarp();
-          any_mma = true;
+          ++issued;
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (!ok) break;
-        if (elect_one()) umma_commit_both(tfull_own + static_cast<uint32_t>(acc * 8));
-        __syncwarp();
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
       }
-      if (!ok && any_mma) {
-        // the MMAs in flight finish before TMEM is released
-        if (elect_one()) umma_commit_pair(smem_u32(drain_bar));
-        __syncwarp();
+      // every slot this CTA filled is released again before it leaves
+      const int outstanding = issued < kStages ? static_cast<int>(issued) : kStages;
+      int st = stage;
+      uint32_t ph = phase;
+      for (int i = 0; i < outstanding; ++i) {
+        if (--st < 0) {
+          st = kStages - 1;
+          ph ^= 1;
+        }
         const unsigned long long t0 = global_timer_ns();
-        while (!mbar_try_wait(drain_bar, 0) && global_timer_ns() - t0 < 10000000ull) {
+        while (!mbar_try_wait_cluster(&empty_bar[st], ph) &&
+               global_timer_ns() - t0 < (ok ? kWaitLimitNs : 10000000ull)) {
+        }
+      }
+    } else if (warp == 1) {
+      if (leader) {
+        // -------------------------------------------------- MMA issuer (pair)
+        constexpr uint32_t IDESC = instr_desc_bf16(2 * BM, BN, A_MN, B_MN);
+        const uint32_t empty_own = smem_u32(empty_bar);
+        const uint32_t tfull_own = smem_u32(tfull_bar);
+        int stage = 0;
+        uint32_t phase = 0;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        bool any_mma = false;
+        int tile, ks0, ks1, part_slot;
+        for (int i = 0; products && ok && todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
+          for (int kc = ks0; kc < ks1 && ok; kc += kDrain) {
+            const int kc1 = LOGITS ? min(ks1, kc + kDrain) : ks1;
+            if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1, abort_flag)) {
+              record_timeout(p.status, abort_flag);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc) * kAcc;
+            for (int ks = kc; ks < kc1; ++ks) {
+              if (!mbar_wait(&full_bar[stage], phase, abort_flag)) {
+                record_timeout(p.status, abort_flag);
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t a_base = smem_u32(ring) + stage * kStage;
+              const uint32_t b_base = a_base + kA;
+              // 16 of K: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
+              const uint64_t adesc0 = smem_desc_sw128(a_base, A_MN ? 8192 : 16, 1024);
+              const uint64_t bdesc0 = smem_desc_sw128(b_base, B_MN ? 8192 : 16, 1024);
+              if (elect_one()) {
+#pragma unroll
+                for (int j = 0; j < BK / 16; ++j)
+                  umma_bf16_pair(d_tmem, adesc0 + j * (A_MN ? 128 : 2),
+                                 bdesc0 + j * (B_MN ? 128 : 2), IDESC,
+                                 (ks > kc || j > 0) ? 1u : 0u);
+                // the slot is free in both CTAs once the MMAs have read it
+                umma_commit_both(empty_own + static_cast<uint32_t>(stage * 8));
+              }
+              __syncwarp();
+              any_mma = true;
+              if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+              }
+            }
+            if (!ok) break;
+            if (elect_one()) umma_commit_both(tfull_own + static_cast<uint32_t>(acc * 8));
+            __syncwarp();
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+            if (!LOGITS) break;
+          }
+        }
+        if (!ok && any_mma) {
+          // the MMAs in flight finish before TMEM is released
+          if (elect_one()) umma_commit_pair(smem_u32(drain_bar));
+          __syncwarp();
+          const unsigned long long t0 = global_timer_ns();
+          while (!mbar_try_wait(drain_bar, 0) && global_timer_ns() - t0 < 10000000ull) {
+          }
         }
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int ew = warp - 2;
+    if (LOGITS) registers_up();
+    const int ew = warp - 4;
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
     const int side = ew >> 2;      // its 64 columns
     const Staged slot{staging + ew * kSlot};
@@ -450,39 +447,142 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
 
+    if (LOGITS) {
+      // Nothing but the sums lives through the main loop: registers are short.
+      const volatile Schedule* plan = schedule;
+      for (int u = first_unit; u < plan->whole; u += plan->clusters) {
+        const int chunks = (plan->k_steps + kDrain - 1) / kDrain;
+        float z[64];
+        bool got = true;
+        for (int kc = 0; kc < chunks; ++kc) {
+          got = __all_sync(0xffffffffu,
+                           mbar_wait_cluster(&tfull_bar[acc], acc_phase, abort_flag));
+          if (!got) break;
+          tc_fence_after();
+          const uint32_t t_side = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                  static_cast<uint32_t>(acc) * kAcc +
+                                  static_cast<uint32_t>(side * 64);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t r[16];
+            tmem_load_16(t_side + q * 16, r);
+            if (kc == 0) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) z[16 * q + j] = __uint_as_float(r[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) z[16 * q + j] += __uint_as_float(r[j]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          // the accumulator is free again once both CTAs' epilogue warps have read it
+          if (lane == 0) mbar_arrive_remote(tempty0 + static_cast<uint32_t>(acc * 8));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+        }
+        if (!got) {
+          record_timeout(p.status, abort_flag);
+          break;
+        }
+        int at_unit = u;
+        asm volatile("" : "+r"(at_unit));  // what follows is computed here, not before
+        const int rows = plan->rows;
+        int mp, nt;
+        unit_tile(at_unit, (rows + 2 * BM - 1) / (2 * BM), p.n_tiles, mp, nt);
+        const int row0 = mp * 2 * BM + static_cast<int>(rank) * BM + quarter * 32;
+        const int side_col = nt * BN + side * 64;
+        const int row = row0 + lane;
+        const int in = p.N - side_col;  // columns in the vocabulary
+        // E's rows behind the last are written up to a whole K step of dW
+        if (row0 >= (rows + BK - 1) / BK * BK || in <= 0) continue;
+        const bool on = row < rows;
+        // rows behind the last, whose x is 0: their terms are 0
+        float ref = STORE ? INFINITY : 0.f;
+        int token = 0, k = p.top, next = INT_MAX;  // the row's next entry from side_col on
+        if (on) {
+          token = p.rows.token[p.first + row];
+          if (STORE) ref = p.rows.ref[p.first + row];
+          const int* idx = p.rows.index + static_cast<long long>(token) * p.top;
+          int lo = 0;
+          while (lo < k) {
+            const int mid = (lo + k) >> 1;
+            if (idx[mid] < side_col)
+              lo = mid + 1;
+            else
+              k = mid;
+          }
+          if (k < p.top) next = idx[k];
+        }
+        if (in < 64) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (j >= in) z[j] = -INFINITY;
+        }
+        float sum = 0.f, top_z = -INFINITY;
+        if (!STORE) {  // the reference is the largest of the 64 columns
+#pragma unroll
+          for (int j = 0; j < 64; ++j) top_z = fmaxf(top_z, z[j]);
+          ref = top_z == -INFINITY ? 0.f : top_z * p.unit;
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += kChunk) {
+          if (c >= in) break;
+          if (stores_pending) staging_free();
+          // the logits at this row's entries
+          const int end = min(side_col + c + kChunk, p.N);
+          while (__any_sync(0xffffffffu, next < end)) {
+            const int at = next - side_col;
+            float of_entry = 0.f;
+#pragma unroll
+            for (int j = c; j < c + kChunk; ++j)
+              if (j == at) of_entry = z[j];
+            if (next < end) {
+              const long long to = static_cast<long long>(token) * p.top + k;
+              p.rows.z[to] = of_entry;
+              next = ++k < p.top ? p.rows.index[to + 1] : INT_MAX;
+            }
+          }
+#pragma unroll
+          for (int j = c; j < c + kChunk; ++j) {
+            if (STORE) top_z = fmaxf(top_z, z[j]);
+            z[j] = exp2_fast(fmaf(z[j], p.unit, -ref));
+            sum += z[j];
+          }
+          if (STORE) {
+#pragma unroll
+            for (int q = 0; q < kChunk / 8; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                w[h] = pack_bf16x2(__float_as_uint(z[c + 8 * q + 2 * h]),
+                                   __float_as_uint(z[c + 8 * q + 2 * h + 1]));
+              st_shared_v4(slot.piece(lane, q), w[0], w[1], w[2], w[3]);
+            }
+            store_tma(row0, side_col + c);
+          }
+        }
+        if (on)
+          p.part[(static_cast<long long>(nt) * kSides + side) * p.ldp + row] =
+              make_float2(top_z, sum);
+      }
+    }
+
     int tile, ks0, ks1, part_slot;
-    for (int i = 0; todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
+    for (int i = 0; !LOGITS && todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
       int mp, nt;
       unit_tile(tile, m_pairs, p.n_tiles, mp, nt);
       const long long row0 = static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32;
       const int side_col = nt * BN + side * 64;
       const long long row = row0 + lane;
-      // E's rows behind the last are written up to a whole K step of dW
-      const long long rows_end = KIND == kLogits ? (n + BK - 1) / BK * BK : M;
-      const bool live = row0 < rows_end && side_col < p.N;  // the same for the whole warp
+      const bool live = row0 < M && side_col < p.N;  // the same for the whole warp
       const bool on = row < M;
       // what the row needs besides the accumulator, under the main loop
       int token = -1;
-      float ref = 0.f;
       float2 scale = make_float2(0.f, 0.f);
-      if (KIND != kDw && live && on) {
+      if (KIND == kDx && live && on) {
         token = p.rows.token[p.first + row];
-        if (KIND == kLogits && p.store) ref = p.rows.ref[p.first + row];
-        if (KIND == kDx) scale = p.rows.scale[p.first + row];
-      }
-      int k = p.top, next = INT_MAX;  // the row's next entry from this warp's columns on
-      if (KIND == kLogits && live && on) {
-        const int* idx = p.rows.index + static_cast<long long>(token) * p.top;
-        int lo = 0, hi = p.top;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (idx[mid] < side_col)
-            lo = mid + 1;
-          else
-            hi = mid;
-        }
-        k = lo;
-        if (k < p.top) next = idx[k];
+        scale = p.rows.scale[p.first + row];
       }
       if (products) {
         const bool got = mbar_wait_cluster(&tfull_bar[acc], acc_phase, abort_flag);
@@ -494,21 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t t_side = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                               static_cast<uint32_t>(acc) * kAcc + static_cast<uint32_t>(side * 64);
-      float sum = 0.f, top_z = -INFINITY;
-      if (KIND == kLogits && !p.store && live) {
-        // the reference is the largest of the 64 columns
-#pragma unroll 1
-        for (int c = 0; c < 64 && side_col + c < p.N; c += 16) {
-          uint32_t r[16];
-          tmem_load_16(t_side + c, r);
-          const int in = p.N - side_col - c;
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (j < in) top_z = fmaxf(top_z, __uint_as_float(r[j]));
-        }
-        ref = top_z == -INFINITY ? 0.f : top_z * p.unit;
-      }
-      if (KIND != kLogits && part_slot >= 0 && live) {
+      if (part_slot >= 0 && live) {
         float* to = p.parts + static_cast<long long>(part_slot) * 2 * BM * BN +
                     (rank * BM + quarter * 32 + lane) * BN + side * 64;
 #pragma unroll 1
@@ -541,13 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 16; ++j) v[j] = 0.f;
           }
           const int in = p.N - col - part * 16;
-          if (KIND == kLogits) {
-            exp_part(v, p.unit, ref, in, sum, top_z);
-            if (!on) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = 0.f;
-            }
-          } else if (KIND == kDx) {
+          if (KIND == kDx) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = v[j] * scale.x * scale.y;
           } else {
@@ -563,11 +643,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
           }
-          if (KIND != kLogits || p.store) stage_part(slot, lane, part, v);
+          stage_part(slot, lane, part, v);
         }
-        if (KIND == kLogits) {
-          if (p.store) store_tma(row0, col);
-        } else if (KIND == kDx) {
+        if (KIND == kDx) {
           store_rows(token, col);
         } else if (last) {
           if (p.vec)
@@ -576,23 +654,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             store_rows(on ? static_cast<int>(row) : -1, col);
         } else {
           __syncwarp();
-        }
-      }
-      if (KIND == kLogits && live) {
-        if (on)
-          p.part[(static_cast<long long>(nt) * kSides + side) * p.ldp + row] =
-              make_float2(top_z, sum);
-        const int end = min(side_col + 64, p.N);
-        while (true) {  // a column that is an entry of some row, all rows that have it
-          const unsigned some = __ballot_sync(0xffffffffu, next < end);
-          if (some == 0) break;
-          const int col = __shfl_sync(0xffffffffu, next, __ffs(some) - 1);
-          const float z = tmem_load_1(t_side + static_cast<uint32_t>(col - side_col));
-          if (next == col) {
-            const long long at = static_cast<long long>(token) * p.top + k;
-            p.rows.z[at] = z;
-            next = ++k < p.top ? p.rows.index[at + 1] : INT_MAX;
-          }
         }
       }
       if (products) {
@@ -682,6 +743,16 @@ __global__ void __launch_bounds__(kSumThreads) loss_sum_kernel(const PairArgs p)
 }
 
 template <int KIND>
+cudaError_t sum_slices(const PairArgs& p, cudaStream_t stream) {
+  prof_begin("loss_sum", stream);
+  const cudaError_t e =
+      launch_pdl(loss_sum_kernel<KIND>, dim3(8 * static_cast<unsigned>(sm_count())),
+                 dim3(kSumThreads), 0, stream, p);
+  prof_end("loss_sum", stream);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int KIND>
 cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
                    const PairArgs& p, long long most_units, const char* tag,
                    cudaStream_t stream) {
@@ -730,14 +801,11 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmOut, p);
   prof_end(tag, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess || KIND == kLogits || p.parts == nullptr) return e;
-  prof_begin("loss_sum", stream);
-  e = launch_pdl(loss_sum_kernel<KIND>, dim3(8 * static_cast<unsigned>(sm_count())),
-                 dim3(kSumThreads), 0, stream, p);
-  prof_end("loss_sum", stream);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  if constexpr (KIND == kDx || KIND == kDw) {
+    if (e == cudaSuccess && p.parts != nullptr) e = sum_slices<KIND>(p, stream);
+  }
+  return e;
 }
-
 PairArgs common(const LossProducts& g) {
   PairArgs p = {};
   p.V = g.V;
@@ -769,8 +837,8 @@ cudaError_t loss_logits(const LossProducts& g, bool only_again, cudaStream_t s) 
       !make_map(&tmB, g.W, g.V, g.d, g.ldw, 2, 64, BN / 2))
     return cudaErrorInvalidValue;
   tmE = tmA;  // a stand-in: not used
-  p.store = g.E != nullptr;
-  if (p.store && !make_map(&tmE, g.E, g.block, g.V, g.lde, 2, kChunk, 32, 64))
+  const bool store = g.E != nullptr;
+  if (store && !make_map(&tmE, g.E, g.block, g.V, g.lde, 2, kChunk, 32, 64))
     return cudaErrorInvalidValue;
   p.n_tiles = (g.V + BN - 1) / BN;
   p.N = g.V;
@@ -778,8 +846,10 @@ cudaError_t loss_logits(const LossProducts& g, bool only_again, cudaStream_t s) 
   p.part = g.part;
   p.ldp = g.ldp;
   if (only_again) p.only = g.rows.again + g.first / g.block;
-  return launch<kLogits>(tmA, tmB, tmE, p, pairs(g.block) * p.n_tiles,
-                         only_again ? "loss_logits_again" : "loss_logits", s);
+  const long long tiles = pairs(g.block) * p.n_tiles;
+  if (!store) return launch<kStats>(tmA, tmB, tmE, p, tiles, "loss_logits", s);
+  return launch<kLogits>(tmA, tmB, tmE, p, tiles, only_again ? "loss_logits_again" : "loss_logits",
+                         s);
 }
 
 cudaError_t loss_dx(const LossProducts& g, cudaStream_t s) {

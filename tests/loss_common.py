@@ -12,9 +12,11 @@ Bounds.  u = 2^-8 or 2^-24 is the unit roundoff of the working type.
  entries  the teacher's p: differences are rounded to 2^-23 of themselves, each
           exponential to 2^-21, the sum of K to K 2^-24; log p alike.
  dz       e / sum - p, each with the errors above.  bf16 rounds each difference to
-          u for the products, which also round x times the row's factor for dW (u
-          once more); products of V (dx) or T (dW) terms add V or T times 2^-23
-          of their magnitudes; the result is rounded once."""
+          u for the products, and shifts the row's factor by the error that its
+          entries' terms have in common: a weighted mean of theirs, at most u.  For
+          dW x times the factor is rounded to u too; products of V (dx) or T (dW)
+          terms add V or T times 2^-23 of their magnitudes; the result is rounded
+          once."""
 
 import numpy as np
 import torch
@@ -72,9 +74,9 @@ def bounds(c, tau, weights, logits):
     tiny = 2.0 ** -109  # fp32 takes smaller dz as 0
     b_dz = np.abs(scale) * (q * e_q + dP + (q + P) * 2.0 ** -21) + tiny
     b_dx, b_dW = np.zeros((T, d)), None
-    b_dx[rows] = (b_dz + np.abs(dz) * (u16 + V * 2.0 ** -23) * 1.01) @ aW
+    b_dx[rows] = (b_dz + np.abs(dz) * (2 * u16 + V * 2.0 ** -23) * 1.02) @ aW
     b_dx += uo * (np.abs(dx) + b_dx) + 1e-38
-    b_dW = (b_dz + np.abs(dz) * (2 * u16 + T * 2.0 ** -23) * 1.02 + b_dz * 2 * u16).T @ ax
+    b_dW = (b_dz + np.abs(dz) * (3 * u16 + T * 2.0 ** -23) * 1.03 + b_dz * 3 * u16).T @ ax
     b_dW += uo * (np.abs(dW) + b_dW) + 1e-38
     return (loss, np.float64(total), dx, dW), (b_loss, b_total, b_dx, b_dW)
 
