@@ -65,6 +65,17 @@ def test_cross_entropy(px, T, d, V, dtype):
     run_and_check(px, c, None, c["w"] if V % 2 else None)
 
 
+# either side of the pieces of K that the logits are summed in (768), several tiles of
+# logits for a cluster of CTAs
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,V", [(70, 768, 300), (70, 776, 300), (130, 1600, 700),
+                                   (90, 4096, 520), (600, 64, 9000), (64, 4096, 260),
+                                   (20, 1536, 140)])
+def test_long_and_wide(px, T, d, V, dtype):
+    c = make(T, d, V, 1, dtype, seed=T + d, ignored=0.1)
+    run_and_check(px, c, None)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,d,V,K,tau", [
     (1, 64, 300, 16, 2.0), (1, 9, 4, 3, 1.0), (5, 128, 1000, 1, 1.0), (40, 256, 2051, 7, 4.0),
@@ -372,3 +383,133 @@ def test_long_rows_pass_32_bits(px):
     assert float((dx2.float() - dx.float()).abs().max()) <= 2.0 ** -6 * float(scale.max())
     off = float((dW2.float() - dW.float()).norm() / dW.float().norm())
     assert off <= 2 * 2.0 ** -7  # both rounded: terms, factors and results
+
+
+@pytest.mark.parametrize("T,d,V", [(5000, 1024, 4000), (4200, 256, 20500), (6000, 1024, 300),
+                                   (40, 1024, 30000), (8200, 64, 600)])
+def test_rounds_of_tiles(px, T, d, V):
+    """More tiles of dx or dW than clusters of CTAs, last rounds cut along K, few tiles of a
+    long K.  The bounds of loss_common, evaluated in float64 on the GPU."""
+    from orthogonal_reparameterized_packed_gb300.loss import PoetxCrossEntropy
+    g = torch.Generator(device="cuda").manual_seed(T)
+    W = (torch.randn((V, d), generator=g, device="cuda") * 2 * d ** -0.5).bfloat16()
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    x = (torch.randn((T, d), generator=g, device="cuda") + 2.0 * W[t].float()).bfloat16()
+    t[::7] = -1
+    h = PoetxCrossEntropy(d, V, T, backward=True, weight_grad=True)
+    loss, dx, dW = h.step(x, W, t)
+    status_ok(px)
+    on = t >= 0
+    X, Y, H = x[on].double(), t[on], W.double()
+    n, u = len(Y), 2.0 ** -8
+    z = X @ H.t()
+    rows = torch.arange(n, device="cuda")
+    lse = torch.logsumexp(z, 1, keepdim=True)
+    want = lse[:, 0] - z[rows, Y]
+    ez = d * 2.0 ** -23 * float((X.abs() @ H.abs().t()).max())
+    e_q = 2.1 * (ez + 2.0 ** -21 * (float(z.abs().max()) + 64) + 2.0 ** -21) + (
+        512 + V / 128) * 2.0 ** -24
+    assert bool(((loss[on].double() - want).abs() <= 2 * e_q + 2.0 ** -20 * (1 + want)).all())
+    assert not loss[~on].any() and not dx[~on].any()
+    q = (z - lse).exp()
+    del z
+    b = q * e_q / n
+    q[rows, Y] -= 1
+    dz = q / n
+    del q
+    top = 2.0 ** -20 / n
+    for got, exact, size in (
+            (dx[on].double(), dz @ H, (2 * u + V * 2.0 ** -23) * 1.02 * (dz.abs() @ H.abs()) +
+             b @ H.abs() + top),
+            (dW.double(), dz.t() @ X, (3 * u + T * 2.0 ** -23) * 1.03 * (dz.abs().t() @ X.abs()) +
+             b.t() @ X.abs() + top * float(X.abs().max()))):
+        size = size + u * (exact.abs() + size)
+        assert bool(((got - exact).abs() <= size).all())
+
+
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+@pytest.mark.parametrize("tau", [None, 2.0])
+@pytest.mark.parametrize("T", [1, 5, 20, 64])
+def test_scores_of_few_tokens(px, T, tau, index):
+    """Losses alone of up to 64 tokens, with tokens that do not count and hold anything, and an
+    index outside the vocabulary."""
+    c = make(T, 128, 700, 1 if tau is None else 6, "bf16", seed=T)
+    rng = np.random.default_rng(T)
+    off = np.flatnonzero(rng.random(T) < 0.3) if T > 1 else np.zeros(0, dtype=int)
+    c["idx"][off] = -5
+    outside = T > 5
+    if outside:
+        c["idx"][2] = 700
+    for weights in (None, c["w"]):
+        want, bound = expected(c, tau, weights)
+        x, rest = c["x"][0].clone(), device(c, tau is not None, index)
+        x[torch.from_numpy(off).cuda()] = float("nan")
+        w = None if weights is None else torch.from_numpy(weights).float().cuda()
+        if w is not None:
+            w[torch.from_numpy(off).cuda()] = float("inf")
+        h = head(c, tau, backward=False, weight_grad=False)
+        h.loss.fill_(9.0)
+        loss = h.forward(x, c["W"][0], *rest, w)
+        torch.cuda.synchronize()
+        assert px.poetx_device_status() == (1 if outside else 0)
+        check((loss, h.total), want, bound)
+    if T > 1:  # none counts
+        none = [torch.full_like(rest[0], -1), *rest[1:]]
+        assert not h.forward(x, c["W"][0], *none).any() and h.total == 0
+
+
+@pytest.mark.parametrize("tau", [None, 2.0])
+def test_scores_captured(px, tau):
+    K = 1 if tau is None else 6
+    c = make(10, 128, 700, K, "bf16", seed=0)
+    h = head(c, tau, backward=False, weight_grad=False)
+    x, W, rest = c["x"][0].clone(), c["W"][0], device(c, tau is not None)
+    h.forward(x, W, *rest)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h.forward(x, W, *rest)
+        h.forward(x, W, *rest)
+    for seed in (1, 2):
+        n = make(10, 128, 700, K, "bf16", seed=seed, ignored=0.3)
+        x.copy_(n["x"][0])
+        W.copy_(n["W"][0])
+        for a, b in zip(rest, device(n, tau is not None)):
+            a.copy_(b)
+        graph.replay()
+        status_ok(px)
+        want, bound = expected(n, tau)
+        check((h.loss, h.total), want, bound)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_two_objects_at_once(px, dtype):
+    """Two heads on two streams, enqueued in turn: both as alone."""
+    cases = [make(300, 256, 2000, 1, dtype, seed=1), make(200, 512, 3000, 5, dtype, seed=2)]
+    taus = [None, 2.0]
+    heads = [head(c, t) for c, t in zip(cases, taus)]
+    rest = [device(c, t is not None) for c, t in zip(cases, taus)]
+    alone = []
+    for h, c, r in zip(heads, cases, rest):
+        out = (*h.step(c["x"][0], c["W"][0], *r), h.total)
+        torch.cuda.synchronize()
+        alone.append([v.clone() for v in out])
+    streams = [torch.cuda.Stream() for _ in heads]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for h, c, r, s in zip(heads, cases, rest, streams):
+            h.step(c["x"][0], c["W"][0], *r, stream=s)
+    torch.cuda.synchronize()
+    status_ok(px)
+    for h, want in zip(heads, alone):
+        assert all(torch.equal(a, b) for a, b in zip((h.loss, h.dx, h.dW, h.total), want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weights_of_every_size(px, dtype):
+    """Weights 2^60 apart, negative ones and zeros: each token's gradient has its own."""
+    c = make(90, 64, 400, 1, dtype, seed=4)
+    c["w"] = c["w"] * np.where(np.arange(90) % 3 == 0, 2.0 ** -30, 2.0 ** 30) * np.where(
+        np.arange(90) % 5 == 0, -1, 1)
+    c["w"][7] = 0.0
+    run_and_check(px, c, None, c["w"])
