@@ -44,8 +44,8 @@ struct Shape {
   static constexpr uint32_t TMEM_COLS = BT < 32 ? 32 : BT;
   // For the losses K's steps are shared out over several accumulators, which are
   // added up with round-to-nearest: the tensor core's own accumulation truncates (24
-  // tokens, K = 2048: losses 2.9e-6 off with one, 2.8e-7 with eight).
-  static constexpr int ACCS = BT <= 32 ? 8 : BT <= 64 ? 4 : 1;
+  // tokens, K = 2048: losses 2.9e-6 off with one, 2.1e-7 with eight).
+  static constexpr int ACCS = BT <= 64 ? 256 / BT : 1;  // 16, 8, 4
   static constexpr uint32_t LOSS_COLS = ACCS * BT < 32 ? 32 : ACCS * BT;
   static_assert(PART <= RING, "the partial tile fits the ring");
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
@@ -229,7 +229,9 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
   const int per = (p.k_steps + p.splits - 1) / p.splits;
   const int k_begin = slice * per;
   const int steps = max(0, min(p.k_steps, k_begin + per) - k_begin);
-  const int accs = LOSS ? min(S::ACCS, steps) : 1;  // accumulators that are used
+  // K steps per accumulator: 256 of K or what gives them all a share
+  const int per_acc = LOSS ? max(4, (steps + S::ACCS - 1) / S::ACCS) : max(1, steps);
+  const int accs = (steps + per_acc - 1) / per_acc;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
@@ -295,6 +297,8 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     constexpr uint32_t IDESC = instr_desc_bf16(BM, BT, A_MN, false);
+    int in_acc = 0;
+    uint32_t d_at = 0;  // the accumulator's first column
     int st = 0;
     uint32_t phase = 0;
     for (int i = 0; i < steps; ++i) {
@@ -307,17 +311,19 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
       // 16 of K: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
       const uint64_t adesc0 = smem_desc_sw128(a_base, A_MN ? 8192 : 16, 1024);
       const uint64_t bdesc0 = smem_desc_sw128(a_base + S::A, 16, 1024);
-      // step i belongs to accumulator i accs / steps
-      const int acc = LOSS ? i * accs / steps : 0;
-      const bool begins = LOSS ? i == 0 || (i - 1) * accs / steps != acc : i == 0;
+      const bool begins = LOSS ? in_acc == 0 : i == 0;
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < BK / 16; ++j)
-          umma_bf16(tmem + static_cast<uint32_t>(acc * BT), adesc0 + j * (A_MN ? 128 : 2),
+          umma_bf16(tmem + (LOSS ? d_at : 0), adesc0 + j * (A_MN ? 128 : 2),
                     bdesc0 + j * 2, IDESC, (!begins || j > 0) ? 1u : 0u);
         umma_commit(&empty_bar[st]);
       }
       __syncwarp();
+      if (LOSS && ++in_acc == per_acc) {
+        in_acc = 0;
+        d_at += BT;
+      }
       if (++st == S::STAGES) {
         st = 0;
         phase ^= 1;
@@ -337,15 +343,24 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::CTAS)
 #pragma unroll 2
     for (int c = (warp >> 2) * 16; c < live_t; c += 32) {
       uint32_t r[16];
-      tmem_load_16(t_base + c, r);
-      if (LOSS) {
-        for (int a = 1; a < accs; ++a) {
-          uint32_t more[16];
-          tmem_load_16(t_base + static_cast<uint32_t>(a * BT) + c, more);
+      if (!LOSS) {
+        tmem_load_16(t_base + c, r);
+      } else {  // four accumulators at a time
+        float sum[16] = {};
+        for (int a = 0; a < accs; a += 4) {
+          uint32_t q[4][16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(more[j]));
+          for (int i = 0; i < 4; ++i)
+            tmem_load_16_begin(t_base + static_cast<uint32_t>(min(a + i, accs - 1) * BT) + c, q[i]);
+          tmem_load_wait();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (a + i < accs)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[j] += __uint_as_float(q[i][j]);
         }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(sum[j]);
       }
 #pragma unroll
       for (int j = 0; j < 16; ++j)

@@ -350,7 +350,7 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
   __shared__ float2 sums[kThreads / 32][R];
   __shared__ double totals[R];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int count = a.targets != nullptr ? 0 : *a.rows.count;
+  const int count = a.direct ? 0 : *a.rows.count;
   const long long n = max(0ll, min(a.block, (a.direct ? a.T : count) - a.first));
   const long long r0 = blockIdx.x * static_cast<long long>(R);
   if (r0 >= n) return;
@@ -513,9 +513,11 @@ __global__ void __launch_bounds__(kThreads, 4) loss_finish_kernel(const FinishAr
   finish_rows<R>(a);
   if (!a.last) return;
   long long tokens;  // that count
-  if (a.targets != nullptr) {  // T is kFewTokens at most
+  if (a.direct) {  // T is kFewTokens at most
     long long i = -1;
-    if (threadIdx.x < a.T) i = index_at(a.targets, a.target_bytes, threadIdx.x);
+    if (threadIdx.x < a.T)
+      i = a.targets != nullptr ? index_at(a.targets, a.target_bytes, threadIdx.x)
+                               : a.rows.pos[threadIdx.x];
     tokens = __syncthreads_count(i >= 0 && i < a.V);
   } else {
     tokens = *a.rows.count;
@@ -1034,7 +1036,7 @@ cudaError_t head_loss(const LossArgs& a, void* scratch, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   const bool direct = few_form(a);
-  if (!direct || !ce) {  // else the two kernels of few_logits take the targets themselves
+  if (!direct) {  // else the kernels of few_logits take targets or entries as they are
     e = launched("loss_order", s, [&] {
       return launch_pdl(loss_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, l, a.T, a.weights,
                         plan.blocks, ce ? a.indices : nullptr, a.index_bytes, a.V,
