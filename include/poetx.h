@@ -387,12 +387,14 @@ poetx_status poetx_adam_update_many(int n_tensors, float* const* theta, const fl
  * and neither its x nor its weight is used (they may be NaN).  If no token
  * counts, total and dW are 0.
  * Logits, softmax, losses and sums are fp32.  BF16 rounds the softmax's terms to
- * bf16 for the gradients' products, and dx and dW once more.  A logit that is
- * not finite makes its token's loss and gradients what the formulas say (inf
- * or NaN).
- * The tokens that count are taken block_tokens at a time (0: as many as keep the
- * workspace's largest part at 2 GiB); the workspace holds one block's terms, in
- * BF16 with dW and more than one block also dW in fp32.  That of `tokens`
+ * bf16 for the gradients' products, and dx and dW once more; F32 takes weighted
+ * terms below 2^-109 as 0.  A logit that is not finite (or above 2^126 tau) makes
+ * its token's loss and gradients inf or NaN, and with them dW.
+ * The tokens that count are taken block_tokens at a time (rounded up to a
+ * multiple of 64; 0: as many as keep one block's terms within 2 GiB).  The
+ * workspace holds the gathered x and one block's terms, in BF16 with dW and more
+ * than one block also dW in fp32, in F32 with gradients the operands of its
+ * products too (up to about five times the terms, and W).  That of `tokens`
  * tokens is enough for any fewer with the same block_tokens; gradients: what is
  * wanted (POETX_GRAD_X | POETX_GRAD_W).
  * 1 <= d, vocab <= 2^20, 1 <= top <= 1024, 1/64 <= temperature <= 64.

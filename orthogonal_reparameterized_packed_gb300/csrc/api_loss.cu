@@ -14,7 +14,9 @@ constexpr int64_t kMaxTokens = 1ll << 22;
 constexpr int kMaxFeatures = 1 << 20;
 constexpr int kMaxTop = 1024;
 
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+bool aligned(const void* p, uintptr_t to) {
+  return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0;
+}
 
 poetx_status to_status(cudaError_t e) { return e == cudaSuccess ? POETX_OK : POETX_ERR_CUDA; }
 

@@ -73,8 +73,8 @@ constexpr int kEntryWarps = 4;
 constexpr int kMostEntries = 1024;
 
 // The entries of a token, a warp each: p = softmax of the teacher's logits at tau
-// over the entries that are there, sorted by their indices.  Differences are divided by tau, not the logits: the type's lowest value
-// stays finite.
+// over the entries that are there, sorted by their indices.  Differences are divided
+// by tau, not the logits: the type's lowest value stays finite.
 __global__ void __launch_bounds__(32 * kEntryWarps)
     loss_entries_kernel(const void* indices, int index_bytes, const void* logits, bool logits_bf16,
                         long long T, int top, int V, float inv_tau, LossRows l, int* status) {
@@ -214,7 +214,9 @@ __global__ void __launch_bounds__(kOrderThreads)
     for (int w = 0; w < 32; ++w) most = fmaxf(most, largest[w]);
     *l.count = before;
     *l.done = 0;
-    *l.most = weights == nullptr ? 1.f / static_cast<float>(max(1, before)) : most > 0.f ? most : 1.f;
+    *l.most = weights == nullptr ? 1.f / static_cast<float>(max(1, before))
+              : most > 0.f       ? most
+                                 : 1.f;
     if (outside) atomicCAS(status, 0, static_cast<int>(POETX_ERR_INVALID_ARG));
   }
 }
@@ -257,7 +259,8 @@ __global__ void __launch_bounds__(kThreads)
     const long long r = t - T;
     const long long n = *l.count;
     if (r >= n && r < (zero_all ? T : (n + 63) / 64 * 64))
-      for (int c = lane * V; c < d; c += 32 * V) *reinterpret_cast<P*>(at_row(xg, r, ldx, c)) = zero;
+      for (int c = lane * V; c < d; c += 32 * V)
+        *reinterpret_cast<P*>(at_row(xg, r, ldx, c)) = zero;
     return;
   }
   const int at = l.pos[t];
@@ -341,12 +344,13 @@ __device__ void total_behind(const LossRows& l, long long count, float by, float
   sum_total<THREADS>(l, count, by, total);
 }
 
-// R rows per CTA, 4 or, for few rows, 1.  The parts of their sums (all threads), then a warp per row:
-// its loss, its factor, and in E the entries' terms e - p sum.  A row whose reference
-// does not fit sets its block's flag.  The second pass does this again where the flag
-// is set, and scales the rows of x for dW.
-template <int R>
+constexpr int kFinishRows = 4;  // 32-byte sectors of the parts
+
+// kFinishRows rows per CTA.  The parts of their sums (all threads), then a warp per row: its loss, its factor, and in E the entries' terms e - p sum.  A row
+// whose reference does not fit sets its block's flag.  The second pass does this again
+// where the flag is set, and scales the rows of x for dW.
 __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
+  constexpr int R = kFinishRows;
   __shared__ float2 sums[kThreads / 32][R];
   __shared__ double totals[R];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -451,7 +455,9 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
           // The row's factor takes up what the rounding of its entries' terms has in
           // common (least squares; for one entry all of it): these are most of the
           // gradient, and their errors would be a whole row's of dx and dW.
-          const float fit = square > 0.f ? both / square : 1.f;
+          // That is within a rounding, 2^-8, unless all of them are next to nothing.
+          float fit = both / square;
+          if (!(fabsf(fit - 1.f) <= 0.0078125f)) fit = 1.f;
           a.rows.scale[r] = make_float2(
               a.tau / s * fit, a.weights != nullptr ? weight : 1.f / static_cast<float>(count));
           const float above = m * a.unit - ref;
@@ -501,16 +507,16 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (i < rows) x[i * a.ldx + c] = __float2bfloat16_rn(__bfloat162float(x[i * a.ldx + c]) * by[i]);
+        if (i < rows)
+          x[i * a.ldx + c] = __float2bfloat16_rn(__bfloat162float(x[i * a.ldx + c]) * by[i]);
     }
   }
 }
 
-template <int R>
 __global__ void __launch_bounds__(kThreads, 4) loss_finish_kernel(const FinishArgs a) {
   pdl_wait();
   pdl_trigger();
-  finish_rows<R>(a);
+  finish_rows(a);
   if (!a.last) return;
   long long tokens;  // that count
   if (a.direct) {  // T is kFewTokens at most
@@ -522,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 4) loss_finish_kernel(const FinishAr
   } else {
     tokens = *a.rows.count;
   }
-  const long long count = ((a.direct ? a.T : tokens) + R - 1) / R;
+  const long long count = ((a.direct ? a.T : tokens) + kFinishRows - 1) / kFinishRows;
   const float by = a.weights == nullptr ? static_cast<float>(max(1ll, tokens)) : 1.f;
   if (!a.second || a.rows.again[a.first / a.block] != 0)
     total_behind<kThreads>(a.rows, count, by, a.total);
@@ -530,8 +536,9 @@ __global__ void __launch_bounds__(kThreads, 4) loss_finish_kernel(const FinishAr
     sum_total<kThreads>(a.rows, count, by, a.total);
 }
 
-// A CTA per row of the block: its loss from the fp32 logits z, and in
-// place of them dz where the gradients are wanted (rows that do not count: 0).
+// A CTA per row of the block: its loss from the fp32 logits z, and in place of them dz
+// where the gradients are wanted (rows that do not count: 0).  Two passes over the row,
+// 16 bytes at a time.
 template <int THREADS>
 __device__ __forceinline__ void loss_row(float* __restrict__ z, long long ld, const LossRows& l,
                                          long long first, int V, int top, float inv_tau, float tau,
@@ -640,8 +647,8 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, long long ld, co
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
-    loss_rows_kernel(float* __restrict__ z, long long ld, LossRows l, long long first, int V, int top,
-                     float inv_tau, float tau, const float* __restrict__ weights, bool grad,
+    loss_rows_kernel(float* __restrict__ z, long long ld, LossRows l, long long first, int V,
+                     int top, float inv_tau, float tau, const float* __restrict__ weights, bool grad,
                      float* __restrict__ loss, bool last, float* __restrict__ total) {
   pdl_wait();
   pdl_trigger();
@@ -706,14 +713,16 @@ struct Plan {
   long long block;  // rows taken at a time, a multiple of 64
   int blocks;
   long long ldx, lde, ldp;
-  size_t meta = 0, again, pos, token, index, p, ent, lead, z, totals, ref, scale, xg, wp, terms, part, acc,
-         cut, turned, scratch, total;
+  size_t meta = 0, again, pos, token, index, p, ent, lead, z, totals, ref, scale, xg, wp, terms,
+         part, acc, cut, turned, scratch, total;
   Plan(const LossArgs& a, bool want_dx, bool want_dw) {
     const size_t T = static_cast<size_t>(a.T), es = a.is_bf16 ? 2 : 4;
     const bool grad = want_dx || want_dw;
     lde = a.is_bf16 ? round64(a.V) : (a.V + 3) / 4 * 4;  // 16-byte rows
     ldx = pitch_of(a.d, a.is_bf16);
-    block = a.block > 0 ? a.block : static_cast<long long>(kBlockBytes / es / static_cast<size_t>(lde) / 64 * 64);
+    block = a.block > 0
+                ? a.block
+                : static_cast<long long>(kBlockBytes / es / static_cast<size_t>(lde) / 64 * 64);
     block = std::max(64ll, std::min(round64(block), round64(a.T)));
     blocks = static_cast<int>((a.T + block - 1) / block);
     ldp = block;
@@ -723,7 +732,7 @@ struct Plan {
       at += round256(bytes);
       return here;
     };
-    again = take(4 * T);  // a block has at least 64 rows, but fewer tokens more blocks
+    again = take(4 * static_cast<size_t>(blocks));
     pos = take(4 * T);
     token = take(4 * T);
     index = take(4 * T * a.top);
@@ -792,7 +801,11 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Losses alone of a few tokens: from x as it lies, the weight streamed once.  The
-// rows do not touch each other, so tokens that do not count may run along.
+// rows do not touch each other, so tokens that do not count may run along.  In graphs
+// behind a flush of L2, streamed / on CTA pairs: 2048 -> 32000, one token 43 / 56 us,
+// 64 46 / 57; 4096 -> 128256, one 181 / 207, 64 197 / 214.  From 65 to 128 tokens it is
+// 52 / 56 and 224 / 217, but the tile's accumulators are too wide for several of them,
+// which the losses' precision takes.
 bool few_form(const LossArgs& a) {
   return a.is_bf16 && a.dx == nullptr && a.dW == nullptr && a.T <= kFewTokens && a.d % 8 == 0;
 }
@@ -873,8 +886,6 @@ cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, cha
   f.E = E;
   f.lde = g.lde;
   f.ldx = g.ldx;
-  // a row of many parts is a CTA's work where there are few rows
-  const bool few = plan.block <= 2 * sm_count();
   f.T = a.T;
   f.total = a.total;
   for (int b = 0; b < plan.blocks; ++b) {
@@ -889,11 +900,10 @@ cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, cha
       f.x = a.dW != nullptr ? xb : nullptr;
       f.last = b == plan.blocks - 1 && (!grad || pass == 1);
       e = launched("loss_finish", s, [&] {
-        return few ? launch_pdl(loss_finish_kernel<1>, dim3(static_cast<unsigned>(plan.block)),
-                                dim3(kThreads), 0, s, f)
-                   : launch_pdl(loss_finish_kernel<4>,
-                                dim3(static_cast<unsigned>((plan.block + 3) / 4)), dim3(kThreads),
-                                0, s, f);
+        return launch_pdl(
+            loss_finish_kernel,
+            dim3(static_cast<unsigned>((plan.block + kFinishRows - 1) / kFinishRows)),
+            dim3(kThreads), 0, s, f);
       });
       if (e != cudaSuccess) return e;
     }
@@ -1047,7 +1057,8 @@ cudaError_t head_loss(const LossArgs& a, void* scratch, cudaStream_t s) {
   if (direct)
     e = cudaSuccess;
   else if (a.is_bf16)
-    e = a.d % 8 == 0 ? run_gather<bf16, 8>(a, plan, l, ws, s) : run_gather<bf16, 1>(a, plan, l, ws, s);
+    e = a.d % 8 == 0 ? run_gather<bf16, 8>(a, plan, l, ws, s)
+                     : run_gather<bf16, 1>(a, plan, l, ws, s);
   else
     e = a.d % 4 == 0 ? run_gather<float, 4>(a, plan, l, ws, s)
                      : run_gather<float, 1>(a, plan, l, ws, s);

@@ -5,8 +5,9 @@
 // The kernel is linear_pair's with other epilogues: clusters of two CTAs compute
 // tiles of 256 x 256 with tcgen05.mma.cta_group::2 over 64-wide K steps from a TMA
 // ring, two TMEM accumulators; warp 0 loads, warp 1 issues the MMAs, and behind their
-// warpgroup 16 epilogue warps take 64 columns of a 32-row quarter each.  dw's A is E as it lies, [rows][V]: an MN-major operand.  The rows are
-// counted on the GPU: tiles behind the last row are not computed.
+// warpgroup 16 epilogue warps take 64 columns of a 32-row quarter each.  dw's A is E as
+// it lies, [rows][V]: an MN-major operand.  The rows are counted on the GPU: tiles
+// behind the last row are not computed.
 //
 // The logits are never stored.  A tile's epilogue takes each z once: its
 // exponential relative to the row's reference, the sum and the largest of 64
@@ -340,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         bool any_mma = false;
         int tile, ks0, ks1, part_slot;
-        for (int i = 0; products && ok && todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
+        for (int i = 0;
+             products && ok && todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
           for (int kc = ks0; kc < ks1 && ok; kc += kDrain) {
             const int kc1 = LOGITS ? min(ks1, kc + kDrain) : ks1;
             if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1, abort_flag)) {

@@ -41,7 +41,9 @@ class _HeadLoss:
         self.dx = torch.empty((tokens, d), dtype=self.dtype, device=dev) if backward else None
         self.dW = torch.empty((vocab, d), dtype=self.dtype, device=dev) if weight_grad else None
         ws = self._workspace_size(GRAD_X * bool(backward) + GRAD_W * bool(weight_grad))
-        # a forward of this object takes no more
+        if ws == 0 and tokens > 0:
+            raise ValueError(f"a head of {vocab} x {d} for {tokens} tokens with {top} entries each "
+                             "is outside the limits")
         ws = max(ws, self._workspace_size(0), 16)
         self.workspace = torch.empty((ws,), dtype=torch.uint8, device=dev)
         self._device = self.loss.get_device()

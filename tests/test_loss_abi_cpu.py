@@ -156,7 +156,8 @@ def test_classes_refuse_what_the_kernels_would_read_wrongly(calls):
     assert [n for n, _ in calls] == ["poetx_cross_entropy", "poetx_distill", "poetx_distill"]
 
 
-def test_classes_refuse_what_they_were_not_made_for(calls):
+def test_classes_refuse_what_they_were_not_made_for(calls, monkeypatch, L):
+    from orthogonal_reparameterized_packed_gb300 import loss as loss_module
     from orthogonal_reparameterized_packed_gb300.loss import PoetxCrossEntropy, PoetxDistill
     x, W, y = on_gpu(8, 16), on_gpu(50, 16), on_gpu(8, dtype=torch.int64)
     with pytest.raises(RuntimeError):
@@ -166,6 +167,11 @@ def test_classes_refuse_what_they_were_not_made_for(calls):
     for block in (0, -1):
         with pytest.raises(ValueError):
             PoetxDistill(16, 50, 8, top=2, device="cpu", block_tokens=block)
+    monkeypatch.setattr(loss_module, "poetx_distill_workspace_size",
+                        poetx.poetx_distill_workspace_size)
+    for top in (0, 1025):
+        with pytest.raises(ValueError, match="limits"):
+            PoetxDistill(16, 50, 8, top=top, device="cpu")
     loss, dx, dW = PoetxCrossEntropy(16, 50, 8, device="cpu", backward=True).step(x, W, y)
     assert dW is None and calls[0][1][8] is None
 
