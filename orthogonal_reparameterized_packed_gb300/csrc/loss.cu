@@ -235,20 +235,95 @@ struct alignas(sizeof(T) * V) Pack {
   T x[V];
 };
 
+// What loss_gather_kernel does in loss_order_kernel's place for up to kStartTokens.
+struct StartArgs {
+  const void* targets;  // null: distillation, pos is 0 or -1
+  int index_bytes, V, blocks;
+  const float* weights;
+  int* status;
+};
+
+constexpr long long kStartTokens = 2048;
+
 // A warp per token: the tokens that count to their rows, zeros to dx and loss of
 // the others; warps from T on: zeros to the rows behind the last, to all of them or
 // up to a multiple of 64.  unit: log2(e) / tau where references are wanted, else 0.
-// V values (16 bytes) at a time.
-template <typename TX, int V>
+// V values (16 bytes) at a time.  START: up to kStartTokens tokens every CTA counts
+// those before its own, which saves the launch that orders them (64 tokens, 1024 ->
+// 32000, with dx and dW: 86.2 -> 84.2 us).
+template <typename TX, int V, bool START>
 __global__ void __launch_bounds__(kThreads)
     loss_gather_kernel(const TX* __restrict__ x, const TX* __restrict__ W, LossRows l, long long T,
                        int d, TX* __restrict__ xg, long long ldx, bool zero_all, float unit,
-                       float* __restrict__ loss, TX* __restrict__ dx) {
+                       float* __restrict__ loss, TX* __restrict__ dx, const StartArgs start) {
   using P = Pack<TX, V>;
+  __shared__ int counts[2][kThreads / 32];
+  __shared__ float largest[kThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x % 32;
-  const long long t = blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const long long t0 = blockIdx.x * static_cast<long long>(kThreads / 32), t = t0 + warp;
+  long long n, at = -1, lead = 0;
+  if (START) {
+    const auto index_of = [&](long long i) {  // -1: does not count
+      if (start.targets == nullptr) return static_cast<long long>(l.pos[i]);
+      const long long v = index_at(start.targets, start.index_bytes, i);
+      return v < start.V ? v : -1ll;
+    };
+    int before = 0, all = 0;
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < kStartTokens / kThreads; ++i) {
+      const long long u = i * kThreads + threadIdx.x;
+      if (u >= T || index_of(u) < 0) continue;
+      ++all;
+      before += u < t0;
+      if (blockIdx.x == 0 && start.weights != nullptr)
+        most = fmaxf(most, fabsf(start.weights[u]));
+    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    before = __reduce_add_sync(0xffffffffu, before);
+    most = warp_max(most);
+    if (lane == 0) counts[0][warp] = all, counts[1][warp] = before, largest[warp] = most;
+    __syncthreads();
+    all = before = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      all += counts[0][w];
+      before += counts[1][w];
+      most = fmaxf(most, largest[w]);
+    }
+    n = all;
+    if (blockIdx.x == 0) {
+      for (int i = threadIdx.x; i < start.blocks; i += kThreads) l.again[i] = 0;
+      if (threadIdx.x == 0) {
+        *l.count = all;
+        *l.done = 0;
+        *l.most = start.weights == nullptr ? 1.f / static_cast<float>(max(1, all))
+                  : most > 0.f             ? most
+                                           : 1.f;
+      }
+    }
+    // the tokens of this CTA before the warp's
+    const long long first = t0 + lane < T && lane < warp ? index_of(t0 + lane) : -1;
+    const long long own = t < T ? index_of(t) : -1;
+    before += __popc(__ballot_sync(0xffffffffu, first >= 0));
+    if (own >= 0) at = before;
+    if (t < T && lane == 0 && start.targets != nullptr) {
+      l.index[t] = own >= 0 ? static_cast<int>(own) : -1;
+      l.p[t] = 1.f;
+      l.ent[t] = 0.f;
+      if (index_at(start.targets, start.index_bytes, t) >= start.V)
+        atomicCAS(start.status, 0, static_cast<int>(POETX_ERR_INVALID_ARG));
+    }
+    if (own >= 0 && lane == 0) l.token[at] = static_cast<int>(t);
+    lead = start.targets != nullptr ? own : own >= 0 ? l.lead[t] : 0;
+  } else {
+    n = *l.count;
+    if (t < T) {
+      at = l.pos[t];
+      lead = l.lead[t];
+    }
+  }
   const auto at_row = [&](auto* base, long long row, long long ld, int c) {
     return base + row * ld + c;
   };
@@ -257,15 +332,12 @@ __global__ void __launch_bounds__(kThreads)
   for (int j = 0; j < V; ++j) from_f(zero.x[j], 0.f);
   if (t >= T) {
     const long long r = t - T;
-    const long long n = *l.count;
     if (r >= n && r < (zero_all ? T : (n + 63) / 64 * 64))
       for (int c = lane * V; c < d; c += 32 * V)
         *reinterpret_cast<P*>(at_row(xg, r, ldx, c)) = zero;
     return;
   }
-  const int at = l.pos[t];
   if (at >= 0) {
-    const long long lead = l.lead[t];
     float dot = 0.f;
 #pragma unroll 4
     for (int c = lane * V; c < d; c += 32 * V) {
@@ -1000,13 +1072,29 @@ template <typename TX, int V>
 cudaError_t run_gather(const LossArgs& a, const Plan& plan, const LossRows& l, char* ws,
                        cudaStream_t s) {
   const bool grad = a.dx != nullptr || a.dW != nullptr;
+  const bool start = a.T <= kStartTokens;
+  StartArgs st;
+  st.targets = a.top_logits == nullptr ? a.indices : nullptr;
+  st.index_bytes = a.index_bytes;
+  st.V = a.V;
+  st.blocks = plan.blocks;
+  st.weights = a.weights;
+  st.status = device_status_ptr();
+  cudaError_t e;
+  if (!start) {
+    e = launched("loss_order", s, [&] {
+      return launch_pdl(loss_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, l, a.T, a.weights,
+                        plan.blocks, st.targets, a.index_bytes, a.V, st.status);
+    });
+    if (e != cudaSuccess) return e;
+  }
   return launched("loss_gather", s, [&] {
-    return launch_pdl(loss_gather_kernel<TX, V>, dim3(warps_grid(a.T + round64(a.T))),
-                      dim3(kThreads), 0, s, static_cast<const TX*>(a.x),
-                      static_cast<const TX*>(a.W), l, a.T, a.d,
+    return launch_pdl(start ? loss_gather_kernel<TX, V, true> : loss_gather_kernel<TX, V, false>,
+                      dim3(warps_grid(a.T + round64(a.T))), dim3(kThreads), 0, s,
+                      static_cast<const TX*>(a.x), static_cast<const TX*>(a.W), l, a.T, a.d,
                       reinterpret_cast<TX*>(ws + plan.xg), plan.ldx, !a.is_bf16,
                       a.is_bf16 && grad ? 1.44269504089f / a.tau : 0.f, a.loss,
-                      static_cast<TX*>(a.dx));
+                      static_cast<TX*>(a.dx), st);
   });
 }
 
@@ -1045,16 +1133,8 @@ cudaError_t head_loss(const LossArgs& a, void* scratch, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
   }
-  const bool direct = few_form(a);
-  if (!direct) {  // else the kernels of few_logits take targets or entries as they are
-    e = launched("loss_order", s, [&] {
-      return launch_pdl(loss_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, l, a.T, a.weights,
-                        plan.blocks, ce ? a.indices : nullptr, a.index_bytes, a.V,
-                        device_status_ptr());
-    });
-    if (e != cudaSuccess) return e;
-  }
-  if (direct)
+  // the kernels of few_logits take targets or entries as they are
+  if (few_form(a))
     e = cudaSuccess;
   else if (a.is_bf16)
     e = a.d % 8 == 0 ? run_gather<bf16, 8>(a, plan, l, ws, s)

@@ -55,7 +55,7 @@ def run_and_check(px, c, tau, weights=None, **kw):
 SHAPES = [(1, 1, 1), (1, 64, 128), (1, 512, 3001), (2, 8, 5), (3, 7, 300), (16, 256, 1000),
           (17, 72, 257), (24, 264, 2049), (33, 96, 255), (64, 128, 512), (65, 320, 777),
           (127, 40, 1030), (128, 64, 128), (130, 512, 4099), (255, 136, 640), (257, 192, 1281),
-          (300, 1000, 513), (513, 256, 1024), (600, 65, 901), (1100, 128, 300), (70, 2048, 3000)]
+          (300, 1000, 513), (513, 256, 1024), (600, 65, 901), (2047, 64, 130), (2049, 72, 100), (1100, 128, 300), (70, 2048, 3000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -80,7 +80,8 @@ def test_long_and_wide(px, T, d, V, dtype):
 @pytest.mark.parametrize("T,d,V,K,tau", [
     (1, 64, 300, 16, 2.0), (1, 9, 4, 3, 1.0), (5, 128, 1000, 1, 1.0), (40, 256, 2051, 7, 4.0),
     (129, 192, 515, 33, 0.5), (260, 96, 3000, 64, 1.5), (33, 72, 100, 100, 3.0),
-    (300, 320, 1300, 20, 1.0), (12, 64, 5000, 1024, 2.0), (515, 512, 777, 130, 64.0)])
+    (300, 320, 1300, 20, 1.0), (12, 64, 5000, 1024, 2.0), (515, 512, 777, 130, 64.0),
+    (2048, 72, 130, 3, 2.0), (2049, 64, 300, 5, 2.0)])
 def test_distill(px, T, d, V, K, tau, dtype):
     c = make(T, d, V, K, dtype, seed=T + K, ignored=0.3 if T > 2 else 0.0)
     run_and_check(px, c, tau, c["w"] if T % 2 else None)
