@@ -45,7 +45,7 @@ struct Shape {
   // For the losses K's steps are shared out over several accumulators, which are
   // added up with round-to-nearest: the tensor core's own accumulation truncates (24
   // tokens, K = 2048: losses 2.9e-6 off with one, 2.1e-7 with eight).
-  static constexpr int ACCS = BT <= 64 ? 256 / BT : 1;  // 16, 8, 4
+  static constexpr int ACCS = BT <= 64 ? 256 / BT : 1;  // up to 64 tokens 16, 8, 4
   static constexpr uint32_t LOSS_COLS = ACCS * BT < 32 ? 32 : ACCS * BT;
   static_assert(PART <= RING, "the partial tile fits the ring");
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
@@ -482,21 +482,28 @@ cudaError_t launch(const LinearProduct& g, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <bool A_MN, bool LOSS>
+template <bool A_MN>
 cudaError_t run(const LinearProduct& g, cudaStream_t s) {
-  if (g.M <= 16) return launch<16, A_MN, LOSS>(g, s);
-  if (g.M <= 32) return launch<32, A_MN, LOSS>(g, s);
-  if (g.M <= 64) return launch<64, A_MN, LOSS>(g, s);
-  if (g.M <= 128) return launch<128, A_MN, LOSS>(g, s);
-  return launch<256, A_MN, LOSS>(g, s);
+  if (g.M <= 16) return launch<16, A_MN, false>(g, s);
+  if (g.M <= 32) return launch<32, A_MN, false>(g, s);
+  if (g.M <= 64) return launch<64, A_MN, false>(g, s);
+  if (g.M <= 128) return launch<128, A_MN, false>(g, s);
+  return launch<256, A_MN, false>(g, s);
+}
+
+// Tiles of more tokens have no room for several accumulators.
+cudaError_t run_loss(const LinearProduct& g, cudaStream_t s) {
+  if (g.M <= 16) return launch<16, false, true>(g, s);
+  if (g.M <= 32) return launch<32, false, true>(g, s);
+  return launch<64, false, true>(g, s);
 }
 
 }  // namespace
 
 cudaError_t linear_stream(const LinearProduct& g, cudaStream_t s) {
   if (g.M <= 0 || g.N <= 0 || g.K <= 0) return cudaSuccess;
-  if (g.loss != nullptr) return run<false, true>(g, s);
-  return g.b_mn ? run<true, false>(g, s) : run<false, false>(g, s);
+  if (g.loss != nullptr) return run_loss(g, s);
+  return g.b_mn ? run<true>(g, s) : run<false>(g, s);
 }
 
 }  // namespace poetx
