@@ -183,6 +183,16 @@ __device__ __forceinline__ void registers_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
 }
 
+// "The accumulator has been read": what it orders are TMEM accesses, by the tcgen05
+// fences on both sides, and no memory, so it need not wait, as a release would, for
+// the stores of the tile before (64 rows, 1024 -> 32000, dW 24.5 -> 18.6 us; 3000 x 256
+// -> 32000, forward 84 -> 74).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t bar_cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                   bar_cluster_addr)
+               : "memory");
+}
+
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     loss_pair_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -479,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           // the accumulator is free again once both CTAs' epilogue warps have read it
-          if (lane == 0) mbar_arrive_remote(tempty0 + static_cast<uint32_t>(acc * 8));
+          if (lane == 0) mbar_arrive_remote_relaxed(tempty0 + static_cast<uint32_t>(acc * 8));
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
         }
@@ -524,7 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sum = 0.f, top_z = -INFINITY;
         if (!STORE) {  // the reference is the largest of the 64 columns
 #pragma unroll
-          for (int j = 0; j < 64; ++j) top_z = fmaxf(top_z, z[j]);
+          for (int j = 0; j < 64; j += 4)
+            top_z = fmaxf(top_z, fmaxf(fmaxf(z[j], z[j + 1]), fmaxf(z[j + 2], z[j + 3])));
           ref = top_z == -INFINITY ? 0.f : top_z * p.unit;
         }
 #pragma unroll
@@ -546,10 +557,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
 #pragma unroll
-          for (int j = c; j < c + kChunk; ++j) {
-            if (STORE) top_z = fmaxf(top_z, z[j]);
-            z[j] = exp2_fast(fmaf(z[j], p.unit, -ref));
-            sum += z[j];
+          for (int j = c; j < c + kChunk; j += 4) {
+            if (STORE)
+              top_z = fmaxf(top_z, fmaxf(fmaxf(z[j], z[j + 1]), fmaxf(z[j + 2], z[j + 3])));
+#pragma unroll
+            for (int i = j; i < j + 4; ++i) z[i] = exp2_fast(fmaf(z[i], p.unit, -ref));
+            sum += (z[j] + z[j + 1]) + (z[j + 2] + z[j + 3]);
           }
           if (STORE) {
 #pragma unroll
@@ -662,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         // the accumulator is free again once both CTAs' epilogue warps have read it
-        if (lane == 0) mbar_arrive_remote(tempty0 + static_cast<uint32_t>(acc * 8));
+        if (lane == 0) mbar_arrive_remote_relaxed(tempty0 + static_cast<uint32_t>(acc * 8));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }
