@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         // the accumulator is free again once both CTAs' epilogue warps have read it
-        if (lane == 0) mbar_arrive_remote(tempty0 + static_cast<uint32_t>(acc * 8));
+        if (lane == 0) mbar_arrive_remote_relaxed(tempty0 + static_cast<uint32_t>(acc * 8));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }

@@ -183,16 +183,6 @@ __device__ __forceinline__ void registers_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
 }
 
-// "The accumulator has been read": what it orders are TMEM accesses, by the tcgen05
-// fences on both sides, and no memory, so it need not wait, as a release would, for
-// the stores of the tile before (64 rows, 1024 -> 32000, dW 24.5 -> 18.6 us; 3000 x 256
-// -> 32000, forward 84 -> 74).
-__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t bar_cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                   bar_cluster_addr)
-               : "memory");
-}
-
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     loss_pair_kernel(const __grid_constant__ CUtensorMap tmA,

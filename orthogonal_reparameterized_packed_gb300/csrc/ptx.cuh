@@ -199,6 +199,16 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster_addr) {
                : "memory");
 }
 
+// The same without the release, for "this accumulator has been read": what that
+// orders are TMEM accesses, by the tcgen05 fences on both sides, and no memory, so it
+// need not wait, as a release does, for the stores of the tile before (dW of 64 tokens,
+// 1024 -> 32000: 24.5 -> 18.6 us; the fp32 products 3 %).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t bar_cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                   bar_cluster_addr)
+               : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(

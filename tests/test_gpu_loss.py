@@ -108,6 +108,39 @@ def test_logits_of_any_size(px, tau, dtype, x_scale):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("tau", [None, 2.0])
+def test_some_blocks_with_wide_logits(px, tau, dtype):
+    """Targets hundreds below the largest logit in some blocks of tokens only."""
+    c = make(300, 72, 900, 1 if tau is None else 5, dtype, seed=11, ignored=0.1)
+    c["idx"][100:130] = np.random.default_rng(5).integers(0, 900, c["idx"][100:130].shape)
+    x = c["x"][0].clone()
+    x[100:130] *= 64.0  # exact
+    c["x"] = (x, host(x))
+    for block in (None, 64):
+        run_and_check(px, c, tau, c["w"], block_tokens=block)
+    few = dict(c, T=20, idx=c["idx"][100:120], s=c["s"][100:120], w=c["w"][100:120],
+               x=(x[100:120].clone(), host(x[100:120])))
+    want, bound = expected(few, tau)
+    h = head(few, tau, backward=False, weight_grad=False)
+    loss = h.forward(few["x"][0], few["W"][0], *device(few, tau is not None))
+    status_ok(px)
+    check((loss, h.total), want, bound)
+
+
+@pytest.mark.parametrize("tau", [None, 2.0])
+@pytest.mark.parametrize("T,d,V,block", [(64, 512, 9000, None), (300, 256, 5000, 128),
+                                         (333, 768, 4001, None)])
+def test_f32_values_that_the_tensor_cores_do_not_take(px, T, d, V, block, tau):
+    """Below 2^-109, in a token and in W: their products on the CUDA cores, dx' slices too."""
+    for where in ("x", "W"):
+        c = make(T, d, V, 1 if tau is None else 5, "f32", seed=T, ignored=0.1)
+        t = c[where][0].clone()
+        t[3, :7] = 1e-36
+        c[where] = (t, host(t))
+        run_and_check(px, c, tau, block_tokens=block)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [None, 2.0])
 def test_tokens_that_do_not_count(px, tau, dtype):
     """Their x, weights and logits may hold anything; rows behind the call's tokens keep
     what they hold."""
