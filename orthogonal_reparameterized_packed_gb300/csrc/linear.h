@@ -67,7 +67,7 @@ cudaError_t linear_simt(const LinearProduct& g, cudaStream_t s);
 
 // In fp32 on the tensor cores, as six bf16 products (linear_split.cu); layouts
 // as for linear_simt, scratch of linear_split_scratch(g) bytes.
-bool linear_split_pays(long long M, int N, int K, int slices = 1);
+bool linear_split_pays(long long M, int N, int K);
 size_t linear_split_scratch(const LinearProduct& g);
 size_t linear_split_scratch_up_to(const LinearProduct& g);  // of any product of at most g.M rows
 cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s);
@@ -81,7 +81,7 @@ cudaError_t linear_fp32(const LinearProduct& g, void* scratch, cudaStream_t s);
 // Pieces of K, 2 to kMaxFp32Slices with outputs of at most most_bytes, where these
 // are faster than linear_fp32 on the whole of K: a product of few tiles and a long K.
 // Else 1.
-constexpr int kMaxFp32Slices = 16;
+constexpr int kMaxFp32Slices = 32;
 int linear_split_slices(long long M, int N, int K, size_t most_bytes);
 
 }  // namespace poetx

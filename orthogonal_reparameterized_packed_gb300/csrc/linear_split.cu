@@ -576,7 +576,7 @@ double loop_us(long long M, int N, int K, bool* narrow, int slices = 1) {
 namespace {
 
 // With 4 bytes written and read per output and slice.
-double split_us(long long M, int N, int K, int slices) {
+double split_us(long long M, int N, int K, int slices = 1) {
   bool narrow;
   return 18.0 + loop_us(M, N, K, &narrow, slices) +
          10e-6 * K * (static_cast<double>(M) + N) / 6.0 +
@@ -588,8 +588,8 @@ double split_us(long long M, int N, int K, int slices) {
 // By the measured costs of both: here the loops above, 18 us for three launches
 // and the pipeline's ends, and 10 bytes per element of the operands for their
 // planes; linear_simt 8 us and 45 TFLOP/s.  They cross near 1000^3.
-bool linear_split_pays(long long M, int N, int K, int slices) {
-  return split_us(M, N, K, slices) < 8.0 + 2e-6 * M * N * K / 45.0;
+bool linear_split_pays(long long M, int N, int K) {
+  return split_us(M, N, K) < 8.0 + 2e-6 * M * N * K / 45.0;
 }
 
 // A slice has at least four K steps, none is empty.  333 x 30001 -> 768 (6 tiles of
@@ -597,7 +597,7 @@ bool linear_split_pays(long long M, int N, int K, int slices) {
 int linear_split_slices(long long M, int N, int K, size_t most_bytes) {
   const int steps = (K + BK - 1) / BK;
   int best = 1;
-  double least = split_us(M, N, K, 1);
+  double least = split_us(M, N, K);
   for (int n = 2; n <= kMaxFp32Slices && steps / n >= 4; ++n) {
     if (4ull * n * M * N > most_bytes) break;
     if ((steps + n - 1) / n * (n - 1) >= steps) continue;
@@ -607,7 +607,12 @@ int linear_split_slices(long long M, int N, int K, size_t most_bytes) {
       best = n;
     }
   }
-  return linear_split_pays(M, N, K, best) ? best : 1;
+  // linear_simt, with at most eight slices of its own: at least 0.05 us (up to 16 tokens
+  // 0.03) for a k of one (512 x 128256 -> 64: 1900 us, here 310 with
+  // the operands' planes)
+  const double simt =
+      8.0 + std::max(2e-6 * M * N * K / 45.0, (M <= 16 ? 0.03 : 0.05) * K / 8.0);
+  return split_us(M, N, K, best) < simt ? best : 1;
 }
 
 namespace {

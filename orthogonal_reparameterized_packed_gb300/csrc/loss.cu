@@ -764,9 +764,8 @@ __global__ void __launch_bounds__(kThreads)
   const long long t = l.token[first + r];
   if (slices > 1 && *whole != 0) slices = 1;
   float v = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxFp32Slices; ++i)
-    if (i < slices) v += rows[(i * block + r) * d + c];
+#pragma unroll 8
+  for (int i = 0; i < slices; ++i) v += rows[(i * block + r) * d + c];
   dx[t * d + c] = v;
 }
 

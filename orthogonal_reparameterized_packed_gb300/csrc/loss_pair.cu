@@ -48,7 +48,7 @@ constexpr int kSmem = kRing + kEpiWarps * kSlot + 256;
 constexpr int kGroupM = 8;
 constexpr uint32_t kAcc = 256;  // TMEM columns of an accumulator
 constexpr int kLeastShare = 8;   // K steps of a slice
-constexpr int kMaxSlices = 16;
+constexpr int kMaxSlices = 64;
 constexpr int kSlots = 4;        // slices' tiles per cluster at most
 constexpr float kCutCost = 20.f;
 // The tensor core's accumulation truncates: over 2048 of K a logit comes out 4e-6 of
@@ -80,9 +80,9 @@ struct Schedule {
     const int left = tiles % clusters;
     if (!may_cut || left == 0) return;
     float best = static_cast<float>(steps);
-    for (int n = 2; n <= kMaxSlices && n * left <= kSlots * clusters; ++n) {
-      const int len = (steps + n - 1) / n;
-      if (len < kLeastShare) break;
+    for (int i = 4; i <= 2 * kMaxSlices; i += i & (i - 1) ? i / 3 : i / 2) {  // 2, 3, 4, 6, 8, 12 ..
+      const int n = i / 2, len = (steps + n - 1) / n;
+      if (n * left > kSlots * clusters || len < kLeastShare) break;
       const float cost = static_cast<float>((n * left + clusters - 1) / clusters * len) +
                          0.4f * static_cast<float>(n * left) + kCutCost;
       if (cost < best && len * (n - 1) < steps) {
