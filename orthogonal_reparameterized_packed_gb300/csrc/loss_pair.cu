@@ -173,9 +173,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// A block of 640 threads has 96 registers each, 61440.  The logits' epilogue keeps 64
-// sums a thread and takes 112 (512 threads: 57344), the first warpgroup keeps 32
-// (4096).  With 96 the sums spilled, and took twice the time.
+// Registers.  The logits' epilogue keeps 64 sums a thread and takes 112 (512 threads),
+// the first warpgroup keeps 32 (128): 61440, which is what 640 threads have at the
+// launch with 96 each.  With 96 in the epilogue the sums spilled, and the product took
+// twice the time.  Fewer at the launch would make the epilogue wait for ever: launch()
+// refuses that.
+constexpr int kLaunchRegisters = 96;
+static_assert(kThreads == 640 && 512 * 112 + 128 * 32 <= kThreads * kLaunchRegisters, "registers");
+
 __device__ __forceinline__ void registers_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
 }
@@ -266,8 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t full0 = map_peer(smem_u32(full_bar), 0);
   const uint32_t tempty0 = map_peer(smem_u32(tempty_bar), 0);
 
-  // Registers: 640 threads get 96 each at the launch, 61440; the epilogue of the logits
-  // takes 112 (57344), the first four warps keep 32 (4096).
   if (warp < 4) {  // the same for each warpgroup, as setmaxnreg needs
     if (LOGITS) registers_down();
     if (warp == 0) {
@@ -589,6 +592,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         token = p.rows.token[p.first + row];
         scale = p.rows.scale[p.first + row];
       }
+      if (KIND == kDw && p.acc != nullptr && p.first > 0 && live && on) {
+        // the sums of the blocks before, into L2 under the main loop
+        const float* sums = p.acc + row * p.N + side_col;
+        for (int c = 0; c < 64 && side_col + c < p.N; c += 32)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(sums + c));
+      }
       if (products) {
         const bool got = mbar_wait_cluster(&tfull_bar[acc], acc_phase, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
@@ -640,12 +649,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 16; ++j) v[j] *= most;
             if (acc_row != nullptr && on) {
               float* at = acc_row + part * 16;
+              if (p.vec) {  // whole quads are inside
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (j < in) {
-                  if (p.first > 0) v[j] += at[j];
-                  if (!last) at[j] = v[j];
+                for (int j = 0; j < 16; j += 4) {
+                  if (j >= in) continue;
+                  float4* quad = reinterpret_cast<float4*>(at + j);
+                  if (p.first > 0) {
+                    const float4 q = *quad;
+                    v[j] += q.x, v[j + 1] += q.y, v[j + 2] += q.z, v[j + 3] += q.w;
+                  }
+                  if (!last) *quad = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                 }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (j < in) {
+                    if (p.first > 0) v[j] += at[j];
+                    if (!last) at[j] = v[j];
+                  }
+              }
             }
           }
           stage_part(slot, lane, part, v);
@@ -793,6 +815,12 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
       e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
       if (e != cudaSuccess) return e;
       if (n < 1) return cudaErrorLaunchOutOfResources;
+      if (KIND == kLogits || KIND == kStats) {
+        cudaFuncAttributes has;
+        e = cudaFuncGetAttributes(&has, kernel);
+        if (e != cudaSuccess) return e;
+        if (has.numRegs < kLaunchRegisters) return cudaErrorLaunchOutOfResources;
+      }
       max_clusters[dev] = n;
       ready[dev] = true;
     }
