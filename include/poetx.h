@@ -393,8 +393,8 @@ poetx_status poetx_adam_update_many(int n_tensors, float* const* theta, const fl
  * The tokens that count are taken block_tokens at a time (rounded up to a
  * multiple of 64; 0: as many as keep one block's terms within 2 GiB).  The
  * workspace holds the gathered x and one block's terms, in BF16 with dW and more
- * than one block also dW in fp32, in F32 with gradients the operands of its
- * products too (up to about five times the terms, and W).  That of `tokens`
+ * than one block also dW in fp32, in F32 what its products split (one and a half
+ * times the terms, the block's x and W) and up to 64 MiB of dx' parts.  That of `tokens`
  * tokens is enough for any fewer with the same block_tokens; gradients: what is
  * wanted (POETX_GRAD_X | POETX_GRAD_W).
  * 1 <= d, vocab <= 2^20, 1 <= top <= 1024, 1/64 <= temperature <= 64.

@@ -42,14 +42,17 @@ struct LinearProduct {
   const int* all_rows = nullptr;
   const int* row_flags = nullptr;
   int segs = 0;
-  // fp32: elements between A's rows and between y's (z's, residual's), 0: K and N.  Up
+  bool a_mn = false;  // linear_simt: A is [K][M], with b_mn
+  // fp32: elements between A's rows and between y's (z's, residual's), 0: none lie between.  Up
   // to three of y's elements behind a row's last are written.
   long long pitch_a = 0, pitch_y = 0;
   // linear_fp32: K in `slices` pieces whose products are apart, piece i's in y + i M pitch_y
-  // (no bias, residual or activation); linear_fp32_slices says how many pay
+  // (no bias, residual or activation); linear_split_slices says how many pay
   int slices = 1;
   // linear_split: the last product on this scratch had the same array B
   bool b_ready = false;
+  // linear_split: linear_planes_bytes(M, K) for A's planes, null: they are in the scratch
+  void* a_planes = nullptr;
   const LossColumns* loss = nullptr;  // linear_stream with B [N][K]
   const char* tag = "linear";
 };
@@ -60,19 +63,28 @@ cudaError_t linear_pair(const LinearProduct& g, cudaStream_t s);
 // For few tokens: the weight streamed once, K split over a cluster (linear_stream.cu).
 cudaError_t linear_stream(const LinearProduct& g, cudaStream_t s);
 
-// In fp32 on the CUDA cores (linear_simt.cu): A, y, z, residual contiguous unless
-// pitch_a, pitch_y say otherwise, B [N][K] or, b_mn, [K][N] contiguous; lda, ldb and
-// ld are not used.
+// In fp32 on the CUDA cores (linear_simt.cu): A ([M][K], or a_mn), y, z, residual
+// contiguous unless pitch_a, pitch_y say otherwise, B [N][K] or, b_mn, [K][N]
+// contiguous; lda, ldb and ld are not used.
 cudaError_t linear_simt(const LinearProduct& g, cudaStream_t s);
 
 // In fp32 on the tensor cores, as six bf16 products (linear_split.cu); layouts
 // as for linear_simt, scratch of linear_split_scratch(g) bytes.
 bool linear_split_pays(long long M, int N, int K);
 size_t linear_split_scratch(const LinearProduct& g);
+size_t linear_split_b_scratch(const LinearProduct& g);  // with a_planes
 size_t linear_split_scratch_up_to(const LinearProduct& g);  // of any product of at most g.M rows
 cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s);
 // Whether linear_split left *scratch not 0: values of B are for the CUDA cores, which
 // computed everything (with slices, the first slice).
+
+// An fp32 array [rows][cols], ld apart, as planes that are kept.
+size_t linear_planes_bytes(long long rows, int cols);
+cudaError_t linear_split_planes(const float* in, long long rows, int cols, long long ld, void* at,
+                                cudaStream_t s);
+// With a_mn and b_mn, from the kept planes of A and B.
+cudaError_t linear_split_turned(const LinearProduct& g, void* a_planes, void* b_planes,
+                                cudaStream_t s);
 
 // In fp32 in the form that takes less time, with linear_split_scratch_up_to(g) bytes
 // of scratch or more (linear.cu); in slices always linear_split.

@@ -1,5 +1,6 @@
 // The matrix products of poetx_linear_* in fp32, on the CUDA cores:
 //   C[M][N] = act(A B + bias) + residual,  A [M][K], B(k, n) = W[n][k] or W[k][n]
+//   (the latter also with A [K][M])
 // Tiles of 16 RM x 128, 256 threads, RM x 8 outputs each (RM = 8, 4, 2: the
 // tile's rows by the number of tokens), K in steps of 16 (64 for few rows, where
 // the bytes in flight count): the next step's operands come into registers
@@ -100,7 +101,8 @@ __device__ __forceinline__ void finish(const SimtArgs& p, long long m, int n, fl
 }
 
 // Grid: x = N tile * splits + slice (a cluster along x), y = row tile.
-template <int RM, bool B_KN, bool FLAT>
+// A_KM: A is [K][M].
+template <int RM, bool A_KM, bool B_KN, bool FLAT>
 __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs p) {
   using S = Shape<RM, FLAT>;
   constexpr int TM = S::TM, LDA = S::LDA, kTK = S::TK;
@@ -133,7 +135,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
       int row, quad;
       piece<TM, KQ>(e, row, quad);
       if (QA % kThreads == 0 || e < QA)
-        ra[q] = load4(p.A, m0 + row, p.M, k + quad * 4, k1, p.lda, p.vec_a);
+        ra[q] = A_KM ? load4(p.A, k + e / (TM / 4), k1, static_cast<int>(m0) + e % (TM / 4) * 4,
+                             static_cast<int>(p.M), p.lda, p.vec_a)
+                     : load4(p.A, m0 + row, p.M, k + quad * 4, k1, p.lda, p.vec_a);
     }
 #pragma unroll
     for (int q = 0; q < NB; ++q) {
@@ -148,7 +152,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_simt_kernel(const SimtArgs
 #pragma unroll
     for (int q = 0; q < NA; ++q) {
       const int e = threadIdx.x + q * kThreads;
-      if (QA % kThreads == 0 || e < QA) {
+      if (A_KM && (QA % kThreads == 0 || e < QA)) {
+        *reinterpret_cast<float4*>(as + e / (TM / 4) * LDA + e % (TM / 4) * 4) = ra[q];
+      } else if (QA % kThreads == 0 || e < QA) {
         int row, quad;
         piece<TM, KQ>(e, row, quad);
         float* d = as + quad * 4 * LDA + row;
@@ -335,11 +341,11 @@ Slices slices_for(long long tiles, int K, int step, double per_k, bool powers) {
 // us per k of a CTA's tile, measured (1024 of K in one slice).
 constexpr double kPerK8 = 0.105, kPerK4 = 0.067, kPerK2 = 0.052, kPerKFlat = 0.03;
 
-template <int RM, bool B_KN, bool FLAT>
+template <int RM, bool A_KM, bool B_KN, bool FLAT>
 cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, double per_k,
                    cudaStream_t stream) {
   using S = Shape<RM, FLAT>;
-  auto* kernel = linear_simt_kernel<RM, B_KN, FLAT>;
+  auto* kernel = linear_simt_kernel<RM, A_KM, B_KN, FLAT>;
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaGetDevice(&dev);
@@ -351,8 +357,8 @@ cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, do
     ready[dev].store(true, std::memory_order_relaxed);
   }
   SimtArgs p;
-  p.lda = g.pitch_a > 0 ? g.pitch_a : g.K;
-  p.A = static_cast<const float*>(g.A) + m_first * p.lda;
+  p.lda = g.pitch_a > 0 ? g.pitch_a : A_KM ? g.M : g.K;
+  p.A = static_cast<const float*>(g.A) + m_first * (A_KM ? 1 : p.lda);
   p.B = static_cast<const float*>(g.B);
   p.epi = fp32_epilogue(g, m_first);
   p.M = rows;
@@ -392,8 +398,9 @@ cudaError_t launch(const LinearProduct& g, long long m_first, long long rows, do
 template <int RM, bool FLAT = false>
 cudaError_t by_major(const LinearProduct& g, long long m, long long rows, double per_k,
                      cudaStream_t s) {
-  return g.b_mn ? launch<RM, true, FLAT>(g, m, rows, per_k, s)
-               : launch<RM, false, FLAT>(g, m, rows, per_k, s);
+  if (g.a_mn) return launch<RM, true, true, FLAT>(g, m, rows, per_k, s);
+  return g.b_mn ? launch<RM, false, true, FLAT>(g, m, rows, per_k, s)
+                : launch<RM, false, false, FLAT>(g, m, rows, per_k, s);
 }
 
 }  // namespace

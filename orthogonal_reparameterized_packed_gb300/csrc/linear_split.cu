@@ -72,10 +72,11 @@ struct SplitArgs {
   int plane_rows_a, plane_rows_b;  // rows between planes of A, of B
   long long M;
   Fp32Epilogue epi;
-  int segs;              // flags per row of A
+  int segs;              // flags per row of A; 0: A is [K][M]
   const int* row_flags;  // A's: rows with one that is not 0 are left to linear_simt
-  int b_flags;           // flags of B, behind `all`: then all rows are
-  int* all;              // set here: whether any of B's is
+  int flags;             // flags of B, and of A where it is [K][M]: then all rows are
+  const int *a_flags, *b_flags;
+  int* all;              // set here: whether any of those is
   int* status;
 };
 
@@ -94,7 +95,7 @@ __device__ __forceinline__ void unit_tile(int u, const SplitArgs& p, int& mp, in
   nt = r / rows;
 }
 
-template <int BN, bool B_MN>
+template <int BN, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB, const SplitArgs p) {
@@ -148,7 +149,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
   int bad = 0;
-  for (int i = threadIdx.x; i < p.b_flags; i += kThreads) bad |= p.all[1 + i];
+  for (int i = threadIdx.x; i < p.flags; i += kThreads) {
+    bad |= p.b_flags[i];
+    if (A_MN) bad |= p.a_flags[i];
+  }
   bad = __syncthreads_or(bad);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.all = bad;
   const int units = bad != 0 ? 0 : p.m_pairs * p.n_tiles * p.slices;
@@ -171,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k0 = begin; k0 < end && ok; k0 += kChunkSteps) {
         const int k1 = min(end, k0 + kChunkSteps);
         for (int pr = 0; pr < kProducts && ok; ++pr) {
-          const int ra = plane_a(pr) * p.plane_rows_a + a_row;
+          const int ra = plane_a(pr) * p.plane_rows_a;
           const int rb = plane_b(pr) * p.plane_rows_b;
           for (int ks = k0; ks < k1; ++ks) {
             if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) {
@@ -184,7 +188,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint8_t* a_dst = ring + stage * kStage;
               uint8_t* b_dst = a_dst + kA;
               const uint32_t bar = full0 + static_cast<uint32_t>(stage * 8);
-              tma_load_2d_pair(a_dst, &tmA, bar, ks * BK, ra);
+              if (!A_MN) {
+                tma_load_2d_pair(a_dst, &tmA, bar, ks * BK, ra + a_row);
+              } else {
+                tma_load_2d_pair(a_dst, &tmA, bar, a_row, ra + ks * BK);
+                tma_load_2d_pair(a_dst + 8192, &tmA, bar, a_row + 64, ra + ks * BK);
+              }
               if (!B_MN) {
                 tma_load_2d_pair(b_dst, &tmB, bar, ks * BK, rb + b_n);
               } else {
@@ -220,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (leader) {
       // -------------------------------------------------- MMA issuer (pair)
-      constexpr uint32_t IDESC = instr_desc_bf16(2 * BM, kBN, false, B_MN);
+      constexpr uint32_t IDESC = instr_desc_bf16(2 * BM, kBN, A_MN, B_MN);
       const uint32_t empty_own = smem_u32(empty_bar);
       const uint32_t tfull_own = smem_u32(tfull_bar);
       int stage = 0;
@@ -249,12 +258,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const uint32_t a_base = smem_u32(ring) + stage * kStage;
-            const uint64_t adesc0 = smem_desc_sw128(a_base, 16, 1024);
+            const uint64_t adesc0 = smem_desc_sw128(a_base, A_MN ? 8192 : 16, 1024);
             const uint64_t bdesc0 = smem_desc_sw128(a_base + kA, B_MN ? 8192 : 16, 1024);
             if (elect_one()) {
 #pragma unroll
               for (int j = 0; j < BK / 16; ++j)
-                umma_bf16_pair(d_tmem, adesc0 + j * 2, bdesc0 + j * (B_MN ? 128 : 2), IDESC,
+                umma_bf16_pair(d_tmem, adesc0 + j * (A_MN ? 128 : 2),
+                               bdesc0 + j * (B_MN ? 128 : 2), IDESC,
                                (i > 0 || j > 0) ? 1u : 0u);
               umma_commit_both(empty_own + static_cast<uint32_t>(stage * 8));
             }
@@ -373,16 +383,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 // One operand: in [rows][cols] fp32 -> planes [3][plane_rows][pitch] bf16, rows
 // from `rows` to plane_rows zero (columns past cols are not read by any tile);
 // flag[r][segs]: whether a value of the row's segment of kSegment columns is
-// neither 0 nor of a magnitude that the planes take.  Of B a flag per CTA, `flags` of
-// them, is enough: one for every row (30001) made each CTA of the product read them
-// for 20 us.
+// neither 0 nor of a magnitude that the planes take.  Where those of all rows count
+// together (B's, and A's as [K][M]), a flag per CTA, `flags` of them, is enough: one for
+// every row (30001) made each CTA of the product read them for 20 us.
 constexpr int kSegment = 1024;
 constexpr unsigned kLeastBits = (127u - 109u) << 23, kMostBits = (127u + 60u) << 23;
 
 struct SplitOperand {
   const float* in;
   bf16* planes;
-  int* flag;
+  int* flag;   // null: none
+  int* whole;  // the CTAs'; null: none
   long long rows, ld, plane_rows, pitch;
   int cols, segs;
 };
@@ -394,7 +405,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     split_planes_kernel(const SplitOperand a, const SplitOperand b, int flags) {
   pdl_wait();
   pdl_trigger();
-  bool bad_b = false;
+  bool bad_a = false, bad_b = false;
   const int lane = threadIdx.x % 32;
   const long long items_a = a.plane_rows * a.segs, items = items_a + b.plane_rows * b.segs;
   for (long long it = blockIdx.x * static_cast<long long>(kSplitThreads / 32) + threadIdx.x / 32;
@@ -448,16 +459,18 @@ __global__ void __launch_bounds__(kSplitThreads)
       }
     }
     bad = __any_sync(0xffffffffu, bad);
-    if (!first)
-      bad_b |= bad;
-    else if (lane == 0)
-      o.flag[at] = bad;
+    (first ? bad_a : bad_b) |= bad;
+    if (o.flag != nullptr && lane == 0) o.flag[at] = bad;
   }
-  if (b.plane_rows == 0) return;  // B's were made before
-  bad_b = __syncthreads_or(bad_b);
-  if (blockIdx.x == 0)
-    for (int i = gridDim.x + threadIdx.x; i < flags; i += kSplitThreads) b.flag[i] = 0;
-  if (threadIdx.x == 0) b.flag[blockIdx.x] = bad_b;
+  const auto whole = [&](int* to, bool bad) {
+    if (to == nullptr) return;
+    bad = __syncthreads_or(bad);
+    if (blockIdx.x == 0)
+      for (int i = gridDim.x + threadIdx.x; i < flags; i += kSplitThreads) to[i] = 0;
+    if (threadIdx.x == 0) to[blockIdx.x] = bad;
+  };
+  whole(a.whole, bad_a);
+  whole(b.whole, bad_b);
 }
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -482,11 +495,12 @@ size_t planes_bytes(long long plane_rows, int cols) {
   return round256(static_cast<size_t>(kPlanes) * plane_rows * pitch64(cols) * 2);
 }
 
-template <int BN, bool B_MN>
-cudaError_t launch(const LinearProduct& g, const void* a_planes, const void* b_planes,
-                   int* all, const int* row_flags, cudaStream_t stream) {
+// a, b: their planes and flags; A_MN: a is [K][M].
+template <int BN, bool A_MN, bool B_MN>
+cudaError_t launch(const LinearProduct& g, const SplitOperand& a, const SplitOperand& b, int* all,
+                   cudaStream_t stream) {
   constexpr int kSmem = Shape<BN>::SMEM, kBN = BN;
-  auto* kernel = linear_split_kernel<BN, B_MN>;
+  auto* kernel = linear_split_kernel<BN, A_MN, B_MN>;
   static bool ready[64] = {false};
   static int max_clusters[64] = {0};
   static std::mutex mu;
@@ -524,12 +538,11 @@ cudaError_t launch(const LinearProduct& g, const void* a_planes, const void* b_p
     cmax = max_clusters[dev];
   }
   SplitArgs p;
-  p.plane_rows_a = static_cast<int>(g.M);
-  p.plane_rows_b = static_cast<int>(b_plane_rows(g));
+  p.plane_rows_a = static_cast<int>(a.plane_rows);
+  p.plane_rows_b = static_cast<int>(b.plane_rows);
   CUtensorMap tmA, tmB;
-  if (!make_map(&tmA, a_planes, kPlanes * g.M, g.K, pitch64(g.K), 2, 64, BM))
-    return cudaErrorInvalidValue;
-  if (!make_map(&tmB, b_planes, kPlanes * b_plane_rows(g), b_cols(g), pitch64(b_cols(g)), 2, 64,
+  if (!make_map(&tmA, a.planes, kPlanes * a.plane_rows, a.cols, a.pitch, 2, 64, A_MN ? 64 : BM) ||
+      !make_map(&tmB, b.planes, kPlanes * b.plane_rows, b.cols, b.pitch, 2, 64,
                 B_MN ? 64 : kBN / 2))
     return cudaErrorInvalidValue;
   p.m_pairs = static_cast<int>((g.M + 2 * BM - 1) / (2 * BM));
@@ -541,9 +554,11 @@ cudaError_t launch(const LinearProduct& g, const void* a_planes, const void* b_p
   p.M = g.M;
   p.epi = fp32_epilogue(g, 0);
   p.all = all;
-  p.row_flags = row_flags;
-  p.segs = segments(g.K);
-  p.b_flags = split_ctas();
+  p.row_flags = A_MN ? nullptr : a.flag;
+  p.segs = A_MN ? 0 : a.segs;
+  p.flags = split_ctas();
+  p.a_flags = a.whole;
+  p.b_flags = b.whole;
   p.status = device_status_ptr();
   const int clusters = static_cast<int>(
       std::min<long long>(static_cast<long long>(p.m_pairs) * p.n_tiles * p.slices, cmax));
@@ -617,18 +632,63 @@ int linear_split_slices(long long M, int N, int K, size_t most_bytes) {
 
 namespace {
 
-size_t row_flag_bytes(const LinearProduct& g) {
-  return round256(static_cast<size_t>(g.M * segments(g.K)) * sizeof(int));
+long long up64(long long n) { return (n + 63) / 64 * 64; }
+
+size_t flag_bytes(long long rows, int cols) {
+  return round256(static_cast<size_t>(rows * segments(cols)) * sizeof(int));
 }
 
 size_t all_flag_bytes() { return round256((1 + split_ctas()) * sizeof(int)); }
 
+SplitOperand operand(const void* in, long long rows, int cols, long long ld,
+                     long long plane_rows) {
+  SplitOperand o = {};
+  o.in = static_cast<const float*>(in);
+  o.rows = rows;
+  o.cols = cols;
+  o.ld = ld > 0 ? ld : cols;
+  o.plane_rows = plane_rows;
+  o.segs = segments(cols);
+  o.pitch = pitch64(cols);
+  return o;
+}
+
+// An operand that is kept, at a place of linear_planes_bytes: a word that says whether
+// the CUDA cores take all of it, the CTAs' flags, the rows', the planes.
+SplitOperand kept(void* at, const void* in, long long rows, int cols, long long ld) {
+  SplitOperand o = operand(in, rows, cols, ld, up64(rows));
+  char* c = static_cast<char*>(at);
+  o.whole = reinterpret_cast<int*>(c) + 1;
+  o.flag = reinterpret_cast<int*>(c + all_flag_bytes());
+  o.planes = reinterpret_cast<bf16*>(c + all_flag_bytes() + flag_bytes(o.plane_rows, cols));
+  return o;
+}
+
+// The planes of a, and of b unless it is null.
+cudaError_t split(const SplitOperand& a, const SplitOperand* b, cudaStream_t s) {
+  const SplitOperand other = b != nullptr ? *b : operand(nullptr, 0, 1, 1, 0);
+  const int grid = static_cast<int>(std::min<long long>(
+      (a.plane_rows * a.segs + other.plane_rows * other.segs + 7) / 8, split_ctas()));
+  prof_begin("linear_split_planes", s);
+  const cudaError_t e = launch_pdl(split_planes_kernel, dim3(grid), dim3(kSplitThreads), 0, s, a,
+                                   other, split_ctas());
+  prof_end("linear_split_planes", s);
+  return e;
+}
+
 }  // namespace
+
+size_t linear_planes_bytes(long long rows, int cols) {
+  return all_flag_bytes() + flag_bytes(up64(rows), cols) + planes_bytes(up64(rows), cols);
+}
+
+size_t linear_split_b_scratch(const LinearProduct& g) {
+  return all_flag_bytes() + planes_bytes(b_plane_rows(g), b_cols(g));
+}
 
 // B's flags and planes come first: their place depends on B alone.
 size_t linear_split_scratch(const LinearProduct& g) {
-  return all_flag_bytes() + planes_bytes(b_plane_rows(g), b_cols(g)) + row_flag_bytes(g) +
-         planes_bytes(g.M, g.K);
+  return linear_split_b_scratch(g) + flag_bytes(g.M, g.K) + planes_bytes(g.M, g.K);
 }
 
 // Whether this form is taken does not grow with the rows: a new pair of row tiles
@@ -647,48 +707,54 @@ size_t linear_split_scratch_up_to(const LinearProduct& g) {
 }
 
 cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) {
-  SplitOperand a, b;
   int* all = static_cast<int*>(scratch);
-  char* b_at = static_cast<char*>(scratch) + all_flag_bytes();
-  char* a_at = b_at + planes_bytes(b_plane_rows(g), b_cols(g));
-  int* row_flags = reinterpret_cast<int*>(a_at);
-  a.in = static_cast<const float*>(g.A);
-  a.planes = reinterpret_cast<bf16*>(a_at + row_flag_bytes(g));
-  a.flag = row_flags;
-  a.rows = a.plane_rows = g.M;
-  a.cols = g.K;
-  a.ld = g.pitch_a > 0 ? g.pitch_a : g.K;
-  a.segs = segments(a.cols);
-  a.pitch = pitch64(a.cols);
-  b.in = static_cast<const float*>(g.B);
-  b.planes = reinterpret_cast<bf16*>(b_at);
-  b.flag = all + 1;
-  b.rows = g.b_mn ? g.K : g.N;
-  b.plane_rows = g.b_ready ? 0 : b_plane_rows(g);
-  b.cols = b_cols(g);
-  b.ld = b.cols;
-  b.segs = segments(b.cols);
-  b.pitch = pitch64(b.cols);
-  const int grid = static_cast<int>(
-      std::min<long long>((a.plane_rows * a.segs + b_plane_rows(g) * b.segs + 7) / 8,
-                          split_ctas()));
-  prof_begin("linear_split_planes", s);
-  cudaError_t e =
-      launch_pdl(split_planes_kernel, dim3(grid), dim3(kSplitThreads), 0, s, a, b, split_ctas());
-  prof_end("linear_split_planes", s);
+  SplitOperand a, b = operand(g.B, g.b_mn ? g.K : g.N, b_cols(g), 0, b_plane_rows(g));
+  b.whole = all + 1;
+  b.planes = reinterpret_cast<bf16*>(static_cast<char*>(scratch) + all_flag_bytes());
+  if (g.a_planes != nullptr) {
+    a = kept(g.a_planes, g.A, g.M, g.K, g.pitch_a);
+  } else {
+    char* at = static_cast<char*>(scratch) + linear_split_b_scratch(g);
+    a = operand(g.A, g.M, g.K, g.pitch_a, g.M);
+    a.flag = reinterpret_cast<int*>(at);
+    a.planes = reinterpret_cast<bf16*>(at + flag_bytes(g.M, g.K));
+  }
+  cudaError_t e = split(a, g.b_ready ? nullptr : &b, s);
   if (e != cudaSuccess) return e;
   bool narrow;
   loop_us(g.M, g.N, g.K, &narrow, g.slices);
-  e = narrow ? g.b_mn ? launch<128, true>(g, a.planes, b.planes, all, row_flags, s)
-                      : launch<128, false>(g, a.planes, b.planes, all, row_flags, s)
-      : g.b_mn ? launch<256, true>(g, a.planes, b.planes, all, row_flags, s)
-               : launch<256, false>(g, a.planes, b.planes, all, row_flags, s);
+  e = narrow ? g.b_mn ? launch<128, false, true>(g, a, b, all, s)
+                      : launch<128, false, false>(g, a, b, all, s)
+      : g.b_mn ? launch<256, false, true>(g, a, b, all, s)
+               : launch<256, false, false>(g, a, b, all, s);
   if (e != cudaSuccess) return e;
   LinearProduct again = g;
   again.all_rows = all;
-  again.row_flags = row_flags;
+  again.row_flags = a.flag;
   again.slices = 1;
   again.segs = a.segs;
+  again.tag = "linear_rows";
+  return linear_simt(again, s);
+}
+
+cudaError_t linear_split_planes(const float* in, long long rows, int cols, long long ld, void* at,
+                                cudaStream_t s) {
+  const SplitOperand o = kept(at, in, rows, cols, ld);
+  return split(o, nullptr, s);
+}
+
+cudaError_t linear_split_turned(const LinearProduct& g, void* a_planes, void* b_planes,
+                                cudaStream_t s) {
+  const SplitOperand a = kept(a_planes, nullptr, g.K, static_cast<int>(g.M), 0),
+                     b = kept(b_planes, nullptr, g.K, g.N, 0);
+  bool narrow;
+  loop_us(g.M, g.N, g.K, &narrow);
+  int* all = static_cast<int*>(a_planes);
+  const cudaError_t e = narrow ? launch<128, true, true>(g, a, b, all, s)
+                               : launch<256, true, true>(g, a, b, all, s);
+  if (e != cudaSuccess) return e;
+  LinearProduct again = g;
+  again.all_rows = all;
   again.tag = "linear_rows";
   return linear_simt(again, s);
 }

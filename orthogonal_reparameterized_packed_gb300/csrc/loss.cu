@@ -418,9 +418,10 @@ __device__ void total_behind(const LossRows& l, long long count, float by, float
 
 constexpr int kFinishRows = 4;  // 32-byte sectors of the parts
 
-// kFinishRows rows per CTA.  The parts of their sums (all threads), then a warp per row: its loss, its factor, and in E the entries' terms e - p sum.  A row
-// whose reference does not fit sets its block's flag.  The second pass does this again
-// where the flag is set, and scales the rows of x for dW.
+// kFinishRows rows per CTA.  The parts of their sums (all threads), then a warp per row:
+// its loss, its factor, and in E the entries' terms e - p sum.  A row whose reference
+// does not fit sets its block's flag.  The second pass does this again where the flag is
+// set, and scales the rows of x for dW.
 __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
   constexpr int R = kFinishRows;
   __shared__ float2 sums[kThreads / 32][R];
@@ -720,34 +721,14 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, long long ld, co
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
     loss_rows_kernel(float* __restrict__ z, long long ld, LossRows l, long long first, int V,
-                     int top, float inv_tau, float tau, const float* __restrict__ weights, bool grad,
-                     float* __restrict__ loss, bool last, float* __restrict__ total) {
+                     int top, float inv_tau, float tau, const float* __restrict__ weights,
+                     bool grad, float* __restrict__ loss, bool last, float* __restrict__ total) {
   pdl_wait();
   pdl_trigger();
   loss_row<THREADS>(z, ld, l, first, V, top, inv_tau, tau, weights, grad, loss);
   if (last)
     total_behind<THREADS>(l, *l.count,
                           weights == nullptr ? static_cast<float>(max(1, *l.count)) : 1.f, total);
-}
-
-// out[c][r] = in[r][c], in [rows][cols], its rows ld apart.
-__global__ void __launch_bounds__(kThreads)
-    loss_transpose_kernel(const float* __restrict__ in, long long ld, float* __restrict__ out,
-                          int rows, int cols) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ float tile[32][33];
-  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-  const int r0 = blockIdx.x * 32, c0 = blockIdx.y * 32;
-#pragma unroll
-  for (int i = ty; i < 32; i += kThreads / 32)
-    if (r0 + i < rows && c0 + tx < cols)
-      tile[i][tx] = in[(r0 + i) * ld + c0 + tx];
-  __syncthreads();
-#pragma unroll
-  for (int i = ty; i < 32; i += kThreads / 32)
-    if (c0 + i < cols && r0 + tx < rows)
-      out[static_cast<long long>(c0 + i) * rows + r0 + tx] = tile[tx][i];
 }
 
 // dx of the block's rows, the sum of `slices` products (the first alone where the
@@ -785,7 +766,7 @@ struct Plan {
   int blocks;
   long long ldx, lde, ldp;
   size_t meta = 0, again, pos, token, index, p, ent, lead, z, totals, ref, scale, xg, wp, terms,
-         part, acc, cut, turned, scratch, total;
+         part, acc, cut, x_planes, z_planes, scratch, total;
   Plan(const LossArgs& a, bool want_dx, bool want_dw) {
     const size_t T = static_cast<size_t>(a.T), es = a.is_bf16 ? 2 : 4;
     const bool grad = want_dx || want_dw;
@@ -826,22 +807,22 @@ struct Plan {
                               std::min(kCutBytes,
                                        4 * kMaxFp32Slices * static_cast<size_t>(block) * a.d))
                    : 0);
-    turned = take(want_dw && !a.is_bf16 ? 4 * static_cast<size_t>(block) * a.V : 0);
+    const bool planes = want_dw && !a.is_bf16;
+    x_planes = take(planes ? linear_planes_bytes(block, a.d) : 0);
+    z_planes = take(planes ? linear_planes_bytes(block, a.V) : 0);
     scratch = take(a.is_bf16 ? 0 : fp32_scratch(a, want_dx, want_dw));
     total = at;
   }
 
-  // The largest of the products' scratch, for blocks of any number of rows.
+  // The largest of the products' scratch, for blocks of any number of rows.  With dW the
+  // operands' planes but W's have places of their own.
   size_t fp32_scratch(const LossArgs& a, bool want_dx, bool want_dw) const {
     LinearProduct g;
     g.M = block, g.N = a.V, g.K = a.d;
+    if (want_dw) return linear_split_b_scratch(g);
     size_t most = linear_split_scratch_up_to(g);
     if (want_dx) {
       g.N = a.d, g.K = a.V, g.b_mn = true;
-      most = std::max(most, linear_split_scratch(g));
-    }
-    if (want_dw) {  // K is the number of rows
-      g.M = a.V, g.N = a.d, g.K = static_cast<int>(block), g.b_mn = true;
       most = std::max(most, linear_split_scratch(g));
     }
     return most;
@@ -984,21 +965,25 @@ cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, cha
   return cudaSuccess;
 }
 
-// fp32: the products of linear_fp32 on a block's logits, which become dz in place,
-// and on their transpose for dW.  Rows that do not count are 0.
+// fp32: the products of linear_fp32 on a block's logits, which become dz in place.  Rows
+// that do not count are 0.  dW takes the planes that the others made of x and dz, as they
+// lie (dz transposed and split for it: 515 tokens, 1000 -> 10007 295 us, now 274; 333 tokens,
+// 768 -> 30001 440, now 399).
 cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char* ws,
                     cudaStream_t s) {
   float* xg = reinterpret_cast<float*>(ws + plan.xg);
   float* z = reinterpret_cast<float*>(ws + plan.terms);
-  float* zt = reinterpret_cast<float*>(ws + plan.turned);
   void* scratch = ws + plan.scratch;
   float* out = reinterpret_cast<float*>(ws + plan.cut);
   const bool grad = a.dx != nullptr || a.dW != nullptr;
+  char* x_planes = a.dW != nullptr ? ws + plan.x_planes : nullptr;
+  char* z_planes = a.dW != nullptr ? ws + plan.z_planes : nullptr;
   cudaError_t e;
   bool ready = false;  // W's planes are in the scratch
   for (long long first = 0; first < a.T; first += plan.block) {
     const long long rows = std::min(plan.block, a.T - first);
     float* xb = xg + first * a.d;
+    bool x_ready = false, z_ready = false;  // the block's planes
     LinearProduct g;
     g.A = xb;
     g.B = a.W;
@@ -1006,9 +991,11 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
     g.pitch_y = plan.lde;
     g.M = rows, g.N = a.V, g.K = a.d;
     g.b_ready = ready;
+    g.a_planes = x_planes;
     g.tag = "loss_logits";
     if ((e = linear_fp32(g, scratch, s)) != cudaSuccess) return e;
-    ready |= linear_split_pays(rows, a.V, a.d);
+    x_ready = linear_split_pays(rows, a.V, a.d);
+    ready |= x_ready;
     e = launched("loss_rows", s, [&] {
       // long rows take 512 threads, four CTAs on an SM: 333 of 30001 28 us (with 1024
       // a second wave), 515 of 10007 19; short ones 256
@@ -1027,11 +1014,13 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
       q.b_mn = true;
       q.slices = linear_split_slices(rows, a.d, a.V, kCutBytes);
       q.b_ready = ready;
+      q.a_planes = z_planes;
       q.y = out;
       q.M = rows, q.N = a.d, q.K = a.V;
       q.tag = "loss_dx";
       if ((e = linear_fp32(q, scratch, s)) != cudaSuccess) return e;
-      ready |= q.slices > 1 || linear_split_pays(rows, a.d, a.V);
+      z_ready = q.slices > 1 || linear_split_pays(rows, a.d, a.V);
+      ready |= z_ready;
       e = launched("loss_scatter", s, [&] {
         return launch_pdl(loss_scatter_kernel,
                           dim3(static_cast<unsigned>(rows),
@@ -1044,24 +1033,26 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
       if (e != cudaSuccess) return e;
     }
     if (a.dW != nullptr) {
-      e = launched("loss_transpose", s, [&] {
-        return launch_pdl(loss_transpose_kernel,
-                          dim3(static_cast<unsigned>((rows + 31) / 32),
-                               static_cast<unsigned>((a.V + 31) / 32)),
-                          dim3(kThreads), 0, s, static_cast<const float*>(z), plan.lde, zt,
-                          static_cast<int>(rows), a.V);
-      });
-      if (e != cudaSuccess) return e;
       LinearProduct q;
-      q.A = zt;
+      q.A = z;
+      q.pitch_a = plan.lde;
       q.B = xb;
-      q.b_mn = true;
+      q.a_mn = q.b_mn = true;
       q.residual = first > 0 ? a.dW : nullptr;
       q.y = a.dW;
       q.M = a.V, q.N = a.d, q.K = static_cast<int>(rows);
       q.tag = "loss_dw";
-      if ((e = linear_fp32(q, scratch, s)) != cudaSuccess) return e;
-      ready &= !linear_split_pays(a.V, a.d, q.K);  // else x's planes took their place
+      if (linear_split_pays(a.V, a.d, q.K)) {
+        if (!x_ready && (e = linear_split_planes(xb, rows, a.d, a.d, x_planes, s)) != cudaSuccess)
+          return e;
+        if (!z_ready &&
+            (e = linear_split_planes(z, rows, a.V, plan.lde, z_planes, s)) != cudaSuccess)
+          return e;
+        e = linear_split_turned(q, z_planes, x_planes, s);
+      } else {
+        e = linear_simt(q, s);
+      }
+      if (e != cudaSuccess) return e;
     }
   }
   return cudaSuccess;

@@ -127,6 +127,34 @@ def test_some_blocks_with_wide_logits(px, tau, dtype):
 
 
 @pytest.mark.parametrize("tau", [None, 2.0])
+@pytest.mark.parametrize("T,d,V,block,tiny", [
+    (515, 512, 5003, None, False), (700, 640, 9001, 321, False), (700, 640, 9001, 321, True)])
+def test_f32_dw_alone_and_over_blocks(px, T, d, V, block, tiny, tau):
+    """dW from planes that no dx product has made, and over blocks whose last is ragged;
+    a value below 2^-109 in one block of tokens leaves that block to the CUDA cores."""
+    c = make(T, d, V, 1 if tau is None else 5, "f32", seed=V + T, ignored=0.1)
+    if tiny:
+        t = c["x"][0].clone()
+        t[T // 2, :7] = 1e-36
+        c["x"] = (t, host(t))
+    h = run_and_check(px, c, tau, block_tokens=block)
+    want, bound = expected(c, tau)
+    dW = h.dW.clone()
+    h.dW.fill_(float("nan"))
+    idx, *rest = device(c, tau is not None)
+    out = (h.loss, h.total, None, h.dW, d, V, T)
+    end = (px.F32, h.block_tokens, h.workspace)
+    if tau is None:
+        px.poetx_cross_entropy(c["x"][0], c["W"][0], idx, 8, None, *out, *end)
+    else:
+        px.poetx_distill(c["x"][0], c["W"][0], idx, 8, rest[0], px.F32, None, *out, c["K"], tau,
+                         *end)
+    status_ok(px)
+    check((h.loss, h.total), want, bound)
+    assert torch.equal(h.dW, dW)
+
+
+@pytest.mark.parametrize("tau", [None, 2.0])
 @pytest.mark.parametrize("T,d,V,block", [(64, 512, 9000, None), (300, 256, 5000, 128),
                                          (333, 768, 4001, None)])
 def test_f32_values_that_the_tensor_cores_do_not_take(px, T, d, V, block, tau):
