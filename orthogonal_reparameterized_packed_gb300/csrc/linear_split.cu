@@ -20,8 +20,8 @@
 // those rows alone and linear_simt, enqueued behind it, computes them; its tiles
 // without such rows return at once.
 //
-// The kernel is linear_pair's with another epilogue: CTA pairs, 256 x 256 or
-// 256 x 128 tiles, 64-wide K steps in a TMA ring, one step per pair of planes;
+// The kernel is linear_pair's with another epilogue: CTA pairs, tiles of 256 x 128 to
+// 256 (tile_width), 64-wide K steps in a TMA ring, one step per pair of planes;
 // 16 epilogue warps (a quarter of the columns each) drain one of two TMEM
 // accumulators into registers while the next 128 of K go into the other.
 #include <algorithm>
@@ -68,6 +68,7 @@ __device__ __forceinline__ int plane_b(int p) { return (0x010120 >> (4 * p)) & 3
 
 struct SplitArgs {
   int m_pairs, n_tiles, k_steps, N;
+  int width;  // of a tile, BN at most
   int slices, slice_steps;  // of K; a slice's outputs are M N values behind the last's
   int plane_rows_a, plane_rows_b;  // rows between planes of A, of B
   long long M;
@@ -166,12 +167,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     long long issued = 0;
+    const uint32_t tx = 2 * (kA + static_cast<uint32_t>(p.width) * BK);  // bytes of a step
     bool ok = true;
     for (int u = first; u < units && ok; u += step) {
       int mp, nt, slice, begin, end;
       unit_tile(u, p, mp, nt, slice, begin, end);
       const int a_row = mp * 2 * BM + static_cast<int>(rank) * BM;
-      const int b_n = nt * kBN + static_cast<int>(rank) * (kBN / 2);
+      const int b_n = nt * p.width + static_cast<int>(rank) * (p.width / 2);
       for (int k0 = begin; k0 < end && ok; k0 += kChunkSteps) {
         const int k1 = min(end, k0 + kChunkSteps);
         for (int pr = 0; pr < kProducts && ok; ++pr) {
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             if (elect_one()) {
-              if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStage);
+              if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
               uint8_t* a_dst = ring + stage * kStage;
               uint8_t* b_dst = a_dst + kA;
               const uint32_t bar = full0 + static_cast<uint32_t>(stage * 8);
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (leader) {
       // -------------------------------------------------- MMA issuer (pair)
-      constexpr uint32_t IDESC = instr_desc_bf16(2 * BM, kBN, A_MN, B_MN);
+      const uint32_t IDESC = instr_desc_bf16(2 * BM, p.width, A_MN, B_MN);
       const uint32_t empty_own = smem_u32(empty_bar);
       const uint32_t tfull_own = smem_u32(tfull_bar);
       int stage = 0;
@@ -304,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int mp, nt, slice, begin, end;
       unit_tile(u, p, mp, nt, slice, begin, end);
       const long long row0 = static_cast<long long>(mp) * 2 * BM + rank * BM + quarter * 32;
-      const int col0 = nt * kBN + side * S::COLS;
+      const int col0 = nt * p.width + side * S::COLS;
+      const int cols = min(p.N, (nt + 1) * p.width) - col0;  // of this warp that are the tile's
       float sum[S::COLS / 16][16] = {};
       for (int k0 = begin; k0 < end; k0 += kChunkSteps) {
         const bool got = mbar_wait_cluster(&tfull_bar[acc], acc_phase, abort_flag);
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (one copy of the epilogue's code: sixteen unrolled ones, with every
       // activation in each, cost 10 us of instruction fetches)
 #pragma unroll 1
-      for (int q = 0; q < S::COLS / 16 && col0 + q * 16 < p.N; ++q) {
+      for (int q = 0; q < S::COLS / 16 && q * 16 < cols; ++q) {
         __syncwarp();
 #pragma unroll
         for (int s = 0; s < S::COLS / 16; ++s)
@@ -497,9 +500,9 @@ size_t planes_bytes(long long plane_rows, int cols) {
 
 // a, b: their planes and flags; A_MN: a is [K][M].
 template <int BN, bool A_MN, bool B_MN>
-cudaError_t launch(const LinearProduct& g, const SplitOperand& a, const SplitOperand& b, int* all,
-                   cudaStream_t stream) {
-  constexpr int kSmem = Shape<BN>::SMEM, kBN = BN;
+cudaError_t launch(const LinearProduct& g, const SplitOperand& a, const SplitOperand& b, int width,
+                   int* all, cudaStream_t stream) {
+  constexpr int kSmem = Shape<BN>::SMEM;
   auto* kernel = linear_split_kernel<BN, A_MN, B_MN>;
   static bool ready[64] = {false};
   static int max_clusters[64] = {0};
@@ -543,10 +546,11 @@ cudaError_t launch(const LinearProduct& g, const SplitOperand& a, const SplitOpe
   CUtensorMap tmA, tmB;
   if (!make_map(&tmA, a.planes, kPlanes * a.plane_rows, a.cols, a.pitch, 2, 64, A_MN ? 64 : BM) ||
       !make_map(&tmB, b.planes, kPlanes * b.plane_rows, b.cols, b.pitch, 2, 64,
-                B_MN ? 64 : kBN / 2))
+                B_MN ? 64 : width / 2))
     return cudaErrorInvalidValue;
   p.m_pairs = static_cast<int>((g.M + 2 * BM - 1) / (2 * BM));
-  p.n_tiles = (g.N + kBN - 1) / kBN;
+  p.width = width;
+  p.n_tiles = (g.N + width - 1) / width;
   p.k_steps = (g.K + BK - 1) / BK;
   p.slices = g.slices;
   p.slice_steps = (p.k_steps + g.slices - 1) / g.slices;
@@ -573,6 +577,27 @@ cudaError_t launch(const LinearProduct& g, const SplitOperand& a, const SplitOpe
 }  // namespace
 
 namespace {
+
+// The width of the tiles.  Of an [N][K] B it may be any multiple of 16, and a narrower
+// one of as many rounds over the clusters leaves less of the last round empty; a step is
+// taken to lie between those of 128 and of 256 wide (loop_us) in proportion.  256 or 128 /
+// any: 515 tokens, 1000 -> 10007 116 / 106 us, 333 tokens, 768 -> 30001 186 / 168, 2048
+// tokens, 2048 -> 5632 224 / 199, 4096^3 545 / 508, 300 tokens, 2048 -> 8192 105 / 101.
+int tile_width(const LinearProduct& g, bool narrow) {
+  if (g.b_mn) return narrow ? 128 : 256;
+  const long long m_pairs = (g.M + 2 * BM - 1) / (2 * BM), clusters = std::max(1, sm_count() / 2);
+  int best = 256;
+  double least = 0.0;
+  for (int w = 256; w >= 128; w -= 16) {
+    const long long rounds = (g.slices * m_pairs * ((g.N + w - 1) / w) + clusters - 1) / clusters;
+    const double us = static_cast<double>(rounds) * (0.53 + 1.18 / 256.0 * w);
+    if (w == 256 || us < 0.98 * least) {
+      least = us;
+      best = w;
+    }
+  }
+  return best;
+}
 
 // Microseconds of the products' main loops: a 64-wide step of the six products
 // takes 1.71 us in a 256-wide tile, 1.12 in a 128-wide one (see linear_pair),
@@ -723,10 +748,11 @@ cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) 
   if (e != cudaSuccess) return e;
   bool narrow;
   loop_us(g.M, g.N, g.K, &narrow, g.slices);
-  e = narrow ? g.b_mn ? launch<128, false, true>(g, a, b, all, s)
-                      : launch<128, false, false>(g, a, b, all, s)
-      : g.b_mn ? launch<256, false, true>(g, a, b, all, s)
-               : launch<256, false, false>(g, a, b, all, s);
+  const int w = tile_width(g, narrow);
+  e = w == 128 ? g.b_mn ? launch<128, false, true>(g, a, b, w, all, s)
+                        : launch<128, false, false>(g, a, b, w, all, s)
+      : g.b_mn ? launch<256, false, true>(g, a, b, w, all, s)
+               : launch<256, false, false>(g, a, b, w, all, s);
   if (e != cudaSuccess) return e;
   LinearProduct again = g;
   again.all_rows = all;
@@ -750,8 +776,8 @@ cudaError_t linear_split_turned(const LinearProduct& g, void* a_planes, void* b_
   bool narrow;
   loop_us(g.M, g.N, g.K, &narrow);
   int* all = static_cast<int*>(a_planes);
-  const cudaError_t e = narrow ? launch<128, true, true>(g, a, b, all, s)
-                               : launch<256, true, true>(g, a, b, all, s);
+  const cudaError_t e = narrow ? launch<128, true, true>(g, a, b, 128, all, s)
+                               : launch<256, true, true>(g, a, b, 256, all, s);
   if (e != cudaSuccess) return e;
   LinearProduct again = g;
   again.all_rows = all;
