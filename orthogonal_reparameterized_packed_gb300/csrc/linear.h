@@ -53,6 +53,7 @@ struct LinearProduct {
   bool b_ready = false;
   // linear_split: linear_planes_bytes(M, K) for A's planes, null: they are in the scratch
   void* a_planes = nullptr;
+  bool a_ready = false;  // they are there, made by the caller
   const LossColumns* loss = nullptr;  // linear_stream with B [N][K]
   const char* tag = "linear";
 };
@@ -78,11 +79,19 @@ cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s);
 // Whether linear_split left *scratch not 0: values of B are for the CUDA cores, which
 // computed everything (with slices, the first slice).
 
-// An fp32 array [rows][cols], ld apart, as planes that are kept.
+// The planes of an fp32 array [rows][cols] that are kept.  A caller that makes them itself:
+// planes [3][plane_rows][pitch] bf16 as linear_planes.cuh has it, rows behind the last 0,
+// and a flag per row, whether a value of it is outside.
+struct Fp32Planes {
+  void* planes;
+  int* flags;
+  long long plane_rows, pitch;
+};
 size_t linear_planes_bytes(long long rows, int cols);
+Fp32Planes linear_planes_at(void* at, long long rows, int cols);
 cudaError_t linear_split_planes(const float* in, long long rows, int cols, long long ld, void* at,
                                 cudaStream_t s);
-// With a_mn and b_mn, from the kept planes of A and B.
+// With a_mn and b_mn, from the kept planes of A, of the caller's making, and of B.
 cudaError_t linear_split_turned(const LinearProduct& g, void* a_planes, void* b_planes,
                                 cudaStream_t s);
 

@@ -30,6 +30,7 @@
 #include "internal.h"
 #include "linear.h"
 #include "linear_fp32.cuh"
+#include "linear_planes.cuh"
 #include "ptx.cuh"
 #include "tc_common.cuh"
 
@@ -57,7 +58,6 @@ struct Shape {
 };
 
 constexpr int kGroupM = 8;
-constexpr int kPlanes = 3;
 constexpr int kProducts = 6;
 constexpr int kChunkSteps = 2;  // K steps accumulated by the tensor core in one go
 
@@ -73,10 +73,10 @@ struct SplitArgs {
   int plane_rows_a, plane_rows_b;  // rows between planes of A, of B
   long long M;
   Fp32Epilogue epi;
-  int segs;              // flags per row of A; 0: A is [K][M]
+  int segs;              // flags per row of A
   const int* row_flags;  // A's: rows with one that is not 0 are left to linear_simt
-  int flags;             // flags of B, and of A where it is [K][M]: then all rows are
-  const int *a_flags, *b_flags;
+  int b_count, a_count;  // flags of B, and of A as [K][M]: then all rows are
+  const int *b_flags, *a_flags;
   int* all;              // set here: whether any of those is
   int* status;
 };
@@ -150,10 +150,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
   int bad = 0;
-  for (int i = threadIdx.x; i < p.flags; i += kThreads) {
-    bad |= p.b_flags[i];
-    if (A_MN) bad |= p.a_flags[i];
-  }
+  for (int i = threadIdx.x; i < p.b_count; i += kThreads) bad |= p.b_flags[i];
+  if (A_MN)
+    for (int i = threadIdx.x; i < p.a_count; i += kThreads) bad |= p.a_flags[i];
   bad = __syncthreads_or(bad);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.all = bad;
   const int units = bad != 0 ? 0 : p.m_pairs * p.n_tiles * p.slices;
@@ -386,11 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // One operand: in [rows][cols] fp32 -> planes [3][plane_rows][pitch] bf16, rows
 // from `rows` to plane_rows zero (columns past cols are not read by any tile);
 // flag[r][segs]: whether a value of the row's segment of kSegment columns is
-// neither 0 nor of a magnitude that the planes take.  Where those of all rows count
-// together (B's, and A's as [K][M]), a flag per CTA, `flags` of them, is enough: one for
-// every row (30001) made each CTA of the product read them for 20 us.
+// neither 0 nor of a magnitude that the planes take.  Of B a flag per CTA, `flags` of
+// them, is enough: one for every row (30001) made each CTA of the product read them
+// for 20 us.
 constexpr int kSegment = 1024;
-constexpr unsigned kLeastBits = (127u - 109u) << 23, kMostBits = (127u + 60u) << 23;
 
 struct SplitOperand {
   const float* in;
@@ -441,25 +439,9 @@ __global__ void __launch_bounds__(kSplitThreads)
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // infinities and NaN have larger bits than 2^60
-        const unsigned u = __float_as_uint(v[j]) & 0x7fffffffu;
-        bad |= u != 0 && u - kLeastBits > kMostBits - kLeastBits;
-      }
-#pragma unroll
-      for (int s = 0; s < kPlanes; ++s) {
-        uint32_t w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * h], v[2 * h + 1]);
-          const float2 f = __bfloat1622float2(q);
-          v[2 * h] -= f.x;  // exact: the rounding error of a bf16 rounding
-          v[2 * h + 1] -= f.y;
-          w[h] = *reinterpret_cast<const uint32_t*>(&q);
-        }
-        // rows are a multiple of 64 elements apart: 8 bytes fit, padding included
-        *reinterpret_cast<uint2*>(o.planes + (s * o.plane_rows + r) * o.pitch + c) =
-            make_uint2(w[0], w[1]);
-      }
+      for (int j = 0; j < 4; ++j) bad |= outside_planes(v[j]);
+      // rows are a multiple of 64 elements apart: 8 bytes fit, padding included
+      store_planes(o.planes + r * o.pitch + c, o.plane_rows * o.pitch, v);
     }
     bad = __any_sync(0xffffffffu, bad);
     (first ? bad_a : bad_b) |= bad;
@@ -560,9 +542,10 @@ cudaError_t launch(const LinearProduct& g, const SplitOperand& a, const SplitOpe
   p.all = all;
   p.row_flags = A_MN ? nullptr : a.flag;
   p.segs = A_MN ? 0 : a.segs;
-  p.flags = split_ctas();
-  p.a_flags = a.whole;
+  p.b_count = split_ctas();
   p.b_flags = b.whole;
+  p.a_count = A_MN ? g.K : 0;
+  p.a_flags = a.flag;
   p.status = device_status_ptr();
   const int clusters = static_cast<int>(
       std::min<long long>(static_cast<long long>(p.m_pairs) * p.n_tiles * p.slices, cmax));
@@ -707,6 +690,11 @@ size_t linear_planes_bytes(long long rows, int cols) {
   return all_flag_bytes() + flag_bytes(up64(rows), cols) + planes_bytes(up64(rows), cols);
 }
 
+Fp32Planes linear_planes_at(void* at, long long rows, int cols) {
+  const SplitOperand o = kept(at, nullptr, rows, cols, 0);
+  return {o.planes, o.flag, o.plane_rows, o.pitch};
+}
+
 size_t linear_split_b_scratch(const LinearProduct& g) {
   return all_flag_bytes() + planes_bytes(b_plane_rows(g), b_cols(g));
 }
@@ -738,13 +726,18 @@ cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) 
   b.planes = reinterpret_cast<bf16*>(static_cast<char*>(scratch) + all_flag_bytes());
   if (g.a_planes != nullptr) {
     a = kept(g.a_planes, g.A, g.M, g.K, g.pitch_a);
+    if (g.a_ready) a.segs = 1;
   } else {
     char* at = static_cast<char*>(scratch) + linear_split_b_scratch(g);
     a = operand(g.A, g.M, g.K, g.pitch_a, g.M);
     a.flag = reinterpret_cast<int*>(at);
     a.planes = reinterpret_cast<bf16*>(at + flag_bytes(g.M, g.K));
   }
-  cudaError_t e = split(a, g.b_ready ? nullptr : &b, s);
+  cudaError_t e = cudaSuccess;
+  if (!g.a_ready)
+    e = split(a, g.b_ready ? nullptr : &b, s);
+  else if (!g.b_ready)
+    e = split(b, nullptr, s);
   if (e != cudaSuccess) return e;
   bool narrow;
   loop_us(g.M, g.N, g.K, &narrow, g.slices);

@@ -17,6 +17,7 @@
 
 #include "internal.h"
 #include "linear.h"
+#include "linear_planes.cuh"
 #include "loss.h"
 #include "poetx.h"
 #include "ptx.cuh"
@@ -609,24 +610,36 @@ __global__ void __launch_bounds__(kThreads, 4) loss_finish_kernel(const FinishAr
     sum_total<kThreads>(a.rows, count, by, a.total);
 }
 
+// Where a block's dz goes as planes too (null: it does not), for rows of the block.
+struct DzPlanes {
+  bf16* planes;
+  int* flags;
+  long long rows, stride, pitch;
+};
+
 // A CTA per row of the block: its loss from the fp32 logits z, and in place of them dz
-// where the gradients are wanted (rows that do not count: 0).  Two passes over the row,
-// 16 bytes at a time.
+// where the gradients are wanted (rows that do not count, and those behind the block's:
+// 0), and its planes.  Two passes over the row, 16 bytes at a time.
 template <int THREADS>
 __device__ __forceinline__ void loss_row(float* __restrict__ z, long long ld, const LossRows& l,
                                          long long first, int V, int top, float inv_tau, float tau,
                                          const float* __restrict__ weights, bool grad,
-                                         float* __restrict__ loss) {
+                                         float* __restrict__ loss, const DzPlanes& dz) {
   __shared__ float ms[THREADS / 32], ss[THREADS / 32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const long long r = first + blockIdx.x;
   float* row = z + static_cast<long long>(blockIdx.x) * ld;
   const int n = *l.count;
   constexpr int kStep = 8 * THREADS;  // values at a time, two quads of a thread
-  if (r >= n) {
-    if (grad)
-      for (int v = 4 * threadIdx.x; v < V; v += 4 * THREADS)
+  bf16* planes = dz.planes + static_cast<long long>(blockIdx.x) * dz.pitch;
+  if (r >= n || blockIdx.x >= dz.rows) {
+    for (int v = 4 * threadIdx.x; grad && v < V; v += 4 * THREADS) {
+      float zero[4] = {0.f, 0.f, 0.f, 0.f};
+      if (blockIdx.x < dz.rows)
         *reinterpret_cast<float4*>(row + v) = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (dz.planes != nullptr) store_planes(planes + v, dz.stride, zero);
+    }
+    if (dz.planes != nullptr && threadIdx.x == 0 && blockIdx.x < dz.rows) dz.flags[blockIdx.x] = 0;
     return;
   }
   // this thread's eight values from v0 on; behind the row's end -inf
@@ -691,21 +704,26 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, long long ld, co
   const float scale = (weights != nullptr ? weights[t] : 1.f / static_cast<float>(n)) * tau;
   __syncthreads();
   const float over = scale / s;
+  bool bad = false;
   for (int v0 = 0; v0 < V; v0 += kStep) {
     float x[8];
     load(v0, x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float dz = over * expf((x[j] - m) * inv_tau);
+      const float term = over * expf((x[j] - m) * inv_tau);
       // below 2^-109 the products on the tensor cores do not take a value: 0
-      x[j] = fabsf(dz) < 1.5407439555e-33f ? 0.f : dz;
+      x[j] = fabsf(term) < 1.5407439555e-33f ? 0.f : term;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int v = v0 + 4 * (threadIdx.x + h * THREADS);
-      if (v < V)
-        *reinterpret_cast<float4*>(row + v) =
-            make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
+      if (v >= V) continue;
+      float q[4] = {x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
+      *reinterpret_cast<float4*>(row + v) = make_float4(q[0], q[1], q[2], q[3]);
+      if (dz.planes == nullptr) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) bad |= outside_planes(q[j]);
+      store_planes(planes + v, dz.stride, q);
     }
   }
   __syncthreads();
@@ -714,18 +732,26 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, long long ld, co
     if (i < 0 || (k > 0 && l.index[base + k - 1] == i)) continue;
     float all = l.p[base + k];
     for (int q = k + 1; q < top && l.index[base + q] == i; ++q) all += l.p[base + q];
-    row[i] -= scale * all;
+    const float term = row[i] - scale * all;
+    row[i] = term;
+    if (dz.planes == nullptr) continue;
+    bad |= outside_planes(term);
+    store_planes(planes + i, dz.stride, term);
   }
+  if (dz.planes == nullptr) return;
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) dz.flags[blockIdx.x] = bad;
 }
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
     loss_rows_kernel(float* __restrict__ z, long long ld, LossRows l, long long first, int V,
                      int top, float inv_tau, float tau, const float* __restrict__ weights,
-                     bool grad, float* __restrict__ loss, bool last, float* __restrict__ total) {
+                     bool grad, float* __restrict__ loss, const DzPlanes dz, bool last,
+                     float* __restrict__ total) {
   pdl_wait();
   pdl_trigger();
-  loss_row<THREADS>(z, ld, l, first, V, top, inv_tau, tau, weights, grad, loss);
+  loss_row<THREADS>(z, ld, l, first, V, top, inv_tau, tau, weights, grad, loss, dz);
   if (last)
     total_behind<THREADS>(l, *l.count,
                           weights == nullptr ? static_cast<float>(max(1, *l.count)) : 1.f, total);
@@ -809,23 +835,18 @@ struct Plan {
                    : 0);
     const bool planes = want_dw && !a.is_bf16;
     x_planes = take(planes ? linear_planes_bytes(block, a.d) : 0);
-    z_planes = take(planes ? linear_planes_bytes(block, a.V) : 0);
-    scratch = take(a.is_bf16 ? 0 : fp32_scratch(a, want_dx, want_dw));
+    z_planes = take(grad && !a.is_bf16 ? linear_planes_bytes(block, a.V) : 0);
+    scratch = take(a.is_bf16 ? 0 : fp32_scratch(a, grad, want_dw));
     total = at;
   }
 
-  // The largest of the products' scratch, for blocks of any number of rows.  With dW the
-  // operands' planes but W's have places of their own.
-  size_t fp32_scratch(const LossArgs& a, bool want_dx, bool want_dw) const {
+  // The largest of the products' scratch, for blocks of any number of rows: of the
+  // logits', without x's planes where dW keeps them; with gradients also W's for dx.
+  size_t fp32_scratch(const LossArgs& a, bool grad, bool want_dw) const {
     LinearProduct g;
     g.M = block, g.N = a.V, g.K = a.d;
-    if (want_dw) return linear_split_b_scratch(g);
-    size_t most = linear_split_scratch_up_to(g);
-    if (want_dx) {
-      g.N = a.d, g.K = a.V, g.b_mn = true;
-      most = std::max(most, linear_split_scratch(g));
-    }
-    return most;
+    return std::max(want_dw ? 0 : linear_split_scratch_up_to(g),
+                    grad ? linear_split_b_scratch(g) : 0);
   }
 };
 
@@ -966,9 +987,10 @@ cudaError_t run_bf16(const LossArgs& a, const Plan& plan, const LossRows& l, cha
 }
 
 // fp32: the products of linear_fp32 on a block's logits, which become dz in place.  Rows
-// that do not count are 0.  dW takes the planes that the others made of x and dz, as they
-// lie (dz transposed and split for it: 515 tokens, 1000 -> 10007 295 us, now 274; 333 tokens,
-// 768 -> 30001 440, now 399).
+// that do not count are 0.  dz' planes are made along with it (a launch of their own: 515
+// tokens, 1000 -> 10007 268 us, not 261; 333 tokens, 768 -> 30001 387, not 377), x's for
+// the logits, and dW takes both as they lie (dz transposed and split again: 21 and 41 us
+// more).
 cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char* ws,
                     cudaStream_t s) {
   float* xg = reinterpret_cast<float*>(ws + plan.xg);
@@ -977,13 +999,27 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
   float* out = reinterpret_cast<float*>(ws + plan.cut);
   const bool grad = a.dx != nullptr || a.dW != nullptr;
   char* x_planes = a.dW != nullptr ? ws + plan.x_planes : nullptr;
-  char* z_planes = a.dW != nullptr ? ws + plan.z_planes : nullptr;
+  char* z_planes = ws + plan.z_planes;
   cudaError_t e;
   bool ready = false;  // W's planes are in the scratch
   for (long long first = 0; first < a.T; first += plan.block) {
     const long long rows = std::min(plan.block, a.T - first);
     float* xb = xg + first * a.d;
-    bool x_ready = false, z_ready = false;  // the block's planes
+    const int slices = a.dx != nullptr ? linear_split_slices(rows, a.d, a.V, kCutBytes) : 1;
+    const bool split_dx =
+        a.dx != nullptr && (slices > 1 || linear_split_pays(rows, a.d, a.V));
+    const bool split_dw =
+        a.dW != nullptr && linear_split_pays(a.V, a.d, static_cast<int>(rows));
+    const bool x_ready = linear_split_pays(rows, a.V, a.d);  // the logits made its planes
+    DzPlanes dz = {};
+    dz.rows = rows;
+    if (split_dx || split_dw) {
+      const Fp32Planes at = linear_planes_at(z_planes, rows, a.V);
+      dz.planes = static_cast<bf16*>(at.planes);
+      dz.flags = at.flags;
+      dz.pitch = at.pitch;
+      dz.stride = at.plane_rows * at.pitch;
+    }
     LinearProduct g;
     g.A = xb;
     g.B = a.W;
@@ -994,16 +1030,16 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
     g.a_planes = x_planes;
     g.tag = "loss_logits";
     if ((e = linear_fp32(g, scratch, s)) != cudaSuccess) return e;
-    x_ready = linear_split_pays(rows, a.V, a.d);
     ready |= x_ready;
     e = launched("loss_rows", s, [&] {
       // long rows take 512 threads, four CTAs on an SM: 333 of 30001 28 us (with 1024
       // a second wave), 515 of 10007 19; short ones 256
       const bool wide = a.V > 8192;
       return launch_pdl(wide ? loss_rows_kernel<512> : loss_rows_kernel<kThreads>,
-                        dim3(static_cast<unsigned>(rows)), dim3(wide ? 512 : kThreads), 0, s, z,
-                        plan.lde, l, first, a.V, a.top, 1.f / a.tau, a.tau, a.weights, grad, a.loss,
-                        first + rows >= a.T, a.total);
+                        dim3(static_cast<unsigned>(dz.planes != nullptr ? round64(rows) : rows)),
+                        dim3(wide ? 512 : kThreads), 0, s, z, plan.lde, l, first, a.V, a.top,
+                        1.f / a.tau, a.tau, a.weights, grad, a.loss, dz, first + rows >= a.T,
+                        a.total);
     });
     if (e != cudaSuccess) return e;
     if (a.dx != nullptr) {
@@ -1012,15 +1048,15 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
       q.pitch_a = plan.lde;
       q.B = a.W;
       q.b_mn = true;
-      q.slices = linear_split_slices(rows, a.d, a.V, kCutBytes);
+      q.slices = slices;
       q.b_ready = ready;
       q.a_planes = z_planes;
+      q.a_ready = true;
       q.y = out;
       q.M = rows, q.N = a.d, q.K = a.V;
       q.tag = "loss_dx";
       if ((e = linear_fp32(q, scratch, s)) != cudaSuccess) return e;
-      z_ready = q.slices > 1 || linear_split_pays(rows, a.d, a.V);
-      ready |= z_ready;
+      ready |= split_dx;
       e = launched("loss_scatter", s, [&] {
         return launch_pdl(loss_scatter_kernel,
                           dim3(static_cast<unsigned>(rows),
@@ -1042,11 +1078,8 @@ cudaError_t run_f32(const LossArgs& a, const Plan& plan, const LossRows& l, char
       q.y = a.dW;
       q.M = a.V, q.N = a.d, q.K = static_cast<int>(rows);
       q.tag = "loss_dw";
-      if (linear_split_pays(a.V, a.d, q.K)) {
+      if (split_dw) {
         if (!x_ready && (e = linear_split_planes(xb, rows, a.d, a.d, x_planes, s)) != cudaSuccess)
-          return e;
-        if (!z_ready &&
-            (e = linear_split_planes(z, rows, a.V, plan.lde, z_planes, s)) != cudaSuccess)
           return e;
         e = linear_split_turned(q, z_planes, x_planes, s);
       } else {
