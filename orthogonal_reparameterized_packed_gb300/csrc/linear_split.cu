@@ -166,7 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     long long issued = 0;
-    const uint32_t tx = 2 * (kA + static_cast<uint32_t>(p.width) * BK);  // bytes of a step
+    // bytes of a step; an MN-major B comes in boxes of 64 columns
+    const uint32_t half = static_cast<uint32_t>(B_MN ? kBN : p.width) / 2;
+    const uint32_t tx = 2 * (kA + half * BK * 2);
     bool ok = true;
     for (int u = first; u < units && ok; u += step) {
       int mp, nt, slice, begin, end;
@@ -561,17 +563,19 @@ cudaError_t launch(const LinearProduct& g, const SplitOperand& a, const SplitOpe
 
 namespace {
 
-// The width of the tiles.  Of an [N][K] B it may be any multiple of 16, and a narrower
-// one of as many rounds over the clusters leaves less of the last round empty; a step is
-// taken to lie between those of 128 and of 256 wide (loop_us) in proportion.  256 or 128 /
-// any: 515 tokens, 1000 -> 10007 116 / 106 us, 333 tokens, 768 -> 30001 186 / 168, 2048
-// tokens, 2048 -> 5632 224 / 199, 4096^3 545 / 508, 300 tokens, 2048 -> 8192 105 / 101.
-int tile_width(const LinearProduct& g, bool narrow) {
-  if (g.b_mn) return narrow ? 128 : 256;
+// The width of the tiles: a narrower one of as many rounds over the clusters leaves less
+// of the last round empty; a step is taken to lie between those of 128 and of 256 wide
+// (loop_us) in proportion.  256 or 128 / any: 515 tokens, 1000 -> 10007 116 / 106 us, 333
+// tokens, 768 -> 30001 186 / 168, 2048 tokens, 2048 -> 5632 224 / 199, 4096^3 545 / 508,
+// 300 tokens, 2048 -> 8192 105 / 101.  Of a [K][N] B, which comes in boxes of 64 columns,
+// multiples of 32: its loads stay those of 256 (dx of 515 tokens, 10007 <- 1000 116 / 111,
+// of 2048, 5632 <- 2048 224 / 209, 4096^3 543 / 507).  linear_split_pays keeps to 128 and
+// 256.
+int tile_width(const LinearProduct& g) {
   const long long m_pairs = (g.M + 2 * BM - 1) / (2 * BM), clusters = std::max(1, sm_count() / 2);
   int best = 256;
   double least = 0.0;
-  for (int w = 256; w >= 128; w -= 16) {
+  for (int w = 256; w >= 128; w -= g.b_mn ? 32 : 16) {
     const long long rounds = (g.slices * m_pairs * ((g.N + w - 1) / w) + clusters - 1) / clusters;
     const double us = static_cast<double>(rounds) * (0.53 + 1.18 / 256.0 * w);
     if (w == 256 || us < 0.98 * least) {
@@ -583,26 +587,18 @@ int tile_width(const LinearProduct& g, bool narrow) {
 }
 
 // Microseconds of the products' main loops: a 64-wide step of the six products
-// takes 1.71 us in a 256-wide tile, 1.12 in a 128-wide one (see linear_pair),
-// which pays where it fills idle clusters.
-double loop_us(long long M, int N, int K, bool* narrow, int slices = 1) {
+// takes 1.71 us in a 256-wide tile, 1.12 in a 128-wide one (see linear_pair).
+double loop_us(long long M, int N, int K, int slices) {
   const long long m_pairs = (M + 2 * BM - 1) / (2 * BM), clusters = std::max(1, sm_count() / 2);
   const long long wide = (slices * m_pairs * ((N + 255) / 256) + clusters - 1) / clusters;
   const long long thin = (slices * m_pairs * ((N + 127) / 128) + clusters - 1) / clusters;
   const long long steps = (K + BK - 1) / BK;
-  *narrow = 1.12 * thin < 1.71 * wide;
-  return (*narrow ? 1.12 * thin : 1.71 * wide) * ((steps + slices - 1) / slices);
+  return std::min(1.12 * thin, 1.71 * wide) * ((steps + slices - 1) / slices);
 }
-
-}  // namespace
-
-namespace {
 
 // With 4 bytes written and read per output and slice.
 double split_us(long long M, int N, int K, int slices = 1) {
-  bool narrow;
-  return 18.0 + loop_us(M, N, K, &narrow, slices) +
-         10e-6 * K * (static_cast<double>(M) + N) / 6.0 +
+  return 18.0 + loop_us(M, N, K, slices) + 10e-6 * K * (static_cast<double>(M) + N) / 6.0 +
          (slices > 1 ? 2e-6 * slices * M * N : 0.0);
 }
 
@@ -739,9 +735,7 @@ cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) 
   else if (!g.b_ready)
     e = split(b, nullptr, s);
   if (e != cudaSuccess) return e;
-  bool narrow;
-  loop_us(g.M, g.N, g.K, &narrow, g.slices);
-  const int w = tile_width(g, narrow);
+  const int w = tile_width(g);
   e = w == 128 ? g.b_mn ? launch<128, false, true>(g, a, b, w, all, s)
                         : launch<128, false, false>(g, a, b, w, all, s)
       : g.b_mn ? launch<256, false, true>(g, a, b, w, all, s)
@@ -766,11 +760,10 @@ cudaError_t linear_split_turned(const LinearProduct& g, void* a_planes, void* b_
                                 cudaStream_t s) {
   const SplitOperand a = kept(a_planes, nullptr, g.K, static_cast<int>(g.M), 0),
                      b = kept(b_planes, nullptr, g.K, g.N, 0);
-  bool narrow;
-  loop_us(g.M, g.N, g.K, &narrow);
+  const int w = tile_width(g);
   int* all = static_cast<int*>(a_planes);
-  const cudaError_t e = narrow ? launch<128, true, true>(g, a, b, 128, all, s)
-                               : launch<256, true, true>(g, a, b, 256, all, s);
+  const cudaError_t e = w == 128 ? launch<128, true, true>(g, a, b, w, all, s)
+                                 : launch<256, true, true>(g, a, b, w, all, s);
   if (e != cudaSuccess) return e;
   LinearProduct again = g;
   again.all_rows = all;

@@ -109,6 +109,18 @@ def test_every_tile_width(px, i):
     run_backward(px, T, b, a, "bf16", ACTS[(i + 1) % 5], True, i % 2 == 1, 130 + i)
 
 
+# fp32 on the tensor cores, whose tiles are as wide as the rounds over the clusters ask for:
+# 128 to 240 by 16 for the forward pass, by 32 for the backward one; 256
+F32_WIDTHS = [(515, 2000), (1100, 2048), (1000, 3001), (515, 4100), (2048, 1500), (2048, 5000),
+              (515, 5000), (1000, 4100), (300, 5000), (2048, 2048), (1280, 3800)]
+
+
+@pytest.mark.parametrize("T,n", F32_WIDTHS)
+def test_every_fp32_tile_width(px, T, n):
+    run_forward(px, T, 320, n, "f32", "none", True, True, False, seed=n)
+    run_backward(px, T, n, 320, "f32", "none", True, False, seed=T)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("T,a,b", [(3, 128, 264), (150, 256, 384), (600, 512, 512)])

@@ -126,6 +126,13 @@ def test_some_blocks_with_wide_logits(px, tau, dtype):
     check((loss, h.total), want, bound)
 
 
+@pytest.mark.parametrize("T,d,V", [(300, 1100, 2048), (300, 2048, 1100), (300, 1500, 2048),
+                                   (300, 3001, 1100), (200, 2048, 2048), (515, 1000, 5000)])
+def test_f32_tile_widths_of_dw(px, T, d, V):
+    c = make(T, d, V, 1, "f32", seed=d, ignored=0.1)
+    run_and_check(px, c, None, c["w"])
+
+
 @pytest.mark.parametrize("tau", [None, 2.0])
 @pytest.mark.parametrize("T,d,V,block,tiny", [
     (515, 512, 5003, None, False), (700, 640, 9001, 321, False), (700, 640, 9001, 321, True)])
