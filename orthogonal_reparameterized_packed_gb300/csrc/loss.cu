@@ -498,15 +498,20 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
     for (int w = 0; w < kThreads / 32; ++w) add(sums[w][warp % R].x, sums[w][warp % R].y);
     if (on) {
       if (own) ref = m == -INFINITY ? 0.f : m * a.unit;
-      // an infinite logit: the sum is infinite too
-      const float log_s = m == INFINITY ? 0.f : log2f(s);
+      // log2 s = log_f + at_s, with the whole number apart: next to a reference 2^28 away
+      // it would cost a small loss 1e-6 of rounding.  An infinite logit: the sum is
+      // infinite too.
+      int whole = 0;
+      float f = m == INFINITY ? 1.f : frexpf(s, &whole);
+      if (f < 0.70710678f) f *= 2.f, --whole;
+      const float log_f = log2f(f), at_s = static_cast<float>(whole);
       float sum = 0.f, both = 0.f, square = 0.f;
       for (int k = lane; k < a.top; k += 32) {
         const int i = k == lane ? i0 : a.rows.index[base + k];
         if (i < 0) continue;
         const float p = k == lane ? p0 : a.rows.p[base + k];
         const float over = fmaf(k == lane ? z0 : a.rows.z[base + k], a.unit, -ref);
-        if (!(p == 0.f)) sum += p * (log_s - over);
+        if (!(p == 0.f)) sum += p * (log_f + (at_s - over));
         if (!own && (k == 0 || a.rows.index[base + k - 1] != i)) {
           float all = p;
           for (int q = k + 1; q < a.top && a.rows.index[base + q] == i; ++q)
