@@ -74,8 +74,9 @@ constexpr int kEntryWarps = 4;
 constexpr int kMostEntries = 1024;
 
 // The entries of a token, a warp each: p = softmax of the teacher's logits at tau
-// over the entries that are there, sorted by their indices.  Differences are divided
-// by tau, not the logits: the type's lowest value stays finite.
+// over the entries that are there, sorted by their indices; those of one index become
+// one, behind the places that hold none.  Differences are divided by tau, not the
+// logits: the type's lowest value stays finite.
 __global__ void __launch_bounds__(32 * kEntryWarps)
     loss_entries_kernel(const void* indices, int index_bytes, const void* logits, bool logits_bf16,
                         long long T, int top, int V, float inv_tau, LossRows l, int* status) {
@@ -137,9 +138,29 @@ __global__ void __launch_bounds__(32 * kEntryWarps)
   }
   __syncwarp();
   sort_entries(key, val, padded, lane);
-  for (int k = lane; k < top; k += 32) {
-    l.index[base + k] = key[k];
-    l.p[base + k] = val[k];
+  // the first of an index, with the sum of its p
+  const auto first_of = [&](int k) {
+    return k < top && key[k] >= 0 && (k == 0 || key[k - 1] != key[k]);
+  };
+  int heads = 0;
+  for (int k = lane; k < padded; k += 32) heads += first_of(k);
+  int to = top - __reduce_add_sync(0xffffffffu, heads);
+  for (int k = lane; k < to; k += 32) {
+    l.index[base + k] = -1;
+    l.p[base + k] = 0.f;
+  }
+  for (int k0 = 0; k0 < top; k0 += 32) {
+    const int k = k0 + lane;
+    const bool head = first_of(k);
+    const unsigned mask = __ballot_sync(0xffffffffu, head);
+    if (head) {
+      float all = val[k];
+      for (int q = k + 1; q < top && key[q] == key[k]; ++q) all += val[q];
+      const long long at = base + to + __popc(mask & ((1u << lane) - 1));
+      l.index[at] = key[k];
+      l.p[at] = all;
+    }
+    to += __popc(mask);
   }
   if (lane == 0) {
     l.pos[t] = any ? 0 : -1;
@@ -512,11 +533,8 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a) {
         const float p = k == lane ? p0 : a.rows.p[base + k];
         const float over = fmaf(k == lane ? z0 : a.rows.z[base + k], a.unit, -ref);
         if (!(p == 0.f)) sum += p * (log_f + (at_s - over));
-        if (!own && (k == 0 || a.rows.index[base + k - 1] != i)) {
-          float all = p;
-          for (int q = k + 1; q < a.top && a.rows.index[base + q] == i; ++q)
-            all += a.rows.p[base + q];
-          const float term = exp2f(over) / s - all;
+        if (!own) {
+          const float term = exp2f(over) / s - p;
           const bf16 kept = __float2bfloat16_rn(term * s);
           a.E[row * a.lde + i] = kept;
           both = fmaf(term, term, both);
@@ -732,12 +750,10 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, long long ld, co
     }
   }
   __syncthreads();
-  for (int k = threadIdx.x; k < top; k += THREADS) {  // the first of every index
+  for (int k = threadIdx.x; k < top; k += THREADS) {
     const int i = l.index[base + k];
-    if (i < 0 || (k > 0 && l.index[base + k - 1] == i)) continue;
-    float all = l.p[base + k];
-    for (int q = k + 1; q < top && l.index[base + q] == i; ++q) all += l.p[base + q];
-    const float term = row[i] - scale * all;
+    if (i < 0) continue;
+    const float term = row[i] - scale * l.p[base + k];
     row[i] = term;
     if (dz.planes == nullptr) continue;
     bad |= outside_planes(term);

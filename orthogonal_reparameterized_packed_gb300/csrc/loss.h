@@ -41,7 +41,7 @@ struct LossRows {
   int* again;    // per block: a row's reference did not fit
   int* pos;      // [T]: a token's row, -1 where it does not count
   int* token;    // [T]: a row's token
-  int* index;    // [T][top] by token, ascending, -1: no entry
+  int* index;    // [T][top] by token, ascending and different, -1: no entry
   float* p;      // [T][top]
   float* ent;    // [T] by token: sum_k p log p
   int* lead;     // [T] by token: the index of its largest p

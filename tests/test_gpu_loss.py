@@ -126,6 +126,20 @@ def test_some_blocks_with_wide_logits(px, tau, dtype):
     check((loss, h.total), want, bound)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,K,few", [(20, 1024, 1), (20, 130, 3), (150, 64, 5), (2100, 33, 2)])
+def test_few_indices_many_times(px, T, K, few, dtype):
+    """Every entry of a token at one of a few indices, some absent; their weights add up."""
+    c = make(T, 64, 300, K, dtype, seed=K, ignored=0.1)
+    rng = np.random.default_rng(K)
+    own = rng.integers(0, 300, (T, few))
+    at = np.take_along_axis(own, rng.integers(0, few, (T, K)), 1)
+    at[:, 1:][rng.random((T, K - 1)) < 0.2] = -1
+    at[(c["idx"] < 0).all(1)] = -1
+    c["idx"] = at
+    run_and_check(px, c, 2.0)
+
+
 @pytest.mark.parametrize("T,d,V", [(300, 1100, 2048), (300, 2048, 1100), (300, 1500, 2048),
                                    (300, 3001, 1100), (200, 2048, 2048), (515, 1000, 5000)])
 def test_f32_tile_widths_of_dw(px, T, d, V):
