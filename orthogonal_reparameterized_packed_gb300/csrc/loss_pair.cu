@@ -502,8 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // E's rows behind the last are written up to a whole K step of dW
         if (row0 >= (rows + BK - 1) / BK * BK || in <= 0) continue;
         const bool on = row < rows;
-        // rows behind the last, whose x is 0: their terms are 0
-        float ref = STORE ? INFINITY : 0.f;
+        float ref = 0.f;
         int token = 0, k = p.top, next = INT_MAX;  // the row's next entry from side_col on
         if (on) {
           token = p.rows.token[p.first + row];
@@ -523,6 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 64; ++j)
             if (j >= in) z[j] = -INFINITY;
+        }
+        if (STORE && !on) {  // rows behind the last: their terms are 0, whatever W holds
+#pragma unroll
+          for (int j = 0; j < 64; ++j) z[j] = -INFINITY;
         }
         float sum = 0.f, top_z = -INFINITY;
         if (!STORE) {  // the reference is the largest of the 64 columns
