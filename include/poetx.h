@@ -387,8 +387,8 @@ poetx_status poetx_adam_update_many(int n_tensors, float* const* theta, const fl
  * and neither its x nor its weight is used (they may be NaN).  If no token
  * counts, total and dW are 0.
  * Logits, softmax, losses and sums are fp32.  BF16 rounds the softmax's terms to
- * bf16 for the gradients' products, and dx and dW once more; F32 takes weighted
- * terms below 2^-109 as 0.  A logit that is not finite (or above 2^126 tau) makes
+ * bf16 for the gradients' products, and dx and dW once more; F32 may take terms
+ * below 2^-45 of their token's weight times tau as 0.  A logit that is not finite (or above 2^126 tau) makes
  * its token's loss and gradients inf or NaN, and with them dW.
  * The tokens that count are taken block_tokens at a time (rounded up to a
  * multiple of 64; 0: as many as keep one block's terms within 2 GiB).  The

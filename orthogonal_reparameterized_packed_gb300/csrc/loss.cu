@@ -727,6 +727,11 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, long long ld, co
   const float scale = (weights != nullptr ? weights[t] : 1.f / static_cast<float>(n)) * tau;
   __syncthreads();
   const float over = scale / s;
+  // Below 2^-109 the products on the tensor cores do not take a value: it is 0 where that is
+  // next to nothing, 2^-45 of the row's factor; a smaller factor leaves it to the CUDA cores.
+  const float least = dz.planes != nullptr && fabsf(scale) >= 5.4210108624e-20f  // 2^-64
+                          ? 1.5407439555e-33f
+                          : 0.f;
   bool bad = false;
   for (int v0 = 0; v0 < V; v0 += kStep) {
     float x[8];
@@ -734,8 +739,7 @@ __device__ __forceinline__ void loss_row(float* __restrict__ z, long long ld, co
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float term = over * expf((x[j] - m) * inv_tau);
-      // below 2^-109 the products on the tensor cores do not take a value: 0
-      x[j] = fabsf(term) < 1.5407439555e-33f ? 0.f : term;
+      x[j] = fabsf(term) < least ? 0.f : term;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
