@@ -398,7 +398,8 @@ poetx_status poetx_adam_update_many(int n_tensors, float* const* theta, const fl
  * tokens is enough for any fewer with the same block_tokens; gradients: what is
  * wanted (POETX_GRAD_X | POETX_GRAD_W).
  * 1 <= d, vocab <= 2^20, 1 <= top <= 1024, 1/64 <= temperature <= 64.
- * Results do not change from run to run.  Outputs and inputs may not overlap. */
+ * Results do not change from run to run.  Outputs and the workspace lie over no
+ * input and not over each other: POETX_ERR_INVALID_ARG. */
 enum { POETX_GRAD_X = 1, POETX_GRAD_W = 2 };
 
 size_t poetx_cross_entropy_workspace_size(int d, int vocab, int64_t tokens, poetx_dtype dtype,

@@ -22,6 +22,32 @@ poetx_status to_status(cudaError_t e) { return e == cudaSuccess ? POETX_OK : POE
 
 bool dtype_ok(poetx_dtype t) { return t == POETX_F32 || t == POETX_BF16; }
 
+// A tensor's bytes, none where it is null.
+struct Span {
+  uintptr_t from, to;
+  Span(const void* p, size_t bytes)
+      : from(reinterpret_cast<uintptr_t>(p)), to(p != nullptr ? from + bytes : from) {}
+  bool meets(const Span& o) const { return from < o.to && o.from < to; }
+};
+
+// Whether an output or the workspace lies over another of them or over an input.
+bool overlaps(const LossArgs& a, const void* workspace, size_t workspace_bytes) {
+  const size_t T = static_cast<size_t>(a.T), d = static_cast<size_t>(a.d), es = a.is_bf16 ? 2 : 4;
+  const size_t head = static_cast<size_t>(a.V) * d * es, entries = T * a.top;
+  const Span written[] = {{a.loss, 4 * T}, {a.total, 4}, {a.dx, T * d * es}, {a.dW, head},
+                          {workspace, workspace_bytes}};
+  const Span read[] = {{a.x, T * d * es}, {a.W, head}, {a.weights, 4 * T},
+                       {a.indices, entries * a.index_bytes},
+                       {a.top_logits, entries * (a.top_bf16 ? 2 : 4)}};
+  for (const Span& w : written) {
+    for (const Span& r : read)
+      if (w.meets(r)) return true;
+    for (const Span& o : written)
+      if (&o != &w && w.meets(o)) return true;
+  }
+  return false;
+}
+
 bool sizes_ok(int d, int vocab, int64_t tokens, int top, poetx_dtype dtype, int64_t block) {
   return dtype_ok(dtype) && d > 0 && vocab > 0 && d <= kMaxFeatures && vocab <= kMaxFeatures &&
          tokens >= 0 && tokens <= kMaxTokens && top > 0 && top <= kMaxTop && block >= 0 &&
@@ -55,17 +81,17 @@ poetx_status run(LossArgs& a, poetx_dtype dtype, void* workspace, size_t workspa
     return to_status(e);
   }
   if (a.x == nullptr || a.W == nullptr || a.indices == nullptr || a.loss == nullptr ||
-      (a.dx != nullptr && (a.dx == a.x || a.dx == a.W || a.dx == a.dW)) ||
-      (a.dW != nullptr && (a.dW == a.x || a.dW == a.W)) || a.weights == a.loss)
+      overlaps(a, nullptr, 0))
     return POETX_ERR_INVALID_ARG;
   for (const void* p : {a.x, a.W, static_cast<const void*>(a.dx)})
     if (!aligned(p, 16)) return POETX_ERR_INVALID_ARG;
   if (!aligned(a.indices, a.index_bytes) || !aligned(a.weights, 4) || !aligned(a.loss, 4) ||
       !aligned(a.top_logits, a.top_bf16 ? 2 : 4))
     return POETX_ERR_INVALID_ARG;
-  if (workspace == nullptr || !aligned(workspace, 16) ||
-      workspace_bytes < head_loss_scratch(a, a.dx != nullptr, a.dW != nullptr))
+  const size_t need = head_loss_scratch(a, a.dx != nullptr, a.dW != nullptr);
+  if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need)
     return POETX_ERR_WORKSPACE;
+  if (overlaps(a, workspace, need)) return POETX_ERR_INVALID_ARG;
   return to_status(head_loss(a, workspace, s));
 }
 
