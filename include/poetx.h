@@ -397,7 +397,8 @@ poetx_status poetx_adam_update_many(int n_tensors, float* const* theta, const fl
  * times the terms, the block's x and W) and up to 64 MiB of dx' parts.  That of `tokens`
  * tokens is enough for any fewer with the same block_tokens; gradients: what is
  * wanted (POETX_GRAD_X | POETX_GRAD_W).
- * 1 <= d, vocab <= 2^20, 1 <= top <= 1024, 1/64 <= temperature <= 64.
+ * 1 <= d, vocab <= 2^20, 0 <= tokens, block_tokens <= 2^22, 1 <= top <= 1024,
+ * 1/64 <= temperature <= 64.
  * Results do not change from run to run.  Outputs and the workspace lie over no
  * input and not over each other: POETX_ERR_INVALID_ARG. */
 enum { POETX_GRAD_X = 1, POETX_GRAD_W = 2 };

@@ -35,16 +35,16 @@ class _HeadLoss:
             raise ValueError("block_tokens: a number of tokens from 1 on is needed")
         self.code = dtype_code(dtype)
         self.dtype = _TORCH_DTYPE[self.code]
+        if tokens < 0 or self._workspace_size(0, max(tokens, 1)) == 0:
+            raise ValueError(f"a head of {vocab} x {d} for {tokens} tokens with {top} entries each "
+                             "is outside the limits")
+        ws = max(self._workspace_size(GRAD_X * bool(backward) + GRAD_W * bool(weight_grad), tokens),
+                 self._workspace_size(0, tokens), 16)
         dev = torch.device(device)
         self.loss = torch.empty((tokens,), dtype=torch.float32, device=dev)
         self.total = torch.empty((), dtype=torch.float32, device=dev)
         self.dx = torch.empty((tokens, d), dtype=self.dtype, device=dev) if backward else None
         self.dW = torch.empty((vocab, d), dtype=self.dtype, device=dev) if weight_grad else None
-        ws = self._workspace_size(GRAD_X * bool(backward) + GRAD_W * bool(weight_grad))
-        if ws == 0 and tokens > 0:
-            raise ValueError(f"a head of {vocab} x {d} for {tokens} tokens with {top} entries each "
-                             "is outside the limits")
-        ws = max(ws, self._workspace_size(0), 16)
         self.workspace = torch.empty((ws,), dtype=torch.uint8, device=dev)
         self._device = self.loss.get_device()
 
@@ -91,9 +91,9 @@ class PoetxCrossEntropy(_HeadLoss):
         super().__init__(d, vocab, tokens, 1, dtype, device, backward, weight_grad, block_tokens)
         self._call = load_library().poetx_cross_entropy
 
-    def _workspace_size(self, gradients):
-        return poetx_cross_entropy_workspace_size(self.d, self.vocab, self.tokens, self.code,
-                                                  gradients, self.block_tokens)
+    def _workspace_size(self, gradients, tokens):
+        return poetx_cross_entropy_workspace_size(self.d, self.vocab, tokens, self.code, gradients,
+                                                  self.block_tokens)
 
     def _run(self, x, W, targets, weights, dx, dW, stream):
         t, (x_at, w_at, weights_at) = self._take(x, W, weights, targets)
@@ -127,13 +127,15 @@ class PoetxDistill(_HeadLoss):
 
     def __init__(self, d, vocab, tokens, top, temperature=1.0, dtype="bf16", device="cuda",
                  backward=False, weight_grad=False, block_tokens=None):
+        if not 1 / 64 <= temperature <= 64:
+            raise ValueError(f"temperature: 1/64 to 64 is needed, got {temperature}")
         self.temperature = temperature
         super().__init__(d, vocab, tokens, top, dtype, device, backward, weight_grad,
                          block_tokens)
         self._call = load_library().poetx_distill
 
-    def _workspace_size(self, gradients):
-        return poetx_distill_workspace_size(self.d, self.vocab, self.tokens, self.top, self.code,
+    def _workspace_size(self, gradients, tokens):
+        return poetx_distill_workspace_size(self.d, self.vocab, tokens, self.top, self.code,
                                             gradients, self.block_tokens)
 
     def _run(self, x, W, top_indices, top_logits, weights, dx, dW, stream):
