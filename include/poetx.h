@@ -388,8 +388,12 @@ poetx_status poetx_adam_update_many(int n_tensors, float* const* theta, const fl
  * counts, total and dW are 0.
  * Logits, softmax, losses and sums are fp32.  BF16 rounds the softmax's terms to
  * bf16 for the gradients' products, and dx and dW once more; F32 may take terms
- * below 2^-45 of their token's weight times tau as 0.  A logit that is not finite (or above 2^126 tau) makes
- * its token's loss and gradients inf or NaN, and with them dW.
+ * below 2^-45 of their token's weight times tau as 0.
+ * A logit of NaN or +infinity makes its token's loss and dx inf or NaN, and with
+ * them all of dW.  One of -infinity has the term 0: the loss is +infinity where it
+ * is at one of the token's entries and else that of the other logits, and of the
+ * gradients only dx is NaN, where W is infinite.  The other tokens' losses and dx
+ * keep their values.  A finite logit beyond 2^126 tau may count as infinite.
  * The tokens that count are taken block_tokens at a time (rounded up to a
  * multiple of 64; 0: as many as keep one block's terms within 2 GiB).  The
  * workspace holds the gathered x and one block's terms, in BF16 with dW and more

@@ -7,7 +7,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests.block_common import status_ok  # noqa: E402
+from oracle import loss_oracle as lo  # noqa: E402
+from tests.block_common import EPS, host, status_ok, within  # noqa: E402
 from tests.loss_common import bounds, check, device, make, rounded  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -67,6 +68,40 @@ def test_an_entry_of_minus_infinity(px, T, d, V, tau, dtype):
     check((torch.cat((dW[:at], dW[at + 1:])),), want[3:], bound[3:], ("dW",))
     alone = head(more, tau, False)
     check((alone.forward(more["x"][0], more["W"][0], *rest), alone.total), want, bound)
+    status_ok(px)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [None, 2.0])
+@pytest.mark.parametrize("T,d,V", [(40, 64, 300), (90, 72, 500), (515, 512, 3001)])
+def test_minus_infinity_at_an_own_entry(px, T, d, V, tau, dtype):
+    """The token's loss is infinite, the other tokens keep their bits, and dW is the formula's:
+    |dz| and |x| are rounded once each and dW's elements once (2^-8 or 2^-24), the softmax's
+    terms are good to 2^-10: logits up to 32 off by d 2^-23 of themselves."""
+    _, c, at, j = one_more(T, d, V, tau, dtype)
+    h, alone = head(c, tau, True), head(c, tau, False)
+    loss, dx, _ = (v.clone() for v in h.step(c["x"][0], c["W"][0], *device(c, tau is not None)))
+    t = int(np.flatnonzero((c["idx"] >= 0).any(1))[3])
+    c["idx"][t, 0] = at
+    rest = device(c, tau is not None)
+    got, gx, gw = h.step(c["x"][0], c["W"][0], *rest)
+    status_ok(px)
+    keep = torch.arange(T, device="cuda") != t
+    on = torch.from_numpy((c["idx"] >= 0).any(1)).cuda()
+    assert got[t] == float("inf") and h.total == float("inf")
+    assert torch.equal(got[keep], loss[keep])
+    assert torch.equal(gx[keep].nan_to_num(), dx[keep].nan_to_num())
+    free = torch.arange(d, device="cuda") != j
+    assert gx[on][:, free].isfinite().all() and not gx[on, j].isfinite().any()
+    m = lo.head_loss(c["x"][1], c["W"][1], c["idx"], c["s"] if tau else np.zeros(c["idx"].shape),
+                     None, tau or 1.0)
+    dz, x = np.abs(m[4]["dz"]), np.abs(c["x"][1][m[4]["rows"]])
+    q = m[4]["q"] * m[4]["w"][m[4]["rows"], None] * (tau or 1.0)
+    u = EPS[dtype]
+    within(host(gw), m[3], (3.1 * u * dz + 2.0 ** -10 * q + T * 2.0 ** -23 * dz).T @ x +
+           u * np.abs(m[3]) + 2.0 ** -109 * T, "dW")
+    got = alone.forward(c["x"][0], c["W"][0], *rest)
+    assert got[t] == float("inf") and got[keep].isfinite().all()
     status_ok(px)
 
 
