@@ -118,7 +118,7 @@ struct Schedule {
 };
 
 struct PairArgs {
-  int n_tiles, N, K, V, top;
+  int n_tiles, N, K, top;
   long long M;           // kDw: the output's rows
   long long first, block;
   long long ld, ldp;
@@ -842,9 +842,9 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
   }
   return e;
 }
+
 PairArgs common(const LossProducts& g) {
   PairArgs p = {};
-  p.V = g.V;
   p.top = g.top;
   p.first = g.first;
   p.block = g.block;
