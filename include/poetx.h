@@ -367,7 +367,7 @@ poetx_status poetx_adam_update_many(int n_tensors, float* const* theta, const fl
 
 /* ------------------------------------------------------------------------
  * The losses at the output head, from the last hidden states x and the head's
- * weight W, without keeping the logits.  The paper has no counterpart: a
+ * weight W, one block of tokens at a time.  The paper has no counterpart: a
  * training step ends in one of them.
  *   u_tv = x_t . W_v / tau,  lse_t = log sum_v exp(u_tv)
  *   cross entropy (tau = 1):  loss_t = lse_t - u_t,target
@@ -394,13 +394,19 @@ poetx_status poetx_adam_update_many(int n_tensors, float* const* theta, const fl
  * is at one of the token's entries and else that of the other logits, and of the
  * gradients only dx is NaN, where W is infinite.  The other tokens' losses and dx
  * keep their values.  A finite logit beyond 2^126 tau may count as infinite.
- * The tokens that count are taken block_tokens at a time (rounded up to a
- * multiple of 64; 0: as many as keep one block's terms within 2 GiB).  The
- * workspace holds the gathered x and one block's terms, in BF16 with dW and more
- * than one block also dW in fp32, in F32 what its products split (one and a half
- * times the terms, the block's x and W) and up to 64 MiB of dx' parts.  That of `tokens`
- * tokens is enough for any fewer with the same block_tokens; gradients: what is
- * wanted (POETX_GRAD_X | POETX_GRAD_W).
+ * The tokens are taken block_tokens at a time (rounded up to a multiple of 64; 0:
+ * as many as keep one block's terms within 2 GiB), those that do not count behind
+ * the others; F32 multiplies their rows of zeros too.  The workspace holds the
+ * gathered x and
+ *   BF16 losses alone  no logit, 1/16 of a block's for its sums,
+ *   BF16 gradients     a block's terms, 2 vocab bytes a token, and with dW and more
+ *                      than one block dW in fp32: small blocks can take more,
+ *   F32                a block's logits, 4 vocab bytes a token; with gradients one
+ *                      and a half times those again for their planes, W's and the
+ *                      block's x's planes (6 bytes an element where the products run
+ *                      on the tensor cores) and up to 64 MiB of dx' parts.
+ * That of `tokens` tokens is enough for any fewer with the same block_tokens;
+ * gradients: what is wanted (POETX_GRAD_X | POETX_GRAD_W).
  * 1 <= d, vocab <= 2^20, 0 <= tokens, block_tokens <= 2^22, 1 <= top <= 1024,
  * 1/64 <= temperature <= 64.
  * Results do not change from run to run.  Outputs and the workspace lie over no

@@ -1,6 +1,7 @@
-"""The losses at the output head, from the last hidden states and the head's weight,
-without keeping the logits: cross entropy and distillation from a teacher's top
-logits.  Each class holds the output buffers and the workspace of one head and
+"""The losses at the output head, from the last hidden states and the head's weight:
+cross entropy and distillation from a teacher's top logits.  bf16 losses alone keep no
+logit, gradients one block of tokens' softmax terms (as many bytes as its logits in
+bf16; fp32 its logits, and two and a half times those for gradients).  Each class holds the output buffers and the workspace of one head and
 enqueues its calls on a stream (the current one by default); calls of one object on
 several streams, or of graphs captured with it, have to be ordered by the caller."""
 
@@ -22,8 +23,9 @@ class _HeadLoss:
 
     backward: a buffer for dx; weight_grad: one for dW too (a head that is not
     frozen).  block_tokens: how many tokens' terms the workspace holds at a time
-    (None: as many as fit 2 GiB); fewer take less memory and, with weight_grad, an
-    fp32 dW in the workspace."""
+    (None: as many as fit 2 GiB).  Fewer take less memory for them, but bf16 heads with
+    weight_grad and more than one block also an fp32 dW, 4 vocab d bytes, in the
+    workspace: less in all only where the terms saved are more than that."""
 
     def __init__(self, d, vocab, tokens, top, dtype, device, backward, weight_grad,
                  block_tokens):

@@ -63,7 +63,8 @@ def test_an_entry_of_minus_infinity(px, T, d, V, tau, dtype):
     on = torch.from_numpy((c["idx"] >= 0).any(1)).cuda()
     assert dx[on, j].isnan().all() and not dx[~on].any()
     keep = np.arange(d) != j
-    check((dx[:, torch.from_numpy(keep).cuda()],), (want[2][:, keep],), (bound[2][:, keep],), ("dx",))
+    check((dx[:, torch.from_numpy(keep).cuda()],), (want[2][:, keep],), (bound[2][:, keep],),
+          ("dx",))
     assert not dW[at].any()
     check((torch.cat((dW[:at], dW[at + 1:])),), want[3:], bound[3:], ("dW",))
     alone = head(more, tau, False)
