@@ -53,11 +53,15 @@ constexpr int kSlots = 4;        // slices' tiles per cluster at most
 constexpr float kCutCost = 20.f;
 // The tensor core's accumulation truncates: over 2048 of K a logit comes out 4e-6 of
 // itself too small, and the losses were 2.4e-6 off where a product rounded to nearest
-// leaves 8e-7.  So the logits take kDrain K steps at a time, and the epilogue adds
-// those up in registers.  Shorter pieces leave the epilogue of the tile before less
-// time, which the first two of them hide.  2049 tokens, 2048 -> 50001, forward: 8 / 12 /
-// 16 / 32 steps 206 / 199 / 199 / 200 us and 5e-7 / 7.5e-7 / 1.1e-6 / 2.3e-6 off.
-constexpr int kDrain = 12;
+// leaves 8e-7.  So the logits take some K steps at a time, and the epilogue adds those up
+// in registers.  A piece of k features loses k 1.0e-9 of itself (measured, 256 to 768):
+// 12 steps at a time 7.5e-7, 8 5e-7, 4 2.6e-7.  Shorter pieces leave the epilogue of the
+// tile before less time, which the first two of them hide.  12 / 8 / 4 / 2 steps, us: one
+// row of tiles, which W's bytes bound, losses of 256 tokens 1024 -> 32000 29.4 / 29.6 / 30.5 /
+// 31.8, 2048 -> 32000 45.2 / 45.3 / 45.7 / 47.5, 4096 -> 128256 205 / 207 / 213 / 219; 1024 tokens
+// 54.4 / 54.4 / 60.4 / 68.5, 90.0 / 89.9 / 95.9 / 107, 644 / 650 / 671 / 736.
+constexpr int kDrain = 8;
+constexpr int kDrainOneRow = 4;  // of tiles
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
 // The order of the work.  Whole rounds of tiles over the clusters come first; the
@@ -67,7 +71,7 @@ static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 // 1638 rows, d = 2048, V = 32000).  A slice's tile is kept in fp32, [256][256], and
 // added up by loss_sum_kernel.
 struct Schedule {
-  int whole, rest, slices, share, k_steps, clusters, rows;
+  int whole, rest, slices, share, k_steps, clusters, rows, drain;
 
   // In units of a K step (0.28 us): the rounds of the rest and, when it is cut, 0.4
   // for a slice's tile written and read and kCutCost for the launch.
@@ -262,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool products = k_steps > 0;  // dW without a row is 0
   if (threadIdx.x == 0) {
     schedule->rows = static_cast<int>(n);
+    schedule->drain = m_pairs > 1 ? kDrain : kDrainOneRow;  // of the logits
     schedule->plan(units, k_steps, step, !LOGITS && p.parts != nullptr);
     if (blockIdx.x == 0 && p.parts != nullptr) *p.schedule = *schedule;
   }
@@ -346,8 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tile, ks0, ks1, part_slot;
         for (int i = 0;
              products && ok && todo.item(i, first_unit, tile, ks0, ks1, part_slot); ++i) {
-          for (int kc = ks0; kc < ks1 && ok; kc += kDrain) {
-            const int kc1 = LOGITS ? min(ks1, kc + kDrain) : ks1;
+          const int piece = LOGITS ? todo.drain : ks1 - ks0;
+          for (int kc = ks0; kc < ks1 && ok; kc += piece) {
+            const int kc1 = min(ks1, kc + piece);
             if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1, abort_flag)) {
               record_timeout(p.status, abort_flag);
               ok = false;
@@ -388,7 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1;
-            if (!LOGITS) break;
           }
         }
         if (!ok && any_mma) {
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Nothing but the sums lives through the main loop: registers are short.
       const volatile Schedule* plan = schedule;
       for (int u = first_unit; u < plan->whole; u += plan->clusters) {
-        const int chunks = (plan->k_steps + kDrain - 1) / kDrain;
+        const int chunks = (plan->k_steps + plan->drain - 1) / plan->drain;
         float z[64];
         bool got = true;
         for (int kc = 0; kc < chunks; ++kc) {

@@ -7,8 +7,8 @@ in the mean, and the sum grows as it goes, so a piece of k features loses k / 16
 then off by that part of its logits, E_q |z| + |z_target|, at most; the rest (exponentials,
 sums of the parts, the last operations) is below 2^-22 of them.  The mean square is held to
 one and a half times k 2^-29, plus 2^-22: all of d = 4096 in one sum loses 7.6e-6.
-bf16: pieces of 768, of 4096 / 16, 4096 / 8 and 4096 / 4 in the form for few tokens
-(16, 8 and 4 sums).  fp32: pieces of 128, 2.4e-7, and half as much for the sum of the pieces;
+bf16: pieces of 512, of 256 up to 256 rows, of 4096 / 16, 4096 / 8 and 4096 / 4 in the form
+for few tokens (16, 8 and 4 sums).  fp32: pieces of 128, 2.4e-7, and half as much for the sum of the pieces;
 operands with 16 of their 24 bits would leave 0.9e-6 to 1.3e-6 (evaluated in numpy).
 
 Losses near 0 have their absolute error: the exponential of the target is good to 2^-22
@@ -74,8 +74,9 @@ def logits_case(T, d, V, dtype):
 # the form that keeps terms and the one that does not, and the one for few tokens, whose
 # weight fills the GPU with whole columns of K
 @pytest.mark.parametrize("T,d,V,backward,piece", [
-    (200, 1600, 1500, True, 768), (200, 1600, 1500, False, 768),
-    (200, 2048, 1500, True, 768), (200, 4096, 1500, True, 768), (200, 4096, 1500, False, 768),
+    (200, 1600, 1500, True, 256), (200, 1600, 1500, False, 256), (3, 2048, 1500, True, 256),
+    (200, 4096, 1500, True, 256), (200, 4096, 1500, False, 256), (300, 1600, 1500, True, 512),
+    (300, 2048, 1500, False, 512), (300, 4096, 1500, True, 512), (300, 4096, 1500, False, 512),
     (1, 4096, 32000, False, 256), (24, 4096, 32000, False, 512), (64, 4096, 32000, False, 1024)])
 def test_losses_of_long_sums(px, T, d, V, backward, piece):
     x, W, t, want, size = logits_case(T, d, V, "bf16")
