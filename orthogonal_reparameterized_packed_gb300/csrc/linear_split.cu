@@ -75,7 +75,7 @@ struct SplitArgs {
   Fp32Epilogue epi;
   int segs;              // flags per row of A
   const int* row_flags;  // A's: rows with one that is not 0 are left to linear_simt
-  int b_count, a_count;  // flags of B, and of A as [K][M]: then all rows are
+  int b_count, a_count;  // flags of B (quads), and of A as [K][M]: then all rows are
   const int *b_flags, *a_flags;
   int* all;              // set here: whether any of those is
   int* status;
@@ -150,7 +150,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
   int bad = 0;
-  for (int i = threadIdx.x; i < p.b_count; i += kThreads) bad |= p.b_flags[i];
+  for (int i = threadIdx.x; i < p.b_count / 4; i += kThreads) {
+    const int4 q = reinterpret_cast<const int4*>(p.b_flags)[i];
+    bad |= q.x | q.y | q.z | q.w;
+  }
   if (A_MN)
     for (int i = threadIdx.x; i < p.a_count; i += kThreads) bad |= p.a_flags[i];
   bad = __syncthreads_or(bad);
@@ -403,8 +406,10 @@ struct SplitOperand {
 
 constexpr int kSplitThreads = 256;
 
-// Both operands, a warp per segment of a row.
-__global__ void __launch_bounds__(kSplitThreads)
+// Both operands, a warp per segment of a row.  Five CTAs on an SM: with the 57 registers
+// that the compiler takes otherwise four fit, and the copies in flight are too few (2048 x
+// 2048 and 5632 x 2048: 25.8 / 28.2 us, 513 x 1537 and 2049 x 1537: 10.4 / 14.5).
+__global__ void __launch_bounds__(kSplitThreads, 5)
     split_planes_kernel(const SplitOperand a, const SplitOperand b, int flags) {
   pdl_wait();
   pdl_trigger();
@@ -642,7 +647,9 @@ size_t flag_bytes(long long rows, int cols) {
   return round256(static_cast<size_t>(rows * segments(cols)) * sizeof(int));
 }
 
-size_t all_flag_bytes() { return round256((1 + split_ctas()) * sizeof(int)); }
+// The word that says whether the CUDA cores take everything, and from the second 16 bytes
+// on the CTAs' flags.
+size_t all_flag_bytes() { return round256((4 + split_ctas()) * sizeof(int)); }
 
 SplitOperand operand(const void* in, long long rows, int cols, long long ld,
                      long long plane_rows) {
@@ -662,7 +669,7 @@ SplitOperand operand(const void* in, long long rows, int cols, long long ld,
 SplitOperand kept(void* at, const void* in, long long rows, int cols, long long ld) {
   SplitOperand o = operand(in, rows, cols, ld, up64(rows));
   char* c = static_cast<char*>(at);
-  o.whole = reinterpret_cast<int*>(c) + 1;
+  o.whole = reinterpret_cast<int*>(c) + 4;
   o.flag = reinterpret_cast<int*>(c + all_flag_bytes());
   o.planes = reinterpret_cast<bf16*>(c + all_flag_bytes() + flag_bytes(o.plane_rows, cols));
   return o;
@@ -718,7 +725,7 @@ size_t linear_split_scratch_up_to(const LinearProduct& g) {
 cudaError_t linear_split(const LinearProduct& g, void* scratch, cudaStream_t s) {
   int* all = static_cast<int*>(scratch);
   SplitOperand a, b = operand(g.B, g.b_mn ? g.K : g.N, b_cols(g), 0, b_plane_rows(g));
-  b.whole = all + 1;
+  b.whole = all + 4;
   b.planes = reinterpret_cast<bf16*>(static_cast<char*>(scratch) + all_flag_bytes());
   if (g.a_planes != nullptr) {
     a = kept(g.a_planes, g.A, g.M, g.K, g.pitch_a);
