@@ -1,9 +1,10 @@
 """The losses at the output head, from the last hidden states and the head's weight:
 cross entropy and distillation from a teacher's top logits.  bf16 losses alone keep no
 logit, gradients one block of tokens' softmax terms (as many bytes as its logits in
-bf16; fp32 its logits, and two and a half times those for gradients).  Each class holds the output buffers and the workspace of one head and
-enqueues its calls on a stream (the current one by default); calls of one object on
-several streams, or of graphs captured with it, have to be ordered by the caller."""
+bf16; fp32 its logits, and two and a half times those for gradients).  Each class holds
+the output buffers and the workspace of one head and enqueues its calls on a stream (the
+current one by default); calls of one object on several streams, or of graphs captured
+with it, have to be ordered by the caller."""
 
 from __future__ import annotations
 
